@@ -7,6 +7,7 @@ cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -24,7 +25,8 @@ EXPORTED = ["attn_fwd", "attn_fwd_rows", "attn_fwd_fp8", "attn_fwd_host", "attn_
             "attn_decode_splitkv", "attn_decode_splitkv_noalloc",
             "attn_status_string", "attn_get_device_error", "attn_decode_workspace_bytes",
             "attn_selftest_wait_timeout", "attn_decode_splitkv_states", "attn_combine_states",
-            "attn_decode_graph_create", "attn_decode_graph_launch", "attn_decode_graph_destroy"]
+            "attn_decode_graph_create", "attn_decode_graph_launch", "attn_decode_graph_destroy",
+            "attn_fwd_mod", "attn_row_ranges", "attn_decode_varlen", "attn_decode_prefix"]
 DEVERR_SELFTEST = 0x10
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024
 
@@ -80,6 +82,15 @@ def load(path: str = LIB_PATH):
         lib.attn_decode_graph_launch.restype = i
         lib.attn_decode_graph_destroy.argtypes = [vp]
         lib.attn_decode_graph_destroy.restype = i
+        lib.attn_fwd_mod.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, f, vp, vp, vp]
+        lib.attn_fwd_mod.restype = i
+        lib.attn_row_ranges.argtypes = [vp, vp, vp, i, i, i, i, vp]
+        lib.attn_row_ranges.restype = i
+        lib.attn_decode_varlen.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, f, vp, vp]
+        lib.attn_decode_varlen.restype = i
+        lib.attn_decode_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, f,
+                                           vp, vp]
+        lib.attn_decode_prefix.restype = i
         lib.attn_decode_workspace_bytes.argtypes = [i, i, i, i]
         lib.attn_decode_workspace_bytes.restype = ctypes.c_longlong
         _lib = lib
@@ -223,6 +234,43 @@ def attn_decode_graph_destroy(handle: int) -> None:
     _check(load().attn_decode_graph_destroy(handle or None))
 
 
+def attn_fwd_mod(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, D, causal, q_offset, scale, softcap=0.0,
+                 slopes=None, ranges=None, stream=None) -> None:
+    """``attn_fwd_mod`` of include/attn.h: ``attn_fwd_rows`` with capped scores,
+    a distance bias (``slopes`` [Hq] fp32) and a key range per query row
+    (``ranges`` [B, Nq, 2] int32)."""
+    _check(load().attn_fwd_mod(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), int(B), int(Hq),
+                               int(Hkv), int(Nq), int(Nk), int(D), int(bool(causal)),
+                               int(q_offset), float(scale), float(softcap), _ptr(slopes),
+                               _ptr(ranges), _stream(stream)))
+
+
+def attn_row_ranges(doc_lens, prefix_lens, ranges, B, N, M, causal, stream=None) -> None:
+    """``attn_row_ranges`` of include/attn.h: the key ranges of packed documents."""
+    _check(load().attn_row_ranges(_ptr(doc_lens), _ptr(prefix_lens), _ptr(ranges), int(B), int(N),
+                                  int(M), int(bool(causal)), _stream(stream)))
+
+
+def attn_decode_varlen(q, kcache, vcache, lens, o, lse, B, Hq, Hkv, Ncap, D, scale, softcap=0.0,
+                       slopes=None, stream=None) -> None:
+    """``attn_decode_varlen`` of include/attn.h: decode with a length per
+    request (``lens`` [B] int32 on the device, or None: all Ncap keys)."""
+    _check(load().attn_decode_varlen(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(lens), _ptr(o),
+                                     _ptr(lse), int(B), int(Hq), int(Hkv), int(Ncap), int(D),
+                                     float(scale), float(softcap), _ptr(slopes),
+                                     _stream(stream)))
+
+
+def attn_decode_prefix(q, kprefix, vprefix, kcache, vcache, lens, o, lse, B, Hq, Hkv, Np, Ncap, D,
+                       scale, softcap=0.0, slopes=None, stream=None) -> None:
+    """``attn_decode_prefix`` of include/attn.h: ``attn_decode_varlen`` behind a
+    prefix (``kprefix`` / ``vprefix`` [Hkv, Np, D]) that all requests share."""
+    _check(load().attn_decode_prefix(_ptr(q), _ptr(kprefix), _ptr(vprefix), _ptr(kcache),
+                                     _ptr(vcache), _ptr(lens), _ptr(o), _ptr(lse), int(B), int(Hq),
+                                     int(Hkv), int(Np), int(Ncap), int(D), float(scale),
+                                     float(softcap), _ptr(slopes), _stream(stream)))
+
+
 def attn_decode_workspace_bytes(B, Hq, D, nsplit) -> int:
     return int(load().attn_decode_workspace_bytes(int(B), int(Hq), int(D), int(nsplit)))
 
@@ -332,4 +380,149 @@ def decode(q, kcache, vcache, nsplit: int, stream=None):
     o = torch.empty_like(q)
     lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     attn_decode_splitkv(q, kcache, vcache, o, lse, B, Hq, Hkv, Nk, D, nsplit, stream)
+    return o, lse
+
+
+# ------------------------------------------------------- modified scores: tensor helpers
+
+
+def _check_aux(dev, **tensors):
+    """The optional int32 / fp32 device arrays of the calls below:
+    name=(tensor or None, dtype, shape)."""
+    import torch
+    for name, (x, dtype, shape) in tensors.items():
+        if x is None:
+            continue
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if x.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+        if tuple(x.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+        if not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if x.device != dev:
+            raise ValueError(f"{name} is on {x.device}, expected {dev}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+@contextlib.contextmanager
+def _on(dev, stream, *tensors):
+    """Makes ``dev`` current, yields the stream to launch on, and when that is
+    not the device's current stream marks the tensors (and whatever the body
+    appends to the yielded list) as used on it, so that the caching allocator
+    does not hand their memory out again while the kernels run."""
+    import torch
+    with torch.cuda.device(dev):
+        cur = torch.cuda.current_stream()
+        if stream is None:
+            s = cur
+        elif isinstance(stream, int):
+            s = torch.cuda.ExternalStream(stream, device=dev) if stream else \
+                torch.cuda.default_stream(dev)
+        else:
+            s = stream
+            if s.device != dev:
+                raise ValueError(f"the stream is on {s.device}, the tensors on {dev}")
+        used = [x for x in tensors if x is not None]
+        yield s, used
+        if s.cuda_stream != cur.cuda_stream:
+            for x in used:
+                x.record_stream(s)
+
+
+def forward_mod(q, k, v, *, causal: bool = False, scale: float | None = None,
+                softcap: float = 0.0, slopes=None, ranges=None, q_offset: int = 0, stream=None):
+    """O, LSE = attention(q [B,Hq,Nq,D], k/v [B,Hkv,Nk,D]) with modified scores:
+    capped at ``softcap`` by a tanh (0: not), biased by ``-slopes[h] * distance``
+    (``slopes`` [Hq] fp32, query row i at position ``q_offset + i``), row i of
+    batch b seeing keys ``ranges[b, i, 0] <= j < ranges[b, i, 1]`` (``ranges``
+    [B,Nq,2] int32, see ``row_ranges``; None: all) and, with ``causal``, of
+    these those at or before its position.  Rows that see nothing give 0 and
+    -inf."""
+    import torch
+    _check_ranks({"q": q, "k": k, "v": v}, {"q": 4, "k": 4, "v": 4})
+    _check_inputs({"q": q, "k": k, "v": v},
+                  {"B": (q.shape[0], k.shape[0], v.shape[0]), "D": (q.shape[3], k.shape[3], v.shape[3]),
+                   "Hkv": (k.shape[1], v.shape[1]), "Nk": (k.shape[2], v.shape[2])})
+    B, Hq, Nq, D = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)),
+               ranges=(ranges, torch.int32, (B, Nq, 2)))
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on(q.device, stream, q, k, v, slopes, ranges) as (s, used):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+        used += [o, lse]
+        attn_fwd_mod(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, D, causal, q_offset, scale, softcap,
+                     slopes, ranges, s)
+    return o, lse
+
+
+def row_ranges(doc_lens, N: int, *, prefix_lens=None, causal: bool = True, stream=None):
+    """[B, N, 2] int32 key ranges for ``forward_mod`` from the lengths of the
+    documents packed into each row (``doc_lens`` [B, M] int32, CUDA): a token
+    sees its own document, with ``causal`` up to itself or to the end of the
+    document's bidirectional prefix (``prefix_lens`` [B, M] int32).  Tokens
+    behind the last document (padding) see nothing."""
+    import torch
+    _check_ranks({"doc_lens": doc_lens}, {"doc_lens": 2})
+    B, M = doc_lens.shape
+    _check_aux(doc_lens.device, doc_lens=(doc_lens, torch.int32, (B, M)),
+               prefix_lens=(prefix_lens, torch.int32, (B, M)))
+    with _on(doc_lens.device, stream, doc_lens, prefix_lens) as (s, used):
+        out = torch.empty((B, int(N), 2), dtype=torch.int32, device=doc_lens.device)
+        used.append(out)
+        attn_row_ranges(doc_lens, prefix_lens, out, B, N, M, causal, s)
+    return out
+
+
+def decode_varlen(q, kcache, vcache, lens=None, *, scale: float | None = None,
+                  softcap: float = 0.0, slopes=None, stream=None):
+    """O, LSE = decode(q [B,Hq,D], caches [B,Hkv,Ncap,D]) over the first
+    ``lens[b]`` keys of request b (``lens`` [B] int32, CUDA; None: all), with
+    the score modifications of ``forward_mod``; the query is at position
+    ``lens[b] - 1``."""
+    import torch
+    _check_decode_inputs(q, kcache, vcache)
+    B, Hq, D = q.shape
+    Hkv, Ncap = kcache.shape[1], kcache.shape[2]
+    _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)), lens=(lens, torch.int32, (B,)))
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on(q.device, stream, q, kcache, vcache, lens, slopes) as (s, used):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        used += [o, lse]
+        attn_decode_varlen(q, kcache, vcache, lens, o, lse, B, Hq, Hkv, Ncap, D, scale, softcap,
+                           slopes, s)
+    return o, lse
+
+
+def decode_prefix(q, kprefix, vprefix, kcache, vcache, lens=None, *, scale: float | None = None,
+                  softcap: float = 0.0, slopes=None, stream=None):
+    """``decode_varlen`` for requests that share a prefix: ``kprefix`` /
+    ``vprefix`` [Hkv,Np,D] are seen by every request before its own
+    ``lens[b]`` cache keys, and read once for the whole batch; the query is at
+    position ``Np + lens[b] - 1``."""
+    import torch
+    _check_ranks({"kprefix": kprefix, "vprefix": vprefix}, {"kprefix": 3, "vprefix": 3})
+    _check_decode_inputs(q, kcache, vcache)
+    _check_inputs({"q": q, "kprefix": kprefix, "vprefix": vprefix},
+                  {"Hkv": (kcache.shape[1], kprefix.shape[0], vprefix.shape[0]),
+                   "Np": (kprefix.shape[1], vprefix.shape[1]),
+                   "D": (q.shape[2], kprefix.shape[2], vprefix.shape[2])})
+    B, Hq, D = q.shape
+    Hkv, Ncap, Np = kcache.shape[1], kcache.shape[2], kprefix.shape[1]
+    _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)), lens=(lens, torch.int32, (B,)))
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on(q.device, stream, q, kprefix, vprefix, kcache, vcache, lens, slopes) as (s, used):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        used += [o, lse]
+        attn_decode_prefix(q, kprefix, vprefix, kcache, vcache, lens, o, lse, B, Hq, Hkv, Np, Ncap,
+                           D, scale, softcap, slopes, s)
     return o, lse

@@ -124,6 +124,11 @@ __global__ void selftest_wait_kernel(unsigned int* err, uint64_t limit_ns) {
 
 }  // namespace
 
+int check_device() {
+  DeviceState* st = nullptr;
+  return device_state(&st);
+}
+
 unsigned int* device_error_word() {
   DeviceState* st = nullptr;
   return device_state(&st) == ATTN_OK ? st->err_word : nullptr;

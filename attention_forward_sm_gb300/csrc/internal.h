@@ -52,6 +52,50 @@ struct DecodeParams {
   uint64_t wait_limit_ns;
 };
 
+// Score modifications (see include/attn.h).  x = scale * <q, k>; capped:
+// tanh(x / softcap) * softcap = tanh(cap_in * <q, k>) * cap_out in log2 units.
+struct ScoreMod {
+  float scale;
+  float cap_in;         // scale / softcap; 0: no cap
+  float cap_out;        // softcap * log2(e)
+  const float* slopes;  // [Hq], or NULL: no distance bias
+};
+
+// Prefill with modified scores.
+struct ModFwdParams {
+  const void* q;      // [B, Hq, Nq, D] bf16
+  const void* k;      // [B, Hkv, Nk, D] bf16
+  const void* v;
+  void* o;            // [B, Hq, Nq, D] bf16
+  float* lse;         // [B, Hq, Nq]
+  const int* ranges;  // [B, Nq, 2] visible keys [lo, hi) of every row, or NULL: all
+  int B, Hq, Hkv, Nq, Nk, D;
+  int causal, q_offset;
+  ScoreMod mod;
+};
+
+// Decode with a length per request, behind a shared prefix if Np > 0.
+struct ModDecodeParams {
+  const void* q;        // [B, Hq, D] bf16
+  const void* kprefix;  // [Hkv, Np, D] bf16
+  const void* vprefix;
+  const void* kcache;   // [B, Hkv, Ncap, D] bf16
+  const void* vcache;
+  const int* lens;      // [B], or NULL: Ncap each
+  void* o;              // [B, Hq, D] bf16
+  float* lse;           // [B, Hq]
+  int B, Hq, Hkv, Np, Ncap, D;
+  ScoreMod mod;
+};
+
+// Check the device and queue the kernels; arguments are checked before.
+// Return an ATTN_* status.
+int mod_fwd(const ModFwdParams& p, cudaStream_t stream);
+int mod_decode(const ModDecodeParams& p, cudaStream_t stream);
+
+// ATTN_OK when the current device is an sm_103, else the status to return.
+int check_device();
+
 // Device error word of the current device (one-time per-device set-up);
 // nullptr when the current device is unusable.
 unsigned int* device_error_word();

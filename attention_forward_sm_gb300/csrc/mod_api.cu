@@ -1,0 +1,124 @@
+// C entries of the attention calls with modified scores (attn_fwd_mod,
+// attn_decode_varlen, attn_decode_prefix): argument checks and launches.  The
+// contracts are in include/attn.h.
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/attn.h"
+#include "internal.h"
+
+namespace attn {
+namespace {
+
+bool misaligned(const void* p, unsigned to) {
+  return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) != 0;
+}
+
+// Checks scale, softcap and slopes and fills *m.
+int score_mod(float scale, float softcap, const float* slopes, ScoreMod* m) {
+  if (!isfinite(scale) || scale < 0.f) return ATTN_ERR_SHAPE;
+  if (!isfinite(softcap) || softcap < 0.f) return ATTN_ERR_SHAPE;
+  *m = ScoreMod{};
+  m->scale = scale;
+  if (softcap > 0.f) {
+    m->cap_in = scale / softcap;
+    m->cap_out = softcap * 1.4426950408889634f;
+    if (!isfinite(m->cap_in) || !isfinite(m->cap_out)) return ATTN_ERR_SHAPE;
+  }
+  if (misaligned(slopes, 4)) return ATTN_ERR_ALIGN;
+  m->slopes = slopes;
+  return ATTN_OK;
+}
+
+int decode_entry(const void* q, const void* kprefix, const void* vprefix, const void* kcache,
+                 const void* vcache, const int* lens, void* o, float* lse, int B, int Hq, int Hkv,
+                 int Np, int Ncap, int D, float scale, float softcap, const float* slopes,
+                 cudaStream_t stream) {
+  if (!q || !kcache || !vcache || !o || !lse) return ATTN_ERR_NULL;
+  constexpr int kMostKeys = 1 << 30;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Ncap < 1 || Ncap > kMostKeys || Np < 0 || Np > kMostKeys)
+    return ATTN_ERR_SHAPE;
+  if (Hq % Hkv != 0 || Hq / Hkv > 128 || Hq > 65535) return ATTN_ERR_SHAPE;
+  if (D != 64 && D != 128) return ATTN_ERR_SHAPE;
+  if (static_cast<long long>(B) * Hkv > (1ll << 20)) return ATTN_ERR_SHAPE;
+  ModDecodeParams p = {};
+  if (int rc = score_mod(scale, softcap, slopes, &p.mod)) return rc;
+  for (const void* x : {q, kprefix, vprefix, kcache, vcache, static_cast<const void*>(o),
+                        static_cast<const void*>(lse)})
+    if (misaligned(x, 16)) return ATTN_ERR_ALIGN;
+  if (misaligned(lens, 4)) return ATTN_ERR_ALIGN;
+  p.q = q;
+  p.kprefix = kprefix;
+  p.vprefix = vprefix;
+  p.kcache = kcache;
+  p.vcache = vcache;
+  p.lens = lens;
+  p.o = o;
+  p.lse = lse;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Np = Np;
+  p.Ncap = Ncap;
+  p.D = D;
+  return mod_decode(p, stream);
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+int attn_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                 int Hkv, int Nq, int Nk, int D, int causal, int q_offset, float scale,
+                 float softcap, const float* slopes, const int* ranges, cudaStream_t stream) {
+  if (!q || !k || !v || !o || !lse) return ATTN_ERR_NULL;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || Hq % Hkv != 0) return ATTN_ERR_SHAPE;
+  if (D != 64 && D != 128) return ATTN_ERR_SHAPE;
+  // the kernels form q_offset + (row within the call) + a few tiles in int
+  if (q_offset < 0 || q_offset > INT_MAX - Nq - 1024 || Nk > INT_MAX - 1024) return ATTN_ERR_SHAPE;
+  if (static_cast<long long>(B) * Hq * ((Nq + 255ll) / 256) >= (1ll << 31) - 65536)
+    return ATTN_ERR_SHAPE;
+  ModFwdParams p = {};
+  if (int rc = score_mod(scale, softcap, slopes, &p.mod)) return rc;
+  for (const void* x : {q, k, v, static_cast<const void*>(o), static_cast<const void*>(lse)})
+    if (misaligned(x, 16)) return ATTN_ERR_ALIGN;
+  if (misaligned(ranges, 8)) return ATTN_ERR_ALIGN;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.o = o;
+  p.lse = lse;
+  p.ranges = ranges;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  p.D = D;
+  p.causal = causal ? 1 : 0;
+  p.q_offset = q_offset;
+  return mod_fwd(p, stream);
+}
+
+int attn_decode_varlen(const void* q, const void* kcache, const void* vcache, const int* lens,
+                       void* o, float* lse, int B, int Hq, int Hkv, int Ncap, int D, float scale,
+                       float softcap, const float* slopes, cudaStream_t stream) {
+  return decode_entry(q, nullptr, nullptr, kcache, vcache, lens, o, lse, B, Hq, Hkv, 0, Ncap, D,
+                      scale, softcap, slopes, stream);
+}
+
+int attn_decode_prefix(const void* q, const void* kprefix, const void* vprefix,
+                       const void* kcache, const void* vcache, const int* lens, void* o,
+                       float* lse, int B, int Hq, int Hkv, int Np, int Ncap, int D, float scale,
+                       float softcap, const float* slopes, cudaStream_t stream) {
+  if (!kprefix || !vprefix) return ATTN_ERR_NULL;
+  if (Np < 1) return ATTN_ERR_SHAPE;
+  return decode_entry(q, kprefix, vprefix, kcache, vcache, lens, o, lse, B, Hq, Hkv, Np, Ncap, D,
+                      scale, softcap, slopes, stream);
+}
+
+}  // extern "C"

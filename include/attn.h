@@ -10,6 +10,10 @@
  *                        keys cut into nsplit chunks whose partial states are
  *                        recombined through their LSE (split-KV / FlashDecode).
  *
+ * and both again with modified scores (capped, biased by distance) and other
+ * masks (documents, prefixes, a length per request, a shared prefix):
+ * attn_fwd_mod, attn_row_ranges, attn_decode_varlen, attn_decode_prefix.
+ *
  * Sources for the operations:
  *   - "FlashAttention-3 vs Triton Kernels" (dailyaiworld), introduction:
  *     FlashAttention's IO-aware tiling computes the softmax attention output
@@ -303,6 +307,105 @@ int attn_decode_graph_create(const void *q, const void *kcache, const void *vcac
  * ATTN_ERR_LAUNCH if the graph launch fails. */
 int attn_decode_graph_launch(attn_decode_graph *graph, cudaStream_t stream);
 int attn_decode_graph_destroy(attn_decode_graph *graph);
+
+/*
+ * Attention with modified scores.  Four calls share one definition of the
+ * score of query row i (at position p_i) and key j:
+ *
+ *   x = scale * <Q_i, K_j>
+ *   x = softcap * tanh(x / softcap)      if softcap > 0   (capped scores)
+ *   x = x - slopes[h] * |p_i - j|        if slopes != NULL (distance bias)
+ *
+ * O_i = sum_j softmax(x)_j V_j and LSE_i = ln sum_j exp(x_j) over the keys j
+ * that row i sees.  A row that sees no key gives O = 0 and LSE = -infinity.
+ *
+ * softcap is 0 (none) or positive with softcap and scale / softcap finite
+ * (ATTN_ERR_SHAPE otherwise); slopes is NULL or Hq fp32 values on the device
+ * (one per query head, finite; positive ones favour near keys).  Numerics as
+ * attn_fwd; the cap is accurate to a few fp32 roundings of the score.
+ *
+ * Keys that a row does not see have no influence on it, whatever K holds
+ * there.  V may hold anything (also NaN) at keys that no row of its
+ * (batch, KV head) sees on either side of the visible span, such as padding
+ * or the unused tail of a cache; a NaN or infinity in V at a key that some
+ * rows see may reach the other rows of the same (batch, KV head) too.
+ */
+
+/*
+ * attn_fwd_mod -- attn_fwd with modified scores and a key range per row.
+ *
+ *   q, k, v, o, lse: as attn_fwd.  Query row i is at position
+ *   p_i = q_offset + i, key j at position j.
+ *   ranges [B, Nq, 2] int32 on the device, or NULL: row i of batch b sees the
+ *   keys ranges[b][i][0] <= j < ranges[b][i][1] (clamped to [0, Nk]; an empty
+ *   range sees nothing).  With causal != 0 it sees of these only j <= p_i.
+ *   attn_row_ranges makes the ranges of packed documents and prefixes.
+ *
+ * Limits: those of attn_fwd_rows; ranges 8-byte aligned, slopes 4-byte
+ * aligned (ATTN_ERR_ALIGN).
+ */
+int attn_fwd_mod(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq,
+                 int Hkv, int Nq, int Nk, int D, int causal, int q_offset, float scale,
+                 float softcap, const float *slopes, const int *ranges, cudaStream_t stream);
+
+/*
+ * attn_row_ranges -- the key ranges of rows that hold packed documents.
+ *
+ *   doc_lens    [B, M] int32: lengths of the documents of each batch row, in
+ *               the order in which they are packed (0 and negative: none)
+ *   prefix_lens [B, M] int32 or NULL: the first prefix_lens tokens of a
+ *               document see one another (only with causal != 0)
+ *   ranges      [B, N, 2] int32, written
+ *
+ * Token i of the document at [s, e) gets the range [s, e), with causal != 0
+ * [s, max(i + 1, min(s + prefix, e))).  Documents are cut at N; tokens behind
+ * the last document get the empty range [0, 0).
+ *
+ * Limits: 1 <= B <= 65535, 1 <= N <= 2^30, M >= 1, B * N < 2^40; ranges
+ * 8-byte, the lengths 4-byte aligned.
+ */
+int attn_row_ranges(const int *doc_lens, const int *prefix_lens, int *ranges, int B, int N, int M,
+                    int causal, cudaStream_t stream);
+
+/*
+ * attn_decode_varlen -- decode of one query row per (batch, head) with a
+ * length per request and modified scores.
+ *
+ *   q       [B, Hq, D]         bf16
+ *   kcache  [B, Hkv, Ncap, D]  bf16, contiguous; request b uses the first
+ *   vcache  [B, Hkv, Ncap, D]  lens[b] keys, the rest may hold anything
+ *   lens    [B] int32 on the device, or NULL (all Ncap keys); clamped to
+ *           [0, Ncap]
+ *   o       [B, Hq, D] bf16, lse [B, Hq] fp32, written
+ *
+ * The query is at position lens[b] - 1, that of the request's last key.  The
+ * lengths stay on the device: the call never waits for them, so it can be
+ * captured once and replayed while they grow.
+ *
+ * Limits: B, Hq, Hkv, Ncap >= 1; Hq % Hkv == 0; Hq / Hkv <= 128; D in
+ * {64, 128}; B * Hkv <= 2^20, Hq <= 65535; Ncap <= 2^30; scale finite and
+ * >= 0; the bf16 pointers and lse 16-byte, lens and slopes 4-byte aligned.
+ * Scratch as attn_decode_splitkv: one buffer per recently used stream, none
+ * allocated by a repeated call; during capture a buffer of the graph's own.
+ */
+int attn_decode_varlen(const void *q, const void *kcache, const void *vcache, const int *lens,
+                       void *o, float *lse, int B, int Hq, int Hkv, int Ncap, int D, float scale,
+                       float softcap, const float *slopes, cudaStream_t stream);
+
+/*
+ * attn_decode_prefix -- attn_decode_varlen for requests that share a prefix.
+ *
+ *   kprefix, vprefix [Hkv, Np, D] bf16, contiguous: the shared keys, held and
+ *   read once for the whole batch; request b sees the Np prefix keys
+ *   (positions 0 .. Np-1) and then its own first lens[b] cache keys
+ *   (positions Np ..).  Its query is at position Np + lens[b] - 1.
+ *
+ * The other arguments, limits and scratch as attn_decode_varlen; 1 <= Np <= 2^30.
+ */
+int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix,
+                       const void *kcache, const void *vcache, const int *lens, void *o,
+                       float *lse, int B, int Hq, int Hkv, int Np, int Ncap, int D, float scale,
+                       float softcap, const float *slopes, cudaStream_t stream);
 
 /* Human-readable name of an ATTN_* status code (static string). */
 const char *attn_status_string(int status);

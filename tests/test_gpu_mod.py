@@ -1,0 +1,590 @@
+"""Attention with modified scores on the GPU: forward_mod, row_ranges,
+decode_varlen and decode_prefix against the definition in 64 bits.
+
+Tolerances, from the roundings (none measured).  A score x is a product of D
+terms summed in fp32 (each step off by one unit, 2^-23, of the sum of the
+terms' magnitudes S), scaled, capped (the tanh is good to 2^-20 of the value,
+a few roundings more) and biased (roundings of the bias relative to the
+nearest key); its error is at most
+    dx = (D + 4) 2^-23 S + 2^-19 |x| + 2^-22 |bias|,
+and a weight exp(x - LSE) is off by 2 dx + 2^-20 of its value.  The weights
+are rounded to bf16 (half a step: 2^-8), and so is O:
+    |dO| <= (2^-8 + 2 dx + 2^-19) sum_j w_j |v_j| + 2^-8 |O| + 2^-133
+(the last: half the smallest bf16),  |dLSE| <= dx + 2^-19 + 2^-22 |LSE|.
+
+The sums over n keys add at most 64 weights to one another and those sums in
+turn, n / 64 + 64 additions in a chain; every addition of positive terms is
+off by 2^-24 of the sum at most, which adds (n / 64 + 64) 2^-24 to the
+relative error of the normaliser (to dLSE) and, with that of the sum of the
+values, twice that to the weights of O.
+"""
+import math
+
+import pytest
+import torch
+
+from attention_forward_sm_gb300 import binding as attn
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    from attention_forward_sm_gb300 import _build
+    _build.build()
+    attn.load()
+    assert torch.cuda.is_available(), "gpu tests need a CUDA device"
+
+
+@pytest.fixture(autouse=True)
+def _no_wait_ran_out():
+    yield
+    assert attn.attn_get_device_error() == 0
+
+
+def rand(seed, shape, sigma=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * sigma).to(torch.bfloat16)
+
+
+def alibi(H):
+    return torch.tensor([2.0 ** (-8.0 * (h + 1) / H) for h in range(H)], device="cuda")
+
+
+def definition(q, k, v, pos, jpos, seen, scale, cap, slope):
+    """One head in 64 bits: q [R, D], k / v [n, D], seen [R, n] ->
+    O, LSE and the tolerances of both."""
+    D = q.shape[1]
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    q, k, v = q.double(), k.double(), v.double()
+    # keys that no row sees may hold anything
+    used = seen.any(0)
+    k, v = torch.where(used[:, None], k, 0.0), torch.where(used[:, None], v, 0.0)
+    x = scale * (q @ k.T)
+    mag = scale * (q.abs() @ k.abs().T)
+    if cap > 0:
+        cap = float(torch.tensor(cap, dtype=torch.float32))
+        x = cap * torch.tanh(x / cap)
+    bias = torch.zeros_like(x)
+    if slope is not None:
+        bias = -float(slope) * (pos.double()[:, None] - jpos.double()[None, :]).abs()
+    best = bias.masked_fill(~seen, -INF).amax(1, keepdim=True)
+    dx = (D + 4) * 2.0**-23 * mag + 2.0**-19 * x.abs() + 2.0**-22 * (bias - best).abs()
+    dx = torch.where(seen, dx, 0.0).amax(1)
+    x = (x + bias).masked_fill(~seen, -INF)
+    lse = torch.logsumexp(x, 1)
+    w = torch.exp(x - torch.where(torch.isinf(lse), 0.0, lse)[:, None])
+    o = w @ v
+    sums = (k.shape[0] / 64 + 64) * 2.0**-24
+    tol_o = (2.0**-8 + 2 * dx[:, None] + 2 * sums + 2.0**-19) * (w @ v.abs()) + 2.0**-8 * o.abs() + 2.0**-133
+    tol_l = dx + sums + 2.0**-19 + 2.0**-22 * lse.abs()
+    return o, lse, tol_o, tol_l
+
+
+def check(o, lse, ref, label=""):
+    ro, rl, to, tl = ref
+    none = torch.isinf(rl)
+    assert torch.equal(lse.double() == -INF, none), f"{label}: rows that see nothing"
+    assert (o[none] == 0).all(), f"{label}: O of rows that see nothing"
+    eo = ((o.double() - ro).abs() / to)[~none]
+    el = ((lse.double() - rl).abs() / tl)[~none]
+    assert not eo.numel() or eo.max() <= 1, f"{label}: O off by {eo.max():.3g} tolerances"
+    assert not el.numel() or el.max() <= 1, f"{label}: LSE off by {el.max():.3g} tolerances"
+
+
+def check_fwd(o, lse, q, k, v, causal, scale, cap, slopes, ranges, q_offset, label=""):
+    B, Hq, Nq, D = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    pos = q_offset + torch.arange(Nq, device="cuda")
+    j = torch.arange(Nk, device="cuda")
+    for b in range(B):
+        seen = torch.ones(Nq, Nk, dtype=torch.bool, device="cuda")
+        if ranges is not None:
+            seen &= (j >= ranges[b, :, :1]) & (j < ranges[b, :, 1:])
+        if causal:
+            seen &= j <= pos[:, None]
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            ref = definition(q[b, h], k[b, g], v[b, g], pos, j, seen, scale, cap,
+                             None if slopes is None else slopes[h])
+            check(o[b, h], lse[b, h], ref, f"{label} b{b} h{h}")
+
+
+def ranges_of(kind, B, Nq, Nk, seed=5):
+    if kind is None:
+        return None
+    if kind == "docs":
+        cut = max(1, Nq // 3)
+        lens = torch.tensor([[cut, 0, 1, Nq - cut - 1 - Nq // 7]] * B, dtype=torch.int32, device="cuda")
+        return attn.row_ranges(lens, Nq)
+    if kind == "prefix":
+        lens = torch.tensor([[Nq // 2, Nq - Nq // 2]] * B, dtype=torch.int32, device="cuda")
+        return attn.row_ranges(lens, Nq, prefix_lens=lens // 3)
+    if kind == "none":
+        return torch.zeros(B, Nq, 2, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    a = torch.randint(-5, Nk + 6, (B, Nq, 2), generator=g, device="cuda", dtype=torch.int32)
+    if kind == "wild":  # out of range on both sides, lo > hi, and the extremes of the type
+        a[:, ::7, 0], a[:, ::7, 1] = -2**31, 2**31 - 1
+        a[:, 3::11, 0], a[:, 3::11, 1] = 2**31 - 1, -2**31
+        return a
+    width = 40
+    lo = a[..., 0].clamp(0, Nk)
+    return torch.stack([lo, (lo + width).clamp(max=Nk)], -1).contiguous()  # "narrow"
+
+
+# ------------------------------------------------------------------------------ prefill
+
+FWD = [
+    # B, Hq, Hkv, Nq, Nk, D, causal, q_offset, cap, bias, ranges
+    (1, 1, 1, 1, 1, 64, False, 0, 0.0, False, None),
+    (1, 1, 1, 1, 1, 128, True, 0, 30.0, True, None),
+    (2, 2, 2, 256, 256, 64, True, 0, 30.0, False, None),
+    (1, 4, 2, 300, 300, 128, True, 0, 50.0, False, None),
+    (1, 4, 2, 300, 300, 128, False, 0, 50.0, False, None),
+    (2, 4, 1, 257, 385, 64, False, 0, 0.0, True, None),
+    (1, 3, 1, 130, 517, 128, True, 387, 0.0, True, None),
+    (1, 7, 1, 129, 127, 128, True, 0, 20.0, True, None),
+    (2, 2, 1, 511, 511, 128, False, 0, 0.0, False, "docs"),
+    (2, 2, 2, 640, 640, 64, False, 0, 25.0, False, "docs"),
+    (1, 6, 2, 400, 400, 128, False, 0, 30.0, True, "prefix"),
+    (1, 2, 2, 333, 333, 64, False, 0, 0.0, True, "prefix"),
+    (2, 2, 1, 300, 450, 128, False, 0, 0.0, False, "wild"),
+    (2, 2, 1, 300, 450, 64, True, 100, 15.0, True, "wild"),
+    (1, 2, 2, 1000, 900, 128, False, 0, 0.0, False, "narrow"),
+    (1, 2, 2, 700, 2000, 64, False, 0, 40.0, True, "narrow"),
+    (1, 2, 1, 270, 140, 128, False, 0, 0.0, True, "none"),
+    (1, 2, 1, 5, 4099, 128, True, 4094, 30.0, True, None),
+    (1, 1, 1, 1030, 1030, 64, True, 0, 0.0, False, "wild"),
+]
+
+
+@pytest.mark.parametrize("case", FWD, ids=lambda c: "-".join(map(str, c)))
+def test_forward_mod(case):
+    B, Hq, Hkv, Nq, Nk, D, causal, off, cap, bias, kind = case
+    q, k, v = (rand(s, sh, sg) for s, sh, sg in ((1, (B, Hq, Nq, D), 6.0 if cap else 1.0),
+                                                 (2, (B, Hkv, Nk, D), 1.0), (3, (B, Hkv, Nk, D), 1.0)))
+    slopes, ranges = (alibi(Hq) if bias else None), ranges_of(kind, B, Nq, Nk)
+    args = dict(causal=causal, softcap=cap, slopes=slopes, ranges=ranges, q_offset=off)
+    o, lse = attn.forward_mod(q, k, v, **args)
+    check_fwd(o, lse, q, k, v, causal, 1 / math.sqrt(D), cap, slopes, ranges, off)
+    o2, lse2 = attn.forward_mod(q, k, v, **args)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)  # the same bits every time
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sigma,cap", [(40.0, 5.0), (200.0, 50.0), (0.01, 1000.0), (1.0, 0.05), (6.0, 50.0)])
+def test_cap_over_its_whole_range(D, sigma, cap):
+    """Scores far beyond the cap, near its knee and far below it."""
+    q, k, v = rand(1, (1, 2, 200, D), sigma), rand(2, (1, 2, 300, D)), rand(3, (1, 2, 300, D))
+    o, lse = attn.forward_mod(q, k, v, softcap=cap)
+    check_fwd(o, lse, q, k, v, False, 1 / math.sqrt(D), cap, None, None, 0)
+
+
+@pytest.mark.parametrize("slope", [0.5, -0.01, 8.0, 0.0])
+@pytest.mark.parametrize("q_offset", [0, 150, 10**6, 2_000_000_000])
+def test_bias_of_far_positions(slope, q_offset):
+    """The bias keeps its digits when every key is far away: it is taken
+    relative to the key that it favours."""
+    D, Nq, Nk = 64, 70, 300
+    q, k, v = rand(1, (1, 2, Nq, D)), rand(2, (1, 1, Nk, D)), rand(3, (1, 1, Nk, D))
+    slopes = torch.tensor([slope, slope / 3], device="cuda")
+    o, lse = attn.forward_mod(q, k, v, slopes=slopes, q_offset=q_offset)
+    check_fwd(o, lse, q, k, v, False, 1 / math.sqrt(D), 0.0, slopes, None, q_offset)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, False), (30.0, True)])
+@pytest.mark.parametrize("trash", [NAN, INF, -INF])
+def test_trash_in_keys_that_no_row_sees(D, cap, bias, trash):
+    """K and V of padding (in front of and behind the visible span, inside and
+    outside of the key tiles that are read) have no influence."""
+    B, N, lo, hi = 2, 400, 37, 301
+    q, k, v = rand(1, (B, 2, N, D)), rand(2, (B, 1, N, D)), rand(3, (B, 1, N, D))
+    ranges = torch.tensor([lo, hi], dtype=torch.int32, device="cuda").expand(B, N, 2).contiguous()
+    for x in (k, v):
+        x[:, :, :lo] = trash
+        x[:, :, hi:] = trash
+    slopes = alibi(2) if bias else None
+    o, lse = attn.forward_mod(q, k, v, softcap=cap, slopes=slopes, ranges=ranges)
+    check_fwd(o, lse, q, k, v, False, 1 / math.sqrt(D), cap, slopes, ranges, 0)
+
+
+def test_nan_in_k_reaches_only_the_rows_that_see_it():
+    N, D = 300, 128
+    q, k, v = rand(1, (1, 1, N, D)), rand(2, (1, 1, N, D)), rand(3, (1, 1, N, D))
+    k[0, 0, 200] = NAN
+    o, lse = attn.forward_mod(q, k, v, causal=True, softcap=30.0)
+    assert torch.isfinite(o[0, 0, :200].float()).all() and torch.isfinite(lse[0, 0, :200]).all()
+    assert torch.isnan(o[0, 0, 200:].float()).all() and torch.isnan(lse[0, 0, 200:]).all()
+
+
+def test_without_modifications_it_is_forward():
+    for D in (64, 128):
+        q, k, v = rand(1, (2, 4, 600, D)), rand(2, (2, 2, 700, D)), rand(3, (2, 2, 700, D))
+        for causal in (False, True):
+            o, lse = attn.forward_mod(q, k, v, causal=causal)
+            ro, rl = attn.forward(q, k, v, causal=causal)
+            # both within the tolerance of the definition: within twice that of one another
+            assert (o.float() - ro.float()).abs().max() <= 2 * 2.0**-6
+            assert (lse - rl).abs().max() <= 1e-4
+
+
+def test_scale_zero_and_large():
+    q, k, v = rand(1, (1, 2, 150, 64)), rand(2, (1, 2, 150, 64)), rand(3, (1, 2, 150, 64))
+    for scale in (0.0, 3.0):
+        for cap in (0.0, 20.0):
+            o, lse = attn.forward_mod(q, k, v, scale=scale, softcap=cap, causal=True)
+            check_fwd(o, lse, q, k, v, True, scale, cap, None, None, 0)
+
+
+def test_many_units_every_row():
+    """More work units than CTAs, of very different lengths, every row checked."""
+    B, H, N, D = 3, 24, 1100, 128
+    q, k, v = rand(1, (B, H, N, D)), rand(2, (B, H, N, D)), rand(3, (B, H, N, D))
+    lens = torch.tensor([[1, 300, 2, 500, 97, 130], [1100, 0, 0, 0, 0, 0], [7, 7, 400, 600, 0, 0]],
+                        dtype=torch.int32, device="cuda")
+    ranges = attn.row_ranges(lens, N)
+    o, lse = attn.forward_mod(q, k, v, ranges=ranges, softcap=12.0)
+    check_fwd(o, lse, q, k, v, False, 1 / math.sqrt(D), 12.0, None, ranges, 0)
+
+
+# ------------------------------------------------------------------------------ ranges
+
+
+def ranges_definition(doc_lens, prefix, N, causal):
+    out = torch.zeros(len(doc_lens), N, 2, dtype=torch.int32)
+    for b, row in enumerate(doc_lens):
+        s = 0
+        for m, n in enumerate(row):
+            e = min(s + max(n, 0), N)
+            for i in range(s, e):
+                hi = e if not causal else max(i + 1, min(s + (max(prefix[b][m], 0) if prefix else 0), e))
+                out[b, i] = torch.tensor([s, hi])
+            s = e
+    return out
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("rows,N", [
+    ([[1]], 1), ([[5]], 3), ([[0]], 4), ([[-3, 2, 0, 0, 4]], 9), ([[2, 3], [6, 0], [0, 6]], 6),
+    ([[1023, 2, 1024]], 2100), ([[1] * 1500], 1400), ([[0] * 1100 + [3] * 1100], 3000),
+    ([[2**31 - 1, 5], [3, 2**31 - 1]], 1030),
+])
+def test_row_ranges(rows, N, causal):
+    lens = torch.tensor(rows, dtype=torch.int32, device="cuda")
+    pre = [[(7 * m) % 5 - 1 if m % 3 else 2**31 - 1 for m in range(len(r))] for r in rows]
+    for prefix in (None, pre):
+        t = None if prefix is None else torch.tensor(prefix, dtype=torch.int32, device="cuda")
+        got = attn.row_ranges(lens, N, prefix_lens=t, causal=causal)
+        assert torch.equal(got.cpu(), ranges_definition(rows, prefix, N, causal))
+
+
+# ------------------------------------------------------------------------------ decode
+
+
+def check_decode(o, lse, q, k, v, lens, cap, slopes, pk=None, pv=None, scale=None, rows=None):
+    B, Hq, D = q.shape
+    Hkv = k.shape[1]
+    G = Hq // Hkv
+    for b in range(B) if rows is None else rows:
+        n = lens[b]
+        for g in range(Hkv):
+            kk, vv = k[b, g, :n], v[b, g, :n]
+            if pk is not None:
+                kk, vv = torch.cat([pk[g], kk]), torch.cat([pv[g], vv])
+            heads = range(g * G, (g + 1) * G)
+            if kk.shape[0] == 0:
+                assert (o[b, list(heads)] == 0).all() and (lse[b, list(heads)] == -INF).all()
+                continue
+            j = torch.arange(kk.shape[0], device="cuda")
+            seen = torch.ones(1, kk.shape[0], dtype=torch.bool, device="cuda")
+            for h in heads:
+                ref = definition(q[b, h:h + 1], kk, vv, j[-1:], j, seen,
+                                 1 / math.sqrt(D) if scale is None else scale, cap,
+                                 None if slopes is None else slopes[h])
+                check(o[b, h:h + 1], lse[b, h:h + 1], ref, f"b{b} h{h} len {n}")
+
+
+DECODE = [
+    # Hq, Hkv, Ncap, D, cap, bias, lens
+    (1, 1, 1, 64, 0.0, False, [1]),
+    (2, 1, 1, 128, 30.0, True, [1, 0]),
+    (4, 2, 300, 128, 0.0, False, [0, 1, 2, 127, 128, 129, 255, 256, 257, 300]),
+    (8, 2, 513, 64, 40.0, True, [513, 0, 64, 65, 384]),
+    (32, 8, 1023, 128, 50.0, False, [1023]),
+    (14, 2, 700, 64, 0.0, True, [700, 3, 511]),
+    (6, 2, 260, 128, 25.0, True, [260, 1]),
+    (16, 1, 400, 128, 0.0, False, [333, 400]),
+    (64, 1, 200, 64, 30.0, False, [199, 0, 130]),
+    (128, 1, 129, 128, 30.0, True, [129, 128]),
+    (40, 2, 140, 128, 0.0, True, [140, 17]),
+    (4, 4, 20000, 128, 50.0, False, [20000, 5, 9000]),
+    (8, 1, 40000, 64, 0.0, True, [40000, 39]),
+]
+
+
+@pytest.mark.parametrize("case", DECODE, ids=lambda c: "-".join(map(str, c[:6])) + f"-B{len(c[6])}")
+def test_decode_varlen(case):
+    Hq, Hkv, Ncap, D, cap, bias, lens = case
+    B = len(lens)
+    q, k, v = rand(1, (B, Hq, D), 6.0 if cap else 1.0), rand(2, (B, Hkv, Ncap, D)), rand(3, (B, Hkv, Ncap, D))
+    for b, n in enumerate(lens):  # the unused tail may hold anything
+        for x in (k, v):
+            x[b, :, n:] = (NAN, INF, -INF)[b % 3]
+    slopes = alibi(Hq) if bias else None
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_varlen(q, k, v, t, softcap=cap, slopes=slopes)
+    check_decode(o, lse, q, k, v, lens, cap, slopes)
+    o2, lse2 = attn.decode_varlen(q, k, v, t, softcap=cap, slopes=slopes)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_varlen_clamps_lengths_and_takes_none():
+    q, k, v = rand(1, (3, 4, 64)), rand(2, (3, 2, 200, 64)), rand(3, (3, 2, 200, 64))
+    t = torch.tensor([-7, 2**31 - 1, -2**31], dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_varlen(q, k, v, t)
+    check_decode(o, lse, q, k, v, [0, 200, 0], 0.0, None)
+    o, lse = attn.decode_varlen(q, k, v)
+    check_decode(o, lse, q, k, v, [200] * 3, 0.0, None)
+
+
+def test_decode_varlen_is_decode():
+    q, k, v = rand(1, (2, 8, 128)), rand(2, (2, 2, 999, 128)), rand(3, (2, 2, 999, 128))
+    o, lse = attn.decode_varlen(q, k, v)
+    ro, rl = attn.decode(q, k, v, nsplit=4)
+    assert (o.float() - ro.float()).abs().max() <= 2.0**-6 and (lse - rl).abs().max() <= 1e-4
+
+
+PREFIX = [
+    # Hq, Hkv, Np, Ncap, D, cap, bias, lens
+    (1, 1, 1, 1, 64, 0.0, False, [0]),
+    (2, 1, 1, 4, 128, 30.0, True, [4, 0, 1]),
+    (4, 2, 128, 130, 128, 0.0, False, [0, 1, 128, 129, 130]),
+    (8, 1, 1001, 200, 64, 0.0, True, [1, 200, 50, 0, 77]),
+    (32, 8, 700, 150, 128, 50.0, False, list(range(0, 150, 4))),
+    (7, 1, 513, 40, 64, 30.0, True, [40, 0, 13] * 13),       # 7 heads: 18 requests to a query tile
+    (12, 4, 400, 64, 128, 0.0, False, [64, 1] * 50),         # 3 heads, 42 requests to a tile
+    (80, 1, 300, 20, 128, 20.0, False, [20, 3, 0, 9]),       # a tile holds one request
+    (128, 1, 200, 129, 64, 0.0, True, [129, 0, 5]),
+    (16, 2, 5000, 300, 128, 0.0, False, [300, 20] * 40),
+    (4, 1, 20000, 10, 64, 40.0, True, [10, 0]),
+]
+
+
+@pytest.mark.parametrize("case", PREFIX, ids=lambda c: "-".join(map(str, c[:7])) + f"-B{len(c[7])}")
+def test_decode_prefix(case):
+    Hq, Hkv, Np, Ncap, D, cap, bias, lens = case
+    B = len(lens)
+    q = rand(1, (B, Hq, D), 6.0 if cap else 1.0)
+    k, v = rand(2, (B, Hkv, Ncap, D)), rand(3, (B, Hkv, Ncap, D))
+    pk, pv = rand(4, (Hkv, Np, D)), rand(5, (Hkv, Np, D))
+    for b, n in enumerate(lens):
+        for x in (k, v):
+            x[b, :, n:] = (NAN, INF, -INF)[b % 3]
+    slopes = alibi(Hq) if bias else None
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_prefix(q, pk, pv, k, v, t, softcap=cap, slopes=slopes)
+    check_decode(o, lse, q, k, v, lens, cap, slopes, pk, pv)
+    o2, lse2 = attn.decode_prefix(q, pk, pv, k, v, t, softcap=cap, slopes=slopes)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("slope", [0.25, -0.25])
+def test_decode_bias_of_both_signs(slope):
+    lens = [900, 0, 3]
+    q, k, v = rand(1, (3, 4, 64)), rand(2, (3, 2, 900, 64)), rand(3, (3, 2, 900, 64))
+    pk, pv = rand(4, (2, 3000, 64)), rand(5, (2, 3000, 64))
+    slopes = torch.tensor([slope, -slope, slope / 50, 0.0], device="cuda")
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_prefix(q, pk, pv, k, v, t, slopes=slopes)
+    check_decode(o, lse, q, k, v, lens, 0.0, slopes, pk, pv)
+    o, lse = attn.decode_varlen(q, k, v, t, slopes=slopes)
+    check_decode(o, lse, q, k, v, lens, 0.0, slopes)
+
+
+def test_many_requests():
+    B, Hq, Hkv, D, Ncap = 700, 4, 2, 64, 33
+    lens = [(17 * b) % 34 for b in range(B)]
+    q, k, v = rand(1, (B, Hq, D)), rand(2, (B, Hkv, Ncap, D)), rand(3, (B, Hkv, Ncap, D))
+    pk, pv = rand(4, (Hkv, 129, D)), rand(5, (Hkv, 129, D))
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_varlen(q, k, v, t)
+    check_decode(o, lse, q, k, v, lens, 0.0, None, rows=range(0, B, 9))
+    o, lse = attn.decode_prefix(q, pk, pv, k, v, t)
+    check_decode(o, lse, q, k, v, lens, 0.0, None, pk, pv, rows=range(0, B, 9))
+
+
+def test_cache_offsets_beyond_32_bits():
+    B, Hkv, Ncap, D = 3, 2, 3_000_000, 128  # 2.3e9 elements, 4.6e9 bytes per cache
+    k = torch.zeros(B, Hkv, Ncap, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    lens = [5, 100, 300]
+    for b, n in enumerate(lens):
+        k[b, :, :n] = rand(10 + b, (Hkv, n, D))
+        v[b, :, :n] = rand(20 + b, (Hkv, n, D))
+    q = rand(1, (B, 4, D))
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_varlen(q, k, v, t)
+    check_decode(o, lse, q, k, v, lens, 0.0, None)
+    # a cache that is full to its end
+    t = torch.tensor([0, 0, Ncap], dtype=torch.int32, device="cuda")
+    k[2, 1, Ncap - 300:] = rand(30, (300, D))
+    v[2, 1, Ncap - 300:] = rand(31, (300, D))
+    o, lse = attn.decode_varlen(q, k, v, t)
+    check_decode(o, lse, q, k, v, [0, 0, Ncap], 0.0, None, rows=[2])
+
+
+# ------------------------------------------------------------------------------ together
+
+
+def test_a_prompt_then_tokens_as_a_server_runs_them():
+    """Packed prompts through row_ranges and forward_mod, then decode steps on
+    caches that grow, with and without sharing the prompt: every step is the
+    last row of a prefill of the same tokens."""
+    Hq, Hkv, D, cap, P, T = 8, 2, 128, 30.0, 210, 4
+    slopes = alibi(Hq)
+    q, k, v = rand(1, (1, Hq, P + T, D), 4.0), rand(2, (1, Hkv, P + T, D)), rand(3, (1, Hkv, P + T, D))
+    lens = torch.tensor([[P + T]], dtype=torch.int32, device="cuda")
+    whole, wl = attn.forward_mod(q, k, v, softcap=cap, slopes=slopes,
+                                 ranges=attn.row_ranges(lens, P + T))
+    # the prompt in two chunks
+    for a, b in ((0, 100), (100, P)):
+        o, l = attn.forward_mod(q[:, :, a:b].contiguous(), k[:, :, :b].contiguous(),
+                                v[:, :, :b].contiguous(), causal=True, q_offset=a, softcap=cap,
+                                slopes=slopes)
+        assert (o.float() - whole[:, :, a:b].float()).abs().max() <= 2.0**-5
+        assert (l - wl[:, :, a:b]).abs().max() <= 1e-4
+    kc = torch.full((1, Hkv, 300, D), NAN, dtype=torch.bfloat16, device="cuda")
+    vc, ks, vs = kc.clone(), kc.clone(), kc.clone()
+    kc[:, :, :P], vc[:, :, :P] = k[:, :, :P], v[:, :, :P]
+    for t in range(T):
+        kc[:, :, P + t], vc[:, :, P + t] = k[:, :, P + t], v[:, :, P + t]
+        ks[:, :, t], vs[:, :, t] = k[:, :, P + t], v[:, :, P + t]
+        q1 = q[:, :, P + t].contiguous()
+        n = torch.tensor([P + t + 1], dtype=torch.int32, device="cuda")
+        for o, l in (attn.decode_varlen(q1, kc, vc, n, softcap=cap, slopes=slopes),
+                     attn.decode_prefix(q1, k[0, :, :P].contiguous(), v[0, :, :P].contiguous(), ks, vs,
+                                        n - P, softcap=cap, slopes=slopes)):
+            assert (o.float() - whole[:, :, P + t].float()).abs().max() <= 2.0**-5
+            assert (l - wl[:, :, P + t]).abs().max() <= 1e-4
+
+
+def _busy(s):
+    with torch.cuda.stream(s):
+        a = torch.ones(4096, 4096, device="cuda")
+        for _ in range(20):
+            a = a @ a * 1e-4
+    return a
+
+
+def test_calls_on_other_streams_at_once():
+    """Two streams that run the calls at the same time, one of them named by
+    its handle; scratch is never shared between them."""
+    sets = []
+    for i in range(2):
+        lens = [500 - 90 * i, 3, 77 + i]
+        sets.append((rand(i, (3, 8, 64)), rand(10 + i, (3, 2, 500, 64)), rand(20 + i, (3, 2, 500, 64)),
+                     rand(30 + i, (2, 900, 64)), rand(40 + i, (2, 900, 64)), lens,
+                     torch.tensor(lens, dtype=torch.int32, device="cuda")))
+    x = rand(50, (1, 2, 300, 64))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for r in range(6):
+        for i, s in enumerate(streams):
+            q, k, v, pk, pv, lens, t = sets[i]
+            h = s if i else s.cuda_stream
+            outs.append((i, True, attn.decode_prefix(q, pk, pv, k, v, t, stream=h)))
+            outs.append((i, False, attn.decode_varlen(q, k, v, t, stream=h)))
+    f = attn.forward_mod(x, x, x, causal=True, stream=streams[0])
+    torch.cuda.synchronize()
+    for i, prefix, (o, lse) in outs:
+        q, k, v, pk, pv, lens, t = sets[i]
+        check_decode(o, lse, q, k, v, lens, 0.0, None, *((pk, pv) if prefix else ()))
+    check_fwd(*f, x, x, x, True, 1 / 8, 0.0, None, None, 0)
+
+
+def test_inputs_written_on_the_call_s_stream_just_before():
+    s = torch.cuda.Stream()
+    q, k, v = rand(1, (2, 4, 64)), rand(2, (2, 2, 300, 64)), rand(3, (2, 2, 300, 64))
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    kk = torch.zeros_like(k)
+    torch.cuda.synchronize()
+    keep = _busy(s)
+    with torch.cuda.stream(s):
+        kk.copy_(k)
+        lens.copy_(torch.tensor([300, 41], dtype=torch.int32, device="cuda"))
+        o, lse = attn.decode_varlen(q, kk, v, lens)
+    s.synchronize()
+    del keep
+    check_decode(o, lse, q, k, v, [300, 41], 0.0, None)
+
+
+def test_captured_calls_follow_the_lengths_and_share_nothing():
+    """Two graphs of decode steps, replayed at the same time on two streams
+    while the lengths on the device grow, and a captured prefill."""
+    B, Hq, Hkv, Ncap, D = 3, 8, 2, 400, 128
+    sets = []
+    for i in range(2):
+        sets.append(dict(q=rand(i, (B, Hq, D)), k=rand(10 + i, (B, Hkv, Ncap, D)),
+                         v=rand(20 + i, (B, Hkv, Ncap, D)), pk=rand(30 + i, (Hkv, 600, D)),
+                         pv=rand(40 + i, (Hkv, 600, D)),
+                         t=torch.zeros(B, dtype=torch.int32, device="cuda")))
+    x = rand(60, (1, 2, 300, D))
+    docs = torch.tensor([[100, 200]], dtype=torch.int32, device="cuda")
+    attn.decode_varlen(sets[0]["q"], sets[0]["k"], sets[0]["v"], sets[0]["t"])
+    torch.cuda.synchronize()
+    graphs = []
+    for i, c in enumerate(sets):
+        s = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            c["a"] = attn.decode_varlen(c["q"], c["k"], c["v"], c["t"], softcap=30.0)
+            c["b"] = attn.decode_prefix(c["q"], c["pk"], c["pv"], c["k"], c["v"], c["t"], softcap=30.0)
+            if i == 0:
+                c["f"] = attn.forward_mod(x, x, x, ranges=attn.row_ranges(docs, 300))
+        graphs.append((g, s))
+    for step in range(3):
+        lens = [[step, 128 * step + 5, 399], [400, step + 1, 0]]
+        for i, c in enumerate(sets):
+            c["t"].copy_(torch.tensor(lens[i], dtype=torch.int32))
+        docs.copy_(torch.tensor([[100 + step, 150]], dtype=torch.int32))
+        torch.cuda.synchronize()
+        for g, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+                g.replay()
+        torch.cuda.synchronize()
+        for i, c in enumerate(sets):
+            check_decode(*c["a"], c["q"], c["k"], c["v"], lens[i], 30.0, None)
+            check_decode(*c["b"], c["q"], c["k"], c["v"], lens[i], 30.0, None, c["pk"], c["pv"])
+        r = ranges_definition([[100 + step, 150]], None, 300, True).cuda()
+        check_fwd(*sets[0]["f"], x, x, x, False, 1 / math.sqrt(D), 0.0, None, r, 0)
+
+
+def test_helpers_refuse_wrong_tensors():
+    q, k = rand(1, (1, 4, 16, 64)), rand(2, (1, 2, 16, 64))
+    q1 = rand(1, (1, 4, 64))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bad = [
+        (ValueError, lambda: attn.forward_mod(q.transpose(1, 2), k, k)),
+        (ValueError, lambda: attn.forward_mod(q, k, k[:, :, :8].contiguous())),
+        (ValueError, lambda: attn.forward_mod(q, k, k, slopes=torch.zeros(3, device="cuda"))),
+        (TypeError, lambda: attn.forward_mod(q, k, k, slopes=torch.zeros(4, device="cuda").double())),
+        (ValueError, lambda: attn.forward_mod(q, k, k, slopes=torch.zeros(4))),
+        (ValueError, lambda: attn.forward_mod(q, k, k, ranges=torch.zeros(1, 15, 2, **i32))),
+        (TypeError, lambda: attn.forward_mod(q, k, k, ranges=torch.zeros(1, 16, 2, device="cuda"))),
+        (ValueError, lambda: attn.forward_mod(q, k, k, ranges=torch.zeros(1, 2, 16, **i32).transpose(1, 2))),
+        (attn.AttnError, lambda: attn.forward_mod(q, k, k, q_offset=-1)),
+        (attn.AttnError, lambda: attn.forward_mod(q, k, k, softcap=-1.0)),
+        (ValueError, lambda: attn.decode_varlen(q1, k, k, torch.zeros(2, **i32))),
+        (TypeError, lambda: attn.decode_varlen(q1, k, k, torch.zeros(1, device="cuda").long())),
+        (ValueError, lambda: attn.decode_prefix(q1, k[0], k[0][:, :8].contiguous(), k, k)),
+        (ValueError, lambda: attn.decode_prefix(q1, k[0, :1], k[0, :1], k, k)),
+        (attn.AttnError, lambda: attn.row_ranges(torch.zeros(1, 2, **i32), 0)),
+    ]
+    for error, call in bad:
+        with pytest.raises(error):
+            call()
