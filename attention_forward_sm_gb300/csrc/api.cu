@@ -90,6 +90,24 @@ int encode_3d(CUtensorMap* map, const void* base, int D, int N, long long BH) {
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_TMA;
 }
 
+// 4-D view [B, Hkv, G, D] of a contiguous bf16 tensor, box {64, G, 1, requests},
+// 128-byte swizzle: the G query heads of a KV head, of `requests` requests, as
+// consecutive rows of a tile.
+int encode_4d(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B, int requests) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn;
+  if (int rc = encode_fn(&fn)) return rc;
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(G),
+                        static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(B)};
+  cuuint64_t strides[3] = {row, row * G, row * G * Hkv};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(requests)};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_TMA;
+}
+
 // 3-D view [BH, rows, inner] of a contiguous e4m3 tensor (bytes), box
 // {128, 128, 1}, 128-byte swizzle.  `inner` * 1 byte must be a multiple of 16.
 int encode_3d_e4m3(CUtensorMap* map, const void* base, int inner, int rows, long long BH) {
@@ -123,6 +141,15 @@ __global__ void selftest_wait_kernel(unsigned int* err, uint64_t limit_ns) {
 }
 
 }  // namespace
+
+int encode_rows(CUtensorMap* map, const void* base, int D, int N, long long BH) {
+  return encode_3d(map, base, D, N, BH);
+}
+
+int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B,
+                   int requests) {
+  return encode_4d(map, base, D, G, Hkv, B, requests);
+}
 
 int check_device() {
   DeviceState* st = nullptr;

@@ -1,5 +1,5 @@
-// Partial-state scratch of attn_decode_splitkv / attn_decode_splitkv_states:
-// a small per-device cache of device buffers, one per recently used stream,
+// Partial-state scratch of the split decodes (attn_decode_splitkv, _states,
+// attn_decode_varlen, attn_decode_prefix): a small per-device cache of device buffers, one per recently used stream,
 // so that a decode step allocates nothing once its stream has been seen.
 //
 // Why: a stream-ordered cudaMallocAsync + cudaFreeAsync pair around the two
@@ -43,34 +43,28 @@ struct Cache {
 };
 Cache g_cache[kMaxDevices];
 
-int plain_path(DecodeParams& p, size_t bytes, size_t o_bytes, cudaStream_t stream) {
+int plain_path(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
+               void* ctx) {
   void* ws = nullptr;
   if (cudaMallocAsync(&ws, bytes, stream) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_ALLOC;
   }
-  p.ws_o = static_cast<float*>(ws);
-  p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + o_bytes);
-  int rc = ATTN_OK;
-  if (launch_decode_split(p, stream) != cudaSuccess ||
-      launch_decode_combine(p, stream) != cudaSuccess)
-    rc = ATTN_ERR_LAUNCH;
+  int rc = launch(ctx, ws, stream);
   if (cudaFreeAsync(ws, stream) != cudaSuccess && rc == ATTN_OK) rc = ATTN_ERR_CUDA;
   return rc;
 }
 
 }  // namespace
 
-int decode_with_cached_scratch(DecodeParams& p, cudaStream_t stream) {
-  if (int rc = decode_bind_device(&p)) return rc;
-  size_t o_bytes = 0;
-  const size_t bytes = decode_scratch_bytes(p, &o_bytes);
+int with_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
+                 void* ctx) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_CUDA;
   }
-  if (cap != cudaStreamCaptureStatusNone) return plain_path(p, bytes, o_bytes, stream);
+  if (cap != cudaStreamCaptureStatusNone) return plain_path(bytes, stream, launch, ctx);
 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
@@ -119,15 +113,31 @@ int decode_with_cached_scratch(DecodeParams& p, cudaStream_t stream) {
     en->bytes = bytes;
   }
   en->last_use = ++c.tick;
-  p.ws_o = static_cast<float*>(en->ptr);
-  p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(en->ptr) + o_bytes);
-  int rc = ATTN_OK;
-  if (launch_decode_split(p, stream) != cudaSuccess ||
-      launch_decode_combine(p, stream) != cudaSuccess)
-    rc = ATTN_ERR_LAUNCH;
+  int rc = launch(ctx, en->ptr, stream);
   // recorded even after a failed launch: whatever did get queued is covered
   if (cudaEventRecord(en->done, stream) != cudaSuccess && rc == ATTN_OK) rc = ATTN_ERR_CUDA;
   return rc;
+}
+
+int decode_with_cached_scratch(DecodeParams& p, cudaStream_t stream) {
+  if (int rc = decode_bind_device(&p)) return rc;
+  struct Ctx {
+    DecodeParams* p;
+    size_t o_bytes;
+  } ctx = {&p, 0};
+  const size_t bytes = decode_scratch_bytes(p, &ctx.o_bytes);
+  return with_scratch(
+      bytes, stream,
+      [](void* c, void* ws, cudaStream_t s) -> int {
+        DecodeParams& p = *static_cast<Ctx*>(c)->p;
+        p.ws_o = static_cast<float*>(ws);
+        p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + static_cast<Ctx*>(c)->o_bytes);
+        return launch_decode_split(p, s) == cudaSuccess &&
+                       launch_decode_combine(p, s) == cudaSuccess
+                   ? ATTN_OK
+                   : ATTN_ERR_LAUNCH;
+      },
+      &ctx);
 }
 
 }  // namespace attn

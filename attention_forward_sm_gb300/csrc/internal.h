@@ -88,6 +88,55 @@ struct ModDecodeParams {
   ScoreMod mod;
 };
 
+// Launch parameters of mod_attn_kernel (mod_sm103a.cuh), prefill and decode.
+struct ModKernelParams {
+  // K and V: [BH, N, D], box {64, 128, 1}.  Q: prefill the same; decode
+  // [B, Hkv, G, D] with box {64, G, 1, per_tile} (tmap_q) or {64, G, 1, 1}
+  // (tmap_q1).  128-byte swizzle.
+  CUtensorMap tmap_q, tmap_q1, tmap_k, tmap_v, tmap_kp, tmap_vp;
+  void* o;
+  float* lse;
+  const int* ranges;
+  const int* lens;
+  int B, Hq, Hkv, G, Nq, Nk;  // Nk: keys (prefill) or the caches' capacity (decode)
+  int causal, q_offset;
+  int longest_first, group_heads;  // prefill: order of the work items
+  int Np, prefix_tiles;            // shared prefix: keys, key tiles
+  int row_blocks, per_tile;        // its items per KV head; requests per query tile
+  int pre_rows;                    // rows of a prefix item's partial states
+  float* pre_o;                    // partial states of prefix items: [slot, pre_rows, D]
+  float* pre_lse;                  // (log2 units, bias relative to its reference)
+  float* part_o;                   // of the requests' own keys: [slot, G, D]
+  float* part_lse;
+  long long* plan;                 // [B + 1] own-key tiles in front of every request
+  float scale_log2;
+  ScoreMod mod;
+  unsigned int* err;
+  uint64_t wait_limit_ns;
+};
+
+// Key tiles per CTA when `total` tiles are dealt to `ctas` CTAs in equal runs.
+__host__ __device__ inline long long split_run(long long total, unsigned ctas) {
+  return (total + ctas - 1) / ctas;
+}
+
+// One launch each, by head size and modifications.
+cudaError_t launch_mod_fwd_d64(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_fwd_d128(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d64(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d128(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+
+// 3-D bf16 view [BH, N, D], box {64, 128, 1}; 4-D view [B, Hkv, G, D] of the
+// queries of a decode, box {64, G, 1, requests}.  Return an ATTN_* status.
+int encode_rows(CUtensorMap* map, const void* base, int D, int N, long long BH);
+int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B, int requests);
+
+// Device scratch of `bytes` for the kernels that launch(ctx, scratch, stream)
+// queues on `stream`: the stream's cached buffer or, during capture, one of the
+// graph's own.  Returns launch's status or an ATTN_ERR_*.
+int with_scratch(size_t bytes, cudaStream_t stream,
+                 int (*launch)(void* ctx, void* scratch, cudaStream_t stream), void* ctx);
+
 // Check the device and queue the kernels; arguments are checked before.
 // Return an ATTN_* status.
 int mod_fwd(const ModFwdParams& p, cudaStream_t stream);

@@ -1,0 +1,267 @@
+// Host side of mod_attn_kernel: tensor maps, the plan of a decode, its scratch,
+// and the kernel that merges a decode's partial states.
+#include <cuda_bf16.h>
+#include <limits.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/attn.h"
+#include "score_mod.cuh"
+
+namespace attn {
+namespace {
+
+int sm_count(int* out) {
+  static std::atomic<int> count[64];  // zero-initialised: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
+  int n = count[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    count[dev].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return ATTN_OK;
+}
+
+// One warp per (request, query head): merges the row's partial states,
+//   L = log2 sum_c 2^(lse_c),  O = sum_c 2^(lse_c - L) O_c,
+// those of the shared prefix's item and those of the request's own item.  The
+// run of key tiles per CTA gives every item's first and last CTA, and with it
+// its slots.  A lane holds D / 32 consecutive elements of O; the states are
+// few and in L2, so the loads of up to four of them are in flight at once and
+// nothing else is shared.
+template <int D>
+__global__ void __launch_bounds__(256) mod_combine_kernel(const ModKernelParams p, unsigned ctas) {
+  constexpr int E = D / 32;
+  // programmatic dependent launch: wait for the split kernel's results
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= static_cast<long long>(p.B) * p.Hq) return;
+  const int b = static_cast<int>(row / p.Hq), h = static_cast<int>(row % p.Hq);
+  const int hkv = h / p.G, g = h % p.G;
+  const long long prefix = static_cast<long long>(p.Hkv) * p.row_blocks * p.prefix_tiles;
+  const long long run = split_run(prefix + p.plan[p.B] * p.Hkv, ctas);
+
+  // the row's parts: count and first row of each of the two groups, rows of a
+  // group one slot apart
+  long long first[2] = {0, 0};
+  int count[2] = {0, 0};
+  if (p.prefix_tiles > 0) {
+    const int item = hkv * p.row_blocks + b / (2 * p.per_tile);
+    const long long t0 = static_cast<long long>(item) * p.prefix_tiles;
+    const long long c0 = t0 / run;
+    count[0] = static_cast<int>((t0 + p.prefix_tiles - 1) / run - c0) + 1;
+    const int in_tile = b % p.per_tile, tile = (b / p.per_tile) & 1;
+    first[0] = (item + c0) * p.pre_rows + tile * 128 + in_tile * p.G + g;
+  }
+  const long long before = p.plan[b], nt = p.plan[b + 1] - before;
+  if (nt > 0) {
+    const long long t0 = prefix + before * p.Hkv + hkv * nt;
+    const long long c0 = t0 / run;
+    count[1] = static_cast<int>((t0 + nt - 1) / run - c0) + 1;
+    first[1] = (static_cast<long long>(b) * p.Hkv + hkv + c0) * p.G + g;
+  }
+  const int total = count[0] + count[1];
+  auto lse_of = [&](int i) {
+    return i < count[0] ? p.pre_lse[first[0] + static_cast<long long>(i) * p.pre_rows]
+                        : p.part_lse[first[1] + static_cast<long long>(i - count[0]) * p.G];
+  };
+  float m = -CUDART_INF_F;
+  for (int i = lane; i < total; i += 32) {
+    const float x = lse_of(i);
+    m = x != x || m != m ? x + m : fmaxf(m, x);  // a NaN state stays one
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d /= 2) {
+    const float x = __shfl_xor_sync(0xFFFFFFFFu, m, d);
+    m = x != x || m != m ? x + m : fmaxf(m, x);
+  }
+  const bool none = m == -CUDART_INF_F;
+  float sum = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  if (!none) {
+    for (int i0 = 0; i0 < total; i0 += 32) {
+      const float w_lane = i0 + lane < total ? ex2_approx(lse_of(i0 + lane) - m) : 0.f;
+      sum += w_lane;
+      const int n = min(32, total - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float w = __shfl_sync(0xFFFFFFFFu, w_lane, i);
+        const int at = i0 + i;
+        const float* src =
+            at < count[0]
+                ? p.pre_o + (first[0] + static_cast<long long>(at) * p.pre_rows) * D
+                : p.part_o + (first[1] + static_cast<long long>(at - count[0]) * p.G) * D;
+        float x[E];
+        if constexpr (E == 4)
+          *reinterpret_cast<float4*>(x) = reinterpret_cast<const float4*>(src)[lane];
+        else
+          *reinterpret_cast<float2*>(x) = reinterpret_cast<const float2*>(src)[lane];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[e], o[e]);
+      }
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  }
+  const float inv = none ? 0.f : 1.f / sum;
+  uint32_t out[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D) +
+                  lane * (E / 2);
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  else
+    *dst = out[0];
+  if (lane == 0) {
+    float lse = none ? -CUDART_INF_F : (m + __log2f(sum)) * kLn2;
+    // a negative slope is relative to the farthest key
+    if (p.mod.slopes && !none && p.mod.slopes[h] < 0.f) {
+      const int len = p.lens ? min(max(p.lens[b], 0), p.Nk) : p.Nk;
+      lse -= p.mod.slopes[h] * static_cast<float>(p.Np + len - 1);
+    }
+    p.lse[row] = lse;
+  }
+}
+
+template <int D>
+cudaError_t launch_combine(const ModKernelParams& p, unsigned ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  const long long rows = static_cast<long long>(p.B) * p.Hq;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mod_combine_kernel<D>, p, ctas);
+}
+
+void common_params(ModKernelParams* k, const ScoreMod& mod) {
+  k->mod = mod;
+  k->scale_log2 = mod.scale * kLog2e;
+  k->err = device_error_word();
+  k->wait_limit_ns = wait_limit_ns();
+}
+
+struct DecodeLaunch {
+  ModKernelParams* k;
+  int D;
+  unsigned ctas;
+  size_t pre_o, pre_lse, part_o, part_lse;  // offsets into the scratch; plan at 0
+};
+
+int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
+  const DecodeLaunch& d = *static_cast<DecodeLaunch*>(ctx);
+  char* base = static_cast<char*>(scratch);
+  d.k->plan = reinterpret_cast<long long*>(base);
+  d.k->pre_o = reinterpret_cast<float*>(base + d.pre_o);
+  d.k->pre_lse = reinterpret_cast<float*>(base + d.pre_lse);
+  d.k->part_o = reinterpret_cast<float*>(base + d.part_o);
+  d.k->part_lse = reinterpret_cast<float*>(base + d.part_lse);
+  cudaError_t e;
+  if (d.D == 128) {
+    e = launch_mod_split_d128(*d.k, d.ctas, stream);
+    if (e == cudaSuccess) e = launch_combine<128>(*d.k, d.ctas, stream);
+  } else {
+    e = launch_mod_split_d64(*d.k, d.ctas, stream);
+    if (e == cudaSuccess) e = launch_combine<64>(*d.k, d.ctas, stream);
+  }
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int mod_fwd(const ModFwdParams& p, cudaStream_t stream) {
+  if (int rc = check_device()) return rc;
+  ModKernelParams k = {};
+  if (int rc = encode_rows(&k.tmap_q, p.q, p.D, p.Nq, static_cast<long long>(p.B) * p.Hq))
+    return rc;
+  if (int rc = encode_rows(&k.tmap_k, p.k, p.D, p.Nk, static_cast<long long>(p.B) * p.Hkv))
+    return rc;
+  if (int rc = encode_rows(&k.tmap_v, p.v, p.D, p.Nk, static_cast<long long>(p.B) * p.Hkv))
+    return rc;
+  k.o = p.o;
+  k.lse = p.lse;
+  k.ranges = p.ranges;
+  k.B = p.B;
+  k.Hq = p.Hq;
+  k.Hkv = p.Hkv;
+  k.G = p.Hq / p.Hkv;
+  k.Nq = p.Nq;
+  k.Nk = p.Nk;
+  k.causal = p.causal;
+  k.q_offset = p.q_offset;
+  // Rows that see different keys: items of later rows, as a rule the longer
+  // ones, first, in groups of heads whose K and V take about a third of the
+  // L2 (as in fwd_sm103a.cu).
+  k.longest_first = p.causal || p.ranges;
+  const double kv_bytes = 4.0 * p.Nk * p.D;
+  const int kv_heads = std::max(1, std::min(static_cast<int>(40.0e6 / kv_bytes), p.B * p.Hkv));
+  k.group_heads = kv_heads * k.G;
+  common_params(&k, p.mod);
+  const unsigned grid =
+      static_cast<unsigned>((p.Nq + 255ll) / 256 * p.B * p.Hq);
+  const cudaError_t e = p.D == 128 ? launch_mod_fwd_d128(k, grid, stream)
+                                   : launch_mod_fwd_d64(k, grid, stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
+  if (int rc = check_device()) return rc;
+  ModKernelParams k = {};
+  k.G = p.Hq / p.Hkv;
+  k.per_tile = 128 / k.G;
+  if (int rc = encode_queries(&k.tmap_q1, p.q, p.D, k.G, p.Hkv, p.B, 1)) return rc;
+  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  if (int rc = encode_rows(&k.tmap_k, p.kcache, p.D, p.Ncap, heads)) return rc;
+  if (int rc = encode_rows(&k.tmap_v, p.vcache, p.D, p.Ncap, heads)) return rc;
+  k.row_blocks = (p.B + 2 * k.per_tile - 1) / (2 * k.per_tile);
+  if (p.Np > 0) {
+    if (int rc = encode_queries(&k.tmap_q, p.q, p.D, k.G, p.Hkv, p.B, k.per_tile)) return rc;
+    if (int rc = encode_rows(&k.tmap_kp, p.kprefix, p.D, p.Np, p.Hkv)) return rc;
+    if (int rc = encode_rows(&k.tmap_vp, p.vprefix, p.D, p.Np, p.Hkv)) return rc;
+    k.prefix_tiles = (p.Np + 127) / 128;
+  }
+  k.pre_rows = p.B <= k.per_tile ? p.B * k.G : 256;
+  k.o = p.o;
+  k.lse = p.lse;
+  k.lens = p.lens;
+  k.B = p.B;
+  k.Hq = p.Hq;
+  k.Hkv = p.Hkv;
+  k.Nk = p.Ncap;
+  k.Np = p.Np;
+  common_params(&k, p.mod);
+
+  int sms = 0;
+  if (int rc = sm_count(&sms)) return rc;
+  const long long prefix_items =
+      p.Np > 0 ? static_cast<long long>(p.Hkv) * k.row_blocks : 0;
+  const long long most_tiles = prefix_items * k.prefix_tiles + heads * ((p.Ncap + 127ll) / 128);
+  DecodeLaunch d = {};
+  d.k = &k;
+  d.D = p.D;
+  d.ctas = static_cast<unsigned>(std::min<long long>(sms, most_tiles));
+  // slot of a state: its item's number + its CTA's
+  const size_t pre = p.Np > 0 ? static_cast<size_t>(prefix_items + d.ctas) * k.pre_rows : 0;
+  const size_t own = static_cast<size_t>(heads + d.ctas) * k.G;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  d.pre_o = up((static_cast<size_t>(p.B) + 1) * sizeof(long long));
+  d.pre_lse = d.pre_o + up(pre * p.D * sizeof(float));
+  d.part_o = d.pre_lse + up(pre * sizeof(float));
+  d.part_lse = d.part_o + up(own * p.D * sizeof(float));
+  const size_t bytes = d.part_lse + up(own * sizeof(float));
+  return with_scratch(bytes, stream, launch_decode, &d);
+}
+
+}  // namespace attn
