@@ -93,7 +93,9 @@ struct ModKernelParams {
   // K and V: [BH, N, D], box {64, 128, 1}.  Q: prefill the same; decode
   // [B, Hkv, G, D] with box {64, G, 1, per_tile} (tmap_q) or {64, G, 1, 1}
   // (tmap_q1).  128-byte swizzle.
-  CUtensorMap tmap_q, tmap_q1, tmap_k, tmap_v, tmap_kp, tmap_vp;
+  // Prefix: tmap_kp, tmap_vp; the last tile of a request's keys: tmap_kt,
+  // tmap_vt, box {64, 32, 1}.
+  CUtensorMap tmap_q, tmap_q1, tmap_k, tmap_v, tmap_kp, tmap_vp, tmap_kt, tmap_vt;
   void* o;
   float* lse;
   const int* ranges;
@@ -108,16 +110,28 @@ struct ModKernelParams {
   float* pre_lse;                  // (log2 units, bias relative to its reference)
   float* part_o;                   // of the requests' own keys: [slot, G, D]
   float* part_lse;
-  long long* plan;                 // [B + 1] own-key tiles in front of every request
+  uint32_t* plan;                  // [B + 1] own-key tiles in front of every request
   float scale_log2;
   ScoreMod mod;
   unsigned int* err;
   uint64_t wait_limit_ns;
 };
 
-// Key tiles per CTA when `total` tiles are dealt to `ctas` CTAs in equal runs.
-__host__ __device__ inline long long split_run(long long total, unsigned ctas) {
-  return (total + ctas - 1) / ctas;
+// Tiles of all shared prefix items.
+__host__ __device__ inline uint32_t prefix_total(const ModKernelParams& p) {
+  return static_cast<uint32_t>(p.Hkv) * p.row_blocks * p.prefix_tiles;
+}
+// `total` tiles dealt out in `runs` <= total runs, as equal as they can be:
+// the first tile of run r, and the run that holds tile x.  Totals are at most
+// kMostTiles, so that the products fit 32 bits (a 64-bit division takes a warp
+// hundreds of cycles, and the planning of a short decode is most of it).
+constexpr uint32_t kMostTiles = 12000000, kMostCtas = 178;
+static_assert(2ull * kMostCtas * kMostTiles < (1ull << 32), "32-bit products");
+__host__ __device__ inline uint32_t run_start(uint32_t total, uint32_t runs, uint32_t r) {
+  return r * total / runs;
+}
+__host__ __device__ inline uint32_t run_of(uint32_t total, uint32_t runs, uint32_t x) {
+  return ((x + 1) * runs - 1) / total;
 }
 
 // One launch each, by head size and modifications.
@@ -126,9 +140,9 @@ cudaError_t launch_mod_fwd_d128(const ModKernelParams& p, unsigned grid, cudaStr
 cudaError_t launch_mod_split_d64(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
 cudaError_t launch_mod_split_d128(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
 
-// 3-D bf16 view [BH, N, D], box {64, 128, 1}; 4-D view [B, Hkv, G, D] of the
+// 3-D bf16 view [BH, N, D], box {64, rows, 1}; 4-D view [B, Hkv, G, D] of the
 // queries of a decode, box {64, G, 1, requests}.  Return an ATTN_* status.
-int encode_rows(CUtensorMap* map, const void* base, int D, int N, long long BH);
+int encode_rows(CUtensorMap* map, const void* base, int D, int N, long long BH, int rows);
 int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B, int requests);
 
 // Device scratch of `bytes` for the kernels that launch(ctx, scratch, stream)

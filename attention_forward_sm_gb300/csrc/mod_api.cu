@@ -42,6 +42,12 @@ int decode_entry(const void* q, const void* kprefix, const void* vprefix, const 
   if (Hq % Hkv != 0 || Hq / Hkv > 128 || Hq > 65535) return ATTN_ERR_SHAPE;
   if (D != 64 && D != 128) return ATTN_ERR_SHAPE;
   if (static_cast<long long>(B) * Hkv > (1ll << 20)) return ATTN_ERR_SHAPE;
+  // key tiles are numbered in 32 bits: of the caches, and of the prefix times the
+  // blocks of two times 128 / G requests that share it
+  const long long blocks = (B + 2ll * (128 / (Hq / Hkv)) - 1) / (2 * (128 / (Hq / Hkv)));
+  if (static_cast<long long>(B) * Hkv * ((Ncap + 127ll) / 128) > kMostTiles ||
+      Hkv * blocks * ((Np + 127ll) / 128) > kMostTiles)
+    return ATTN_ERR_SHAPE;
   ModDecodeParams p = {};
   if (int rc = score_mod(scale, softcap, slopes, &p.mod)) return rc;
   for (const void* x : {q, kprefix, vprefix, kcache, vcache, static_cast<const void*>(o),

@@ -30,8 +30,8 @@ int sm_count(int* out) {
 // One warp per (request, query head): merges the row's partial states,
 //   L = log2 sum_c 2^(lse_c),  O = sum_c 2^(lse_c - L) O_c,
 // those of the shared prefix's item and those of the request's own item.  The
-// run of key tiles per CTA gives every item's first and last CTA, and with it
-// its slots.  A lane holds D / 32 consecutive elements of O; the states are
+// runs of key tiles give every item's first and last run, and with it its
+// slots.  A lane holds D / 32 consecutive elements of O; the states are
 // few and in L2, so the loads of up to four of them are in flight at once and
 // nothing else is shared.
 template <int D>
@@ -44,27 +44,27 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const ModKernelParams 
   if (row >= static_cast<long long>(p.B) * p.Hq) return;
   const int b = static_cast<int>(row / p.Hq), h = static_cast<int>(row % p.Hq);
   const int hkv = h / p.G, g = h % p.G;
-  const long long prefix = static_cast<long long>(p.Hkv) * p.row_blocks * p.prefix_tiles;
-  const long long run = split_run(prefix + p.plan[p.B] * p.Hkv, ctas);
 
   // the row's parts: count and first row of each of the two groups, rows of a
   // group one slot apart
   long long first[2] = {0, 0};
   int count[2] = {0, 0};
+  const uint32_t before = p.plan[b], nt = p.plan[b + 1] - before, own = p.plan[p.B] * p.Hkv;
   if (p.prefix_tiles > 0) {
+    const uint32_t all = prefix_total(p), runs = min(all, ctas);
     const int item = hkv * p.row_blocks + b / (2 * p.per_tile);
-    const long long t0 = static_cast<long long>(item) * p.prefix_tiles;
-    const long long c0 = t0 / run;
-    count[0] = static_cast<int>((t0 + p.prefix_tiles - 1) / run - c0) + 1;
+    const uint32_t t0 = static_cast<uint32_t>(item) * p.prefix_tiles;
+    const uint32_t r0 = run_of(all, runs, t0);
+    count[0] = static_cast<int>(run_of(all, runs, t0 + p.prefix_tiles - 1) - r0) + 1;
     const int in_tile = b % p.per_tile, tile = (b / p.per_tile) & 1;
-    first[0] = (item + c0) * p.pre_rows + tile * 128 + in_tile * p.G + g;
+    first[0] = static_cast<long long>(item + r0) * p.pre_rows + tile * 128 + in_tile * p.G + g;
   }
-  const long long before = p.plan[b], nt = p.plan[b + 1] - before;
   if (nt > 0) {
-    const long long t0 = prefix + before * p.Hkv + hkv * nt;
-    const long long c0 = t0 / run;
-    count[1] = static_cast<int>((t0 + nt - 1) / run - c0) + 1;
-    first[1] = (static_cast<long long>(b) * p.Hkv + hkv + c0) * p.G + g;
+    const uint32_t runs = min(own, 2 * ctas);
+    const uint32_t t0 = before * p.Hkv + hkv * nt;
+    const uint32_t r0 = run_of(own, runs, t0);
+    count[1] = static_cast<int>(run_of(own, runs, t0 + nt - 1) - r0) + 1;
+    first[1] = (static_cast<long long>(b) * p.Hkv + hkv + r0) * p.G + g;
   }
   const int total = count[0] + count[1];
   auto lse_of = [&](int i) {
@@ -98,13 +98,17 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const ModKernelParams 
             at < count[0]
                 ? p.pre_o + (first[0] + static_cast<long long>(at) * p.pre_rows) * D
                 : p.part_o + (first[1] + static_cast<long long>(at - count[0]) * p.G) * D;
-        float x[E];
-        if constexpr (E == 4)
-          *reinterpret_cast<float4*>(x) = reinterpret_cast<const float4*>(src)[lane];
-        else
-          *reinterpret_cast<float2*>(x) = reinterpret_cast<const float2*>(src)[lane];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, x[e], o[e]);
+        if constexpr (E == 4) {
+          const float4 x = reinterpret_cast<const float4*>(src)[lane];
+          o[0] = fmaf(w, x.x, o[0]);
+          o[1] = fmaf(w, x.y, o[1]);
+          o[2] = fmaf(w, x.z, o[2]);
+          o[3] = fmaf(w, x.w, o[3]);
+        } else {
+          const float2 x = reinterpret_cast<const float2*>(src)[lane];
+          o[0] = fmaf(w, x.x, o[0]);
+          o[1] = fmaf(w, x.y, o[1]);
+        }
       }
     }
 #pragma unroll
@@ -148,7 +152,9 @@ cudaError_t launch_combine(const ModKernelParams& p, unsigned ctas, cudaStream_t
 
 void common_params(ModKernelParams* k, const ScoreMod& mod) {
   k->mod = mod;
-  k->scale_log2 = mod.scale * kLog2e;
+  // Never 0: an unseen score is -inf and has to stay it.  1e-37 times any product
+  // below 1e30 is 0 next to a score's fp32 roundings.
+  k->scale_log2 = std::max(mod.scale * kLog2e, 1e-37f);
   k->err = device_error_word();
   k->wait_limit_ns = wait_limit_ns();
 }
@@ -163,7 +169,7 @@ struct DecodeLaunch {
 int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
   const DecodeLaunch& d = *static_cast<DecodeLaunch*>(ctx);
   char* base = static_cast<char*>(scratch);
-  d.k->plan = reinterpret_cast<long long*>(base);
+  d.k->plan = reinterpret_cast<uint32_t*>(base);
   d.k->pre_o = reinterpret_cast<float*>(base + d.pre_o);
   d.k->pre_lse = reinterpret_cast<float*>(base + d.pre_lse);
   d.k->part_o = reinterpret_cast<float*>(base + d.part_o);
@@ -184,11 +190,11 @@ int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
 int mod_fwd(const ModFwdParams& p, cudaStream_t stream) {
   if (int rc = check_device()) return rc;
   ModKernelParams k = {};
-  if (int rc = encode_rows(&k.tmap_q, p.q, p.D, p.Nq, static_cast<long long>(p.B) * p.Hq))
+  if (int rc = encode_rows(&k.tmap_q, p.q, p.D, p.Nq, static_cast<long long>(p.B) * p.Hq, 128))
     return rc;
-  if (int rc = encode_rows(&k.tmap_k, p.k, p.D, p.Nk, static_cast<long long>(p.B) * p.Hkv))
+  if (int rc = encode_rows(&k.tmap_k, p.k, p.D, p.Nk, static_cast<long long>(p.B) * p.Hkv, 128))
     return rc;
-  if (int rc = encode_rows(&k.tmap_v, p.v, p.D, p.Nk, static_cast<long long>(p.B) * p.Hkv))
+  if (int rc = encode_rows(&k.tmap_v, p.v, p.D, p.Nk, static_cast<long long>(p.B) * p.Hkv, 128))
     return rc;
   k.o = p.o;
   k.lse = p.lse;
@@ -223,13 +229,15 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   k.per_tile = 128 / k.G;
   if (int rc = encode_queries(&k.tmap_q1, p.q, p.D, k.G, p.Hkv, p.B, 1)) return rc;
   const long long heads = static_cast<long long>(p.B) * p.Hkv;
-  if (int rc = encode_rows(&k.tmap_k, p.kcache, p.D, p.Ncap, heads)) return rc;
-  if (int rc = encode_rows(&k.tmap_v, p.vcache, p.D, p.Ncap, heads)) return rc;
+  if (int rc = encode_rows(&k.tmap_k, p.kcache, p.D, p.Ncap, heads, 128)) return rc;
+  if (int rc = encode_rows(&k.tmap_v, p.vcache, p.D, p.Ncap, heads, 128)) return rc;
+  if (int rc = encode_rows(&k.tmap_kt, p.kcache, p.D, p.Ncap, heads, 32)) return rc;
+  if (int rc = encode_rows(&k.tmap_vt, p.vcache, p.D, p.Ncap, heads, 32)) return rc;
   k.row_blocks = (p.B + 2 * k.per_tile - 1) / (2 * k.per_tile);
   if (p.Np > 0) {
     if (int rc = encode_queries(&k.tmap_q, p.q, p.D, k.G, p.Hkv, p.B, k.per_tile)) return rc;
-    if (int rc = encode_rows(&k.tmap_kp, p.kprefix, p.D, p.Np, p.Hkv)) return rc;
-    if (int rc = encode_rows(&k.tmap_vp, p.vprefix, p.D, p.Np, p.Hkv)) return rc;
+    if (int rc = encode_rows(&k.tmap_kp, p.kprefix, p.D, p.Np, p.Hkv, 128)) return rc;
+    if (int rc = encode_rows(&k.tmap_vp, p.vprefix, p.D, p.Np, p.Hkv, 128)) return rc;
     k.prefix_tiles = (p.Np + 127) / 128;
   }
   k.pre_rows = p.B <= k.per_tile ? p.B * k.G : 256;
@@ -251,12 +259,12 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   DecodeLaunch d = {};
   d.k = &k;
   d.D = p.D;
-  d.ctas = static_cast<unsigned>(std::min<long long>(sms, most_tiles));
-  // slot of a state: its item's number + its CTA's
+  d.ctas = static_cast<unsigned>(std::min<long long>({sms, most_tiles, kMostCtas}));
+  // slot of a state: its item's number + its run's
   const size_t pre = p.Np > 0 ? static_cast<size_t>(prefix_items + d.ctas) * k.pre_rows : 0;
-  const size_t own = static_cast<size_t>(heads + d.ctas) * k.G;
+  const size_t own = static_cast<size_t>(heads + 2ll * d.ctas) * k.G;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  d.pre_o = up((static_cast<size_t>(p.B) + 1) * sizeof(long long));
+  d.pre_o = up((static_cast<size_t>(p.B) + 1) * sizeof(uint32_t));
   d.pre_lse = d.pre_o + up(pre * p.D * sizeof(float));
   d.part_o = d.pre_lse + up(pre * sizeof(float));
   d.part_lse = d.part_o + up(own * p.D * sizeof(float));

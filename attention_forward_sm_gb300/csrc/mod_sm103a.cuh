@@ -9,21 +9,24 @@
 // warps, a K/V ring.  What differs:
 //
 //   * A work item names the key tiles that its rows can see (each of the two
-//     query tiles an interval of its own), found by the load warp and handed to
-//     the other roles through shared memory.  Documents far from a row cost it
-//     nothing, and an item that sees nothing is not loaded at all.
-//   * Two spare warps clear the rows of V that lie outside of the item's
-//     visible span in its first and last tile before the MMA reads them: their
-//     weights are 0, but 0 * NaN in a cache's unused tail would not be.
+//     query tiles an interval of its own), found by a planning warp ahead of
+//     the others and handed to them through shared memory.  Documents far from
+//     a row cost it nothing, and an item that sees nothing is not loaded.
+//   * The softmax warps clear the rows of V that lie outside of the item's
+//     visible span in its first and last tile before they release their
+//     weights: those are 0 there, but 0 * NaN in a cache's unused tail is not.
 //   * Prefill (kSplit = false): an item is (batch, head, 256 query rows), handed
 //     out by cluster launch control.
 //   * Decode (kSplit = true): the rows of an item are the query heads that share
 //     a KV head: those of 128 / G requests per tile for the shared prefix, of
-//     one request for its own keys.  The key tiles of all items, laid end to
-//     end, are cut into equal runs, one per CTA, whatever the lengths are; an
-//     item cut by a run's end leaves fp32 partial states that a second kernel
-//     merges through their log-sum-exp.  A prefix tile is read once for 256
-//     rows, and at fewer than ~300 rows its bytes cost more than its products.
+//     one request for its own keys.  The prefix tiles of all items, laid end to
+//     end, are cut into equal runs, one per CTA; so are the tiles of the
+//     requests' own keys, whatever the lengths are, two runs per CTA: one for
+//     each query tile, two chains of Q K^T, softmax and P V that do not wait
+//     for one another.  An item cut by a run's end leaves fp32 partial states
+//     that a second kernel merges through their log-sum-exp.  A prefix tile is
+//     read once for 256 rows, and at fewer than ~300 rows its bytes cost more
+//     than its products.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -38,14 +41,14 @@
 namespace attn {
 namespace {
 
-constexpr int kModThreads = 640;  // 16 softmax warps, load, MMA, 2 warps that clear V edges
-constexpr int kModWarpLoad = 16, kModWarpMma = 17, kModWarpEdge = 18;
-constexpr int kWorkReaders = 19;  // everyone but the load warp
+constexpr int kModThreads = 640;  // 16 softmax warps, load, MMA, 2 planning warps
+constexpr int kModWarpLoad = 16, kModWarpMma = 17, kModWarpPlan = 18;
 // setmaxnreg split of the 61440 registers the launch gets (640 threads x 96)
 constexpr uint32_t kModRegSoftmax = 104, kModRegOther = 64;
 static_assert(4 * 128 * kModRegSoftmax + 128 * kModRegOther <= 640 * 96, "register split");
 
-// One work item, written by the load warp.  Key tiles are relative to tile0.
+// One work item, written by a planning warp, once for each query tile (a decode's
+// own-key items: for the one that has it).  Key tiles are relative to tile0.
 struct Work {
   int n;          // key tiles to load (0: no row sees any key); -1: no more work
   int tile0;      // first key tile
@@ -54,21 +57,27 @@ struct Work {
   int lo, hi;     // visible span of the item
   int id;         // prefill: batch * Hq + head; decode: KV head
   int q0;         // prefill: first query row; decode: first request of tile 0
-  int kind;       // decode: 0 shared prefix, 1 own keys
+  int kind;       // decode: 0 shared prefix, 1 own keys, 2 end of the prefix items
   int slot;       // decode: where its partial states go
+  uint32_t v_first, v_last;  // ring items of V in the first and the last tile
 };
 
+// Items of a query tile in flight: a decode's are short, and planned well ahead;
+// a prefill's are taken from the grid, and only one ahead, which keeps the end
+// of the grid even.
+template <bool kSplit>
+constexpr int kWorkSlots = kSplit ? 4 : 2;
+
 struct ModMisc {
-  uint64_t q_full, q_empty, unit_done;
+  uint64_t q_full[2], q_empty[2], unit_done;
   uint64_t s_full[2], s_read[2], p_full[2], o_done[2];
   uint64_t mma_done;
-  uint64_t edge_next;     // the next V tile of the ring is an edge tile (one phase each)
-  uint64_t v_edge;        // it is cleared (one phase each)
   uint64_t kv_full[8], kv_empty[8];
   uint64_t clc_full;      // the answer to the request for more work arrived
-  uint64_t work_full[2], work_empty[2];
+  uint64_t work_full[2][4], work_empty[2][4];
   uint4 clc_resp;
-  Work work[2];           // item k in slot k % 2
+  Work work[2][4];        // query tile t's item k in slot k % kWorkSlots
+  int4 seen[16];  // per softmax warp: keys [x, y) that all its rows see, [z, w) that any does
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -103,20 +112,47 @@ __device__ __forceinline__ uint64_t cap2(const CapCoef& k, uint64_t x, uint64_t 
   return fma_f32x2(x, t, add);
 }
 
+// Which of a thread's 64 columns its row sees: bit i of words[i / 32].
+struct Seen {
+  uint32_t words[2];
+};
+__device__ __forceinline__ Seen seen_columns(int from, int to) {  // columns [from, to)
+  Seen m;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int f = min(max(from - 32 * h, 0), 32), e = min(max(to - 32 * h, 0), 32);
+    // funnel shifts take 32: all ones from f on, none from e on
+    m.words[h] = e > f ? (__funnelshift_lc(0u, 0xFFFFFFFFu, f)) &
+                             ~(__funnelshift_lc(0u, 0xFFFFFFFFu, e))
+                       : 0u;
+  }
+  return m;
+}
+__device__ __forceinline__ void mask_to(float (&s)[64], const Seen& m, float with) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i) s[i] = (m.words[i / 32] >> (i % 32)) & 1u ? s[i] : with;
+}
+
 // The pass over one tile of 64 scores of a thread (half a row): from raw
-// products s to weights, in place.  Returns by reference the tile's maximum
-// for the row (both halves) in `mx` and leaves s in log2 units (kCap && !kBias:
-// still raw; the cap is applied with the exponential).
+// products s to weights.
 template <bool kCap, bool kBias>
 struct Scores {
-  // kb: key of s[0].  masked: some of the warp's rows do not see all 128 keys.
+  // Modifies the scores and returns the row's maximum (both halves) in log2
+  // units.  kb: key of s[0].  masked: some row of the warp does not see all 128
+  // keys of the tile.  Afterwards `final` says whether s holds scores in log2
+  // units (unseen: -inf) or still raw products (capped ones, none masked,
+  // which get their cap together with the exponential; `poly`: by the
+  // polynomial), or, without cap and bias, raw products with -inf.
   __device__ static __forceinline__ float prepare(float (&s)[64], const ModKernelParams& p,
                                                   const RowInfo& row, int kb, bool masked,
-                                                  bool& poly) {
+                                                  bool& final, bool& poly) {
+    final = kBias || (kCap && masked);
     poly = true;
+    Seen seen;
+    if (masked) seen = seen_columns(row.lo - kb, row.hi - kb);
     if constexpr (kCap) {
-      // the polynomial holds while |x| <= 1; garbage in unseen keys only
-      // chooses the slower path
+      // the polynomial holds while |x| <= 1; what lies at unseen keys has no say
+      if (masked) mask_to(s, seen, 0.f);
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
       for (int i = 0; i < 64; i += 4) {
@@ -124,9 +160,7 @@ struct Scores {
         a1 = max3f(a1, fabsf(s[i + 2]), fabsf(s[i + 3]));
       }
       poly = __all_sync(0xFFFFFFFFu, fmaxf(a0, a1) * p.mod.cap_in <= 1.f);
-    }
-    if constexpr (kBias) {
-      if constexpr (kCap) {
+      if (final) {
         if (poly) {
           const CapCoef c = cap_coef(p.mod.cap_out);
           const uint64_t in2 = f32x2(p.mod.cap_in, p.mod.cap_in), zero = f32x2(0.f, 0.f);
@@ -138,6 +172,8 @@ struct Scores {
           for (int i = 0; i < 64; ++i) s[i] = tanh_any(s[i] * p.mod.cap_in) * p.mod.cap_out;
         }
       }
+    }
+    if constexpr (kBias) {
       const uint64_t mul = kCap ? f32x2(1.f, 1.f) : f32x2(p.scale_log2, p.scale_log2);
       // |pos - j| is linear in j over the keys that the row sees, but where
       // they lie on both sides of pos
@@ -175,12 +211,7 @@ struct Scores {
         }
       }
     }
-    if (masked) {
-      const int from = row.lo - kb, to = row.hi - kb;  // columns [from, to) seen
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (i < from || i >= to) s[i] = -CUDART_INF_F;
-    }
+    if (masked) mask_to(s, seen, -CUDART_INF_F);
     float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]);
     float a2 = fmaxf(s[4], s[5]), a3 = fmaxf(s[6], s[7]);
 #pragma unroll
@@ -192,8 +223,7 @@ struct Scores {
     }
     float mx = max3f(a0, a1, fmaxf(a2, a3));
     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));  // the row's other half
-    if (mx == -CUDART_INF_F) return mx;
-    if constexpr (kBias) return mx;
+    if (final || mx == -CUDART_INF_F) return mx;
     // the cap is monotone: the largest raw score is the largest capped one
     if constexpr (kCap) return tanh_any(mx * p.mod.cap_in) * p.mod.cap_out;
     return mx * p.scale_log2;
@@ -201,9 +231,10 @@ struct Scores {
 
   // pk = 2^(score - m) as bf16 pairs, low key first; returns their sum in
   // fp32 before the rounding to bf16 (2^-9 of a weight on average: its effect
-  // on O is that of the rounding of O itself).  Unseen keys are exactly 0.
+  // on O is that of the rounding of O itself).  Unseen keys are -inf and give
+  // exactly 0 (scale_log2 is never 0, see mod_launch.cu).
   __device__ static __forceinline__ float weights(const float (&s)[64], const ModKernelParams& p,
-                                                  float neg_m, bool masked, bool poly,
+                                                  float neg_m, bool final, bool poly,
                                                   uint32_t (&pk)[32]) {
     const uint64_t negm2 = f32x2(neg_m, neg_m);
     uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
@@ -211,19 +242,14 @@ struct Scores {
       float x0, x1, x2, x3;
       unpack_f32x2(x01, x0, x1);
       unpack_f32x2(x23, x2, x3);
-      float p0 = ex2_approx(x0), p1 = ex2_approx(x1), p2 = ex2_approx(x2), p3 = ex2_approx(x3);
-      if (masked) {  // an unseen score is -inf, but what became of it need not be
-        p0 = s[i] == -CUDART_INF_F ? 0.f : p0;
-        p1 = s[i + 1] == -CUDART_INF_F ? 0.f : p1;
-        p2 = s[i + 2] == -CUDART_INF_F ? 0.f : p2;
-        p3 = s[i + 3] == -CUDART_INF_F ? 0.f : p3;
-      }
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
       acc0 = add_f32x2(acc0, f32x2(p0, p1));
       acc1 = add_f32x2(acc1, f32x2(p2, p3));
       pk[i / 2] = pack_bf16x2(p0, p1);
       pk[i / 2 + 1] = pack_bf16x2(p2, p3);
     };
-    if constexpr (kBias) {
+    if (final) {
 #pragma unroll
       for (int i = 0; i < 64; i += 4)
         emit(i, add_f32x2(f32x2(s[i], s[i + 1]), negm2), add_f32x2(f32x2(s[i + 2], s[i + 3]), negm2));
@@ -258,16 +284,31 @@ struct Scores {
   }
 };
 
-// Everything below indexes a warp's loop over work items: item k is in slot
-// k % 2 from work_full (phase k / 2) until every reader arrived on work_empty.
-__device__ __forceinline__ bool work_wait(ModMisc& ms, const ModKernelParams& p, int k,
+// Query tile t's item k is in slot k % kSlots from work_full (phase k / kSlots)
+// until every reader arrived on work_empty.
+template <int kSlots>
+__device__ __forceinline__ bool work_wait(ModMisc& ms, const ModKernelParams& p, int t, int k,
                                           uint32_t abort_flag, uint32_t site) {
-  return warp_all(mbar_wait(&ms.work_full[k & 1], (k >> 1) & 1, abort_flag, p.err, site,
-                            p.wait_limit_ns));
+  return warp_all(mbar_wait(&ms.work_full[t][k % kSlots], (k / kSlots) & 1, abort_flag, p.err,
+                            site, p.wait_limit_ns));
 }
-__device__ __forceinline__ void work_done(ModMisc& ms, int k, int lane) {
+template <int kSlots>
+__device__ __forceinline__ void work_done(ModMisc& ms, int t, int k, int lane) {
   __syncwarp();
-  if (lane == 0) mbar_arrive(&ms.work_empty[k & 1]);
+  if (lane == 0) mbar_arrive(&ms.work_empty[t][k % kSlots]);
+}
+template <int kSlots>
+__device__ __forceinline__ bool work_publish(ModMisc& ms, const ModKernelParams& p, int t, int k,
+                                             const Work& w, uint32_t abort_flag, int lane) {
+  if (k >= kSlots &&
+      !warp_all(mbar_wait(&ms.work_empty[t][k % kSlots], (k / kSlots + 1) & 1, abort_flag, p.err,
+                          kErrWaitLoad, p.wait_limit_ns)))
+    return false;
+  if (lane == 0) {
+    ms.work[t][k % kSlots] = w;
+    mbar_arrive(&ms.work_full[t][k % kSlots]);
+  }
+  return true;
 }
 
 // Prefill item u (warp-wide): the query rows, and the key tiles they see.
@@ -356,77 +397,132 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
   return x;
 }
 
-// Decode: walks the key tiles [x, end) of this CTA through the items (warp-wide).
-struct SplitPlan {
-  long long x, end;    // tiles of all items, laid end to end: shared prefix first
-  long long prefix;    // tiles of the shared prefix's items
-  long long before;    // own-key tiles of the requests in front of block b0, per KV head
-  int b0;              // first of the 32 requests that the lanes hold
-  int tiles, scan;     // this lane's request: its tiles and their inclusive sum
+// Decode: the prefix tiles of this CTA's run, [x, end), item by item.
+struct PrefixPlan {
+  uint32_t x, end;
+  __device__ __forceinline__ void start(const ModKernelParams& p) {
+    const uint32_t total = prefix_total(p);
+    const uint32_t runs = min(total, gridDim.x);
+    x = end = 0;
+    if (blockIdx.x < runs) {
+      x = run_start(total, runs, blockIdx.x);
+      end = run_start(total, runs, blockIdx.x + 1);
+    }
+  }
+  __device__ __forceinline__ bool next(const ModKernelParams& p, Work& w) {
+    if (x >= end) return false;
+    const uint32_t tiles = p.prefix_tiles, item = x / tiles;
+    w.tile0 = static_cast<int>(x - item * tiles);
+    w.n = static_cast<int>(min(tiles - w.tile0, end - x));
+    w.kind = 0;
+    w.edges = 0;
+    w.id = static_cast<int>(item) / p.row_blocks;
+    w.q0 = (static_cast<int>(item) - w.id * p.row_blocks) * 2 * p.per_tile;
+    w.lo = 0;
+    w.hi = p.Np;
+    w.slot = static_cast<int>(item + blockIdx.x);
+    w.a[0] = w.a[1] = 0;
+    w.b[0] = w.n;
+    w.b[1] = w.q0 + p.per_tile < p.B ? w.n : 0;
+    x += w.n;
+    return true;
+  }
+};
+
+// Decode: query tile t's run of the requests' own key tiles (warp-wide).  Run
+// r of 2 x CTAs belongs to query tile r / CTAs; the CTAs count from the other
+// end than those of the prefix, which matters where there are fewer tiles than
+// CTAs.  The tiles of all items are laid end to end, request by request, KV head by
+// KV head.
+struct OwnPlan {
+  int left;        // tiles left of the run
+  int run;
+  int b0, at;      // request b0 + at, of a block of 32 that the lanes hold
+  int id, tile0;   // KV head, tile within the item
+  int len, tiles;  // this lane's request: its keys and key tiles
+  uint32_t mine, other;  // tiles of this run and of the CTA's other one
 
   __device__ __forceinline__ void load_block(const ModKernelParams& p, int lane) {
-    tiles = b0 + lane < p.B ? key_tiles(request_len(p, b0 + lane)) : 0;
-    scan = warp_scan(tiles, lane);
+    len = b0 + lane < p.B ? request_len(p, b0 + lane) : 0;
+    tiles = key_tiles(len);
   }
-  __device__ __forceinline__ void start(const ModKernelParams& p, int lane) {
-    long long own = 0;
-    for (int b = lane; b < p.B; b += 32) own += key_tiles(request_len(p, b));
-#pragma unroll
-    for (int d = 16; d >= 1; d /= 2) own += __shfl_xor_sync(0xFFFFFFFFu, own, d);
-    prefix = static_cast<long long>(p.Hkv) * p.row_blocks * p.prefix_tiles;
-    const long long total = prefix + own * p.Hkv;
-    const long long run = split_run(total, gridDim.x);
-    x = min(run * blockIdx.x, total);
-    end = min(x + run, total);
-    before = 0;
+  __device__ __forceinline__ void start(const ModKernelParams& p, int t, int lane) {
+    // how many tiles there are: the first requests stay in the lanes
     b0 = 0;
     load_block(p, lane);
-  }
-  __device__ __forceinline__ Work next(const ModKernelParams& p, int lane) {
-    Work w;
-    w.n = -1;
-    w.edges = 0;
-    w.a[0] = w.a[1] = w.b[0] = w.b[1] = 0;
-    w.lo = 0;
-    if (x >= end) return w;
-    if (x < prefix) {
-      const int item = static_cast<int>(x / p.prefix_tiles);
-      w.tile0 = static_cast<int>(x % p.prefix_tiles);
-      w.n = static_cast<int>(min(static_cast<long long>(p.prefix_tiles - w.tile0), end - x));
-      w.kind = 0;
-      w.id = item / p.row_blocks;
-      w.q0 = (item % p.row_blocks) * 2 * p.per_tile;
-      w.hi = p.Np;
-      w.slot = item + static_cast<int>(blockIdx.x);
-      w.b[0] = w.n;
-      w.b[1] = w.q0 + p.per_tile < p.B ? w.n : 0;
-    } else {
-      long long y = x - prefix;
-      for (;;) {  // the block of 32 requests that holds tile y
-        const long long block = static_cast<long long>(__shfl_sync(0xFFFFFFFFu, scan, 31)) * p.Hkv;
-        if (y < before + block) break;
-        before += block;
-        b0 += 32;
-        load_block(p, lane);
-      }
-      y -= before;
-      const unsigned behind =
-          __ballot_sync(0xFFFFFFFFu, y < static_cast<long long>(scan) * p.Hkv);
-      const int at = __ffs(behind) - 1;
-      const int nt = __shfl_sync(0xFFFFFFFFu, tiles, at);
-      y -= static_cast<long long>(__shfl_sync(0xFFFFFFFFu, scan, at) - nt) * p.Hkv;
-      w.id = static_cast<int>(y / nt);
-      w.tile0 = static_cast<int>(y % nt);
-      w.n = static_cast<int>(min(static_cast<long long>(nt - w.tile0), end - x));
-      w.kind = 1;
-      w.q0 = b0 + at;
-      w.hi = request_len(p, w.q0);
-      w.slot = w.q0 * p.Hkv + w.id + static_cast<int>(blockIdx.x);
-      w.b[0] = w.n;
-      if (w.hi < min((w.tile0 + w.n) * kBN, p.Nk)) w.edges = 2;
+    uint32_t own = tiles;
+#pragma unroll 4
+    for (int b = 32 + lane; b < p.B; b += 32) own += key_tiles(request_len(p, b));
+    const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, own) * p.Hkv;
+    const uint32_t runs = min(total, 2 * gridDim.x);
+    const uint32_t r0 = gridDim.x - 1 - blockIdx.x, r1 = r0 + gridDim.x;
+    const uint32_t r = t ? r1 : r0, q = t ? r0 : r1;
+    uint32_t x = 0;
+    mine = other = 0;
+    if (r < runs) {
+      x = run_start(total, runs, r);
+      mine = run_start(total, runs, r + 1) - x;
     }
-    x += w.n;
-    return w;
+    if (q < runs) other = run_start(total, runs, q + 1) - run_start(total, runs, q);
+    run = static_cast<int>(r);
+    left = static_cast<int>(mine);
+    at = id = tile0 = 0;
+    if (left == 0) return;
+    for (;;) {  // the block, the request and the KV head that hold tile x
+      const int scan = warp_scan(tiles, lane);
+      const uint32_t block = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, scan, 31)) * p.Hkv;
+      if (x < block) {
+        at = __ffs(__ballot_sync(0xFFFFFFFFu, x < static_cast<uint32_t>(scan) * p.Hkv)) - 1;
+        const int nt = __shfl_sync(0xFFFFFFFFu, tiles, at);
+        x -= static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, scan, at) - nt) * p.Hkv;
+        id = static_cast<int>(x / nt);
+        tile0 = static_cast<int>(x - static_cast<uint32_t>(id) * nt);
+        return;
+      }
+      x -= block;
+      b0 += 32;
+      load_block(p, lane);
+    }
+  }
+  // The next item; ring0: ring items of the prefix tiles before.
+  __device__ __forceinline__ bool next(const ModKernelParams& p, int t, int lane, uint32_t ring0,
+                                       Work& w) {
+    if (left == 0) return false;
+    const int nt = __shfl_sync(0xFFFFFFFFu, tiles, at);
+    w.hi = __shfl_sync(0xFFFFFFFFu, len, at);
+    w.id = id;
+    w.tile0 = tile0;
+    w.n = min(nt - tile0, left);
+    w.kind = 1;
+    w.q0 = b0 + at;
+    w.lo = 0;
+    w.slot = w.q0 * p.Hkv + id + run;
+    w.a[0] = w.a[1] = 0;
+    w.b[0] = t ? 0 : w.n;
+    w.b[1] = t ? w.n : 0;
+    w.edges = w.hi < (tile0 + w.n) * kBN ? 2 : 0;
+    // the two runs' tiles take turns in the ring
+    const uint32_t s = mine - left + w.n - 1;  // step of the item's last tile
+    w.v_first = 0;
+    w.v_last = ring0 + 2 * (s + min(t ? s + 1 : s, other)) + 1;
+    left -= w.n;
+    if (left > 0) {
+      tile0 = 0;
+      if (++id == p.Hkv) {
+        id = 0;
+        for (;;) {  // the next request that has keys
+          const unsigned some = __ballot_sync(0xFFFFFFFFu, tiles > 0 && lane > at);
+          if (some) {
+            at = __ffs(some) - 1;
+            break;
+          }
+          b0 += 32;
+          at = -1;
+          load_block(p, lane);
+        }
+      }
+    }
+    return true;
   }
 };
 
@@ -435,6 +531,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
     mod_attn_kernel(const __grid_constant__ ModKernelParams p) {
   using C = Cfg<D, false>;
   constexpr uint32_t kS = C::kStages;
+  constexpr int kSlots = kWorkSlots<kSplit>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -444,20 +541,22 @@ __global__ void __launch_bounds__(kModThreads, 1)
 
   // ---- setup: barriers (load warp), TMEM (MMA warp)
   if (warp == kModWarpLoad && lane == 0) {
-    mbar_init(&ms.q_full, 1);
-    mbar_init(&ms.q_empty, 1);
     mbar_init(&ms.unit_done, 1);
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&ms.q_full[t], 1);
+      mbar_init(&ms.q_empty[t], 1);
       mbar_init(&ms.s_full[t], 1);
       mbar_init(&ms.s_read[t], 8);
       mbar_init(&ms.p_full[t], 8);
       mbar_init(&ms.o_done[t], 1);
-      mbar_init(&ms.work_full[t], 1);
-      mbar_init(&ms.work_empty[t], kWorkReaders);
+      // readers: 8 softmax warps, load and MMA warp (a prefill's last two read
+      // the first query tile's copy only)
+      for (int i = 0; i < kSlots; ++i) {
+        mbar_init(&ms.work_full[t][i], 1);
+        mbar_init(&ms.work_empty[t][i], kSplit || t == 0 ? 10 : 8);
+      }
     }
     mbar_init(&ms.mma_done, 1);
-    mbar_init(&ms.edge_next, 1);
-    mbar_init(&ms.v_edge, 2);
     mbar_init(&ms.clc_full, 1);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&ms.kv_full[s], 1);
@@ -484,6 +583,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem_base;
+  // the merge kernel may be scheduled as this one's CTAs leave; it waits for all
+  if constexpr (kSplit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp < 16) {
     // =====================================================================
@@ -502,45 +603,43 @@ __global__ void __launch_bounds__(kModThreads, 1)
     uint32_t step = 0;   // tiles done by this query tile: phase of s_full
     uint32_t units = 0;  // items that this query tile took part in: phase of o_done
     for (int k = 0;; ++k) {
-      if (!work_wait(ms, p, k, abort_flag, kErrWaitSoftmax)) break;
-      const Work& w = ms.work[k & 1];
-      const int n_all = w.n, tile0 = w.tile0, ja = w.a[t], jb = w.b[t];
-      const int id = w.id, q0 = w.q0, kind = w.kind, slot = w.slot, wlo = w.lo, whi = w.hi;
-      work_done(ms, k, lane);
-      if (n_all < 0) break;
+      if (!work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax)) break;
+      const Work& w = ms.work[t][k % kSlots];  // read where needed: registers are scarce
+      if (w.n < 0) break;
+      const int ja = w.a[t], jb = w.b[t];
       // the row: which query, which keys
       RowInfo row;
       bool valid;
       size_t out = 0;  // its row in the outputs
       int head = 0;
-      row.lo = wlo;
-      row.hi = whi;
+      row.lo = w.lo;
+      row.hi = w.hi;
       if constexpr (kSplit) {
-        const int G = p.G;
+        const int G = p.G, kind = w.kind;
         const int req = kind ? 0 : r / G;
-        const int b = q0 + (kind ? 0 : t * p.per_tile) + req;
+        const int b = w.q0 + (kind ? 0 : t * p.per_tile) + req;
         const int g = r - req * G;
         valid = jb > 0 && (kind ? r < G : req < p.per_tile) && b < p.B;
-        head = id * G + g;
+        head = w.id * G + g;
         row.pos = 0;
         if constexpr (kBias) {
           // positions count from the item's first key
-          if (valid) row.pos = (kind ? whi : p.Np + request_len(p, b)) - 1;
+          if (valid) row.pos = (kind ? w.hi : p.Np + request_len(p, b)) - 1;
         }
-        out = kind ? static_cast<size_t>(slot) * G + r
-                   : static_cast<size_t>(slot) * p.pre_rows + t * kBM + r;
+        out = kind ? static_cast<size_t>(w.slot) * G + r
+                   : static_cast<size_t>(w.slot) * p.pre_rows + t * kBM + r;
       } else {
-        const int i = q0 + t * kBM + r;
+        const int i = w.q0 + t * kBM + r;
         valid = i < p.Nq;
-        head = id % p.Hq;
+        head = w.id % p.Hq;
         row.pos = p.q_offset + i;
-        out = static_cast<size_t>(id) * p.Nq + i;
+        out = static_cast<size_t>(w.id) * p.Nq + i;
         if (valid) {
           row.lo = 0;
           row.hi = p.Nk;
           if (p.ranges) {
             const int2 rg = reinterpret_cast<const int2*>(
-                p.ranges)[static_cast<size_t>(id / p.Hq) * p.Nq + i];
+                p.ranges)[static_cast<size_t>(w.id / p.Hq) * p.Nq + i];
             row.lo = max(rg.x, 0);
             row.hi = min(rg.y, p.Nk);
           }
@@ -555,24 +654,60 @@ __global__ void __launch_bounds__(kModThreads, 1)
           row.slope = p.mod.slopes[head] * kLog2e;
           if constexpr (kSplit) {
             // nearest: the query's own position; farthest: the first key of all
-            if (row.slope < 0.f) row.ref = (kind ? p.Np : 0) + row.pos;
+            if (row.slope < 0.f) row.ref = (w.kind ? p.Np : 0) + row.pos;
           } else if (row.lo < row.hi) {
             row.ref = bias_ref(row.slope, row.pos, row.lo, row.hi);
           }
         }
       }
+      // Keys that all rows of the warp see, and that any does.  (Rows that are not
+      // there took the item's span and see what the others do.)
       const bool live = __any_sync(0xFFFFFFFFu, valid && row.lo < row.hi);
+      {
+        int4 seen;
+        seen.x = __reduce_max_sync(0xFFFFFFFFu, row.lo);
+        seen.y = __reduce_min_sync(0xFFFFFFFFu, row.hi);
+        seen.z = __reduce_min_sync(0xFFFFFFFFu, row.lo < row.hi ? row.lo : INT_MAX);
+        seen.w = live ? __reduce_max_sync(0xFFFFFFFFu, row.hi) : 0;
+        if (lane == 0) ms.seen[warp] = seen;
+        __syncwarp();
+      }
       float m = -CUDART_INF_F, l = 0.f;  // l: sum over this thread's half of the row
       bool ok = true;
       for (int j = ja; j < jb; ++j, ++step) {
+        const int kt = (w.tile0 + j) * kBN;  // first key of the tile
+        bool masked, dead;
+        {
+          const int4 seen = ms.seen[warp];
+          masked = kt < seen.x || kt + kBN > seen.y;
+          dead = kt >= seen.w || kt + kBN <= seen.z;  // no row sees a key of the tile
+        }
+        const int edges = w.edges;
+        const bool edge = ((edges & 1) && j == 0) || ((edges & 2) && j == w.n - 1);
         if (!warp_all(mbar_wait(&ms.s_full[t], step & 1, abort_flag, p.err, kErrWaitSoftmax,
                                 p.wait_limit_ns))) {
           ok = false;
           break;
         }
-        const int kt = (tile0 + j) * kBN;  // first key of the tile
-        if (!live || !__any_sync(0xFFFFFFFFu, row.lo < kt + kBN && row.hi > kt)) {
-          // no row of the warp sees a key of this tile
+        if (edge) {
+          // clear V's unseen rows, all warps of the query tile together (where
+          // both query tiles use the tile, each does).  The tile of V that was
+          // in its ring slot before has been multiplied already (before this
+          // S), so the slot's barrier is in this tile's phase.
+          const uint32_t iv = j == w.n - 1 ? w.v_last : w.v_first;
+          if (!warp_all(mbar_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
+                                  kErrWaitSoftmax, p.wait_limit_ns))) {
+            ok = false;
+            break;
+          }
+          uint4* v = reinterpret_cast<uint4*>(smem + C::kOffKV + (iv % kS) * C::kTileBytes);
+          for (int i = (warp & 7) * 32 + lane; i < kBN * C::kChunks * 8; i += 256) {
+            const int key = kt + ((i >> 3) & (kBN - 1));
+            if (key < w.lo || key >= w.hi) v[i] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (dead) {
           if (live) {
             uint32_t pk[32];
 #pragma unroll
@@ -597,11 +732,9 @@ __global__ void __launch_bounds__(kModThreads, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
         }
-        const bool masked =
-            __any_sync(0xFFFFFFFFu, row.lo > kt || row.hi < kt + kBN);
-        bool poly;
+        bool final, poly;
         const float m_tile =
-            Scores<kCap, kBias>::prepare(s, p, row, kt + c * 64, masked, poly);
+            Scores<kCap, kBias>::prepare(s, p, row, kt + c * 64, masked, final, poly);
         if constexpr (C::kSplitS) {
           // S_t has been read: the MMA warp may write the next tile's keys
           // [64, 128) over columns 64..127, which P does not use
@@ -617,7 +750,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
         }
         const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
         uint32_t pk[32];
-        const float rsum = Scores<kCap, kBias>::weights(s, p, neg_m, masked, poly, pk);
+        const float rsum = Scores<kCap, kBias>::weights(s, p, neg_m, final, poly, pk);
         l = fmaf(l, alpha, rsum);
         // rescale O_t when a row's maximum rose past the threshold: every P V
         // of earlier tiles has retired (it was issued before this S_t)
@@ -645,7 +778,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
         ++units;
         if (!ok) break;
       }
-      if (kSplit && !live) continue;
+      if (!kSplit || live) {
       tc_fence_after();
       // ---- epilogue: O / l and the LSE; a row that saw nothing gives 0 and -inf
       const float l_row = l + __shfl_xor_sync(0xFFFFFFFFu, l, 16);
@@ -662,17 +795,15 @@ __global__ void __launch_bounds__(kModThreads, 1)
           for (int i = 0; i < 32; ++i) v[i] = 0;
         }
         if constexpr (kSplit) {
-          float4* dst = reinterpret_cast<float4*>((kind ? p.part_o : p.pre_o) + out * D +
-                                                  c * (D / 2) + kk * 32);
+          float* dst = (w.kind ? p.part_o : p.pre_o) + out * D + c * (D / 2) + kk * 32;
           if (valid) {
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              float4 x;
-              x.x = none ? 0.f : __uint_as_float(v[4 * g]) * inv;
-              x.y = none ? 0.f : __uint_as_float(v[4 * g + 1]) * inv;
-              x.z = none ? 0.f : __uint_as_float(v[4 * g + 2]) * inv;
-              x.w = none ? 0.f : __uint_as_float(v[4 * g + 3]) * inv;
-              dst[g] = x;
+            for (int g = 0; g < 4; ++g) {
+              float x[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                x[i] = none ? 0.f : __uint_as_float(v[8 * g + i]) * inv;
+              st_global_v8(dst + 8 * g, x);  // a whole 32-byte sector
             }
           }
         } else {
@@ -694,10 +825,12 @@ __global__ void __launch_bounds__(kModThreads, 1)
       }
       if (valid && c == 0) {
         if constexpr (kSplit)
-          (kind ? p.part_lse : p.pre_lse)[out] = lse2;
+          (w.kind ? p.part_lse : p.pre_lse)[out] = lse2;
         else
           p.lse[out] = (lse2 - row.slope * static_cast<float>(row.ref)) * kLn2;
       }
+      }
+      work_done<kSlots>(ms, t, k, lane);
     }
   } else if (warp == kModWarpLoad) {
     // =====================================================================
@@ -705,112 +838,141 @@ __global__ void __launch_bounds__(kModThreads, 1)
     // tile j is ring items 2 (j + tiles before), + 1 (K, then V).
     // =====================================================================
     reg_dealloc<kModRegOther>();
-    uint32_t g = 0;         // next ring item
-    uint32_t q_loads = 0;   // Q loads issued
-    bool clc_pending = false, ok = true;
-    uint32_t clc_done = 0;  // answers read
-    SplitPlan plan;
-    Work w;
-    if constexpr (kSplit) {
-      plan.start(p, lane);
-      w = plan.next(p, lane);
-    } else {
-      w = plan_unit(p, static_cast<int>(blockIdx.x), lane);
-    }
-    for (int k = 0; ok; ++k) {
-      if (k >= 2 && !warp_all(mbar_wait(&ms.work_empty[k & 1], ((k >> 1) + 1) & 1, abort_flag,
-                                        p.err, kErrWaitLoad, p.wait_limit_ns)))
-        break;
-      if (lane == 0) {
-        ms.work[k & 1] = w;
-        mbar_arrive(&ms.work_full[k & 1]);
-      }
-      if (w.n < 0) break;
-      const CUtensorMap* mk = &p.tmap_k;
-      const CUtensorMap* mv = &p.tmap_v;
-      int bhkv;
-      uint64_t policy;
+    uint32_t g = 0;              // next ring item
+    uint32_t q0_loads = 0, q1_loads = 0;  // loads of Q_0, Q_1 issued
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      return warp_all(mbar_wait(bar, phase & 1u, abort_flag, p.err, kErrWaitLoad, p.wait_limit_ns));
+    };
+    // one K or V tile into the ring
+    auto load_tile = [&](const CUtensorMap* map, int key, int bh, uint64_t policy) {
+      const uint32_t s = g % kS;
+      if (!wait(&ms.kv_empty[s], (g / kS) + 1)) return false;
+      mbar_arrive_expect_tx_elect(&ms.kv_full[s], C::kTileBytes);
+      uint8_t* dst = smem + C::kOffKV + s * C::kTileBytes;
+      for (int ch = 0; ch < C::kChunks; ++ch)
+        tma_load_3d_elect(dst + ch * (kBM * 128), map, &ms.kv_full[s], ch * C::kAtomElems, key, bh,
+                          policy);
+      ++g;
+      return true;
+    };
+    // the last tile of a request: its first `rows` keys, 32 at a time, so that
+    // little of the cache's unused tail is read
+    auto load_tail = [&](const CUtensorMap* map, int key, int rows, int bh, uint64_t policy) {
+      const uint32_t s = g % kS;
+      if (!wait(&ms.kv_empty[s], (g / kS) + 1)) return false;
+      const int boxes = (rows + 31) / 32;
+      mbar_arrive_expect_tx_elect(&ms.kv_full[s], boxes * C::kChunks * 32 * 128);
+      uint8_t* dst = smem + C::kOffKV + s * C::kTileBytes;
+      for (int ch = 0; ch < C::kChunks; ++ch)
+        for (int i = 0; i < boxes; ++i)
+          tma_load_3d_elect(dst + ch * (kBM * 128) + i * (32 * 128), map, &ms.kv_full[s],
+                            ch * C::kAtomElems, key + 32 * i, bh, policy);
+      ++g;
+      return true;
+    };
+    // Q_t, once its last Q K^T (or copy to TMEM) read it
+    auto load_q = [&](int t, int kind, int id, int q0) {
+      const uint32_t before = t ? q1_loads : q0_loads;
+      if (before > 0 && !wait(&ms.q_empty[t], before - 1)) return false;
+      if (t)
+        ++q1_loads;
+      else
+        ++q0_loads;
+      uint8_t* dst = smem + C::kOffQ + t * C::kTileBytes;
       if constexpr (kSplit) {
-        if (w.kind == 0) {
-          mk = &p.tmap_kp;
-          mv = &p.tmap_vp;
-        }
-        bhkv = w.kind ? w.q0 * p.Hkv + w.id : w.id;
-        // a request's own keys are read once, the prefix once per row block
-        policy = w.kind || p.row_blocks == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
-      } else {
-        bhkv = (w.id / p.Hq) * p.Hkv + (w.id % p.Hq) / p.G;
-        policy = l2_policy_evict_last();
-      }
-      for (int it = 0; it < 2 * w.n; ++it, ++g) {
-        const uint32_t s = g % kS;
-        if (!warp_all(mbar_wait(&ms.kv_empty[s], ((g / kS) & 1u) ^ 1u, abort_flag, p.err,
-                                kErrWaitLoad, p.wait_limit_ns))) {
-          ok = false;
-          break;
-        }
-        mbar_arrive_expect_tx_elect(&ms.kv_full[s], C::kTileBytes);
-        uint8_t* dst = smem + C::kOffKV + s * C::kTileBytes;
-        const CUtensorMap* map = (it & 1) ? mv : mk;
+        const uint32_t rows = (kind ? 1 : p.per_tile) * p.G;
+        mbar_arrive_expect_tx_elect(&ms.q_full[t], C::kChunks * rows * 128);
         for (int ch = 0; ch < C::kChunks; ++ch)
-          tma_load_3d_elect(dst + ch * (kBM * 128), map, &ms.kv_full[s], ch * C::kAtomElems,
-                            (w.tile0 + (it >> 1)) * kBN, bhkv, policy);
-        if (it == 0) {
-          // Q, once the previous item's last Q K^T (or copy to TMEM) read it
-          if (q_loads > 0 &&
-              !warp_all(mbar_wait(&ms.q_empty, (q_loads - 1) & 1, abort_flag, p.err, kErrWaitLoad,
-                                  p.wait_limit_ns))) {
-            ok = false;
-            ++g;
-            break;
-          }
-          const bool two = w.b[1] > w.a[1];
-          if constexpr (kSplit) {
-            const uint32_t rows = (w.kind ? 1 : p.per_tile) * p.G;
-            mbar_arrive_expect_tx_elect(&ms.q_full, (two ? 2 : 1) * C::kChunks * rows * 128);
-            for (int t = 0; t < (two ? 2 : 1); ++t)
-              for (int ch = 0; ch < C::kChunks; ++ch)
-                tma_load_4d_elect(smem + C::kOffQ + t * C::kTileBytes + ch * (kBM * 128),
-                                  w.kind ? &p.tmap_q1 : &p.tmap_q, &ms.q_full,
-                                  ch * C::kAtomElems, 0, w.id, w.q0 + t * p.per_tile,
-                                  l2_policy_evict_last());
-          } else {
-            mbar_arrive_expect_tx_elect(&ms.q_full, 2 * C::kTileBytes);
-            for (int t = 0; t < 2; ++t)
-              for (int ch = 0; ch < C::kChunks; ++ch)
-                tma_load_3d_elect(smem + C::kOffQ + t * C::kTileBytes + ch * (kBM * 128),
-                                  &p.tmap_q, &ms.q_full, ch * C::kAtomElems, w.q0 + t * kBM, w.id,
-                                  l2_policy_evict_first());
-          }
-          ++q_loads;
-        }
-      }
-      if (!ok) break;
-      if constexpr (kSplit) {
-        w = plan.next(p, lane);
+          tma_load_4d_elect(dst + ch * (kBM * 128), kind ? &p.tmap_q1 : &p.tmap_q, &ms.q_full[t],
+                            ch * C::kAtomElems, 0, id, q0 + (kind ? 0 : t * p.per_tile),
+                            l2_policy_evict_last());
       } else {
-        // everything of this item is on its way: ask for the next one
-        mbar_arrive_expect_tx_elect(&ms.clc_full, 16);
-        clc_try_cancel_elect(smem_u32(&ms.clc_resp), &ms.clc_full);
-        clc_pending = true;
-        if (!warp_all(mbar_wait(&ms.clc_full, clc_done & 1, abort_flag, p.err, kErrWaitLoad,
-                                p.wait_limit_ns)))
-          break;
-        clc_pending = false;
-        ++clc_done;
-        const int nu = clc_response_ctaid_x(smem_u32(&ms.clc_resp));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (nu < 0)
-          w.n = -1;
-        else
-          w = plan_unit(p, nu, lane);
+        mbar_arrive_expect_tx_elect(&ms.q_full[t], C::kTileBytes);
+        for (int ch = 0; ch < C::kChunks; ++ch)
+          tma_load_3d_elect(dst + ch * (kBM * 128), &p.tmap_q, &ms.q_full[t], ch * C::kAtomElems,
+                            q0 + t * kBM, id, l2_policy_evict_first());
+      }
+      return true;
+    };
+    // ---- items of two query tiles that share their K and V tiles
+    int k = 0;
+    for (; ok && (!kSplit || p.prefix_tiles > 0); ++k) {
+      ok = work_wait<kSlots>(ms, p, 0, k, abort_flag, kErrWaitLoad);
+      if (!ok) break;
+      const Work& w = ms.work[0][k % kSlots];
+      const int n = w.n, tile0 = w.tile0, id = w.id, q0 = w.q0;
+      const bool use0 = w.b[0] > w.a[0], use1 = w.b[1] > w.a[1];
+      const bool last_item = kSplit ? w.kind == 2 : n < 0;
+      work_done<kSlots>(ms, 0, k, lane);
+      if constexpr (kSplit) {
+        ok = work_wait<kSlots>(ms, p, 1, k, abort_flag, kErrWaitLoad);
+        if (!ok) break;
+        work_done<kSlots>(ms, 1, k, lane);
+      }
+      if (last_item) {
+        ++k;
+        break;
+      }
+      int bh = id;
+      uint64_t policy = l2_policy_evict_last();
+      if constexpr (kSplit) {
+        if (p.row_blocks == 1) policy = l2_policy_evict_first();  // read once
+      } else {
+        bh = (id / p.Hq) * p.Hkv + (id % p.Hq) / p.G;
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int key = (tile0 + j) * kBN;
+        ok = load_tile(kSplit ? &p.tmap_kp : &p.tmap_k, key, bh, policy);
+        if (j == 0) {
+          ok = ok && (!use0 || load_q(0, 0, id, q0));
+          ok = ok && (!use1 || load_q(1, 0, id, q0));
+        }
+        ok = ok && load_tile(kSplit ? &p.tmap_vp : &p.tmap_v, key, bh, policy);
+      }
+    }
+    // ---- decode: the two runs of own keys, a tile of either in turn
+    if constexpr (kSplit) {
+      int ks[2] = {k, k}, left[2] = {0, 0}, key[2], hi[2], bh[2];
+      int done = 0;
+      const uint64_t policy = l2_policy_evict_first();  // every byte is read once
+      while (ok && done != 3) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || (done >> t & 1)) continue;
+          int id = 0, q0 = 0;
+          const bool fresh = left[t] == 0;
+          if (fresh) {
+            ok = work_wait<kSlots>(ms, p, t, ks[t], abort_flag, kErrWaitLoad);
+            if (!ok) break;
+            const Work& w = ms.work[t][ks[t] % kSlots];
+            left[t] = w.n;
+            key[t] = w.tile0 * kBN;
+            hi[t] = w.hi;
+            id = w.id;
+            q0 = w.q0;
+            work_done<kSlots>(ms, t, ks[t]++, lane);
+            bh[t] = q0 * p.Hkv + id;
+            if (left[t] < 0) {
+              done |= 1 << t;
+              continue;
+            }
+          }
+          const int rows = hi[t] - key[t];
+          ok = rows >= kBN ? load_tile(&p.tmap_k, key[t], bh[t], policy)
+                           : load_tail(&p.tmap_kt, key[t], rows, bh[t], policy);
+          if (ok && fresh) ok = load_q(t, 1, id, q0);
+          ok = ok && (rows >= kBN ? load_tile(&p.tmap_v, key[t], bh[t], policy)
+                                  : load_tail(&p.tmap_vt, key[t], rows, bh[t], policy));
+          key[t] += kBN;
+          --left[t];
+        }
       }
     }
     if (abort_set(abort_flag)) {
       // let the copies still in flight land before the CTA exits
-      if (q_loads > 0) drain_wait(&ms.q_full, (q_loads - 1) & 1);
-      if (clc_pending) drain_wait(&ms.clc_full, clc_done & 1);
+      if (q0_loads > 0) drain_wait(&ms.q_full[0], (q0_loads - 1) & 1);
+      if (q1_loads > 0) drain_wait(&ms.q_full[1], (q1_loads - 1) & 1);
       for (uint32_t it = g > kS ? g - kS : 0u; it < g; ++it)
         drain_wait(&ms.kv_full[it % kS], (it / kS) & 1u);
     }
@@ -854,20 +1016,32 @@ __global__ void __launch_bounds__(kModThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       return warp_all(mbar_wait(bar, phase & 1u, abort_flag, p.err, kErrWaitMma, p.wait_limit_ns));
     };
-    uint32_t items = 0;          // items with keys so far
     uint32_t tiles = 0;          // key tiles so far: ring items 2 tiles ..
-    uint32_t edge = 0;           // edge tiles so far
     uint32_t steps0 = 0, steps1 = 0;  // S_0, S_1 issued so far
+    uint32_t qs0 = 0, qs1 = 0;        // Q_0, Q_1 taken so far
+    int k = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!work_wait(ms, p, k, abort_flag, kErrWaitMma)) break;
-      const Work& w = ms.work[k & 1];
-      const int n = w.n, edges = w.edges;
+    // ---- items of two query tiles on the same K and V tiles
+    for (uint32_t items = 0; ok && (!kSplit || p.prefix_tiles > 0); ++k) {
+      ok = work_wait<kSlots>(ms, p, 0, k, abort_flag, kErrWaitMma);
+      if (!ok) break;
+      const Work& w = ms.work[0][k % kSlots];
+      const int n = w.n;
       const int a0 = w.a[0], a1 = w.a[1], b0 = w.b[0], b1 = w.b[1];
-      work_done(ms, k, lane);
-      if (n < 0) break;
+      const bool last_item = kSplit ? w.kind == 2 : n < 0;
+      work_done<kSlots>(ms, 0, k, lane);
+      if constexpr (kSplit) {
+        ok = work_wait<kSlots>(ms, p, 1, k, abort_flag, kErrWaitMma);
+        if (!ok) break;
+        work_done<kSlots>(ms, 1, k, lane);
+      }
+      if (last_item) {
+        ++k;
+        break;
+      }
       if (n == 0) continue;
-      ok = wait(&ms.q_full, items);
+      if (b0 > a0) ok = wait(&ms.q_full[0], qs0++);
+      if (ok && b1 > a1) ok = wait(&ms.q_full[1], qs1++);
       if constexpr (C::kQInTmem) {
         // Q_0, Q_1 into TMEM once every MMA of the previous item retired (see
         // fwd_sm103a.cu)
@@ -875,29 +1049,32 @@ __global__ void __launch_bounds__(kModThreads, 1)
         if (ok) {
           tc_fence_after();
           const uint32_t q0 = desc_k + kQ0, q1 = desc_k + kQ1;
-          tmem_cp_128x256b<C::kColQ0 + 0, 0>(tmem, q0);
-          tmem_cp_128x256b<C::kColQ0 + 8, 2>(tmem, q0);
-          tmem_cp_128x256b<C::kColQ0 + 16, 4>(tmem, q0);
-          tmem_cp_128x256b<C::kColQ0 + 24, 6>(tmem, q0);
-          tmem_cp_128x256b<C::kColQ1 + 0, 0>(tmem, q1);
-          tmem_cp_128x256b<C::kColQ1 + 8, 2>(tmem, q1);
-          tmem_cp_128x256b<C::kColQ1 + 16, 4>(tmem, q1);
-          tmem_cp_128x256b<C::kColQ1 + 24, 6>(tmem, q1);
-          mma_commit(&ms.q_empty);
+          if (b0 > a0) {
+            tmem_cp_128x256b<C::kColQ0 + 0, 0>(tmem, q0);
+            tmem_cp_128x256b<C::kColQ0 + 8, 2>(tmem, q0);
+            tmem_cp_128x256b<C::kColQ0 + 16, 4>(tmem, q0);
+            tmem_cp_128x256b<C::kColQ0 + 24, 6>(tmem, q0);
+            mma_commit(&ms.q_empty[0]);
+          }
+          if (b1 > a1) {
+            tmem_cp_128x256b<C::kColQ1 + 0, 0>(tmem, q1);
+            tmem_cp_128x256b<C::kColQ1 + 8, 2>(tmem, q1);
+            tmem_cp_128x256b<C::kColQ1 + 16, 4>(tmem, q1);
+            tmem_cp_128x256b<C::kColQ1 + 24, 6>(tmem, q1);
+            mma_commit(&ms.q_empty[1]);
+          }
         }
       }
       for (int j = 0; ok && j <= n; ++j) {
         const uint32_t ik = 2u * (tiles + j), iv = ik - 1u;
         const uint32_t bk = desc_k + (ik % kS) * kTileDesc, bv = desc_k + (iv % kS) * kTileDesc;
         if (j < n) ok = wait(&ms.kv_full[ik % kS], ik / kS);
-        if (ok && j > 0) {
-          ok = wait(&ms.kv_full[iv % kS], iv / kS);
-          if (ok && (((edges & 1) && j == 1) || ((edges & 2) && j == n)))
-            ok = wait(&ms.v_edge, edge++);
-        }
+        if (ok && j > 0) ok = wait(&ms.kv_full[iv % kS], iv / kS);
         if (!ok) break;
         tc_fence_after();
-        for (int t = 0; t < 2 && ok; ++t) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok) break;
           const int a = t ? a1 : a0, b = t ? b1 : b0;
           const bool pv = j > a && j <= b, qk = j >= a && j < b;
           const uint32_t last = (t ? steps1 : steps0) - 1u;  // the step whose P V is due
@@ -922,35 +1099,120 @@ __global__ void __launch_bounds__(kModThreads, 1)
               ++steps1;
             else
               ++steps0;
+            if (!C::kQInTmem && j == b - 1) mma_commit(&ms.q_empty[t]);
           }
         }
         if (!ok) break;
         if (j < n) mma_commit(&ms.kv_empty[ik % kS]);
         if (j > 0) mma_commit(&ms.kv_empty[iv % kS]);
-        if (!C::kQInTmem && j == n - 1) mma_commit(&ms.q_empty);
-        // V_j is an edge tile: have it cleared while the softmax works on S_j.
-        // Asked for here, its slot's barrier is in V_j's own phase: a warp
-        // that waited for it from afar could take an earlier tile for it.
-        if (j < n && (((edges & 1) && j == 0) || ((edges & 2) && j == n - 1)) && lane == 0)
-          mbar_arrive(&ms.edge_next);
       }
       if (!ok) break;
       if (C::kQInTmem) mma_commit(&ms.unit_done);
       ++items;
       tiles += n;
     }
+    // ---- decode: the requests' own keys, a chain of its own per query tile.
+    // The chains take turns, a tile each, so that one's softmax runs beside
+    // the other's MMAs.  S reads Q from shared memory at D = 64 too: the bytes
+    // of K and V set the pace here.
+    if constexpr (kSplit) {
+      uint32_t ring = 2u * tiles;
+      int ks[2] = {k, k};
+      int left[2] = {0, 0};                    // tiles left of the item
+      uint32_t v_item[2] = {0, 0};             // ring item of the V whose P V is due
+      int due[2] = {0, 0};  // 0: none; bit 0: P V due; 1: accumulate; 2: item's last
+      int done = 0;
+      while (ok && (done != 3 || due[0] || due[1])) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok) break;
+          if (due[t]) {
+            const uint32_t iv = v_item[t];
+            ok = wait(&ms.kv_full[iv % kS], iv / kS);
+            ok = ok && wait(&ms.p_full[t], (t ? steps1 : steps0) - 1u);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(t, desc_k + (iv % kS) * kTileDesc, (due[t] >> 1) & 1u);
+            mma_commit(&ms.kv_empty[iv % kS]);
+            if (due[t] & 4) mma_commit(&ms.o_done[t]);
+            due[t] = 0;
+          }
+          if (done >> t & 1) continue;
+          bool first = false;
+          if (left[t] == 0) {
+            ok = work_wait<kSlots>(ms, p, t, ks[t], abort_flag, kErrWaitMma);
+            if (!ok) break;
+            const Work& w = ms.work[t][ks[t] % kSlots];
+            left[t] = w.n;
+            work_done<kSlots>(ms, t, ks[t]++, lane);
+            if (left[t] < 0) {
+              left[t] = 0;
+              done |= 1 << t;
+              continue;
+            }
+            first = true;
+            ok = wait(&ms.q_full[t], t ? qs1++ : qs0++);
+          }
+          const uint32_t ik = ring, iv = ring + 1u;
+          ring += 2u;
+          ok = ok && wait(&ms.kv_full[ik % kS], ik / kS);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t bk = desc_k + (ik % kS) * kTileDesc;
+          if (t)
+            issue_s_steps<D, false, C::kColS1, kQ1, 0, 0>(tmem, desc_k, bk);
+          else
+            issue_s_steps<D, false, C::kColS0, kQ0, 0, 0>(tmem, desc_k, bk);
+          mma_commit(&ms.s_full[t]);
+          mma_commit(&ms.kv_empty[ik % kS]);
+          if (t)
+            ++steps1;
+          else
+            ++steps0;
+          const bool last = left[t] == 1;
+          if (last) mma_commit(&ms.q_empty[t]);
+          v_item[t] = iv;
+          due[t] = 1 | (first ? 0 : 2) | (last ? 4 : 0);
+          --left[t];
+        }
+      }
+    }
     // all issued MMAs retire before the CTA releases TMEM
     mma_commit(&ms.mma_done);
     drain_wait(&ms.mma_done, 0);
   } else {
     // =====================================================================
-    // V edges: clear the rows of V that no row of the item sees
+    // planning warps
     // =====================================================================
     reg_dealloc<kModRegOther>();
+    Work w;
+    bool ok = true;
+    uint32_t ring = 0;  // ring items so far
+    int k = 0;
     if constexpr (kSplit) {
+      const int t = warp - kModWarpPlan;  // plans for this query tile
+      if (p.prefix_tiles > 0) {
+        PrefixPlan plan;
+        plan.start(p);
+        while (ok && plan.next(p, w)) {
+          w.v_first = w.v_last = 0;  // no edges
+          ring += 2 * w.n;
+          ok = work_publish<kSlots>(ms, p, t, k++, w, abort_flag, lane);
+        }
+        w.n = 0;
+        w.kind = 2;
+        w.a[0] = w.a[1] = w.b[0] = w.b[1] = 0;
+        ok = ok && work_publish<kSlots>(ms, p, t, k++, w, abort_flag, lane);
+      }
+      OwnPlan plan;
+      plan.start(p, t, lane);
+      while (ok && plan.next(p, t, lane, ring, w))
+        ok = work_publish<kSlots>(ms, p, t, k++, w, abort_flag, lane);
+      w.n = -1;
+      ok = ok && work_publish<kSlots>(ms, p, t, k++, w, abort_flag, lane);
       // CTA 0 leaves the merge kernel where every request's tiles begin
-      if (blockIdx.x == 0 && warp == kModWarpEdge + 1) {
-        long long before = 0;
+      if (blockIdx.x == 0 && t == 1) {
+        uint32_t before = 0;
         for (int b = 0; b < p.B; b += 32) {
           const int nt = b + lane < p.B ? key_tiles(request_len(p, b + lane)) : 0;
           const int scan = warp_scan(nt, lane);
@@ -959,42 +1221,39 @@ __global__ void __launch_bounds__(kModThreads, 1)
         }
         if (lane == 0) p.plan[p.B] = before;
       }
-    }
-    uint32_t tiles = 0, asked = 0;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!work_wait(ms, p, k, abort_flag, kErrWaitLoad)) break;
-      const Work& w = ms.work[k & 1];
-      const int n = w.n, edges = w.edges;
-      const int from = w.lo - w.tile0 * kBN;  // rows [from, to) are seen, from the first tile on
-      const int to = w.hi - w.tile0 * kBN;
-      work_done(ms, k, lane);
-      if (n < 0) break;
-      for (int e = 0; e < 2 && ok; ++e) {
-        const int j = e ? n - 1 : 0;
-        const bool here = e ? (edges & 2) && !(n == 1 && (edges & 1)) : (edges & 1) != 0;
-        if (!here) continue;
-        const uint32_t iv = 2u * (tiles + j) + 1u;
-        ok = warp_all(mbar_wait(&ms.edge_next, asked++ & 1u, abort_flag, p.err, kErrWaitLoad,
-                                p.wait_limit_ns)) &&
-             warp_all(mbar_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
-                                kErrWaitLoad, p.wait_limit_ns));
-        if (!ok) break;
-        uint8_t* v = smem + C::kOffKV + (iv % kS) * C::kTileBytes;
-        const int r0 = from - j * kBN, r1 = to - j * kBN;
-        for (int i = (warp - kModWarpEdge) * 32 + lane; i < kBN * C::kChunks * 8; i += 64) {
-          const int row = (i >> 3) & (kBN - 1);
-          if (row < r0 || row >= r1) reinterpret_cast<uint4*>(v)[i] = make_uint4(0, 0, 0, 0);
+    } else if (warp == kModWarpPlan) {
+      w = plan_unit(p, static_cast<int>(blockIdx.x), lane);
+      for (;; ++k) {
+        w.v_first = ring + 1u;
+        w.v_last = ring + 2u * w.n - 1u;
+        ok = work_publish<kSlots>(ms, p, 0, k, w, abort_flag, lane) &&
+             work_publish<kSlots>(ms, p, 1, k, w, abort_flag, lane);
+        if (!ok || w.n < 0) break;
+        ring += 2u * w.n;
+        // Ask for another item once the one before this is done: one is then
+        // always planned ahead, and no more.
+        if (k >= 1 && !warp_all(mbar_wait(&ms.work_empty[0][(k - 1) % kSlots],
+                                          ((k - 1) / kSlots) & 1, abort_flag, p.err, kErrWaitLoad,
+                                          p.wait_limit_ns)))
+          break;
+        mbar_arrive_expect_tx_elect(&ms.clc_full, 16);
+        clc_try_cancel_elect(smem_u32(&ms.clc_resp), &ms.clc_full);
+        if (!warp_all(mbar_wait(&ms.clc_full, k & 1, abort_flag, p.err, kErrWaitLoad,
+                                p.wait_limit_ns))) {
+          drain_wait(&ms.clc_full, k & 1);
+          break;
         }
+        const int nu = clc_response_ctaid_x(smem_u32(&ms.clc_resp));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.v_edge);
+        if (nu < 0)
+          w.n = -1;
+        else
+          w = plan_unit(p, nu, lane);
       }
-      tiles += n;
     }
   }
 
-  if constexpr (kSplit) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == kModWarpMma) {

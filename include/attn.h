@@ -383,8 +383,8 @@ int attn_row_ranges(const int *doc_lens, const int *prefix_lens, int *ranges, in
  * captured once and replayed while they grow.
  *
  * Limits: B, Hq, Hkv, Ncap >= 1; Hq % Hkv == 0; Hq / Hkv <= 128; D in
- * {64, 128}; B * Hkv <= 2^20, Hq <= 65535; Ncap <= 2^30; scale finite and
- * >= 0; the bf16 pointers and lse 16-byte, lens and slopes 4-byte aligned.
+ * {64, 128}; B * Hkv <= 2^20, Hq <= 65535; Ncap <= 2^30, and at most 12e6
+ * tiles of 128 keys in all: B * Hkv * ceil(Ncap / 128); scale finite and >= 0; the bf16 pointers and lse 16-byte, lens and slopes 4-byte aligned.
  * Scratch as attn_decode_splitkv: one buffer per recently used stream, none
  * allocated by a repeated call; during capture a buffer of the graph's own.
  */
@@ -400,7 +400,9 @@ int attn_decode_varlen(const void *q, const void *kcache, const void *vcache, co
  *   (positions 0 .. Np-1) and then its own first lens[b] cache keys
  *   (positions Np ..).  Its query is at position Np + lens[b] - 1.
  *
- * The other arguments, limits and scratch as attn_decode_varlen; 1 <= Np <= 2^30.
+ * The other arguments, limits and scratch as attn_decode_varlen; 1 <= Np <=
+ * 2^30, and Hkv * ceil(Np / 128) * ceil(B / (2 * floor(128 * Hkv / Hq))) <=
+ * 12e6 (the prefix is walked once for 2 * floor(128 * Hkv / Hq) requests).
  */
 int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix,
                        const void *kcache, const void *vcache, const int *lens, void *o,

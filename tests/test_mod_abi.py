@@ -24,6 +24,7 @@ SCORE = [(dict(scale=-0.5), SHAPE), (dict(scale=INF), SHAPE), (dict(scale=NAN), 
          (dict(slopes=A + 2), ALIGN)]
 DECODE = [(dict(B=0), SHAPE), (dict(Hq=3), SHAPE), (dict(Hkv=0), SHAPE), (dict(Ncap=0), SHAPE),
           (dict(Ncap=2**30 + 1), SHAPE), (dict(D=96), SHAPE),
+          (dict(B=2000, Ncap=2**19), SHAPE),        # more than 12e6 key tiles
           (dict(Hq=258, Hkv=2), SHAPE),             # more than 128 query heads on a KV head
           (dict(Hq=70000, Hkv=70000), SHAPE), (dict(B=2**20, Hkv=2), SHAPE),
           (dict(q=A + 8), ALIGN), (dict(kcache=A + 2), ALIGN), (dict(vcache=A + 4), ALIGN),
@@ -73,7 +74,7 @@ def test_decode_varlen_refusals(lib, change, status):
 
 
 PREFIX = SCORE + DECODE + [(dict(kprefix=0), NULL), (dict(vprefix=0), NULL), (dict(Np=0), SHAPE),
-                           (dict(Np=2**30 + 1), SHAPE), (dict(kprefix=A + 8), ALIGN),
+                           (dict(Np=2**30 + 1), SHAPE), (dict(Np=2**28, B=2000), SHAPE), (dict(kprefix=A + 8), ALIGN),
                            (dict(vprefix=A + 8), ALIGN)]
 
 
