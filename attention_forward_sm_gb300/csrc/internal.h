@@ -59,7 +59,12 @@ struct ScoreMod {
   float cap_in;         // scale / softcap; 0: no cap
   float cap_out;        // softcap * log2(e)
   const float* slopes;  // [Hq], or NULL: no distance bias
+  // s T(s^2) = the capped score for a raw product |s| <= cap_limit[i] (ascending;
+  // 0: not usable), T of kCapN<i> coefficients.
+  float cap_limit[3];
+  float cap_coef[3][6];
 };
+constexpr int kCapN0 = 3, kCapN1 = 4, kCapN2 = 6;
 
 // Prefill with modified scores.
 struct ModFwdParams {

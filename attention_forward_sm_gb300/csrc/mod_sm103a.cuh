@@ -90,27 +90,25 @@ struct RowInfo {
   float slope;  // times log2(e)
 };
 
-// Packed 2^... helpers ------------------------------------------------------
-
-// tanh_poly of score_mod.cuh on two values, times cap_out, minus m.
-struct CapCoef {
-  uint64_t c[6];
+// softcap * tanh(scale s / softcap) in log2 units, plus `add`, of two raw
+// products: s T(s^2) with T of degree N - 1 and all factors in its coefficients.
+// T's degree is what costs: N + 1 packed operations.  (FFMA2 does two fmas an
+// issue slot, but takes the fp32 pipe twice as long as one.)
+template <int N>
+struct CapPoly {
+  uint64_t c[N];
+  __device__ __forceinline__ explicit CapPoly(const float* coef) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = f32x2(coef[i], coef[i]);
+  }
+  __device__ __forceinline__ uint64_t operator()(uint64_t s, uint64_t add) const {
+    const uint64_t y = mul_f32x2(s, s);
+    uint64_t t = fma_f32x2(y, c[N - 1], c[N - 2]);
+#pragma unroll
+    for (int i = N - 3; i >= 0; --i) t = fma_f32x2(y, t, c[i]);
+    return fma_f32x2(s, t, add);
+  }
 };
-__device__ __forceinline__ CapCoef cap_coef(float out) {
-  const float c[6] = {0x1.ffffecp-1f, -0x1.5549d8p-2f, 0x1.0ffd3ap-3f,
-                      -0x1.a697a8p-5f, 0x1.11f45ap-6f, -0x1.90d924p-9f};
-  CapCoef r;
-#pragma unroll
-  for (int i = 0; i < 6; ++i) r.c[i] = f32x2(c[i] * out, c[i] * out);
-  return r;
-}
-__device__ __forceinline__ uint64_t cap2(const CapCoef& k, uint64_t x, uint64_t add) {
-  const uint64_t y = mul_f32x2(x, x);
-  uint64_t t = fma_f32x2(y, k.c[5], k.c[4]);
-#pragma unroll
-  for (int i = 3; i >= 0; --i) t = fma_f32x2(y, t, k.c[i]);
-  return fma_f32x2(x, t, add);
-}
 
 // Which of a thread's 64 columns its row sees: bit i of words[i / 32].
 struct Seen {
@@ -134,76 +132,110 @@ __device__ __forceinline__ void mask_to(float (&s)[64], const Seen& m, float wit
 }
 
 // The pass over one tile of 64 scores of a thread (half a row): from raw
-// products s to weights.
+// products s to weights 2^(x - m) of the scores x in log2 units.
+//
+// m need not be the row's largest score, only near enough that no weight
+// overflows and none that matters underflows, and the same for all of a row's
+// keys.  So where the modifications are cheap to apply together with the
+// exponential (`fused`), they are not applied before it just to find the
+// maximum: m comes from the largest raw product, or largest magnitude for
+// capped scores (the cap is odd and rises), and the bias of the nearest key
+// of the tile.  That is above the largest score by twice the capped largest
+// magnitude and the bias' change over the tile at most; kLoose limits it.
+// Weights then lie above 2^-kLoose where exact ones lie above 1/2, as precise.
+constexpr float kLoose = 100.f;
+
 template <bool kCap, bool kBias>
 struct Scores {
-  // Modifies the scores and returns the row's maximum (both halves) in log2
-  // units.  kb: key of s[0].  masked: some row of the warp does not see all 128
-  // keys of the tile.  Afterwards `final` says whether s holds scores in log2
-  // units (unseen: -inf) or still raw products (capped ones, none masked,
-  // which get their cap together with the exponential; `poly`: by the
-  // polynomial), or, without cap and bias, raw products with -inf.
-  __device__ static __forceinline__ float prepare(float (&s)[64], const ModKernelParams& p,
-                                                  const RowInfo& row, int kb, bool masked,
-                                                  bool& final, bool& poly) {
-    final = kBias || (kCap && masked);
-    poly = true;
+  bool fused;
+  int tier;        // capped, fused: which polynomial
+  float slope, rel;  // biased, fused: key kb + i has bias slope * (rel + i)
+
+  // kb: key of s[0], kt: of the tile.  masked: some row of the warp does not see
+  // all 128 keys of the tile.  Returns the row's m for the tile (both halves);
+  // s holds raw products if fused, else scores, -inf for unseen keys.
+  __device__ __forceinline__ float prepare(float (&s)[64], const ModKernelParams& p,
+                                           const RowInfo& row, int kt, int kb, bool masked) {
     Seen seen;
     if (masked) seen = seen_columns(row.lo - kb, row.hi - kb);
+    float top = 0.f;    // capped: largest score of the row by magnitude
+    bool poly = false;  // capped: the longest polynomial holds
+    fused = true;
     if constexpr (kCap) {
-      // the polynomial holds while |x| <= 1; what lies at unseen keys has no say
-      if (masked) mask_to(s, seen, 0.f);
+      fused = !masked;
+      if (masked) mask_to(s, seen, 0.f);  // what lies at unseen keys has no say
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
       for (int i = 0; i < 64; i += 4) {
         a0 = max3f(a0, fabsf(s[i]), fabsf(s[i + 1]));
         a1 = max3f(a1, fabsf(s[i + 2]), fabsf(s[i + 3]));
       }
-      poly = __all_sync(0xFFFFFFFFu, fmaxf(a0, a1) * p.mod.cap_in <= 1.f);
-      if (final) {
-        if (poly) {
-          const CapCoef c = cap_coef(p.mod.cap_out);
-          const uint64_t in2 = f32x2(p.mod.cap_in, p.mod.cap_in), zero = f32x2(0.f, 0.f);
+      a0 = fmaxf(a0, a1);
+      a0 = fmaxf(a0, __shfl_xor_sync(0xFFFFFFFFu, a0, 16));  // the row's other half
+      // the shortest polynomial that holds for all of the warp's scores
+      // (magnitudes are ordered like their bits)
+      const float all = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a0)));
+      poly = all <= p.mod.cap_limit[2];
+      tier = all <= p.mod.cap_limit[0] ? 0 : (all <= p.mod.cap_limit[1] ? 1 : 2);
+      fused = fused && (tier < 2 || poly);
+      top = tanh_any(a0 * p.mod.cap_in) * p.mod.cap_out;
+    }
+    bool linear = true;
+    if constexpr (kBias) {
+      // |pos - j| is linear in j over the keys that the row sees, but where
+      // they lie on both sides of pos: bias = slope * (j - c0), c0 = pos - ref
+      // (left of pos) or pos + ref (right).  The difference is small whatever
+      // its terms are.
+      const bool left = row.hi - 1 <= row.pos || kt + kBN - 1 <= row.pos;
+      const bool right = row.lo >= row.pos || kt >= row.pos;
+      linear = __all_sync(0xFFFFFFFFu, left || right);
+      slope = left ? row.slope : -row.slope;
+      const unsigned c0 = static_cast<unsigned>(row.pos) +
+                          static_cast<unsigned>(left ? -row.ref : row.ref);
+      rel = static_cast<float>(static_cast<int>(static_cast<unsigned>(kb) - c0));
+      // of the keys seen in the tile, the one that the bias favours
+      const int from = max(row.lo, kt), to = min(row.hi, kt + kBN) - 1;
+      const int best = slope >= 0.f ? to : from;
+      const float most = slope * (rel + static_cast<float>(best - kb));
+      fused = fused && linear &&
+              __all_sync(0xFFFFFFFFu, 2.f * top + fabsf(slope) * (kBN - 1) <= kLoose);
+      if constexpr (kCap) {
+        if (fused) return top + most;
+      } else if (fused) {
+        if (masked) mask_to(s, seen, -CUDART_INF_F);
+        const float mx = row_max(s);
+        return mx == -CUDART_INF_F ? mx : fmaf(mx, p.scale_log2, most);
+      }
+    } else if constexpr (kCap) {
+      fused = fused && __all_sync(0xFFFFFFFFu, 2.f * top <= kLoose);
+      if (fused) return top;
+    } else {
+      if (masked) mask_to(s, seen, -CUDART_INF_F);
+      const float mx = row_max(s);
+      return mx == -CUDART_INF_F ? mx : mx * p.scale_log2;
+    }
+
+    // ---- one modification after the other
+    if constexpr (kCap) {
+      if (poly) {
+        const CapPoly<kCapN2> cap(p.mod.cap_coef[2]);
+        const uint64_t zero = f32x2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < 64; i += 2)
-            unpack_f32x2(cap2(c, mul_f32x2(f32x2(s[i], s[i + 1]), in2), zero), s[i], s[i + 1]);
-        } else {
+        for (int i = 0; i < 64; i += 2)
+          unpack_f32x2(cap(f32x2(s[i], s[i + 1]), zero), s[i], s[i + 1]);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] = tanh_any(s[i] * p.mod.cap_in) * p.mod.cap_out;
-        }
+        for (int i = 0; i < 64; ++i) s[i] = tanh_any(s[i] * p.mod.cap_in) * p.mod.cap_out;
       }
     }
     if constexpr (kBias) {
-      const uint64_t mul = kCap ? f32x2(1.f, 1.f) : f32x2(p.scale_log2, p.scale_log2);
-      // |pos - j| is linear in j over the keys that the row sees, but where
-      // they lie on both sides of pos
-      const bool left = row.hi - 1 <= row.pos || kb + 63 <= row.pos;
-      const bool right = row.lo >= row.pos || kb >= row.pos;
-      if (__all_sync(0xFFFFFFFFu, left || right)) {
-        const float sl = left ? row.slope : -row.slope;
-        // bias = sl * (j - c0), c0 = pos - ref (left) or pos + ref (right);
-        // the difference is small whatever its terms are
-        const unsigned c0 = static_cast<unsigned>(row.pos) +
-                            static_cast<unsigned>(left ? -row.ref : row.ref);
-        const float rel = static_cast<float>(static_cast<int>(static_cast<unsigned>(kb) - c0));
-        uint64_t off[4];
+      const float m1 = kCap ? 1.f : p.scale_log2;
+      if (linear) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) off[i] = f32x2(sl * (2 * i), sl * (2 * i + 1));
-#pragma unroll
-        for (int g = 0; g < 64; g += 8) {
-          const float b0 = sl * (rel + g);
-          const uint64_t b2 = f32x2(b0, b0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = g + 2 * i;
-            unpack_f32x2(fma_f32x2(f32x2(s[e], s[e + 1]), mul, add_f32x2(b2, off[i])), s[e],
-                         s[e + 1]);
-          }
-        }
+        for (int i = 0; i < 64; ++i)
+          s[i] = fmaf(s[i], m1, slope * (rel + static_cast<float>(i)));
       } else {
         const unsigned d0 = static_cast<unsigned>(row.pos) - static_cast<unsigned>(kb);
-        float m1, unused;
-        unpack_f32x2(mul, m1, unused);
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
           const int dist = abs(static_cast<int>(d0 - i)) - row.ref;
@@ -212,6 +244,10 @@ struct Scores {
       }
     }
     if (masked) mask_to(s, seen, -CUDART_INF_F);
+    return row_max(s);
+  }
+
+  __device__ static __forceinline__ float row_max(const float (&s)[64]) {
     float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]);
     float a2 = fmaxf(s[4], s[5]), a3 = fmaxf(s[6], s[7]);
 #pragma unroll
@@ -221,62 +257,59 @@ struct Scores {
       a2 = max3f(a2, s[i + 4], s[i + 5]);
       a3 = max3f(a3, s[i + 6], s[i + 7]);
     }
-    float mx = max3f(a0, a1, fmaxf(a2, a3));
-    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));  // the row's other half
-    if (final || mx == -CUDART_INF_F) return mx;
-    // the cap is monotone: the largest raw score is the largest capped one
-    if constexpr (kCap) return tanh_any(mx * p.mod.cap_in) * p.mod.cap_out;
-    return mx * p.scale_log2;
+    const float mx = max3f(a0, a1, fmaxf(a2, a3));
+    return fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));  // the row's other half
   }
 
-  // pk = 2^(score - m) as bf16 pairs, low key first; returns their sum in
-  // fp32 before the rounding to bf16 (2^-9 of a weight on average: its effect
-  // on O is that of the rounding of O itself).  Unseen keys are -inf and give
+  // pk = the weights as bf16 pairs, low key first; returns their sum in fp32
+  // before the rounding to bf16 (2^-9 of a weight on average: its effect on O
+  // is that of the rounding of O itself).  Unseen keys are -inf and give
   // exactly 0 (scale_log2 is never 0, see mod_launch.cu).
-  __device__ static __forceinline__ float weights(const float (&s)[64], const ModKernelParams& p,
-                                                  float neg_m, bool final, bool poly,
-                                                  uint32_t (&pk)[32]) {
-    const uint64_t negm2 = f32x2(neg_m, neg_m);
+  __device__ __forceinline__ float weights(const float (&s)[64], const ModKernelParams& p,
+                                           float neg_m, uint32_t (&pk)[32]) const {
     uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
-    auto emit = [&](int i, uint64_t x01, uint64_t x23) {
-      float x0, x1, x2, x3;
-      unpack_f32x2(x01, x0, x1);
-      unpack_f32x2(x23, x2, x3);
-      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-      const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
-      acc0 = add_f32x2(acc0, f32x2(p0, p1));
-      acc1 = add_f32x2(acc1, f32x2(p2, p3));
-      pk[i / 2] = pack_bf16x2(p0, p1);
-      pk[i / 2 + 1] = pack_bf16x2(p2, p3);
-    };
-    if (final) {
+    // pass(f): f(pair of s, what to add to its scores) -> exponents
+    auto pass = [&](bool with_bias, auto f) {
+      uint64_t off[4], add = f32x2(neg_m, neg_m);
+      if (with_bias) {
 #pragma unroll
-      for (int i = 0; i < 64; i += 4)
-        emit(i, add_f32x2(f32x2(s[i], s[i + 1]), negm2), add_f32x2(f32x2(s[i + 2], s[i + 3]), negm2));
-    } else if constexpr (kCap) {
-      if (poly) {
-        const CapCoef c = cap_coef(p.mod.cap_out);
-        const uint64_t in2 = f32x2(p.mod.cap_in, p.mod.cap_in);
+        for (int i = 0; i < 4; ++i) off[i] = f32x2(slope * (2 * i), slope * (2 * i + 1));
+      }
 #pragma unroll
-        for (int i = 0; i < 64; i += 4)
-          emit(i, cap2(c, mul_f32x2(f32x2(s[i], s[i + 1]), in2), negm2),
-               cap2(c, mul_f32x2(f32x2(s[i + 2], s[i + 3]), in2), negm2));
-      } else {
+      for (int g = 0; g < 64; g += 8) {
+        if (with_bias) {
+          const float b = fmaf(slope, rel + static_cast<float>(g), neg_m);
+          add = f32x2(b, b);
+        }
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          float x[4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            x[v] = fmaf(tanh_any(s[i + v] * p.mod.cap_in), p.mod.cap_out, neg_m);
-          emit(i, f32x2(x[0], x[1]), f32x2(x[2], x[3]));
+        for (int i = 0; i < 8; i += 4) {
+          const int e = g + i;
+          const uint64_t a01 = with_bias ? add_f32x2(add, off[i / 2]) : add;
+          const uint64_t a23 = with_bias ? add_f32x2(add, off[i / 2 + 1]) : add;
+          float x0, x1, x2, x3;
+          unpack_f32x2(f(f32x2(s[e], s[e + 1]), a01), x0, x1);
+          unpack_f32x2(f(f32x2(s[e + 2], s[e + 3]), a23), x2, x3);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
+          acc0 = add_f32x2(acc0, f32x2(p0, p1));
+          acc1 = add_f32x2(acc1, f32x2(p2, p3));
+          pk[e / 2] = pack_bf16x2(p0, p1);
+          pk[e / 2 + 1] = pack_bf16x2(p2, p3);
         }
       }
+    };
+    if ((kCap || kBias) && !fused) {
+      pass(false, [](uint64_t x, uint64_t add) { return add_f32x2(x, add); });
+    } else if constexpr (kCap) {
+      if (tier == 0)
+        pass(kBias, CapPoly<kCapN0>(p.mod.cap_coef[0]));
+      else if (tier == 1)
+        pass(kBias, CapPoly<kCapN1>(p.mod.cap_coef[1]));
+      else
+        pass(kBias, CapPoly<kCapN2>(p.mod.cap_coef[2]));
     } else {
       const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
-#pragma unroll
-      for (int i = 0; i < 64; i += 4)
-        emit(i, fma_f32x2(f32x2(s[i], s[i + 1]), scale2, negm2),
-             fma_f32x2(f32x2(s[i + 2], s[i + 3]), scale2, negm2));
+      pass(kBias, [&](uint64_t x, uint64_t add) { return fma_f32x2(x, scale2, add); });
     }
     float u0, u1;
     unpack_f32x2(add_f32x2(acc0, acc1), u0, u1);
@@ -732,9 +765,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
         }
-        bool final, poly;
-        const float m_tile =
-            Scores<kCap, kBias>::prepare(s, p, row, kt + c * 64, masked, final, poly);
+        Scores<kCap, kBias> scores;
+        const float m_tile = scores.prepare(s, p, row, kt, kt + c * 64, masked);
         if constexpr (C::kSplitS) {
           // S_t has been read: the MMA warp may write the next tile's keys
           // [64, 128) over columns 64..127, which P does not use
@@ -750,7 +782,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
         }
         const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
         uint32_t pk[32];
-        const float rsum = Scores<kCap, kBias>::weights(s, p, neg_m, final, poly, pk);
+        const float rsum = scores.weights(s, p, neg_m, pk);
         l = fmaf(l, alpha, rsum);
         // rescale O_t when a row's maximum rose past the threshold: every P V
         // of earlier tiles has retired (it was issued before this S_t)
