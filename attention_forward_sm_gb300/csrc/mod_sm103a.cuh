@@ -62,6 +62,13 @@ struct Work {
   uint32_t v_first, v_last;  // ring items of V in the first and the last tile
 };
 
+// What the softmax warps know about a row: it sees keys [lo, hi) of the item's
+// K/V, and with a bias key j gets -slope * (|pos - j| - ref), pos and j counted
+// alike.  Kept in shared memory: a pass needs its registers for the scores.
+struct RowInfo {
+  int lo, hi, pos, ref;
+};
+
 // Items of a query tile in flight: a decode's are short, and planned well ahead;
 // a prefill's are taken from the grid, and only one ahead, which keeps the end
 // of the grid even.
@@ -69,6 +76,8 @@ template <bool kSplit>
 constexpr int kWorkSlots = kSplit ? 4 : 2;
 
 struct ModMisc {
+  RowInfo rows[2 * kBM];
+  float slopes[2 * kBM];  // times log2(e)
   uint64_t q_full[2], q_empty[2], unit_done;
   uint64_t s_full[2], s_read[2], p_full[2], o_done[2];
   uint64_t mma_done;
@@ -82,14 +91,6 @@ struct ModMisc {
   int abort_flag;
 };
 
-// What the softmax warps know about a row: it sees keys [lo, hi) of the item's
-// K/V, and with a bias key j gets -slope * (|pos - j| - ref), pos and j counted
-// alike.
-struct RowInfo {
-  int lo, hi, pos, ref;
-  float slope;  // times log2(e)
-};
-
 // softcap * tanh(scale s / softcap) in log2 units, plus `add`, of two raw
 // products: s T(s^2) with T of degree N - 1 and all factors in its coefficients.
 // T's degree is what costs: N + 1 packed operations.  (FFMA2 does two fmas an
@@ -98,8 +99,11 @@ template <int N>
 struct CapPoly {
   uint64_t c[N];
   __device__ __forceinline__ explicit CapPoly(const float* coef) {
+    // volatile: else the coefficients of every polynomial stay in registers
+    // across the tiles, and others spill
 #pragma unroll
-    for (int i = 0; i < N; ++i) c[i] = f32x2(coef[i], coef[i]);
+    for (int i = 0; i < N; ++i)
+      asm volatile("mov.b64 %0, {%1, %1};" : "=l"(c[i]) : "f"(coef[i]));
   }
   __device__ __forceinline__ uint64_t operator()(uint64_t s, uint64_t add) const {
     const uint64_t y = mul_f32x2(s, s);
@@ -155,8 +159,11 @@ struct Scores {
   // all 128 keys of the tile.  Returns the row's m for the tile (both halves);
   // s holds raw products if fused, else scores, -inf for unseen keys.
   __device__ __forceinline__ float prepare(float (&s)[64], const ModKernelParams& p,
-                                           const RowInfo& row, int kt, int kb, bool masked) {
+                                           const RowInfo& info, float row_slope, int kt, int kb,
+                                           bool masked) {
     Seen seen;
+    RowInfo row;
+    if (masked || kBias) row = info;
     if (masked) seen = seen_columns(row.lo - kb, row.hi - kb);
     float top = 0.f;    // capped: largest score of the row by magnitude
     bool poly = false;  // capped: the longest polynomial holds
@@ -171,14 +178,14 @@ struct Scores {
         a1 = max3f(a1, fabsf(s[i + 2]), fabsf(s[i + 3]));
       }
       a0 = fmaxf(a0, a1);
-      a0 = fmaxf(a0, __shfl_xor_sync(0xFFFFFFFFu, a0, 16));  // the row's other half
       // the shortest polynomial that holds for all of the warp's scores
       // (magnitudes are ordered like their bits)
       const float all = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a0)));
+      a0 = fmaxf(a0, __shfl_xor_sync(0xFFFFFFFFu, a0, 16));  // the row's other half
       poly = all <= p.mod.cap_limit[2];
       tier = all <= p.mod.cap_limit[0] ? 0 : (all <= p.mod.cap_limit[1] ? 1 : 2);
       fused = fused && (tier < 2 || poly);
-      top = tanh_any(a0 * p.mod.cap_in) * p.mod.cap_out;
+      top = fminf(a0 * p.scale_log2, p.mod.cap_out);  // |tanh x| <= |x|, 1
     }
     bool linear = true;
     if constexpr (kBias) {
@@ -189,7 +196,7 @@ struct Scores {
       const bool left = row.hi - 1 <= row.pos || kt + kBN - 1 <= row.pos;
       const bool right = row.lo >= row.pos || kt >= row.pos;
       linear = __all_sync(0xFFFFFFFFu, left || right);
-      slope = left ? row.slope : -row.slope;
+      slope = left ? row_slope : -row_slope;
       const unsigned c0 = static_cast<unsigned>(row.pos) +
                           static_cast<unsigned>(left ? -row.ref : row.ref);
       rel = static_cast<float>(static_cast<int>(static_cast<unsigned>(kb) - c0));
@@ -239,7 +246,7 @@ struct Scores {
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
           const int dist = abs(static_cast<int>(d0 - i)) - row.ref;
-          s[i] = fmaf(s[i], m1, -row.slope * static_cast<float>(dist));
+          s[i] = fmaf(s[i], m1, -row_slope * static_cast<float>(dist));
         }
       }
     }
@@ -270,32 +277,28 @@ struct Scores {
     uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
     // pass(f): f(pair of s, what to add to its scores) -> exponents
     auto pass = [&](bool with_bias, auto f) {
-      uint64_t off[4], add = f32x2(neg_m, neg_m);
-      if (with_bias) {
+      uint64_t add = f32x2(neg_m, neg_m);
+      const uint64_t next = f32x2(2.f * slope, 2.f * slope);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) off[i] = f32x2(slope * (2 * i), slope * (2 * i + 1));
-      }
-#pragma unroll
-      for (int g = 0; g < 64; g += 8) {
-        if (with_bias) {
-          const float b = fmaf(slope, rel + static_cast<float>(g), neg_m);
-          add = f32x2(b, b);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const int e = g + i;
-          const uint64_t a01 = with_bias ? add_f32x2(add, off[i / 2]) : add;
-          const uint64_t a23 = with_bias ? add_f32x2(add, off[i / 2 + 1]) : add;
-          float x0, x1, x2, x3;
-          unpack_f32x2(f(f32x2(s[e], s[e + 1]), a01), x0, x1);
-          unpack_f32x2(f(f32x2(s[e + 2], s[e + 3]), a23), x2, x3);
-          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
-          acc0 = add_f32x2(acc0, f32x2(p0, p1));
-          acc1 = add_f32x2(acc1, f32x2(p2, p3));
-          pk[e / 2] = pack_bf16x2(p0, p1);
-          pk[e / 2 + 1] = pack_bf16x2(p2, p3);
-        }
+      for (int e = 0; e < 64; e += 4) {
+        // The bias minus m, pair by pair: exact at every 16th key, a sum
+        // of a few steps in between (its roundings are below the score's).
+        if (with_bias && e % 16 == 0)
+          add = f32x2(fmaf(slope, rel + static_cast<float>(e), neg_m),
+                      fmaf(slope, rel + static_cast<float>(e + 1), neg_m));
+        const uint64_t a01 = add;
+        if (with_bias) add = add_f32x2(add, next);
+        const uint64_t a23 = add;
+        if (with_bias && e % 16 != 12) add = add_f32x2(add, next);
+        float x0, x1, x2, x3;
+        unpack_f32x2(f(f32x2(s[e], s[e + 1]), a01), x0, x1);
+        unpack_f32x2(f(f32x2(s[e + 2], s[e + 3]), a23), x2, x3);
+        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+        const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
+        acc0 = add_f32x2(acc0, f32x2(p0, p1));
+        acc1 = add_f32x2(acc1, f32x2(p2, p3));
+        pk[e / 2] = pack_bf16x2(p0, p1);
+        pk[e / 2 + 1] = pack_bf16x2(p2, p3);
       }
     };
     if ((kCap || kBias) && !fused) {
@@ -342,6 +345,26 @@ __device__ __forceinline__ bool work_publish(ModMisc& ms, const ModKernelParams&
     mbar_arrive(&ms.work_full[t][k % kSlots]);
   }
   return true;
+}
+
+// Row r of query tile t of an item: whether it exists, its query head, and where
+// its output (decode: its partial state) goes.
+template <bool kSplit>
+__device__ __forceinline__ bool item_row(const ModKernelParams& p, const Work& w, int t, int r,
+                                         bool tile_used, int& head, size_t& out) {
+  if constexpr (kSplit) {
+    const int req = w.kind ? 0 : r / p.G, g = r - req * p.G;
+    head = w.id * p.G + g;
+    out = w.kind ? static_cast<size_t>(w.slot) * p.G + r
+                 : static_cast<size_t>(w.slot) * p.pre_rows + t * kBM + r;
+    return tile_used &&
+           (w.kind ? r < p.G : req < p.per_tile && w.q0 + t * p.per_tile + req < p.B);
+  } else {
+    const int i = w.q0 + t * kBM + r;
+    head = w.id % p.Hq;
+    out = static_cast<size_t>(w.id) * p.Nq + i;
+    return i < p.Nq;
+  }
 }
 
 // Prefill item u (warp-wide): the query rows, and the key tiles they see.
@@ -641,68 +664,60 @@ __global__ void __launch_bounds__(kModThreads, 1)
       if (w.n < 0) break;
       const int ja = w.a[t], jb = w.b[t];
       // the row: which query, which keys
-      RowInfo row;
-      bool valid;
-      size_t out = 0;  // its row in the outputs
-      int head = 0;
-      row.lo = w.lo;
-      row.hi = w.hi;
-      if constexpr (kSplit) {
-        const int G = p.G, kind = w.kind;
-        const int req = kind ? 0 : r / G;
-        const int b = w.q0 + (kind ? 0 : t * p.per_tile) + req;
-        const int g = r - req * G;
-        valid = jb > 0 && (kind ? r < G : req < p.per_tile) && b < p.B;
-        head = w.id * G + g;
-        row.pos = 0;
-        if constexpr (kBias) {
-          // positions count from the item's first key
-          if (valid) row.pos = (kind ? w.hi : p.Np + request_len(p, b)) - 1;
-        }
-        out = kind ? static_cast<size_t>(w.slot) * G + r
-                   : static_cast<size_t>(w.slot) * p.pre_rows + t * kBM + r;
-      } else {
-        const int i = w.q0 + t * kBM + r;
-        valid = i < p.Nq;
-        head = w.id % p.Hq;
-        row.pos = p.q_offset + i;
-        out = static_cast<size_t>(w.id) * p.Nq + i;
-        if (valid) {
-          row.lo = 0;
-          row.hi = p.Nk;
-          if (p.ranges) {
-            const int2 rg = reinterpret_cast<const int2*>(
-                p.ranges)[static_cast<size_t>(w.id / p.Hq) * p.Nq + i];
-            row.lo = max(rg.x, 0);
-            row.hi = min(rg.y, p.Nk);
-          }
-          if (p.causal) row.hi = min(row.hi, row.pos + 1);
-          if (row.lo >= row.hi) row.lo = row.hi = 0;
-        }
-      }
-      row.slope = 0.f;
-      row.ref = 0;
-      if constexpr (kBias) {
-        if (valid) {
-          row.slope = p.mod.slopes[head] * kLog2e;
-          if constexpr (kSplit) {
-            // nearest: the query's own position; farthest: the first key of all
-            if (row.slope < 0.f) row.ref = (w.kind ? p.Np : 0) + row.pos;
-          } else if (row.lo < row.hi) {
-            row.ref = bias_ref(row.slope, row.pos, row.lo, row.hi);
-          }
-        }
-      }
-      // Keys that all rows of the warp see, and that any does.  (Rows that are not
-      // there took the item's span and see what the others do.)
-      const bool live = __any_sync(0xFFFFFFFFu, valid && row.lo < row.hi);
+      bool live;  // does a row of the warp exist and see a key?
       {
+        RowInfo row;
+        float slope = 0.f;
+        int head;
+        size_t out;
+        const bool valid = item_row<kSplit>(p, w, t, r, jb > 0, head, out);
+        // rows that are not there take the item's span and see what the others do
+        row.lo = w.lo;
+        row.hi = w.hi;
+        row.pos = row.ref = 0;
+        if constexpr (kSplit) {
+          if constexpr (kBias) {
+            if (valid) {
+              // positions count from the item's first key
+              const int b = w.q0 + (w.kind ? 0 : t * p.per_tile + r / p.G);
+              row.pos = (w.kind ? w.hi : p.Np + request_len(p, b)) - 1;
+              slope = p.mod.slopes[head] * kLog2e;
+              // nearest: the query's own position; farthest: the first key of all
+              if (slope < 0.f) row.ref = (w.kind ? p.Np : 0) + row.pos;
+            }
+          }
+        } else {
+          const int i = w.q0 + t * kBM + r;
+          row.pos = p.q_offset + i;
+          if (valid) {
+            row.lo = 0;
+            row.hi = p.Nk;
+            if (p.ranges) {
+              const int2 rg = reinterpret_cast<const int2*>(
+                  p.ranges)[static_cast<size_t>(w.id / p.Hq) * p.Nq + i];
+              row.lo = max(rg.x, 0);
+              row.hi = min(rg.y, p.Nk);
+            }
+            if (p.causal) row.hi = min(row.hi, row.pos + 1);
+            if (row.lo >= row.hi) row.lo = row.hi = 0;
+            if constexpr (kBias) {
+              slope = p.mod.slopes[head] * kLog2e;
+              if (row.lo < row.hi) row.ref = bias_ref(slope, row.pos, row.lo, row.hi);
+            }
+          }
+        }
+        live = __any_sync(0xFFFFFFFFu, valid && row.lo < row.hi);
+        // keys that all rows of the warp see, and that any does
         int4 seen;
         seen.x = __reduce_max_sync(0xFFFFFFFFu, row.lo);
         seen.y = __reduce_min_sync(0xFFFFFFFFu, row.hi);
         seen.z = __reduce_min_sync(0xFFFFFFFFu, row.lo < row.hi ? row.lo : INT_MAX);
         seen.w = live ? __reduce_max_sync(0xFFFFFFFFu, row.hi) : 0;
         if (lane == 0) ms.seen[warp] = seen;
+        if (c == 0) {
+          ms.rows[t * kBM + r] = row;
+          if constexpr (kBias) ms.slopes[t * kBM + r] = slope;
+        }
         __syncwarp();
       }
       float m = -CUDART_INF_F, l = 0.f;  // l: sum over this thread's half of the row
@@ -766,7 +781,9 @@ __global__ void __launch_bounds__(kModThreads, 1)
           for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
         }
         Scores<kCap, kBias> scores;
-        const float m_tile = scores.prepare(s, p, row, kt, kt + c * 64, masked);
+        const float m_tile =
+            scores.prepare(s, p, ms.rows[t * kBM + r], kBias ? ms.slopes[t * kBM + r] : 0.f, kt,
+                           kt + c * 64, masked);
         if constexpr (C::kSplitS) {
           // S_t has been read: the MMA warp may write the next tile's keys
           // [64, 128) over columns 64..127, which P does not use
@@ -813,6 +830,9 @@ __global__ void __launch_bounds__(kModThreads, 1)
       if (!kSplit || live) {
       tc_fence_after();
       // ---- epilogue: O / l and the LSE; a row that saw nothing gives 0 and -inf
+      int head;
+      size_t out;
+      const bool valid = item_row<kSplit>(p, w, t, r, jb > 0, head, out);
       const float l_row = l + __shfl_xor_sync(0xFFFFFFFFu, l, 16);
       const bool none = l_row == 0.f;
       const float inv = none ? 0.f : 1.f / l_row;
@@ -859,7 +879,9 @@ __global__ void __launch_bounds__(kModThreads, 1)
         if constexpr (kSplit)
           (w.kind ? p.part_lse : p.pre_lse)[out] = lse2;
         else
-          p.lse[out] = (lse2 - row.slope * static_cast<float>(row.ref)) * kLn2;
+          p.lse[out] = (kBias ? lse2 - ms.slopes[t * kBM + r] *
+                                           static_cast<float>(ms.rows[t * kBM + r].ref)
+                              : lse2) * kLn2;
       }
       }
       work_done<kSlots>(ms, t, k, lane);
