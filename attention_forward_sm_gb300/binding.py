@@ -7,7 +7,6 @@ cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -43,6 +42,8 @@ class AttnError(RuntimeError):
 def load(path: str = LIB_PATH):
     """Load libattn.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -384,12 +385,36 @@ def decode(q, kcache, vcache, nsplit: int, stream=None):
 
 
 # ------------------------------------------------------- modified scores: tensor helpers
+#
+# These calls are short enough (a decode step: 10 us on the GPU) that the host's
+# part of them shows.  So every argument is checked by plain attribute
+# comparisons first, and only a call that fails them goes through the checks that
+# find the words for it.
+
+_torch = None
+
+
+def _import_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _bf16(x, dev: int) -> bool:
+    return x.dtype is _torch.bfloat16 and x.is_cuda and x.get_device() == dev and x.is_contiguous()
+
+
+def _aux_ok(x, dtype, shape, dev: int) -> bool:
+    return x is None or (isinstance(x, _torch.Tensor) and x.dtype is dtype and x.shape == shape
+                         and x.is_cuda and x.get_device() == dev and x.is_contiguous())
 
 
 def _check_aux(dev, **tensors):
     """The optional int32 / fp32 device arrays of the calls below:
     name=(tensor or None, dtype, shape)."""
-    import torch
+    torch = _import_torch()
     for name, (x, dtype, shape) in tensors.items():
         if x is None:
             continue
@@ -407,29 +432,48 @@ def _check_aux(dev, **tensors):
             raise ValueError(f"{name} must be contiguous")
 
 
-@contextlib.contextmanager
-def _on(dev, stream, *tensors):
-    """Makes ``dev`` current, yields the stream to launch on, and when that is
-    not the device's current stream marks the tensors (and whatever the body
-    appends to the yielded list) as used on it, so that the caching allocator
-    does not hand their memory out again while the kernels run."""
-    import torch
-    with torch.cuda.device(dev):
-        cur = torch.cuda.current_stream()
-        if stream is None:
-            s = cur
-        elif isinstance(stream, int):
-            s = torch.cuda.ExternalStream(stream, device=dev) if stream else \
-                torch.cuda.default_stream(dev)
-        else:
-            s = stream
-            if s.device != dev:
-                raise ValueError(f"the stream is on {s.device}, the tensors on {dev}")
-        used = [x for x in tensors if x is not None]
-        yield s, used
-        if s.cuda_stream != cur.cuda_stream:
-            for x in used:
-                x.record_stream(s)
+def _current_raw_stream(dev: int) -> int:
+    return _torch.cuda.current_stream(dev).cuda_stream
+
+
+def _launch(fn, args, dev: int, stream, used):
+    """Calls the library's ``fn`` with ``dev`` current, on ``stream`` (None: the
+    device's current one).  On another stream than the current one the tensors
+    of ``used`` are marked as used there, so that the caching allocator does not
+    hand their memory out again while the kernels run."""
+    if _torch.cuda.current_device() != dev:
+        with _torch.cuda.device(dev):
+            return _launch(fn, args, dev, stream, used)
+    cur = _raw_stream(dev)
+    if stream is None:
+        s = cur
+    elif isinstance(stream, int):
+        s = stream
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        s = stream.cuda_stream
+    rc = fn(*args, s)
+    if rc:
+        _check(rc)
+    if s != cur:
+        side = stream
+        if isinstance(stream, int):
+            side = _torch.cuda.ExternalStream(s, device=dev) if s else \
+                _torch.cuda.default_stream(dev)
+        for x in used:
+            if x is not None:
+                x.record_stream(side)
+
+
+def _raw_stream(dev: int) -> int:
+    global _raw_stream
+    _raw_stream = getattr(_import_torch()._C, "_cuda_getCurrentRawStream", _current_raw_stream)
+    return _raw_stream(dev)
+
+
+def _addr(x):
+    return None if x is None else x.data_ptr()
 
 
 def forward_mod(q, k, v, *, causal: bool = False, scale: float | None = None,
@@ -441,23 +485,25 @@ def forward_mod(q, k, v, *, causal: bool = False, scale: float | None = None,
     [B,Nq,2] int32, see ``row_ranges``; None: all) and, with ``causal``, of
     these those at or before its position.  Rows that see nothing give 0 and
     -inf."""
-    import torch
+    torch = _torch or _import_torch()
     _check_ranks({"q": q, "k": k, "v": v}, {"q": 4, "k": 4, "v": 4})
-    _check_inputs({"q": q, "k": k, "v": v},
-                  {"B": (q.shape[0], k.shape[0], v.shape[0]), "D": (q.shape[3], k.shape[3], v.shape[3]),
-                   "Hkv": (k.shape[1], v.shape[1]), "Nk": (k.shape[2], v.shape[2])})
     B, Hq, Nq, D = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)),
-               ranges=(ranges, torch.int32, (B, Nq, 2)))
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _on(q.device, stream, q, k, v, slopes, ranges) as (s, used):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-        used += [o, lse]
-        attn_fwd_mod(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, D, causal, q_offset, scale, softcap,
-                     slopes, ranges, s)
+    _, Hkv, Nk, _ = k.shape
+    dev = q.get_device()
+    if not (k.shape == (B, Hkv, Nk, D) and v.shape == k.shape and _bf16(q, dev) and _bf16(k, dev)
+            and _bf16(v, dev) and _aux_ok(slopes, torch.float32, (Hq,), dev)
+            and _aux_ok(ranges, torch.int32, (B, Nq, 2), dev)):
+        _check_inputs({"q": q, "k": k, "v": v},
+                      {"B": (B, k.shape[0], v.shape[0]), "D": (D, k.shape[3], v.shape[3]),
+                       "Hkv": (Hkv, v.shape[1]), "Nk": (Nk, v.shape[2])})
+        _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)),
+                   ranges=(ranges, torch.int32, (B, Nq, 2)))
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+    _launch(load().attn_fwd_mod,
+            (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
+             Nq, Nk, D, bool(causal), q_offset, D ** -0.5 if scale is None else scale, softcap,
+             _addr(slopes), _addr(ranges)), dev, stream, (q, k, v, slopes, ranges, o, lse))
     return o, lse
 
 
@@ -467,16 +513,35 @@ def row_ranges(doc_lens, N: int, *, prefix_lens=None, causal: bool = True, strea
     sees its own document, with ``causal`` up to itself or to the end of the
     document's bidirectional prefix (``prefix_lens`` [B, M] int32).  Tokens
     behind the last document (padding) see nothing."""
-    import torch
+    torch = _torch or _import_torch()
     _check_ranks({"doc_lens": doc_lens}, {"doc_lens": 2})
     B, M = doc_lens.shape
-    _check_aux(doc_lens.device, doc_lens=(doc_lens, torch.int32, (B, M)),
-               prefix_lens=(prefix_lens, torch.int32, (B, M)))
-    with _on(doc_lens.device, stream, doc_lens, prefix_lens) as (s, used):
-        out = torch.empty((B, int(N), 2), dtype=torch.int32, device=doc_lens.device)
-        used.append(out)
-        attn_row_ranges(doc_lens, prefix_lens, out, B, N, M, causal, s)
+    dev = doc_lens.get_device()
+    if not (_aux_ok(doc_lens, torch.int32, (B, M), dev)
+            and _aux_ok(prefix_lens, torch.int32, (B, M), dev)):
+        _check_aux(doc_lens.device, doc_lens=(doc_lens, torch.int32, (B, M)),
+                   prefix_lens=(prefix_lens, torch.int32, (B, M)))
+    out = torch.empty((B, N, 2), dtype=torch.int32, device=doc_lens.device)
+    _launch(load().attn_row_ranges,
+            (doc_lens.data_ptr(), _addr(prefix_lens), out.data_ptr(), B, N, M, bool(causal)), dev,
+            stream, (doc_lens, prefix_lens, out))
     return out
+
+
+def _decode_args(q, kcache, vcache, lens, slopes):
+    """Checks what the two decode calls share; (B, Hq, Hkv, Ncap, D, device)."""
+    torch = _torch or _import_torch()
+    _check_ranks({"q": q, "kcache": kcache, "vcache": vcache}, {"q": 3, "kcache": 4, "vcache": 4})
+    B, Hq, D = q.shape
+    _, Hkv, Ncap, _ = kcache.shape
+    dev = q.get_device()
+    if not (kcache.shape == (B, Hkv, Ncap, D) and vcache.shape == kcache.shape and _bf16(q, dev)
+            and _bf16(kcache, dev) and _bf16(vcache, dev)
+            and _aux_ok(slopes, torch.float32, (Hq,), dev)
+            and _aux_ok(lens, torch.int32, (B,), dev)):
+        _check_decode_inputs(q, kcache, vcache)
+        _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)), lens=(lens, torch.int32, (B,)))
+    return B, Hq, Hkv, Ncap, D, dev
 
 
 def decode_varlen(q, kcache, vcache, lens=None, *, scale: float | None = None,
@@ -485,19 +550,13 @@ def decode_varlen(q, kcache, vcache, lens=None, *, scale: float | None = None,
     ``lens[b]`` keys of request b (``lens`` [B] int32, CUDA; None: all), with
     the score modifications of ``forward_mod``; the query is at position
     ``lens[b] - 1``."""
-    import torch
-    _check_decode_inputs(q, kcache, vcache)
-    B, Hq, D = q.shape
-    Hkv, Ncap = kcache.shape[1], kcache.shape[2]
-    _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)), lens=(lens, torch.int32, (B,)))
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _on(q.device, stream, q, kcache, vcache, lens, slopes) as (s, used):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-        used += [o, lse]
-        attn_decode_varlen(q, kcache, vcache, lens, o, lse, B, Hq, Hkv, Ncap, D, scale, softcap,
-                           slopes, s)
+    B, Hq, Hkv, Ncap, D, dev = _decode_args(q, kcache, vcache, lens, slopes)
+    o = _torch.empty_like(q)
+    lse = _torch.empty((B, Hq), dtype=_torch.float32, device=q.device)
+    _launch(load().attn_decode_varlen,
+            (q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), _addr(lens), o.data_ptr(),
+             lse.data_ptr(), B, Hq, Hkv, Ncap, D, D ** -0.5 if scale is None else scale, softcap,
+             _addr(slopes)), dev, stream, (q, kcache, vcache, lens, slopes, o, lse))
     return o, lse
 
 
@@ -507,22 +566,19 @@ def decode_prefix(q, kprefix, vprefix, kcache, vcache, lens=None, *, scale: floa
     ``vprefix`` [Hkv,Np,D] are seen by every request before its own
     ``lens[b]`` cache keys, and read once for the whole batch; the query is at
     position ``Np + lens[b] - 1``."""
-    import torch
     _check_ranks({"kprefix": kprefix, "vprefix": vprefix}, {"kprefix": 3, "vprefix": 3})
-    _check_decode_inputs(q, kcache, vcache)
-    _check_inputs({"q": q, "kprefix": kprefix, "vprefix": vprefix},
-                  {"Hkv": (kcache.shape[1], kprefix.shape[0], vprefix.shape[0]),
-                   "Np": (kprefix.shape[1], vprefix.shape[1]),
-                   "D": (q.shape[2], kprefix.shape[2], vprefix.shape[2])})
-    B, Hq, D = q.shape
-    Hkv, Ncap, Np = kcache.shape[1], kcache.shape[2], kprefix.shape[1]
-    _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)), lens=(lens, torch.int32, (B,)))
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _on(q.device, stream, q, kprefix, vprefix, kcache, vcache, lens, slopes) as (s, used):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-        used += [o, lse]
-        attn_decode_prefix(q, kprefix, vprefix, kcache, vcache, lens, o, lse, B, Hq, Hkv, Np, Ncap,
-                           D, scale, softcap, slopes, s)
+    B, Hq, Hkv, Ncap, D, dev = _decode_args(q, kcache, vcache, lens, slopes)
+    Np = kprefix.shape[1]
+    if not (kprefix.shape == (Hkv, Np, D) and vprefix.shape == kprefix.shape
+            and _bf16(kprefix, dev) and _bf16(vprefix, dev)):
+        _check_inputs({"q": q, "kprefix": kprefix, "vprefix": vprefix},
+                      {"Hkv": (Hkv, kprefix.shape[0], vprefix.shape[0]),
+                       "Np": (Np, vprefix.shape[1]), "D": (D, kprefix.shape[2], vprefix.shape[2])})
+    o = _torch.empty_like(q)
+    lse = _torch.empty((B, Hq), dtype=_torch.float32, device=q.device)
+    _launch(load().attn_decode_prefix,
+            (q.data_ptr(), kprefix.data_ptr(), vprefix.data_ptr(), kcache.data_ptr(),
+             vcache.data_ptr(), _addr(lens), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Np, Ncap, D,
+             D ** -0.5 if scale is None else scale, softcap, _addr(slopes)), dev, stream,
+            (q, kprefix, vprefix, kcache, vcache, lens, slopes, o, lse))
     return o, lse
