@@ -27,6 +27,11 @@
 //     that a second kernel merges through their log-sum-exp.  A prefix tile is
 //     read once for 256 rows, and at fewer than ~300 rows its bytes cost more
 //     than its products.
+//   * Own keys of at most 16 query heads per KV head are multiplied the other way
+//     round, S^T = K Q^T and O^T += V^T P^T: the 128 keys of a tile are the rows
+//     of the product, so 128 threads share a tile's scores, a key each, where
+//     as rows of S the few heads would occupy a fraction of one warp.  P^T goes
+//     through shared memory (it is the B operand).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -82,10 +87,14 @@ struct ModMisc {
   uint64_t s_full[2], s_read[2], p_full[2], o_done[2];
   uint64_t mma_done;
   uint64_t kv_full[8], kv_empty[8];
+  uint64_t q2_full[2][2], q2_empty[2][2];  // own keys, keys as rows: Q_t in two buffers
+  uint64_t p2_full[2];    // P^T_t in shared memory (one arrival per warp of four)
   uint64_t clc_full;      // the answer to the request for more work arrived
   uint64_t work_full[2][4], work_empty[2][4];
   uint4 clc_resp;
   Work work[2][4];        // query tile t's item k in slot k % kWorkSlots
+  float red[2][4][16];      // keys as rows: per warp and head, a maximum or a sum
+  float own_slopes[2][16];  // times log2(e)
   int4 seen[16];  // per softmax warp: keys [x, y) that all its rows see, [z, w) that any does
   uint32_t tmem_base;
   int abort_flag;
@@ -582,6 +591,201 @@ struct OwnPlan {
   }
 };
 
+// Decode of the requests' own keys with the keys as rows (G <= kSwapHeads query
+// heads per KV head).  S^T [128 keys, 16 heads] and O^T [D, 16 heads] of query
+// tile t lie in the first 16 of its S and O columns; Q_t and P^T_t in its Q tile
+// of shared memory: Q at kSwapQ of either buffer, P^T [16 heads, 128 keys]
+// at kSwapP, both in the 128-byte-swizzled layout of a K-major operand.
+constexpr int kSwapHeads = 16;
+constexpr uint32_t kSwapQ = 4096, kSwapP = 8192;  // bytes: buffer 1 of Q; P^T
+constexpr uint32_t kSwapPChunk = kSwapHeads * 128;  // 64 keys of P^T
+
+template <int D>
+struct SwapMma {
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kSwapHeads, false);
+  // A = V^T: V is [keys, D], so M runs along its rows (A MN-major, bit 15)
+  static constexpr uint32_t kIdescO = idesc_bf16_f32(128, kSwapHeads, false) | (1u << 15);
+  template <uint32_t kCol, int KK = 0>
+  __device__ static __forceinline__ void s(uint32_t tmem, uint32_t k_desc, uint32_t q_desc) {
+    if constexpr (KK < D / 16) {
+      constexpr uint32_t off = ((KK >> 2) * (kBM * 128) + (KK & 3) * 32) >> 4;
+      mma_ss<false, kCol, off, off, kIdescS>(tmem, k_desc, q_desc, KK > 0 ? 1u : 0u);
+      s<kCol, KK + 1>(tmem, k_desc, q_desc);
+    }
+  }
+  template <uint32_t kCol, int KK = 0>
+  __device__ static __forceinline__ void o(uint32_t tmem, uint32_t v_desc, uint32_t p_desc,
+                                           uint32_t acc) {
+    if constexpr (KK < kBN / 16) {
+      // the 64-element chunks of M are a tile's chunks apart; at D = 64 there
+      // is one, taken twice (lanes 64.. of O^T are not used)
+      constexpr uint32_t lbo = D == 128 ? static_cast<uint32_t>((kBM * 128) >> 4) << 16 : 0u;
+      constexpr uint32_t off_v = ((KK * 16 * 128) >> 4) + lbo - (1u << 16);  // desc has lbo 16
+      constexpr uint32_t off_p = ((KK >> 2) * kSwapPChunk + (KK & 3) * 32) >> 4;
+      mma_ss<false, kCol, off_v, off_p, kIdescO>(tmem, v_desc, p_desc, KK > 0 ? 1u : acc);
+      o<kCol, KK + 1>(tmem, v_desc, p_desc, acc);
+    }
+  }
+};
+
+// Softmax, epilogue and V's edge: four warps, thread = key of the tile (S^T, P^T)
+// or element of the head (O^T); NH >= G heads in registers.  The running maximum
+// is common to all 128 threads.  It is kept while no score exceeds it by more than 2^8:
+// one barrier that votes on that, and on every warp's waits having ended well,
+// is all that the threads of a tile exchange.
+template <int D, int NH, bool kCap, bool kBias>
+__device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, uint8_t* smem,
+                                         uint32_t tmem, int t, int k, uint32_t step,
+                                         uint32_t units) {
+  using C = Cfg<D, false>;
+  constexpr uint32_t kS = C::kStages;
+  constexpr int kSlots = kWorkSlots<true>;
+  const uint32_t abort_flag = smem_u32(&ms.abort_flag);
+  const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, me = q * 32 + lane;
+  const uint32_t bar = 1 + t;
+  const uint32_t s_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                          (t ? C::kColS1 : C::kColS0);
+  const uint32_t o_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                          (t ? C::kColO1 : C::kColO0);
+  // P^T[n][me]: row n of chunk me / 64, 16-byte unit (me % 64) / 8 swizzled by n
+  uint8_t* const pt = smem + C::kOffQ + t * C::kTileBytes + kSwapP + (me >> 6) * kSwapPChunk +
+                      (me & 7) * 2;
+  const int unit = (me & 63) >> 3;
+  const int G = p.G;
+  for (;; ++k) {
+    bool ok = work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax);
+    const Work& w = ms.work[t][k % kSlots];
+    if constexpr (kBias) {
+      if (ok && w.n > 0 && me < G) ms.own_slopes[t][me] = p.mod.slopes[w.id * G + me] * kLog2e;
+    }
+    if (bar_any(bar, 128, !ok)) return;
+    const int n_tiles = w.n, tile0 = w.tile0, len = w.hi;
+    if (n_tiles < 0) return;
+    float m[NH], l[NH];
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+      m[n] = -CUDART_INF_F;
+      l[n] = 0.f;
+    }
+    for (int j = 0; j < n_tiles; ++j, ++step) {
+      const int key = (tile0 + j) * kBN + me;
+      ok = warp_all(mbar_wait(&ms.s_full[t], step & 1, abort_flag, p.err, kErrWaitSoftmax,
+                              p.wait_limit_ns));
+      if ((w.edges & 2) && j == n_tiles - 1) {
+        // V behind the request's keys: its weights are 0, but 0 * NaN is not.
+        // (What was in V's ring slot before is multiplied: before this S.)
+        const uint32_t iv = w.v_last;
+        ok = ok && warp_all(mbar_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
+                                      kErrWaitSoftmax, p.wait_limit_ns));
+        uint4* v = reinterpret_cast<uint4*>(smem + C::kOffKV + (iv % kS) * C::kTileBytes);
+        const int keep = len - (tile0 + j) * kBN;
+        if (ok)
+          for (int i = me; i < kBN * C::kChunks * 8; i += 128)
+            if (((i >> 3) & (kBN - 1)) >= keep) v[i] = make_uint4(0, 0, 0, 0);
+      }
+      tc_fence_after();
+      float s[NH];
+      {
+        uint32_t sr[16];
+        tmem_ld_lane16(s_addr, sr);
+#pragma unroll
+        for (int n = 0; n < NH; ++n) s[n] = __uint_as_float(sr[n]);
+      }
+      bool above = false;
+#pragma unroll
+      for (int n = 0; n < NH; ++n) {
+        if constexpr (kCap)
+          s[n] = tanh_any(s[n] * p.mod.cap_in) * p.mod.cap_out;
+        else
+          s[n] *= p.scale_log2;
+        if constexpr (kBias) {
+          // the query is at the request's last key; a negative slope counts
+          // from the first key of all
+          const float slope = ms.own_slopes[t][n];
+          const int dist = len - 1 - key - (slope < 0.f ? p.Np + len - 1 : 0);
+          s[n] = fmaf(-slope, static_cast<float>(dist), s[n]);
+        }
+        if (key >= len || n >= G) s[n] = -CUDART_INF_F;
+        above = above || s[n] > m[n] + C::kRescale;
+      }
+      if (bar_any(bar, 128, above || !ok)) {
+        if (bar_any(bar, 128, !ok)) return;
+        // the tile's maximum of every head
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+          // as integers of the same order
+          int x = __float_as_int(s[n]);
+          x ^= (x >> 31) & 0x7FFFFFFF;
+          x = __reduce_max_sync(0xFFFFFFFFu, x);
+          if (lane == n) ms.red[t][q][n] = __int_as_float(x ^ ((x >> 31) & 0x7FFFFFFF));
+        }
+        bar_sync(bar, 128);
+        bool scale_o = false;
+        float alpha[NH];
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+          const float mx = fmaxf(fmaxf(ms.red[t][0][n], ms.red[t][1][n]),
+                                 fmaxf(ms.red[t][2][n], ms.red[t][3][n]));
+          alpha[n] = 1.f;
+          if (mx > m[n] + C::kRescale) {
+            if (m[n] != -CUDART_INF_F) alpha[n] = ex2_approx(m[n] - mx);
+            m[n] = mx;
+          }
+          l[n] *= alpha[n];
+          scale_o = scale_o || alpha[n] != 1.f;
+        }
+        if (j > 0 && scale_o) {  // alike in all threads
+          uint32_t v[16];
+          tmem_ld_lane16(o_addr, v);
+#pragma unroll
+          for (int n = 0; n < NH; ++n) v[n] = __float_as_uint(__uint_as_float(v[n]) * alpha[n]);
+          tmem_st_lane16(o_addr, v);
+          tmem_st_wait();
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NH; ++n) {
+        // -inf - -inf: nothing was seen yet, nor is this key
+        const float x = s[n] == -CUDART_INF_F ? 0.f : ex2_approx(s[n] - m[n]);
+        l[n] += x;
+        if (n < G)
+          *reinterpret_cast<__nv_bfloat16*>(pt + n * 128 + ((unit ^ (n & 7)) << 4)) =
+              __float2bfloat16_rn(x);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.p2_full[t]);
+    }
+    ok = warp_all(mbar_wait(&ms.o_done[t], units & 1, abort_flag, p.err, kErrWaitCorr,
+                            p.wait_limit_ns));
+    ++units;
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+#pragma unroll
+      for (int d = 16; d >= 1; d /= 2) l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], d);
+      if (lane == n) ms.red[t][q][n] = l[n];
+    }
+    if (bar_any(bar, 128, !ok)) return;
+    tc_fence_after();
+    const size_t row0 = static_cast<size_t>(w.slot) * G;
+    uint32_t o[16];
+    tmem_ld_lane16(o_addr, o);
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+      const float sum = (ms.red[t][0][n] + ms.red[t][1][n]) + (ms.red[t][2][n] + ms.red[t][3][n]);
+      const bool none = sum == 0.f;
+      const float inv = none ? 0.f : 1.f / sum;
+      if (n < G) {
+        if (me < D) p.part_o[(row0 + n) * D + me] = none ? 0.f : __uint_as_float(o[n]) * inv;
+        if (me == 0) p.part_lse[row0 + n] = none ? -CUDART_INF_F : m[n] + __log2f(sum);
+      }
+    }
+    tc_fence_before();
+    work_done<kSlots>(ms, t, k, lane);
+  }
+}
+
 template <int D, bool kSplit, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kModThreads, 1)
     mod_attn_kernel(const __grid_constant__ ModKernelParams p) {
@@ -601,6 +805,11 @@ __global__ void __launch_bounds__(kModThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&ms.q_full[t], 1);
       mbar_init(&ms.q_empty[t], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&ms.q2_full[t][i], 1);
+        mbar_init(&ms.q2_empty[t][i], 1);
+      }
+      mbar_init(&ms.p2_full[t], 4);
       mbar_init(&ms.s_full[t], 1);
       mbar_init(&ms.s_read[t], 8);
       mbar_init(&ms.p_full[t], 8);
@@ -658,10 +867,18 @@ __global__ void __launch_bounds__(kModThreads, 1)
     const uint32_t o_addr = lane_addr + (t ? C::kColO1 : C::kColO0);
     uint32_t step = 0;   // tiles done by this query tile: phase of s_full
     uint32_t units = 0;  // items that this query tile took part in: phase of o_done
-    for (int k = 0;; ++k) {
-      if (!work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax)) break;
+    const bool swap = kSplit && p.G <= kSwapHeads;  // own keys as rows
+    int k = 0;
+    bool fine = true;
+    for (; !swap || p.prefix_tiles > 0; ++k) {
+      fine = work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax);
+      if (!fine) break;
       const Work& w = ms.work[t][k % kSlots];  // read where needed: registers are scarce
       if (w.n < 0) break;
+      if (swap && w.kind == 2) {
+        work_done<kSlots>(ms, t, k++, lane);
+        break;
+      }
       const int ja = w.a[t], jb = w.b[t];
       // the row: which query, which keys
       bool live;  // does a row of the warp exist and see a key?
@@ -820,11 +1037,13 @@ __global__ void __launch_bounds__(kModThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.p_full[t]);
       }
+      fine = ok;
       if (!ok) break;
       if (jb > ja) {
         ok = warp_all(mbar_wait(&ms.o_done[t], units & 1, abort_flag, p.err, kErrWaitCorr,
                                 p.wait_limit_ns));
         ++units;
+        fine = ok;
         if (!ok) break;
       }
       if (!kSplit || live) {
@@ -885,6 +1104,24 @@ __global__ void __launch_bounds__(kModThreads, 1)
       }
       }
       work_done<kSlots>(ms, t, k, lane);
+    }
+    if constexpr (kSplit) {
+      if (swap && fine) {
+        if (warp & 4) {  // four warps per query tile do, the others only let items pass
+          for (;; ++k) {
+            if (!work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax)) break;
+            const int n = ms.work[t][k % kSlots].n;
+            work_done<kSlots>(ms, t, k, lane);
+            if (n < 0) break;
+          }
+        } else if (p.G <= 4) {
+          own_keys<D, 4, kCap, kBias>(p, ms, smem, tmem, t, k, step, units);
+        } else if (p.G <= 8) {
+          own_keys<D, 8, kCap, kBias>(p, ms, smem, tmem, t, k, step, units);
+        } else {
+          own_keys<D, 16, kCap, kBias>(p, ms, smem, tmem, t, k, step, units);
+        }
+      }
     }
   } else if (warp == kModWarpLoad) {
     // =====================================================================
@@ -987,6 +1224,26 @@ __global__ void __launch_bounds__(kModThreads, 1)
     }
     // ---- decode: the two runs of own keys, a tile of either in turn
     if constexpr (kSplit) {
+      const bool swap = p.G <= kSwapHeads;
+      uint32_t q2_0 = 0, q2_1 = 0;  // loads of Q_0, Q_1 for the products with keys as rows
+      auto load_q2 = [&](int t, int id, int q0) {
+        const uint32_t i = t ? q2_1 : q2_0, buf = i & 1;
+        // the buffer: free of the item two before, and of the prefix items' Q
+        const uint32_t before = t ? q1_loads : q0_loads;
+        if (i >= 2 ? !wait(&ms.q2_empty[t][buf], (i >> 1) + 1)
+                   : before > 0 && !wait(&ms.q_empty[t], before - 1))
+          return false;
+        if (t)
+          ++q2_1;
+        else
+          ++q2_0;
+        mbar_arrive_expect_tx_elect(&ms.q2_full[t][buf], C::kChunks * p.G * 128);
+        for (int ch = 0; ch < C::kChunks; ++ch)
+          tma_load_4d_elect(smem + C::kOffQ + t * C::kTileBytes + ch * (kBM * 128) + buf * kSwapQ,
+                            &p.tmap_q1, &ms.q2_full[t][buf], ch * C::kAtomElems, 0, id, q0,
+                            l2_policy_evict_last());
+        return true;
+      };
       int ks[2] = {k, k}, left[2] = {0, 0}, key[2], hi[2], bh[2];
       int done = 0;
       const uint64_t policy = l2_policy_evict_first();  // every byte is read once
@@ -1015,13 +1272,20 @@ __global__ void __launch_bounds__(kModThreads, 1)
           const int rows = hi[t] - key[t];
           ok = rows >= kBN ? load_tile(&p.tmap_k, key[t], bh[t], policy)
                            : load_tail(&p.tmap_kt, key[t], rows, bh[t], policy);
-          if (ok && fresh) ok = load_q(t, 1, id, q0);
+          if (ok && fresh) ok = swap ? load_q2(t, id, q0) : load_q(t, 1, id, q0);
           ok = ok && (rows >= kBN ? load_tile(&p.tmap_v, key[t], bh[t], policy)
                                   : load_tail(&p.tmap_vt, key[t], rows, bh[t], policy));
           key[t] += kBN;
           --left[t];
         }
       }
+      if (abort_set(abort_flag))
+        for (uint32_t back = 1; back <= 2; ++back) {
+          if (q2_0 >= back)
+            drain_wait(&ms.q2_full[0][(q2_0 - back) & 1], ((q2_0 - back) >> 1) & 1);
+          if (q2_1 >= back)
+            drain_wait(&ms.q2_full[1][(q2_1 - back) & 1], ((q2_1 - back) >> 1) & 1);
+        }
     }
     if (abort_set(abort_flag)) {
       // let the copies still in flight land before the CTA exits
@@ -1171,6 +1435,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
     // of K and V set the pace here.
     if constexpr (kSplit) {
       uint32_t ring = 2u * tiles;
+      const bool swap = p.G <= kSwapHeads;
+      uint32_t q2[2] = {0, 0}, p2[2] = {0, 0};  // Q taken, P V issued, with keys as rows
       int ks[2] = {k, k};
       int left[2] = {0, 0};                    // tiles left of the item
       uint32_t v_item[2] = {0, 0};             // ring item of the V whose P V is due
@@ -1183,10 +1449,17 @@ __global__ void __launch_bounds__(kModThreads, 1)
           if (due[t]) {
             const uint32_t iv = v_item[t];
             ok = wait(&ms.kv_full[iv % kS], iv / kS);
-            ok = ok && wait(&ms.p_full[t], (t ? steps1 : steps0) - 1u);
+            ok = ok && (swap ? wait(&ms.p2_full[t], p2[t]++)
+                             : wait(&ms.p_full[t], (t ? steps1 : steps0) - 1u));
             if (!ok) break;
             tc_fence_after();
-            issue_pv(t, desc_k + (iv % kS) * kTileDesc, (due[t] >> 1) & 1u);
+            const uint32_t v_desc = desc_k + (iv % kS) * kTileDesc, acc = (due[t] >> 1) & 1u;
+            if (!swap)
+              issue_pv(t, v_desc, acc);
+            else if (t)
+              SwapMma<D>::template o<C::kColO1>(tmem, v_desc, desc_k + kQ1 + (kSwapP >> 4), acc);
+            else
+              SwapMma<D>::template o<C::kColO0>(tmem, v_desc, desc_k + kQ0 + (kSwapP >> 4), acc);
             mma_commit(&ms.kv_empty[iv % kS]);
             if (due[t] & 4) mma_commit(&ms.o_done[t]);
             due[t] = 0;
@@ -1205,7 +1478,12 @@ __global__ void __launch_bounds__(kModThreads, 1)
               continue;
             }
             first = true;
-            ok = wait(&ms.q_full[t], t ? qs1++ : qs0++);
+            if (swap) {
+              ok = wait(&ms.q2_full[t][q2[t] & 1], q2[t] >> 1);
+              ++q2[t];
+            } else {
+              ok = wait(&ms.q_full[t], t ? qs1++ : qs0++);
+            }
           }
           const uint32_t ik = ring, iv = ring + 1u;
           ring += 2u;
@@ -1213,7 +1491,12 @@ __global__ void __launch_bounds__(kModThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t bk = desc_k + (ik % kS) * kTileDesc;
-          if (t)
+          const uint32_t buf = ((q2[t] - 1u) & 1u) * (kSwapQ >> 4);
+          if (swap && t)
+            SwapMma<D>::template s<C::kColS1>(tmem, bk, desc_k + kQ1 + buf);
+          else if (swap)
+            SwapMma<D>::template s<C::kColS0>(tmem, bk, desc_k + kQ0 + buf);
+          else if (t)
             issue_s_steps<D, false, C::kColS1, kQ1, 0, 0>(tmem, desc_k, bk);
           else
             issue_s_steps<D, false, C::kColS0, kQ0, 0, 0>(tmem, desc_k, bk);
@@ -1224,7 +1507,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
           else
             ++steps0;
           const bool last = left[t] == 1;
-          if (last) mma_commit(&ms.q_empty[t]);
+          if (last) mma_commit(swap ? &ms.q2_empty[t][(q2[t] - 1u) & 1u] : &ms.q_empty[t]);
           v_item[t] = iv;
           due[t] = 1 | (first ? 0 : 2) | (last ? 4 : 0);
           --left[t];
