@@ -142,8 +142,14 @@ __host__ __device__ inline uint32_t run_of(uint32_t total, uint32_t runs, uint32
 // One launch each, by head size and modifications.
 cudaError_t launch_mod_fwd_d64(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
 cudaError_t launch_mod_fwd_d128(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d64(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d128(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d64_h0(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d64_h4(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d64_h8(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d64_h16(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d128_h0(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d128_h4(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d128_h8(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_mod_split_d128_h16(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
 
 // 3-D bf16 view [BH, N, D], box {64, rows, 1}; 4-D view [B, Hkv, G, D] of the
 // queries of a decode, box {64, G, 1, requests}.  Return an ATTN_* status.

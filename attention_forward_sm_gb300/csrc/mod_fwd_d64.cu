@@ -1,10 +1,11 @@
-// mod_attn_kernel, prefill, D = 64 (a translation unit of its own: they compile in parallel).
+// mod_attn_kernel, prefill, D = 64 (translation units of their own compile in
+// parallel).
 #include "mod_sm103a.cuh"
 
 namespace attn {
 
 cudaError_t launch_mod_fwd_d64(const ModKernelParams& p, unsigned grid, cudaStream_t stream) {
-  return launch_variant<64, false>(p, grid, stream);
+  return launch_variant<64, false, 0>(p, grid, stream);
 }
 
 }  // namespace attn

@@ -174,14 +174,17 @@ int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
   d.k->pre_lse = reinterpret_cast<float*>(base + d.pre_lse);
   d.k->part_o = reinterpret_cast<float*>(base + d.part_o);
   d.k->part_lse = reinterpret_cast<float*>(base + d.part_lse);
-  cudaError_t e;
-  if (d.D == 128) {
-    e = launch_mod_split_d128(*d.k, d.ctas, stream);
-    if (e == cudaSuccess) e = launch_combine<128>(*d.k, d.ctas, stream);
-  } else {
-    e = launch_mod_split_d64(*d.k, d.ctas, stream);
-    if (e == cudaSuccess) e = launch_combine<64>(*d.k, d.ctas, stream);
-  }
+  using Launch = cudaError_t (*)(const ModKernelParams&, unsigned, cudaStream_t);
+  static const Launch split[2][4] = {
+      {launch_mod_split_d64_h4, launch_mod_split_d64_h8, launch_mod_split_d64_h16,
+       launch_mod_split_d64_h0},
+      {launch_mod_split_d128_h4, launch_mod_split_d128_h8, launch_mod_split_d128_h16,
+       launch_mod_split_d128_h0}};
+  const int G = d.k->G, heads = G <= 4 ? 0 : (G <= 8 ? 1 : (G <= 16 ? 2 : 3));
+  cudaError_t e = split[d.D == 128][heads](*d.k, d.ctas, stream);
+  if (e == cudaSuccess)
+    e = d.D == 128 ? launch_combine<128>(*d.k, d.ctas, stream)
+                   : launch_combine<64>(*d.k, d.ctas, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 

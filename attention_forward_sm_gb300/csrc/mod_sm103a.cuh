@@ -46,6 +46,27 @@
 namespace attn {
 namespace {
 
+// mbar_wait of ptx.cuh in fewer instructions: the kernel has a wait at every turn,
+// and its code has to stay in the instruction cache.
+__device__ __forceinline__ bool mod_wait(uint64_t* bar, uint32_t parity, uint32_t abort_sa,
+                                         unsigned int* err, uint32_t site, uint64_t limit_ns) {
+  uint32_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0u) {
+      uint32_t now;  // wraps after 4.3 s, the limit is 2
+      asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+      if (it == 64u) t0 = now;
+      if (abort_set(abort_sa)) return false;
+      if (now - t0 > static_cast<uint32_t>(limit_ns)) {
+        abort_raise(abort_sa);
+        atomicOr(err, site);
+        return false;
+      }
+    }
+  }
+}
+
 constexpr int kModThreads = 640;  // 16 softmax warps, load, MMA, 2 planning warps
 constexpr int kModWarpLoad = 16, kModWarpMma = 17, kModWarpPlan = 18;
 // setmaxnreg split of the 61440 registers the launch gets (640 threads x 96)
@@ -99,6 +120,12 @@ struct ModMisc {
   uint32_t tmem_base;
   int abort_flag;
 };
+
+// TMEM columns of query tile 0: S (P over its first half), O, at D = 64 Q; tile
+// 1's lie kTileCols behind.
+constexpr uint32_t kTileCols = 128, kColS = 0, kColO = 256;
+template <int D>
+constexpr uint32_t kColQ = kColO + D;  // D = 64: 320 and 448
 
 // softcap * tanh(scale s / softcap) in log2 units, plus `add`, of two raw
 // products: s T(s^2) with T of degree N - 1 and all factors in its coefficients.
@@ -334,7 +361,7 @@ struct Scores {
 template <int kSlots>
 __device__ __forceinline__ bool work_wait(ModMisc& ms, const ModKernelParams& p, int t, int k,
                                           uint32_t abort_flag, uint32_t site) {
-  return warp_all(mbar_wait(&ms.work_full[t][k % kSlots], (k / kSlots) & 1, abort_flag, p.err,
+  return warp_all(mod_wait(&ms.work_full[t][k % kSlots], (k / kSlots) & 1, abort_flag, p.err,
                             site, p.wait_limit_ns));
 }
 template <int kSlots>
@@ -346,7 +373,7 @@ template <int kSlots>
 __device__ __forceinline__ bool work_publish(ModMisc& ms, const ModKernelParams& p, int t, int k,
                                              const Work& w, uint32_t abort_flag, int lane) {
   if (k >= kSlots &&
-      !warp_all(mbar_wait(&ms.work_empty[t][k % kSlots], (k / kSlots + 1) & 1, abort_flag, p.err,
+      !warp_all(mod_wait(&ms.work_empty[t][k % kSlots], (k / kSlots + 1) & 1, abort_flag, p.err,
                           kErrWaitLoad, p.wait_limit_ns)))
     return false;
   if (lane == 0) {
@@ -644,9 +671,9 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
   const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, me = q * 32 + lane;
   const uint32_t bar = 1 + t;
   const uint32_t s_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                          (t ? C::kColS1 : C::kColS0);
+                          kColS + t * kTileCols;
   const uint32_t o_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                          (t ? C::kColO1 : C::kColO0);
+                          kColO + t * kTileCols;
   // P^T[n][me]: row n of chunk me / 64, 16-byte unit (me % 64) / 8 swizzled by n
   uint8_t* const pt = smem + C::kOffQ + t * C::kTileBytes + kSwapP + (me >> 6) * kSwapPChunk +
                       (me & 7) * 2;
@@ -669,13 +696,13 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
     }
     for (int j = 0; j < n_tiles; ++j, ++step) {
       const int key = (tile0 + j) * kBN + me;
-      ok = warp_all(mbar_wait(&ms.s_full[t], step & 1, abort_flag, p.err, kErrWaitSoftmax,
+      ok = warp_all(mod_wait(&ms.s_full[t], step & 1, abort_flag, p.err, kErrWaitSoftmax,
                               p.wait_limit_ns));
       if ((w.edges & 2) && j == n_tiles - 1) {
         // V behind the request's keys: its weights are 0, but 0 * NaN is not.
         // (What was in V's ring slot before is multiplied: before this S.)
         const uint32_t iv = w.v_last;
-        ok = ok && warp_all(mbar_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
+        ok = ok && warp_all(mod_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
                                       kErrWaitSoftmax, p.wait_limit_ns));
         uint4* v = reinterpret_cast<uint4*>(smem + C::kOffKV + (iv % kS) * C::kTileBytes);
         const int keep = len - (tile0 + j) * kBN;
@@ -757,7 +784,7 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.p2_full[t]);
     }
-    ok = warp_all(mbar_wait(&ms.o_done[t], units & 1, abort_flag, p.err, kErrWaitCorr,
+    ok = warp_all(mod_wait(&ms.o_done[t], units & 1, abort_flag, p.err, kErrWaitCorr,
                             p.wait_limit_ns));
     ++units;
 #pragma unroll
@@ -786,7 +813,7 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
   }
 }
 
-template <int D, bool kSplit, bool kCap, bool kBias>
+template <int D, bool kSplit, bool kCap, bool kBias, int kHeads>
 __global__ void __launch_bounds__(kModThreads, 1)
     mod_attn_kernel(const __grid_constant__ ModKernelParams p) {
   using C = Cfg<D, false>;
@@ -863,11 +890,11 @@ __global__ void __launch_bounds__(kModThreads, 1)
     const int r = lbase + (lane & 15);                           // row within the tile
     const int c = lane >> 4;                                     // column half of the row
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(lbase) << 16);
-    const uint32_t s_addr = lane_addr + (t ? C::kColS1 : C::kColS0);
-    const uint32_t o_addr = lane_addr + (t ? C::kColO1 : C::kColO0);
+    const uint32_t s_addr = lane_addr + kColS + t * kTileCols;
+    const uint32_t o_addr = lane_addr + kColO + t * kTileCols;
     uint32_t step = 0;   // tiles done by this query tile: phase of s_full
     uint32_t units = 0;  // items that this query tile took part in: phase of o_done
-    const bool swap = kSplit && p.G <= kSwapHeads;  // own keys as rows
+    constexpr bool swap = kHeads > 0;  // own keys as rows
     int k = 0;
     bool fine = true;
     for (; !swap || p.prefix_tiles > 0; ++k) {
@@ -949,7 +976,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
         }
         const int edges = w.edges;
         const bool edge = ((edges & 1) && j == 0) || ((edges & 2) && j == w.n - 1);
-        if (!warp_all(mbar_wait(&ms.s_full[t], step & 1, abort_flag, p.err, kErrWaitSoftmax,
+        if (!warp_all(mod_wait(&ms.s_full[t], step & 1, abort_flag, p.err, kErrWaitSoftmax,
                                 p.wait_limit_ns))) {
           ok = false;
           break;
@@ -960,7 +987,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
           // in its ring slot before has been multiplied already (before this
           // S), so the slot's barrier is in this tile's phase.
           const uint32_t iv = j == w.n - 1 ? w.v_last : w.v_first;
-          if (!warp_all(mbar_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
+          if (!warp_all(mod_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
                                   kErrWaitSoftmax, p.wait_limit_ns))) {
             ok = false;
             break;
@@ -1040,7 +1067,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
       fine = ok;
       if (!ok) break;
       if (jb > ja) {
-        ok = warp_all(mbar_wait(&ms.o_done[t], units & 1, abort_flag, p.err, kErrWaitCorr,
+        ok = warp_all(mod_wait(&ms.o_done[t], units & 1, abort_flag, p.err, kErrWaitCorr,
                                 p.wait_limit_ns));
         ++units;
         fine = ok;
@@ -1105,8 +1132,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
       }
       work_done<kSlots>(ms, t, k, lane);
     }
-    if constexpr (kSplit) {
-      if (swap && fine) {
+    if constexpr (swap) {
+      if (fine) {
         if (warp & 4) {  // four warps per query tile do, the others only let items pass
           for (;; ++k) {
             if (!work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax)) break;
@@ -1114,12 +1141,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
             work_done<kSlots>(ms, t, k, lane);
             if (n < 0) break;
           }
-        } else if (p.G <= 4) {
-          own_keys<D, 4, kCap, kBias>(p, ms, smem, tmem, t, k, step, units);
-        } else if (p.G <= 8) {
-          own_keys<D, 8, kCap, kBias>(p, ms, smem, tmem, t, k, step, units);
         } else {
-          own_keys<D, 16, kCap, kBias>(p, ms, smem, tmem, t, k, step, units);
+          own_keys<D, kHeads, kCap, kBias>(p, ms, smem, tmem, t, k, step, units);
         }
       }
     }
@@ -1133,32 +1156,23 @@ __global__ void __launch_bounds__(kModThreads, 1)
     uint32_t q0_loads = 0, q1_loads = 0;  // loads of Q_0, Q_1 issued
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-      return warp_all(mbar_wait(bar, phase & 1u, abort_flag, p.err, kErrWaitLoad, p.wait_limit_ns));
+      return warp_all(mod_wait(bar, phase & 1u, abort_flag, p.err, kErrWaitLoad, p.wait_limit_ns));
     };
-    // one K or V tile into the ring
-    auto load_tile = [&](const CUtensorMap* map, int key, int bh, uint64_t policy) {
+    // A K or V tile into the ring: `boxes` boxes of 128 keys (one), or of 32 (the
+    // last tile of a request's keys: little of the cache's unused tail is read)
+    auto load_tile = [&](const CUtensorMap* map, int key, int box_keys, int boxes, int bh,
+                         uint64_t policy) {
       const uint32_t s = g % kS;
       if (!wait(&ms.kv_empty[s], (g / kS) + 1)) return false;
-      mbar_arrive_expect_tx_elect(&ms.kv_full[s], C::kTileBytes);
+      mbar_arrive_expect_tx_elect(&ms.kv_full[s], boxes * box_keys * (C::kChunks * 128));
       uint8_t* dst = smem + C::kOffKV + s * C::kTileBytes;
-      for (int ch = 0; ch < C::kChunks; ++ch)
-        tma_load_3d_elect(dst + ch * (kBM * 128), map, &ms.kv_full[s], ch * C::kAtomElems, key, bh,
-                          policy);
-      ++g;
-      return true;
-    };
-    // the last tile of a request: its first `rows` keys, 32 at a time, so that
-    // little of the cache's unused tail is read
-    auto load_tail = [&](const CUtensorMap* map, int key, int rows, int bh, uint64_t policy) {
-      const uint32_t s = g % kS;
-      if (!wait(&ms.kv_empty[s], (g / kS) + 1)) return false;
-      const int boxes = (rows + 31) / 32;
-      mbar_arrive_expect_tx_elect(&ms.kv_full[s], boxes * C::kChunks * 32 * 128);
-      uint8_t* dst = smem + C::kOffKV + s * C::kTileBytes;
-      for (int ch = 0; ch < C::kChunks; ++ch)
-        for (int i = 0; i < boxes; ++i)
+#pragma unroll 1
+      for (int i = 0; i < boxes; ++i) {
+#pragma unroll
+        for (int ch = 0; ch < C::kChunks; ++ch)
           tma_load_3d_elect(dst + ch * (kBM * 128) + i * (32 * 128), map, &ms.kv_full[s],
                             ch * C::kAtomElems, key + 32 * i, bh, policy);
+      }
       ++g;
       return true;
     };
@@ -1212,80 +1226,92 @@ __global__ void __launch_bounds__(kModThreads, 1)
       } else {
         bh = (id / p.Hq) * p.Hkv + (id % p.Hq) / p.G;
       }
-      for (int j = 0; j < n && ok; ++j) {
-        const int key = (tile0 + j) * kBN;
-        ok = load_tile(kSplit ? &p.tmap_kp : &p.tmap_k, key, bh, policy);
-        if (j == 0) {
+#pragma unroll 1
+      for (int i = 0; i < 2 * n && ok; ++i) {  // K, V, K, V, ..
+        ok = load_tile((i & 1) ? (kSplit ? &p.tmap_vp : &p.tmap_v)
+                               : (kSplit ? &p.tmap_kp : &p.tmap_k),
+                       (tile0 + (i >> 1)) * kBN, kBN, 1, bh, policy);
+        if (i == 0) {
           ok = ok && (!use0 || load_q(0, 0, id, q0));
           ok = ok && (!use1 || load_q(1, 0, id, q0));
         }
-        ok = ok && load_tile(kSplit ? &p.tmap_vp : &p.tmap_v, key, bh, policy);
       }
     }
     // ---- decode: the two runs of own keys, a tile of either in turn
     if constexpr (kSplit) {
-      const bool swap = p.G <= kSwapHeads;
-      uint32_t q2_0 = 0, q2_1 = 0;  // loads of Q_0, Q_1 for the products with keys as rows
-      auto load_q2 = [&](int t, int id, int q0) {
-        const uint32_t i = t ? q2_1 : q2_0, buf = i & 1;
-        // the buffer: free of the item two before, and of the prefix items' Q
-        const uint32_t before = t ? q1_loads : q0_loads;
-        if (i >= 2 ? !wait(&ms.q2_empty[t][buf], (i >> 1) + 1)
-                   : before > 0 && !wait(&ms.q_empty[t], before - 1))
-          return false;
-        if (t)
-          ++q2_1;
-        else
-          ++q2_0;
-        mbar_arrive_expect_tx_elect(&ms.q2_full[t][buf], C::kChunks * p.G * 128);
-        for (int ch = 0; ch < C::kChunks; ++ch)
-          tma_load_4d_elect(smem + C::kOffQ + t * C::kTileBytes + ch * (kBM * 128) + buf * kSwapQ,
-                            &p.tmap_q1, &ms.q2_full[t][buf], ch * C::kAtomElems, 0, id, q0,
-                            l2_policy_evict_last());
-        return true;
+      // Both runs go through the same code, in turn: the state of one is kept aside
+      // while the other's is worked on.
+      struct Run {
+        int k, left, key, hi, bh;
+        uint32_t q2;  // loads of Q for the products with keys as rows
+        bool over;
       };
-      int ks[2] = {k, k}, left[2] = {0, 0}, key[2], hi[2], bh[2];
-      int done = 0;
+      Run cur = {k, 0, 0, 0, 0, 0, false}, other = cur;
       const uint64_t policy = l2_policy_evict_first();  // every byte is read once
-      while (ok && done != 3) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || (done >> t & 1)) continue;
+#pragma unroll 1
+      for (int t = 0; ok && !(cur.over && other.over); t ^= 1) {
+        if (!cur.over) {
+          const bool fresh = cur.left == 0;
           int id = 0, q0 = 0;
-          const bool fresh = left[t] == 0;
           if (fresh) {
-            ok = work_wait<kSlots>(ms, p, t, ks[t], abort_flag, kErrWaitLoad);
+            ok = work_wait<kSlots>(ms, p, t, cur.k, abort_flag, kErrWaitLoad);
             if (!ok) break;
-            const Work& w = ms.work[t][ks[t] % kSlots];
-            left[t] = w.n;
-            key[t] = w.tile0 * kBN;
-            hi[t] = w.hi;
+            const Work& w = ms.work[t][cur.k % kSlots];
+            cur.left = w.n;
+            cur.key = w.tile0 * kBN;
+            cur.hi = w.hi;
             id = w.id;
             q0 = w.q0;
-            work_done<kSlots>(ms, t, ks[t]++, lane);
-            bh[t] = q0 * p.Hkv + id;
-            if (left[t] < 0) {
-              done |= 1 << t;
-              continue;
-            }
+            cur.bh = q0 * p.Hkv + id;
+            work_done<kSlots>(ms, t, cur.k++, lane);
+            cur.over = cur.left < 0;
           }
-          const int rows = hi[t] - key[t];
-          ok = rows >= kBN ? load_tile(&p.tmap_k, key[t], bh[t], policy)
-                           : load_tail(&p.tmap_kt, key[t], rows, bh[t], policy);
-          if (ok && fresh) ok = swap ? load_q2(t, id, q0) : load_q(t, 1, id, q0);
-          ok = ok && (rows >= kBN ? load_tile(&p.tmap_v, key[t], bh[t], policy)
-                                  : load_tail(&p.tmap_vt, key[t], rows, bh[t], policy));
-          key[t] += kBN;
-          --left[t];
+          if (!cur.over) {
+            const int rows = cur.hi - cur.key;
+            const bool whole = rows >= kBN;
+#pragma unroll 1
+            for (int i = 0; i < 2 && ok; ++i) {  // K, V
+              ok = load_tile(i ? (whole ? &p.tmap_v : &p.tmap_vt)
+                               : (whole ? &p.tmap_k : &p.tmap_kt),
+                             cur.key, whole ? kBN : 32, whole ? 1 : (rows + 31) / 32, cur.bh,
+                             policy);
+              if (i == 0 && fresh && ok) {
+                if constexpr (kHeads > 0) {
+                  const uint32_t buf = cur.q2 & 1;
+                  // the buffer: free of the item two before, and of the prefix items' Q
+                  const uint32_t before = t ? q1_loads : q0_loads;
+                  ok = cur.q2 >= 2 ? wait(&ms.q2_empty[t][buf], (cur.q2 >> 1) + 1)
+                                   : before == 0 || wait(&ms.q_empty[t], before - 1);
+                  if (!ok) break;
+                  ++cur.q2;
+                  mbar_arrive_expect_tx_elect(&ms.q2_full[t][buf], C::kChunks * p.G * 128);
+                  for (int ch = 0; ch < C::kChunks; ++ch)
+                    tma_load_4d_elect(smem + C::kOffQ + t * C::kTileBytes + ch * (kBM * 128) +
+                                          buf * kSwapQ,
+                                      &p.tmap_q1, &ms.q2_full[t][buf], ch * C::kAtomElems, 0, id,
+                                      q0, l2_policy_evict_last());
+                } else {
+                  ok = load_q(t, 1, id, q0);
+                }
+              }
+            }
+            cur.key += kBN;
+            --cur.left;
+          }
         }
+        const Run next = other;
+        other = cur;
+        cur = next;
       }
-      if (abort_set(abort_flag))
-        for (uint32_t back = 1; back <= 2; ++back) {
-          if (q2_0 >= back)
-            drain_wait(&ms.q2_full[0][(q2_0 - back) & 1], ((q2_0 - back) >> 1) & 1);
-          if (q2_1 >= back)
-            drain_wait(&ms.q2_full[1][(q2_1 - back) & 1], ((q2_1 - back) >> 1) & 1);
-        }
+      if (abort_set(abort_flag)) {
+        // (which of the two is whose does not matter to an upper bound of drains)
+        for (int t = 0; t < 2; ++t)
+          for (uint32_t buf = 0; buf < 2; ++buf) {
+            const uint32_t a = (cur.q2 + 1 - buf) / 2, b = (other.q2 + 1 - buf) / 2;
+            if (a > 0) drain_wait(&ms.q2_full[t][buf], (a - 1) & 1);
+            if (b > 0) drain_wait(&ms.q2_full[t][buf], (b - 1) & 1);
+          }
+      }
     }
     if (abort_set(abort_flag)) {
       // let the copies still in flight land before the CTA exits
@@ -1305,34 +1331,25 @@ __global__ void __launch_bounds__(kModThreads, 1)
     constexpr uint32_t kQFromK = static_cast<uint32_t>((C::kOffKV - C::kOffQ) >> 4);
     constexpr uint32_t kVFromK = static_cast<uint32_t>(((kBM * 128) >> 4) - 1) << 16;
     static_assert((kS & (kS - 1)) == 0, "ring depth must be a power of two");
-    constexpr uint32_t kQ0 = 0u - kQFromK, kQ1 = kQ0 + kTileDesc;
-    constexpr uint32_t kTQ0 = C::kQInTmem ? C::kColQ0 : 0, kTQ1 = C::kQInTmem ? C::kColQ1 : 0;
-    // S_t = Q_t K^T: all keys, or (kHalf) the lower / upper 64
+    constexpr uint32_t kQ0 = 0u - kQFromK;
+    // Query tile 1's TMEM columns all lie kTileCols behind tile 0's and its Q in
+    // shared memory a tile behind, so one copy of the issuing code serves both.
+    constexpr uint32_t kTQ = C::kQInTmem ? kColQ<D> : 0;
+    // S_t = Q_t K^T: all keys, or (half) the lower / upper 64
     auto issue_s = [&](int t, uint32_t b0, int half) {
-      if (t) {
-        if (half == 0)
-          issue_s_steps<D, false, C::kColS1, kQ1, 0, kTQ1>(tmem, desc_k, b0);
-        else if (half == 1)
-          issue_s_steps<D, false, C::kColS1, kQ1, 1, kTQ1>(tmem, desc_k, b0);
-        else
-          issue_s_steps<D, false, C::kColS1, kQ1, 2, kTQ1>(tmem, desc_k, b0);
-      } else {
-        if (half == 0)
-          issue_s_steps<D, false, C::kColS0, kQ0, 0, kTQ0>(tmem, desc_k, b0);
-        else if (half == 1)
-          issue_s_steps<D, false, C::kColS0, kQ0, 1, kTQ0>(tmem, desc_k, b0);
-        else
-          issue_s_steps<D, false, C::kColS0, kQ0, 2, kTQ0>(tmem, desc_k, b0);
-      }
+      const uint32_t base = tmem + t * kTileCols, a0 = desc_k + t * kTileDesc;
+      if (half == 0)
+        issue_s_steps<D, false, kColS, kQ0, 0, kTQ>(base, a0, b0);
+      else if (half == 1)
+        issue_s_steps<D, false, kColS, kQ0, 1, kTQ>(base, a0, b0);
+      else
+        issue_s_steps<D, false, kColS, kQ0, 2, kTQ>(base, a0, b0);
     };
     auto issue_pv = [&](int t, uint32_t b0, uint32_t acc) {
-      if (t)
-        issue_pv_steps<D, false, C::kColO1, C::kColS1, kVFromK>(tmem, b0, acc);
-      else
-        issue_pv_steps<D, false, C::kColO0, C::kColS0, kVFromK>(tmem, b0, acc);
+      issue_pv_steps<D, false, kColO, kColS, kVFromK>(tmem + t * kTileCols, b0, acc);
     };
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-      return warp_all(mbar_wait(bar, phase & 1u, abort_flag, p.err, kErrWaitMma, p.wait_limit_ns));
+      return warp_all(mod_wait(bar, phase & 1u, abort_flag, p.err, kErrWaitMma, p.wait_limit_ns));
     };
     uint32_t tiles = 0;          // key tiles so far: ring items 2 tiles ..
     uint32_t steps0 = 0, steps1 = 0;  // S_0, S_1 issued so far
@@ -1366,20 +1383,15 @@ __global__ void __launch_bounds__(kModThreads, 1)
         if (ok && items > 0) ok = wait(&ms.unit_done, items - 1);
         if (ok) {
           tc_fence_after();
-          const uint32_t q0 = desc_k + kQ0, q1 = desc_k + kQ1;
-          if (b0 > a0) {
-            tmem_cp_128x256b<C::kColQ0 + 0, 0>(tmem, q0);
-            tmem_cp_128x256b<C::kColQ0 + 8, 2>(tmem, q0);
-            tmem_cp_128x256b<C::kColQ0 + 16, 4>(tmem, q0);
-            tmem_cp_128x256b<C::kColQ0 + 24, 6>(tmem, q0);
-            mma_commit(&ms.q_empty[0]);
-          }
-          if (b1 > a1) {
-            tmem_cp_128x256b<C::kColQ1 + 0, 0>(tmem, q1);
-            tmem_cp_128x256b<C::kColQ1 + 8, 2>(tmem, q1);
-            tmem_cp_128x256b<C::kColQ1 + 16, 4>(tmem, q1);
-            tmem_cp_128x256b<C::kColQ1 + 24, 6>(tmem, q1);
-            mma_commit(&ms.q_empty[1]);
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            if (t ? b1 <= a1 : b0 <= a0) continue;
+            const uint32_t base = tmem + t * kTileCols, q = desc_k + kQ0 + t * kTileDesc;
+            tmem_cp_128x256b<kTQ + 0, 0>(base, q);
+            tmem_cp_128x256b<kTQ + 8, 2>(base, q);
+            tmem_cp_128x256b<kTQ + 16, 4>(base, q);
+            tmem_cp_128x256b<kTQ + 24, 6>(base, q);
+            mma_commit(&ms.q_empty[t]);
           }
         }
       }
@@ -1390,7 +1402,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
         if (ok && j > 0) ok = wait(&ms.kv_full[iv % kS], iv / kS);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
           if (!ok) break;
           const int a = t ? a1 : a0, b = t ? b1 : b0;
@@ -1435,83 +1447,71 @@ __global__ void __launch_bounds__(kModThreads, 1)
     // of K and V set the pace here.
     if constexpr (kSplit) {
       uint32_t ring = 2u * tiles;
-      const bool swap = p.G <= kSwapHeads;
-      uint32_t q2[2] = {0, 0}, p2[2] = {0, 0};  // Q taken, P V issued, with keys as rows
-      int ks[2] = {k, k};
-      int left[2] = {0, 0};                    // tiles left of the item
-      uint32_t v_item[2] = {0, 0};             // ring item of the V whose P V is due
-      int due[2] = {0, 0};  // 0: none; bit 0: P V due; 1: accumulate; 2: item's last
-      int done = 0;
-      while (ok && (done != 3 || due[0] || due[1])) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
+      struct Chain {
+        int k, left;      // next item; tiles left of this one
+        int due;          // P V: 0 none; bit 0: due; 1: accumulate; 2: the item's last
+        uint32_t v_item;  // ring item of its V
+        uint32_t q, pv;   // Q taken, P V issued
+        bool over;
+      };
+      Chain cur = {k, 0, 0, 0, kHeads > 0 ? 0 : qs0, kHeads > 0 ? 0 : steps0, false};
+      Chain other = {k, 0, 0, 0, kHeads > 0 ? 0 : qs1, kHeads > 0 ? 0 : steps1, false};
+#pragma unroll 1
+      for (int t = 0; ok && !(cur.over && other.over && !cur.due && !other.due); t ^= 1) {
+        const uint32_t base = tmem + t * kTileCols, q_desc = desc_k + kQ0 + t * kTileDesc;
+        if (cur.due) {
+          const uint32_t iv = cur.v_item;
+          ok = wait(&ms.kv_full[iv % kS], iv / kS) &&
+               wait(kHeads > 0 ? &ms.p2_full[t] : &ms.p_full[t], cur.pv);
           if (!ok) break;
-          if (due[t]) {
-            const uint32_t iv = v_item[t];
-            ok = wait(&ms.kv_full[iv % kS], iv / kS);
-            ok = ok && (swap ? wait(&ms.p2_full[t], p2[t]++)
-                             : wait(&ms.p_full[t], (t ? steps1 : steps0) - 1u));
+          ++cur.pv;
+          tc_fence_after();
+          const uint32_t v_desc = desc_k + (iv % kS) * kTileDesc, acc = (cur.due >> 1) & 1u;
+          if constexpr (kHeads > 0)
+            SwapMma<D>::template o<kColO>(base, v_desc, q_desc + (kSwapP >> 4), acc);
+          else
+            issue_pv(t, v_desc, acc);
+          mma_commit(&ms.kv_empty[iv % kS]);
+          if (cur.due & 4) mma_commit(&ms.o_done[t]);
+          cur.due = 0;
+        }
+        if (!cur.over) {
+          const bool first = cur.left == 0;
+          if (first) {
+            ok = work_wait<kSlots>(ms, p, t, cur.k, abort_flag, kErrWaitMma);
+            if (!ok) break;
+            cur.left = ms.work[t][cur.k % kSlots].n;
+            work_done<kSlots>(ms, t, cur.k++, lane);
+            cur.over = cur.left < 0;
+            if (!cur.over) {
+              ok = kHeads > 0 ? wait(&ms.q2_full[t][cur.q & 1], cur.q >> 1)
+                              : wait(&ms.q_full[t], cur.q);
+              ++cur.q;
+            }
+          }
+          if (!cur.over) {
+            const uint32_t ik = ring, buf = (cur.q - 1u) & 1u;
+            ring += 2u;
+            ok = ok && wait(&ms.kv_full[ik % kS], ik / kS);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t v_desc = desc_k + (iv % kS) * kTileDesc, acc = (due[t] >> 1) & 1u;
-            if (!swap)
-              issue_pv(t, v_desc, acc);
-            else if (t)
-              SwapMma<D>::template o<C::kColO1>(tmem, v_desc, desc_k + kQ1 + (kSwapP >> 4), acc);
+            const uint32_t bk = desc_k + (ik % kS) * kTileDesc;
+            if constexpr (kHeads > 0)
+              SwapMma<D>::template s<kColS>(base, bk, q_desc + buf * (kSwapQ >> 4));
             else
-              SwapMma<D>::template o<C::kColO0>(tmem, v_desc, desc_k + kQ0 + (kSwapP >> 4), acc);
-            mma_commit(&ms.kv_empty[iv % kS]);
-            if (due[t] & 4) mma_commit(&ms.o_done[t]);
-            due[t] = 0;
+              issue_s_steps<D, false, kColS, kQ0, 0, 0>(base, desc_k + t * kTileDesc, bk);
+            mma_commit(&ms.s_full[t]);
+            mma_commit(&ms.kv_empty[ik % kS]);
+            const bool last = cur.left == 1;
+            if (last) mma_commit(kHeads > 0 ? &ms.q2_empty[t][buf] : &ms.q_empty[t]);
+            cur.v_item = ik + 1u;
+            cur.due = 1 | (first ? 0 : 2) | (last ? 4 : 0);
+            --cur.left;
           }
-          if (done >> t & 1) continue;
-          bool first = false;
-          if (left[t] == 0) {
-            ok = work_wait<kSlots>(ms, p, t, ks[t], abort_flag, kErrWaitMma);
-            if (!ok) break;
-            const Work& w = ms.work[t][ks[t] % kSlots];
-            left[t] = w.n;
-            work_done<kSlots>(ms, t, ks[t]++, lane);
-            if (left[t] < 0) {
-              left[t] = 0;
-              done |= 1 << t;
-              continue;
-            }
-            first = true;
-            if (swap) {
-              ok = wait(&ms.q2_full[t][q2[t] & 1], q2[t] >> 1);
-              ++q2[t];
-            } else {
-              ok = wait(&ms.q_full[t], t ? qs1++ : qs0++);
-            }
-          }
-          const uint32_t ik = ring, iv = ring + 1u;
-          ring += 2u;
-          ok = ok && wait(&ms.kv_full[ik % kS], ik / kS);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t bk = desc_k + (ik % kS) * kTileDesc;
-          const uint32_t buf = ((q2[t] - 1u) & 1u) * (kSwapQ >> 4);
-          if (swap && t)
-            SwapMma<D>::template s<C::kColS1>(tmem, bk, desc_k + kQ1 + buf);
-          else if (swap)
-            SwapMma<D>::template s<C::kColS0>(tmem, bk, desc_k + kQ0 + buf);
-          else if (t)
-            issue_s_steps<D, false, C::kColS1, kQ1, 0, 0>(tmem, desc_k, bk);
-          else
-            issue_s_steps<D, false, C::kColS0, kQ0, 0, 0>(tmem, desc_k, bk);
-          mma_commit(&ms.s_full[t]);
-          mma_commit(&ms.kv_empty[ik % kS]);
-          if (t)
-            ++steps1;
-          else
-            ++steps0;
-          const bool last = left[t] == 1;
-          if (last) mma_commit(swap ? &ms.q2_empty[t][(q2[t] - 1u) & 1u] : &ms.q_empty[t]);
-          v_item[t] = iv;
-          due[t] = 1 | (first ? 0 : 2) | (last ? 4 : 0);
-          --left[t];
         }
+        const Chain next = other;
+        other = cur;
+        cur = next;
       }
     }
     // all issued MMAs retire before the CTA releases TMEM
@@ -1569,13 +1569,13 @@ __global__ void __launch_bounds__(kModThreads, 1)
         ring += 2u * w.n;
         // Ask for another item once the one before this is done: one is then
         // always planned ahead, and no more.
-        if (k >= 1 && !warp_all(mbar_wait(&ms.work_empty[0][(k - 1) % kSlots],
+        if (k >= 1 && !warp_all(mod_wait(&ms.work_empty[0][(k - 1) % kSlots],
                                           ((k - 1) / kSlots) & 1, abort_flag, p.err, kErrWaitLoad,
                                           p.wait_limit_ns)))
           break;
         mbar_arrive_expect_tx_elect(&ms.clc_full, 16);
         clc_try_cancel_elect(smem_u32(&ms.clc_resp), &ms.clc_full);
-        if (!warp_all(mbar_wait(&ms.clc_full, k & 1, abort_flag, p.err, kErrWaitLoad,
+        if (!warp_all(mod_wait(&ms.clc_full, k & 1, abort_flag, p.err, kErrWaitLoad,
                                 p.wait_limit_ns))) {
           drain_wait(&ms.clc_full, k & 1);
           break;
@@ -1599,10 +1599,10 @@ __global__ void __launch_bounds__(kModThreads, 1)
   }
 }
 
-template <int D, bool kSplit, bool kCap, bool kBias>
+template <int D, bool kSplit, bool kCap, bool kBias, int kHeads>
 cudaError_t launch_one(const ModKernelParams& p, unsigned grid, cudaStream_t stream) {
   using C = Cfg<D, false>;
-  auto kernel = mod_attn_kernel<D, kSplit, kCap, kBias>;
+  auto kernel = mod_attn_kernel<D, kSplit, kCap, kBias, kHeads>;
   // the shared-memory opt-in is a per-device property of the function
   static std::atomic<bool> attr_done[64];  // zero-initialised: false
   int dev = 0;
@@ -1619,13 +1619,15 @@ cudaError_t launch_one(const ModKernelParams& p, unsigned grid, cudaStream_t str
 }
 
 // The variant is the caller's request alone: what is not asked for is not computed.
-template <int D, bool kSplit>
+// kHeads: 0, or query heads per KV head that a decode's threads hold (4, 8, 16:
+// the smallest that G fits in; above 16 the heads are the rows).
+template <int D, bool kSplit, int kHeads>
 cudaError_t launch_variant(const ModKernelParams& p, unsigned grid, cudaStream_t stream) {
   const bool cap = p.mod.cap_out > 0.f, bias = p.mod.slopes != nullptr;
-  if (cap && bias) return launch_one<D, kSplit, true, true>(p, grid, stream);
-  if (cap) return launch_one<D, kSplit, true, false>(p, grid, stream);
-  if (bias) return launch_one<D, kSplit, false, true>(p, grid, stream);
-  return launch_one<D, kSplit, false, false>(p, grid, stream);
+  if (cap && bias) return launch_one<D, kSplit, true, true, kHeads>(p, grid, stream);
+  if (cap) return launch_one<D, kSplit, true, false, kHeads>(p, grid, stream);
+  if (bias) return launch_one<D, kSplit, false, true, kHeads>(p, grid, stream);
+  return launch_one<D, kSplit, false, false, kHeads>(p, grid, stream);
 }
 
 }  // namespace

@@ -1,0 +1,10 @@
+// mod_attn_kernel, decode, D = 128, at most 16 query heads per KV head.
+#include "mod_sm103a.cuh"
+
+namespace attn {
+
+cudaError_t launch_mod_split_d128_h16(const ModKernelParams& p, unsigned grid, cudaStream_t stream) {
+  return launch_variant<128, true, 16>(p, grid, stream);
+}
+
+}  // namespace attn
