@@ -69,9 +69,15 @@ __device__ __forceinline__ bool mod_wait(uint64_t* bar, uint32_t parity, uint32_
 
 constexpr int kModThreads = 640;  // 16 softmax warps, load, MMA, 2 planning warps
 constexpr int kModWarpLoad = 16, kModWarpMma = 17, kModWarpPlan = 18;
-// setmaxnreg split of the 61440 registers the launch gets (640 threads x 96)
-constexpr uint32_t kModRegSoftmax = 104, kModRegOther = 64;
-static_assert(4 * 128 * kModRegSoftmax + 128 * kModRegOther <= 640 * 96, "register split");
+// setmaxnreg split of the 61440 registers the launch gets (640 threads x 96).  A
+// prefill's other roles fit 32 registers, which leaves its softmax the most; a
+// decode's loaders and planners need more, its scores are few.
+template <bool kSplit>
+constexpr uint32_t kModRegSoftmax = kSplit ? 104 : 112;
+template <bool kSplit>
+constexpr uint32_t kModRegOther = kSplit ? 64 : 32;
+static_assert(4 * 128 * kModRegSoftmax<true> + 128 * kModRegOther<true> <= 640 * 96, "registers");
+static_assert(4 * 128 * kModRegSoftmax<false> + 128 * kModRegOther<false> <= 640 * 96, "registers");
 
 // One work item, written by a planning warp, once for each query tile (a decode's
 // own-key items: for the one that has it).  Key tiles are relative to tile0.
@@ -884,7 +890,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
     // rows, threads i and i + 16 the two 64-key halves of row i (the layout of
     // fwd_sm103a.cu).
     // =====================================================================
-    reg_alloc<kModRegSoftmax>();
+    reg_alloc<kModRegSoftmax<kSplit>>();
     const int t = warp >> 3;
     const int lbase = (warp & 3) * 32 + ((warp >> 2) & 1) * 16;  // first TMEM lane of the warp
     const int r = lbase + (lane & 15);                           // row within the tile
@@ -1151,7 +1157,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
     // TMA loader and planner.  Ring items run on across work items: the item's
     // tile j is ring items 2 (j + tiles before), + 1 (K, then V).
     // =====================================================================
-    reg_dealloc<kModRegOther>();
+    reg_dealloc<kModRegOther<kSplit>>();
     uint32_t g = 0;              // next ring item
     uint32_t q0_loads = 0, q1_loads = 0;  // loads of Q_0, Q_1 issued
     bool ok = true;
@@ -1325,7 +1331,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
     // MMA issuer (warp-wide, one elected thread per instruction).  Step j of an
     // item issues, per query tile, O_t += P_t V_{j-1} and S_t = Q_t K_j^T.
     // =====================================================================
-    reg_dealloc<kModRegOther>();
+    reg_dealloc<kModRegOther<kSplit>>();
     constexpr uint32_t kTileDesc = C::kTileBytes >> 4;
     const uint32_t desc_k = sdesc_sw128_lo(smem_u32(smem + C::kOffKV), 16);
     constexpr uint32_t kQFromK = static_cast<uint32_t>((C::kOffKV - C::kOffQ) >> 4);
@@ -1521,7 +1527,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
     // =====================================================================
     // planning warps
     // =====================================================================
-    reg_dealloc<kModRegOther>();
+    reg_dealloc<kModRegOther<kSplit>>();
     Work w;
     bool ok = true;
     uint32_t ring = 0;  // ring items so far
