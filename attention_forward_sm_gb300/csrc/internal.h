@@ -108,6 +108,7 @@ struct ModKernelParams {
   int B, Hq, Hkv, G, Nq, Nk;  // Nk: keys (prefill) or the caches' capacity (decode)
   int causal, q_offset;
   int longest_first, group_heads;  // prefill: order of the work items
+  int o_sectors;                   // prefill: o is 32-byte aligned
   int Np, prefix_tiles;            // shared prefix: keys, key tiles
   int row_blocks, per_tile;        // its items per KV head; requests per query tile
   int pre_rows;                    // rows of a prefix item's partial states

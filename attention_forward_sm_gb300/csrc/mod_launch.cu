@@ -217,6 +217,7 @@ int mod_fwd(const ModFwdParams& p, cudaStream_t stream) {
   const double kv_bytes = 4.0 * p.Nk * p.D;
   const int kv_heads = std::max(1, std::min(static_cast<int>(40.0e6 / kv_bytes), p.B * p.Hkv));
   k.group_heads = kv_heads * k.G;
+  k.o_sectors = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
   common_params(&k, p.mod);
   const unsigned grid =
       static_cast<unsigned>((p.Nq + 255ll) / 256 * p.B * p.Hq);

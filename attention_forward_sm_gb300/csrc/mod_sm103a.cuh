@@ -120,6 +120,7 @@ struct ModMisc {
   uint64_t work_full[2][4], work_empty[2][4];
   uint4 clc_resp;
   Work work[2][4];        // query tile t's item k in slot k % kWorkSlots
+  int2 ranges[2][2 * kBM];  // prefill: keys [x, y) that the rows of item k % 2 see
   float red[2][4][16];      // keys as rows: per warp and head, a maximum or a sum
   float own_slopes[2][16];  // times log2(e)
   int4 seen[16];  // per softmax warp: keys [x, y) that all its rows see, [z, w) that any does
@@ -194,7 +195,8 @@ constexpr float kLoose = 100.f;
 template <bool kCap, bool kBias>
 struct Scores {
   bool fused;
-  int tier;        // capped, fused: which polynomial
+  int tier;          // capped, fused: which polynomial; 3: the longest, some keys unseen
+  Seen seen;         // (of them)
   float slope, rel;  // biased, fused: key kb + i has bias slope * (rel + i)
 
   // kb: key of s[0], kt: of the tile.  masked: some row of the warp does not see
@@ -203,7 +205,6 @@ struct Scores {
   __device__ __forceinline__ float prepare(float (&s)[64], const ModKernelParams& p,
                                            const RowInfo& info, float row_slope, int kt, int kb,
                                            bool masked) {
-    Seen seen;
     RowInfo row;
     if (masked || kBias) row = info;
     if (masked) seen = seen_columns(row.lo - kb, row.hi - kb);
@@ -211,7 +212,6 @@ struct Scores {
     bool poly = false;  // capped: the longest polynomial holds
     fused = true;
     if constexpr (kCap) {
-      fused = !masked;
       if (masked) mask_to(s, seen, 0.f);  // what lies at unseen keys has no say
       float a0 = 0.f, a1 = 0.f;
 #pragma unroll
@@ -226,7 +226,11 @@ struct Scores {
       a0 = fmaxf(a0, __shfl_xor_sync(0xFFFFFFFFu, a0, 16));  // the row's other half
       poly = all <= p.mod.cap_limit[2];
       tier = all <= p.mod.cap_limit[0] ? 0 : (all <= p.mod.cap_limit[1] ? 1 : 2);
-      fused = fused && (tier < 2 || poly);
+      fused = tier < 2 || poly;
+      if (masked) {
+        fused = poly;
+        tier = 3;
+      }
       top = fminf(a0 * p.scale_log2, p.mod.cap_out);  // |tanh x| <= |x|, 1
     }
     bool linear = true;
@@ -249,7 +253,8 @@ struct Scores {
       fused = fused && linear &&
               __all_sync(0xFFFFFFFFu, 2.f * top + fabsf(slope) * (kBN - 1) <= kLoose);
       if constexpr (kCap) {
-        if (fused) return top + most;
+        // (a row that sees none of the tile's keys: neither is there a nearest)
+        if (fused) return from <= to ? top + most : -CUDART_INF_F;
       } else if (fused) {
         if (masked) mask_to(s, seen, -CUDART_INF_F);
         const float mx = row_max(s);
@@ -317,8 +322,9 @@ struct Scores {
   __device__ __forceinline__ float weights(const float (&s)[64], const ModKernelParams& p,
                                            float neg_m, uint32_t (&pk)[32]) const {
     uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
-    // pass(f): f(pair of s, what to add to its scores) -> exponents
-    auto pass = [&](bool with_bias, auto f) {
+    // pass(f): f(pair of s, what to add to its scores) -> exponents; with_mask:
+    // unseen keys get -inf for theirs
+    auto pass = [&](bool with_bias, bool with_mask, auto f) {
       uint64_t add = f32x2(neg_m, neg_m);
       const uint64_t next = f32x2(2.f * slope, 2.f * slope);
 #pragma unroll
@@ -335,6 +341,13 @@ struct Scores {
         float x0, x1, x2, x3;
         unpack_f32x2(f(f32x2(s[e], s[e + 1]), a01), x0, x1);
         unpack_f32x2(f(f32x2(s[e + 2], s[e + 3]), a23), x2, x3);
+        if (with_mask) {
+          const uint32_t w = seen.words[e / 32];
+          x0 = (w >> (e % 32)) & 1u ? x0 : -CUDART_INF_F;
+          x1 = (w >> (e % 32 + 1)) & 1u ? x1 : -CUDART_INF_F;
+          x2 = (w >> (e % 32 + 2)) & 1u ? x2 : -CUDART_INF_F;
+          x3 = (w >> (e % 32 + 3)) & 1u ? x3 : -CUDART_INF_F;
+        }
         const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
         const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
         acc0 = add_f32x2(acc0, f32x2(p0, p1));
@@ -344,17 +357,19 @@ struct Scores {
       }
     };
     if ((kCap || kBias) && !fused) {
-      pass(false, [](uint64_t x, uint64_t add) { return add_f32x2(x, add); });
+      pass(false, false, [](uint64_t x, uint64_t add) { return add_f32x2(x, add); });
     } else if constexpr (kCap) {
       if (tier == 0)
-        pass(kBias, CapPoly<kCapN0>(p.mod.cap_coef[0]));
+        pass(kBias, false, CapPoly<kCapN0>(p.mod.cap_coef[0]));
       else if (tier == 1)
-        pass(kBias, CapPoly<kCapN1>(p.mod.cap_coef[1]));
+        pass(kBias, false, CapPoly<kCapN1>(p.mod.cap_coef[1]));
+      else if (tier == 2)
+        pass(kBias, false, CapPoly<kCapN2>(p.mod.cap_coef[2]));
       else
-        pass(kBias, CapPoly<kCapN2>(p.mod.cap_coef[2]));
+        pass(kBias, true, CapPoly<kCapN2>(p.mod.cap_coef[2]));
     } else {
       const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
-      pass(kBias, [&](uint64_t x, uint64_t add) { return fma_f32x2(x, scale2, add); });
+      pass(kBias, false, [&](uint64_t x, uint64_t add) { return fma_f32x2(x, scale2, add); });
     }
     float u0, u1;
     unpack_f32x2(add_f32x2(acc0, acc1), u0, u1);
@@ -409,8 +424,9 @@ __device__ __forceinline__ bool item_row(const ModKernelParams& p, const Work& w
   }
 }
 
-// Prefill item u (warp-wide): the query rows, and the key tiles they see.
-__device__ __forceinline__ Work plan_unit(const ModKernelParams& p, int u, int lane) {
+// Prefill item u (warp-wide): the query rows, and the key tiles they see; with
+// ranges also every row's, in rows[].
+__device__ __forceinline__ Work plan_unit(const ModKernelParams& p, int u, int2* rows, int lane) {
   const int nqb = (p.Nq + 2 * kBM - 1) / (2 * kBM);
   int qblk, bh;
   if (p.longest_first) {  // as decode_unit of fwd_sm103a.cu
@@ -431,33 +447,46 @@ __device__ __forceinline__ Work plan_unit(const ModKernelParams& p, int u, int l
   w.kind = 1;
   w.slot = 0;
   int lo[2], hi[2];
+  if (p.ranges) {
+    // row lane + 32 i of the item; all loads before the first use
+    constexpr int kRows = 2 * kBM / 32;
+    const int2* rg = reinterpret_cast<const int2*>(p.ranges) + static_cast<size_t>(bh / p.Hq) * p.Nq;
+    int2 r[kRows];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = w.q0 + t * kBM;
-    lo[t] = INT_MAX;
-    hi[t] = 0;
-    if (p.ranges) {
-      const int2* rg = reinterpret_cast<const int2*>(p.ranges) +
-                       static_cast<size_t>(bh / p.Hq) * p.Nq;
+    for (int i = 0; i < kRows; ++i) {
+      const int row = w.q0 + i * 32 + lane;
+      r[i] = row < p.Nq ? rg[row] : make_int2(0, 0);
+    }
+    lo[0] = lo[1] = INT_MAX;
+    hi[0] = hi[1] = 0;
 #pragma unroll
-      for (int i = 0; i < kBM / 32; ++i) {
-        const int row = first + i * 32 + lane;
-        if (row < p.Nq) {
-          const int2 r = rg[row];
-          const int l = max(r.x, 0);
-          int h = min(r.y, p.Nk);
-          if (p.causal) h = min(h, p.q_offset + row + 1);
-          if (l < h) {
-            lo[t] = min(lo[t], l);
-            hi[t] = max(hi[t], h);
-          }
-        }
+    for (int i = 0; i < kRows; ++i) {
+      r[i].x = max(r[i].x, 0);
+      r[i].y = min(r[i].y, p.Nk);
+      if (p.causal) r[i].y = min(r[i].y, p.q_offset + w.q0 + i * 32 + lane + 1);
+      if (r[i].x < r[i].y) {
+        lo[i / (kRows / 2)] = min(lo[i / (kRows / 2)], r[i].x);
+        hi[i / (kRows / 2)] = max(hi[i / (kRows / 2)], r[i].y);
+      } else {
+        r[i] = make_int2(0, 0);
       }
+      rows[i * 32 + lane] = r[i];
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
       lo[t] = __reduce_min_sync(0xFFFFFFFFu, lo[t]);
       hi[t] = __reduce_max_sync(0xFFFFFFFFu, hi[t]);
-    } else if (first < p.Nq) {
-      lo[t] = 0;
-      hi[t] = p.causal ? min(p.Nk, p.q_offset + min(first + kBM, p.Nq)) : p.Nk;
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int first = w.q0 + t * kBM;
+      lo[t] = INT_MAX;
+      hi[t] = 0;
+      if (first < p.Nq) {
+        lo[t] = 0;
+        hi[t] = p.causal ? min(p.Nk, p.q_offset + min(first + kBM, p.Nq)) : p.Nk;
+      }
     }
   }
   w.lo = min(lo[0], lo[1]);
@@ -943,13 +972,12 @@ __global__ void __launch_bounds__(kModThreads, 1)
             row.lo = 0;
             row.hi = p.Nk;
             if (p.ranges) {
-              const int2 rg = reinterpret_cast<const int2*>(
-                  p.ranges)[static_cast<size_t>(w.id / p.Hq) * p.Nq + i];
-              row.lo = max(rg.x, 0);
-              row.hi = min(rg.y, p.Nk);
+              const int2 rg = ms.ranges[k & 1][t * kBM + r];
+              row.lo = rg.x;
+              row.hi = rg.y;
+            } else if (p.causal) {
+              row.hi = min(row.hi, row.pos + 1);
             }
-            if (p.causal) row.hi = min(row.hi, row.pos + 1);
-            if (row.lo >= row.hi) row.lo = row.hi = 0;
             if constexpr (kBias) {
               slope = p.mod.slopes[head] * kLog2e;
               if (row.lo < row.hi) row.ref = bias_ref(slope, row.pos, row.lo, row.hi);
@@ -1003,7 +1031,6 @@ __global__ void __launch_bounds__(kModThreads, 1)
             const int key = kt + ((i >> 3) & (kBN - 1));
             if (key < w.lo || key >= w.hi) v[i] = make_uint4(0, 0, 0, 0);
           }
-          fence_proxy_async_smem();
         }
         if (dead) {
           if (live) {
@@ -1014,6 +1041,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
             tmem_st_pair32<32>(s_addr, pk);
             tmem_st_wait();
           }
+          if (edge) fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -1065,6 +1093,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
           tmem_st_wait();
         }
         tmem_st_pair32<32>(s_addr, pk);
+        if (edge) fence_proxy_async_smem();
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -1111,8 +1140,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
             }
           }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out * D +
-                                                c * (D / 2)) + kk * 4;
+          __nv_bfloat16* dst =
+              static_cast<__nv_bfloat16*>(p.o) + out * D + c * (D / 2) + kk * 32;
           uint32_t o2[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -1120,10 +1149,15 @@ __global__ void __launch_bounds__(kModThreads, 1)
                          : pack_bf16x2(__uint_as_float(v[2 * i]) * inv,
                                        __uint_as_float(v[2 * i + 1]) * inv);
           if (valid) {
+            if (p.o_sectors) {
+              st_global_v8(dst, o2);
+              st_global_v8(dst + 16, o2 + 8);
+            } else {
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              st_global_v4_evict_first(dst + g, o2[4 * g], o2[4 * g + 1], o2[4 * g + 2],
-                                       o2[4 * g + 3]);
+              for (int g = 0; g < 4; ++g)
+                reinterpret_cast<uint4*>(dst)[g] =
+                    make_uint4(o2[4 * g], o2[4 * g + 1], o2[4 * g + 2], o2[4 * g + 3]);
+            }
           }
         }
       }
@@ -1565,7 +1599,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
         if (lane == 0) p.plan[p.B] = before;
       }
     } else if (warp == kModWarpPlan) {
-      w = plan_unit(p, static_cast<int>(blockIdx.x), lane);
+      w = plan_unit(p, static_cast<int>(blockIdx.x), ms.ranges[0], lane);
       for (;; ++k) {
         w.v_first = ring + 1u;
         w.v_last = ring + 2u * w.n - 1u;
@@ -1575,10 +1609,12 @@ __global__ void __launch_bounds__(kModThreads, 1)
         ring += 2u * w.n;
         // Ask for another item once the one before this is done: one is then
         // always planned ahead, and no more.
-        if (k >= 1 && !warp_all(mod_wait(&ms.work_empty[0][(k - 1) % kSlots],
-                                          ((k - 1) / kSlots) & 1, abort_flag, p.err, kErrWaitLoad,
-                                          p.wait_limit_ns)))
-          break;
+        if (k >= 1)
+          for (int t = 0; t < 2; ++t)
+            ok = ok && warp_all(mod_wait(&ms.work_empty[t][(k - 1) % kSlots],
+                                         ((k - 1) / kSlots) & 1, abort_flag, p.err, kErrWaitLoad,
+                                         p.wait_limit_ns));
+        if (!ok) break;
         mbar_arrive_expect_tx_elect(&ms.clc_full, 16);
         clc_try_cancel_elect(smem_u32(&ms.clc_resp), &ms.clc_full);
         if (!warp_all(mod_wait(&ms.clc_full, k & 1, abort_flag, p.err, kErrWaitLoad,
@@ -1592,7 +1628,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
         if (nu < 0)
           w.n = -1;
         else
-          w = plan_unit(p, nu, lane);
+          w = plan_unit(p, nu, ms.ranges[(k + 1) & 1], lane);
       }
     }
   }
