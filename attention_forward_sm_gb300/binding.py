@@ -402,13 +402,9 @@ def _import_torch():
     return _torch
 
 
-def _bf16(x, dev: int) -> bool:
-    return x.dtype is _torch.bfloat16 and x.is_cuda and x.get_device() == dev and x.is_contiguous()
-
-
-def _aux_ok(x, dtype, shape, dev: int) -> bool:
-    return x is None or (isinstance(x, _torch.Tensor) and x.dtype is dtype and x.shape == shape
-                         and x.is_cuda and x.get_device() == dev and x.is_contiguous())
+def _aux_bad(x, dtype, shape, dev: int) -> bool:
+    return not (isinstance(x, _torch.Tensor) and x.dtype is dtype and x.shape == shape
+                and x.get_device() == dev and x.is_contiguous())
 
 
 def _check_aux(dev, **tensors):
@@ -436,44 +432,38 @@ def _current_raw_stream(dev: int) -> int:
     return _torch.cuda.current_stream(dev).cuda_stream
 
 
-def _launch(fn, args, dev: int, stream, used):
+def _side_launch(fn, args, dev: int, stream, used):
     """Calls the library's ``fn`` with ``dev`` current, on ``stream`` (None: the
     device's current one).  On another stream than the current one the tensors
     of ``used`` are marked as used there, so that the caching allocator does not
     hand their memory out again while the kernels run."""
-    if _torch.cuda.current_device() != dev:
-        with _torch.cuda.device(dev):
-            return _launch(fn, args, dev, stream, used)
-    cur = _raw_stream(dev)
-    if stream is None:
-        s = cur
-    elif isinstance(stream, int):
-        s = stream
-    else:
-        if stream.device.index != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
-        s = stream.cuda_stream
-    rc = fn(*args, s)
-    if rc:
-        _check(rc)
-    if s != cur:
-        side = stream
-        if isinstance(stream, int):
-            side = _torch.cuda.ExternalStream(s, device=dev) if s else \
-                _torch.cuda.default_stream(dev)
-        for x in used:
-            if x is not None:
-                x.record_stream(side)
+    with _torch.cuda.device(dev):
+        cur = _raw_stream(dev)
+        if stream is None:
+            s = cur
+        elif isinstance(stream, int):
+            s = stream
+        else:
+            if stream.device.index != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+            s = stream.cuda_stream
+        rc = fn(*args, s)
+        if rc:
+            _check(rc)
+        if s != cur:
+            side = stream
+            if isinstance(stream, int):
+                side = _torch.cuda.ExternalStream(s, device=dev) if s else \
+                    _torch.cuda.default_stream(dev)
+            for x in used:
+                if x is not None:
+                    x.record_stream(side)
 
 
 def _raw_stream(dev: int) -> int:
     global _raw_stream
     _raw_stream = getattr(_import_torch()._C, "_cuda_getCurrentRawStream", _current_raw_stream)
     return _raw_stream(dev)
-
-
-def _addr(x):
-    return None if x is None else x.data_ptr()
 
 
 def forward_mod(q, k, v, *, causal: bool = False, scale: float | None = None,
@@ -486,24 +476,38 @@ def forward_mod(q, k, v, *, causal: bool = False, scale: float | None = None,
     these those at or before its position.  Rows that see nothing give 0 and
     -inf."""
     torch = _torch or _import_torch()
-    _check_ranks({"q": q, "k": k, "v": v}, {"q": 4, "k": 4, "v": 4})
-    B, Hq, Nq, D = q.shape
-    _, Hkv, Nk, _ = k.shape
-    dev = q.get_device()
-    if not (k.shape == (B, Hkv, Nk, D) and v.shape == k.shape and _bf16(q, dev) and _bf16(k, dev)
-            and _bf16(v, dev) and _aux_ok(slopes, torch.float32, (Hq,), dev)
-            and _aux_ok(ranges, torch.int32, (B, Nq, 2), dev)):
+    try:
+        B, Hq, Nq, D = q.shape
+        Bk, Hkv, Nk, Dk = k.shape
+        dev, bf16 = q.get_device(), torch.bfloat16
+        fine = (v.shape == k.shape and Bk == B and Dk == D and dev >= 0
+                and q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16
+                and k.get_device() == dev and v.get_device() == dev
+                and q.is_contiguous() and k.is_contiguous() and v.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine or slopes is not None and _aux_bad(slopes, torch.float32, (Hq,), dev) \
+            or ranges is not None and _aux_bad(ranges, torch.int32, (B, Nq, 2), dev):
+        _check_ranks({"q": q, "k": k, "v": v}, {"q": 4, "k": 4, "v": 4})
         _check_inputs({"q": q, "k": k, "v": v},
-                      {"B": (B, k.shape[0], v.shape[0]), "D": (D, k.shape[3], v.shape[3]),
-                       "Hkv": (Hkv, v.shape[1]), "Nk": (Nk, v.shape[2])})
+                      {"B": (q.shape[0], k.shape[0], v.shape[0]),
+                       "D": (q.shape[3], k.shape[3], v.shape[3]),
+                       "Hkv": (k.shape[1], v.shape[1]), "Nk": (k.shape[2], v.shape[2])})
         _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)),
                    ranges=(ranges, torch.int32, (B, Nq, 2)))
     o = torch.empty_like(q)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-    _launch(load().attn_fwd_mod,
-            (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
-             Nq, Nk, D, bool(causal), q_offset, D ** -0.5 if scale is None else scale, softcap,
-             _addr(slopes), _addr(ranges)), dev, stream, (q, k, v, slopes, ranges, o, lse))
+    fn = (_lib or load()).attn_fwd_mod
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
+            Nq, Nk, D, bool(causal), q_offset, D ** -0.5 if scale is None else scale, softcap,
+            None if slopes is None else slopes.data_ptr(),
+            None if ranges is None else ranges.data_ptr())
+    if stream is None and torch.cuda.current_device() == dev:
+        rc = fn(*args, _raw_stream(dev))
+        if rc:
+            _check(rc)
+    else:
+        _side_launch(fn, args, dev, stream, (q, k, v, slopes, ranges, o, lse))
     return o, lse
 
 
@@ -517,31 +521,71 @@ def row_ranges(doc_lens, N: int, *, prefix_lens=None, causal: bool = True, strea
     _check_ranks({"doc_lens": doc_lens}, {"doc_lens": 2})
     B, M = doc_lens.shape
     dev = doc_lens.get_device()
-    if not (_aux_ok(doc_lens, torch.int32, (B, M), dev)
-            and _aux_ok(prefix_lens, torch.int32, (B, M), dev)):
+    if dev < 0 or _aux_bad(doc_lens, torch.int32, (B, M), dev) \
+            or prefix_lens is not None and _aux_bad(prefix_lens, torch.int32, (B, M), dev):
         _check_aux(doc_lens.device, doc_lens=(doc_lens, torch.int32, (B, M)),
                    prefix_lens=(prefix_lens, torch.int32, (B, M)))
     out = torch.empty((B, N, 2), dtype=torch.int32, device=doc_lens.device)
-    _launch(load().attn_row_ranges,
-            (doc_lens.data_ptr(), _addr(prefix_lens), out.data_ptr(), B, N, M, bool(causal)), dev,
-            stream, (doc_lens, prefix_lens, out))
+    fn = (_lib or load()).attn_row_ranges
+    args = (doc_lens.data_ptr(), None if prefix_lens is None else prefix_lens.data_ptr(),
+            out.data_ptr(), B, N, M, bool(causal))
+    if stream is None and torch.cuda.current_device() == dev:
+        rc = fn(*args, _raw_stream(dev))
+        if rc:
+            _check(rc)
+    else:
+        _side_launch(fn, args, dev, stream, (doc_lens, prefix_lens, out))
     return out
 
 
-def _decode_args(q, kcache, vcache, lens, slopes):
-    """Checks what the two decode calls share; (B, Hq, Hkv, Ncap, D, device)."""
-    torch = _torch or _import_torch()
-    _check_ranks({"q": q, "kcache": kcache, "vcache": vcache}, {"q": 3, "kcache": 4, "vcache": 4})
-    B, Hq, D = q.shape
-    _, Hkv, Ncap, _ = kcache.shape
-    dev = q.get_device()
-    if not (kcache.shape == (B, Hkv, Ncap, D) and vcache.shape == kcache.shape and _bf16(q, dev)
-            and _bf16(kcache, dev) and _bf16(vcache, dev)
-            and _aux_ok(slopes, torch.float32, (Hq,), dev)
-            and _aux_ok(lens, torch.int32, (B,), dev)):
+def _decode(fn, q, pre, kcache, vcache, lens, scale, softcap, slopes, stream):
+    """What the two decode calls share; pre: () or (kprefix, vprefix)."""
+    torch = _torch
+    try:
+        B, Hq, D = q.shape
+        Bk, Hkv, Ncap, Dk = kcache.shape
+        dev, bf16 = q.get_device(), torch.bfloat16
+        fine = (vcache.shape == kcache.shape and Bk == B and Dk == D and dev >= 0
+                and q.dtype is bf16 and kcache.dtype is bf16 and vcache.dtype is bf16
+                and kcache.get_device() == dev and vcache.get_device() == dev
+                and q.is_contiguous() and kcache.is_contiguous() and vcache.is_contiguous())
+        if pre:
+            kprefix, vprefix = pre
+            Hp, Np, Dp = kprefix.shape
+            fine = (fine and vprefix.shape == kprefix.shape and Hp == Hkv and Dp == D
+                    and kprefix.dtype is bf16 and vprefix.dtype is bf16
+                    and kprefix.get_device() == dev and vprefix.get_device() == dev
+                    and kprefix.is_contiguous() and vprefix.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine or lens is not None and _aux_bad(lens, torch.int32, (B,), dev) \
+            or slopes is not None and _aux_bad(slopes, torch.float32, (Hq,), dev):
+        if pre:
+            _check_ranks({"kprefix": pre[0], "vprefix": pre[1]}, {"kprefix": 3, "vprefix": 3})
         _check_decode_inputs(q, kcache, vcache)
+        if pre:
+            _check_inputs({"q": q, "kprefix": pre[0], "vprefix": pre[1]},
+                          {"Hkv": (Hkv, pre[0].shape[0], pre[1].shape[0]),
+                           "Np": (pre[0].shape[1], pre[1].shape[1]),
+                           "D": (D, pre[0].shape[2], pre[1].shape[2])})
         _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)), lens=(lens, torch.int32, (B,)))
-    return B, Hq, Hkv, Ncap, D, dev
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    tail = (None if lens is None else lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv)
+    score = (Ncap, D, D ** -0.5 if scale is None else scale, softcap,
+             None if slopes is None else slopes.data_ptr())
+    if pre:
+        args = (q.data_ptr(), kprefix.data_ptr(), vprefix.data_ptr(), kcache.data_ptr(),
+                vcache.data_ptr(), *tail, Np, *score)
+    else:
+        args = (q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), *tail, *score)
+    if stream is None and torch.cuda.current_device() == dev:
+        rc = fn(*args, _raw_stream(dev))
+        if rc:
+            _check(rc)
+    else:
+        _side_launch(fn, args, dev, stream, (q, *pre, kcache, vcache, lens, slopes, o, lse))
+    return o, lse
 
 
 def decode_varlen(q, kcache, vcache, lens=None, *, scale: float | None = None,
@@ -550,14 +594,9 @@ def decode_varlen(q, kcache, vcache, lens=None, *, scale: float | None = None,
     ``lens[b]`` keys of request b (``lens`` [B] int32, CUDA; None: all), with
     the score modifications of ``forward_mod``; the query is at position
     ``lens[b] - 1``."""
-    B, Hq, Hkv, Ncap, D, dev = _decode_args(q, kcache, vcache, lens, slopes)
-    o = _torch.empty_like(q)
-    lse = _torch.empty((B, Hq), dtype=_torch.float32, device=q.device)
-    _launch(load().attn_decode_varlen,
-            (q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), _addr(lens), o.data_ptr(),
-             lse.data_ptr(), B, Hq, Hkv, Ncap, D, D ** -0.5 if scale is None else scale, softcap,
-             _addr(slopes)), dev, stream, (q, kcache, vcache, lens, slopes, o, lse))
-    return o, lse
+    _torch or _import_torch()
+    return _decode((_lib or load()).attn_decode_varlen, q, (), kcache, vcache, lens, scale, softcap,
+                   slopes, stream)
 
 
 def decode_prefix(q, kprefix, vprefix, kcache, vcache, lens=None, *, scale: float | None = None,
@@ -566,19 +605,6 @@ def decode_prefix(q, kprefix, vprefix, kcache, vcache, lens=None, *, scale: floa
     ``vprefix`` [Hkv,Np,D] are seen by every request before its own
     ``lens[b]`` cache keys, and read once for the whole batch; the query is at
     position ``Np + lens[b] - 1``."""
-    _check_ranks({"kprefix": kprefix, "vprefix": vprefix}, {"kprefix": 3, "vprefix": 3})
-    B, Hq, Hkv, Ncap, D, dev = _decode_args(q, kcache, vcache, lens, slopes)
-    Np = kprefix.shape[1]
-    if not (kprefix.shape == (Hkv, Np, D) and vprefix.shape == kprefix.shape
-            and _bf16(kprefix, dev) and _bf16(vprefix, dev)):
-        _check_inputs({"q": q, "kprefix": kprefix, "vprefix": vprefix},
-                      {"Hkv": (Hkv, kprefix.shape[0], vprefix.shape[0]),
-                       "Np": (Np, vprefix.shape[1]), "D": (D, kprefix.shape[2], vprefix.shape[2])})
-    o = _torch.empty_like(q)
-    lse = _torch.empty((B, Hq), dtype=_torch.float32, device=q.device)
-    _launch(load().attn_decode_prefix,
-            (q.data_ptr(), kprefix.data_ptr(), vprefix.data_ptr(), kcache.data_ptr(),
-             vcache.data_ptr(), _addr(lens), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Np, Ncap, D,
-             D ** -0.5 if scale is None else scale, softcap, _addr(slopes)), dev, stream,
-            (q, kprefix, vprefix, kcache, vcache, lens, slopes, o, lse))
-    return o, lse
+    _torch or _import_torch()
+    return _decode((_lib or load()).attn_decode_prefix, q, (kprefix, vprefix), kcache, vcache, lens,
+                   scale, softcap, slopes, stream)

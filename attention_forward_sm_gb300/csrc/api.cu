@@ -28,6 +28,7 @@ struct DeviceState {
   std::once_flag once;
   bool is_sm103 = false;
   unsigned int* err_word = nullptr;
+  int sms = 0;
   cudaError_t init_error = cudaSuccess;
 };
 DeviceState g_dev[kMaxDevices];
@@ -50,6 +51,8 @@ int device_state(DeviceState** out) {
     if (st.init_error == cudaSuccess)
       st.init_error = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     st.is_sm103 = (major == 10 && minor == 3);
+    if (st.init_error == cudaSuccess)
+      st.init_error = cudaDeviceGetAttribute(&st.sms, cudaDevAttrMultiProcessorCount, dev);
     if (st.init_error == cudaSuccess && st.is_sm103)
       st.init_error = cudaGetSymbolAddress(reinterpret_cast<void**>(&st.err_word), g_error_word);
   });
@@ -154,6 +157,15 @@ int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, in
 int check_device() {
   DeviceState* st = nullptr;
   return device_state(&st);
+}
+
+int device_info(DeviceInfo* out) {
+  DeviceState* st = nullptr;
+  if (int rc = device_state(&st)) return rc;
+  out->dev = static_cast<int>(st - g_dev);
+  out->sms = st->sms;
+  out->err_word = st->err_word;
+  return ATTN_OK;
 }
 
 unsigned int* device_error_word() {

@@ -8,9 +8,10 @@
 // Nk65536 step), about 2 % of a bandwidth-bound step.
 //
 // Ordering.  A buffer belongs to one stream at a time.  Each use records the
-// entry's event after the launches and the next use waits on it, so a buffer
-// is never used by two calls at once, even when a destroyed stream's handle
-// comes back for a new stream while the old one still has work queued.  A
+// entry's event after the launches, and the first use on another stream waits on
+// it, so a buffer is never used by two calls at once.  Streams are told apart
+// by their ids: a destroyed stream's handle may come back for a new stream while
+// the old one still has work queued, its id does not.  A
 // buffer that grows, or whose entry is taken over by another stream, is freed
 // stream-ordered after that event.  Calls during stream capture take the
 // plain stream-ordered allocation path, so a captured graph owns its scratch.
@@ -28,7 +29,7 @@ constexpr int kMaxDevices = 64;
 constexpr int kEntries = 8;  // streams remembered per device
 
 struct Entry {
-  cudaStream_t stream = nullptr;
+  unsigned long long stream = 0;  // its id: unlike a handle, never given out again
   void* ptr = nullptr;
   size_t bytes = 0;
   cudaEvent_t done = nullptr;  // recorded after the entry's last use
@@ -57,7 +58,7 @@ int plain_path(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cu
 
 }  // namespace
 
-int with_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
+int with_scratch(size_t bytes, int dev, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
                  void* ctx) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
@@ -66,16 +67,20 @@ int with_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, 
   }
   if (cap != cudaStreamCaptureStatusNone) return plain_path(bytes, stream, launch, ctx);
 
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_DEVICE;
   Cache& c = g_cache[dev];
   // held until the launches and the event record are queued, so that no
   // other host thread frees or regrows this buffer in between
   std::lock_guard<std::mutex> lock(c.mu);
   Entry* en = nullptr;
+  unsigned long long id = 0;
+  if (cudaStreamGetId(stream, &id) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_CUDA;
+  }
   for (Entry& x : c.e)
-    if (x.live && x.stream == stream) en = &x;
+    if (x.live && x.stream == id) en = &x;
+  const bool same = en != nullptr;  // the buffer's previous use is in front of us on our stream
   if (!en) {
     // a free entry, else the least recently used one
     for (Entry& x : c.e)
@@ -89,14 +94,14 @@ int with_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, 
         if (x.last_use < en->last_use) en = &x;
     }
     en->live = true;
-    en->stream = stream;
+    en->stream = id;
     if (!en->done && cudaEventCreateWithFlags(&en->done, cudaEventDisableTiming) != cudaSuccess) {
       en->live = false;
       return ATTN_ERR_CUDA;
     }
   }
-  // after the entry's previous use, whichever stream made it
-  if (cudaStreamWaitEvent(stream, en->done, 0) != cudaSuccess) return ATTN_ERR_CUDA;
+  // after the entry's previous use, if another stream made it
+  if (!same && cudaStreamWaitEvent(stream, en->done, 0) != cudaSuccess) return ATTN_ERR_CUDA;
   if (en->bytes < bytes) {
     if (en->ptr && cudaFreeAsync(en->ptr, stream) != cudaSuccess) {
       en->live = false;
@@ -126,8 +131,10 @@ int decode_with_cached_scratch(DecodeParams& p, cudaStream_t stream) {
     size_t o_bytes;
   } ctx = {&p, 0};
   const size_t bytes = decode_scratch_bytes(p, &ctx.o_bytes);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
   return with_scratch(
-      bytes, stream,
+      bytes, dev, stream,
       [](void* c, void* ws, cudaStream_t s) -> int {
         DecodeParams& p = *static_cast<Ctx*>(c)->p;
         p.ws_o = static_cast<float*>(ws);

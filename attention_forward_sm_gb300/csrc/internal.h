@@ -98,9 +98,8 @@ struct ModKernelParams {
   // K and V: [BH, N, D], box {64, 128, 1}.  Q: prefill the same; decode
   // [B, Hkv, G, D] with box {64, G, 1, per_tile} (tmap_q) or {64, G, 1, 1}
   // (tmap_q1).  128-byte swizzle.
-  // Prefix: tmap_kp, tmap_vp; the last tile of a request's keys: tmap_kt,
-  // tmap_vt, box {64, 32, 1}.
-  CUtensorMap tmap_q, tmap_q1, tmap_k, tmap_v, tmap_kp, tmap_vp, tmap_kt, tmap_vt;
+  // Prefix: tmap_kp, tmap_vp; a decode's caches have boxes {64, 32, 1}.
+  CUtensorMap tmap_q, tmap_q1, tmap_k, tmap_v, tmap_kp, tmap_vp;
   void* o;
   float* lse;
   const int* ranges;
@@ -141,16 +140,27 @@ __host__ __device__ inline uint32_t run_of(uint32_t total, uint32_t runs, uint32
 }
 
 // One launch each, by head size and modifications.
-cudaError_t launch_mod_fwd_d64(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_fwd_d128(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d64_h0(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d64_h4(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d64_h8(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d64_h16(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d128_h0(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d128_h4(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d128_h8(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
-cudaError_t launch_mod_split_d128_h16(const ModKernelParams& p, unsigned grid, cudaStream_t stream);
+// (`dev`: the current device.)
+cudaError_t launch_mod_fwd_d64(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
+cudaError_t launch_mod_fwd_d128(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
+cudaError_t launch_mod_split_d64_h0(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
+cudaError_t launch_mod_split_d64_h4(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
+cudaError_t launch_mod_split_d64_h8(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
+cudaError_t launch_mod_split_d64_h16(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
+cudaError_t launch_mod_split_d128_h0(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
+cudaError_t launch_mod_split_d128_h4(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
+cudaError_t launch_mod_split_d128_h8(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
+cudaError_t launch_mod_split_d128_h16(const ModKernelParams& p, unsigned grid, int dev,
+                               cudaStream_t stream);
 
 // 3-D bf16 view [BH, N, D], box {64, rows, 1}; 4-D view [B, Hkv, G, D] of the
 // queries of a decode, box {64, G, 1, requests}.  Return an ATTN_* status.
@@ -160,7 +170,8 @@ int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, in
 // Device scratch of `bytes` for the kernels that launch(ctx, scratch, stream)
 // queues on `stream`: the stream's cached buffer or, during capture, one of the
 // graph's own.  Returns launch's status or an ATTN_ERR_*.
-int with_scratch(size_t bytes, cudaStream_t stream,
+// `dev`: the current device.
+int with_scratch(size_t bytes, int dev, cudaStream_t stream,
                  int (*launch)(void* ctx, void* scratch, cudaStream_t stream), void* ctx);
 
 // Check the device and queue the kernels; arguments are checked before.
@@ -168,8 +179,14 @@ int with_scratch(size_t bytes, cudaStream_t stream,
 int mod_fwd(const ModFwdParams& p, cudaStream_t stream);
 int mod_decode(const ModDecodeParams& p, cudaStream_t stream);
 
-// ATTN_OK when the current device is an sm_103, else the status to return.
+// ATTN_OK when the current device is an sm_103, else the status to return; and
+// what a launch needs to know of it, asked for once.
+struct DeviceInfo {
+  int dev, sms;
+  unsigned int* err_word;
+};
 int check_device();
+int device_info(DeviceInfo* out);
 
 // Device error word of the current device (one-time per-device set-up);
 // nullptr when the current device is unusable.

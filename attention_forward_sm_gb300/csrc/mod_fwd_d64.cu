@@ -4,8 +4,9 @@
 
 namespace attn {
 
-cudaError_t launch_mod_fwd_d64(const ModKernelParams& p, unsigned grid, cudaStream_t stream) {
-  return launch_variant<64, false, 0>(p, grid, stream);
+cudaError_t launch_mod_fwd_d64(const ModKernelParams& p, unsigned grid, int dev,
+                                 cudaStream_t stream) {
+  return launch_variant<64, false, 0>(p, grid, dev, stream);
 }
 
 }  // namespace attn

@@ -13,19 +13,20 @@
 namespace attn {
 namespace {
 
-int sm_count(int* out) {
-  static std::atomic<int> count[64];  // zero-initialised: not asked yet
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ATTN_ERR_CUDA;
-  int n = count[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return ATTN_ERR_CUDA;
-    count[dev].store(n, std::memory_order_relaxed);
-  }
-  *out = n;
-  return ATTN_OK;
-}
+// What the merge needs of ModKernelParams (a launch copies its parameters).
+struct CombineParams {
+  void* o;
+  float* lse;
+  const int* lens;
+  const float* slopes;
+  const float* pre_o;
+  const float* pre_lse;
+  const float* part_o;
+  const float* part_lse;
+  const uint32_t* plan;
+  int B, Hq, Hkv, G, Nk, Np, row_blocks, per_tile, prefix_tiles, pre_rows;
+  uint32_t prefix_total, ctas;
+};
 
 // One warp per (request, query head): merges the row's partial states,
 //   L = log2 sum_c 2^(lse_c),  O = sum_c 2^(lse_c - L) O_c,
@@ -35,7 +36,7 @@ int sm_count(int* out) {
 // few and in L2, so the loads of up to four of them are in flight at once and
 // nothing else is shared.
 template <int D>
-__global__ void __launch_bounds__(256) mod_combine_kernel(const ModKernelParams p, unsigned ctas) {
+__global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p) {
   constexpr int E = D / 32;
   // programmatic dependent launch: wait for the split kernel's results
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const ModKernelParams 
   int count[2] = {0, 0};
   const uint32_t before = p.plan[b], nt = p.plan[b + 1] - before, own = p.plan[p.B] * p.Hkv;
   if (p.prefix_tiles > 0) {
-    const uint32_t all = prefix_total(p), runs = min(all, ctas);
+    const uint32_t all = p.prefix_total, runs = min(all, p.ctas);
     const int item = hkv * p.row_blocks + b / (2 * p.per_tile);
     const uint32_t t0 = static_cast<uint32_t>(item) * p.prefix_tiles;
     const uint32_t r0 = run_of(all, runs, t0);
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const ModKernelParams 
     first[0] = static_cast<long long>(item + r0) * p.pre_rows + tile * 128 + in_tile * p.G + g;
   }
   if (nt > 0) {
-    const uint32_t runs = min(own, 2 * ctas);
+    const uint32_t runs = min(own, 2 * p.ctas);
     const uint32_t t0 = before * p.Hkv + hkv * nt;
     const uint32_t r0 = run_of(own, runs, t0);
     count[1] = static_cast<int>(run_of(own, runs, t0 + nt - 1) - r0) + 1;
@@ -127,9 +128,9 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const ModKernelParams 
   if (lane == 0) {
     float lse = none ? -CUDART_INF_F : (m + __log2f(sum)) * kLn2;
     // a negative slope is relative to the farthest key
-    if (p.mod.slopes && !none && p.mod.slopes[h] < 0.f) {
+    if (p.slopes && !none && p.slopes[h] < 0.f) {
       const int len = p.lens ? min(max(p.lens[b], 0), p.Nk) : p.Nk;
-      lse -= p.mod.slopes[h] * static_cast<float>(p.Np + len - 1);
+      lse -= p.slopes[h] * static_cast<float>(p.Np + len - 1);
     }
     p.lse[row] = lse;
   }
@@ -147,21 +148,26 @@ cudaError_t launch_combine(const ModKernelParams& p, unsigned ctas, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mod_combine_kernel<D>, p, ctas);
+  const CombineParams c = {p.o,        p.lse,      p.lens,     p.mod.slopes, p.pre_o,
+                           p.pre_lse,  p.part_o,   p.part_lse, p.plan,       p.B,
+                           p.Hq,       p.Hkv,      p.G,        p.Nk,         p.Np,
+                           p.row_blocks, p.per_tile, p.prefix_tiles, p.pre_rows,
+                           prefix_total(p), ctas};
+  return cudaLaunchKernelEx(&cfg, mod_combine_kernel<D>, c);
 }
 
-void common_params(ModKernelParams* k, const ScoreMod& mod) {
+void common_params(ModKernelParams* k, const ScoreMod& mod, const DeviceInfo& di) {
   k->mod = mod;
   // Never 0: an unseen score is -inf and has to stay it.  1e-37 times any product
   // below 1e30 is 0 next to a score's fp32 roundings.
   k->scale_log2 = std::max(mod.scale * kLog2e, 1e-37f);
-  k->err = device_error_word();
+  k->err = di.err_word;
   k->wait_limit_ns = wait_limit_ns();
 }
 
 struct DecodeLaunch {
   ModKernelParams* k;
-  int D;
+  int D, dev;
   unsigned ctas;
   size_t pre_o, pre_lse, part_o, part_lse;  // offsets into the scratch; plan at 0
 };
@@ -174,14 +180,14 @@ int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
   d.k->pre_lse = reinterpret_cast<float*>(base + d.pre_lse);
   d.k->part_o = reinterpret_cast<float*>(base + d.part_o);
   d.k->part_lse = reinterpret_cast<float*>(base + d.part_lse);
-  using Launch = cudaError_t (*)(const ModKernelParams&, unsigned, cudaStream_t);
+  using Launch = cudaError_t (*)(const ModKernelParams&, unsigned, int, cudaStream_t);
   static const Launch split[2][4] = {
       {launch_mod_split_d64_h4, launch_mod_split_d64_h8, launch_mod_split_d64_h16,
        launch_mod_split_d64_h0},
       {launch_mod_split_d128_h4, launch_mod_split_d128_h8, launch_mod_split_d128_h16,
        launch_mod_split_d128_h0}};
   const int G = d.k->G, heads = G <= 4 ? 0 : (G <= 8 ? 1 : (G <= 16 ? 2 : 3));
-  cudaError_t e = split[d.D == 128][heads](*d.k, d.ctas, stream);
+  cudaError_t e = split[d.D == 128][heads](*d.k, d.ctas, d.dev, stream);
   if (e == cudaSuccess)
     e = d.D == 128 ? launch_combine<128>(*d.k, d.ctas, stream)
                    : launch_combine<64>(*d.k, d.ctas, stream);
@@ -191,7 +197,8 @@ int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
 }  // namespace
 
 int mod_fwd(const ModFwdParams& p, cudaStream_t stream) {
-  if (int rc = check_device()) return rc;
+  DeviceInfo di;
+  if (int rc = device_info(&di)) return rc;
   ModKernelParams k = {};
   if (int rc = encode_rows(&k.tmap_q, p.q, p.D, p.Nq, static_cast<long long>(p.B) * p.Hq, 128))
     return rc;
@@ -218,25 +225,24 @@ int mod_fwd(const ModFwdParams& p, cudaStream_t stream) {
   const int kv_heads = std::max(1, std::min(static_cast<int>(40.0e6 / kv_bytes), p.B * p.Hkv));
   k.group_heads = kv_heads * k.G;
   k.o_sectors = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
-  common_params(&k, p.mod);
+  common_params(&k, p.mod, di);
   const unsigned grid =
       static_cast<unsigned>((p.Nq + 255ll) / 256 * p.B * p.Hq);
-  const cudaError_t e = p.D == 128 ? launch_mod_fwd_d128(k, grid, stream)
-                                   : launch_mod_fwd_d64(k, grid, stream);
+  const cudaError_t e = p.D == 128 ? launch_mod_fwd_d128(k, grid, di.dev, stream)
+                                   : launch_mod_fwd_d64(k, grid, di.dev, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
-  if (int rc = check_device()) return rc;
+  DeviceInfo di;
+  if (int rc = device_info(&di)) return rc;
   ModKernelParams k = {};
   k.G = p.Hq / p.Hkv;
   k.per_tile = 128 / k.G;
   if (int rc = encode_queries(&k.tmap_q1, p.q, p.D, k.G, p.Hkv, p.B, 1)) return rc;
   const long long heads = static_cast<long long>(p.B) * p.Hkv;
-  if (int rc = encode_rows(&k.tmap_k, p.kcache, p.D, p.Ncap, heads, 128)) return rc;
-  if (int rc = encode_rows(&k.tmap_v, p.vcache, p.D, p.Ncap, heads, 128)) return rc;
-  if (int rc = encode_rows(&k.tmap_kt, p.kcache, p.D, p.Ncap, heads, 32)) return rc;
-  if (int rc = encode_rows(&k.tmap_vt, p.vcache, p.D, p.Ncap, heads, 32)) return rc;
+  if (int rc = encode_rows(&k.tmap_k, p.kcache, p.D, p.Ncap, heads, 32)) return rc;
+  if (int rc = encode_rows(&k.tmap_v, p.vcache, p.D, p.Ncap, heads, 32)) return rc;
   k.row_blocks = (p.B + 2 * k.per_tile - 1) / (2 * k.per_tile);
   if (p.Np > 0) {
     if (int rc = encode_queries(&k.tmap_q, p.q, p.D, k.G, p.Hkv, p.B, k.per_tile)) return rc;
@@ -253,17 +259,16 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   k.Hkv = p.Hkv;
   k.Nk = p.Ncap;
   k.Np = p.Np;
-  common_params(&k, p.mod);
+  common_params(&k, p.mod, di);
 
-  int sms = 0;
-  if (int rc = sm_count(&sms)) return rc;
   const long long prefix_items =
       p.Np > 0 ? static_cast<long long>(p.Hkv) * k.row_blocks : 0;
   const long long most_tiles = prefix_items * k.prefix_tiles + heads * ((p.Ncap + 127ll) / 128);
   DecodeLaunch d = {};
   d.k = &k;
   d.D = p.D;
-  d.ctas = static_cast<unsigned>(std::min<long long>({sms, most_tiles, kMostCtas}));
+  d.dev = di.dev;
+  d.ctas = static_cast<unsigned>(std::min<long long>({di.sms, most_tiles, kMostCtas}));
   // slot of a state: its item's number + its run's
   const size_t pre = p.Np > 0 ? static_cast<size_t>(prefix_items + d.ctas) * k.pre_rows : 0;
   const size_t own = static_cast<size_t>(heads + 2ll * d.ctas) * k.G;
@@ -273,7 +278,7 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   d.part_o = d.pre_lse + up(pre * sizeof(float));
   d.part_lse = d.part_o + up(own * p.D * sizeof(float));
   const size_t bytes = d.part_lse + up(own * sizeof(float));
-  return with_scratch(bytes, stream, launch_decode, &d);
+  return with_scratch(bytes, di.dev, stream, launch_decode, &d);
 }
 
 }  // namespace attn

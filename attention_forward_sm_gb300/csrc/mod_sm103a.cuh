@@ -1198,8 +1198,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       return warp_all(mod_wait(bar, phase & 1u, abort_flag, p.err, kErrWaitLoad, p.wait_limit_ns));
     };
-    // A K or V tile into the ring: `boxes` boxes of 128 keys (one), or of 32 (the
-    // last tile of a request's keys: little of the cache's unused tail is read)
+    // A K or V tile into the ring: a box of 128 keys, or (a request's own keys) as
+    // many of 32 as hold keys: little of a cache's unused tail is read
     auto load_tile = [&](const CUtensorMap* map, int key, int box_keys, int boxes, int bh,
                          uint64_t policy) {
       const uint32_t s = g % kS;
@@ -1307,14 +1307,10 @@ __global__ void __launch_bounds__(kModThreads, 1)
             cur.over = cur.left < 0;
           }
           if (!cur.over) {
-            const int rows = cur.hi - cur.key;
-            const bool whole = rows >= kBN;
+            const int boxes = (min(cur.hi - cur.key, kBN) + 31) / 32;
 #pragma unroll 1
             for (int i = 0; i < 2 && ok; ++i) {  // K, V
-              ok = load_tile(i ? (whole ? &p.tmap_v : &p.tmap_vt)
-                               : (whole ? &p.tmap_k : &p.tmap_kt),
-                             cur.key, whole ? kBN : 32, whole ? 1 : (rows + 31) / 32, cur.bh,
-                             policy);
+              ok = load_tile(i ? &p.tmap_v : &p.tmap_k, cur.key, 32, boxes, cur.bh, policy);
               if (i == 0 && fresh && ok) {
                 if constexpr (kHeads > 0) {
                   const uint32_t buf = cur.q2 & 1;
@@ -1642,15 +1638,12 @@ __global__ void __launch_bounds__(kModThreads, 1)
 }
 
 template <int D, bool kSplit, bool kCap, bool kBias, int kHeads>
-cudaError_t launch_one(const ModKernelParams& p, unsigned grid, cudaStream_t stream) {
+cudaError_t launch_one(const ModKernelParams& p, unsigned grid, int dev, cudaStream_t stream) {
   using C = Cfg<D, false>;
   auto kernel = mod_attn_kernel<D, kSplit, kCap, kBias, kHeads>;
   // the shared-memory opt-in is a per-device property of the function
   static std::atomic<bool> attr_done[64];  // zero-initialised: false
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  cudaError_t e;
   if (!attr_done[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -1664,12 +1657,13 @@ cudaError_t launch_one(const ModKernelParams& p, unsigned grid, cudaStream_t str
 // kHeads: 0, or query heads per KV head that a decode's threads hold (4, 8, 16:
 // the smallest that G fits in; above 16 the heads are the rows).
 template <int D, bool kSplit, int kHeads>
-cudaError_t launch_variant(const ModKernelParams& p, unsigned grid, cudaStream_t stream) {
+cudaError_t launch_variant(const ModKernelParams& p, unsigned grid, int dev,
+                           cudaStream_t stream) {
   const bool cap = p.mod.cap_out > 0.f, bias = p.mod.slopes != nullptr;
-  if (cap && bias) return launch_one<D, kSplit, true, true, kHeads>(p, grid, stream);
-  if (cap) return launch_one<D, kSplit, true, false, kHeads>(p, grid, stream);
-  if (bias) return launch_one<D, kSplit, false, true, kHeads>(p, grid, stream);
-  return launch_one<D, kSplit, false, false, kHeads>(p, grid, stream);
+  if (cap && bias) return launch_one<D, kSplit, true, true, kHeads>(p, grid, dev, stream);
+  if (cap) return launch_one<D, kSplit, true, false, kHeads>(p, grid, dev, stream);
+  if (bias) return launch_one<D, kSplit, false, true, kHeads>(p, grid, dev, stream);
+  return launch_one<D, kSplit, false, false, kHeads>(p, grid, dev, stream);
 }
 
 }  // namespace

@@ -3,8 +3,9 @@
 
 namespace attn {
 
-cudaError_t launch_mod_split_d128_h0(const ModKernelParams& p, unsigned grid, cudaStream_t stream) {
-  return launch_variant<128, true, 0>(p, grid, stream);
+cudaError_t launch_mod_split_d128_h0(const ModKernelParams& p, unsigned grid, int dev,
+                                 cudaStream_t stream) {
+  return launch_variant<128, true, 0>(p, grid, dev, stream);
 }
 
 }  // namespace attn

@@ -3,8 +3,9 @@
 
 namespace attn {
 
-cudaError_t launch_mod_split_d64_h16(const ModKernelParams& p, unsigned grid, cudaStream_t stream) {
-  return launch_variant<64, true, 16>(p, grid, stream);
+cudaError_t launch_mod_split_d64_h16(const ModKernelParams& p, unsigned grid, int dev,
+                                 cudaStream_t stream) {
+  return launch_variant<64, true, 16>(p, grid, dev, stream);
 }
 
 }  // namespace attn
