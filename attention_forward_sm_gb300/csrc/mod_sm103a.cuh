@@ -115,14 +115,14 @@ struct ModMisc {
   uint64_t mma_done;
   uint64_t kv_full[8], kv_empty[8];
   uint64_t q2_full[2][2], q2_empty[2][2];  // own keys, keys as rows: Q_t in two buffers
-  uint64_t p2_full[2];    // P^T_t in shared memory (one arrival per warp of four)
+  uint64_t s2_full[2][2], p2_full[2][2], o2_done[2][2];  // and their products
   uint64_t clc_full;      // the answer to the request for more work arrived
   uint64_t work_full[2][4], work_empty[2][4];
   uint4 clc_resp;
   Work work[2][4];        // query tile t's item k in slot k % kWorkSlots
   int2 ranges[2][2 * kBM];  // prefill: keys [x, y) that the rows of item k % 2 see
-  float red[2][4][16];      // keys as rows: per warp and head, a maximum or a sum
-  float own_slopes[2][16];  // times log2(e)
+  float red[4][4][16];      // keys as rows: per team, warp and head, a maximum or a sum
+  float own_slopes[4][16];  // times log2(e)
   int4 seen[16];  // per softmax warp: keys [x, y) that all its rows see, [z, w) that any does
   uint32_t tmem_base;
   int abort_flag;
@@ -654,13 +654,15 @@ struct OwnPlan {
 };
 
 // Decode of the requests' own keys with the keys as rows (G <= kSwapHeads query
-// heads per KV head).  S^T [128 keys, 16 heads] and O^T [D, 16 heads] of query
-// tile t lie in the first 16 of its S and O columns; Q_t and P^T_t in its Q tile
-// of shared memory: Q at kSwapQ of either buffer, P^T [16 heads, 128 keys]
-// at kSwapP, both in the 128-byte-swizzled layout of a K-major operand.
+// heads per KV head).  The items of a query tile's run alternate between two teams
+// of four warps, each with its own S^T [128 keys, 16 heads] and O^T [D, 16 heads]
+// (16 columns of the query tile's S and O), Q and P^T [16 heads, 128 keys] (in
+// its Q tile of shared memory, 128-byte-swizzled as K-major operands), so one
+// team's epilogue and the next item's products and softmax overlap.
 constexpr int kSwapHeads = 16;
-constexpr uint32_t kSwapQ = 4096, kSwapP = 8192;  // bytes: buffer 1 of Q; P^T
-constexpr uint32_t kSwapPChunk = kSwapHeads * 128;  // 64 keys of P^T
+constexpr uint32_t kTeamCols = 16;
+constexpr uint32_t kTeamQ = 4096, kSwapP = 8192, kTeamP = 4096;  // bytes
+constexpr uint32_t kSwapPChunk = kSwapHeads * 128;               // 64 keys of P^T
 
 template <int D>
 struct SwapMma {
@@ -675,54 +677,62 @@ struct SwapMma {
       s<kCol, KK + 1>(tmem, k_desc, q_desc);
     }
   }
+  // the first 16 * steps keys of the tile
   template <uint32_t kCol, int KK = 0>
   __device__ static __forceinline__ void o(uint32_t tmem, uint32_t v_desc, uint32_t p_desc,
-                                           uint32_t acc) {
+                                           uint32_t acc, int steps) {
     if constexpr (KK < kBN / 16) {
+      if (KK >= steps) return;
       // the 64-element chunks of M are a tile's chunks apart; at D = 64 there
       // is one, taken twice (lanes 64.. of O^T are not used)
       constexpr uint32_t lbo = D == 128 ? static_cast<uint32_t>((kBM * 128) >> 4) << 16 : 0u;
       constexpr uint32_t off_v = ((KK * 16 * 128) >> 4) + lbo - (1u << 16);  // desc has lbo 16
       constexpr uint32_t off_p = ((KK >> 2) * kSwapPChunk + (KK & 3) * 32) >> 4;
       mma_ss<false, kCol, off_v, off_p, kIdescO>(tmem, v_desc, p_desc, KK > 0 ? 1u : acc);
-      o<kCol, KK + 1>(tmem, v_desc, p_desc, acc);
+      o<kCol, KK + 1>(tmem, v_desc, p_desc, acc, steps);
     }
   }
 };
 
 // Softmax, epilogue and V's edge: four warps, thread = key of the tile (S^T, P^T)
 // or element of the head (O^T); NH >= G heads in registers.  The running maximum
-// is common to all 128 threads.  It is kept while no score exceeds it by more than 2^8:
-// one barrier that votes on that, and on every warp's waits having ended well,
-// is all that the threads of a tile exchange.
+// is common to all 128 threads.  It is kept while no score exceeds it by more than
+// 2^8: one barrier that votes on that, and on every warp's waits having ended
+// well, is all that the threads of a tile exchange.
 template <int D, int NH, bool kCap, bool kBias>
 __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, uint8_t* smem,
-                                         uint32_t tmem, int t, int k, uint32_t step,
-                                         uint32_t units) {
+                                         uint32_t tmem, int t, int k) {
   using C = Cfg<D, false>;
   constexpr uint32_t kS = C::kStages;
   constexpr int kSlots = kWorkSlots<true>;
   const uint32_t abort_flag = smem_u32(&ms.abort_flag);
   const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, me = q * 32 + lane;
-  const uint32_t bar = 1 + t;
-  const uint32_t s_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                          kColS + t * kTileCols;
-  const uint32_t o_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) +
-                          kColO + t * kTileCols;
+  const int team = (threadIdx.x >> 7) & 1, id = t * 2 + team;
+  const uint32_t bar = 1 + id;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + t * kTileCols +
+                         team * kTeamCols;
+  const uint32_t s_addr = lanes + kColS, o_addr = lanes + kColO;
   // P^T[n][me]: row n of chunk me / 64, 16-byte unit (me % 64) / 8 swizzled by n
-  uint8_t* const pt = smem + C::kOffQ + t * C::kTileBytes + kSwapP + (me >> 6) * kSwapPChunk +
-                      (me & 7) * 2;
+  uint8_t* const pt = smem + C::kOffQ + t * C::kTileBytes + kSwapP + team * kTeamP +
+                      (me >> 6) * kSwapPChunk + (me & 7) * 2;
   const int unit = (me & 63) >> 3;
   const int G = p.G;
-  for (;; ++k) {
+  uint32_t step = 0, units = 0;  // tiles and items of this team: phases
+  for (int turn = 0;; turn ^= 1, ++k) {
     bool ok = work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax);
     const Work& w = ms.work[t][k % kSlots];
+    const bool mine = turn == team;
     if constexpr (kBias) {
-      if (ok && w.n > 0 && me < G) ms.own_slopes[t][me] = p.mod.slopes[w.id * G + me] * kLog2e;
+      if (ok && mine && w.n > 0 && me < G)
+        ms.own_slopes[id][me] = p.mod.slopes[w.id * G + me] * kLog2e;
     }
     if (bar_any(bar, 128, !ok)) return;
     const int n_tiles = w.n, tile0 = w.tile0, len = w.hi;
     if (n_tiles < 0) return;
+    if (!mine) {
+      work_done<kSlots>(ms, t, k, lane);
+      continue;
+    }
     float m[NH], l[NH];
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
@@ -731,19 +741,24 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
     }
     for (int j = 0; j < n_tiles; ++j, ++step) {
       const int key = (tile0 + j) * kBN + me;
-      ok = warp_all(mod_wait(&ms.s_full[t], step & 1, abort_flag, p.err, kErrWaitSoftmax,
+      ok = warp_all(mod_wait(&ms.s2_full[t][team], step & 1, abort_flag, p.err, kErrWaitSoftmax,
                               p.wait_limit_ns));
       if ((w.edges & 2) && j == n_tiles - 1) {
         // V behind the request's keys: its weights are 0, but 0 * NaN is not.
+        // The product takes 16 keys at a time, up to the last that holds one.
         // (What was in V's ring slot before is multiplied: before this S.)
         const uint32_t iv = w.v_last;
         ok = ok && warp_all(mod_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
-                                      kErrWaitSoftmax, p.wait_limit_ns));
-        uint4* v = reinterpret_cast<uint4*>(smem + C::kOffKV + (iv % kS) * C::kTileBytes);
-        const int keep = len - (tile0 + j) * kBN;
+                                     kErrWaitSoftmax, p.wait_limit_ns));
+        uint8_t* v = smem + C::kOffKV + (iv % kS) * C::kTileBytes;
+        const int keep = len - (tile0 + j) * kBN, row0 = keep & ~15;
         if (ok)
-          for (int i = me; i < kBN * C::kChunks * 8; i += 128)
-            if (((i >> 3) & (kBN - 1)) >= keep) v[i] = make_uint4(0, 0, 0, 0);
+          for (int i = me; i < 16 * C::kChunks * 8; i += 128) {
+            const int row = row0 + ((i >> 3) & 15);
+            if (row >= keep && row < kBN)
+              *reinterpret_cast<uint4*>(v + (i >> 7) * (kBM * 128) + row * 128 + (i & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          }
       }
       tc_fence_after();
       float s[NH];
@@ -763,7 +778,7 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
         if constexpr (kBias) {
           // the query is at the request's last key; a negative slope counts
           // from the first key of all
-          const float slope = ms.own_slopes[t][n];
+          const float slope = ms.own_slopes[id][n];
           const int dist = len - 1 - key - (slope < 0.f ? p.Np + len - 1 : 0);
           s[n] = fmaf(-slope, static_cast<float>(dist), s[n]);
         }
@@ -779,15 +794,15 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
           int x = __float_as_int(s[n]);
           x ^= (x >> 31) & 0x7FFFFFFF;
           x = __reduce_max_sync(0xFFFFFFFFu, x);
-          if (lane == n) ms.red[t][q][n] = __int_as_float(x ^ ((x >> 31) & 0x7FFFFFFF));
+          if (lane == n) ms.red[id][q][n] = __int_as_float(x ^ ((x >> 31) & 0x7FFFFFFF));
         }
         bar_sync(bar, 128);
         bool scale_o = false;
         float alpha[NH];
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-          const float mx = fmaxf(fmaxf(ms.red[t][0][n], ms.red[t][1][n]),
-                                 fmaxf(ms.red[t][2][n], ms.red[t][3][n]));
+          const float mx = fmaxf(fmaxf(ms.red[id][0][n], ms.red[id][1][n]),
+                                 fmaxf(ms.red[id][2][n], ms.red[id][3][n]));
           alpha[n] = 1.f;
           if (mx > m[n] + C::kRescale) {
             if (m[n] != -CUDART_INF_F) alpha[n] = ex2_approx(m[n] - mx);
@@ -817,16 +832,16 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.p2_full[t]);
+      if (lane == 0) mbar_arrive(&ms.p2_full[t][team]);
     }
-    ok = warp_all(mod_wait(&ms.o_done[t], units & 1, abort_flag, p.err, kErrWaitCorr,
+    ok = warp_all(mod_wait(&ms.o2_done[t][team], units & 1, abort_flag, p.err, kErrWaitCorr,
                             p.wait_limit_ns));
     ++units;
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
 #pragma unroll
       for (int d = 16; d >= 1; d /= 2) l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], d);
-      if (lane == n) ms.red[t][q][n] = l[n];
+      if (lane == n) ms.red[id][q][n] = l[n];
     }
     if (bar_any(bar, 128, !ok)) return;
     tc_fence_after();
@@ -835,7 +850,7 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
     tmem_ld_lane16(o_addr, o);
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
-      const float sum = (ms.red[t][0][n] + ms.red[t][1][n]) + (ms.red[t][2][n] + ms.red[t][3][n]);
+      const float sum = (ms.red[id][0][n] + ms.red[id][1][n]) + (ms.red[id][2][n] + ms.red[id][3][n]);
       const bool none = sum == 0.f;
       const float inv = none ? 0.f : 1.f / sum;
       if (n < G) {
@@ -870,8 +885,10 @@ __global__ void __launch_bounds__(kModThreads, 1)
       for (int i = 0; i < 2; ++i) {
         mbar_init(&ms.q2_full[t][i], 1);
         mbar_init(&ms.q2_empty[t][i], 1);
+        mbar_init(&ms.s2_full[t][i], 1);
+        mbar_init(&ms.p2_full[t][i], 4);
+        mbar_init(&ms.o2_done[t][i], 1);
       }
-      mbar_init(&ms.p2_full[t], 4);
       mbar_init(&ms.s_full[t], 1);
       mbar_init(&ms.s_read[t], 8);
       mbar_init(&ms.p_full[t], 8);
@@ -1174,16 +1191,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
     }
     if constexpr (swap) {
       if (fine) {
-        if (warp & 4) {  // four warps per query tile do, the others only let items pass
-          for (;; ++k) {
-            if (!work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax)) break;
-            const int n = ms.work[t][k % kSlots].n;
-            work_done<kSlots>(ms, t, k, lane);
-            if (n < 0) break;
-          }
-        } else {
-          own_keys<D, kHeads, kCap, kBias>(p, ms, smem, tmem, t, k, step, units);
-        }
+        own_keys<D, kHeads, kCap, kBias>(p, ms, smem, tmem, t, k);
       }
     }
   } else if (warp == kModWarpLoad) {
@@ -1323,7 +1331,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
                   mbar_arrive_expect_tx_elect(&ms.q2_full[t][buf], C::kChunks * p.G * 128);
                   for (int ch = 0; ch < C::kChunks; ++ch)
                     tma_load_4d_elect(smem + C::kOffQ + t * C::kTileBytes + ch * (kBM * 128) +
-                                          buf * kSwapQ,
+                                          buf * kTeamQ,
                                       &p.tmap_q1, &ms.q2_full[t][buf], ch * C::kAtomElems, 0, id,
                                       q0, l2_policy_evict_last());
                 } else {
@@ -1484,66 +1492,98 @@ __global__ void __launch_bounds__(kModThreads, 1)
     if constexpr (kSplit) {
       uint32_t ring = 2u * tiles;
       struct Chain {
-        int k, left;      // next item; tiles left of this one
-        int due;          // P V: 0 none; bit 0: due; 1: accumulate; 2: the item's last
-        uint32_t v_item;  // ring item of its V
-        uint32_t q, pv;   // Q taken, P V issued
+        int k, left;        // next item; tiles left of this one
+        int due;            // P V: 0 none; bit 0: due; 1: accumulate; 2: the item's last
+        int due_steps;      // its 16-key steps
+        uint32_t due_item;  // its item's number: team = number % 2
+        uint32_t v_item;    // ring item of its V
+        uint32_t items;     // items taken so far (their Qs)
+        uint32_t pv0, pv1;  // P V issued (keys as rows: for either team)
+        int last_keys;      // keys in the item's last tile
         bool over;
       };
-      Chain cur = {k, 0, 0, 0, kHeads > 0 ? 0 : qs0, kHeads > 0 ? 0 : steps0, false};
-      Chain other = {k, 0, 0, 0, kHeads > 0 ? 0 : qs1, kHeads > 0 ? 0 : steps1, false};
+      Chain cur = {k, 0, 0, 0, 0, 0, kHeads > 0 ? 0 : qs0, kHeads > 0 ? 0 : steps0, 0, 0, false};
+      Chain other = {k, 0, 0, 0, 0, 0, kHeads > 0 ? 0 : qs1, kHeads > 0 ? 0 : steps1, 0, 0, false};
 #pragma unroll 1
       for (int t = 0; ok && !(cur.over && other.over && !cur.due && !other.due); t ^= 1) {
         const uint32_t base = tmem + t * kTileCols, q_desc = desc_k + kQ0 + t * kTileDesc;
-        if (cur.due) {
-          const uint32_t iv = cur.v_item;
+        auto issue_due = [&]() {
+          const uint32_t iv = cur.v_item, team = cur.due_item & 1;
           ok = wait(&ms.kv_full[iv % kS], iv / kS) &&
-               wait(kHeads > 0 ? &ms.p2_full[t] : &ms.p_full[t], cur.pv);
-          if (!ok) break;
-          ++cur.pv;
+               wait(kHeads > 0 ? &ms.p2_full[t][team] : &ms.p_full[t],
+                    kHeads > 0 && team ? cur.pv1 : cur.pv0);
+          if (!ok) return;
+          if (kHeads > 0 && team)
+            ++cur.pv1;
+          else
+            ++cur.pv0;
           tc_fence_after();
           const uint32_t v_desc = desc_k + (iv % kS) * kTileDesc, acc = (cur.due >> 1) & 1u;
           if constexpr (kHeads > 0)
-            SwapMma<D>::template o<kColO>(base, v_desc, q_desc + (kSwapP >> 4), acc);
+            SwapMma<D>::template o<kColO>(base + team * kTeamCols, v_desc,
+                                          q_desc + ((kSwapP + team * kTeamP) >> 4), acc,
+                                          cur.due_steps);
           else
             issue_pv(t, v_desc, acc);
           mma_commit(&ms.kv_empty[iv % kS]);
-          if (cur.due & 4) mma_commit(&ms.o_done[t]);
+          if (cur.due & 4) mma_commit(kHeads > 0 ? &ms.o2_done[t][team] : &ms.o_done[t]);
           cur.due = 0;
-        }
+        };
+        // A new item's S (the other team's, in columns of its own) need not wait for the
+        // weights of the last one, if its K is there already.  (And the last one's
+        // V: the ring slot that the new item's V will have is then in that V's
+        // phase, as the team that may clear its edge relies on.)
+        const bool ahead =
+            kHeads > 0 && cur.due && !cur.over && cur.left == 0 &&
+            warp_all(mbar_test(&ms.kv_full[ring % kS], (ring / kS) & 1u) &&
+                     mbar_test(&ms.kv_full[cur.v_item % kS], (cur.v_item / kS) & 1u));
+        if (cur.due && !ahead) issue_due();
+        if (!ok) break;
         if (!cur.over) {
           const bool first = cur.left == 0;
+          const int had = cur.due;
+          int next_due = 0, next_steps = 0;
+          uint32_t next_v = 0;
           if (first) {
             ok = work_wait<kSlots>(ms, p, t, cur.k, abort_flag, kErrWaitMma);
             if (!ok) break;
-            cur.left = ms.work[t][cur.k % kSlots].n;
+            const Work& w = ms.work[t][cur.k % kSlots];
+            cur.left = w.n;
+            cur.last_keys = min(w.hi - (w.tile0 + w.n - 1) * kBN, kBN);
             work_done<kSlots>(ms, t, cur.k++, lane);
             cur.over = cur.left < 0;
             if (!cur.over) {
-              ok = kHeads > 0 ? wait(&ms.q2_full[t][cur.q & 1], cur.q >> 1)
-                              : wait(&ms.q_full[t], cur.q);
-              ++cur.q;
+              const uint32_t i = cur.items++;
+              ok = kHeads > 0 ? wait(&ms.q2_full[t][i & 1], i >> 1) : wait(&ms.q_full[t], i);
             }
           }
           if (!cur.over) {
-            const uint32_t ik = ring, buf = (cur.q - 1u) & 1u;
+            const uint32_t ik = ring, team = (cur.items - 1u) & 1;
             ring += 2u;
             ok = ok && wait(&ms.kv_full[ik % kS], ik / kS);
             if (!ok) break;
             tc_fence_after();
             const uint32_t bk = desc_k + (ik % kS) * kTileDesc;
             if constexpr (kHeads > 0)
-              SwapMma<D>::template s<kColS>(base, bk, q_desc + buf * (kSwapQ >> 4));
+              SwapMma<D>::template s<kColS>(base + team * kTeamCols, bk,
+                                            q_desc + team * (kTeamQ >> 4));
             else
               issue_s_steps<D, false, kColS, kQ0, 0, 0>(base, desc_k + t * kTileDesc, bk);
-            mma_commit(&ms.s_full[t]);
+            mma_commit(kHeads > 0 ? &ms.s2_full[t][team] : &ms.s_full[t]);
             mma_commit(&ms.kv_empty[ik % kS]);
             const bool last = cur.left == 1;
-            if (last) mma_commit(kHeads > 0 ? &ms.q2_empty[t][buf] : &ms.q_empty[t]);
-            cur.v_item = ik + 1u;
-            cur.due = 1 | (first ? 0 : 2) | (last ? 4 : 0);
+            if (last) mma_commit(kHeads > 0 ? &ms.q2_empty[t][team] : &ms.q_empty[t]);
+            next_v = ik + 1u;
+            next_due = 1 | (first ? 0 : 2) | (last ? 4 : 0);
+            next_steps = last ? (cur.last_keys + 15) / 16 : kBN / 16;
             --cur.left;
           }
+          if (had) issue_due();
+          if (!ok) break;
+          cur.due = next_due;
+          cur.due_steps = next_steps;
+          cur.v_item = next_v;
+          cur.due_item = cur.items - 1u;
         }
         const Chain next = other;
         other = cur;
