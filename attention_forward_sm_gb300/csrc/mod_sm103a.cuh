@@ -92,7 +92,20 @@ struct Work {
   int kind;       // decode: 0 shared prefix, 1 own keys, 2 end of the prefix items
   int slot;       // decode: where its partial states go
   uint32_t v_first, v_last;  // ring items of V in the first and the last tile
+  uint32_t other;            // decode's own keys: tiles of the CTA's other run
 };
+
+// The ring items of a decode's two runs of own keys: step by step, K of query tile
+// 0 and 1, then V of both, as far as they have a tile in that step: a tile's
+// successor can then load its K while its own V is still waiting for weights.
+// Of step s of query tile t's run, the other having `other` tiles: the number of K,
+// and what to add for V.
+__device__ __forceinline__ uint32_t own_ring_k(uint32_t s, uint32_t other, int t) {
+  return 2 * (s + min(s, other)) + (t == 1 && s < other ? 1 : 0);
+}
+__device__ __forceinline__ uint32_t own_ring_v(uint32_t s, uint32_t other) {
+  return s < other ? 2 : 1;
+}
 
 // What the softmax warps know about a row: it sees keys [lo, hi) of the item's
 // K/V, and with a bias key j gets -slope * (|pos - j| - ref), pos and j counted
@@ -628,10 +641,10 @@ struct OwnPlan {
     w.b[0] = t ? 0 : w.n;
     w.b[1] = t ? w.n : 0;
     w.edges = w.hi < (tile0 + w.n) * kBN ? 2 : 0;
-    // the two runs' tiles take turns in the ring
     const uint32_t s = mine - left + w.n - 1;  // step of the item's last tile
     w.v_first = 0;
-    w.v_last = ring0 + 2 * (s + min(t ? s + 1 : s, other)) + 1;
+    w.v_last = ring0 + own_ring_k(s, other, t) + own_ring_v(s, other);
+    w.other = other;
     left -= w.n;
     if (left > 0) {
       tile0 = 0;
@@ -1297,48 +1310,49 @@ __global__ void __launch_bounds__(kModThreads, 1)
       Run cur = {k, 0, 0, 0, 0, 0, false}, other = cur;
       const uint64_t policy = l2_policy_evict_first();  // every byte is read once
 #pragma unroll 1
-      for (int t = 0; ok && !(cur.over && other.over); t ^= 1) {
+      for (int turn = 0; ok && !(cur.over && other.over); ++turn) {
+        // K of query tile 0, of 1, V of 0, of 1
+        const int t = turn & 1;
+        const bool is_v = (turn & 2) != 0;
+        bool fresh = false;
+        int id = 0, q0 = 0;
+        if (!cur.over && !is_v && cur.left == 0) {
+          ok = work_wait<kSlots>(ms, p, t, cur.k, abort_flag, kErrWaitLoad);
+          if (!ok) break;
+          const Work& w = ms.work[t][cur.k % kSlots];
+          cur.left = w.n;
+          cur.key = w.tile0 * kBN;
+          cur.hi = w.hi;
+          id = w.id;
+          q0 = w.q0;
+          cur.bh = q0 * p.Hkv + id;
+          work_done<kSlots>(ms, t, cur.k++, lane);
+          cur.over = cur.left < 0;
+          fresh = true;
+        }
         if (!cur.over) {
-          const bool fresh = cur.left == 0;
-          int id = 0, q0 = 0;
-          if (fresh) {
-            ok = work_wait<kSlots>(ms, p, t, cur.k, abort_flag, kErrWaitLoad);
-            if (!ok) break;
-            const Work& w = ms.work[t][cur.k % kSlots];
-            cur.left = w.n;
-            cur.key = w.tile0 * kBN;
-            cur.hi = w.hi;
-            id = w.id;
-            q0 = w.q0;
-            cur.bh = q0 * p.Hkv + id;
-            work_done<kSlots>(ms, t, cur.k++, lane);
-            cur.over = cur.left < 0;
-          }
-          if (!cur.over) {
-            const int boxes = (min(cur.hi - cur.key, kBN) + 31) / 32;
-#pragma unroll 1
-            for (int i = 0; i < 2 && ok; ++i) {  // K, V
-              ok = load_tile(i ? &p.tmap_v : &p.tmap_k, cur.key, 32, boxes, cur.bh, policy);
-              if (i == 0 && fresh && ok) {
-                if constexpr (kHeads > 0) {
-                  const uint32_t buf = cur.q2 & 1;
-                  // the buffer: free of the item two before, and of the prefix items' Q
-                  const uint32_t before = t ? q1_loads : q0_loads;
-                  ok = cur.q2 >= 2 ? wait(&ms.q2_empty[t][buf], (cur.q2 >> 1) + 1)
-                                   : before == 0 || wait(&ms.q_empty[t], before - 1);
-                  if (!ok) break;
-                  ++cur.q2;
-                  mbar_arrive_expect_tx_elect(&ms.q2_full[t][buf], C::kChunks * p.G * 128);
-                  for (int ch = 0; ch < C::kChunks; ++ch)
-                    tma_load_4d_elect(smem + C::kOffQ + t * C::kTileBytes + ch * (kBM * 128) +
-                                          buf * kTeamQ,
-                                      &p.tmap_q1, &ms.q2_full[t][buf], ch * C::kAtomElems, 0, id,
-                                      q0, l2_policy_evict_last());
-                } else {
-                  ok = load_q(t, 1, id, q0);
-                }
-              }
+          const int boxes = (min(cur.hi - cur.key, kBN) + 31) / 32;
+          ok = load_tile(is_v ? &p.tmap_v : &p.tmap_k, cur.key, 32, boxes, cur.bh, policy);
+          if (fresh && ok) {
+            if constexpr (kHeads > 0) {
+              const uint32_t buf = cur.q2 & 1;
+              // the buffer: free of the item two before, and of the prefix items' Q
+              const uint32_t before = t ? q1_loads : q0_loads;
+              ok = cur.q2 >= 2 ? wait(&ms.q2_empty[t][buf], (cur.q2 >> 1) + 1)
+                               : before == 0 || wait(&ms.q_empty[t], before - 1);
+              if (!ok) break;
+              ++cur.q2;
+              mbar_arrive_expect_tx_elect(&ms.q2_full[t][buf], C::kChunks * p.G * 128);
+              for (int ch = 0; ch < C::kChunks; ++ch)
+                tma_load_4d_elect(smem + C::kOffQ + t * C::kTileBytes + ch * (kBM * 128) +
+                                      buf * kTeamQ,
+                                  &p.tmap_q1, &ms.q2_full[t][buf], ch * C::kAtomElems, 0, id, q0,
+                                  l2_policy_evict_last());
+            } else {
+              ok = load_q(t, 1, id, q0);
             }
+          }
+          if (is_v) {
             cur.key += kBN;
             --cur.left;
           }
@@ -1490,7 +1504,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
     // the other's MMAs.  S reads Q from shared memory at D = 64 too: the bytes
     // of K and V set the pace here.
     if constexpr (kSplit) {
-      uint32_t ring = 2u * tiles;
+      const uint32_t ring = 2u * tiles;
       struct Chain {
         int k, left;        // next item; tiles left of this one
         int due;            // P V: 0 none; bit 0: due; 1: accumulate; 2: the item's last
@@ -1500,10 +1514,14 @@ __global__ void __launch_bounds__(kModThreads, 1)
         uint32_t items;     // items taken so far (their Qs)
         uint32_t pv0, pv1;  // P V issued (keys as rows: for either team)
         int last_keys;      // keys in the item's last tile
+        uint32_t step;      // tiles of the run done
+        uint32_t other;     // tiles of the other run
         bool over;
       };
-      Chain cur = {k, 0, 0, 0, 0, 0, kHeads > 0 ? 0 : qs0, kHeads > 0 ? 0 : steps0, 0, 0, false};
-      Chain other = {k, 0, 0, 0, 0, 0, kHeads > 0 ? 0 : qs1, kHeads > 0 ? 0 : steps1, 0, 0, false};
+      Chain cur = {k, 0, 0, 0, 0, 0, kHeads > 0 ? 0 : qs0, kHeads > 0 ? 0 : steps0,
+                   0, 0, 0, 0, false};
+      Chain other = {k, 0, 0, 0, 0, 0, kHeads > 0 ? 0 : qs1, kHeads > 0 ? 0 : steps1,
+                     0, 0, 0, 0, false};
 #pragma unroll 1
       for (int t = 0; ok && !(cur.over && other.over && !cur.due && !other.due); t ^= 1) {
         const uint32_t base = tmem + t * kTileCols, q_desc = desc_k + kQ0 + t * kTileDesc;
@@ -1533,9 +1551,10 @@ __global__ void __launch_bounds__(kModThreads, 1)
         // weights of the last one, if its K is there already.  (And the last one's
         // V: the ring slot that the new item's V will have is then in that V's
         // phase, as the team that may clear its edge relies on.)
+        const uint32_t ahead_k = ring + own_ring_k(cur.step, cur.other, t);
         const bool ahead =
             kHeads > 0 && cur.due && !cur.over && cur.left == 0 &&
-            warp_all(mbar_test(&ms.kv_full[ring % kS], (ring / kS) & 1u) &&
+            warp_all(mbar_test(&ms.kv_full[ahead_k % kS], (ahead_k / kS) & 1u) &&
                      mbar_test(&ms.kv_full[cur.v_item % kS], (cur.v_item / kS) & 1u));
         if (cur.due && !ahead) issue_due();
         if (!ok) break;
@@ -1550,6 +1569,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
             const Work& w = ms.work[t][cur.k % kSlots];
             cur.left = w.n;
             cur.last_keys = min(w.hi - (w.tile0 + w.n - 1) * kBN, kBN);
+            cur.other = w.other;
             work_done<kSlots>(ms, t, cur.k++, lane);
             cur.over = cur.left < 0;
             if (!cur.over) {
@@ -1558,8 +1578,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
             }
           }
           if (!cur.over) {
-            const uint32_t ik = ring, team = (cur.items - 1u) & 1;
-            ring += 2u;
+            const uint32_t ik = ring + own_ring_k(cur.step, cur.other, t);
+            const uint32_t team = (cur.items - 1u) & 1;
             ok = ok && wait(&ms.kv_full[ik % kS], ik / kS);
             if (!ok) break;
             tc_fence_after();
@@ -1573,7 +1593,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
             mma_commit(&ms.kv_empty[ik % kS]);
             const bool last = cur.left == 1;
             if (last) mma_commit(kHeads > 0 ? &ms.q2_empty[t][team] : &ms.q_empty[t]);
-            next_v = ik + 1u;
+            next_v = ik + own_ring_v(cur.step, cur.other);
+            ++cur.step;
             next_due = 1 | (first ? 0 : 2) | (last ? 4 : 0);
             next_steps = last ? (cur.last_keys + 15) / 16 : kBN / 16;
             --cur.left;
