@@ -91,20 +91,19 @@ struct Work {
   int q0;         // prefill: first query row; decode: first request of tile 0
   int kind;       // decode: 0 shared prefix, 1 own keys, 2 end of the prefix items
   int slot;       // decode: where its partial states go
-  uint32_t v_first, v_last;  // ring items of V in the first and the last tile
-  uint32_t other;            // decode's own keys: tiles of the CTA's other run
+  uint32_t v_first, v_last;  // ring items of V in the first and the last tile; own
+                             // keys: ring items of the prefix, number of the first tile
 };
 
-// The ring items of a decode's two runs of own keys: step by step, K of query tile
-// 0 and 1, then V of both, as far as they have a tile in that step: a tile's
-// successor can then load its K while its own V is still waiting for weights.
-// Of step s of query tile t's run, the other having `other` tiles: the number of K,
-// and what to add for V.
-__device__ __forceinline__ uint32_t own_ring_k(uint32_t s, uint32_t other, int t) {
-  return 2 * (s + min(s, other)) + (t == 1 && s < other ? 1 : 0);
-}
-__device__ __forceinline__ uint32_t own_ring_v(uint32_t s, uint32_t other) {
-  return s < other ? 2 : 1;
+// A decode's own keys use the ring's slots as four rings, K and V of either query
+// tile, so that each is loaded as soon as its own slot is free.  Tile n of one is
+// given the ring item number that stands for its slot (% kS) and the slot's use (/
+// kS), after `before` items of the shared prefix.
+template <uint32_t kS>
+__device__ __forceinline__ uint32_t own_item(uint32_t before, bool is_v, int t, uint32_t n) {
+  constexpr uint32_t kPer = kS / 4;
+  const uint32_t slot = ((is_v ? 2u : 0u) + t) * kPer + n % kPer;
+  return ((before + kS - 1 - slot) / kS + n / kPer) * kS + slot;
 }
 
 // What the softmax warps know about a row: it sees keys [lo, hi) of the item's
@@ -128,7 +127,9 @@ struct ModMisc {
   uint64_t mma_done;
   uint64_t kv_full[8], kv_empty[8];
   uint64_t q2_full[2][2], q2_empty[2][2];  // own keys, keys as rows: Q_t in two buffers
-  uint64_t s2_full[2][2], p2_full[2][2], o2_done[2][2];  // and their products
+  uint64_t s2_full[2][2], s2_read[2][2];   // S^T of a team: in TMEM; read (an arrival per warp)
+  uint64_t pv2_done[2][2];                 // O^T += V^T P^T of a tile of a team retired
+  uint64_t own_start[2];                   // the query tile's warps are done with prefix items
   uint64_t clc_full;      // the answer to the request for more work arrived
   uint64_t work_full[2][4], work_empty[2][4];
   uint4 clc_resp;
@@ -137,6 +138,7 @@ struct ModMisc {
   float red[4][4][16];      // keys as rows: per team, warp and head, a maximum or a sum
   float own_slopes[4][16];  // times log2(e)
   int4 seen[16];  // per softmax warp: keys [x, y) that all its rows see, [z, w) that any does
+  int own_pv[2];  // O^T += V^T P^T issued so far in the query tile's run of own keys
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -580,7 +582,7 @@ struct OwnPlan {
   int b0, at;      // request b0 + at, of a block of 32 that the lanes hold
   int id, tile0;   // KV head, tile within the item
   int len, tiles;  // this lane's request: its keys and key tiles
-  uint32_t mine, other;  // tiles of this run and of the CTA's other one
+  uint32_t mine;   // tiles of this run
 
   __device__ __forceinline__ void load_block(const ModKernelParams& p, int lane) {
     len = b0 + lane < p.B ? request_len(p, b0 + lane) : 0;
@@ -595,15 +597,13 @@ struct OwnPlan {
     for (int b = 32 + lane; b < p.B; b += 32) own += key_tiles(request_len(p, b));
     const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, own) * p.Hkv;
     const uint32_t runs = min(total, 2 * gridDim.x);
-    const uint32_t r0 = gridDim.x - 1 - blockIdx.x, r1 = r0 + gridDim.x;
-    const uint32_t r = t ? r1 : r0, q = t ? r0 : r1;
+    const uint32_t r = t * gridDim.x + gridDim.x - 1 - blockIdx.x;
     uint32_t x = 0;
-    mine = other = 0;
+    mine = 0;
     if (r < runs) {
       x = run_start(total, runs, r);
       mine = run_start(total, runs, r + 1) - x;
     }
-    if (q < runs) other = run_start(total, runs, q + 1) - run_start(total, runs, q);
     run = static_cast<int>(r);
     left = static_cast<int>(mine);
     at = id = tile0 = 0;
@@ -641,10 +641,8 @@ struct OwnPlan {
     w.b[0] = t ? 0 : w.n;
     w.b[1] = t ? w.n : 0;
     w.edges = w.hi < (tile0 + w.n) * kBN ? 2 : 0;
-    const uint32_t s = mine - left + w.n - 1;  // step of the item's last tile
-    w.v_first = 0;
-    w.v_last = ring0 + own_ring_k(s, other, t) + own_ring_v(s, other);
-    w.other = other;
+    w.v_first = ring0;
+    w.v_last = mine - left;
     left -= w.n;
     if (left > 0) {
       tile0 = 0;
@@ -712,6 +710,29 @@ struct SwapMma {
 // is common to all 128 threads.  It is kept while no score exceeds it by more than
 // 2^8: one barrier that votes on that, and on every warp's waits having ended
 // well, is all that the threads of a tile exchange.
+// Waits, as mod_wait does, until the products of the first n tiles of query tile
+// t's run have been issued.
+__device__ __forceinline__ bool own_turn(ModMisc& ms, const ModKernelParams& p, int t, uint32_t n,
+                                         uint32_t abort_sa) {
+  uint32_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    const int done = *const_cast<volatile int*>(&ms.own_pv[t]);
+    if (warp_all(done >= static_cast<int>(n))) return true;
+    if ((it & 255u) == 0u) {
+      uint32_t now;
+      asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+      if (it == 256u) t0 = now;
+      const bool late = now - t0 > static_cast<uint32_t>(p.wait_limit_ns);
+      if (!warp_all(!abort_set(abort_sa))) return false;
+      if (!warp_all(!late)) {
+        abort_raise(abort_sa);
+        if ((threadIdx.x & 31) == 0) atomicOr(p.err, kErrWaitSoftmax);
+        return false;
+      }
+    }
+  }
+}
+
 template <int D, int NH, bool kCap, bool kBias>
 __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, uint8_t* smem,
                                          uint32_t tmem, int t, int k) {
@@ -730,18 +751,27 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
                       (me >> 6) * kSwapPChunk + (me & 7) * 2;
   const int unit = (me & 63) >> 3;
   const int G = p.G;
-  uint32_t step = 0, units = 0;  // tiles and items of this team: phases
+  uint32_t step = 0;  // tiles of this team: phases
+  // PV in flight land before this team's warps leave
+  auto leave = [&]() {
+    if (q == 0 && step > 0) drain_wait(&ms.pv2_done[t][team], (step - 1) & 1);
+  };
+  // the other warps may still be reading the last prefix item's O
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&ms.own_start[t]);
+  bool started = warp_all(mod_wait(&ms.own_start[t], 0, abort_flag, p.err, kErrWaitSoftmax,
+                                   p.wait_limit_ns));
   for (int turn = 0;; turn ^= 1, ++k) {
-    bool ok = work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax);
+    bool ok = started && work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax);
     const Work& w = ms.work[t][k % kSlots];
     const bool mine = turn == team;
     if constexpr (kBias) {
       if (ok && mine && w.n > 0 && me < G)
         ms.own_slopes[id][me] = p.mod.slopes[w.id * G + me] * kLog2e;
     }
-    if (bar_any(bar, 128, !ok)) return;
+    if (bar_any(bar, 128, !ok)) break;
     const int n_tiles = w.n, tile0 = w.tile0, len = w.hi;
-    if (n_tiles < 0) return;
+    if (n_tiles < 0) return;  // (every product of this team has retired)
     if (!mine) {
       work_done<kSlots>(ms, t, k, lane);
       continue;
@@ -756,23 +786,6 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
       const int key = (tile0 + j) * kBN + me;
       ok = warp_all(mod_wait(&ms.s2_full[t][team], step & 1, abort_flag, p.err, kErrWaitSoftmax,
                               p.wait_limit_ns));
-      if ((w.edges & 2) && j == n_tiles - 1) {
-        // V behind the request's keys: its weights are 0, but 0 * NaN is not.
-        // The product takes 16 keys at a time, up to the last that holds one.
-        // (What was in V's ring slot before is multiplied: before this S.)
-        const uint32_t iv = w.v_last;
-        ok = ok && warp_all(mod_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
-                                     kErrWaitSoftmax, p.wait_limit_ns));
-        uint8_t* v = smem + C::kOffKV + (iv % kS) * C::kTileBytes;
-        const int keep = len - (tile0 + j) * kBN, row0 = keep & ~15;
-        if (ok)
-          for (int i = me; i < 16 * C::kChunks * 8; i += 128) {
-            const int row = row0 + ((i >> 3) & 15);
-            if (row >= keep && row < kBN)
-              *reinterpret_cast<uint4*>(v + (i >> 7) * (kBM * 128) + row * 128 + (i & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-          }
-      }
       tc_fence_after();
       float s[NH];
       {
@@ -781,6 +794,9 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
 #pragma unroll
         for (int n = 0; n < NH; ++n) s[n] = __uint_as_float(sr[n]);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.s2_read[t][team]);
       bool above = false;
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
@@ -798,8 +814,12 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
         if (key >= len || n >= G) s[n] = -CUDART_INF_F;
         above = above || s[n] > m[n] + C::kRescale;
       }
+      // this team's last product is done with P^T and O^T
+      if (step > 0)
+        ok = ok && warp_all(mod_wait(&ms.pv2_done[t][team], (step - 1) & 1, abort_flag, p.err,
+                                     kErrWaitCorr, p.wait_limit_ns));
       if (bar_any(bar, 128, above || !ok)) {
-        if (bar_any(bar, 128, !ok)) return;
+        if (bar_any(bar, 128, !ok)) return leave();
         // the tile's maximum of every head
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
@@ -826,6 +846,7 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
         }
         if (j > 0 && scale_o) {  // alike in all threads
           uint32_t v[16];
+          tc_fence_after();
           tmem_ld_lane16(o_addr, v);
 #pragma unroll
           for (int n = 0; n < NH; ++n) v[n] = __float_as_uint(__uint_as_float(v[n]) * alpha[n]);
@@ -842,21 +863,56 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
           *reinterpret_cast<__nv_bfloat16*>(pt + n * 128 + ((unit ^ (n & 7)) << 4)) =
               __float2bfloat16_rn(x);
       }
+      // V, once the tile before it in the run has been multiplied (the slot's barrier is
+      // then in this tile's phase)
+      const uint32_t n_run = w.v_last + j;
+      const uint32_t iv = own_item<kS>(w.v_first, true, t, n_run);
+      const bool edge = (w.edges & 2) && j == n_tiles - 1;
+      const int keep = len - (tile0 + j) * kBN;  // keys of the tile, if it is an edge
+      if (edge || q == 0) {
+        ok = own_turn(ms, p, t, n_run, abort_flag) &&
+             warp_all(mod_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
+                               kErrWaitSoftmax, p.wait_limit_ns));
+        if (edge && ok) {
+          // Behind the request's keys the weights are 0, but 0 * NaN is not.  The product
+          // takes 16 keys at a time, up to the last that holds one.
+          uint8_t* v = smem + C::kOffKV + (iv % kS) * C::kTileBytes;
+          const int row0 = keep & ~15;
+          for (int i = me; i < 16 * C::kChunks * 8; i += 128) {
+            const int row = row0 + ((i >> 3) & 15);
+            if (row >= keep && row < kBN)
+              *reinterpret_cast<uint4*>(v + (i >> 7) * (kBM * 128) + row * 128 + (i & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
       fence_proxy_async_smem();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.p2_full[t][team]);
+      if (bar_any(bar, 128, !ok)) return leave();
+      if (q == 0) {
+        // O^T (+)= V^T P^T, issued by this team itself: its P^T is complete here, and the
+        // MMA warp need not wait for it
+        tc_fence_after();
+        const uint32_t desc_k = sdesc_sw128_lo(smem_u32(smem + C::kOffKV), 16);
+        const uint32_t p_desc = sdesc_sw128_lo(
+            smem_u32(smem + C::kOffQ + t * C::kTileBytes + kSwapP + team * kTeamP), 16);
+        SwapMma<D>::template o<kColO>(tmem + t * kTileCols + team * kTeamCols,
+                                      desc_k + (iv % kS) * (C::kTileBytes >> 4), p_desc,
+                                      j > 0 ? 1u : 0u, edge ? (keep + 15) / 16 : kBN / 16);
+        mma_commit(&ms.kv_empty[iv % kS]);
+        mma_commit(&ms.pv2_done[t][team]);
+        if (lane == 0) *const_cast<volatile int*>(&ms.own_pv[t]) = static_cast<int>(n_run) + 1;
+      }
     }
-    ok = warp_all(mod_wait(&ms.o2_done[t][team], units & 1, abort_flag, p.err, kErrWaitCorr,
-                            p.wait_limit_ns));
-    ++units;
+    ok = warp_all(mod_wait(&ms.pv2_done[t][team], (step - 1) & 1, abort_flag, p.err, kErrWaitCorr,
+                           p.wait_limit_ns));
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
 #pragma unroll
       for (int d = 16; d >= 1; d /= 2) l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], d);
       if (lane == n) ms.red[id][q][n] = l[n];
     }
-    if (bar_any(bar, 128, !ok)) return;
+    if (bar_any(bar, 128, !ok)) return leave();
     tc_fence_after();
     const size_t row0 = static_cast<size_t>(w.slot) * G;
     uint32_t o[16];
@@ -874,6 +930,7 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
     tc_fence_before();
     work_done<kSlots>(ms, t, k, lane);
   }
+  leave();
 }
 
 template <int D, bool kSplit, bool kCap, bool kBias, int kHeads>
@@ -899,9 +956,11 @@ __global__ void __launch_bounds__(kModThreads, 1)
         mbar_init(&ms.q2_full[t][i], 1);
         mbar_init(&ms.q2_empty[t][i], 1);
         mbar_init(&ms.s2_full[t][i], 1);
-        mbar_init(&ms.p2_full[t][i], 4);
-        mbar_init(&ms.o2_done[t][i], 1);
+        mbar_init(&ms.s2_read[t][i], 4);
+        mbar_init(&ms.pv2_done[t][i], 1);
       }
+      mbar_init(&ms.own_start[t], 8);
+      ms.own_pv[t] = 0;
       mbar_init(&ms.s_full[t], 1);
       mbar_init(&ms.s_read[t], 8);
       mbar_init(&ms.p_full[t], 8);
@@ -1050,7 +1109,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
           // both query tiles use the tile, each does).  The tile of V that was
           // in its ring slot before has been multiplied already (before this
           // S), so the slot's barrier is in this tile's phase.
-          const uint32_t iv = j == w.n - 1 ? w.v_last : w.v_first;
+          uint32_t iv = j == w.n - 1 ? w.v_last : w.v_first;
+          if (kSplit && w.kind == 1) iv = own_item<kS>(w.v_first, true, t, w.v_last + j);
           if (!warp_all(mod_wait(&ms.kv_full[iv % kS], (iv / kS) & 1u, abort_flag, p.err,
                                   kErrWaitSoftmax, p.wait_limit_ns))) {
             ok = false;
@@ -1300,75 +1360,144 @@ __global__ void __launch_bounds__(kModThreads, 1)
     }
     // ---- decode: the two runs of own keys, a tile of either in turn
     if constexpr (kSplit) {
-      // Both runs go through the same code, in turn: the state of one is kept aside
-      // while the other's is worked on.
-      struct Run {
-        int k, left, key, hi, bh;
-        uint32_t q2;  // loads of Q for the products with keys as rows
+      // K of query tile 0, of 1, V of 0, of 1: four sequences of tiles that go
+      // through the same code in turn, each issued when its ring slot is free.
+      struct Seq {
+        int k, left;       // next item; tiles left of this one
+        int key, hi, bh;   // next key, the item's end, row of the cache
+        uint32_t n;        // tiles issued
         bool over;
       };
-      Run cur = {k, 0, 0, 0, 0, 0, false}, other = cur;
+      const uint32_t before = g;  // ring items of the prefix
+      const int k0 = k;
       const uint64_t policy = l2_policy_evict_first();  // every byte is read once
+      Seq cur = {k, 0, 0, 0, 0, 0, false}, s1 = cur, s2 = cur, s3 = cur;
+      uint32_t idle = 0, t0 = 0;
+      auto ready = [&](uint64_t* bar, uint32_t phase) {
+        return warp_all(mbar_test(bar, phase & 1u));
+      };
+      int turn = 0;
 #pragma unroll 1
-      for (int turn = 0; ok && !(cur.over && other.over); ++turn) {
-        // K of query tile 0, of 1, V of 0, of 1
+      for (; !(cur.over && s1.over && s2.over && s3.over); ++turn) {
         const int t = turn & 1;
         const bool is_v = (turn & 2) != 0;
-        bool fresh = false;
-        int id = 0, q0 = 0;
-        if (!cur.over && !is_v && cur.left == 0) {
-          ok = work_wait<kSlots>(ms, p, t, cur.k, abort_flag, kErrWaitLoad);
-          if (!ok) break;
-          const Work& w = ms.work[t][cur.k % kSlots];
-          cur.left = w.n;
-          cur.key = w.tile0 * kBN;
-          cur.hi = w.hi;
-          id = w.id;
-          q0 = w.q0;
-          cur.bh = q0 * p.Hkv + id;
-          work_done<kSlots>(ms, t, cur.k++, lane);
-          cur.over = cur.left < 0;
-          fresh = true;
-        }
+        bool did = false;
         if (!cur.over) {
-          const int boxes = (min(cur.hi - cur.key, kBN) + 31) / 32;
-          ok = load_tile(is_v ? &p.tmap_v : &p.tmap_k, cur.key, 32, boxes, cur.bh, policy);
-          if (fresh && ok) {
-            if constexpr (kHeads > 0) {
-              const uint32_t buf = cur.q2 & 1;
-              // the buffer: free of the item two before, and of the prefix items' Q
-              const uint32_t before = t ? q1_loads : q0_loads;
-              ok = cur.q2 >= 2 ? wait(&ms.q2_empty[t][buf], (cur.q2 >> 1) + 1)
-                               : before == 0 || wait(&ms.q_empty[t], before - 1);
-              if (!ok) break;
-              ++cur.q2;
-              mbar_arrive_expect_tx_elect(&ms.q2_full[t][buf], C::kChunks * p.G * 128);
-              for (int ch = 0; ch < C::kChunks; ++ch)
-                tma_load_4d_elect(smem + C::kOffQ + t * C::kTileBytes + ch * (kBM * 128) +
-                                      buf * kTeamQ,
-                                  &p.tmap_q1, &ms.q2_full[t][buf], ch * C::kAtomElems, 0, id, q0,
-                                  l2_policy_evict_last());
+          // s2 is the other sequence of this query tile: V follows K's items, and
+          // gives their slots free
+          const int slot = cur.k % kSlots;
+          const bool fresh = cur.left == 0;
+          bool go = !fresh || (is_v ? cur.k < s2.k
+                                    : ready(&ms.work_full[t][slot], cur.k / kSlots));
+          if (go && fresh) {
+            const Work& w = ms.work[t][slot];
+            if (w.n < 0) {
+              cur.over = true;
+              ++cur.k;
+              if (is_v) work_done<kSlots>(ms, t, cur.k - 1, lane);
+              go = false;
+              did = true;
             } else {
-              ok = load_q(t, 1, id, q0);
+              cur.key = w.tile0 * kBN;
+              cur.hi = w.hi;
+              cur.bh = w.q0 * p.Hkv + w.id;
             }
           }
-          if (is_v) {
+          const uint32_t it = own_item<kS>(before, is_v, t, cur.n);
+          go = go && ready(&ms.kv_empty[it % kS], it / kS + 1);
+          const uint32_t i = static_cast<uint32_t>(cur.k - k0);  // number of a fresh item
+          if (go && fresh && !is_v) {
+            // its Q's buffer: free of the item two (without buffers by team: one)
+            // before, and of the prefix items' Q
+            const uint32_t loads = t ? q1_loads : q0_loads;
+            if constexpr (kHeads > 0)
+              go = i >= 2 ? ready(&ms.q2_empty[t][i & 1], (i >> 1) + 1)
+                          : loads == 0 || ready(&ms.q_empty[t], loads - 1);
+            else
+              go = loads == 0 || ready(&ms.q_empty[t], loads - 1);
+          }
+          if (go) {
+            const Work& w = ms.work[t][slot];
+            if (fresh) cur.left = w.n;
+            const int boxes = (min(cur.hi - cur.key, kBN) + 31) / 32;
+            const CUtensorMap* map = is_v ? &p.tmap_v : &p.tmap_k;
+            uint64_t* full = &ms.kv_full[it % kS];
+            uint8_t* dst = smem + C::kOffKV + (it % kS) * C::kTileBytes;
+            mbar_arrive_expect_tx_elect(full, boxes * 32 * (C::kChunks * 128));
+#pragma unroll 1
+            for (int x = 0; x < boxes; ++x) {
+#pragma unroll
+              for (int ch = 0; ch < C::kChunks; ++ch)
+                tma_load_3d_elect(dst + ch * (kBM * 128) + x * (32 * 128), map, full,
+                                  ch * C::kAtomElems, cur.key + 32 * x, cur.bh, policy);
+            }
+            if (fresh && !is_v) {
+              if constexpr (kHeads > 0) {
+                uint8_t* q = smem + C::kOffQ + t * C::kTileBytes + (i & 1) * kTeamQ;
+                mbar_arrive_expect_tx_elect(&ms.q2_full[t][i & 1], C::kChunks * p.G * 128);
+                for (int ch = 0; ch < C::kChunks; ++ch)
+                  tma_load_4d_elect(q + ch * (kBM * 128), &p.tmap_q1, &ms.q2_full[t][i & 1],
+                                    ch * C::kAtomElems, 0, w.id, w.q0, l2_policy_evict_last());
+              } else {
+                load_q(t, 1, w.id, w.q0);
+              }
+            }
+            if (fresh) {
+              if (is_v) work_done<kSlots>(ms, t, cur.k, lane);
+              ++cur.k;
+            }
             cur.key += kBN;
             --cur.left;
+            ++cur.n;
+            did = true;
           }
         }
-        const Run next = other;
-        other = cur;
+        const Seq next = s1;
+        s1 = s2;
+        s2 = s3;
+        s3 = cur;
         cur = next;
+        // as mod_wait: give up on an abort or after the time limit
+        idle = did ? 0 : idle + 1;
+        if (idle && (idle & 255u) == 0u) {
+          uint32_t now;
+          asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+          if (idle == 256u) t0 = now;
+          const bool late = now - t0 > static_cast<uint32_t>(p.wait_limit_ns);
+          const bool gone = !warp_all(!abort_set(abort_flag));
+          if (gone || !warp_all(!late)) {
+            if (!gone) {
+              abort_raise(abort_flag);
+              if (lane == 0) atomicOr(p.err, kErrWaitLoad);
+            }
+            ++turn;  // (the sequences have moved on)
+            break;
+          }
+        }
       }
       if (abort_set(abort_flag)) {
-        // (which of the two is whose does not matter to an upper bound of drains)
-        for (int t = 0; t < 2; ++t)
-          for (uint32_t buf = 0; buf < 2; ++buf) {
-            const uint32_t a = (cur.q2 + 1 - buf) / 2, b = (other.q2 + 1 - buf) / 2;
-            if (a > 0) drain_wait(&ms.q2_full[t][buf], (a - 1) & 1);
-            if (b > 0) drain_wait(&ms.q2_full[t][buf], (b - 1) & 1);
+        // let the copies still in flight land: the last use of every slot and Q buffer
+        for (; turn & 3; ++turn) {
+          const Seq next = s1;
+          s1 = s2;
+          s2 = s3;
+          s3 = cur;
+          cur = next;
+        }
+        auto drain = [&](const Seq& s, bool is_v, int t) {
+          for (uint32_t n = s.n > kS / 4 ? s.n - kS / 4 : 0; n < s.n; ++n) {
+            const uint32_t it = own_item<kS>(before, is_v, t, n);
+            drain_wait(&ms.kv_full[it % kS], (it / kS) & 1);
           }
+          if (kHeads == 0 || is_v) return;
+          const int items = s.k - k0 - (s.over ? 1 : 0);
+          for (int i = max(items - 2, 0); i < items; ++i)
+            drain_wait(&ms.q2_full[t][i & 1], (i >> 1) & 1);
+        };
+        drain(cur, false, 0);
+        drain(s1, false, 1);
+        drain(s2, true, 0);
+        drain(s3, true, 1);
       }
     }
     if (abort_set(abort_flag)) {
@@ -1505,110 +1634,137 @@ __global__ void __launch_bounds__(kModThreads, 1)
     // of K and V set the pace here.
     if constexpr (kSplit) {
       const uint32_t ring = 2u * tiles;
-      struct Chain {
-        int k, left;        // next item; tiles left of this one
-        int due;            // P V: 0 none; bit 0: due; 1: accumulate; 2: the item's last
-        int due_steps;      // its 16-key steps
-        uint32_t due_item;  // its item's number: team = number % 2
-        uint32_t v_item;    // ring item of its V
-        uint32_t items;     // items taken so far (their Qs)
-        uint32_t pv0, pv1;  // P V issued (keys as rows: for either team)
-        int last_keys;      // keys in the item's last tile
-        uint32_t step;      // tiles of the run done
-        uint32_t other;     // tiles of the other run
-        bool over;
-      };
-      Chain cur = {k, 0, 0, 0, 0, 0, kHeads > 0 ? 0 : qs0, kHeads > 0 ? 0 : steps0,
-                   0, 0, 0, 0, false};
-      Chain other = {k, 0, 0, 0, 0, 0, kHeads > 0 ? 0 : qs1, kHeads > 0 ? 0 : steps1,
-                     0, 0, 0, 0, false};
-#pragma unroll 1
-      for (int t = 0; ok && !(cur.over && other.over && !cur.due && !other.due); t ^= 1) {
-        const uint32_t base = tmem + t * kTileCols, q_desc = desc_k + kQ0 + t * kTileDesc;
-        auto issue_due = [&]() {
-          const uint32_t iv = cur.v_item, team = cur.due_item & 1;
-          ok = wait(&ms.kv_full[iv % kS], iv / kS) &&
-               wait(kHeads > 0 ? &ms.p2_full[t][team] : &ms.p_full[t],
-                    kHeads > 0 && team ? cur.pv1 : cur.pv0);
-          if (!ok) return;
-          if (kHeads > 0 && team)
-            ++cur.pv1;
-          else
-            ++cur.pv0;
-          tc_fence_after();
-          const uint32_t v_desc = desc_k + (iv % kS) * kTileDesc, acc = (cur.due >> 1) & 1u;
-          if constexpr (kHeads > 0)
-            SwapMma<D>::template o<kColO>(base + team * kTeamCols, v_desc,
-                                          q_desc + ((kSwapP + team * kTeamP) >> 4), acc,
-                                          cur.due_steps);
-          else
-            issue_pv(t, v_desc, acc);
-          mma_commit(&ms.kv_empty[iv % kS]);
-          if (cur.due & 4) mma_commit(kHeads > 0 ? &ms.o2_done[t][team] : &ms.o_done[t]);
-          cur.due = 0;
+      if constexpr (kHeads > 0) {
+        // S^T = K Q^T of either run, whenever its K and Q are there and the team's S is
+        // free; the teams multiply with V themselves.
+        struct Chain {
+          int k, left;     // next item; tiles left of this one
+          uint32_t items;  // items taken: the next one's team = items % 2
+          uint32_t n;      // S issued
+          uint32_t s0, s1; // of them for either team
+          bool over;
         };
-        // A new item's S (the other team's, in columns of its own) need not wait for the
-        // weights of the last one, if its K is there already.  (And the last one's
-        // V: the ring slot that the new item's V will have is then in that V's
-        // phase, as the team that may clear its edge relies on.)
-        const uint32_t ahead_k = ring + own_ring_k(cur.step, cur.other, t);
-        const bool ahead =
-            kHeads > 0 && cur.due && !cur.over && cur.left == 0 &&
-            warp_all(mbar_test(&ms.kv_full[ahead_k % kS], (ahead_k / kS) & 1u) &&
-                     mbar_test(&ms.kv_full[cur.v_item % kS], (cur.v_item / kS) & 1u));
-        if (cur.due && !ahead) issue_due();
-        if (!ok) break;
-        if (!cur.over) {
-          const bool first = cur.left == 0;
-          const int had = cur.due;
-          int next_due = 0, next_steps = 0;
-          uint32_t next_v = 0;
-          if (first) {
-            ok = work_wait<kSlots>(ms, p, t, cur.k, abort_flag, kErrWaitMma);
-            if (!ok) break;
-            const Work& w = ms.work[t][cur.k % kSlots];
-            cur.left = w.n;
-            cur.last_keys = min(w.hi - (w.tile0 + w.n - 1) * kBN, kBN);
-            cur.other = w.other;
-            work_done<kSlots>(ms, t, cur.k++, lane);
-            cur.over = cur.left < 0;
-            if (!cur.over) {
-              const uint32_t i = cur.items++;
-              ok = kHeads > 0 ? wait(&ms.q2_full[t][i & 1], i >> 1) : wait(&ms.q_full[t], i);
+        Chain cur = {k, 0, 0, 0, 0, 0, false}, other = cur;
+        uint32_t idle = 0, t0 = 0;
+        auto ready = [&](uint64_t* bar, uint32_t phase) {
+          return warp_all(mbar_test(bar, phase & 1u));
+        };
+#pragma unroll 1
+        for (int t = 0; !(cur.over && other.over); t ^= 1) {
+          bool did = false;
+          if (!cur.over) {
+            const bool first = cur.left == 0;
+            const int slot = cur.k % kSlots;
+            const uint32_t team = (first ? cur.items : cur.items - 1u) & 1;
+            const uint32_t used = team ? cur.s1 : cur.s0;
+            const uint32_t ik = own_item<kS>(ring, false, t, cur.n);
+            bool go = !first || ready(&ms.work_full[t][slot], cur.k / kSlots);
+            int n = cur.left;
+            if (go && first) {
+              n = ms.work[t][slot].n;
+              if (n < 0) {
+                work_done<kSlots>(ms, t, cur.k, lane);
+                cur.over = did = true;
+                go = false;
+              } else {
+                go = ready(&ms.q2_full[t][team], cur.items >> 1);
+              }
+            }
+            if (go && (used == 0 || ready(&ms.s2_read[t][team], used - 1)) &&
+                ready(&ms.kv_full[ik % kS], ik / kS)) {
+              tc_fence_after();
+              SwapMma<D>::template s<kColS>(
+                  tmem + t * kTileCols + team * kTeamCols, desc_k + (ik % kS) * kTileDesc,
+                  desc_k + kQ0 + t * kTileDesc + team * (kTeamQ >> 4));
+              mma_commit(&ms.s2_full[t][team]);
+              mma_commit(&ms.kv_empty[ik % kS]);
+              if (n == 1) mma_commit(&ms.q2_empty[t][team]);
+              if (first) {
+                work_done<kSlots>(ms, t, cur.k++, lane);
+                ++cur.items;
+              }
+              if (team)
+                ++cur.s1;
+              else
+                ++cur.s0;
+              ++cur.n;
+              cur.left = n - 1;
+              did = true;
             }
           }
-          if (!cur.over) {
-            const uint32_t ik = ring + own_ring_k(cur.step, cur.other, t);
-            const uint32_t team = (cur.items - 1u) & 1;
-            ok = ok && wait(&ms.kv_full[ik % kS], ik / kS);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t bk = desc_k + (ik % kS) * kTileDesc;
-            if constexpr (kHeads > 0)
-              SwapMma<D>::template s<kColS>(base + team * kTeamCols, bk,
-                                            q_desc + team * (kTeamQ >> 4));
-            else
-              issue_s_steps<D, false, kColS, kQ0, 0, 0>(base, desc_k + t * kTileDesc, bk);
-            mma_commit(kHeads > 0 ? &ms.s2_full[t][team] : &ms.s_full[t]);
-            mma_commit(&ms.kv_empty[ik % kS]);
-            const bool last = cur.left == 1;
-            if (last) mma_commit(kHeads > 0 ? &ms.q2_empty[t][team] : &ms.q_empty[t]);
-            next_v = ik + own_ring_v(cur.step, cur.other);
-            ++cur.step;
-            next_due = 1 | (first ? 0 : 2) | (last ? 4 : 0);
-            next_steps = last ? (cur.last_keys + 15) / 16 : kBN / 16;
-            --cur.left;
+          const Chain next = other;
+          other = cur;
+          cur = next;
+          // as mod_wait: give up on an abort or after the time limit
+          idle = did ? 0 : idle + 1;
+          if (idle && (idle & 255u) == 0u) {
+            uint32_t now;
+            asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+            if (idle == 256u) t0 = now;
+            const bool late = now - t0 > static_cast<uint32_t>(p.wait_limit_ns);
+            if (!warp_all(!abort_set(abort_flag))) break;
+            if (!warp_all(!late)) {
+              abort_raise(abort_flag);
+              if (lane == 0) atomicOr(p.err, kErrWaitMma);
+              break;
+            }
           }
-          if (had) issue_due();
-          if (!ok) break;
-          cur.due = next_due;
-          cur.due_steps = next_steps;
-          cur.v_item = next_v;
-          cur.due_item = cur.items - 1u;
         }
-        const Chain next = other;
-        other = cur;
-        cur = next;
+      } else {
+        struct Chain {
+          int k, left;      // next item; tiles left of this one
+          int due;          // P V: 0 none; bit 0: due; 1: accumulate; 2: the item's last
+          uint32_t v_item;  // ring item of its V
+          uint32_t q, pv;   // Q taken, P V issued
+          uint32_t n;       // S issued
+          bool over;
+        };
+        Chain cur = {k, 0, 0, 0, qs0, steps0, 0, false}, other = {k, 0, 0, 0, qs1, steps1, 0, false};
+#pragma unroll 1
+        for (int t = 0; ok && !(cur.over && other.over && !cur.due && !other.due); t ^= 1) {
+          if (cur.due) {
+            const uint32_t iv = cur.v_item;
+            ok = wait(&ms.kv_full[iv % kS], iv / kS) && wait(&ms.p_full[t], cur.pv);
+            if (!ok) break;
+            ++cur.pv;
+            tc_fence_after();
+            issue_pv(t, desc_k + (iv % kS) * kTileDesc, (cur.due >> 1) & 1u);
+            mma_commit(&ms.kv_empty[iv % kS]);
+            if (cur.due & 4) mma_commit(&ms.o_done[t]);
+            cur.due = 0;
+          }
+          if (!cur.over) {
+            const bool first = cur.left == 0;
+            if (first) {
+              ok = work_wait<kSlots>(ms, p, t, cur.k, abort_flag, kErrWaitMma);
+              if (!ok) break;
+              cur.left = ms.work[t][cur.k % kSlots].n;
+              work_done<kSlots>(ms, t, cur.k++, lane);
+              cur.over = cur.left < 0;
+              if (!cur.over) ok = wait(&ms.q_full[t], cur.q++);
+            }
+            if (!cur.over) {
+              const uint32_t ik = own_item<kS>(ring, false, t, cur.n);
+              ok = ok && wait(&ms.kv_full[ik % kS], ik / kS);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s_steps<D, false, kColS, kQ0, 0, 0>(tmem + t * kTileCols,
+                                                        desc_k + t * kTileDesc,
+                                                        desc_k + (ik % kS) * kTileDesc);
+              mma_commit(&ms.s_full[t]);
+              mma_commit(&ms.kv_empty[ik % kS]);
+              const bool last = cur.left == 1;
+              if (last) mma_commit(&ms.q_empty[t]);
+              cur.v_item = own_item<kS>(ring, true, t, cur.n);
+              ++cur.n;
+              cur.due = 1 | (first ? 0 : 2) | (last ? 4 : 0);
+              --cur.left;
+            }
+          }
+          const Chain next = other;
+          other = cur;
+          cur = next;
+        }
       }
     }
     // all issued MMAs retire before the CTA releases TMEM
