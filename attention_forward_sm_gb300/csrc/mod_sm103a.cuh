@@ -1279,26 +1279,21 @@ __global__ void __launch_bounds__(kModThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       return warp_all(mod_wait(bar, phase & 1u, abort_flag, p.err, kErrWaitLoad, p.wait_limit_ns));
     };
-    // A K or V tile into the ring: a box of 128 keys, or (a request's own keys) as
-    // many of 32 as hold keys: little of a cache's unused tail is read
-    auto load_tile = [&](const CUtensorMap* map, int key, int box_keys, int boxes, int bh,
-                         uint64_t policy) {
+    // a K or V tile into the ring
+    auto load_tile = [&](const CUtensorMap* map, int key, int bh, uint64_t policy) {
       const uint32_t s = g % kS;
       if (!wait(&ms.kv_empty[s], (g / kS) + 1)) return false;
-      mbar_arrive_expect_tx_elect(&ms.kv_full[s], boxes * box_keys * (C::kChunks * 128));
+      mbar_arrive_expect_tx_elect(&ms.kv_full[s], C::kTileBytes);
       uint8_t* dst = smem + C::kOffKV + s * C::kTileBytes;
-#pragma unroll 1
-      for (int i = 0; i < boxes; ++i) {
 #pragma unroll
-        for (int ch = 0; ch < C::kChunks; ++ch)
-          tma_load_3d_elect(dst + ch * (kBM * 128) + i * (32 * 128), map, &ms.kv_full[s],
-                            ch * C::kAtomElems, key + 32 * i, bh, policy);
-      }
+      for (int ch = 0; ch < C::kChunks; ++ch)
+        tma_load_3d_elect(dst + ch * (kBM * 128), map, &ms.kv_full[s], ch * C::kAtomElems, key, bh,
+                          policy);
       ++g;
       return true;
     };
-    // Q_t, once its last Q K^T (or copy to TMEM) read it
-    auto load_q = [&](int t, int kind, int id, int q0) {
+    // Q_t of an item of two query tiles, once its last Q K^T (or copy to TMEM) read it
+    auto load_q = [&](int t, int id, int q0) {
       const uint32_t before = t ? q1_loads : q0_loads;
       if (before > 0 && !wait(&ms.q_empty[t], before - 1)) return false;
       if (t)
@@ -1307,12 +1302,10 @@ __global__ void __launch_bounds__(kModThreads, 1)
         ++q0_loads;
       uint8_t* dst = smem + C::kOffQ + t * C::kTileBytes;
       if constexpr (kSplit) {
-        const uint32_t rows = (kind ? 1 : p.per_tile) * p.G;
-        mbar_arrive_expect_tx_elect(&ms.q_full[t], C::kChunks * rows * 128);
+        mbar_arrive_expect_tx_elect(&ms.q_full[t], C::kChunks * p.per_tile * p.G * 128);
         for (int ch = 0; ch < C::kChunks; ++ch)
-          tma_load_4d_elect(dst + ch * (kBM * 128), kind ? &p.tmap_q1 : &p.tmap_q, &ms.q_full[t],
-                            ch * C::kAtomElems, 0, id, q0 + (kind ? 0 : t * p.per_tile),
-                            l2_policy_evict_last());
+          tma_load_4d_elect(dst + ch * (kBM * 128), &p.tmap_q, &ms.q_full[t], ch * C::kAtomElems, 0,
+                            id, q0 + t * p.per_tile, l2_policy_evict_last());
       } else {
         mbar_arrive_expect_tx_elect(&ms.q_full[t], C::kTileBytes);
         for (int ch = 0; ch < C::kChunks; ++ch)
@@ -1351,154 +1344,133 @@ __global__ void __launch_bounds__(kModThreads, 1)
       for (int i = 0; i < 2 * n && ok; ++i) {  // K, V, K, V, ..
         ok = load_tile((i & 1) ? (kSplit ? &p.tmap_vp : &p.tmap_v)
                                : (kSplit ? &p.tmap_kp : &p.tmap_k),
-                       (tile0 + (i >> 1)) * kBN, kBN, 1, bh, policy);
+                       (tile0 + (i >> 1)) * kBN, bh, policy);
         if (i == 0) {
-          ok = ok && (!use0 || load_q(0, 0, id, q0));
-          ok = ok && (!use1 || load_q(1, 0, id, q0));
+          ok = ok && (!use0 || load_q(0, id, q0));
+          ok = ok && (!use1 || load_q(1, id, q0));
         }
       }
     }
     // ---- decode: the two runs of own keys, a tile of either in turn
     if constexpr (kSplit) {
-      // K of query tile 0, of 1, V of 0, of 1: four sequences of tiles that go
-      // through the same code in turn, each issued when its ring slot is free.
-      struct Seq {
-        int k, left;       // next item; tiles left of this one
-        int key, hi, bh;   // next key, the item's end, row of the cache
-        uint32_t n;        // tiles issued
-        bool over;
-      };
+      // K of query tile 0, of 1, V of 0, of 1: four sequences of tiles, one a lane,
+      // each issued when its ring slot is free.
       const uint32_t before = g;  // ring items of the prefix
-      const int k0 = k;
+      const int t = lane & 1;
+      const bool is_v = (lane & 2) != 0;
+      int item = 0, left = 0;         // next item's number; tiles left of this one
+      int key = 0, hi = 0, bh = 0;    // next key, the item's end, row of the cache
+      uint32_t n = 0;                 // tiles issued
+      bool over = lane >= 4;
+      // (an item's Q comes with its first K; the buffer has to be free of the item
+      // two, without buffers by team one, before, and of the prefix items' Q)
+      const uint32_t loads = t ? q1_loads : q0_loads;
       const uint64_t policy = l2_policy_evict_first();  // every byte is read once
-      Seq cur = {k, 0, 0, 0, 0, 0, false}, s1 = cur, s2 = cur, s3 = cur;
       uint32_t idle = 0, t0 = 0;
-      auto ready = [&](uint64_t* bar, uint32_t phase) {
-        return warp_all(mbar_test(bar, phase & 1u));
-      };
-      int turn = 0;
 #pragma unroll 1
-      for (; !(cur.over && s1.over && s2.over && s3.over); ++turn) {
-        const int t = turn & 1;
-        const bool is_v = (turn & 2) != 0;
+      for (;;) {
+        const int k_item = __shfl_sync(0xFFFFFFFFu, item, t);  // V follows K's items
+        const uint32_t it = own_item<kS>(before, is_v, t, n);
         bool did = false;
-        if (!cur.over) {
-          // s2 is the other sequence of this query tile: V follows K's items, and
-          // gives their slots free
-          const int slot = cur.k % kSlots;
-          const bool fresh = cur.left == 0;
-          bool go = !fresh || (is_v ? cur.k < s2.k
-                                    : ready(&ms.work_full[t][slot], cur.k / kSlots));
-          if (go && fresh) {
-            const Work& w = ms.work[t][slot];
-            if (w.n < 0) {
-              cur.over = true;
-              ++cur.k;
-              if (is_v) work_done<kSlots>(ms, t, cur.k - 1, lane);
-              go = false;
-              did = true;
-            } else {
-              cur.key = w.tile0 * kBN;
-              cur.hi = w.hi;
-              cur.bh = w.q0 * p.Hkv + w.id;
+        if (!over && mbar_test(&ms.kv_empty[it % kS], ((it / kS) + 1) & 1u)) {
+          const bool fresh = left == 0;
+          const int at = k + item, slot = at % kSlots;
+          bool go = true;
+          if (fresh) {
+            go = is_v ? item < k_item
+                      : mbar_test(&ms.work_full[t][slot], (at / kSlots) & 1u);
+            if (go) {
+              const Work& w = ms.work[t][slot];
+              if (w.n < 0) {
+                over = did = true;
+                go = false;
+                ++item;
+                if (is_v) mbar_arrive(&ms.work_empty[t][slot]);
+              } else if (!is_v) {
+                if (kHeads > 0 && item >= 2)
+                  go = mbar_test(&ms.q2_empty[t][item & 1], ((item >> 1) + 1) & 1u);
+                else if (kHeads > 0)
+                  go = loads == 0 || mbar_test(&ms.q_empty[t], (loads - 1) & 1u);
+                else
+                  go = loads + item == 0 || mbar_test(&ms.q_empty[t], (loads + item - 1) & 1u);
+              }
             }
-          }
-          const uint32_t it = own_item<kS>(before, is_v, t, cur.n);
-          go = go && ready(&ms.kv_empty[it % kS], it / kS + 1);
-          const uint32_t i = static_cast<uint32_t>(cur.k - k0);  // number of a fresh item
-          if (go && fresh && !is_v) {
-            // its Q's buffer: free of the item two (without buffers by team: one)
-            // before, and of the prefix items' Q
-            const uint32_t loads = t ? q1_loads : q0_loads;
-            if constexpr (kHeads > 0)
-              go = i >= 2 ? ready(&ms.q2_empty[t][i & 1], (i >> 1) + 1)
-                          : loads == 0 || ready(&ms.q_empty[t], loads - 1);
-            else
-              go = loads == 0 || ready(&ms.q_empty[t], loads - 1);
           }
           if (go) {
             const Work& w = ms.work[t][slot];
-            if (fresh) cur.left = w.n;
-            const int boxes = (min(cur.hi - cur.key, kBN) + 31) / 32;
+            if (fresh) {
+              left = w.n;
+              key = w.tile0 * kBN;
+              hi = w.hi;
+              bh = w.q0 * p.Hkv + w.id;
+            }
+            // as many boxes of 32 keys as hold keys: little of a cache's unused tail is read
+            const int boxes = (min(hi - key, kBN) + 31) / 32;
             const CUtensorMap* map = is_v ? &p.tmap_v : &p.tmap_k;
             uint64_t* full = &ms.kv_full[it % kS];
             uint8_t* dst = smem + C::kOffKV + (it % kS) * C::kTileBytes;
-            mbar_arrive_expect_tx_elect(full, boxes * 32 * (C::kChunks * 128));
+            mbar_arrive_expect_tx(full, boxes * 32 * (C::kChunks * 128));
 #pragma unroll 1
             for (int x = 0; x < boxes; ++x) {
 #pragma unroll
               for (int ch = 0; ch < C::kChunks; ++ch)
-                tma_load_3d_elect(dst + ch * (kBM * 128) + x * (32 * 128), map, full,
-                                  ch * C::kAtomElems, cur.key + 32 * x, cur.bh, policy);
+                tma_load_3d(dst + ch * (kBM * 128) + x * (32 * 128), map, full,
+                            ch * C::kAtomElems, key + 32 * x, bh, policy);
             }
             if (fresh && !is_v) {
-              if constexpr (kHeads > 0) {
-                uint8_t* q = smem + C::kOffQ + t * C::kTileBytes + (i & 1) * kTeamQ;
-                mbar_arrive_expect_tx_elect(&ms.q2_full[t][i & 1], C::kChunks * p.G * 128);
-                for (int ch = 0; ch < C::kChunks; ++ch)
-                  tma_load_4d_elect(q + ch * (kBM * 128), &p.tmap_q1, &ms.q2_full[t][i & 1],
-                                    ch * C::kAtomElems, 0, w.id, w.q0, l2_policy_evict_last());
-              } else {
-                load_q(t, 1, w.id, w.q0);
-              }
+              const int buf = kHeads > 0 ? item & 1 : 0;
+              uint64_t* q_full = kHeads > 0 ? &ms.q2_full[t][buf] : &ms.q_full[t];
+              uint8_t* q = smem + C::kOffQ + t * C::kTileBytes + buf * kTeamQ;
+              mbar_arrive_expect_tx(q_full, C::kChunks * p.G * 128);
+#pragma unroll
+              for (int ch = 0; ch < C::kChunks; ++ch)
+                tma_load_4d(q + ch * (kBM * 128), &p.tmap_q1, q_full, ch * C::kAtomElems, 0, w.id,
+                            w.q0, l2_policy_evict_last());
             }
             if (fresh) {
-              if (is_v) work_done<kSlots>(ms, t, cur.k, lane);
-              ++cur.k;
+              if (is_v) mbar_arrive(&ms.work_empty[t][slot]);
+              ++item;
             }
-            cur.key += kBN;
-            --cur.left;
-            ++cur.n;
+            key += kBN;
+            --left;
+            ++n;
             did = true;
           }
         }
-        const Seq next = s1;
-        s1 = s2;
-        s2 = s3;
-        s3 = cur;
-        cur = next;
+        __syncwarp();
+        if (warp_all(over)) break;
         // as mod_wait: give up on an abort or after the time limit
-        idle = did ? 0 : idle + 1;
+        idle = warp_all(!did) ? idle + 1 : 0;
         if (idle && (idle & 255u) == 0u) {
           uint32_t now;
           asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
           if (idle == 256u) t0 = now;
           const bool late = now - t0 > static_cast<uint32_t>(p.wait_limit_ns);
-          const bool gone = !warp_all(!abort_set(abort_flag));
-          if (gone || !warp_all(!late)) {
-            if (!gone) {
-              abort_raise(abort_flag);
-              if (lane == 0) atomicOr(p.err, kErrWaitLoad);
-            }
-            ++turn;  // (the sequences have moved on)
+          if (!warp_all(!abort_set(abort_flag))) break;
+          if (!warp_all(!late)) {
+            abort_raise(abort_flag);
+            if (lane == 0) atomicOr(p.err, kErrWaitLoad);
             break;
           }
         }
       }
-      if (abort_set(abort_flag)) {
+      if (lane < 4 && abort_set(abort_flag)) {
         // let the copies still in flight land: the last use of every slot and Q buffer
-        for (; turn & 3; ++turn) {
-          const Seq next = s1;
-          s1 = s2;
-          s2 = s3;
-          s3 = cur;
-          cur = next;
+        for (uint32_t i = n > kS / 4 ? n - kS / 4 : 0; i < n; ++i) {
+          const uint32_t it = own_item<kS>(before, is_v, t, i);
+          drain_wait(&ms.kv_full[it % kS], (it / kS) & 1);
         }
-        auto drain = [&](const Seq& s, bool is_v, int t) {
-          for (uint32_t n = s.n > kS / 4 ? s.n - kS / 4 : 0; n < s.n; ++n) {
-            const uint32_t it = own_item<kS>(before, is_v, t, n);
-            drain_wait(&ms.kv_full[it % kS], (it / kS) & 1);
+        if (!is_v) {
+          const int items = item - (over ? 1 : 0);
+          if (kHeads > 0) {
+            for (int i = max(items - 2, 0); i < items; ++i)
+              drain_wait(&ms.q2_full[t][i & 1], (i >> 1) & 1);
+          } else if (items > 0) {
+            drain_wait(&ms.q_full[t], (loads + items - 1) & 1);
           }
-          if (kHeads == 0 || is_v) return;
-          const int items = s.k - k0 - (s.over ? 1 : 0);
-          for (int i = max(items - 2, 0); i < items; ++i)
-            drain_wait(&ms.q2_full[t][i & 1], (i >> 1) & 1);
-        };
-        drain(cur, false, 0);
-        drain(s1, false, 1);
-        drain(s2, true, 0);
-        drain(s3, true, 1);
+        }
       }
+      __syncwarp();
     }
     if (abort_set(abort_flag)) {
       // let the copies still in flight land before the CTA exits
