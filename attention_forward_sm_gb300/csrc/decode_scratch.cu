@@ -1,6 +1,7 @@
 // Partial-state scratch of the split decodes (attn_decode_splitkv, _states,
-// attn_decode_varlen, attn_decode_prefix): a small per-device cache of device buffers, one per recently used stream,
-// so that a decode step allocates nothing once its stream has been seen.
+// attn_decode_varlen, attn_decode_prefix): a small per-device cache of device
+// buffers, one per recently used stream, so that a decode step allocates nothing
+// once its stream has been seen.
 //
 // Why: a stream-ordered cudaMallocAsync + cudaFreeAsync pair around the two
 // decode kernels costs about 6 us of GPU time per call on GB300 (measured:
@@ -58,8 +59,8 @@ int plain_path(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cu
 
 }  // namespace
 
-int with_scratch(size_t bytes, int dev, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
-                 void* ctx) {
+int with_scratch(size_t bytes, int dev, cudaStream_t stream,
+                 int (*launch)(void*, void*, cudaStream_t), void* ctx) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
     cudaGetLastError();
@@ -80,7 +81,9 @@ int with_scratch(size_t bytes, int dev, cudaStream_t stream, int (*launch)(void*
   }
   for (Entry& x : c.e)
     if (x.live && x.stream == id) en = &x;
-  const bool same = en != nullptr;  // the buffer's previous use is in front of us on our stream
+  // is the buffer's previous use in front of us on our stream?  (The handle of
+  // the per-thread stream stands for another stream in every thread.)
+  const bool same = en != nullptr && stream != cudaStreamPerThread;
   if (!en) {
     // a free entry, else the least recently used one
     for (Entry& x : c.e)

@@ -63,7 +63,6 @@ constexpr int kClcReaders = 18;   // loader, MMA issuer, 16 softmax warps
 constexpr uint32_t kRegSoftmax = 112, kRegOther = 32;
 static_assert(4 * 128 * kRegSoftmax + 128 * kRegOther <= 640 * 96, "register split");
 
-
 struct Misc {
   uint64_t q_full;        // the unit's Q tiles arrived (one phase per unit)
   uint64_t q_empty;       // the unit's Q tiles were read (its last Q K^T, or with Q in

@@ -465,7 +465,8 @@ __device__ __forceinline__ Work plan_unit(const ModKernelParams& p, int u, int2*
   if (p.ranges) {
     // row lane + 32 i of the item; all loads before the first use
     constexpr int kRows = 2 * kBM / 32;
-    const int2* rg = reinterpret_cast<const int2*>(p.ranges) + static_cast<size_t>(bh / p.Hq) * p.Nq;
+    const int2* rg =
+        reinterpret_cast<const int2*>(p.ranges) + static_cast<size_t>(bh / p.Hq) * p.Nq;
     int2 r[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -919,7 +920,8 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
     tmem_ld_lane16(o_addr, o);
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
-      const float sum = (ms.red[id][0][n] + ms.red[id][1][n]) + (ms.red[id][2][n] + ms.red[id][3][n]);
+      const float sum =
+          (ms.red[id][0][n] + ms.red[id][1][n]) + (ms.red[id][2][n] + ms.red[id][3][n]);
       const bool none = sum == 0.f;
       const float inv = none ? 0.f : 1.f / sum;
       if (n < G) {
@@ -946,7 +948,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
   const uint32_t abort_flag = smem_u32(&ms.abort_flag);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- setup: barriers (load warp), TMEM (MMA warp)
+  // ---- set-up: barriers (load warp), TMEM (MMA warp)
   if (warp == kModWarpLoad && lane == 0) {
     mbar_init(&ms.unit_done, 1);
     for (int t = 0; t < 2; ++t) {
@@ -1683,7 +1685,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
           uint32_t n;       // S issued
           bool over;
         };
-        Chain cur = {k, 0, 0, 0, qs0, steps0, 0, false}, other = {k, 0, 0, 0, qs1, steps1, 0, false};
+        Chain cur = {k, 0, 0, 0, qs0, steps0, 0, false};
+        Chain other = {k, 0, 0, 0, qs1, steps1, 0, false};
 #pragma unroll 1
         for (int t = 0; ok && !(cur.over && other.over && !cur.due && !other.due); t ^= 1) {
           if (cur.due) {

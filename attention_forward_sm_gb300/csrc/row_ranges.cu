@@ -109,7 +109,8 @@ extern "C" int attn_row_ranges(const int* doc_lens, const int* prefix_lens, int*
                                int N, int M, int causal, cudaStream_t stream) {
   using namespace attn;
   if (!doc_lens || !ranges) return ATTN_ERR_NULL;
-  if (B < 1 || B > 65535 || N < 1 || N > (1 << 30) || M < 1) return ATTN_ERR_SHAPE;
+  if (B < 1 || B > 65535 || N < 1 || N > (1 << 30) || M < 1 || M > (1 << 30))
+    return ATTN_ERR_SHAPE;
   if (static_cast<long long>(B) * N >= (1ll << 40)) return ATTN_ERR_SHAPE;
   if ((reinterpret_cast<uintptr_t>(ranges) & 7u) || (reinterpret_cast<uintptr_t>(doc_lens) & 3u) ||
       (reinterpret_cast<uintptr_t>(prefix_lens) & 3u))

@@ -31,11 +31,6 @@ __device__ __forceinline__ float tanh_any(float x) {
   return fabsf(x) <= 1.f ? tanh_poly(x) : (x == x ? far : x);
 }
 
-// Score in log2 units from the raw product s = <q, k>, without the bias.
-__device__ __forceinline__ float mod_score(const ScoreMod& m, float s) {
-  return m.cap_in > 0.f ? tanh_any(s * m.cap_in) * m.cap_out : s * (m.scale * kLog2e);
-}
-
 // The bias is taken relative to the visible key that it favours, at distance
 // ref: the nearest one for a slope >= 0, the farthest one otherwise.  Scores
 // then keep their fp32 digits however far all visible keys are, and the LSE

@@ -191,8 +191,9 @@ int attn_fwd_fp8(const void *q, const void *k, const void *vt, void *o, float *l
  * library keeps per stream: on each device it remembers the last 8 streams
  * it decoded on, each with one buffer taken from the stream-ordered
  * allocator, grown when a call needs more and otherwise reused, so a
- * repeated decode step allocates nothing.  Each use waits (on the GPU) for
- * the buffer's previous use, so calls never share scratch while running.
+ * repeated decode step allocates nothing.  Each use comes after the buffer's
+ * previous one (by stream order, or waiting for it on the GPU where another
+ * stream made it), so calls never share scratch while running.
  * The buffers stay allocated until the process exits or their entry passes
  * to another stream.  During stream capture a call allocates its scratch on
  * the stream and frees it after the combine instead (the graph owns it).
@@ -327,8 +328,8 @@ int attn_decode_graph_destroy(attn_decode_graph *graph);
  * Keys that a row does not see have no influence on it, whatever K holds
  * there.  V may hold anything (also NaN) at keys that no row of its
  * (batch, KV head) sees on either side of the visible span, such as padding
- * or the unused tail of a cache; a NaN or infinity in V at a key that some
- * rows see may reach the other rows of the same (batch, KV head) too.
+ * or the unused tail of a cache; a NaN or infinity in V at a key inside the
+ * span may reach all rows of the same (batch, KV head).
  */
 
 /*
@@ -361,8 +362,8 @@ int attn_fwd_mod(const void *q, const void *k, const void *v, void *o, float *ls
  * [s, max(i + 1, min(s + prefix, e))).  Documents are cut at N; tokens behind
  * the last document get the empty range [0, 0).
  *
- * Limits: 1 <= B <= 65535, 1 <= N <= 2^30, M >= 1, B * N < 2^40; ranges
- * 8-byte, the lengths 4-byte aligned.
+ * Limits: 1 <= B <= 65535, 1 <= N <= 2^30, 1 <= M <= 2^30, B * N < 2^40;
+ * ranges 8-byte, the lengths 4-byte aligned.
  */
 int attn_row_ranges(const int *doc_lens, const int *prefix_lens, int *ranges, int B, int N, int M,
                     int causal, cudaStream_t stream);
@@ -384,7 +385,8 @@ int attn_row_ranges(const int *doc_lens, const int *prefix_lens, int *ranges, in
  *
  * Limits: B, Hq, Hkv, Ncap >= 1; Hq % Hkv == 0; Hq / Hkv <= 128; D in
  * {64, 128}; B * Hkv <= 2^20, Hq <= 65535; Ncap <= 2^30, and at most 12e6
- * tiles of 128 keys in all: B * Hkv * ceil(Ncap / 128); scale finite and >= 0; the bf16 pointers and lse 16-byte, lens and slopes 4-byte aligned.
+ * tiles of 128 keys in all: B * Hkv * ceil(Ncap / 128); scale finite and >= 0;
+ * the bf16 pointers and lse 16-byte, lens and slopes 4-byte aligned.
  * Scratch as attn_decode_splitkv: one buffer per recently used stream, none
  * allocated by a repeated call; during capture a buffer of the graph's own.
  */

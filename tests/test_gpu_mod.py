@@ -588,3 +588,94 @@ def test_helpers_refuse_wrong_tensors():
     for error, call in bad:
         with pytest.raises(error):
             call()
+
+
+def _guarded(shape, dtype, lead):
+    """A buffer of one value around the tensor that is returned with it; the
+    tensor starts `lead` bytes behind a 512-byte boundary."""
+    size = math.prod(shape)
+    each = torch.empty((), dtype=dtype).element_size()
+    whole = torch.full((1024 + size + 1024,), 7.0, dtype=dtype, device="cuda")
+    start = 512 + lead // each
+    return whole, whole[start:start + size].view(shape), start
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lead", [0, 16])
+def test_only_the_outputs_are_written(D, lead):
+    """The C calls with outputs inside larger buffers, 32-byte aligned or only
+    16-byte aligned: the same bits, and nothing around them changes."""
+    B, Hq, Hkv, N = 2, 4, 2, 301
+    x, kv = rand(1, (B, Hq, N, D)), rand(2, (B, Hkv, N, D))
+    want = attn.forward_mod(x, kv, kv, causal=True, softcap=20.0)
+    wo, o, at_o = _guarded((B, Hq, N, D), torch.bfloat16, lead)
+    wl, lse, at_l = _guarded((B, Hq, N), torch.float32, lead)
+    attn.attn_fwd_mod(x, kv, kv, o, lse, B, Hq, Hkv, N, N, D, 1, 0, D ** -0.5, 20.0)
+    q, lens = x[:, :, 0].contiguous(), torch.tensor([301, 77], dtype=torch.int32, device="cuda")
+    want_d = attn.decode_varlen(q, kv, kv, lens, softcap=20.0)
+    wod, od, at_od = _guarded((B, Hq, D), torch.bfloat16, lead)
+    wld, ld, at_ld = _guarded((B, Hq), torch.float32, lead)
+    attn.attn_decode_varlen(q, kv, kv, lens, od, ld, B, Hq, Hkv, N, D, D ** -0.5, 20.0)
+    wr, ranges, at_r = _guarded((B, N, 2), torch.int32, lead)
+    docs = torch.tensor([[100, 150], [301, 0]], dtype=torch.int32, device="cuda")
+    attn.attn_row_ranges(docs, None, ranges, B, N, 2, 1)
+    torch.cuda.synchronize()
+    assert torch.equal(ranges, attn.row_ranges(docs, N))
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert torch.equal(od, want_d[0]) and torch.equal(ld, want_d[1])
+    for whole, out, at in ((wo, o, at_o), (wl, lse, at_l), (wod, od, at_od), (wld, ld, at_ld), (wr, ranges, at_r)):
+        assert bool((whole[:at] == 7).all()) and bool((whole[at + out.numel():] == 7).all())
+
+
+def test_the_same_call_gives_the_same_bits():
+    """Whatever the order in which blocks run: prefill of ragged documents and
+    decodes whose keys are cut in parts."""
+    x = rand(1, (2, 8, 1500, 128))
+    kv = rand(2, (2, 2, 1500, 128))
+    r = attn.row_ranges(torch.tensor([[700, 20, 500], [3, 1400, 0]], dtype=torch.int32, device="cuda"), 1500)
+    q = rand(3, (40, 8, 128))
+    c = rand(4, (40, 2, 700, 128))
+    p = rand(5, (2, 5000, 128))
+    lens = torch.tensor([(37 * i) % 701 for i in range(40)], dtype=torch.int32, device="cuda")
+    calls = (lambda: attn.forward_mod(x, kv, kv, ranges=r, softcap=30.0, slopes=alibi(8)),
+             lambda: attn.decode_varlen(q, c, c, lens),
+             lambda: attn.decode_prefix(q, p, p, c, c, lens, slopes=alibi(8)))
+    for call in calls:
+        first = call()
+        for _ in range(5):
+            again = call()
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_threads_with_streams_of_their_own_under_one_handle():
+    """The per-thread default stream: one handle, another stream in each thread."""
+    import threading
+    per_thread = 2  # cudaStreamPerThread
+    B, Hq, Hkv, Ncap, D = 4, 8, 2, 2000, 64
+    lib, done = attn.load(), {}
+    sets = []
+    for i in range(3):
+        lens = [1900 - 300 * i, 5 + i, 0, 777]
+        sets.append((rand(i, (B, Hq, D)), rand(10 + i, (B, Hkv, Ncap, D)), rand(20 + i, (B, Hkv, Ncap, D)), lens,
+                     torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                     [(torch.empty((B, Hq, D), dtype=torch.bfloat16, device="cuda"),
+                       torch.empty((B, Hq), device="cuda")) for _ in range(20)]))
+    torch.cuda.synchronize()
+
+    def work(i):
+        q, k, v, _, t, outs = sets[i]
+        torch.cuda.set_device(0)
+        done[i] = [lib.attn_decode_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), t.data_ptr(), o.data_ptr(),
+                                          lse.data_ptr(), B, Hq, Hkv, Ncap, D, 0.125, 0.0, None, per_thread)
+                   for o, lse in outs]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i, (q, k, v, lens, _, outs) in enumerate(sets):
+        assert done[i] == [0] * 20
+        for o, lse in outs:
+            check_decode(o, lse, q, k, v, lens, 0.0, None)

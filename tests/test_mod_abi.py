@@ -59,8 +59,8 @@ def test_fwd_mod_refusals(lib, change, status):
 
 RANGES = [(dict(doc_lens=0), NULL), (dict(ranges=0), NULL), (dict(B=0), SHAPE), (dict(B=65536), SHAPE),
           (dict(N=0), SHAPE), (dict(N=2**30 + 1), SHAPE), (dict(M=0), SHAPE),
-          (dict(B=2048, N=2**30), SHAPE), (dict(ranges=A + 4), ALIGN), (dict(doc_lens=A + 1), ALIGN),
-          (dict(prefix_lens=A + 2), ALIGN)]
+          (dict(M=2**30 + 1), SHAPE), (dict(B=2048, N=2**30), SHAPE), (dict(ranges=A + 4), ALIGN),
+          (dict(doc_lens=A + 1), ALIGN), (dict(prefix_lens=A + 2), ALIGN)]
 
 
 @pytest.mark.parametrize("change,status", RANGES, ids=_ids(RANGES))
