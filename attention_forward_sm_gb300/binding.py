@@ -460,6 +460,14 @@ def _side_launch(fn, args, dev: int, stream, used):
                     x.record_stream(side)
 
 
+# The first call of each of these two puts the quickest way there is in its place.
+def _current_device() -> int:
+    global _current_device
+    torch = _import_torch()
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
+
+
 def _raw_stream(dev: int) -> int:
     global _raw_stream
     _raw_stream = getattr(_import_torch()._C, "_cuda_getCurrentRawStream", _current_raw_stream)
@@ -495,14 +503,15 @@ def forward_mod(q, k, v, *, causal: bool = False, scale: float | None = None,
                        "Hkv": (k.shape[1], v.shape[1]), "Nk": (k.shape[2], v.shape[2])})
         _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)),
                    ranges=(ranges, torch.int32, (B, Nq, 2)))
-    o = torch.empty_like(q)
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+    device = q.device
+    o = torch.empty_strided((B, Hq, Nq, D), (Hq * Nq * D, Nq * D, D, 1), dtype=bf16, device=device)
+    lse = torch.empty_strided((B, Hq, Nq), (Hq * Nq, Nq, 1), dtype=torch.float32, device=device)
     fn = (_lib or load()).attn_fwd_mod
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
             Nq, Nk, D, bool(causal), q_offset, D ** -0.5 if scale is None else scale, softcap,
             None if slopes is None else slopes.data_ptr(),
             None if ranges is None else ranges.data_ptr())
-    if stream is None and torch.cuda.current_device() == dev:
+    if stream is None and _current_device() == dev:
         rc = fn(*args, _raw_stream(dev))
         if rc:
             _check(rc)
@@ -518,18 +527,22 @@ def row_ranges(doc_lens, N: int, *, prefix_lens=None, causal: bool = True, strea
     document's bidirectional prefix (``prefix_lens`` [B, M] int32).  Tokens
     behind the last document (padding) see nothing."""
     torch = _torch or _import_torch()
-    _check_ranks({"doc_lens": doc_lens}, {"doc_lens": 2})
-    B, M = doc_lens.shape
-    dev = doc_lens.get_device()
-    if dev < 0 or _aux_bad(doc_lens, torch.int32, (B, M), dev) \
-            or prefix_lens is not None and _aux_bad(prefix_lens, torch.int32, (B, M), dev):
-        _check_aux(doc_lens.device, doc_lens=(doc_lens, torch.int32, (B, M)),
-                   prefix_lens=(prefix_lens, torch.int32, (B, M)))
-    out = torch.empty((B, N, 2), dtype=torch.int32, device=doc_lens.device)
+    i32 = torch.int32
+    try:
+        B, M = doc_lens.shape
+        dev = doc_lens.get_device()
+        fine = dev >= 0 and doc_lens.dtype is i32 and doc_lens.is_contiguous()
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine or prefix_lens is not None and _aux_bad(prefix_lens, i32, (B, M), dev):
+        _check_ranks({"doc_lens": doc_lens}, {"doc_lens": 2})
+        _check_aux(doc_lens.device, doc_lens=(doc_lens, i32, (B, M)),
+                   prefix_lens=(prefix_lens, i32, (B, M)))
+    out = torch.empty((B, N, 2), dtype=i32, device=doc_lens.device)
     fn = (_lib or load()).attn_row_ranges
     args = (doc_lens.data_ptr(), None if prefix_lens is None else prefix_lens.data_ptr(),
             out.data_ptr(), B, N, M, bool(causal))
-    if stream is None and torch.cuda.current_device() == dev:
+    if stream is None and _current_device() == dev:
         rc = fn(*args, _raw_stream(dev))
         if rc:
             _check(rc)
@@ -569,8 +582,9 @@ def _decode(fn, q, pre, kcache, vcache, lens, scale, softcap, slopes, stream):
                            "Np": (pre[0].shape[1], pre[1].shape[1]),
                            "D": (D, pre[0].shape[2], pre[1].shape[2])})
         _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)), lens=(lens, torch.int32, (B,)))
-    o = torch.empty_like(q)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    device = q.device
+    o = torch.empty_strided((B, Hq, D), (Hq * D, D, 1), dtype=bf16, device=device)
+    lse = torch.empty_strided((B, Hq), (Hq, 1), dtype=torch.float32, device=device)
     tail = (None if lens is None else lens.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv)
     score = (Ncap, D, D ** -0.5 if scale is None else scale, softcap,
              None if slopes is None else slopes.data_ptr())
@@ -579,7 +593,7 @@ def _decode(fn, q, pre, kcache, vcache, lens, scale, softcap, slopes, stream):
                 vcache.data_ptr(), *tail, Np, *score)
     else:
         args = (q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), *tail, *score)
-    if stream is None and torch.cuda.current_device() == dev:
+    if stream is None and _current_device() == dev:
         rc = fn(*args, _raw_stream(dev))
         if rc:
             _check(rc)
