@@ -137,6 +137,7 @@ struct ModMisc {
   int2 ranges[2][2 * kBM];  // prefill: keys [x, y) that the rows of item k % 2 see
   float red[4][4][16];      // keys as rows: per team, warp and head, a maximum or a sum
   float own_slopes[4][16];  // times log2(e)
+  bool slow[16];  // per softmax warp, biased: scores are modified before the exponential
   int4 seen[16];  // per softmax warp: keys [x, y) that all its rows see, [z, w) that any does
   int own_pv[2];  // O^T += V^T P^T issued so far in the query tile's run of own keys
   uint32_t tmem_base;
@@ -199,33 +200,62 @@ __device__ __forceinline__ void mask_to(float (&s)[64], const Seen& m, float wit
 // m need not be the row's largest score, only near enough that no weight
 // overflows and none that matters underflows, and the same for all of a row's
 // keys.  So where the modifications are cheap to apply together with the
-// exponential (`fused`), they are not applied before it just to find the
-// maximum: m comes from the largest raw product, or largest magnitude for
-// capped scores (the cap is odd and rises), and the bias of the nearest key
-// of the tile.  That is above the largest score by twice the capped largest
-// magnitude and the bias' change over the tile at most; kLoose limits it.
-// Weights then lie above 2^-kLoose where exact ones lie above 1/2, as precise.
+// exponential (`fused`), they are not applied before it just to find the maximum.
+//   * Capped: with A the largest raw magnitude of the warp's scores, capped, and
+//     the bias of the key that it favours, m = A + bias: at most 2 A above the
+//     score of that key.
+//   * Biased only: m is the largest of the sums of a group's largest raw product
+//     and its most favoured key's bias, for groups of 16 keys: too large by the
+//     bias' change over a group at most.
+// kLoose limits both.  Weights then lie above 2^-kLoose where exact ones lie above
+// 1/2, as precise.
+//
+// The bias relative to its reference is -|slope| |j - c0| with one key c0 per row
+// (its own position if it sees that; else, and for a negative slope, the end of
+// its keys that the bias favours), which no key of a tile passes (`linear`) but
+// in the diagonal's tile of a row that sees keys on both sides.  A negative slope
+// on both sides has no such c0.
 constexpr float kLoose = 100.f;
 
 template <bool kCap, bool kBias>
 struct Scores {
   bool fused;
   int tier;          // capped, fused: which polynomial; 3: the longest, some keys unseen
+                     // or not linear
   Seen seen;         // (of them)
-  float slope, rel;  // biased, fused: key kb + i has bias slope * (rel + i)
+  bool linear;
+  float slope, rel;  // biased: key kb + i has bias -slope * |rel + i|, slope >= 0
+  float most;        // capped and biased: the bias of the tile's most favoured key
 
-  // kb: key of s[0], kt: of the tile.  masked: some row of the warp does not see
-  // all 128 keys of the tile.  Returns the row's m for the tile (both halves);
-  // s holds raw products if fused, else scores, -inf for unseen keys.
-  __device__ __forceinline__ float prepare(float (&s)[64], const ModKernelParams& p,
-                                           const RowInfo& info, float row_slope, int kt, int kb,
-                                           bool masked) {
+  // What does not depend on the scores, found while they are still multiplied.
+  // kb: key of the thread's first score, kt: of the tile.  masked: some row of the
+  // warp does not see all 128 keys of the tile.
+  __device__ __forceinline__ void look(const RowInfo* info, const float* row_slope, int kt, int kb,
+                                       bool masked) {
     RowInfo row;
-    if (masked || kBias) row = info;
-    if (masked) seen = seen_columns(row.lo - kb, row.hi - kb);
-    float top = 0.f;    // capped: largest score of the row by magnitude
-    bool poly = false;  // capped: the longest polynomial holds
-    fused = true;
+    if (masked || kBias) row = *info;
+    linear = true;
+    if constexpr (kBias) {
+      const bool left = row.hi - 1 <= row.pos || kt + kBN - 1 <= row.pos;
+      slope = fabsf(*row_slope);
+      const unsigned c0 = static_cast<unsigned>(row.pos) +
+                          static_cast<unsigned>(left ? -row.ref : row.ref);
+      const int to_c0 = static_cast<int>(c0 - static_cast<unsigned>(kt));
+      linear = __all_sync(0xFFFFFFFFu, to_c0 <= 0 || to_c0 >= kBN - 1);
+      rel = static_cast<float>(static_cast<int>(static_cast<unsigned>(kb) - c0));
+      if constexpr (kCap) {
+        const int from = max(row.lo, kt) - kt, to = min(row.hi - kt, kBN) - 1;
+        const int off = max(max(from - to_c0, to_c0 - to), 0);  // c0 to the nearest
+        // (a row that sees none of the tile's keys: neither is there a nearest)
+        most = from <= to ? -slope * static_cast<float>(off) : -CUDART_INF_F;
+      }
+    }
+    if (masked || !linear) seen = seen_columns(row.lo - kb, row.hi - kb);
+  }
+
+  // From s to the row's m for the tile (both halves); false: it cannot be fused.
+  __device__ __forceinline__ bool prepare(float (&s)[64], const ModKernelParams& p, bool masked,
+                                          float& m) {
     if constexpr (kCap) {
       if (masked) mask_to(s, seen, 0.f);  // what lies at unseen keys has no say
       float a0 = 0.f, a1 = 0.f;
@@ -238,82 +268,61 @@ struct Scores {
       // the shortest polynomial that holds for all of the warp's scores
       // (magnitudes are ordered like their bits)
       const float all = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a0)));
-      a0 = fmaxf(a0, __shfl_xor_sync(0xFFFFFFFFu, a0, 16));  // the row's other half
-      poly = all <= p.mod.cap_limit[2];
       tier = all <= p.mod.cap_limit[0] ? 0 : (all <= p.mod.cap_limit[1] ? 1 : 2);
-      fused = tier < 2 || poly;
-      if (masked) {
-        fused = poly;
-        tier = 3;
-      }
-      top = fminf(a0 * p.scale_log2, p.mod.cap_out);  // |tanh x| <= |x|, 1
-    }
-    bool linear = true;
-    if constexpr (kBias) {
-      // |pos - j| is linear in j over the keys that the row sees, but where
-      // they lie on both sides of pos: bias = slope * (j - c0), c0 = pos - ref
-      // (left of pos) or pos + ref (right).  The difference is small whatever
-      // its terms are.
-      const bool left = row.hi - 1 <= row.pos || kt + kBN - 1 <= row.pos;
-      const bool right = row.lo >= row.pos || kt >= row.pos;
-      linear = __all_sync(0xFFFFFFFFu, left || right);
-      slope = left ? row_slope : -row_slope;
-      const unsigned c0 = static_cast<unsigned>(row.pos) +
-                          static_cast<unsigned>(left ? -row.ref : row.ref);
-      rel = static_cast<float>(static_cast<int>(static_cast<unsigned>(kb) - c0));
-      // of the keys seen in the tile, the one that the bias favours
-      const int from = max(row.lo, kt), to = min(row.hi, kt + kBN) - 1;
-      const int best = slope >= 0.f ? to : from;
-      const float most = slope * (rel + static_cast<float>(best - kb));
-      fused = fused && linear &&
-              __all_sync(0xFFFFFFFFu, 2.f * top + fabsf(slope) * (kBN - 1) <= kLoose);
-      if constexpr (kCap) {
-        // (a row that sees none of the tile's keys: neither is there a nearest)
-        if (fused) return from <= to ? top + most : -CUDART_INF_F;
-      } else if (fused) {
-        if (masked) mask_to(s, seen, -CUDART_INF_F);
-        const float mx = row_max(s);
-        return mx == -CUDART_INF_F ? mx : fmaf(mx, p.scale_log2, most);
-      }
-    } else if constexpr (kCap) {
-      fused = fused && __all_sync(0xFFFFFFFFu, 2.f * top <= kLoose);
-      if (fused) return top;
+      const bool holds = all <= p.mod.cap_limit[2] || (tier < 2 && !masked && linear);
+      if (masked || !linear) tier = 3;
+      // no score of the warp's rows is larger: |tanh x| <= |x|, 1
+      const float top = fminf(all * p.scale_log2, p.mod.cap_out);
+      m = kBias ? top + most : top;
+      return holds && 2.f * top <= kLoose;
     } else {
       if (masked) mask_to(s, seen, -CUDART_INF_F);
-      const float mx = row_max(s);
-      return mx == -CUDART_INF_F ? mx : mx * p.scale_log2;
-    }
-
-    // ---- one modification after the other
-    if constexpr (kCap) {
-      if (poly) {
-        const CapPoly<kCapN2> cap(p.mod.cap_coef[2]);
-        const uint64_t zero = f32x2(0.f, 0.f);
+      if constexpr (kBias) {
+        m = -CUDART_INF_F;
 #pragma unroll
-        for (int i = 0; i < 64; i += 2)
-          unpack_f32x2(cap(f32x2(s[i], s[i + 1]), zero), s[i], s[i + 1]);
-      } else {
+        for (int g = 0; g < 64; g += 16) {
+          float a0 = fmaxf(s[g], s[g + 1]), a1 = fmaxf(s[g + 2], s[g + 3]);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) s[i] = tanh_any(s[i] * p.mod.cap_in) * p.mod.cap_out;
-      }
-    }
-    if constexpr (kBias) {
-      const float m1 = kCap ? 1.f : p.scale_log2;
-      if (linear) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-          s[i] = fmaf(s[i], m1, slope * (rel + static_cast<float>(i)));
-      } else {
-        const unsigned d0 = static_cast<unsigned>(row.pos) - static_cast<unsigned>(kb);
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const int dist = abs(static_cast<int>(d0 - i)) - row.ref;
-          s[i] = fmaf(s[i], m1, -row_slope * static_cast<float>(dist));
+          for (int i = g + 4; i < g + 16; i += 4) {
+            a0 = max3f(a0, s[i], s[i + 1]);
+            a1 = max3f(a1, s[i + 2], s[i + 3]);
+          }
+          const float at = rel + static_cast<float>(g);  // c0 to the group
+          const float off = fmaxf(fmaxf(at, -15.f - at), 0.f);
+          m = fmaxf(m, fmaf(fmaxf(a0, a1), p.scale_log2, -slope * off));
         }
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));  // the row's other half
+      } else {
+        const float mx = row_max(s);
+        m = mx == -CUDART_INF_F ? mx : mx * p.scale_log2;
       }
+      return true;
     }
-    if (masked) mask_to(s, seen, -CUDART_INF_F);
-    return row_max(s);
+  }
+
+  // The thread's 64 products in TMEM, at s_addr, become scores, -inf for unseen
+  // keys.  In a loop over TMEM and not in the registers: unrolled over those, the
+  // code of this rare way made the usual one slower by a tenth to a sixth.
+  __device__ static __forceinline__ void modify(uint32_t s_addr, const ModKernelParams& p,
+                                                const RowInfo* info, const float* row_slope,
+                                                int kb) {
+    const RowInfo row = *info;
+    const float away = kBias ? -*row_slope : 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 64; i0 += 16) {
+      uint32_t v[16];
+      tmem_ld_pair16<64>(s_addr + i0, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = kb + i0 + i;
+        float x = __uint_as_float(v[i]);
+        x = kCap ? tanh_any(x * p.mod.cap_in) * p.mod.cap_out : x * p.scale_log2;
+        if constexpr (kBias) x = fmaf(away, static_cast<float>(abs(row.pos - key) - row.ref), x);
+        v[i] = __float_as_uint(key >= row.lo && key < row.hi ? x : -CUDART_INF_F);
+      }
+      tmem_st_pair16<64>(s_addr + i0, v);
+    }
+    tmem_st_wait();
   }
 
   __device__ static __forceinline__ float row_max(const float (&s)[64]) {
@@ -337,25 +346,40 @@ struct Scores {
   __device__ __forceinline__ float weights(const float (&s)[64], const ModKernelParams& p,
                                            float neg_m, uint32_t (&pk)[32]) const {
     uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
-    // pass(f): f(pair of s, what to add to its scores) -> exponents; with_mask:
+    // pass(.., f): f(pair of s, what to add to its scores) -> exponents; with_mask:
     // unseen keys get -inf for theirs
-    auto pass = [&](bool with_bias, bool with_mask, auto f) {
-      uint64_t add = f32x2(neg_m, neg_m);
-      const uint64_t next = f32x2(2.f * slope, 2.f * slope);
+    enum Bias { kNone, kLinear, kBent };
+    auto pass = [&](Bias bias, bool with_mask, auto f) {
+      uint64_t add = f32x2(neg_m, neg_m), a = add;
+      // linear: the bias minus m itself; else what |.| is taken of
+      const float step = bias == kBent || rel < 0.f ? slope : -slope;
+      const float from = bias == kBent ? 0.f : neg_m;
+      const uint64_t next = f32x2(2.f * step, 2.f * step);
 #pragma unroll
       for (int e = 0; e < 64; e += 4) {
-        // The bias minus m, pair by pair: exact at every 16th key, a sum
-        // of a few steps in between (its roundings are below the score's).
-        if (with_bias && e % 16 == 0)
-          add = f32x2(fmaf(slope, rel + static_cast<float>(e), neg_m),
-                      fmaf(slope, rel + static_cast<float>(e + 1), neg_m));
-        const uint64_t a01 = add;
-        if (with_bias) add = add_f32x2(add, next);
-        const uint64_t a23 = add;
-        if (with_bias && e % 16 != 12) add = add_f32x2(add, next);
+        uint64_t add2[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // Pair by pair: exact at every 16th key, a sum of a few steps in
+          // between (its roundings are below the score's).
+          if (bias != kNone) {
+            const float at = rel + static_cast<float>(e);
+            if (h == 0 && e % 16 == 0)
+              a = f32x2(fmaf(step, at, from), fmaf(step, at + 1.f, from));
+            else
+              a = add_f32x2(a, next);
+            add = a;
+            if (bias == kBent) {
+              float b0, b1;
+              unpack_f32x2(a, b0, b1);
+              add = f32x2(neg_m - fabsf(b0), neg_m - fabsf(b1));
+            }
+          }
+          add2[h] = add;
+        }
         float x0, x1, x2, x3;
-        unpack_f32x2(f(f32x2(s[e], s[e + 1]), a01), x0, x1);
-        unpack_f32x2(f(f32x2(s[e + 2], s[e + 3]), a23), x2, x3);
+        unpack_f32x2(f(f32x2(s[e], s[e + 1]), add2[0]), x0, x1);
+        unpack_f32x2(f(f32x2(s[e + 2], s[e + 3]), add2[1]), x2, x3);
         if (with_mask) {
           const uint32_t w = seen.words[e / 32];
           x0 = (w >> (e % 32)) & 1u ? x0 : -CUDART_INF_F;
@@ -371,20 +395,25 @@ struct Scores {
         pk[e / 2 + 1] = pack_bf16x2(p2, p3);
       }
     };
+    constexpr Bias kLin = kBias ? kLinear : kNone;
     if ((kCap || kBias) && !fused) {
-      pass(false, false, [](uint64_t x, uint64_t add) { return add_f32x2(x, add); });
+      pass(kNone, false, [](uint64_t x, uint64_t add) { return add_f32x2(x, add); });
     } else if constexpr (kCap) {
       if (tier == 0)
-        pass(kBias, false, CapPoly<kCapN0>(p.mod.cap_coef[0]));
+        pass(kLin, false, CapPoly<kCapN0>(p.mod.cap_coef[0]));
       else if (tier == 1)
-        pass(kBias, false, CapPoly<kCapN1>(p.mod.cap_coef[1]));
+        pass(kLin, false, CapPoly<kCapN1>(p.mod.cap_coef[1]));
       else if (tier == 2)
-        pass(kBias, false, CapPoly<kCapN2>(p.mod.cap_coef[2]));
+        pass(kLin, false, CapPoly<kCapN2>(p.mod.cap_coef[2]));
       else
-        pass(kBias, true, CapPoly<kCapN2>(p.mod.cap_coef[2]));
+        pass(kBias ? kBent : kNone, true, CapPoly<kCapN2>(p.mod.cap_coef[2]));
     } else {
       const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
-      pass(kBias, false, [&](uint64_t x, uint64_t add) { return fma_f32x2(x, scale2, add); });
+      auto scaled = [&](uint64_t x, uint64_t add) { return fma_f32x2(x, scale2, add); };
+      if (kBias && !linear)
+        pass(kBent, false, scaled);
+      else
+        pass(kLin, false, scaled);
     }
     float u0, u1;
     unpack_f32x2(add_f32x2(acc0, acc1), u0, u1);
@@ -706,11 +735,6 @@ struct SwapMma {
   }
 };
 
-// Softmax, epilogue and V's edge: four warps, thread = key of the tile (S^T, P^T)
-// or element of the head (O^T); NH >= G heads in registers.  The running maximum
-// is common to all 128 threads.  It is kept while no score exceeds it by more than
-// 2^8: one barrier that votes on that, and on every warp's waits having ended
-// well, is all that the threads of a tile exchange.
 // Waits, as mod_wait does, until the products of the first n tiles of query tile
 // t's run have been issued.
 __device__ __forceinline__ bool own_turn(ModMisc& ms, const ModKernelParams& p, int t, uint32_t n,
@@ -734,6 +758,11 @@ __device__ __forceinline__ bool own_turn(ModMisc& ms, const ModKernelParams& p, 
   }
 }
 
+// Softmax, epilogue and V's edge: four warps, thread = key of the tile (S^T, P^T)
+// or element of the head (O^T); NH >= G heads in registers.  The running maximum
+// is common to all 128 threads.  It is kept while no score exceeds it by more than
+// 2^8: one barrier that votes on that, and on every warp's waits having ended
+// well, is all that the threads of a tile exchange.
 template <int D, int NH, bool kCap, bool kBias>
 __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, uint8_t* smem,
                                          uint32_t tmem, int t, int k) {
@@ -1083,6 +1112,13 @@ __global__ void __launch_bounds__(kModThreads, 1)
         seen.z = __reduce_min_sync(0xFFFFFFFFu, row.lo < row.hi ? row.lo : INT_MAX);
         seen.w = live ? __reduce_max_sync(0xFFFFFFFFu, row.hi) : 0;
         if (lane == 0) ms.seen[warp] = seen;
+        if constexpr (kBias) {
+          // rows whose bias does not go with the exponential
+          const bool slow =
+              __any_sync(0xFFFFFFFFu, (slope < 0.f && row.lo < row.pos && row.hi - 1 > row.pos) ||
+                                          (!kCap && fabsf(slope) * 15.f > kLoose));
+          if (lane == 0) ms.slow[warp] = slow;
+        }
         if (c == 0) {
           ms.rows[t * kBM + r] = row;
           if constexpr (kBias) ms.slopes[t * kBM + r] = slope;
@@ -1098,6 +1134,12 @@ __global__ void __launch_bounds__(kModThreads, 1)
           const int4 seen = ms.seen[warp];
           masked = kt < seen.x || kt + kBN > seen.y;
           dead = kt >= seen.w || kt + kBN <= seen.z;  // no row sees a key of the tile
+        }
+        Scores<kCap, kBias> scores;
+        bool slow = false;
+        if (!dead) {
+          scores.look(&ms.rows[t * kBM + r], &ms.slopes[t * kBM + r], kt, kt + c * 64, masked);
+          if constexpr (kBias) slow = ms.slow[warp];
         }
         const int edges = w.edges;
         const bool edge = ((edges & 1) && j == 0) || ((edges & 2) && j == w.n - 1);
@@ -1143,17 +1185,20 @@ __global__ void __launch_bounds__(kModThreads, 1)
           continue;
         }
         tc_fence_after();
-        float s[64];
-        {
+        float s[64], m_tile;
+        auto load = [&] {
           uint32_t sr[64];
           tmem_ld_pair64<64>(s_addr, sr);
 #pragma unroll
           for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
+        };
+        load();
+        scores.fused = !slow && scores.prepare(s, p, masked, m_tile);
+        if ((kCap || kBias) && !scores.fused) {
+          scores.modify(s_addr, p, &ms.rows[t * kBM + r], &ms.slopes[t * kBM + r], kt + c * 64);
+          load();
+          m_tile = scores.row_max(s);
         }
-        Scores<kCap, kBias> scores;
-        const float m_tile =
-            scores.prepare(s, p, ms.rows[t * kBM + r], kBias ? ms.slopes[t * kBM + r] : 0.f, kt,
-                           kt + c * 64, masked);
         if constexpr (C::kSplitS) {
           // S_t has been read: the MMA warp may write the next tile's keys
           // [64, 128) over columns 64..127, which P does not use
