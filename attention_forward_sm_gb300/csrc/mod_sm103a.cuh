@@ -219,13 +219,14 @@ constexpr float kLoose = 100.f;
 
 template <bool kCap, bool kBias>
 struct Scores {
-  bool fused;
-  int tier;          // capped, fused: which polynomial; 3: the longest, some keys unseen
-                     // or not linear
-  Seen seen;         // (of them)
+  static constexpr int kModified = 4;
+  int tier;          // capped: which polynomial; 3: the longest, some keys unseen or
+                     // not linear; kModified: the scores are modified already
+  Seen seen;         // (of 3)
   bool linear;
   float slope, rel;  // biased: key kb + i has bias -slope * |rel + i|, slope >= 0
-  float most;        // capped and biased: the bias of the tile's most favoured key
+  float most[4];     // bias of the most favoured key: capped: of the tile, in [0];
+                     // else of every 16 keys
 
   // What does not depend on the scores, found while they are still multiplied.
   // kb: key of the thread's first score, kt: of the tile.  masked: some row of the
@@ -247,7 +248,18 @@ struct Scores {
         const int from = max(row.lo, kt) - kt, to = min(row.hi - kt, kBN) - 1;
         const int off = max(max(from - to_c0, to_c0 - to), 0);  // c0 to the nearest
         // (a row that sees none of the tile's keys: neither is there a nearest)
-        most = from <= to ? -slope * static_cast<float>(off) : -CUDART_INF_F;
+        most[0] = from <= to ? -slope * static_cast<float>(off) : -CUDART_INF_F;
+      } else if (linear) {
+        const float step = rel < 0.f ? slope : -slope;
+        most[0] = step * (rel < 0.f ? rel + 15.f : rel);
+#pragma unroll
+        for (int g = 1; g < 4; ++g) most[g] = fmaf(step, 16.f * g, most[0]);
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float at = rel + 16.f * g;  // c0 to the keys
+          most[g] = -slope * fmaxf(fmaxf(at, -15.f - at), 0.f);
+        }
       }
     }
     if (masked || !linear) seen = seen_columns(row.lo - kb, row.hi - kb);
@@ -273,7 +285,7 @@ struct Scores {
       if (masked || !linear) tier = 3;
       // no score of the warp's rows is larger: |tanh x| <= |x|, 1
       const float top = fminf(all * p.scale_log2, p.mod.cap_out);
-      m = kBias ? top + most : top;
+      m = kBias ? top + most[0] : top;
       return holds && 2.f * top <= kLoose;
     } else {
       if (masked) mask_to(s, seen, -CUDART_INF_F);
@@ -287,15 +299,14 @@ struct Scores {
             a0 = max3f(a0, s[i], s[i + 1]);
             a1 = max3f(a1, s[i + 2], s[i + 3]);
           }
-          const float at = rel + static_cast<float>(g);  // c0 to the group
-          const float off = fmaxf(fmaxf(at, -15.f - at), 0.f);
-          m = fmaxf(m, fmaf(fmaxf(a0, a1), p.scale_log2, -slope * off));
+          m = fmaxf(m, fmaf(fmaxf(a0, a1), p.scale_log2, most[g / 16]));
         }
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));  // the row's other half
       } else {
         const float mx = row_max(s);
         m = mx == -CUDART_INF_F ? mx : mx * p.scale_log2;
       }
+      tier = 0;
       return true;
     }
   }
@@ -396,7 +407,7 @@ struct Scores {
       }
     };
     constexpr Bias kLin = kBias ? kLinear : kNone;
-    if ((kCap || kBias) && !fused) {
+    if ((kCap || kBias) && tier == kModified) {
       pass(kNone, false, [](uint64_t x, uint64_t add) { return add_f32x2(x, add); });
     } else if constexpr (kCap) {
       if (tier == 0)
@@ -1193,8 +1204,8 @@ __global__ void __launch_bounds__(kModThreads, 1)
           for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
         };
         load();
-        scores.fused = !slow && scores.prepare(s, p, masked, m_tile);
-        if ((kCap || kBias) && !scores.fused) {
+        if ((kBias && slow) || !scores.prepare(s, p, masked, m_tile)) {
+          scores.tier = scores.kModified;
           scores.modify(s_addr, p, &ms.rows[t * kBM + r], &ms.slopes[t * kBM + r], kt + c * 64);
           load();
           m_tile = scores.row_max(s);
