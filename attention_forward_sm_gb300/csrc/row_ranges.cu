@@ -28,6 +28,7 @@ __global__ void __launch_bounds__(kThreads)
                       int2* __restrict__ ranges, int N, int M, int causal) {
   __shared__ int ends[kTokens];
   __shared__ int warp_sum[kThreads / 32];
+  __shared__ int2 staged[kTokens];
   const int b = blockIdx.y;
   const int t0 = blockIdx.x * kTokens;
   const int last = min(t0 + kTokens, N) - 1;
@@ -70,24 +71,28 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < kPer; ++i) ends[threadIdx.x * kPer + i] = min(before + e[i], N);
     __syncthreads();
     const int docs = min(kTokens, M - m0);
+    int doc = -1;  // of the token before, in this turn
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int tok = t0 + i * kThreads + threadIdx.x;
+      const int tok = t0 + threadIdx.x * kPer + i;
       if (tok < carry || tok >= total) continue;
-      int lo = 0, hi = docs - 1;  // ends[docs - 1] = total > tok
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (ends[mid] > tok)
-          hi = mid;
-        else
-          lo = mid + 1;
+      if (doc < 0 || ends[doc] <= tok) {
+        int lo = doc + 1, hi = docs - 1;  // ends[docs - 1] = total > tok
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (ends[mid] > tok)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        doc = lo;
       }
-      const int s = lo > 0 ? ends[lo - 1] : carry, end = ends[lo];
+      const int s = doc > 0 ? ends[doc - 1] : carry, end = ends[doc];
       int vis = end;
       if (causal) {
         vis = tok + 1;
         if (prefix_lens) {
-          const int pre = min(max(prefix_lens[static_cast<size_t>(b) * M + m0 + lo], 0), N);
+          const int pre = min(max(prefix_lens[static_cast<size_t>(b) * M + m0 + doc], 0), N);
           vis = max(vis, min(s + pre, end));
         }
       }
@@ -95,10 +100,14 @@ __global__ void __launch_bounds__(kThreads)
     }
     carry = total;
   }
+  // through shared memory, so that a warp writes consecutive tokens
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) staged[threadIdx.x * kPer + i] = out[i];
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int tok = t0 + i * kThreads + threadIdx.x;
-    if (tok < N) ranges[static_cast<size_t>(b) * N + tok] = out[i];
+    const int at = i * kThreads + threadIdx.x;
+    if (t0 + at < N) ranges[static_cast<size_t>(b) * N + t0 + at] = staged[at];
   }
 }
 
