@@ -107,7 +107,8 @@ struct ModKernelParams {
   int B, Hq, Hkv, G, Nq, Nk;  // Nk: keys (prefill) or the caches' capacity (decode)
   int causal, q_offset;
   int longest_first, group_heads;  // prefill: order of the work items
-  int o_sectors;                   // prefill: o is 32-byte aligned
+  int o_sectors;                   // prefill: o is 32-byte aligned (stores of whole
+                                   // sectors: packed documents 77 us, else 83)
   int Np, prefix_tiles;            // shared prefix: keys, key tiles
   int row_blocks, per_tile;        // its items per KV head; requests per query tile
   int pre_rows;                    // rows of a prefix item's partial states
@@ -151,15 +152,11 @@ cudaError_t launch_mod_split_d64_h4(const ModKernelParams& p, unsigned grid, int
                                cudaStream_t stream);
 cudaError_t launch_mod_split_d64_h8(const ModKernelParams& p, unsigned grid, int dev,
                                cudaStream_t stream);
-cudaError_t launch_mod_split_d64_h16(const ModKernelParams& p, unsigned grid, int dev,
-                               cudaStream_t stream);
 cudaError_t launch_mod_split_d128_h0(const ModKernelParams& p, unsigned grid, int dev,
                                cudaStream_t stream);
 cudaError_t launch_mod_split_d128_h4(const ModKernelParams& p, unsigned grid, int dev,
                                cudaStream_t stream);
 cudaError_t launch_mod_split_d128_h8(const ModKernelParams& p, unsigned grid, int dev,
-                               cudaStream_t stream);
-cudaError_t launch_mod_split_d128_h16(const ModKernelParams& p, unsigned grid, int dev,
                                cudaStream_t stream);
 
 // 3-D bf16 view [BH, N, D], box {64, rows, 1}; 4-D view [B, Hkv, G, D] of the

@@ -34,7 +34,10 @@ struct CombineParams {
 // runs of key tiles give every item's first and last run, and with it its
 // slots.  A lane holds D / 32 consecutive elements of O; the states are
 // few and in L2, so the loads of up to four of them are in flight at once and
-// nothing else is shared.
+// nothing else is shared.  Bound by latency: 3.5 us behind the split kernel of 8
+// requests with up to 64k keys (256 rows of up to 6 states) and of 256 requests
+// behind a shared prefix (8192 rows of 3 or 4) alike, of which the launch is
+// hidden behind that kernel's end.
 template <int D>
 __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p) {
   constexpr int E = D / 32;
@@ -181,12 +184,14 @@ int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
   d.k->part_o = reinterpret_cast<float*>(base + d.part_o);
   d.k->part_lse = reinterpret_cast<float*>(base + d.part_lse);
   using Launch = cudaError_t (*)(const ModKernelParams&, unsigned, int, cudaStream_t);
-  static const Launch split[2][4] = {
-      {launch_mod_split_d64_h4, launch_mod_split_d64_h8, launch_mod_split_d64_h16,
-       launch_mod_split_d64_h0},
-      {launch_mod_split_d128_h4, launch_mod_split_d128_h8, launch_mod_split_d128_h16,
-       launch_mod_split_d128_h0}};
-  const int G = d.k->G, heads = G <= 4 ? 0 : (G <= 8 ? 1 : (G <= 16 ? 2 : 3));
+  static const Launch split[2][3] = {
+      {launch_mod_split_d64_h4, launch_mod_split_d64_h8, launch_mod_split_d64_h0},
+      {launch_mod_split_d128_h4, launch_mod_split_d128_h8, launch_mod_split_d128_h0}};
+  // Own keys with the keys as rows (h4, h8: heads a thread holds) or, above 8
+  // heads, the heads.  Measured with 64 requests of up to 4096 / 256 keys, Hkv 8,
+  // D 128: 4 heads 85.8 / 19.7 us (heads as rows 91.4 / 22.4), 8 heads 103.6 /
+  // 21.4 (104.3 / 22.7), 16 heads 100.1 / 27.6 (98.2 / 23.5).
+  const int G = d.k->G, heads = G <= 4 ? 0 : (G <= 8 ? 1 : 2);
   cudaError_t e = split[d.D == 128][heads](*d.k, d.ctas, d.dev, stream);
   if (e == cudaSuccess)
     e = d.D == 128 ? launch_combine<128>(*d.k, d.ctas, stream)

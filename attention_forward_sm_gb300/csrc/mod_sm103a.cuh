@@ -27,11 +27,27 @@
 //     that a second kernel merges through their log-sum-exp.  A prefix tile is
 //     read once for 256 rows, and at fewer than ~300 rows its bytes cost more
 //     than its products.
-//   * Own keys of at most 16 query heads per KV head are multiplied the other way
+//   * Own keys of at most 8 query heads per KV head are multiplied the other way
 //     round, S^T = K Q^T and O^T += V^T P^T: the 128 keys of a tile are the rows
 //     of the product, so 128 threads share a tile's scores, a key each, where
 //     as rows of S the few heads would occupy a fraction of one warp.  P^T goes
 //     through shared memory (it is the B operand).
+//
+// What bounds it and what it measures (us on a GB300, by CUDA events).
+//   * Prefill, long rows: the chain of a query tile, product, softmax, product,
+//     of which two run at a time.  B1 Hq32 Hkv8 N8192 D128 causal: 344 (1.60
+//     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 467, biased 460,
+//     both 571; D64 274, 448, 397.  The tensor pipe is 49% busy capped, the issue
+//     slots 55%: a pass over a tile is longer than the products of the other.
+//   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
+//     for its first scores and its epilogue next to 2.9k a tile.  Packed documents
+//     B4 H16 N4096 D128: 91, tensor pipe 37%.
+//   * Decode of own keys: DRAM.  8 requests of up to 64k keys, Hkv8 D128: 91, 533
+//     MB at 6.1 TB/s in this kernel (91% of a measured copy).
+//   * Decode behind a prefix: softmax and products of the prefix first, then DRAM.
+//     64 requests behind 16384 keys 45, 256 (capped) behind 8192 79.
+// Code that is not in the instruction cache shows: 264 KB of a decode instead of
+// 96 KB cost it 40% of its time, and a prefill's rarely taken ways 5 to 15%.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -70,8 +86,9 @@ __device__ __forceinline__ bool mod_wait(uint64_t* bar, uint32_t parity, uint32_
 constexpr int kModThreads = 640;  // 16 softmax warps, load, MMA, 2 planning warps
 constexpr int kModWarpLoad = 16, kModWarpMma = 17, kModWarpPlan = 18;
 // setmaxnreg split of the 61440 registers the launch gets (640 threads x 96).  A
-// prefill's other roles fit 32 registers, which leaves its softmax the most; a
-// decode's loaders and planners need more, its scores are few.
+// prefill's other roles fit 32 registers, which leaves its softmax the most (B1 Hq32
+// Hkv8 N8192 D128 causal capped: 489 us, with 104 / 64 530); a decode's loaders and
+// planners need more, its scores are few.
 template <bool kSplit>
 constexpr uint32_t kModRegSoftmax = kSplit ? 104 : 112;
 template <bool kSplit>
@@ -312,8 +329,9 @@ struct Scores {
   }
 
   // The thread's 64 products in TMEM, at s_addr, become scores, -inf for unseen
-  // keys.  In a loop over TMEM and not in the registers: unrolled over those, the
-  // code of this rare way made the usual one slower by a tenth to a sixth.
+  // keys.  In a loop over TMEM and not in the registers: unrolled over those, this
+  // rare way was a quarter of the kernel (117 KB, now 90), and the usual one slower
+  // for it (prefix documents, capped and biased: 112 us, now 107).
   __device__ static __forceinline__ void modify(uint32_t s_addr, const ModKernelParams& p,
                                                 const RowInfo* info, const float* row_slope,
                                                 int kb) {
@@ -705,13 +723,15 @@ struct OwnPlan {
   }
 };
 
-// Decode of the requests' own keys with the keys as rows (G <= kSwapHeads query
+// Decode of the requests' own keys with the keys as rows (G <= 8 query
 // heads per KV head).  The items of a query tile's run alternate between two teams
 // of four warps, each with its own S^T [128 keys, 16 heads] and O^T [D, 16 heads]
 // (16 columns of the query tile's S and O), Q and P^T [16 heads, 128 keys] (in
 // its Q tile of shared memory, 128-byte-swizzled as K-major operands), so one
-// team's epilogue and the next item's products and softmax overlap.
-constexpr int kSwapHeads = 16;
+// team's epilogue and the next item's products and softmax overlap (256 requests
+// behind 8192 shared keys: 85 us with one team, 82 with two, 79 where the teams
+// issue their own products with V).
+constexpr int kSwapHeads = 16;  // the least a product has; columns from G on mean nothing
 constexpr uint32_t kTeamCols = 16;
 constexpr uint32_t kTeamQ = 4096, kSwapP = 8192, kTeamP = 4096;  // bytes
 constexpr uint32_t kSwapPChunk = kSwapHeads * 128;               // 64 keys of P^T
@@ -1894,8 +1914,8 @@ cudaError_t launch_one(const ModKernelParams& p, unsigned grid, int dev, cudaStr
 }
 
 // The variant is the caller's request alone: what is not asked for is not computed.
-// kHeads: 0, or query heads per KV head that a decode's threads hold (4, 8, 16:
-// the smallest that G fits in; above 16 the heads are the rows).
+// kHeads: query heads per KV head that a decode's threads hold, or 0: the heads are
+// the rows.
 template <int D, bool kSplit, int kHeads>
 cudaError_t launch_variant(const ModKernelParams& p, unsigned grid, int dev,
                            cudaStream_t stream) {

@@ -1,4 +1,4 @@
-// mod_attn_kernel, decode, D = 128, more than 16 query heads per KV head.
+// mod_attn_kernel, decode, D = 128, more than 8 query heads per KV head.
 #include "mod_sm103a.cuh"
 
 namespace attn {

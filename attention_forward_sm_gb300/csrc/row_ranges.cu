@@ -8,8 +8,11 @@
 // 8 bytes written per token and 4 or 8 read per document: the work is too
 // small to be bound by memory (8 x 131072 tokens: 8.4 MB), so it is one
 // launch with no intermediate: a CTA takes kTokens tokens of one row, scans
-// the lengths 1024 at a time up to its last token, and each token finds its
-// document by bisection in the scanned ends in shared memory.
+// the lengths 1024 at a time up to its last token, and each thread finds its
+// first token's document by bisection in the scanned ends in shared memory; the
+// next three are in the same one or search behind it.  Bound by the latency of
+// those steps and by instructions (a search per token: 65% of the issue slots):
+// 4 x 4096 tokens 2.3 us, 8 x 131072 of 513 documents 6.6 us (7.4).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
