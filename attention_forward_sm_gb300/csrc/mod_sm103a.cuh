@@ -37,7 +37,7 @@
 //   * Prefill, long rows: the chain of a query tile, product, softmax, product,
 //     of which two run at a time.  B1 Hq32 Hkv8 N8192 D128 causal: 344 (1.60
 //     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 467, biased 460,
-//     both 571; D64 274, 448, 397.  The tensor pipe is 49% busy capped, the issue
+//     both 571; D64 274, 442, 390.  The tensor pipe is 49% busy capped, the issue
 //     slots 55%: a pass over a tile is longer than the products of the other.
 //   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
 //     for its first scores and its epilogue next to 2.9k a tile.  Packed documents
@@ -129,6 +129,12 @@ __device__ __forceinline__ uint32_t own_item(uint32_t before, bool is_v, int t, 
 struct RowInfo {
   int lo, hi, pos, ref;
 };
+
+// Is S_t written in two halves, that of the keys [64, 128) while the softmax warps
+// still have the tile before?  Not with a cap or a bias: D64 B1 Hq32 Hkv8 N8192
+// causal 442 us capped (in halves 449), 390 biased (397); D128 471 (486), 460 (472).
+template <int D, bool kCap, bool kBias>
+constexpr bool kSplitScores = Cfg<D, false>::kSplitS && !kCap && !kBias;
 
 // Items of a query tile in flight: a decode's are short, and planned well ahead;
 // a prefill's are taken from the grid, and only one ahead, which keeps the end
@@ -1210,7 +1216,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (C::kSplitS) mbar_arrive(&ms.s_read[t]);
+            if (kSplitScores<D, kCap, kBias>) mbar_arrive(&ms.s_read[t]);
             mbar_arrive(&ms.p_full[t]);
           }
           continue;
@@ -1230,7 +1236,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
           load();
           m_tile = scores.row_max(s);
         }
-        if constexpr (C::kSplitS) {
+        if constexpr (kSplitScores<D, kCap, kBias>) {
           // S_t has been read: the MMA warp may write the next tile's keys
           // [64, 128) over columns 64..127, which P does not use
           tc_fence_before();
@@ -1638,7 +1644,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
           const bool pv = j > a && j <= b, qk = j >= a && j < b;
           const uint32_t last = (t ? steps1 : steps0) - 1u;  // the step whose P V is due
           if (pv) {
-            if constexpr (C::kSplitS) {
+            if constexpr (kSplitScores<D, kCap, kBias>) {
               ok = wait(&ms.s_read[t], last);
               if (!ok) break;
               tc_fence_after();
@@ -1649,10 +1655,10 @@ __global__ void __launch_bounds__(kModThreads, 1)
             tc_fence_after();
             issue_pv(t, bv, j - 1 > a ? 1u : 0u);
             if (j == b) mma_commit(&ms.o_done[t]);
-            if (C::kSplitS && qk) issue_s(t, bk, 1);
+            if (kSplitScores<D, kCap, kBias> && qk) issue_s(t, bk, 1);
           }
           if (qk) {
-            if (!(C::kSplitS && pv)) issue_s(t, bk, 0);
+            if (!(kSplitScores<D, kCap, kBias> && pv)) issue_s(t, bk, 0);
             mma_commit(&ms.s_full[t]);
             if (t)
               ++steps1;

@@ -98,7 +98,7 @@ def load_peaks():
         return dict(FALLBACK_PEAKS), "fallback"
 
 
-KERNEL_HEADERS = ("ptx.cuh", "internal.h")  # included by every kernel file
+KERNEL_HEADERS = ("ptx.cuh", "internal.h", "fwd_tile.cuh")  # what the kernel files include
 
 
 def kernel_source_hash(name: str) -> str:
