@@ -37,7 +37,7 @@
 //   * Prefill, long rows: the chain of a query tile, product, softmax, product,
 //     of which two run at a time.  B1 Hq32 Hkv8 N8192 D128 causal: 344 (1.60
 //     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 467, biased 460,
-//     both 571; D64 274, 442, 390.  The tensor pipe is 49% busy capped, the issue
+//     both 571; D64 274, 442, 381.  The tensor pipe is 49% busy capped, the issue
 //     slots 55%: a pass over a tile is longer than the products of the other.
 //   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
 //     for its first scores and its epilogue next to 2.9k a tile.  Packed documents
@@ -260,6 +260,7 @@ struct Scores {
     if (masked || kBias) row = *info;
     linear = true;
     if constexpr (kBias) {
+      tier = 0;
       const bool left = row.hi - 1 <= row.pos || kt + kBN - 1 <= row.pos;
       slope = fabsf(*row_slope);
       const unsigned c0 = static_cast<unsigned>(row.pos) +
@@ -313,6 +314,10 @@ struct Scores {
     } else {
       if (masked) mask_to(s, seen, -CUDART_INF_F);
       if constexpr (kBias) {
+        if (tier == kModified) {
+          m = row_max(s);
+          return true;
+        }
         m = -CUDART_INF_F;
 #pragma unroll
         for (int g = 0; g < 64; g += 16) {
@@ -329,7 +334,6 @@ struct Scores {
         const float mx = row_max(s);
         m = mx == -CUDART_INF_F ? mx : mx * p.scale_log2;
       }
-      tier = 0;
       return true;
     }
   }
@@ -1229,12 +1233,23 @@ __global__ void __launch_bounds__(kModThreads, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
         };
-        load();
-        if ((kBias && slow) || !scores.prepare(s, p, masked, m_tile)) {
-          scores.tier = scores.kModified;
+        auto modify = [&] {
           scores.modify(s_addr, p, &ms.rows[t * kBM + r], &ms.slopes[t * kBM + r], kt + c * 64);
+          scores.tier = scores.kModified;
+        };
+        if constexpr (kCap) {
           load();
-          m_tile = scores.row_max(s);
+          if (slow || !scores.prepare(s, p, masked, m_tile)) {
+            modify();
+            load();
+            m_tile = scores.row_max(s);
+          }
+        } else {
+          if constexpr (kBias) {
+            if (slow) modify();
+          }
+          load();
+          scores.prepare(s, p, masked, m_tile);
         }
         if constexpr (kSplitScores<D, kCap, kBias>) {
           // S_t has been read: the MMA warp may write the next tile's keys
