@@ -78,13 +78,15 @@ int encode_fn(PFN_cuTensorMapEncodeTiled_v12000* fn) {
 
 // 3-D view [BH, N, D] of a contiguous bf16 tensor, box {64, rows, 1},
 // 128-byte swizzle (the layout the MMA descriptors expect).
-int encode_3d(CUtensorMap* map, const void* base, int D, int N, long long BH, int rows = 128) {
+// (`stride` rows from one of the BH to the next; 0: N.)
+int encode_3d(CUtensorMap* map, const void* base, int D, int N, long long BH, int rows = 128,
+              int stride = 0) {
   PFN_cuTensorMapEncodeTiled_v12000 fn;
   if (int rc = encode_fn(&fn)) return rc;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(N),
                         static_cast<cuuint64_t>(BH)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
-                           static_cast<cuuint64_t>(N) * static_cast<cuuint64_t>(D) * 2};
+                           static_cast<cuuint64_t>(stride ? stride : N) * D * 2};
   cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
@@ -145,8 +147,9 @@ __global__ void selftest_wait_kernel(unsigned int* err, uint64_t limit_ns) {
 
 }  // namespace
 
-int encode_rows(CUtensorMap* map, const void* base, int D, int N, long long BH, int rows) {
-  return encode_3d(map, base, D, N, BH, rows);
+int encode_rows(CUtensorMap* map, const void* base, int D, int N, long long BH, int rows,
+                int stride) {
+  return encode_3d(map, base, D, N, BH, rows, stride);
 }
 
 int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B,

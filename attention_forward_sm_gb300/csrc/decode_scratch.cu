@@ -45,8 +45,10 @@ struct Cache {
 };
 Cache g_cache[kMaxDevices];
 
-int plain_path(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
-               void* ctx) {
+}  // namespace
+
+int with_own_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
+                     void* ctx) {
   void* ws = nullptr;
   if (cudaMallocAsync(&ws, bytes, stream) != cudaSuccess) {
     cudaGetLastError();
@@ -57,8 +59,6 @@ int plain_path(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cu
   return rc;
 }
 
-}  // namespace
-
 int with_scratch(size_t bytes, int dev, cudaStream_t stream,
                  int (*launch)(void*, void*, cudaStream_t), void* ctx) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -66,7 +66,7 @@ int with_scratch(size_t bytes, int dev, cudaStream_t stream,
     cudaGetLastError();
     return ATTN_ERR_CUDA;
   }
-  if (cap != cudaStreamCaptureStatusNone) return plain_path(bytes, stream, launch, ctx);
+  if (cap != cudaStreamCaptureStatusNone) return with_own_scratch(bytes, stream, launch, ctx);
 
   if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_DEVICE;
   Cache& c = g_cache[dev];

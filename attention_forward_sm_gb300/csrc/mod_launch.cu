@@ -58,16 +58,18 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
     const uint32_t all = p.prefix_total, runs = min(all, p.ctas);
     const int item = hkv * p.row_blocks + b / (2 * p.per_tile);
     const uint32_t t0 = static_cast<uint32_t>(item) * p.prefix_tiles;
-    const uint32_t r0 = run_of(all, runs, t0);
-    count[0] = static_cast<int>(run_of(all, runs, t0 + p.prefix_tiles - 1) - r0) + 1;
+    const Pieces pieces(all, runs);
+    const uint32_t r0 = piece_of(all, runs, pieces, t0);
+    count[0] = static_cast<int>(piece_of(all, runs, pieces, t0 + p.prefix_tiles - 1) - r0) + 1;
     const int in_tile = b % p.per_tile, tile = (b / p.per_tile) & 1;
     first[0] = static_cast<long long>(item + r0) * p.pre_rows + tile * 128 + in_tile * p.G + g;
   }
   if (nt > 0) {
     const uint32_t runs = min(own, 2 * p.ctas);
     const uint32_t t0 = before * p.Hkv + hkv * nt;
-    const uint32_t r0 = run_of(own, runs, t0);
-    count[1] = static_cast<int>(run_of(own, runs, t0 + nt - 1) - r0) + 1;
+    const Pieces pieces(own, runs);
+    const uint32_t r0 = piece_of(own, runs, pieces, t0);
+    count[1] = static_cast<int>(piece_of(own, runs, pieces, t0 + nt - 1) - r0) + 1;
     first[1] = (static_cast<long long>(b) * p.Hkv + hkv + r0) * p.G + g;
   }
   const int total = count[0] + count[1];
@@ -199,17 +201,19 @@ int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
-}  // namespace
-
-int mod_fwd(const ModFwdParams& p, cudaStream_t stream) {
-  DeviceInfo di;
-  if (int rc = device_info(&di)) return rc;
+// The keys [key0, key0 + nk) of a prefill.
+int launch_fwd(const ModFwdParams& p, const DeviceInfo& di, int key0, int nk,
+               cudaStream_t stream) {
   ModKernelParams k = {};
   if (int rc = encode_rows(&k.tmap_q, p.q, p.D, p.Nq, static_cast<long long>(p.B) * p.Hq, 128))
     return rc;
-  if (int rc = encode_rows(&k.tmap_k, p.k, p.D, p.Nk, static_cast<long long>(p.B) * p.Hkv, 128))
+  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  const size_t skip = static_cast<size_t>(key0) * p.D * 2;
+  if (int rc = encode_rows(&k.tmap_k, static_cast<const char*>(p.k) + skip, p.D, nk, heads, 128,
+                           p.Nk))
     return rc;
-  if (int rc = encode_rows(&k.tmap_v, p.v, p.D, p.Nk, static_cast<long long>(p.B) * p.Hkv, 128))
+  if (int rc = encode_rows(&k.tmap_v, static_cast<const char*>(p.v) + skip, p.D, nk, heads, 128,
+                           p.Nk))
     return rc;
   k.o = p.o;
   k.lse = p.lse;
@@ -219,14 +223,15 @@ int mod_fwd(const ModFwdParams& p, cudaStream_t stream) {
   k.Hkv = p.Hkv;
   k.G = p.Hq / p.Hkv;
   k.Nq = p.Nq;
-  k.Nk = p.Nk;
+  k.Nk = nk;
   k.causal = p.causal;
-  k.q_offset = p.q_offset;
+  k.q_offset = p.q_offset - key0;
+  k.key0 = key0;
   // Rows that see different keys: items of later rows, as a rule the longer
   // ones, first, in groups of heads whose K and V take about a third of the
   // L2 (as in fwd_sm103a.cu).
   k.longest_first = p.causal || p.ranges;
-  const double kv_bytes = 4.0 * p.Nk * p.D;
+  const double kv_bytes = 4.0 * nk * p.D;
   const int kv_heads = std::max(1, std::min(static_cast<int>(40.0e6 / kv_bytes), p.B * p.Hkv));
   k.group_heads = kv_heads * k.G;
   k.o_sectors = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
@@ -236,6 +241,97 @@ int mod_fwd(const ModFwdParams& p, cudaStream_t stream) {
   const cudaError_t e = p.D == 128 ? launch_mod_fwd_d128(k, grid, di.dev, stream)
                                    : launch_mod_fwd_d64(k, grid, di.dev, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+// Adds a segment's result (O, LSE of the output tensors) to the sum of those before,
+//   acc = sum_i e^(LSE_i - T) O_i,  state = (T, sum_i e^(LSE_i - T)),
+// T the largest LSE so far.  The first segment starts the sum, the last one leaves
+// O = acc / sum and LSE = T + ln sum in the output.  A warp per row and turn; 10
+// bytes read and written per element, next to 2^18 keys a row.
+template <int D>
+__global__ void __launch_bounds__(256)
+    segment_merge_kernel(__nv_bfloat16* o, float* lse, float* acc, float2* states, long long rows,
+                         bool first, bool last) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long warps = static_cast<long long>(gridDim.x) * 8;
+  for (long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < rows;
+       row += warps) {
+    const float2 before = first ? make_float2(-CUDART_INF_F, 0.f) : states[row];
+    const float x = lse[row];
+    // (a NaN stays one)
+    const float top = x != x || before.x != before.x ? x + before.x : fmaxf(x, before.x);
+    const bool none = top == -CUDART_INF_F;
+    const float wa = none ? 0.f : expf(before.x - top), ws = none ? 0.f : expf(x - top);
+    const float sum = fmaf(before.y, wa, ws);
+    const float out = last ? (none ? 0.f : 1.f / sum) : 1.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const long long at = row * D + i * 32 + lane;
+      // (a weight of 0 takes nothing, not even from a NaN that stands there)
+      float v = first || wa == 0.f ? 0.f : wa * acc[at];
+      if (ws != 0.f) v = fmaf(ws, __bfloat162float(o[at]), v);
+      if (last)
+        o[at] = __float2bfloat16_rn(v * out);
+      else
+        acc[at] = v;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      if (last)
+        lse[row] = none ? top : top + logf(sum);
+      else
+        states[row] = make_float2(top, sum);
+    }
+  }
+}
+
+struct SegmentsLaunch {
+  const ModFwdParams* p;
+  const DeviceInfo* di;
+  int count;  // segments that some row can see
+  long long rows;
+  size_t states;  // offset into the scratch
+};
+
+int launch_segments(void* ctx, void* scratch, cudaStream_t stream) {
+  const SegmentsLaunch& d = *static_cast<SegmentsLaunch*>(ctx);
+  const ModFwdParams& p = *d.p;
+  float* acc = static_cast<float*>(scratch);
+  float2* states = reinterpret_cast<float2*>(static_cast<char*>(scratch) + d.states);
+  const unsigned grid =
+      static_cast<unsigned>(std::min<long long>((d.rows + 7) / 8, 8ll * d.di->sms));
+  for (int i = 0; i < d.count; ++i) {
+    const int key0 = i * kSegmentKeys;
+    if (int rc = launch_fwd(p, *d.di, key0, std::min(kSegmentKeys, p.Nk - key0), stream)) return rc;
+    const bool first = i == 0, last = i == d.count - 1;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o);
+    if (p.D == 128)
+      segment_merge_kernel<128><<<grid, 256, 0, stream>>>(o, p.lse, acc, states, d.rows, first,
+                                                           last);
+    else
+      segment_merge_kernel<64><<<grid, 256, 0, stream>>>(o, p.lse, acc, states, d.rows, first,
+                                                           last);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_LAUNCH;
+  }
+  return ATTN_OK;
+}
+
+}  // namespace
+
+int mod_fwd(const ModFwdParams& p, cudaStream_t stream) {
+  DeviceInfo di;
+  if (int rc = device_info(&di)) return rc;
+  // without ranges, causal rows see no key behind the last one's position
+  const long long seen =
+      p.causal ? std::min<long long>(p.Nk, static_cast<long long>(p.q_offset) + p.Nq) : p.Nk;
+  if (p.Nk <= kSegmentKeys) return launch_fwd(p, di, 0, p.Nk, stream);
+  if (seen <= kSegmentKeys) return launch_fwd(p, di, 0, static_cast<int>(seen), stream);
+  SegmentsLaunch d = {&p, &di, static_cast<int>((seen + kSegmentKeys - 1) / kSegmentKeys),
+                      static_cast<long long>(p.B) * p.Hq * p.Nq, 0};
+  d.states = static_cast<size_t>(d.rows) * p.D * sizeof(float);
+  return with_own_scratch(d.states + static_cast<size_t>(d.rows) * sizeof(float2), stream,
+                          launch_segments, &d);
 }
 
 int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
@@ -265,7 +361,6 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   k.Nk = p.Ncap;
   k.Np = p.Np;
   common_params(&k, p.mod, di);
-
   const long long prefix_items =
       p.Np > 0 ? static_cast<long long>(p.Hkv) * k.row_blocks : 0;
   const long long most_tiles = prefix_items * k.prefix_tiles + heads * ((p.Ncap + 127ll) / 128);
@@ -274,9 +369,17 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   d.D = p.D;
   d.dev = di.dev;
   d.ctas = static_cast<unsigned>(std::min<long long>({di.sms, most_tiles, kMostCtas}));
-  // slot of a state: its item's number + its run's
-  const size_t pre = p.Np > 0 ? static_cast<size_t>(prefix_items + d.ctas) * k.pre_rows : 0;
-  const size_t own = static_cast<size_t>(heads + 2ll * d.ctas) * k.G;
+  // slot of a state: its item's number + its piece's
+  const uint32_t pre_tiles = prefix_total(k), own_tiles = static_cast<uint32_t>(
+                                                  heads * ((p.Ncap + 127ll) / 128));
+  const uint32_t pre_runs = std::min(pre_tiles, d.ctas), own_runs = std::min(own_tiles, 2 * d.ctas);
+  const size_t pre =
+      p.Np > 0 ? (prefix_items + static_cast<size_t>(pre_runs) *
+                                     Pieces(pre_tiles, pre_runs).per_run) * k.pre_rows
+               : 0;
+  // (with fewer keys than the caches hold there are fewer pieces)
+  const size_t own =
+      (heads + static_cast<size_t>(own_runs) * Pieces(own_tiles, own_runs).per_run) * k.G;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   d.pre_o = up((static_cast<size_t>(p.B) + 1) * sizeof(uint32_t));
   d.pre_lse = d.pre_o + up(pre * p.D * sizeof(float));

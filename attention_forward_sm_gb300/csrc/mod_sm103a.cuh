@@ -45,7 +45,7 @@
 //   * Decode of own keys: DRAM.  8 requests of up to 64k keys, Hkv8 D128: 91, 533
 //     MB at 6.1 TB/s in this kernel (91% of a measured copy).
 //   * Decode behind a prefix: softmax and products of the prefix first, then DRAM.
-//     64 requests behind 16384 keys 45, 256 (capped) behind 8192 79.
+//     64 requests behind 16384 keys 45, 256 (capped) behind 8192 81.
 // Code that is not in the instruction cache shows: 264 KB of a decode instead of
 // 96 KB cost it 40% of its time, and a prefill's rarely taken ways 5 to 15%.
 #pragma once
@@ -545,8 +545,8 @@ __device__ __forceinline__ Work plan_unit(const ModKernelParams& p, int u, int2*
     hi[0] = hi[1] = 0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      r[i].x = max(r[i].x, 0);
-      r[i].y = min(r[i].y, p.Nk);
+      r[i].x = max(max(r[i].x, 0) - p.key0, 0);
+      r[i].y = min(max(r[i].y, 0) - p.key0, p.Nk);
       if (p.causal) r[i].y = min(r[i].y, p.q_offset + w.q0 + i * 32 + lane + 1);
       if (r[i].x < r[i].y) {
         lo[i / (kRows / 2)] = min(lo[i / (kRows / 2)], r[i].x);
@@ -610,14 +610,17 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
 
 // Decode: the prefix tiles of this CTA's run, [x, end), item by item.
 struct PrefixPlan {
-  uint32_t x, end;
+  uint32_t begin, x, end;
+  Pieces pieces = Pieces(0, 1);
   __device__ __forceinline__ void start(const ModKernelParams& p) {
     const uint32_t total = prefix_total(p);
     const uint32_t runs = min(total, gridDim.x);
-    x = end = 0;
+    begin = x = end = 0;
     if (blockIdx.x < runs) {
       x = run_start(total, runs, blockIdx.x);
       end = run_start(total, runs, blockIdx.x + 1);
+      begin = x;
+      pieces = Pieces(total, runs);
     }
   }
   __device__ __forceinline__ bool next(const ModKernelParams& p, Work& w) {
@@ -625,13 +628,15 @@ struct PrefixPlan {
     const uint32_t tiles = p.prefix_tiles, item = x / tiles;
     w.tile0 = static_cast<int>(x - item * tiles);
     w.n = static_cast<int>(min(tiles - w.tile0, end - x));
+    if (pieces.per_run > 1)
+      w.n = min(w.n, static_cast<int>(pieces.tiles - (x - begin) % pieces.tiles));
     w.kind = 0;
     w.edges = 0;
     w.id = static_cast<int>(item) / p.row_blocks;
     w.q0 = (static_cast<int>(item) - w.id * p.row_blocks) * 2 * p.per_tile;
     w.lo = 0;
     w.hi = p.Np;
-    w.slot = static_cast<int>(item + blockIdx.x);
+    w.slot = static_cast<int>(item + pieces.of(blockIdx.x, x - begin));
     w.a[0] = w.a[1] = 0;
     w.b[0] = w.n;
     w.b[1] = w.q0 + p.per_tile < p.B ? w.n : 0;
@@ -648,6 +653,7 @@ struct PrefixPlan {
 struct OwnPlan {
   int left;        // tiles left of the run
   int run;
+  Pieces pieces = Pieces(0, 1);
   int b0, at;      // request b0 + at, of a block of 32 that the lanes hold
   int id, tile0;   // KV head, tile within the item
   int len, tiles;  // this lane's request: its keys and key tiles
@@ -674,6 +680,7 @@ struct OwnPlan {
       mine = run_start(total, runs, r + 1) - x;
     }
     run = static_cast<int>(r);
+    pieces = Pieces(total, runs);
     left = static_cast<int>(mine);
     at = id = tile0 = 0;
     if (left == 0) return;
@@ -701,19 +708,22 @@ struct OwnPlan {
     w.hi = __shfl_sync(0xFFFFFFFFu, len, at);
     w.id = id;
     w.tile0 = tile0;
+    const uint32_t done = mine - left;
     w.n = min(nt - tile0, left);
+    if (pieces.per_run > 1) w.n = min(w.n, static_cast<int>(pieces.tiles - done % pieces.tiles));
     w.kind = 1;
     w.q0 = b0 + at;
     w.lo = 0;
-    w.slot = w.q0 * p.Hkv + id + run;
+    w.slot = w.q0 * p.Hkv + id + static_cast<int>(pieces.of(run, done));
     w.a[0] = w.a[1] = 0;
     w.b[0] = t ? 0 : w.n;
     w.b[1] = t ? w.n : 0;
     w.edges = w.hi < (tile0 + w.n) * kBN ? 2 : 0;
     w.v_first = ring0;
-    w.v_last = mine - left;
+    w.v_last = done;
     left -= w.n;
-    if (left > 0) {
+    tile0 += w.n;
+    if (left > 0 && tile0 == nt) {
       tile0 = 0;
       if (++id == p.Hkv) {
         id = 0;

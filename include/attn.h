@@ -342,6 +342,11 @@ int attn_decode_graph_destroy(attn_decode_graph *graph);
  *   range sees nothing).  With causal != 0 it sees of these only j <= p_i.
  *   attn_row_ranges makes the ranges of packed documents and prefixes.
  *
+ * Rows that can see more than 2^18 keys are computed 2^18 keys at a time, since
+ * the tensor cores' accumulators lose up to 2^-27 of a sum with every term; the
+ * parts (O in bf16) are joined in fp32.  Such a call takes (D + 2) * 4 bytes of
+ * scratch per row and head, allocated and freed on the stream (ATTN_ERR_ALLOC).
+ *
  * Limits: those of attn_fwd_rows; ranges 8-byte aligned, slopes 4-byte
  * aligned (ATTN_ERR_ALIGN).
  */

@@ -679,3 +679,58 @@ def test_threads_with_streams_of_their_own_under_one_handle():
         assert done[i] == [0] * 20
         for o, lse in outs:
             check_decode(o, lse, q, k, v, lens, 0.0, None)
+
+
+def test_rows_of_more_keys_than_an_accumulator_takes():
+    """128 rows of 1.9e8 keys, 128 that see the last key alone.  Every weight is 1 and
+    every sum of one accumulator a multiple of 16 below 2^19: exact."""
+    N = 190_000_000
+    if torch.cuda.mem_get_info()[0] < 60 * 2**30:
+        pytest.skip("needs 49 GB")
+    k = torch.zeros((1, 1, N, 64), dtype=torch.bfloat16, device="cuda")
+    v = torch.ones((1, 1, N, 64), dtype=torch.bfloat16, device="cuda")
+    ranges = torch.tensor([[[0, N]] * 128 + [[N - 1, N]] * 128], dtype=torch.int32, device="cuda")
+    o, lse = attn.forward_mod(rand(1, (1, 1, 256, 64)), k, v, ranges=ranges)
+    torch.cuda.synchronize()
+    assert attn.attn_get_device_error() == 0
+    assert bool((o == 1).all()) and bool((lse[..., 128:] == 0).all())
+    assert bool(((lse[..., :128] - math.log(N)).abs() < 1e-4).all())
+
+
+@pytest.mark.parametrize("heads", [2, 12])
+def test_runs_of_more_keys_than_an_accumulator_takes(heads):
+    """As above for single tokens: a CTA's share of the keys, own ones and those of a
+    prefix, goes into several partial states."""
+    N = 150_000_000
+    if torch.cuda.mem_get_info()[0] < 60 * 2**30:
+        pytest.skip("needs 39 GB")
+    k = torch.zeros((1, 1, N, 64), dtype=torch.bfloat16, device="cuda")
+    v = torch.ones((1, 1, N, 64), dtype=torch.bfloat16, device="cuda")
+    q = rand(1, (1, heads, 64))
+    lens = torch.tensor([N - 77], dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_varlen(q, k, v, lens)
+    assert bool((o == 1).all()) and bool(((lse - math.log(N - 77)).abs() < 1e-4).all())
+    own = k[:, :, :1000].contiguous()
+    lens = torch.tensor([1000], dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_prefix(q, k[0], v[0], own, torch.ones_like(own), lens)
+    assert bool((o == 1).all()) and bool(((lse - math.log(N + 1000)).abs() < 1e-4).all())
+
+
+@pytest.mark.parametrize("D,cap,bias,kind", [
+    (64, 0.0, 0, "causal"), (128, 20.0, 0, "ranges"), (64, 0.0, 1, "ranges"), (128, 20.0, -1, "causal ranges"),
+    (64, 0.0, 0, "early")])
+def test_prefill_of_several_segments_of_keys(D, cap, bias, kind):
+    """Keys in three segments: rows that see all, some or none of them."""
+    Hq, Hkv, Nq, Nk = 2, 1, 140, 600_000
+    q, k, v = rand(1, (1, Hq, Nq, D)), rand(2, (1, Hkv, Nk, D)), rand(3, (1, Hkv, Nk, D))
+    # (a bias of a few units over the length: both near and far keys count)
+    slopes = torch.tensor([3e-6, 1e-5], device="cuda") * bias if bias else None
+    q_offset = 1000 if kind == "early" else Nk - Nq - 30_000
+    ranges = None
+    if "ranges" in kind:
+        rows = [(0, Nk), (5, 6), (262_143, 262_145), (262_144, 524_288), (300_000, 299_999), (100, 599_990),
+                (524_200, Nk), (599_999, Nk + 50), (-3, 262_144)]
+        ranges = torch.tensor([[rows[i % len(rows)] for i in range(Nq)]], dtype=torch.int32, device="cuda")
+    causal = "causal" in kind or kind == "early"
+    o, lse = attn.forward_mod(q, k, v, causal=causal, softcap=cap, slopes=slopes, ranges=ranges, q_offset=q_offset)
+    check_fwd(o, lse, q, k, v, causal, 1 / math.sqrt(D), cap, slopes, ranges, q_offset)
