@@ -195,6 +195,19 @@ def test_bias_of_far_positions(slope, q_offset):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 20.0, 0.5])
+@pytest.mark.parametrize("kind", [None, "wild", "prefix"])
+def test_bias_of_keys_on_both_sides(D, cap, kind):
+    """Slopes of either sign, shallow and steep, for rows that see keys on both sides
+    of their position, on one side, or none; scores within the cap and far beyond."""
+    q, k, v = rand(1, (1, 6, 260, D), 2.0), rand(2, (1, 2, 390, D)), rand(3, (1, 2, 390, D))
+    slopes = torch.tensor([0.02, -0.02, 0.9, -0.9, 6.0, 0.0], device="cuda")
+    r = ranges_of(kind, 1, 260, 390) if kind else None
+    o, lse = attn.forward_mod(q, k, v, softcap=cap, slopes=slopes, ranges=r, q_offset=60)
+    check_fwd(o, lse, q, k, v, False, 1 / math.sqrt(D), cap, slopes, r, 60)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, False), (30.0, True)])
 @pytest.mark.parametrize("trash", [NAN, INF, -INF])
 def test_trash_in_keys_that_no_row_sees(D, cap, bias, trash):
