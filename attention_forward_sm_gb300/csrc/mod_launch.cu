@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/attn.h"
 #include "score_mod.cuh"
@@ -41,11 +42,11 @@ struct CombineParams {
 template <int D>
 __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p) {
   constexpr int E = D / 32;
-  // programmatic dependent launch: wait for the split kernel's results
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // programmatic dependent launch: what needs no result of the split kernel goes in
+  // front of the wait for it, beside that kernel's last CTAs
   const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.B) * p.Hq) return;
+  const uint32_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= static_cast<uint32_t>(p.B) * p.Hq) return;
   const int b = static_cast<int>(row / p.Hq), h = static_cast<int>(row % p.Hq);
   const int hkv = h / p.G, g = h % p.G;
 
@@ -53,7 +54,6 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
   // group one slot apart
   long long first[2] = {0, 0};
   int count[2] = {0, 0};
-  const uint32_t before = p.plan[b], nt = p.plan[b + 1] - before, own = p.plan[p.B] * p.Hkv;
   if (p.prefix_tiles > 0) {
     const uint32_t all = p.prefix_total, runs = min(all, p.ctas);
     const int item = hkv * p.row_blocks + b / (2 * p.per_tile);
@@ -64,6 +64,10 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
     const int in_tile = b % p.per_tile, tile = (b / p.per_tile) & 1;
     first[0] = static_cast<long long>(item + r0) * p.pre_rows + tile * 128 + in_tile * p.G + g;
   }
+  const int len = p.lens ? min(max(p.lens[b], 0), p.Nk) : p.Nk;
+  const float slope = p.slopes ? p.slopes[h] : 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint32_t before = p.plan[b], nt = p.plan[b + 1] - before, own = p.plan[p.B] * p.Hkv;
   if (nt > 0) {
     const uint32_t runs = min(own, 2 * p.ctas);
     const uint32_t t0 = before * p.Hkv + hkv * nt;
@@ -77,16 +81,28 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
     return i < count[0] ? p.pre_lse[first[0] + static_cast<long long>(i) * p.pre_rows]
                         : p.part_lse[first[1] + static_cast<long long>(i - count[0]) * p.G];
   };
-  float m = -CUDART_INF_F;
+  using Vec = std::conditional_t<E == 4, float4, float2>;
+  auto state_of = [&](int i) {
+    const float* src = i < count[0]
+                           ? p.pre_o + (first[0] + static_cast<long long>(i) * p.pre_rows) * D
+                           : p.part_o + (first[1] + static_cast<long long>(i - count[0]) * p.G) * D;
+    return reinterpret_cast<const Vec*>(src)[lane];
+  };
+  // the first states come in together with the lse
+  constexpr int kAhead = 4;
+  Vec ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (i < total) ahead[i] = state_of(i);
+  // the largest lse, as integers of the same order; a NaN state stays one
+  int top = INT_MIN;
   for (int i = lane; i < total; i += 32) {
     const float x = lse_of(i);
-    m = x != x || m != m ? x + m : fmaxf(m, x);  // a NaN state stays one
+    const int y = __float_as_int(x);
+    top = max(top, x != x ? INT_MAX : y ^ ((y >> 31) & INT_MAX));
   }
-#pragma unroll
-  for (int d = 16; d >= 1; d /= 2) {
-    const float x = __shfl_xor_sync(0xFFFFFFFFu, m, d);
-    m = x != x || m != m ? x + m : fmaxf(m, x);
-  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  const float m = total > 0 ? __int_as_float(top ^ ((top >> 31) & INT_MAX)) : -CUDART_INF_F;
   const bool none = m == -CUDART_INF_F;
   float sum = 0.f, o[E];
 #pragma unroll
@@ -94,38 +110,33 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
   if (!none) {
     for (int i0 = 0; i0 < total; i0 += 32) {
       const float w_lane = i0 + lane < total ? ex2_approx(lse_of(i0 + lane) - m) : 0.f;
-      sum += w_lane;
       const int n = min(32, total - i0);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
+      auto add = [&](int i, const Vec& x) {
         const float w = __shfl_sync(0xFFFFFFFFu, w_lane, i);
-        const int at = i0 + i;
-        const float* src =
-            at < count[0]
-                ? p.pre_o + (first[0] + static_cast<long long>(at) * p.pre_rows) * D
-                : p.part_o + (first[1] + static_cast<long long>(at - count[0]) * p.G) * D;
+        sum += w;
+        o[0] = fmaf(w, x.x, o[0]);
+        o[1] = fmaf(w, x.y, o[1]);
         if constexpr (E == 4) {
-          const float4 x = reinterpret_cast<const float4*>(src)[lane];
-          o[0] = fmaf(w, x.x, o[0]);
-          o[1] = fmaf(w, x.y, o[1]);
           o[2] = fmaf(w, x.z, o[2]);
           o[3] = fmaf(w, x.w, o[3]);
-        } else {
-          const float2 x = reinterpret_cast<const float2*>(src)[lane];
-          o[0] = fmaf(w, x.x, o[0]);
-          o[1] = fmaf(w, x.y, o[1]);
         }
-      }
-    }
+      };
+      int i = 0;
+      if (i0 == 0) {
 #pragma unroll
-    for (int d = 16; d >= 1; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        for (int k = 0; k < kAhead; ++k)
+          if (k < total) add(k, ahead[k]);
+        i = min(kAhead, total);
+      }
+#pragma unroll 4
+      for (; i < n; ++i) add(i, state_of(i0 + i));
+    }
   }
   const float inv = none ? 0.f : 1.f / sum;
   uint32_t out[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D) +
-                  lane * (E / 2);
+  uint32_t* dst = static_cast<uint32_t*>(p.o) + static_cast<size_t>(row) * (D / 2) + lane * (E / 2);
   if constexpr (E == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
   else
@@ -133,10 +144,7 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
   if (lane == 0) {
     float lse = none ? -CUDART_INF_F : (m + __log2f(sum)) * kLn2;
     // a negative slope is relative to the farthest key
-    if (p.slopes && !none && p.slopes[h] < 0.f) {
-      const int len = p.lens ? min(max(p.lens[b], 0), p.Nk) : p.Nk;
-      lse -= p.slopes[h] * static_cast<float>(p.Np + len - 1);
-    }
+    if (slope < 0.f && !none) lse -= slope * static_cast<float>(p.Np + len - 1);
     p.lse[row] = lse;
   }
 }
