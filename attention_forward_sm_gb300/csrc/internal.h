@@ -60,7 +60,9 @@ struct ScoreMod {
   float cap_out;        // softcap * log2(e)
   const float* slopes;  // [Hq], or NULL: no distance bias
   // s T(s^2) = the capped score for a raw product |s| <= cap_limit[i] (ascending;
-  // 0: not usable), T of kCapN<i> coefficients.
+  // -1: not usable), T of kCapN<i> coefficients.  At s = cap_off the last two, whose
+  // leading coefficients are negative, are below any score by more than 10^6.
+  float cap_off;
   float cap_limit[3];
   float cap_coef[3][6];
 };

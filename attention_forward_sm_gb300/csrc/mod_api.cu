@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/attn.h"
 #include "internal.h"
 
@@ -28,6 +30,7 @@ void cap_polynomials(ScoreMod* m) {
       {0x1.ffffeep-1, -0x1.5542dap-2, 0x1.0e2146p-3, -0x1.6baa52p-5},
       {0x1.ffffecp-1, -0x1.5549d8p-2, 0x1.0ffd3ap-3, -0x1.a697a8p-5, 0x1.11f45ap-6,
        -0x1.90d924p-9}};
+  constexpr double kOff = 64.0;
   const double in = m->cap_in, out = m->cap_out;
   for (int i = 0; i < 3; ++i) {
     bool fits = in > 0.0;
@@ -37,11 +40,20 @@ void cap_polynomials(ScoreMod* m) {
       m->cap_coef[i][k] = static_cast<float>(x);
       fits = fits && fabs(x) < 1e37 && fabs(x) > 1e-37;
     }
-    // the powers of s have to fit too: (s^2)^(n - 1) up to the limit
+    // what is formed on the way has to fit too, up to the limit and at cap_off
     const double limit = x_most[i] / in;
-    fits = fits && pow(limit, 2.0 * (n[i] - 1)) < 1e37;
-    m->cap_limit[i] = fits ? static_cast<float>(limit) : 0.f;
+    for (const double s : {limit, kOff / in}) {
+      double t = 0.0;
+      for (int k = n[i] - 1; fits && k >= 0; --k) {
+        t = t * (s * s) + m->cap_coef[i][k];
+        fits = fabs(t) < 1e37;
+      }
+      fits = fits && s * s < 1e37 && fabs(s * t) < 1e37;
+      if (i > 0 && s != limit) fits = fits && s * t < -1e6 - 2.0 * out;
+    }
+    m->cap_limit[i] = fits ? static_cast<float>(limit) : -1.f;
   }
+  m->cap_off = in > 0.0 ? static_cast<float>(kOff / in) : 0.f;
 }
 
 // Checks scale, softcap and slopes and fills *m.

@@ -36,8 +36,8 @@
 // What bounds it and what it measures (us on a GB300, by CUDA events).
 //   * Prefill, long rows: the chain of a query tile, product, softmax, product,
 //     of which two run at a time.  B1 Hq32 Hkv8 N8192 D128 causal: 344 (1.60
-//     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 467, biased 460,
-//     both 571; D64 274, 442, 381.  The tensor pipe is 49% busy capped, the issue
+//     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 462, biased 460,
+//     both 568; D64 274, 453, 383.  The tensor pipe is 49% busy capped, the issue
 //     slots 55%: a pass over a tile is longer than the products of the other.
 //   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
 //     for its first scores and its epilogue next to 2.9k a tile.  Packed documents
@@ -240,12 +240,17 @@ __device__ __forceinline__ void mask_to(float (&s)[64], const Seen& m, float wit
 // on both sides has no such c0.
 constexpr float kLoose = 100.f;
 
-template <bool kCap, bool kBias>
+template <int D, bool kCap, bool kBias>
 struct Scores {
+  // A capped tile's unseen keys: 0 for the maximum and cap_off for the weights in one
+  // go, or one after the other around a loop that masked tiles share with others.
+  // Which one the compiler makes the better kernel of: B1 Hq32 Hkv8 N8192 causal D128
+  // 462 us (one after the other 472), D64 467 (453).
+  static constexpr bool kOneGo = D == 128;
   static constexpr int kModified = 4;
-  int tier;          // capped: which polynomial; 3: the longest, some keys unseen or
-                     // not linear; kModified: the scores are modified already
-  Seen seen;         // (of 3)
+  int tier;          // capped: which polynomial; 3: the longest, not linear;
+                     // kModified: the scores are modified already
+  Seen seen;         // if masked
   bool linear;
   float slope, rel;  // biased: key kb + i has bias -slope * |rel + i|, slope >= 0
   float most[4];     // bias of the most favoured key: capped: of the tile, in [0];
@@ -286,30 +291,47 @@ struct Scores {
         }
       }
     }
-    if (masked || !linear) seen = seen_columns(row.lo - kb, row.hi - kb);
+    if (masked) seen = seen_columns(row.lo - kb, row.hi - kb);
   }
 
   // From s to the row's m for the tile (both halves); false: it cannot be fused.
   __device__ __forceinline__ bool prepare(float (&s)[64], const ModKernelParams& p, bool masked,
                                           float& m) {
     if constexpr (kCap) {
-      if (masked) mask_to(s, seen, 0.f);  // what lies at unseen keys has no say
       float a0 = 0.f, a1 = 0.f;
+      // what lies at unseen keys has no say, and gets a weight of 0
+      if (!kOneGo && masked) mask_to(s, seen, 0.f);
+      if (kOneGo && masked) {
 #pragma unroll
-      for (int i = 0; i < 64; i += 4) {
-        a0 = max3f(a0, fabsf(s[i]), fabsf(s[i + 1]));
-        a1 = max3f(a1, fabsf(s[i + 2]), fabsf(s[i + 3]));
+        for (int i = 0; i < 64; i += 2) {
+          const bool in0 = (seen.words[i / 32] >> (i % 32)) & 1u;
+          const bool in1 = (seen.words[i / 32] >> (i % 32 + 1)) & 1u;
+          const float x0 = in0 ? s[i] : 0.f, x1 = in1 ? s[i + 1] : 0.f;
+          if (i % 4 == 0)
+            a0 = max3f(a0, fabsf(x0), fabsf(x1));
+          else
+            a1 = max3f(a1, fabsf(x0), fabsf(x1));
+          s[i] = in0 ? s[i] : p.mod.cap_off;
+          s[i + 1] = in1 ? s[i + 1] : p.mod.cap_off;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          a0 = max3f(a0, fabsf(s[i]), fabsf(s[i + 1]));
+          a1 = max3f(a1, fabsf(s[i + 2]), fabsf(s[i + 3]));
+        }
       }
       a0 = fmaxf(a0, a1);
       // the shortest polynomial that holds for all of the warp's scores
       // (magnitudes are ordered like their bits)
       const float all = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a0)));
-      tier = all <= p.mod.cap_limit[0] ? 0 : (all <= p.mod.cap_limit[1] ? 1 : 2);
-      const bool holds = all <= p.mod.cap_limit[2] || (tier < 2 && !masked && linear);
-      if (masked || !linear) tier = 3;
+      tier = !masked && all <= p.mod.cap_limit[0] ? 0 : (all <= p.mod.cap_limit[1] ? 1 : 2);
+      if (!linear) tier = 3;
+      const bool holds = tier < 2 || all <= p.mod.cap_limit[2];
       // no score of the warp's rows is larger: |tanh x| <= |x|, 1
       const float top = fminf(all * p.scale_log2, p.mod.cap_out);
       m = kBias ? top + most[0] : top;
+      if (!kOneGo && masked) mask_to(s, seen, p.mod.cap_off);
       return holds && 2.f * top <= kLoose;
     } else {
       if (masked) mask_to(s, seen, -CUDART_INF_F);
@@ -381,14 +403,14 @@ struct Scores {
   // pk = the weights as bf16 pairs, low key first; returns their sum in fp32
   // before the rounding to bf16 (2^-9 of a weight on average: its effect on O
   // is that of the rounding of O itself).  Unseen keys are -inf and give
-  // exactly 0 (scale_log2 is never 0, see mod_launch.cu).
+  // exactly 0 (scale_log2 is never 0, see mod_launch.cu); capped they are cap_off,
+  // for which the polynomials give less than -10^6.
   __device__ __forceinline__ float weights(const float (&s)[64], const ModKernelParams& p,
                                            float neg_m, uint32_t (&pk)[32]) const {
     uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
-    // pass(.., f): f(pair of s, what to add to its scores) -> exponents; with_mask:
-    // unseen keys get -inf for theirs
+    // pass(.., f): f(pair of s, what to add to its scores) -> exponents
     enum Bias { kNone, kLinear, kBent };
-    auto pass = [&](Bias bias, bool with_mask, auto f) {
+    auto pass = [&](Bias bias, auto f) {
       uint64_t add = f32x2(neg_m, neg_m), a = add;
       // linear: the bias minus m itself; else what |.| is taken of
       const float step = bias == kBent || rel < 0.f ? slope : -slope;
@@ -419,13 +441,6 @@ struct Scores {
         float x0, x1, x2, x3;
         unpack_f32x2(f(f32x2(s[e], s[e + 1]), add2[0]), x0, x1);
         unpack_f32x2(f(f32x2(s[e + 2], s[e + 3]), add2[1]), x2, x3);
-        if (with_mask) {
-          const uint32_t w = seen.words[e / 32];
-          x0 = (w >> (e % 32)) & 1u ? x0 : -CUDART_INF_F;
-          x1 = (w >> (e % 32 + 1)) & 1u ? x1 : -CUDART_INF_F;
-          x2 = (w >> (e % 32 + 2)) & 1u ? x2 : -CUDART_INF_F;
-          x3 = (w >> (e % 32 + 3)) & 1u ? x3 : -CUDART_INF_F;
-        }
         const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
         const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
         acc0 = add_f32x2(acc0, f32x2(p0, p1));
@@ -436,23 +451,23 @@ struct Scores {
     };
     constexpr Bias kLin = kBias ? kLinear : kNone;
     if ((kCap || kBias) && tier == kModified) {
-      pass(kNone, false, [](uint64_t x, uint64_t add) { return add_f32x2(x, add); });
+      pass(kNone, [](uint64_t x, uint64_t add) { return add_f32x2(x, add); });
     } else if constexpr (kCap) {
       if (tier == 0)
-        pass(kLin, false, CapPoly<kCapN0>(p.mod.cap_coef[0]));
+        pass(kLin, CapPoly<kCapN0>(p.mod.cap_coef[0]));
       else if (tier == 1)
-        pass(kLin, false, CapPoly<kCapN1>(p.mod.cap_coef[1]));
-      else if (tier == 2)
-        pass(kLin, false, CapPoly<kCapN2>(p.mod.cap_coef[2]));
+        pass(kLin, CapPoly<kCapN1>(p.mod.cap_coef[1]));
+      else if (!kBias || tier == 2)
+        pass(kLin, CapPoly<kCapN2>(p.mod.cap_coef[2]));
       else
-        pass(kBias ? kBent : kNone, true, CapPoly<kCapN2>(p.mod.cap_coef[2]));
+        pass(kBent, CapPoly<kCapN2>(p.mod.cap_coef[2]));
     } else {
       const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
       auto scaled = [&](uint64_t x, uint64_t add) { return fma_f32x2(x, scale2, add); };
       if (kBias && !linear)
-        pass(kBent, false, scaled);
+        pass(kBent, scaled);
       else
-        pass(kLin, false, scaled);
+        pass(kLin, scaled);
     }
     float u0, u1;
     unpack_f32x2(add_f32x2(acc0, acc1), u0, u1);
@@ -1186,7 +1201,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
           masked = kt < seen.x || kt + kBN > seen.y;
           dead = kt >= seen.w || kt + kBN <= seen.z;  // no row sees a key of the tile
         }
-        Scores<kCap, kBias> scores;
+        Scores<D, kCap, kBias> scores;
         bool slow = false;
         if (!dead) {
           scores.look(&ms.rows[t * kBM + r], &ms.slopes[t * kBM + r], kt, kt + c * 64, masked);
