@@ -195,6 +195,24 @@ def test_bias_of_far_positions(slope, q_offset):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [1e-30, 1e-7, 1e-3, 0.3, 1e4, 1e12, 1e30])
+@pytest.mark.parametrize("bias", [False, True])
+def test_caps_far_from_the_scores_in_masked_tiles(D, cap, bias):
+    """Caps for which some polynomials, or all, cannot be formed in fp32; scores of
+    0 too; rows that see a part of a tile, with anything at the keys they do not see."""
+    q, k, v = rand(1, (1, 2, 200, D)), rand(2, (1, 1, 300, D)), rand(3, (1, 1, 300, D))
+    k[:, :, 40:60] = 0
+    k[:, :, 291:] = 1e30
+    ranges = torch.tensor([[[i % 97, min(290, i + 50)] for i in range(200)]], dtype=torch.int32, device="cuda")
+    slopes = torch.tensor([0.1, 0.01], device="cuda") if bias else None
+    o, lse = attn.forward_mod(q, k, v, softcap=cap, slopes=slopes, ranges=ranges)
+    check_fwd(o, lse, q, k, v, False, 1 / math.sqrt(D), cap, slopes, ranges, 0)
+    lens = torch.tensor([290], dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_varlen(q[:, :, 0].contiguous(), k, v, lens, softcap=cap, slopes=slopes)
+    check_decode(o, lse, q[:, :, 0], k, v, [290], cap, slopes)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("cap", [0.0, 20.0, 0.5])
 @pytest.mark.parametrize("kind", [None, "wild", "prefix"])
 def test_bias_of_keys_on_both_sides(D, cap, kind):
