@@ -120,6 +120,7 @@ struct ModKernelParams {
   int Np, prefix_tiles;            // shared prefix: keys, key tiles
   int row_blocks, per_tile;        // its items per KV head; requests per query tile
   int pre_rows;                    // rows of a prefix item's partial states
+  float prefix_cost, own_cost;     // what a key tile of either costs a CTA
   float* pre_o;                    // partial states of prefix items: [slot, pre_rows, D]
   float* pre_lse;                  // (log2 units, bias relative to its reference)
   float* part_o;                   // of the requests' own keys: [slot, G, D]
@@ -146,6 +147,19 @@ __host__ __device__ inline uint32_t run_start(uint32_t total, uint32_t runs, uin
 }
 __host__ __device__ inline uint32_t run_of(uint32_t total, uint32_t runs, uint32_t x) {
   return ((x + 1) * runs - 1) / total;
+}
+// Of `ctas` CTAs, how many have own keys alone, the others then being left to the
+// shared prefix; 0: all have both, one after the other.  Apart, the products of the
+// one run beside the loads of the other, and no CTA goes from one to the other.
+// Either kind needs a tile for each CTA at least, and a share of eight CTAs, that the
+// rounding of the shares does not cost more.
+__host__ __device__ inline uint32_t own_share(uint32_t ctas, uint32_t prefix, uint32_t own,
+                                              float prefix_cost, float own_cost) {
+  if (prefix < ctas || own < ctas) return 0;
+  const float o = own_cost * static_cast<float>(own);
+  const float share = o / (o + prefix_cost * static_cast<float>(prefix));
+  const uint32_t n = static_cast<uint32_t>(static_cast<float>(ctas) * share + 0.5f);
+  return n < 8 || n + 8 > ctas ? 0 : n;
 }
 // Runs of more than kSegmentKeys keys are cut into pieces, equally many per run; an
 // item's part in each has a partial state of its own.

@@ -27,6 +27,7 @@ struct CombineParams {
   const uint32_t* plan;
   int B, Hq, Hkv, G, Nk, Np, row_blocks, per_tile, prefix_tiles, pre_rows;
   uint32_t prefix_total, ctas;
+  float prefix_cost, own_cost;
 };
 
 // One warp per (request, query head): merges the row's partial states,
@@ -35,10 +36,9 @@ struct CombineParams {
 // runs of key tiles give every item's first and last run, and with it its
 // slots.  A lane holds D / 32 consecutive elements of O; the states are
 // few and in L2, so the loads of up to four of them are in flight at once and
-// nothing else is shared.  Bound by latency: 3.5 us behind the split kernel of 8
-// requests with up to 64k keys (256 rows of up to 6 states) and of 256 requests
-// behind a shared prefix (8192 rows of 3 or 4) alike, of which the launch is
-// hidden behind that kernel's end.
+// nothing else is shared.  Bound by latency: 1.5 to 3 us behind the split kernel, of
+// which its plan (of the prefix, where that needs no lengths) and the launch are
+// hidden behind that kernel's end, and the first states come with the lse.
 template <int D>
 __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p) {
   constexpr int E = D / 32;
@@ -54,8 +54,8 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
   // group one slot apart
   long long first[2] = {0, 0};
   int count[2] = {0, 0};
-  if (p.prefix_tiles > 0) {
-    const uint32_t all = p.prefix_total, runs = min(all, p.ctas);
+  auto prefix_parts = [&](uint32_t share) {
+    const uint32_t all = p.prefix_total, runs = min(all, p.ctas - share);
     const int item = hkv * p.row_blocks + b / (2 * p.per_tile);
     const uint32_t t0 = static_cast<uint32_t>(item) * p.prefix_tiles;
     const Pieces pieces(all, runs);
@@ -63,13 +63,21 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
     count[0] = static_cast<int>(piece_of(all, runs, pieces, t0 + p.prefix_tiles - 1) - r0) + 1;
     const int in_tile = b % p.per_tile, tile = (b / p.per_tile) & 1;
     first[0] = static_cast<long long>(item + r0) * p.pre_rows + tile * 128 + in_tile * p.G + g;
-  }
+  };
+  // (CTAs are shared out by the lengths where there are enough tiles of the prefix)
+  const bool shared = p.prefix_total >= p.ctas;
+  if (p.prefix_tiles > 0 && !shared) prefix_parts(0);
   const int len = p.lens ? min(max(p.lens[b], 0), p.Nk) : p.Nk;
   const float slope = p.slopes ? p.slopes[h] : 0.f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t before = p.plan[b], nt = p.plan[b + 1] - before, own = p.plan[p.B] * p.Hkv;
+  uint32_t share = 0;
+  if (shared) {
+    share = own_share(p.ctas, p.prefix_total, own, p.prefix_cost, p.own_cost);
+    prefix_parts(share);
+  }
   if (nt > 0) {
-    const uint32_t runs = min(own, 2 * p.ctas);
+    const uint32_t runs = min(own, 2 * (share ? share : p.ctas));
     const uint32_t t0 = before * p.Hkv + hkv * nt;
     const Pieces pieces(own, runs);
     const uint32_t r0 = piece_of(own, runs, pieces, t0);
@@ -165,7 +173,7 @@ cudaError_t launch_combine(const ModKernelParams& p, unsigned ctas, cudaStream_t
                            p.pre_lse,  p.part_o,   p.part_lse, p.plan,       p.B,
                            p.Hq,       p.Hkv,      p.G,        p.Nk,         p.Np,
                            p.row_blocks, p.per_tile, p.prefix_tiles, p.pre_rows,
-                           prefix_total(p), ctas};
+                           prefix_total(p), ctas, p.prefix_cost, p.own_cost};
   return cudaLaunchKernelEx(&cfg, mod_combine_kernel<D>, c);
 }
 
@@ -368,6 +376,15 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   k.Hkv = p.Hkv;
   k.Nk = p.Ncap;
   k.Np = p.Np;
+  // What a key tile costs a CTA in us: of the prefix, 256 rows, as measured in a
+  // prefill; of own keys, where the shares that follow made the call fastest, with
+  // what short requests cost besides their keys.  Shares against all CTAs doing both:
+  // serving sizes (64 requests of up to 1024 keys behind 16384, D 128, 4 heads per KV
+  // head) 38.5 us, 42.8; 8 heads 34.7, 41.0; 1 head, 256 requests 62.6, 71.2; capped,
+  // 256 behind 8192 75.0, 80.3; D 64, 128 requests 49.5, 51.2.
+  const bool cap = p.mod.cap_out > 0.f, bias = p.mod.slopes != nullptr;
+  k.prefix_cost = (p.D == 128 ? 1.5f : 1.2f) + (cap ? 0.6f : 0.f) + (bias ? 0.5f : 0.f);
+  k.own_cost = p.D == 128 ? 1.15f : 0.6f + (cap ? 0.3f : 0.f) + (k.G > 4 ? 0.2f : 0.f);
   common_params(&k, p.mod, di);
   const long long prefix_items =
       p.Np > 0 ? static_cast<long long>(p.Hkv) * k.row_blocks : 0;
@@ -378,16 +395,11 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   d.dev = di.dev;
   d.ctas = static_cast<unsigned>(std::min<long long>({di.sms, most_tiles, kMostCtas}));
   // slot of a state: its item's number + its piece's
-  const uint32_t pre_tiles = prefix_total(k), own_tiles = static_cast<uint32_t>(
-                                                  heads * ((p.Ncap + 127ll) / 128));
-  const uint32_t pre_runs = std::min(pre_tiles, d.ctas), own_runs = std::min(own_tiles, 2 * d.ctas);
-  const size_t pre =
-      p.Np > 0 ? (prefix_items + static_cast<size_t>(pre_runs) *
-                                     Pieces(pre_tiles, pre_runs).per_run) * k.pre_rows
-               : 0;
-  // (with fewer keys than the caches hold there are fewer pieces)
-  const size_t own =
-      (heads + static_cast<size_t>(own_runs) * Pieces(own_tiles, own_runs).per_run) * k.G;
+  // (n runs of `tiles` in all have at most tiles / kPieceTiles + 2 n pieces)
+  const size_t pre_tiles = prefix_total(k), own_tiles = heads * ((p.Ncap + 127ll) / 128);
+  const size_t pre = p.Np > 0 ? (prefix_items + pre_tiles / kPieceTiles + 2ull * d.ctas) * k.pre_rows
+                              : 0;
+  const size_t own = (heads + own_tiles / kPieceTiles + 4ull * d.ctas) * k.G;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   d.pre_o = up((static_cast<size_t>(p.B) + 1) * sizeof(uint32_t));
   d.pre_lse = d.pre_o + up(pre * p.D * sizeof(float));

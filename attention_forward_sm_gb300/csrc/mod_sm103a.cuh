@@ -23,7 +23,8 @@
 //     end, are cut into equal runs, one per CTA; so are the tiles of the
 //     requests' own keys, whatever the lengths are, two runs per CTA: one for
 //     each query tile, two chains of Q K^T, softmax and P V that do not wait
-//     for one another.  An item cut by a run's end leaves fp32 partial states
+//     for one another.  Where there is enough of both, some CTAs have own keys
+//     alone and the others the prefix (own_share in internal.h).  An item cut by a run's end leaves fp32 partial states
 //     that a second kernel merges through their log-sum-exp.  A prefix tile is
 //     read once for 256 rows, and at fewer than ~300 rows its bytes cost more
 //     than its products.
@@ -42,10 +43,12 @@
 //   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
 //     for its first scores and its epilogue next to 2.9k a tile.  Packed documents
 //     B4 H16 N4096 D128: 91, tensor pipe 37%.
-//   * Decode of own keys: DRAM.  8 requests of up to 64k keys, Hkv8 D128: 91, 533
-//     MB at 6.1 TB/s in this kernel (91% of a measured copy).
-//   * Decode behind a prefix: softmax and products of the prefix first, then DRAM.
-//     64 requests behind 16384 keys 45, 256 (capped) behind 8192 81.
+//   * Decode of own keys: DRAM.  8 requests of up to 64k keys, Hkv8 D128: 89, 533
+//     MB at 6.1 TB/s in this kernel (92% of a measured copy).
+//   * Decode behind a prefix: the prefix' chain of product, softmax, product on some
+//     CTAs (1.5 us a tile of 256 rows, capped 2.1), on the others the latency of short
+//     items of own keys (0.6 us a tile of them at 2.5 tiles an item).  64 requests
+//     behind 16384 keys 39, 256 (capped) behind 8192 75.
 // Code that is not in the instruction cache shows: 264 KB of a decode instead of
 // 96 KB cost it 40% of its time, and a prefill's rarely taken ways 5 to 15%.
 #pragma once
@@ -132,7 +135,7 @@ struct RowInfo {
 
 // Is S_t written in two halves, that of the keys [64, 128) while the softmax warps
 // still have the tile before?  Not with a cap or a bias: D64 B1 Hq32 Hkv8 N8192
-// causal 442 us capped (in halves 449), 390 biased (397); D128 471 (486), 460 (472).
+// causal 453 us capped (in halves 453), 384 biased (392); D128 465 (486), 461 (474).
 template <int D, bool kCap, bool kBias>
 constexpr bool kSplitScores = Cfg<D, false>::kSplitS && !kCap && !kBias;
 
@@ -627,9 +630,9 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {
 struct PrefixPlan {
   uint32_t begin, x, end;
   Pieces pieces = Pieces(0, 1);
-  __device__ __forceinline__ void start(const ModKernelParams& p) {
+  __device__ __forceinline__ void start(const ModKernelParams& p, uint32_t share) {
     const uint32_t total = prefix_total(p);
-    const uint32_t runs = min(total, gridDim.x);
+    const uint32_t runs = min(total, gridDim.x - share);
     begin = x = end = 0;
     if (blockIdx.x < runs) {
       x = run_start(total, runs, blockIdx.x);
@@ -661,9 +664,8 @@ struct PrefixPlan {
 };
 
 // Decode: query tile t's run of the requests' own key tiles (warp-wide).  Run
-// r of 2 x CTAs belongs to query tile r / CTAs; the CTAs count from the other
-// end than those of the prefix, which matters where there are fewer tiles than
-// CTAs.  The tiles of all items are laid end to end, request by request, KV head by
+// r of 2 x CTAs belongs to query tile r / CTAs; the CTAs (those that have own keys)
+// count from the other end than those of the prefix.  The tiles of all items are laid end to end, request by request, KV head by
 // KV head.
 struct OwnPlan {
   int left;        // tiles left of the run
@@ -678,19 +680,23 @@ struct OwnPlan {
     len = b0 + lane < p.B ? request_len(p, b0 + lane) : 0;
     tiles = key_tiles(len);
   }
-  __device__ __forceinline__ void start(const ModKernelParams& p, int t, int lane) {
-    // how many tiles there are: the first requests stay in the lanes
+  // How many tiles there are of all requests; the first ones stay in the lanes.
+  __device__ __forceinline__ uint32_t total_tiles(const ModKernelParams& p, int lane) {
     b0 = 0;
     load_block(p, lane);
     uint32_t own = tiles;
 #pragma unroll 4
     for (int b = 32 + lane; b < p.B; b += 32) own += key_tiles(request_len(p, b));
-    const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, own) * p.Hkv;
-    const uint32_t runs = min(total, 2 * gridDim.x);
-    const uint32_t r = t * gridDim.x + gridDim.x - 1 - blockIdx.x;
+    return __reduce_add_sync(0xFFFFFFFFu, own) * p.Hkv;
+  }
+  __device__ __forceinline__ void start(const ModKernelParams& p, int t, int lane,
+                                        uint32_t total, uint32_t share) {
+    const uint32_t ctas = share ? share : gridDim.x;
+    const uint32_t runs = min(total, 2 * ctas);
+    const uint32_t cta = gridDim.x - 1 - blockIdx.x, r = t * ctas + cta;
     uint32_t x = 0;
     mine = 0;
-    if (r < runs) {
+    if (cta < ctas && r < runs) {
       x = run_start(total, runs, r);
       mine = run_start(total, runs, r + 1) - x;
     }
@@ -1870,9 +1876,17 @@ __global__ void __launch_bounds__(kModThreads, 1)
     int k = 0;
     if constexpr (kSplit) {
       const int t = warp - kModWarpPlan;  // plans for this query tile
+      OwnPlan own;
+      uint32_t total = 0, share = 0;
+      // (else every CTA has both)
+      const bool shared = prefix_total(p) >= gridDim.x;
+      if (shared) {
+        total = own.total_tiles(p, lane);
+        share = own_share(gridDim.x, prefix_total(p), total, p.prefix_cost, p.own_cost);
+      }
       if (p.prefix_tiles > 0) {
         PrefixPlan plan;
-        plan.start(p);
+        plan.start(p, share);
         while (ok && plan.next(p, w)) {
           w.v_first = w.v_last = 0;  // no edges
           ring += 2 * w.n;
@@ -1883,9 +1897,9 @@ __global__ void __launch_bounds__(kModThreads, 1)
         w.a[0] = w.a[1] = w.b[0] = w.b[1] = 0;
         ok = ok && work_publish<kSlots>(ms, p, t, k++, w, abort_flag, lane);
       }
-      OwnPlan plan;
-      plan.start(p, t, lane);
-      while (ok && plan.next(p, t, lane, ring, w))
+      if (!shared) total = own.total_tiles(p, lane);
+      own.start(p, t, lane, total, share);
+      while (ok && own.next(p, t, lane, ring, w))
         ok = work_publish<kSlots>(ms, p, t, k++, w, abort_flag, lane);
       w.n = -1;
       ok = ok && work_publish<kSlots>(ms, p, t, k++, w, abort_flag, lane);
