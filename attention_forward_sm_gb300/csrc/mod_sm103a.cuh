@@ -24,10 +24,10 @@
 //     requests' own keys, whatever the lengths are, two runs per CTA: one for
 //     each query tile, two chains of Q K^T, softmax and P V that do not wait
 //     for one another.  Where there is enough of both, some CTAs have own keys
-//     alone and the others the prefix (own_share in internal.h).  An item cut by a run's end leaves fp32 partial states
-//     that a second kernel merges through their log-sum-exp.  A prefix tile is
-//     read once for 256 rows, and at fewer than ~300 rows its bytes cost more
-//     than its products.
+//     alone and the others the prefix (own_share in internal.h).  An item cut by
+//     a run's end leaves fp32 partial states that a second kernel merges through
+//     their log-sum-exp.  A prefix tile is read once for 256 rows, and at fewer
+//     than ~300 rows its bytes cost more than its products.
 //   * Own keys of at most 8 query heads per KV head are multiplied the other way
 //     round, S^T = K Q^T and O^T += V^T P^T: the 128 keys of a tile are the rows
 //     of the product, so 128 threads share a tile's scores, a key each, where
