@@ -30,7 +30,7 @@ struct CombineParams {
   float prefix_cost, own_cost;
 };
 
-// One warp per (request, query head): merges the row's partial states,
+// W warps per (request, query head), 1 or 8: they merge the row's partial states,
 //   L = log2 sum_c 2^(lse_c),  O = sum_c 2^(lse_c - L) O_c,
 // those of the shared prefix's item and those of the request's own item.  The
 // runs of key tiles give every item's first and last run, and with it its
@@ -39,14 +39,15 @@ struct CombineParams {
 // nothing else is shared.  Bound by latency: 1.5 to 3 us behind the split kernel, of
 // which its plan (of the prefix, where that needs no lengths) and the launch are
 // hidden behind that kernel's end, and the first states come with the lse.
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p) {
   constexpr int E = D / 32;
   // programmatic dependent launch: what needs no result of the split kernel goes in
   // front of the wait for it, beside that kernel's last CTAs
   const int lane = threadIdx.x & 31;
-  const uint32_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= static_cast<uint32_t>(p.B) * p.Hq) return;
+  const int warp = threadIdx.x >> 5, part = warp % W;
+  const uint32_t row = blockIdx.x * (8 / W) + warp / W;
+  if (row >= static_cast<uint32_t>(p.B) * p.Hq) return;  // (a whole block, at W = 8)
   const int b = static_cast<int>(row / p.Hq), h = static_cast<int>(row % p.Hq);
   const int hkv = h / p.G, g = h % p.G;
 
@@ -84,13 +85,17 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
     count[1] = static_cast<int>(piece_of(own, runs, pieces, t0 + nt - 1) - r0) + 1;
     first[1] = (static_cast<long long>(b) * p.Hkv + hkv + r0) * p.G + g;
   }
-  const int total = count[0] + count[1];
-  auto lse_of = [&](int i) {
+  // this warp's parts: every W-th
+  const int all_parts = count[0] + count[1];
+  const int total = all_parts > part ? (all_parts - part + W - 1) / W : 0;
+  auto lse_of = [&](int j) {
+    const int i = part + W * j;
     return i < count[0] ? p.pre_lse[first[0] + static_cast<long long>(i) * p.pre_rows]
                         : p.part_lse[first[1] + static_cast<long long>(i - count[0]) * p.G];
   };
   using Vec = std::conditional_t<E == 4, float4, float2>;
-  auto state_of = [&](int i) {
+  auto state_of = [&](int j) {
+    const int i = part + W * j;
     const float* src = i < count[0]
                            ? p.pre_o + (first[0] + static_cast<long long>(i) * p.pre_rows) * D
                            : p.part_o + (first[1] + static_cast<long long>(i - count[0]) * p.G) * D;
@@ -110,8 +115,8 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
     top = max(top, x != x ? INT_MAX : y ^ ((y >> 31) & INT_MAX));
   }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
-  const float m = total > 0 ? __int_as_float(top ^ ((top >> 31) & INT_MAX)) : -CUDART_INF_F;
-  const bool none = m == -CUDART_INF_F;
+  float m = total > 0 ? __int_as_float(top ^ ((top >> 31) & INT_MAX)) : -CUDART_INF_F;
+  bool none = m == -CUDART_INF_F;
   float sum = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -140,6 +145,34 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
       for (; i < n; ++i) add(i, state_of(i0 + i));
     }
   }
+  if constexpr (W > 1) {
+    // the row's warps through shared memory; the first one goes on
+    __shared__ float sums[8][D], tops[8][2];
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = o[e];
+    if (lane == 0) {
+      tops[warp][0] = m;
+      tops[warp][1] = sum;
+    }
+    __syncthreads();
+    if (part > 0) return;
+    for (int i = 1; i < W; ++i) {
+      const float x = tops[warp + i][0];
+      m = x != x || m != m ? x + m : fmaxf(m, x);
+    }
+    none = m == -CUDART_INF_F;
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float x = tops[warp + i][0];
+      const float w = none || x == -CUDART_INF_F ? 0.f : ex2_approx(x - m);
+      sum = fmaf(w, tops[warp + i][1], sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(w, sums[warp + i][lane * E + e], o[e]);
+    }
+  }
   const float inv = none ? 0.f : 1.f / sum;
   uint32_t out[E / 2];
 #pragma unroll
@@ -157,11 +190,11 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
   }
 }
 
-template <int D>
+template <int D, int W>
 cudaError_t launch_combine(const ModKernelParams& p, unsigned ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   const long long rows = static_cast<long long>(p.B) * p.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 8 / W - 1) / (8 / W)));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -174,7 +207,7 @@ cudaError_t launch_combine(const ModKernelParams& p, unsigned ctas, cudaStream_t
                            p.Hq,       p.Hkv,      p.G,        p.Nk,         p.Np,
                            p.row_blocks, p.per_tile, p.prefix_tiles, p.pre_rows,
                            prefix_total(p), ctas, p.prefix_cost, p.own_cost};
-  return cudaLaunchKernelEx(&cfg, mod_combine_kernel<D>, c);
+  return cudaLaunchKernelEx(&cfg, mod_combine_kernel<D, W>, c);
 }
 
 void common_params(ModKernelParams* k, const ScoreMod& mod, const DeviceInfo& di) {
@@ -190,6 +223,7 @@ struct DecodeLaunch {
   ModKernelParams* k;
   int D, dev;
   unsigned ctas;
+  bool wide;  // the merge: a block per row
   size_t pre_o, pre_lse, part_o, part_lse;  // offsets into the scratch; plan at 0
 };
 
@@ -212,8 +246,9 @@ int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
   const int G = d.k->G, heads = G <= 4 ? 0 : (G <= 8 ? 1 : 2);
   cudaError_t e = split[d.D == 128][heads](*d.k, d.ctas, d.dev, stream);
   if (e == cudaSuccess)
-    e = d.D == 128 ? launch_combine<128>(*d.k, d.ctas, stream)
-                   : launch_combine<64>(*d.k, d.ctas, stream);
+    e = d.D == 128
+            ? (d.wide ? launch_combine<128, 8> : launch_combine<128, 1>)(*d.k, d.ctas, stream)
+            : (d.wide ? launch_combine<64, 8> : launch_combine<64, 1>)(*d.k, d.ctas, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
@@ -394,6 +429,16 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   d.D = p.D;
   d.dev = di.dev;
   d.ctas = static_cast<unsigned>(std::min<long long>({di.sms, most_tiles, kMostCtas}));
+  // The merge takes a block of warps per row where rows with many parts are few
+  // (measured: 64 rows of 76 parts 17 us the whole call, a warp per row 38; 256 rows
+  // of 5 parts 84, 90; but 2048 rows of 10 parts 44, 39).
+  const long long own_runs = std::min(2ll * d.ctas, most_tiles);
+  const long long parts =
+      std::max((own_runs + heads - 1) / heads,
+               p.Np > 0 ? (std::min<long long>(d.ctas, prefix_items * k.prefix_tiles) +
+                           prefix_items - 1) / prefix_items
+                        : 0);
+  d.wide = parts >= 4 && static_cast<long long>(p.B) * p.Hq <= 4ll * di.sms;
   // slot of a state: its item's number + its piece's
   // (n runs of `tiles` in all have at most tiles / kPieceTiles + 2 n pieces)
   const size_t pre_tiles = prefix_total(k), own_tiles = heads * ((p.Ncap + 127ll) / 128);

@@ -43,8 +43,8 @@
 //   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
 //     for its first scores and its epilogue next to 2.9k a tile.  Packed documents
 //     B4 H16 N4096 D128: 91, tensor pipe 37%.
-//   * Decode of own keys: DRAM.  8 requests of up to 64k keys, Hkv8 D128: 89, 533
-//     MB at 6.1 TB/s in this kernel (92% of a measured copy).
+//   * Decode of own keys: DRAM.  8 requests of up to 64k keys, Hkv8 D128: 84, 533
+//     MB at 6.3 TB/s with the merge (94% of a measured copy).
 //   * Decode behind a prefix: the prefix' chain of product, softmax, product on some
 //     CTAs (1.5 us a tile of 256 rows, capped 2.1), on the others the latency of short
 //     items of own keys (0.6 us a tile of them at 2.5 tiles an item).  64 requests
