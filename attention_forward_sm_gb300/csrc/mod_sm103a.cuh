@@ -37,7 +37,7 @@
 // What bounds it and what it measures (us on a GB300, by CUDA events).
 //   * Prefill, long rows: the chain of a query tile, product, softmax, product,
 //     of which two run at a time.  B1 Hq32 Hkv8 N8192 D128 causal: 344 (1.60
-//     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 462, biased 460,
+//     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 459, biased 460,
 //     both 568; D64 274, 453, 383.  The tensor pipe is 49% busy capped, the issue
 //     slots 55%: a pass over a tile is longer than the products of the other.
 //   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
@@ -140,8 +140,9 @@ template <int D, bool kCap, bool kBias>
 constexpr bool kSplitScores = Cfg<D, false>::kSplitS && !kCap && !kBias;
 
 // Items of a query tile in flight: a decode's are short, and planned well ahead;
-// a prefill's are taken from the grid, and only one ahead, which keeps the end
-// of the grid even.
+// a prefill's are taken from the grid, and only one ahead, late in the item before
+// (see the planner): B2 H16 N4001 D64 causal biased 106 us, where it was taken at
+// that item's start 109; prefix documents capped and biased 102, 106.
 template <bool kSplit>
 constexpr int kWorkSlots = kSplit ? 4 : 2;
 
@@ -156,6 +157,7 @@ struct ModMisc {
   uint64_t s2_full[2][2], s2_read[2][2];   // S^T of a team: in TMEM; read (an arrival per warp)
   uint64_t pv2_done[2][2];                 // O^T += V^T P^T of a tile of a team retired
   uint64_t own_start[2];                   // the query tile's warps are done with prefix items
+  uint64_t item_loaded;   // prefill: every load of an item has been issued
   uint64_t clc_full;      // the answer to the request for more work arrived
   uint64_t work_full[2][4], work_empty[2][4];
   uint4 clc_resp;
@@ -1077,6 +1079,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
     }
     mbar_init(&ms.mma_done, 1);
     mbar_init(&ms.clc_full, 1);
+    mbar_init(&ms.item_loaded, 1);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&ms.kv_full[s], 1);
       mbar_init(&ms.kv_empty[s], 1);
@@ -1472,6 +1475,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
           ok = ok && (!use1 || load_q(1, id, q0));
         }
       }
+      if (!kSplit && lane == 0) mbar_arrive(&ms.item_loaded);
     }
     // ---- decode: the two runs of own keys, a tile of either in turn
     if constexpr (kSplit) {
@@ -1923,8 +1927,12 @@ __global__ void __launch_bounds__(kModThreads, 1)
              work_publish<kSlots>(ms, p, 1, k, w, abort_flag, lane);
         if (!ok || w.n < 0) break;
         ring += 2u * w.n;
-        // Ask for another item once the one before this is done: one is then
-        // always planned ahead, and no more.
+        // Ask for another item when the last loads of this one are issued, a few tiles
+        // before its end: early enough to be planned in time, and so late that the
+        // items, longest first, go to the CTAs that are done first.  (And once the one
+        // before this is done, whose ranges[] the next takes.)
+        ok = warp_all(mod_wait(&ms.item_loaded, k & 1, abort_flag, p.err, kErrWaitLoad,
+                               p.wait_limit_ns));
         if (k >= 1)
           for (int t = 0; t < 2; ++t)
             ok = ok && warp_all(mod_wait(&ms.work_empty[t][(k - 1) % kSlots],
