@@ -431,14 +431,16 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   d.ctas = static_cast<unsigned>(std::min<long long>({di.sms, most_tiles, kMostCtas}));
   // The merge takes a block of warps per row where rows with many parts are few
   // (measured: 64 rows of 76 parts 17 us the whole call, a warp per row 38; 256 rows
-  // of 5 parts 84, 90; but 2048 rows of 10 parts 44, 39).
+  // of 5 parts 84, 90; 768 of 20 23.5, 26; but 800 of 5 15.8, 14.7, and 2048 of 10 44,
+  // 39).
   const long long own_runs = std::min(2ll * d.ctas, most_tiles);
   const long long parts =
       std::max((own_runs + heads - 1) / heads,
                p.Np > 0 ? (std::min<long long>(d.ctas, prefix_items * k.prefix_tiles) +
                            prefix_items - 1) / prefix_items
                         : 0);
-  d.wide = parts >= 4 && static_cast<long long>(p.B) * p.Hq <= 4ll * di.sms;
+  const long long rows = static_cast<long long>(p.B) * p.Hq;
+  d.wide = rows <= 4ll * di.sms ? parts >= 4 : rows <= 8ll * di.sms && parts >= 8;
   // slot of a state: its item's number + its piece's
   // (n runs of `tiles` in all have at most tiles / kPieceTiles + 2 n pieces)
   const size_t pre_tiles = prefix_total(k), own_tiles = heads * ((p.Ncap + 127ll) / 128);

@@ -42,7 +42,7 @@
 //     slots 55%: a pass over a tile is longer than the products of the other.
 //   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
 //     for its first scores and its epilogue next to 2.9k a tile.  Packed documents
-//     B4 H16 N4096 D128: 91, tensor pipe 37%.
+//     B4 H16 N4096 D128: 89, tensor pipe 37%.
 //   * Decode of own keys: DRAM.  8 requests of up to 64k keys, Hkv8 D128: 84, 533
 //     MB at 6.3 TB/s with the merge (94% of a measured copy).
 //   * Decode behind a prefix: the prefix' chain of product, softmax, product on some
