@@ -214,11 +214,6 @@ __device__ __forceinline__ void st_global_v4_evict_first(void* addr, uint32_t a,
 }
 
 // 32-byte global store (sm_100+), address 32-byte aligned.
-__device__ __forceinline__ void st_global_v8(float* addr, const float (&x)[8]) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(addr), "f"(x[0]),
-               "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-               : "memory");
-}
 __device__ __forceinline__ void st_global_v8(void* addr, const uint32_t* x) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(addr), "r"(x[0]),
                "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
