@@ -30,7 +30,7 @@ struct CombineParams {
   float prefix_cost, own_cost;
 };
 
-// W warps per (request, query head), 1 or 8: they merge the row's partial states,
+// W warps per (request, query head), 1, 2 or 8: they merge the row's partial states,
 //   L = log2 sum_c 2^(lse_c),  O = sum_c 2^(lse_c - L) O_c,
 // those of the shared prefix's item and those of the request's own item.  The
 // runs of key tiles give every item's first and last run, and with it its
@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5, part = warp % W;
   const uint32_t row = blockIdx.x * (8 / W) + warp / W;
-  if (row >= static_cast<uint32_t>(p.B) * p.Hq) return;  // (a whole block, at W = 8)
+  // (no row: whole rows of warps leave, and a barrier does not count them)
+  if (row >= static_cast<uint32_t>(p.B) * p.Hq) return;
   const int b = static_cast<int>(row / p.Hq), h = static_cast<int>(row % p.Hq);
   const int hkv = h / p.G, g = h % p.G;
 
@@ -223,7 +224,7 @@ struct DecodeLaunch {
   ModKernelParams* k;
   int D, dev;
   unsigned ctas;
-  bool wide;  // the merge: a block per row
+  int merge_warps;  // per row: 1, 2 or 8
   size_t pre_o, pre_lse, part_o, part_lse;  // offsets into the scratch; plan at 0
 };
 
@@ -246,9 +247,12 @@ int launch_decode(void* ctx, void* scratch, cudaStream_t stream) {
   const int G = d.k->G, heads = G <= 4 ? 0 : (G <= 8 ? 1 : 2);
   cudaError_t e = split[d.D == 128][heads](*d.k, d.ctas, d.dev, stream);
   if (e == cudaSuccess)
-    e = d.D == 128
-            ? (d.wide ? launch_combine<128, 8> : launch_combine<128, 1>)(*d.k, d.ctas, stream)
-            : (d.wide ? launch_combine<64, 8> : launch_combine<64, 1>)(*d.k, d.ctas, stream);
+    e = (d.D == 128 ? (d.merge_warps == 8   ? launch_combine<128, 8>
+                       : d.merge_warps == 2 ? launch_combine<128, 2>
+                                            : launch_combine<128, 1>)
+                    : (d.merge_warps == 8   ? launch_combine<64, 8>
+                       : d.merge_warps == 2 ? launch_combine<64, 2>
+                                            : launch_combine<64, 1>))(*d.k, d.ctas, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
@@ -429,10 +433,10 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   d.D = p.D;
   d.dev = di.dev;
   d.ctas = static_cast<unsigned>(std::min<long long>({di.sms, most_tiles, kMostCtas}));
-  // The merge takes a block of warps per row where rows with many parts are few
-  // (measured: 64 rows of 76 parts 17 us the whole call, a warp per row 38; 256 rows
-  // of 5 parts 84, 90; 768 of 20 23.5, 26; but 800 of 5 15.8, 14.7, and 2048 of 10 44,
-  // 39).
+  // The merge takes more warps per row where rows with many parts are few.  Measured,
+  // the whole call in us with 8, 2, 1 warps: 64 rows of 76 parts 17, -, 38; 256 of 5
+  // 84, -, 90; 768 of 20 23.5, -, 26; 800 of 5 15.8, -, 14.7; 2048 of 20 43.8, 37.9,
+  // 39.8; 8192 of 6 105, 81, 78.
   const long long own_runs = std::min(2ll * d.ctas, most_tiles);
   const long long parts =
       std::max((own_runs + heads - 1) / heads,
@@ -440,7 +444,10 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
                            prefix_items - 1) / prefix_items
                         : 0);
   const long long rows = static_cast<long long>(p.B) * p.Hq;
-  d.wide = rows <= 4ll * di.sms ? parts >= 4 : rows <= 8ll * di.sms && parts >= 8;
+  d.merge_warps = rows <= 4ll * di.sms && parts >= 4    ? 8
+                  : rows <= 8ll * di.sms && parts >= 8  ? 8
+                  : rows <= 16ll * di.sms && parts >= 8 ? 2
+                                                        : 1;
   // slot of a state: its item's number + its piece's
   // (n runs of `tiles` in all have at most tiles / kPieceTiles + 2 n pieces)
   const size_t pre_tiles = prefix_total(k), own_tiles = heads * ((p.Ncap + 127ll) / 128);

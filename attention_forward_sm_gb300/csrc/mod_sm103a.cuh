@@ -48,7 +48,7 @@
 //   * Decode behind a prefix: the prefix' chain of product, softmax, product on some
 //     CTAs (1.5 us a tile of 256 rows, capped 2.1), on the others the latency of short
 //     items of own keys (0.6 us a tile of them at 2.5 tiles an item).  64 requests
-//     behind 16384 keys 39, 256 (capped) behind 8192 75.
+//     behind 16384 keys 38, 256 (capped) behind 8192 76.
 // Code that is not in the instruction cache shows: 264 KB of a decode instead of
 // 96 KB cost it 40% of its time, and a prefill's rarely taken ways 5 to 15%.
 #pragma once

@@ -765,3 +765,21 @@ def test_prefill_of_several_segments_of_keys(D, cap, bias, kind):
     causal = "causal" in kind or kind == "early"
     o, lse = attn.forward_mod(q, k, v, causal=causal, softcap=cap, slopes=slopes, ranges=ranges, q_offset=q_offset)
     check_fwd(o, lse, q, k, v, causal, 1 / math.sqrt(D), cap, slopes, ranges, q_offset)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Np,lens", [(1, 5, 1, 30_000, 700), (3, 4, 2, 9000, 9000), (150, 5, 1, 20_000, 90),
+                                             (333, 5, 1, 20_000, 30), (401, 3, 1, 20_000, 30),
+                                             (400, 8, 1, 20_000, 30)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_and_many_rows_of_few_and_many_parts(B, Hq, Hkv, Np, lens, D):
+    """Rows whose keys are cut in few or many parts, with any number of rows to a
+    block of the merge."""
+    own = [max(0, lens - 7 * i) for i in range(B)]
+    q, k, v = rand(1, (B, Hq, D)), rand(2, (B, Hkv, lens, D)), rand(3, (B, Hkv, lens, D))
+    pk, pv = rand(4, (Hkv, Np, D)), rand(5, (Hkv, Np, D))
+    t = torch.tensor(own, dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_prefix(q, pk, pv, k, v, t)
+    some = sorted({0, 1 % B, B // 2, B - 1})
+    check_decode(o, lse, q, k, v, own, 0.0, None, pk, pv, rows=some)
+    o, lse = attn.decode_varlen(q, k, v, t)
+    check_decode(o, lse, q, k, v, own, 0.0, None, rows=some)
