@@ -231,7 +231,7 @@ __device__ __forceinline__ void mask_to(float (&s)[64], const Seen& m, float wit
 // exponential (`fused`), they are not applied before it just to find the maximum.
 //   * Capped: with A the largest raw magnitude of the warp's scores, capped, and
 //     the bias of the key that it favours, m = A + bias: at most 2 A above the
-//     score of that key.
+//     score of that key.  (-inf for a row that sees no key of the tile.)
 //   * Biased only: m is the largest of the sums of a group's largest raw product
 //     and its most favoured key's bias, for groups of 16 keys: too large by the
 //     bias' change over a group at most.
@@ -258,8 +258,8 @@ struct Scores {
   Seen seen;         // if masked
   bool linear;
   float slope, rel;  // biased: key kb + i has bias -slope * |rel + i|, slope >= 0
-  float most[4];     // bias of the most favoured key: capped: of the tile, in [0];
-                     // else of every 16 keys
+  float most[4];     // bias of the most favoured key that the row sees: capped: of the
+                     // tile, in [0] (-inf: it sees none); else of every 16 keys
 
   // What does not depend on the scores, found while they are still multiplied.
   // kb: key of the thread's first score, kt: of the tile.  masked: some row of the
@@ -297,6 +297,10 @@ struct Scores {
       }
     }
     if (masked) seen = seen_columns(row.lo - kb, row.hi - kb);
+    // Without a bias too: a row that sees none of the tile's keys takes nothing from the
+    // others' scores, its own may lie any distance below them.
+    if (kCap && !kBias)
+      most[0] = masked && (row.lo >= kt + kBN || row.hi <= kt) ? -CUDART_INF_F : 0.f;
   }
 
   // From s to the row's m for the tile (both halves); false: it cannot be fused.
@@ -335,7 +339,7 @@ struct Scores {
       const bool holds = tier < 2 || all <= p.mod.cap_limit[2];
       // no score of the warp's rows is larger: |tanh x| <= |x|, 1
       const float top = fminf(all * p.scale_log2, p.mod.cap_out);
-      m = kBias ? top + most[0] : top;
+      m = top + most[0];
       if (!kOneGo && masked) mask_to(s, seen, p.mod.cap_off);
       return holds && 2.f * top <= kLoose;
     } else {

@@ -783,3 +783,19 @@ def test_few_and_many_rows_of_few_and_many_parts(B, Hq, Hkv, Np, lens, D):
     check_decode(o, lse, q, k, v, own, 0.0, None, pk, pv, rows=some)
     o, lse = attn.decode_varlen(q, k, v, t)
     check_decode(o, lse, q, k, v, own, 0.0, None, rows=some)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [50.0, 200.0, 1000.0])
+@pytest.mark.parametrize("causal", [False, True])
+def test_capped_rows_behind_tiles_that_they_do_not_see(D, cap, causal):
+    """Rows of a second document, all of whose scores are far below 0, among 16 rows
+    whose others see tiles in front of it: what those tiles hold has no say in them."""
+    N, first = 600, 200  # rows 192 .. 199 are the first document's, 200 .. 207 not
+    q = (1 + 0.1 * rand(1, (1, 2, N, D)).float()).bfloat16()
+    k = 0.1 * rand(2, (1, 2, N, D)).float()
+    k[:, :, first:] -= 150 * D ** -0.5  # scores about -150
+    k, v = k.bfloat16(), rand(3, (1, 2, N, D))
+    ranges = attn.row_ranges(torch.tensor([[first, N - first]], dtype=torch.int32, device="cuda"), N, causal=causal)
+    o, lse = attn.forward_mod(q, k, v, softcap=cap, ranges=ranges)
+    check_fwd(o, lse, q, k, v, False, D ** -0.5, cap, None, ranges, 0)
