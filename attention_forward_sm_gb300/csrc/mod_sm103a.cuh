@@ -841,9 +841,11 @@ __device__ __forceinline__ bool own_turn(ModMisc& ms, const ModKernelParams& p, 
 // is common to all 128 threads.  It is kept while no score exceeds it by more than
 // 2^8: one barrier that votes on that, and on every warp's waits having ended
 // well, is all that the threads of a tile exchange.
+// fine: the warp's waits so far ended well.  Every warp of a team comes here, also one
+// that gave up: the others may be here already, at a barrier that counts it.
 template <int D, int NH, bool kCap, bool kBias>
 __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, uint8_t* smem,
-                                         uint32_t tmem, int t, int k) {
+                                         uint32_t tmem, int t, int k, bool fine) {
   using C = Cfg<D, false>;
   constexpr uint32_t kS = C::kStages;
   constexpr int kSlots = kWorkSlots<true>;
@@ -867,8 +869,8 @@ __device__ __forceinline__ void own_keys(const ModKernelParams& p, ModMisc& ms, 
   // the other warps may still be reading the last prefix item's O
   __syncwarp();
   if (lane == 0) mbar_arrive(&ms.own_start[t]);
-  bool started = warp_all(mod_wait(&ms.own_start[t], 0, abort_flag, p.err, kErrWaitSoftmax,
-                                   p.wait_limit_ns));
+  const bool started = fine && warp_all(mod_wait(&ms.own_start[t], 0, abort_flag, p.err,
+                                                 kErrWaitSoftmax, p.wait_limit_ns));
   for (int turn = 0;; turn ^= 1, ++k) {
     bool ok = started && work_wait<kSlots>(ms, p, t, k, abort_flag, kErrWaitSoftmax);
     const Work& w = ms.work[t][k % kSlots];
@@ -1391,11 +1393,7 @@ __global__ void __launch_bounds__(kModThreads, 1)
       }
       work_done<kSlots>(ms, t, k, lane);
     }
-    if constexpr (swap) {
-      if (fine) {
-        own_keys<D, kHeads, kCap, kBias>(p, ms, smem, tmem, t, k);
-      }
-    }
+    if constexpr (swap) own_keys<D, kHeads, kCap, kBias>(p, ms, smem, tmem, t, k, fine);
   } else if (warp == kModWarpLoad) {
     // =====================================================================
     // TMA loader and planner.  Ring items run on across work items: the item's
