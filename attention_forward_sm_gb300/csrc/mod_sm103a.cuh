@@ -504,6 +504,7 @@ __device__ __forceinline__ bool work_publish(ModMisc& ms, const ModKernelParams&
       !warp_all(mod_wait(&ms.work_empty[t][k % kSlots], (k / kSlots + 1) & 1, abort_flag, p.err,
                           kErrWaitLoad, p.wait_limit_ns)))
     return false;
+  __syncwarp();  // every lane's stores (the rows' ranges) come before the arrival
   if (lane == 0) {
     ms.work[t][k % kSlots] = w;
     mbar_arrive(&ms.work_full[t][k % kSlots]);

@@ -28,3 +28,10 @@ def test_every_warp_of_a_team_votes_after_a_wait_ran_out():
     body = src[src.index("void own_keys("):]
     assert "started = fine && " in body[:body.index("bar_any(")]
     assert not re.search(r"\breturn;", body[:body.index("bar_any(")])
+
+
+def test_an_item_is_published_after_every_lane_s_stores():
+    """All lanes of the planning warp write the rows' ranges, one arrives for the warp."""
+    src = _source("mod_sm103a.cuh")
+    body = src[src.index("bool work_publish("):]
+    assert "__syncwarp();" in body[:body.index("mbar_arrive(&ms.work_full")]
