@@ -9,26 +9,11 @@
 #include <type_traits>
 
 #include "../../include/attn.h"
+#include "mod_plan.cuh"
 #include "score_mod.cuh"
 
 namespace attn {
 namespace {
-
-// What the merge needs of ModKernelParams (a launch copies its parameters).
-struct CombineParams {
-  void* o;
-  float* lse;
-  const int* lens;
-  const float* slopes;
-  const float* pre_o;
-  const float* pre_lse;
-  const float* part_o;
-  const float* part_lse;
-  const uint32_t* plan;
-  int B, Hq, Hkv, G, Nk, Np, row_blocks, per_tile, prefix_tiles, pre_rows;
-  uint32_t prefix_total, ctas;
-  float prefix_cost, own_cost;
-};
 
 // W warps per (request, query head), 1, 2 or 8: they merge the row's partial states,
 //   L = log2 sum_c 2^(lse_c),  O = sum_c 2^(lse_c - L) O_c,
@@ -52,40 +37,14 @@ __global__ void __launch_bounds__(256) mod_combine_kernel(const CombineParams p)
   const int b = static_cast<int>(row / p.Hq), h = static_cast<int>(row % p.Hq);
   const int hkv = h / p.G, g = h % p.G;
 
-  // the row's parts: count and first row of each of the two groups, rows of a
-  // group one slot apart
-  long long first[2] = {0, 0};
-  int count[2] = {0, 0};
-  auto prefix_parts = [&](uint32_t share) {
-    const uint32_t all = p.prefix_total, runs = min(all, p.ctas - share);
-    const int item = hkv * p.row_blocks + b / (2 * p.per_tile);
-    const uint32_t t0 = static_cast<uint32_t>(item) * p.prefix_tiles;
-    const Pieces pieces(all, runs);
-    const uint32_t r0 = piece_of(all, runs, pieces, t0);
-    count[0] = static_cast<int>(piece_of(all, runs, pieces, t0 + p.prefix_tiles - 1) - r0) + 1;
-    const int in_tile = b % p.per_tile, tile = (b / p.per_tile) & 1;
-    first[0] = static_cast<long long>(item + r0) * p.pre_rows + tile * 128 + in_tile * p.G + g;
-  };
-  // (CTAs are shared out by the lengths where there are enough tiles of the prefix)
-  const bool shared = p.prefix_total >= p.ctas;
-  if (p.prefix_tiles > 0 && !shared) prefix_parts(0);
+  RowParts parts;
+  parts.before(p, b, hkv, g);
   const int len = p.lens ? min(max(p.lens[b], 0), p.Nk) : p.Nk;
   const float slope = p.slopes ? p.slopes[h] : 0.f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const uint32_t before = p.plan[b], nt = p.plan[b + 1] - before, own = p.plan[p.B] * p.Hkv;
-  uint32_t share = 0;
-  if (shared) {
-    share = own_share(p.ctas, p.prefix_total, own, p.prefix_cost, p.own_cost);
-    prefix_parts(share);
-  }
-  if (nt > 0) {
-    const uint32_t runs = min(own, 2 * (share ? share : p.ctas));
-    const uint32_t t0 = before * p.Hkv + hkv * nt;
-    const Pieces pieces(own, runs);
-    const uint32_t r0 = piece_of(own, runs, pieces, t0);
-    count[1] = static_cast<int>(piece_of(own, runs, pieces, t0 + nt - 1) - r0) + 1;
-    first[1] = (static_cast<long long>(b) * p.Hkv + hkv + r0) * p.G + g;
-  }
+  parts.after(p, b, hkv, g);
+  const int(&count)[2] = parts.count;
+  const long long(&first)[2] = parts.first;
   // this warp's parts: every W-th
   const int all_parts = count[0] + count[1];
   const int total = all_parts > part ? (all_parts - part + W - 1) / W : 0;

@@ -1,0 +1,101 @@
+"""The plan of a decode with modified scores, on the host: every key tile of every
+request and KV head is in exactly one item, partial states never share a slot, and the
+merge looks for a row's states where the split kernel leaves them."""
+import collections
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "attention_forward_sm_gb300", "csrc")
+
+
+@pytest.fixture(scope="module")
+def planner(tmp_path_factory):
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    if not os.path.exists(os.path.join(cuda, "include", "cuda.h")):
+        pytest.skip("needs the CUDA headers")
+    exe = str(tmp_path_factory.mktemp("plan") / "plan")
+    subprocess.run(["g++", "-std=c++20", "-O1", "-w", "-I", CSRC, "-I", os.path.join(cuda, "include"),
+                    os.path.join(ROOT, "tests", "mod_plan_host.cpp"), "-o", exe], check=True)
+
+    def run(**problem):
+        res = subprocess.run([exe] + [f"{k}={v}" for k, v in problem.items()], capture_output=True, text=True,
+                             timeout=60, check=True)
+        items, rows, err, sizes = [], [], None, None
+        for line in res.stdout.splitlines():
+            kind, *values = line.split()
+            values = [int(v) for v in values]
+            if kind == "item":
+                items.append(values)
+            elif kind == "row":
+                rows.append(values)
+            elif kind == "err":
+                err = values[0]
+            else:
+                sizes = values
+        return items, rows, err, sizes
+    return run
+
+
+PROBLEMS = [
+    dict(B=1, Hkv=8, G=4, Ncap=2048, lo=1023, hi=1023),
+    dict(B=1, Hkv=1, G=1, Ncap=1, lo=0),
+    dict(B=8, Hkv=8, G=4, Ncap=8192, lo=50),
+    dict(B=70, Hkv=2, G=3, Ncap=700, lo=0),
+    dict(B=200, Hkv=1, G=8, Ncap=200, lo=0, hi=130),
+    dict(B=5, Hkv=1, G=8, Np=1001, Ncap=256, lo=1, hi=200),
+    dict(B=64, Hkv=8, G=4, Np=16384, Ncap=1024, lo=16),
+    dict(B=256, Hkv=8, G=4, Np=8192, Ncap=512, lo=8, own_cost=1.15, prefix_cost=2.1),
+    dict(B=100, Hkv=4, G=3, Np=4000, Ncap=300, lo=0, ctas=40),
+    dict(B=33, Hkv=1, G=128, Np=900, Ncap=129, lo=0, ctas=20),
+    dict(B=3, Hkv=1, G=2, Np=3_000_000, Ncap=2_000_000, lo=1_000_000, ctas=5),  # runs in several pieces
+    dict(B=40, Hkv=2, G=2, Np=300, Ncap=64, lo=0, hi=0),
+]
+
+
+def _check(items, rows, sizes, problem):
+    per_tile, row_blocks, pre_rows = sizes
+    G, Hkv = problem["G"], problem["Hkv"]
+    # what the split kernels do: (KV head, request) -> its own tiles; (KV head, block) -> the prefix's
+    tiles = collections.defaultdict(list)
+    slots = set()
+    for cta, t, kind, head, q0, tile0, n, keys, slot in items:
+        if kind == 2 or kind < 0 or (kind == 0 and t == 1):
+            continue  # (both query tiles get the prefix's items)
+        assert n > 0 and (kind, slot) not in slots
+        slots.add((kind, slot))
+        tiles[(kind, head, q0)].append((tile0, n, slot, keys))
+    np_tiles = -(-problem.get("Np", 0) // 128)
+    seen_rows = set()
+    for b, head, g, first0, count0, first1, count1 in rows:
+        seen_rows.add((b, head))
+        pre = []
+        if np_tiles:
+            block = b // (2 * per_tile)
+            pre = sorted(tiles[(0, head, block * 2 * per_tile)])
+            at = ((b // per_tile) % 2) * 128 + (b % per_tile) * G + g
+            assert [first0 + i * pre_rows for i in range(count0)] == [s * pre_rows + at for _, _, s, _ in pre]
+        else:
+            assert count0 == 0
+        own = sorted(tiles[(1, head, b)])
+        assert [first1 + i * G for i in range(count1)] == [s * G + g for _, _, s, _ in own]
+        for parts, most in ((pre, np_tiles), (own, -(-own[0][3] // 128) if own else 0)):
+            end = 0
+            for tile0, n, _, _ in parts:
+                assert tile0 == end
+                end = tile0 + n
+            assert end == most
+    assert {(b, h) for k, h, q in tiles if k == 1 for b in (q,)} <= seen_rows
+    # as many items as there are requests with keys, or blocks of them behind the prefix
+    if np_tiles:
+        assert len({k for k in tiles if k[0] == 0}) == Hkv * row_blocks
+
+
+@pytest.mark.parametrize("problem", PROBLEMS, ids=lambda p: "-".join(f"{k}{v}" for k, v in p.items()))
+@pytest.mark.parametrize("seed", [1, 2])
+def test_every_tile_once_and_every_part_found(planner, problem, seed):
+    items, rows, err, sizes = planner(seed=seed, **problem)
+    assert err == 0
+    _check(items, rows, sizes, problem)
