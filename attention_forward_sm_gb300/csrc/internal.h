@@ -15,6 +15,7 @@ enum : unsigned int {
   kErrWaitSoftmax = 1u << 2,  // softmax gave up waiting for S
   kErrWaitCorr = 1u << 3,     // correction / epilogue gave up waiting
   kErrSelfTest = 1u << 4,     // the wait self-test ran out, as intended
+  kErrLens = 1u << 5,         // a decode's lengths changed while it was planned
 };
 
 // Forward (prefill) launch parameters.  Tensor maps are 3-D views with a

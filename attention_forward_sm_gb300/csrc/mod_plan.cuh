@@ -95,6 +95,18 @@ struct OwnPlan {
     len = b0 + lane < p.B ? request_len(p, b0 + lane) : 0;
     tiles = key_tiles(len);
   }
+  // false: behind the last request, with tiles left: the lengths are not those that the
+  // total came from, which is the caller's mistake.  The run ends here.
+  __device__ __forceinline__ bool next_block(const ModKernelParams& p, int lane) {
+    b0 += 32;
+    if (b0 >= p.B) {
+      if (lane == 0) atomicOr(p.err, kErrLens);
+      left = 0;
+      return false;
+    }
+    load_block(p, lane);
+    return true;
+  }
   // How many tiles there are of all requests; the first ones stay in the lanes.
   __device__ __forceinline__ uint32_t total_tiles(const ModKernelParams& p, int lane) {
     b0 = 0;
@@ -132,8 +144,7 @@ struct OwnPlan {
         return;
       }
       x -= block;
-      b0 += 32;
-      load_block(p, lane);
+      if (!next_block(p, lane)) return;
     }
   }
   // The next item; ring0: ring items of the prefix tiles before.
@@ -169,9 +180,8 @@ struct OwnPlan {
             at = __ffs(some) - 1;
             break;
           }
-          b0 += 32;
           at = -1;
-          load_block(p, lane);
+          if (!next_block(p, lane)) break;
         }
       }
     }

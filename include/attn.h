@@ -75,6 +75,7 @@ enum attn_status {
 #define ATTN_DEVERR_WAIT_SOFTMAX 0x4u /* softmax gave up waiting for scores */
 #define ATTN_DEVERR_WAIT_CORR 0x8u    /* correction / epilogue gave up waiting */
 #define ATTN_DEVERR_SELFTEST 0x10u    /* attn_selftest_wait_timeout ran out, as intended */
+#define ATTN_DEVERR_LENS 0x20u        /* a decode's lengths changed while it ran */
 
 /*
  * attn_fwd -- attention forward (prefill).
@@ -386,7 +387,10 @@ int attn_row_ranges(const int *doc_lens, const int *prefix_lens, int *ranges, in
  *
  * The query is at position lens[b] - 1, that of the request's last key.  The
  * lengths stay on the device: the call never waits for them, so it can be
- * captured once and replayed while they grow.
+ * captured once and replayed with other lengths each time.  From the call's (or
+ * replay's) start on its stream to its end they must not change: the kernels read
+ * them more than once.  If they do all the same, the outputs are unspecified and
+ * an ATTN_DEVERR_* bit may be set, but the call ends and writes nothing else.
  *
  * Limits: B, Hq, Hkv, Ncap >= 1; Hq % Hkv == 0; Hq / Hkv <= 128; D in
  * {64, 128}; B * Hkv <= 2^20, Hq <= 65535; Ncap <= 2^30, and at most 12e6

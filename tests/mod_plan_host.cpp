@@ -30,11 +30,14 @@ void entry(int l) {
   swapcontext(&lanes[l], &back);
 }
 void yield() { swapcontext(&lanes[lane], &back); }
+long long operations = 0, shrink_after = -1;  // a caller's mistake, after so many operations
+std::function<void()> shrink;
 // every lane's x, once all have given theirs
 const uint64_t* exchange(uint64_t x) {
   const int l = lane, ph = phase[l];
   phase[l] ^= 1;
   slots[ph][l] = x;
+  if (l == 0 && operations++ == shrink_after) shrink();
   yield();
   return slots[ph];
 }
@@ -109,7 +112,7 @@ int main(int argc, char** argv) {
   const int B = static_cast<int>(number("B", 1)), Hkv = static_cast<int>(number("Hkv", 1));
   const int G = static_cast<int>(number("G", 1)), Np = static_cast<int>(number("Np", 0));
   const int Ncap = static_cast<int>(number("Ncap", 1));
-  // lengths by a generator; how many of them a later reading finds shortened
+  // lengths by a generator
   uint64_t seed = static_cast<uint64_t>(number("seed", 1)) * 2654435761u + 12345;
   const int lo = static_cast<int>(number("lo", 0)), hi = static_cast<int>(number("hi", Ncap));
   std::vector<int> lens(B);
@@ -117,7 +120,8 @@ int main(int argc, char** argv) {
     seed = seed * 6364136223846793005ull + 1442695040888963407ull;
     x = lo + static_cast<int>((seed >> 33) % static_cast<uint64_t>(hi - lo + 1));
   }
-  const int shrink_after = static_cast<int>(number("shrink_after", -1));
+  warp::shrink_after = static_cast<long long>(number("shrink_after", -1));
+  warp::shrink = [&] { std::fill(lens.begin(), lens.end(), 0); };
 
   ModKernelParams p = {};
   unsigned err = 0;
@@ -147,13 +151,8 @@ int main(int argc, char** argv) {
       std::vector<Work> items;
       warp::run([&](int lane) {
         Work w = {};
-        int published = 0;
         plan_decode(p, t, lane, w, [&] {
           if (lane == 0) items.push_back(w);
-          // the caller's mistake: lengths change under the call
-          if (lane == 0 && shrink_after >= 0 && published == shrink_after)
-            std::fill(lens.begin(), lens.end(), 0);
-          ++published;
           return true;
         });
       });

@@ -99,3 +99,21 @@ def test_every_tile_once_and_every_part_found(planner, problem, seed):
     items, rows, err, sizes = planner(seed=seed, **problem)
     assert err == 0
     _check(items, rows, sizes, problem)
+
+
+@pytest.mark.parametrize("problem", [
+    dict(B=170, Hkv=2, G=3, Ncap=700, lo=1, ctas=9),
+    dict(B=200, Hkv=1, G=8, Ncap=200, lo=1, ctas=4),
+    dict(B=64, Hkv=8, G=4, Np=16384, Ncap=1024, lo=16, ctas=20),
+], ids=lambda p: f"B{p['B']}")
+def test_lengths_that_shrink_during_a_call(planner, problem):
+    """A caller's mistake, at one point of the planning after another: every run ends all
+    the same, and where one finds tiles missing the error word says so."""
+    found = 0
+    for after in list(range(24)) + list(range(24, 400, 11)):
+        items, _, err, _ = planner(shrink_after=after, **problem)
+        done = [(i[0], i[1]) for i in items if i[2] == -1]
+        assert len(done) == 2 * problem["ctas"] == len(set(done))
+        assert err in (0, 1 << 5)
+        found += err != 0
+    assert found > 0
