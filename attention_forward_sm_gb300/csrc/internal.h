@@ -126,7 +126,8 @@ struct ModKernelParams {
   float* pre_lse;                  // (log2 units, bias relative to its reference)
   float* part_o;                   // of the requests' own keys: [slot, G, D]
   float* part_lse;
-  uint32_t* plan;                  // [B + 1] own-key tiles in front of every request
+  uint32_t* plan;                  // [B + 2] own-key tiles in front of every request, of
+                                   // all; the CTAs that have own keys alone
   float scale_log2;
   ScoreMod mod;
   unsigned int* err;

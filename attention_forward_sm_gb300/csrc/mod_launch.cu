@@ -166,7 +166,7 @@ cudaError_t launch_combine(const ModKernelParams& p, unsigned ctas, cudaStream_t
                            p.pre_lse,  p.part_o,   p.part_lse, p.plan,       p.B,
                            p.Hq,       p.Hkv,      p.G,        p.Nk,         p.Np,
                            p.row_blocks, p.per_tile, p.prefix_tiles, p.pre_rows,
-                           prefix_total(p), ctas, p.prefix_cost, p.own_cost};
+                           prefix_total(p), ctas};
   return cudaLaunchKernelEx(&cfg, mod_combine_kernel<D, W>, c);
 }
 
@@ -414,7 +414,7 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
                               : 0;
   const size_t own = (heads + own_tiles / kPieceTiles + 4ull * d.ctas) * k.G;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  d.pre_o = up((static_cast<size_t>(p.B) + 1) * sizeof(uint32_t));
+  d.pre_o = up((static_cast<size_t>(p.B) + 2) * sizeof(uint32_t));
   d.pre_lse = d.pre_o + up(pre * p.D * sizeof(float));
   d.part_o = d.pre_lse + up(pre * sizeof(float));
   d.part_lse = d.part_o + up(own * p.D * sizeof(float));

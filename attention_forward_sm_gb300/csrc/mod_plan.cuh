@@ -222,7 +222,8 @@ __device__ __forceinline__ void plan_decode(const ModKernelParams& p, int t, int
   while (ok && own.next(p, t, lane, ring, w)) ok = publish();
   w.n = -1;
   ok = ok && publish();
-  // CTA 0 leaves the merge kernel where every request's tiles begin
+  // CTA 0 leaves the merge kernel where every request's tiles begin, and the share, whose
+  // rounding another kernel need not repeat
   if (blockIdx.x == 0 && t == 1) {
     uint32_t before = 0;
     for (int b = 0; b < p.B; b += 32) {
@@ -231,7 +232,10 @@ __device__ __forceinline__ void plan_decode(const ModKernelParams& p, int t, int
       if (b + lane < p.B) p.plan[b + lane] = before + scan - nt;
       before += __shfl_sync(0xFFFFFFFFu, scan, 31);
     }
-    if (lane == 0) p.plan[p.B] = before;
+    if (lane == 0) {
+      p.plan[p.B] = before;
+      p.plan[p.B + 1] = share;
+    }
   }
 }
 
@@ -248,7 +252,6 @@ struct CombineParams {
   const uint32_t* plan;
   int B, Hq, Hkv, G, Nk, Np, row_blocks, per_tile, prefix_tiles, pre_rows;
   uint32_t prefix_total, ctas;
-  float prefix_cost, own_cost;
 };
 
 // The partial states of a row (request b, query head g of KV head hkv): count and first
@@ -278,11 +281,8 @@ struct RowParts {
   }
   __device__ __forceinline__ void after(const CombineParams& p, int b, int hkv, int g) {
     const uint32_t front = p.plan[b], nt = p.plan[b + 1] - front, own = p.plan[p.B] * p.Hkv;
-    uint32_t share = 0;
-    if (shared(p)) {
-      share = own_share(p.ctas, p.prefix_total, own, p.prefix_cost, p.own_cost);
-      prefix(p, b, hkv, g, share);
-    }
+    const uint32_t share = p.plan[p.B + 1];
+    if (shared(p)) prefix(p, b, hkv, g, share);
     if (nt > 0) {
       const uint32_t runs = min(own, 2 * (share ? share : p.ctas));
       const uint32_t t0 = front * p.Hkv + hkv * nt;

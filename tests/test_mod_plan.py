@@ -117,3 +117,13 @@ def test_lengths_that_shrink_during_a_call(planner, problem):
         assert err in (0, 1 << 5)
         found += err != 0
     assert found > 0
+
+
+@pytest.mark.parametrize("other", [0.8, 1.3])
+@pytest.mark.parametrize("problem", [PROBLEMS[6], PROBLEMS[7], PROBLEMS[8]], ids=lambda p: f"B{p['B']}")
+def test_the_merge_takes_the_shares_as_they_were(planner, problem, other):
+    """Shares of CTAs are found in floating point.  The merge, another kernel, must not
+    depend on finding the same: here it would find others."""
+    items, rows, err, sizes = planner(other=other, **problem)
+    assert err == 0
+    _check(items, rows, sizes, problem)
