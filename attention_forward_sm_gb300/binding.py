@@ -432,32 +432,32 @@ def _current_raw_stream(dev: int) -> int:
     return _torch.cuda.current_stream(dev).cuda_stream
 
 
-def _side_launch(fn, args, dev: int, stream, used):
-    """Calls the library's ``fn`` with ``dev`` current, on ``stream`` (None: the
-    device's current one).  On another stream than the current one the tensors
-    of ``used`` are marked as used there, so that the caching allocator does not
-    hand their memory out again while the kernels run."""
-    with _torch.cuda.device(dev):
-        cur = _raw_stream(dev)
+def _elsewhere(call, dev: int, stream, inputs):
+    """``call()`` with ``dev`` current, on ``stream`` (None: the device's current
+    one).  On another stream than the current one the outputs are allocated there
+    too: the caching allocator may give memory out again that kernels of the
+    current stream are still to read, which only that stream waits for.  The
+    inputs are marked as used on the other stream and the outputs as used on the
+    current one, so that neither's memory is handed out while it is in use."""
+    cuda = _torch.cuda
+    with cuda.device(dev):
         if stream is None:
-            s = cur
-        elif isinstance(stream, int):
-            s = stream
-        else:
-            if stream.device.index != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
-            s = stream.cuda_stream
-        rc = fn(*args, s)
-        if rc:
-            _check(rc)
-        if s != cur:
-            side = stream
-            if isinstance(stream, int):
-                side = _torch.cuda.ExternalStream(s, device=dev) if s else \
-                    _torch.cuda.default_stream(dev)
-            for x in used:
-                if x is not None:
-                    x.record_stream(side)
+            return call()
+        if isinstance(stream, int):
+            stream = cuda.ExternalStream(stream, device=dev) if stream else cuda.default_stream(dev)
+        elif stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        current = cuda.current_stream(dev)
+        if stream.cuda_stream == current.cuda_stream:
+            return call()
+        with cuda.stream(stream):
+            out = call()
+        for x in inputs:
+            if x is not None:
+                x.record_stream(stream)
+        for x in out if isinstance(out, tuple) else (out,):
+            x.record_stream(current)
+        return out
 
 
 # The first call of each of these two puts the quickest way there is in its place.
@@ -503,20 +503,20 @@ def forward_mod(q, k, v, *, causal: bool = False, scale: float | None = None,
                        "Hkv": (k.shape[1], v.shape[1]), "Nk": (k.shape[2], v.shape[2])})
         _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)),
                    ranges=(ranges, torch.int32, (B, Nq, 2)))
+    if stream is not None or _current_device() != dev:
+        return _elsewhere(lambda: forward_mod(q, k, v, causal=causal, scale=scale, softcap=softcap,
+                                              slopes=slopes, ranges=ranges, q_offset=q_offset),
+                          dev, stream, (q, k, v, slopes, ranges))
     device = q.device
     o = torch.empty_strided((B, Hq, Nq, D), (Hq * Nq * D, Nq * D, D, 1), dtype=bf16, device=device)
     lse = torch.empty_strided((B, Hq, Nq), (Hq * Nq, Nq, 1), dtype=torch.float32, device=device)
-    fn = (_lib or load()).attn_fwd_mod
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
-            Nq, Nk, D, bool(causal), q_offset, D ** -0.5 if scale is None else scale, softcap,
-            None if slopes is None else slopes.data_ptr(),
-            None if ranges is None else ranges.data_ptr())
-    if stream is None and _current_device() == dev:
-        rc = fn(*args, _raw_stream(dev))
-        if rc:
-            _check(rc)
-    else:
-        _side_launch(fn, args, dev, stream, (q, k, v, slopes, ranges, o, lse))
+    rc = (_lib or load()).attn_fwd_mod(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, Nk,
+        D, bool(causal), q_offset, D ** -0.5 if scale is None else scale, softcap,
+        None if slopes is None else slopes.data_ptr(), None if ranges is None else ranges.data_ptr(),
+        _raw_stream(dev))
+    if rc:
+        _check(rc)
     return o, lse
 
 
@@ -538,16 +538,15 @@ def row_ranges(doc_lens, N: int, *, prefix_lens=None, causal: bool = True, strea
         _check_ranks({"doc_lens": doc_lens}, {"doc_lens": 2})
         _check_aux(doc_lens.device, doc_lens=(doc_lens, i32, (B, M)),
                    prefix_lens=(prefix_lens, i32, (B, M)))
+    if stream is not None or _current_device() != dev:
+        return _elsewhere(lambda: row_ranges(doc_lens, N, prefix_lens=prefix_lens, causal=causal),
+                          dev, stream, (doc_lens, prefix_lens))
     out = torch.empty((B, N, 2), dtype=i32, device=doc_lens.device)
-    fn = (_lib or load()).attn_row_ranges
-    args = (doc_lens.data_ptr(), None if prefix_lens is None else prefix_lens.data_ptr(),
-            out.data_ptr(), B, N, M, bool(causal))
-    if stream is None and _current_device() == dev:
-        rc = fn(*args, _raw_stream(dev))
-        if rc:
-            _check(rc)
-    else:
-        _side_launch(fn, args, dev, stream, (doc_lens, prefix_lens, out))
+    rc = (_lib or load()).attn_row_ranges(
+        doc_lens.data_ptr(), None if prefix_lens is None else prefix_lens.data_ptr(),
+        out.data_ptr(), B, N, M, bool(causal), _raw_stream(dev))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -582,6 +581,9 @@ def _decode(fn, q, pre, kcache, vcache, lens, scale, softcap, slopes, stream):
                            "Np": (pre[0].shape[1], pre[1].shape[1]),
                            "D": (D, pre[0].shape[2], pre[1].shape[2])})
         _check_aux(q.device, slopes=(slopes, torch.float32, (Hq,)), lens=(lens, torch.int32, (B,)))
+    if stream is not None or _current_device() != dev:
+        return _elsewhere(lambda: _decode(fn, q, pre, kcache, vcache, lens, scale, softcap, slopes, None),
+                          dev, stream, (q, *pre, kcache, vcache, lens, slopes))
     device = q.device
     o = torch.empty_strided((B, Hq, D), (Hq * D, D, 1), dtype=bf16, device=device)
     lse = torch.empty_strided((B, Hq), (Hq, 1), dtype=torch.float32, device=device)
@@ -593,12 +595,9 @@ def _decode(fn, q, pre, kcache, vcache, lens, scale, softcap, slopes, stream):
                 vcache.data_ptr(), *tail, Np, *score)
     else:
         args = (q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), *tail, *score)
-    if stream is None and _current_device() == dev:
-        rc = fn(*args, _raw_stream(dev))
-        if rc:
-            _check(rc)
-    else:
-        _side_launch(fn, args, dev, stream, (q, *pre, kcache, vcache, lens, slopes, o, lse))
+    rc = fn(*args, _raw_stream(dev))
+    if rc:
+        _check(rc)
     return o, lse
 
 

@@ -799,3 +799,51 @@ def test_capped_rows_behind_tiles_that_they_do_not_see(D, cap, causal):
     ranges = attn.row_ranges(torch.tensor([[first, N - first]], dtype=torch.int32, device="cuda"), N, causal=causal)
     o, lse = attn.forward_mod(q, k, v, softcap=cap, ranges=ranges)
     check_fwd(o, lse, q, k, v, False, D ** -0.5, cap, None, ranges, 0)
+
+
+def _calls_on(stream):
+    """Each helper on `stream`: (call, output shapes and types)."""
+    q, k = rand(1, (2, 4, 1500, 64)), rand(2, (2, 2, 1500, 64))
+    q1, p = rand(3, (2, 4, 64)), rand(4, (2, 900, 64))
+    lens = torch.tensor([1500, 700], dtype=torch.int32, device="cuda")
+    docs = torch.tensor([[1000, 300], [20, 1]], dtype=torch.int32, device="cuda")
+    return [lambda: attn.forward_mod(q, k, k, causal=True, stream=stream),
+            lambda: attn.decode_varlen(q1, k, k, lens, stream=stream),
+            lambda: attn.decode_prefix(q1, p, p, k, k, lens, stream=stream),
+            lambda: (attn.row_ranges(docs, 1500, stream=stream),)]
+
+
+@pytest.mark.parametrize("which", range(4), ids=["forward_mod", "decode_varlen", "decode_prefix", "row_ranges"])
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_on_another_stream_take_no_memory_that_is_still_read(which, handle):
+    """Freed memory that the current stream is still to read is not written by a call on
+    another stream; nor are that call's outputs by the next one, once they are freed,
+    while the current stream is still to read them."""
+    side = torch.cuda.Stream()
+    call = _calls_on(side.cuda_stream if handle else side)[which]
+    want = [x.clone() for x in _calls_on(None)[which]()]
+    torch.cuda.synchronize()
+    # memory of the outputs' sizes, read by the current stream long after it is freed
+    olds = [torch.full_like(x, 3) for _ in range(4) for x in want]
+    torch.cuda.synchronize()
+    busy = _busy(torch.cuda.current_stream())
+    reads = [x.clone() for x in olds]
+    del olds
+    for _ in range(4):
+        got = call()
+    side.synchronize()  # (the current stream is still busy)
+    torch.cuda.synchronize()
+    assert all(bool((x == 3).all()) for x in reads)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    # the outputs themselves, read by the current stream after they are freed
+    got = call()
+    torch.cuda.current_stream().wait_stream(side)
+    del busy
+    busy = _busy(torch.cuda.current_stream())
+    reads = [x.clone() for x in got]
+    del got
+    with torch.cuda.stream(side):
+        over = [torch.full_like(x, 5) for _ in range(4) for x in want]
+    torch.cuda.synchronize()
+    del busy, over
+    assert all(torch.equal(x, y) for x, y in zip(reads, want))
