@@ -106,6 +106,24 @@ def _ptr(x) -> int:
     return x.data_ptr()
 
 
+def _int(x) -> int:
+    """A size for a C int, which would take what does not fit modulo 2^32."""
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        _check(-3)  # ATTN_ERR_SHAPE
+    return x
+
+
+_LEAST_CAP = 2.0 ** -149  # below it a float would round to 0, which stands for no cap
+
+
+def _cap(softcap) -> float:
+    softcap = float(softcap)
+    if 0 < softcap < _LEAST_CAP:
+        _check(-3)  # ATTN_ERR_SHAPE
+    return softcap
+
+
 def _stream(stream) -> int:
     if stream is None:
         import torch
@@ -240,16 +258,16 @@ def attn_fwd_mod(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, D, causal, q_offset, scale
     """``attn_fwd_mod`` of include/attn.h: ``attn_fwd_rows`` with capped scores,
     a distance bias (``slopes`` [Hq] fp32) and a key range per query row
     (``ranges`` [B, Nq, 2] int32)."""
-    _check(load().attn_fwd_mod(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), int(B), int(Hq),
-                               int(Hkv), int(Nq), int(Nk), int(D), int(bool(causal)),
-                               int(q_offset), float(scale), float(softcap), _ptr(slopes),
+    _check(load().attn_fwd_mod(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _int(B), _int(Hq),
+                               _int(Hkv), _int(Nq), _int(Nk), _int(D), int(bool(causal)),
+                               _int(q_offset), float(scale), _cap(softcap), _ptr(slopes),
                                _ptr(ranges), _stream(stream)))
 
 
 def attn_row_ranges(doc_lens, prefix_lens, ranges, B, N, M, causal, stream=None) -> None:
     """``attn_row_ranges`` of include/attn.h: the key ranges of packed documents."""
-    _check(load().attn_row_ranges(_ptr(doc_lens), _ptr(prefix_lens), _ptr(ranges), int(B), int(N),
-                                  int(M), int(bool(causal)), _stream(stream)))
+    _check(load().attn_row_ranges(_ptr(doc_lens), _ptr(prefix_lens), _ptr(ranges), _int(B), _int(N),
+                                  _int(M), int(bool(causal)), _stream(stream)))
 
 
 def attn_decode_varlen(q, kcache, vcache, lens, o, lse, B, Hq, Hkv, Ncap, D, scale, softcap=0.0,
@@ -257,8 +275,8 @@ def attn_decode_varlen(q, kcache, vcache, lens, o, lse, B, Hq, Hkv, Ncap, D, sca
     """``attn_decode_varlen`` of include/attn.h: decode with a length per
     request (``lens`` [B] int32 on the device, or None: all Ncap keys)."""
     _check(load().attn_decode_varlen(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(lens), _ptr(o),
-                                     _ptr(lse), int(B), int(Hq), int(Hkv), int(Ncap), int(D),
-                                     float(scale), float(softcap), _ptr(slopes),
+                                     _ptr(lse), _int(B), _int(Hq), _int(Hkv), _int(Ncap), _int(D),
+                                     float(scale), _cap(softcap), _ptr(slopes),
                                      _stream(stream)))
 
 
@@ -267,9 +285,9 @@ def attn_decode_prefix(q, kprefix, vprefix, kcache, vcache, lens, o, lse, B, Hq,
     """``attn_decode_prefix`` of include/attn.h: ``attn_decode_varlen`` behind a
     prefix (``kprefix`` / ``vprefix`` [Hkv, Np, D]) that all requests share."""
     _check(load().attn_decode_prefix(_ptr(q), _ptr(kprefix), _ptr(vprefix), _ptr(kcache),
-                                     _ptr(vcache), _ptr(lens), _ptr(o), _ptr(lse), int(B), int(Hq),
-                                     int(Hkv), int(Np), int(Ncap), int(D), float(scale),
-                                     float(softcap), _ptr(slopes), _stream(stream)))
+                                     _ptr(vcache), _ptr(lens), _ptr(o), _ptr(lse), _int(B), _int(Hq),
+                                     _int(Hkv), _int(Np), _int(Ncap), _int(D), float(scale),
+                                     _cap(softcap), _ptr(slopes), _stream(stream)))
 
 
 def attn_decode_workspace_bytes(B, Hq, D, nsplit) -> int:
@@ -507,6 +525,8 @@ def forward_mod(q, k, v, *, causal: bool = False, scale: float | None = None,
         return _elsewhere(lambda: forward_mod(q, k, v, causal=causal, scale=scale, softcap=softcap,
                                               slopes=slopes, ranges=ranges, q_offset=q_offset),
                           dev, stream, (q, k, v, slopes, ranges))
+    if q_offset >> 31 or 0 < softcap < _LEAST_CAP:
+        _check(-3)  # ATTN_ERR_SHAPE: ctypes would pass it modulo 2^32, or as no cap
     device = q.device
     o = torch.empty_strided((B, Hq, Nq, D), (Hq * Nq * D, Nq * D, D, 1), dtype=bf16, device=device)
     lse = torch.empty_strided((B, Hq, Nq), (Hq * Nq, Nq, 1), dtype=torch.float32, device=device)
@@ -541,6 +561,8 @@ def row_ranges(doc_lens, N: int, *, prefix_lens=None, causal: bool = True, strea
     if stream is not None or _current_device() != dev:
         return _elsewhere(lambda: row_ranges(doc_lens, N, prefix_lens=prefix_lens, causal=causal),
                           dev, stream, (doc_lens, prefix_lens))
+    if N >> 31 or M >> 31:
+        _check(-3)  # ATTN_ERR_SHAPE: ctypes would pass it modulo 2^32
     out = torch.empty((B, N, 2), dtype=i32, device=doc_lens.device)
     rc = (_lib or load()).attn_row_ranges(
         doc_lens.data_ptr(), None if prefix_lens is None else prefix_lens.data_ptr(),
@@ -584,6 +606,8 @@ def _decode(fn, q, pre, kcache, vcache, lens, scale, softcap, slopes, stream):
     if stream is not None or _current_device() != dev:
         return _elsewhere(lambda: _decode(fn, q, pre, kcache, vcache, lens, scale, softcap, slopes, None),
                           dev, stream, (q, *pre, kcache, vcache, lens, slopes))
+    if 0 < softcap < _LEAST_CAP:
+        _check(-3)  # ATTN_ERR_SHAPE: ctypes would pass it as no cap
     device = q.device
     o = torch.empty_strided((B, Hq, D), (Hq * D, D, 1), dtype=bf16, device=device)
     lse = torch.empty_strided((B, Hq), (Hq, 1), dtype=torch.float32, device=device)

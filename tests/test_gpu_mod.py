@@ -847,3 +847,14 @@ def test_outputs_on_another_stream_take_no_memory_that_is_still_read(which, hand
     torch.cuda.synchronize()
     del busy, over
     assert all(torch.equal(x, y) for x, y in zip(reads, want))
+
+
+def test_helpers_refuse_values_that_change_on_their_way_to_c():
+    q, docs = rand(1, (1, 2, 16, 64)), torch.tensor([[10, 6]], dtype=torch.int32, device="cuda")
+    for call in (lambda: attn.forward_mod(q, q, q, causal=True, q_offset=2**32),
+                 lambda: attn.forward_mod(q, q, q, causal=True, q_offset=5 - 2**32),
+                 lambda: attn.row_ranges(docs, 2**32 + 16), lambda: attn.row_ranges(docs, 16 - 2**32),
+                 lambda: attn.forward_mod(q, q, q, softcap=1e-46),
+                 lambda: attn.decode_varlen(q[:, :, 0].contiguous(), q, q, softcap=1e-46)):
+        with pytest.raises(attn.AttnError):
+            call()

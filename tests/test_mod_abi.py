@@ -102,3 +102,27 @@ def test_helpers_refuse_what_the_library_cannot_see():
         attn.row_ranges(torch.zeros(1, 2), 8)
     with pytest.raises(TypeError, match="torch tensor"):
         attn.row_ranges([[1, 2]], 8)
+
+
+WIDE = [(fn, name) for fn, case in (("attn_fwd_mod", OK_FWD), ("attn_row_ranges", OK_RANGES),
+                                    ("attn_decode_varlen", OK_VARLEN), ("attn_decode_prefix", OK_PREFIX))
+        for name in case if name in ("B", "Hq", "Hkv", "Nq", "Nk", "Ncap", "Np", "N", "M", "D", "q_offset")]
+
+
+@pytest.mark.parametrize("fn,name", WIDE, ids=lambda x: x)
+@pytest.mark.parametrize("turns", [1, -1])
+def test_sizes_that_only_fit_after_wrapping_are_refused(lib, fn, name, turns):
+    """2^32 more or less is the same int in C."""
+    case = {"attn_fwd_mod": OK_FWD, "attn_row_ranges": OK_RANGES, "attn_decode_varlen": OK_VARLEN,
+            "attn_decode_prefix": OK_PREFIX}[fn]
+    with pytest.raises(attn.AttnError) as e:
+        getattr(attn, fn)(**{**case, name: case[name] + turns * 2**32}, stream=0)
+    assert e.value.status == SHAPE
+
+
+@pytest.mark.parametrize("fn,case", [("attn_fwd_mod", OK_FWD), ("attn_decode_varlen", OK_VARLEN),
+                                     ("attn_decode_prefix", OK_PREFIX)], ids=lambda x: x if isinstance(x, str) else "")
+def test_caps_that_a_float_rounds_to_none_are_refused(lib, fn, case):
+    with pytest.raises(attn.AttnError) as e:
+        getattr(attn, fn)(**{**case, "softcap": 1e-46}, stream=0)
+    assert e.value.status == SHAPE
