@@ -104,7 +104,10 @@ int with_scratch(size_t bytes, int dev, cudaStream_t stream,
     }
   }
   // after the entry's previous use, if another stream made it
-  if (!same && cudaStreamWaitEvent(stream, en->done, 0) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (!same && cudaStreamWaitEvent(stream, en->done, 0) != cudaSuccess) {
+    en->live = false;  // nobody's: whoever takes it next waits
+    return ATTN_ERR_CUDA;
+  }
   if (en->bytes < bytes) {
     if (en->ptr && cudaFreeAsync(en->ptr, stream) != cudaSuccess) {
       en->live = false;
