@@ -234,10 +234,10 @@ constexpr float kLoose = 100.f;
 template <int D, bool kCap, bool kBias>
 struct Scores {
   // A capped tile's unseen keys: 0 for the maximum and cap_off for the weights in one
-  // go, or one after the other around a loop that masked tiles share with others.
-  // Which one the compiler makes the better kernel of: B1 Hq32 Hkv8 N8192 causal D128
-  // 462 us (one after the other 472), D64 467 (453).
-  static constexpr bool kOneGo = D == 128;
+  // go, or one after the other.  The work is the same; which one the compiler makes the
+  // better kernel of was measured, B1 Hq32 Hkv8 N8192 causal in us: D128 464 in one go
+  // (one after the other 472), D64 469 (460), D64 biased 525 (547).
+  static constexpr bool kOneGo = D == 128 || kBias;
   static constexpr int kModified = 4;
   int tier;          // capped: which polynomial; 3: the longest, not linear;
                      // kModified: the scores are modified already
@@ -295,7 +295,6 @@ struct Scores {
     if constexpr (kCap) {
       float a0 = 0.f, a1 = 0.f;
       // what lies at unseen keys has no say, and gets a weight of 0
-      if (!kOneGo && masked) mask_to(s, seen, 0.f);
       if (kOneGo && masked) {
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {
@@ -309,6 +308,18 @@ struct Scores {
           s[i] = in0 ? s[i] : p.mod.cap_off;
           s[i + 1] = in1 ? s[i + 1] : p.mod.cap_off;
         }
+      } else if (masked) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          const uint32_t w = seen.words[i / 32];
+          const float x0 = (w >> (i % 32)) & 1u ? s[i] : 0.f;
+          const float x1 = (w >> (i % 32 + 1)) & 1u ? s[i + 1] : 0.f;
+          const float x2 = (w >> (i % 32 + 2)) & 1u ? s[i + 2] : 0.f;
+          const float x3 = (w >> (i % 32 + 3)) & 1u ? s[i + 3] : 0.f;
+          a0 = max3f(a0, fabsf(x0), fabsf(x1));
+          a1 = max3f(a1, fabsf(x2), fabsf(x3));
+        }
+        mask_to(s, seen, p.mod.cap_off);
       } else {
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
@@ -326,7 +337,6 @@ struct Scores {
       // no score of the warp's rows is larger: |tanh x| <= |x|, 1
       const float top = fminf(all * p.scale_log2, p.mod.cap_out);
       m = top + most[0];
-      if (!kOneGo && masked) mask_to(s, seen, p.mod.cap_off);
       return holds && 2.f * top <= kLoose;
     } else {
       if (masked) mask_to(s, seen, -CUDART_INF_F);
