@@ -858,3 +858,80 @@ def test_helpers_refuse_values_that_change_on_their_way_to_c():
                  lambda: attn.decode_varlen(q[:, :, 0].contiguous(), q, q, softcap=1e-46)):
         with pytest.raises(attn.AttnError):
             call()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (12.0, False), (0.0, True), (12.0, True)],
+                         ids=["plain", "cap", "bias", "both"])
+@pytest.mark.parametrize("kind", ["all", "causal", "ranges", "causal ranges"])
+def test_items_one_after_another_on_a_cta(D, cap, bias, kind):
+    """More work items than CTAs, every row checked: what an item leaves behind (Q, the
+    rows' data, the parities of every barrier) is not what the next one takes.  With
+    ranges the items are of very different lengths, some of them empty."""
+    B, Hq, Hkv, Nq, Nk = 3, 24, 12, 1100, 1300
+    q, k, v = rand(1, (B, Hq, Nq, D), 3.0), rand(2, (B, Hkv, Nk, D)), rand(3, (B, Hkv, Nk, D))
+    slopes = alibi(Hq) if bias else None
+    ranges = None
+    if "ranges" in kind:
+        lens = torch.tensor([[1, 300, 2, 500, 97, 130], [0, 0, 600, 0, 0, 0], [7, 7, 400, 600, 0, 0]],
+                            dtype=torch.int32, device="cuda")
+        ranges = attn.row_ranges(lens, Nq, causal=False)
+    causal, q_offset = "causal" in kind, 77
+    o, lse = attn.forward_mod(q, k, v, causal=causal, q_offset=q_offset, softcap=cap, slopes=slopes, ranges=ranges)
+    check_fwd(o, lse, q, k, v, causal, D ** -0.5, cap, slopes, ranges, q_offset)
+
+
+def _sizes(rng, lo, hi):
+    return max(lo, min(hi, round(math.exp(rng.uniform(math.log(lo), math.log(hi))))))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_prefills(seed):
+    import random
+    rng = random.Random(1000 + seed)
+    D, Hkv, G = rng.choice([64, 128]), rng.choice([1, 2, 3]), rng.choice([1, 2, 4, 5])
+    B, Nq, Nk = rng.randint(1, 3), _sizes(rng, 1, 700), _sizes(rng, 1, 900)
+    Hq, causal, q_offset = Hkv * G, rng.random() < 0.5, rng.choice([0, 0, rng.randint(0, 900)])
+    cap, sigma = rng.choice([0.0, 0.7, 20.0, 50.0, 300.0]), rng.choice([0.1, 1.0, 8.0, 40.0])
+    kind = rng.choice([None, "wild", "narrow", "docs", "prefix", "none"])
+    if kind in ("docs", "prefix") and Nq < 8:
+        kind = "wild"
+    slopes = None
+    if rng.random() < 0.5:
+        slopes = torch.tensor([rng.choice([1, 1, -1, 0]) * 10 ** rng.uniform(-4, 1) for _ in range(Hq)],
+                              dtype=torch.float32, device="cuda")
+    q, k, v = rand(seed, (B, Hq, Nq, D), sigma), rand(seed + 100, (B, Hkv, Nk, D)), rand(seed + 200, (B, Hkv, Nk, D))
+    # scores of one sign in parts, so that a row's keys differ from its neighbours'
+    if rng.random() < 0.5:
+        q += sigma
+        k[:, :, Nk // 2:] -= 1
+    ranges = ranges_of(kind, B, Nq, Nk, seed)
+    scale = rng.choice([D ** -0.5, 0.02, 1.0])
+    o, lse = attn.forward_mod(q, k, v, causal=causal, q_offset=q_offset, softcap=cap, slopes=slopes, ranges=ranges,
+                              scale=scale)
+    check_fwd(o, lse, q, k, v, causal, scale, cap, slopes, ranges, q_offset, f"{D, B, Hq, Hkv, Nq, Nk, cap, kind}")
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_decodes(seed):
+    import random
+    rng = random.Random(2000 + seed)
+    D, Hkv, G = rng.choice([64, 128]), rng.choice([1, 2, 3]), rng.choice([1, 2, 4, 5, 8, 9, 16, 33])
+    B, Ncap, Np = _sizes(rng, 1, 60), _sizes(rng, 1, 2000), _sizes(rng, 1, 9000)
+    Hq, cap, sigma = Hkv * G, rng.choice([0.0, 0.7, 20.0, 300.0]), rng.choice([0.1, 1.0, 8.0])
+    lens = [rng.choice([0, 1, Ncap, rng.randint(0, Ncap)]) for _ in range(B)]
+    slopes = None
+    if rng.random() < 0.5:
+        slopes = torch.tensor([rng.choice([1, 1, -1, 0]) * 10 ** rng.uniform(-4, 0) for _ in range(Hq)],
+                              dtype=torch.float32, device="cuda")
+    q, k, v = rand(seed, (B, Hq, D), sigma), rand(seed + 100, (B, Hkv, Ncap, D)), rand(seed + 200, (B, Hkv, Ncap, D))
+    pk, pv = rand(seed + 300, (Hkv, Np, D)), rand(seed + 400, (Hkv, Np, D))
+    for b, n in enumerate(lens):
+        for x in (k, v):
+            x[b, :, n:] = (NAN, INF, -INF)[b % 3]
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    some = sorted({0, B - 1, *(rng.randrange(B) for _ in range(4))})
+    o, lse = attn.decode_varlen(q, k, v, t, softcap=cap, slopes=slopes)
+    check_decode(o, lse, q, k, v, lens, cap, slopes, rows=some)
+    o, lse = attn.decode_prefix(q, pk, pv, k, v, t, softcap=cap, slopes=slopes)
+    check_decode(o, lse, q, k, v, lens, cap, slopes, pk, pv, rows=some)
