@@ -382,7 +382,20 @@ int mod_decode(const ModDecodeParams& p, cudaStream_t stream) {
   // 256 behind 8192 75.0, 80.3; D 64, 128 requests 49.5, 51.2.
   const bool cap = p.mod.cap_out > 0.f, bias = p.mod.slopes != nullptr;
   k.prefix_cost = (p.D == 128 ? 1.5f : 1.2f) + (cap ? 0.6f : 0.f) + (bias ? 0.5f : 0.f);
-  k.own_cost = p.D == 128 ? 1.15f : 0.6f + (cap ? 0.3f : 0.f) + (k.G > 4 ? 0.2f : 0.f);
+  // The whole call at own costs of 0.45, 0.6, 0.75, 0.9, 1.2, 1.7, 64 requests as above:
+  // D 64, 4 heads 32.1, 30.9, 31.5, 32.4, 31.7, 37.8, capped 41.0, 39.8, 40.0, 41.9,
+  // 43.3, 47.2, 8 heads (4 KV heads) 36.8, 32.5, 28.3, 29.7, 30.6, 32.7, capped 49.7,
+  // 42.1, 39.8, 36.9, 38.2, 40.7; 256 behind 8192, D 64, 4 heads 55.6, 49.4, 50.9, 53.7,
+  // 60.0, 70.1, capped 72.2, 66.7, 69.5, 72.4, 80.2, 90.5; 128 behind 8192, D 64, 1
+  // head, capped and biased 35.7, 32.8, 31.1, 30.0, 32.5, 35.7; 256 behind 8192, D 128
+  // 90.9, 78.5, 71.4, 67.1, 65.3, 74.8, capped 114.7, 96.6, 84.9, 78.3, 75.6, 84.2,
+  // biased 108.6, 91.9, 82.5, 75.7, 75.6, 83.7: no matter of caps or heads at D 128.
+  if (p.D == 128)
+    k.own_cost = 1.15f;
+  else if (k.G <= 4)
+    k.own_cost = cap ? 0.75f : 0.6f;
+  else
+    k.own_cost = cap ? 1.1f : 0.8f;
   common_params(&k, p.mod, di);
   const long long prefix_items =
       p.Np > 0 ? static_cast<long long>(p.Hkv) * k.row_blocks : 0;
