@@ -215,11 +215,11 @@ int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, in
 // queues on `stream`: the stream's cached buffer or, during capture, one of the
 // graph's own.  Returns launch's status or an ATTN_ERR_*.
 // `dev`: the current device.
-// As with_scratch, with a buffer that is allocated for the call alone.
-int with_own_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
-                     void* ctx);
 int with_scratch(size_t bytes, int dev, cudaStream_t stream,
                  int (*launch)(void* ctx, void* scratch, cudaStream_t stream), void* ctx);
+// The same with a buffer that is allocated for the call alone.
+int with_own_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
+                     void* ctx);
 
 // Check the device and queue the kernels; arguments are checked before.
 // Return an ATTN_* status.

@@ -80,8 +80,8 @@ struct PrefixPlan {
 
 // Decode: query tile t's run of the requests' own key tiles (warp-wide).  Run
 // r of 2 x CTAs belongs to query tile r / CTAs; the CTAs (those that have own keys)
-// count from the other end than those of the prefix.  The tiles of all items are laid end to end, request by request, KV head by
-// KV head.
+// count from the other end than those of the prefix.  The tiles of all items are laid
+// end to end, request by request, KV head by KV head.
 struct OwnPlan {
   int left;        // tiles left of the run
   int run;

@@ -1182,58 +1182,58 @@ __global__ void __launch_bounds__(kModThreads, 1)
         if (!ok) break;
       }
       if (!kSplit || live) {
-      tc_fence_after();
-      // ---- epilogue: O / l and the LSE; a row that saw nothing gives 0 and -inf
-      int head;
-      size_t out;
-      const bool valid = item_row<kSplit>(p, w, t, r, jb > 0, head, out);
-      const float l_row = l + __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-      const bool none = l_row == 0.f;  // or no tiles: O in TMEM is not the item's
-      const float inv = none ? 0.f : 1.f / l_row;
-      const float lse2 = none ? -CUDART_INF_F : m + __log2f(l_row);
-      // rolled: code that runs once an item comes from far at every line
+        tc_fence_after();
+        // ---- epilogue: O / l and the LSE; a row that saw nothing gives 0 and -inf
+        int head;
+        size_t out;
+        const bool valid = item_row<kSplit>(p, w, t, r, jb > 0, head, out);
+        const float l_row = l + __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+        const bool none = l_row == 0.f;  // or no tiles: O in TMEM is not the item's
+        const float inv = none ? 0.f : 1.f / l_row;
+        const float lse2 = none ? -CUDART_INF_F : m + __log2f(l_row);
+        // rolled: code that runs once an item comes from far at every line
 #pragma unroll 1
-      for (int kk = 0; kk < D / 32; ++kk) {
-        uint32_t v[16];  // columns c * D / 2 + [16 kk, 16 kk + 16) of the row
-        tmem_ld_pair16<D / 2>(o_addr + kk * 16, v);
-        const size_t at = out * D + c * (D / 2) + kk * 16;
-        if constexpr (kSplit) {
-          float* dst = (w.kind ? p.part_o : p.pre_o) + at;
+        for (int kk = 0; kk < D / 32; ++kk) {
+          uint32_t v[16];  // columns c * D / 2 + [16 kk, 16 kk + 16) of the row
+          tmem_ld_pair16<D / 2>(o_addr + kk * 16, v);
+          const size_t at = out * D + c * (D / 2) + kk * 16;
+          if constexpr (kSplit) {
+            float* dst = (w.kind ? p.part_o : p.pre_o) + at;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            v[i] = none ? 0u : __float_as_uint(__uint_as_float(v[i]) * inv);
-          if (valid) {
-            st_global_v8(dst, v);  // a whole 32-byte sector
-            st_global_v8(dst + 8, v + 8);
-          }
-        } else {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + at;
-          uint32_t o2[8];
+            for (int i = 0; i < 16; ++i)
+              v[i] = none ? 0u : __float_as_uint(__uint_as_float(v[i]) * inv);
+            if (valid) {
+              st_global_v8(dst, v);  // a whole 32-byte sector
+              st_global_v8(dst + 8, v + 8);
+            }
+          } else {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + at;
+            uint32_t o2[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            o2[i] = none ? 0u
-                         : pack_bf16x2(__uint_as_float(v[2 * i]) * inv,
-                                       __uint_as_float(v[2 * i + 1]) * inv);
-          if (valid) {
-            if (p.o_sectors) {
-              st_global_v8(dst, o2);
-            } else {
+            for (int i = 0; i < 8; ++i)
+              o2[i] = none ? 0u
+                           : pack_bf16x2(__uint_as_float(v[2 * i]) * inv,
+                                         __uint_as_float(v[2 * i + 1]) * inv);
+            if (valid) {
+              if (p.o_sectors) {
+                st_global_v8(dst, o2);
+              } else {
 #pragma unroll
-              for (int g = 0; g < 2; ++g)
-                reinterpret_cast<uint4*>(dst)[g] =
-                    make_uint4(o2[4 * g], o2[4 * g + 1], o2[4 * g + 2], o2[4 * g + 3]);
+                for (int g = 0; g < 2; ++g)
+                  reinterpret_cast<uint4*>(dst)[g] =
+                      make_uint4(o2[4 * g], o2[4 * g + 1], o2[4 * g + 2], o2[4 * g + 3]);
+              }
             }
           }
         }
-      }
-      if (valid && c == 0) {
-        if constexpr (kSplit)
-          (w.kind ? p.part_lse : p.pre_lse)[out] = lse2;
-        else
-          p.lse[out] = (kBias ? lse2 - ms.slopes[t * kBM + r] *
-                                           static_cast<float>(ms.rows[t * kBM + r].ref)
-                              : lse2) * kLn2;
-      }
+        if (valid && c == 0) {
+          if constexpr (kSplit)
+            (w.kind ? p.part_lse : p.pre_lse)[out] = lse2;
+          else
+            p.lse[out] = (kBias ? lse2 - ms.slopes[t * kBM + r] *
+                                             static_cast<float>(ms.rows[t * kBM + r].ref)
+                                : lse2) * kLn2;
+        }
       }
       work_done<kSlots>(ms, t, k, lane);
     }
