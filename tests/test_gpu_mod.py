@@ -935,3 +935,76 @@ def test_random_decodes(seed):
     check_decode(o, lse, q, k, v, lens, cap, slopes, rows=some)
     o, lse = attn.decode_prefix(q, pk, pv, k, v, t, softcap=cap, slopes=slopes)
     check_decode(o, lse, q, k, v, lens, cap, slopes, pk, pv, rows=some)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_query_and_output_offsets_beyond_32_bits(D):
+    """More than 2^32 elements of Q and O: the last rows of the last heads are theirs."""
+    if torch.cuda.mem_get_info()[0] < 60 * 2**30:
+        pytest.skip("needs 40 GB")
+    Hq, Hkv, Nk, tail = 64, 2, 5000, 300
+    Nq = 2**32 // (Hq * D) + 1111
+    q = torch.zeros((1, Hq, Nq, D), dtype=torch.bfloat16, device="cuda")
+    heads = (0, Hq // 2 - 1, Hq - 1)
+    for h in heads:
+        q[0, h, Nq - tail:] = rand(h, (tail, D))
+    k, v = rand(100, (1, Hkv, Nk, D)), rand(101, (1, Hkv, Nk, D))
+    lo = (torch.arange(Nq, device="cuda") * (Nk - 50) // Nq).int()
+    ranges = torch.stack([lo, lo + 50], -1)[None].contiguous()
+    o, lse = attn.forward_mod(q, k, v, ranges=ranges, softcap=20.0)
+    j, rows = torch.arange(Nk, device="cuda"), slice(Nq - tail, Nq)
+    seen = (j >= ranges[0, rows, :1]) & (j < ranges[0, rows, 1:])
+    for h in heads:
+        ref = definition(q[0, h, rows], k[0, h // 32], v[0, h // 32], j[:tail], j, seen, D ** -0.5, 20.0, None)
+        check(o[0, h, rows], lse[0, h, rows], ref, f"h{h}")
+
+
+def test_captured_prefill_of_several_segments_beside_an_eager_one():
+    """The accumulators of segments belong to their call: two graphs and an eager call at
+    once, each replayed on keys that changed."""
+    Hq, Nq, Nk, D = 2, 130, 300_000, 64
+    sets, graphs = [], []
+    for i in range(3):
+        sets.append([rand(i, (1, Hq, Nq, D)), rand(10 + i, (1, 1, Nk, D)), rand(20 + i, (1, 1, Nk, D))])
+    torch.cuda.synchronize()
+    for q, k, v in sets[:2]:
+        g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=s):
+            out = attn.forward_mod(q, k, v, softcap=30.0)
+        graphs.append((g, s, out))
+    for turn in range(2):
+        for i, x in enumerate(sets):
+            x[1].copy_(rand(50 + 3 * turn + i, x[1].shape))
+        torch.cuda.synchronize()
+        for g, s, _ in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = attn.forward_mod(*sets[2], softcap=30.0)
+        torch.cuda.synchronize()
+        for x, out in zip(sets, [graphs[0][2], graphs[1][2], eager]):
+            check_fwd(*out, *x, False, 1 / 8, 30.0, None, None, 0)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (24, 2)])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, True)])
+def test_nan_in_a_query_or_a_request_s_keys_stays_there(Hq, Hkv, cap, bias):
+    lens = [300, 40, 129, 0]
+    q, k, v = rand(1, (4, Hq, 64)), rand(2, (4, Hkv, 300, 64)), rand(3, (4, Hkv, 300, 64))
+    pk, pv = rand(4, (Hkv, 1000, 64)), rand(5, (Hkv, 1000, 64))
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    slopes = alibi(Hq) if bias else None
+    clean = [attn.decode_varlen(q, k, v, t, softcap=cap, slopes=slopes),
+             attn.decode_prefix(q, pk, pv, k, v, t, softcap=cap, slopes=slopes)]
+    q[0, 3], k[1, 1, 17], k[2, 0, 128, 5] = NAN, NAN, NAN
+    G = Hq // Hkv
+    hit = torch.zeros(4, Hq, dtype=torch.bool, device="cuda")
+    hit[0, 3], hit[1, G:], hit[2, :G] = True, True, True
+    dirty = [attn.decode_varlen(q, k, v, t, softcap=cap, slopes=slopes),
+             attn.decode_prefix(q, pk, pv, k, v, t, softcap=cap, slopes=slopes)]
+    for (o, lse), (co, cl) in zip(dirty, clean):
+        assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+        # (a running maximum that a NaN keeps in place is another reference: not other values)
+        assert torch.equal(torch.isinf(lse[~hit]), torch.isinf(cl[~hit]))
+        assert torch.allclose(o[~hit].float(), co[~hit].float(), atol=2.0**-6, rtol=2.0**-7)
+        fin = ~torch.isinf(cl) & ~hit
+        assert torch.allclose(lse[fin], cl[fin], atol=1e-4, rtol=0)
