@@ -458,24 +458,29 @@ def _elsewhere(call, dev: int, stream, inputs):
     inputs are marked as used on the other stream and the outputs as used on the
     current one, so that neither's memory is handed out while it is in use."""
     cuda = _torch.cuda
-    with cuda.device(dev):
-        if stream is None:
-            return call()
-        if isinstance(stream, int):
-            stream = cuda.ExternalStream(stream, device=dev) if stream else cuda.default_stream(dev)
-        elif stream.device.index != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
-        current = cuda.current_stream(dev)
-        if stream.cuda_stream == current.cuda_stream:
-            return call()
-        with cuda.stream(stream):
-            out = call()
-        for x in inputs:
-            if x is not None:
-                x.record_stream(stream)
-        for x in out if isinstance(out, tuple) else (out,):
-            x.record_stream(current)
-        return out
+    if _current_device() != dev:
+        with cuda.device(dev):
+            return _elsewhere(call, dev, stream, inputs)
+    if stream is None:
+        return call()
+    if isinstance(stream, int):
+        stream = cuda.ExternalStream(stream, device=dev) if stream else cuda.default_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    current = cuda.current_stream(dev)
+    if stream.cuda_stream == current.cuda_stream:
+        return call()
+    cuda.set_stream(stream)  # (and back: 10 us less than by a context)
+    try:
+        out = call()
+    finally:
+        cuda.set_stream(current)
+    for x in inputs:
+        if x is not None:
+            x.record_stream(stream)
+    for x in out if isinstance(out, tuple) else (out,):
+        x.record_stream(current)
+    return out
 
 
 # The first call of each of these two puts the quickest way there is in its place.
