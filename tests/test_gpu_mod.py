@@ -1008,3 +1008,25 @@ def test_nan_in_a_query_or_a_request_s_keys_stays_there(Hq, Hkv, cap, bias):
         assert torch.allclose(o[~hit].float(), co[~hit].float(), atol=2.0**-6, rtol=2.0**-7)
         fin = ~torch.isinf(cl) & ~hit
         assert torch.allclose(lse[fin], cl[fin], atol=1e-4, rtol=0)
+
+
+def test_calls_captured_on_a_stream_beside_the_capturing_one():
+    q, k, v = rand(1, (3, 8, 64)), rand(2, (3, 2, 500, 64)), rand(3, (3, 2, 500, 64))
+    x, lens = rand(4, (1, 2, 300, 64)), torch.tensor([500, 3, 77], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    g, s, side = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        side.wait_stream(s)
+        a = attn.decode_varlen(q, k, v, lens, stream=side)
+        b = attn.forward_mod(x, x, x, causal=True, stream=side)
+        c = attn.decode_varlen(q, k, v, lens, softcap=5.0)
+        s.wait_stream(side)
+        d = attn.forward_mod(x, x, x, softcap=5.0)
+    for turn in range(2):
+        lens.copy_(torch.tensor([400 + turn, 0, 78], dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        check_decode(*a, q, k, v, [400 + turn, 0, 78], 0.0, None)
+        check_decode(*c, q, k, v, [400 + turn, 0, 78], 5.0, None)
+        check_fwd(*b, x, x, x, True, 1 / 8, 0.0, None, None, 0)
+        check_fwd(*d, x, x, x, False, 1 / 8, 5.0, None, None, 0)
