@@ -36,10 +36,10 @@
 //
 // What bounds it and what it measures (us on a GB300, by CUDA events).
 //   * Prefill, long rows: the chain of a query tile, product, softmax, product,
-//     of which two run at a time.  B1 Hq32 Hkv8 N8192 D128 causal: 344 (1.60
-//     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 459, biased 460,
-//     both 568; D64 274, 453, 383.  The tensor pipe is 49% busy capped, the issue
-//     slots 55%: a pass over a tile is longer than the products of the other.
+//     of which two run at a time.  B1 Hq32 Hkv8 N8192 D128 causal: 350 (1.57
+//     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 465, biased 460,
+//     both 568; D64 271, 460, 380, 524.  The tensor pipe is 50% busy capped, the issue
+//     slots 56%: a pass over a tile is longer than the products of the other.
 //   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
 //     for its first scores and its epilogue next to 2.9k a tile.  Packed documents
 //     B4 H16 N4096 D128: 89, tensor pipe 37%.
@@ -121,7 +121,8 @@ struct RowInfo {
 
 // Is S_t written in two halves, that of the keys [64, 128) while the softmax warps
 // still have the tile before?  Not with a cap or a bias: D64 B1 Hq32 Hkv8 N8192
-// causal 453 us capped (in halves 453), 384 biased (392); D128 465 (486), 461 (474).
+// causal 460 us capped (in halves 452, but packed documents 94, not 92), 380 biased
+// (387); D128 468 (486), 461 (472).
 template <int D, bool kCap, bool kBias>
 constexpr bool kSplitScores = Cfg<D, false>::kSplitS && !kCap && !kBias;
 

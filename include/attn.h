@@ -424,7 +424,7 @@ int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix,
 const char *attn_status_string(int status);
 
 /* Synchronises `stream`, then returns the device error word of the current
- * device (ATTN_DEVERR_* bits, 0 when no kernel gave up a wait) and clears
+ * device (ATTN_DEVERR_* bits, 0 when no kernel reported anything) and clears
  * it.  Returns a negative ATTN_ERR_* code if a CUDA call fails. */
 int attn_get_device_error(cudaStream_t stream);
 
