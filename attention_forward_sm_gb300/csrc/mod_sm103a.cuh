@@ -1039,10 +1039,13 @@ __global__ void __launch_bounds__(kModThreads, 1)
         seen.w = live ? __reduce_max_sync(0xFFFFFFFFu, row.hi) : 0;
         if (lane == 0) ms.seen[warp] = seen;
         if constexpr (kBias) {
-          // rows whose bias does not go with the exponential
+          // Rows whose bias does not go with the exponential: those that look both ways with
+          // a negative slope, and steep slopes, for which the biases of 16 keys, summed up in
+          // steps, lose digits of the nearest one's (and, without a cap, say too little
+          // about the largest score).
           const bool slow =
               __any_sync(0xFFFFFFFFu, (slope < 0.f && row.lo < row.pos && row.hi - 1 > row.pos) ||
-                                          (!kCap && fabsf(slope) * 15.f > kLoose));
+                                          fabsf(slope) * 15.f > kLoose);
           if (lane == 0) ms.slow[warp] = slow;
         }
         if (c == 0) {

@@ -1030,3 +1030,27 @@ def test_calls_captured_on_a_stream_beside_the_capturing_one():
         check_decode(*c, q, k, v, [400 + turn, 0, 78], 5.0, None)
         check_fwd(*b, x, x, x, True, 1 / 8, 0.0, None, None, 0)
         check_fwd(*d, x, x, x, False, 1 / 8, 5.0, None, None, 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("slope", [4.0, 4.7, 17.0, 100.0, 3e4])
+@pytest.mark.parametrize("cap", [0.0, 20.0, 100.0])
+def test_steep_biases(D, slope, cap):
+    """Slopes at which a few keys, or one, have all the weight: the roundings of biases
+    of keys far from those have no part in the result."""
+    q, k, v = rand(1, (1, 4, 300, D), 0.05), rand(2, (1, 2, 400, D)), rand(3, (1, 2, 400, D))
+    slopes = torch.tensor([slope, -slope, slope / 3, 0.1], device="cuda")
+    i = torch.arange(300, device="cuda")
+    one = torch.stack([i + 50, i + 51], -1)[None].int()  # each row sees the key at its position alone
+    for causal, kind in ((True, None), (False, "prefix"), (False, "narrow"), (False, "one"), (False, "before")):
+        ranges = one if kind == "one" else one - 30 if kind == "before" else ranges_of(kind, 1, 300, 400)
+        o, lse = attn.forward_mod(q, k, v, causal=causal, q_offset=50, softcap=cap, slopes=slopes, ranges=ranges)
+        check_fwd(o, lse, q, k, v, causal, D ** -0.5, cap, slopes, ranges, 50, kind)
+    q1, pk, pv = rand(4, (3, 4, D), 0.05), rand(5, (2, 333, D)), rand(6, (2, 333, D))
+    k3, v3 = rand(7, (3, 2, 200, D)), rand(8, (3, 2, 200, D))
+    lens = [200, 0, 17]
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = attn.decode_prefix(q1, pk, pv, k3, v3, t, softcap=cap, slopes=slopes)
+    check_decode(o, lse, q1, k3, v3, lens, cap, slopes, pk, pv)
+    o, lse = attn.decode_varlen(q1, k3, v3, t, softcap=cap, slopes=slopes)
+    check_decode(o, lse, q1, k3, v3, lens, cap, slopes)
