@@ -38,7 +38,7 @@
 //   * Prefill, long rows: the chain of a query tile, product, softmax, product,
 //     of which two run at a time.  B1 Hq32 Hkv8 N8192 D128 causal: 350 (1.57
 //     PFLOP/s, as without modifications in fwd_sm103a.cu), capped 465, biased 460,
-//     both 568; D64 271, 460, 380, 524.  The tensor pipe is 50% busy capped, the issue
+//     both 568; D64 271, 460, 380, 520.  The tensor pipe is 50% busy capped, the issue
 //     slots 56%: a pass over a tile is longer than the products of the other.
 //   * Prefill, short rows: what an item costs besides its tiles, about 5k cycles
 //     for its first scores and its epilogue next to 2.9k a tile.  Packed documents
