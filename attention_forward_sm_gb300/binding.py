@@ -25,7 +25,8 @@ EXPORTED = ["attn_fwd", "attn_fwd_rows", "attn_fwd_fp8", "attn_fwd_host", "attn_
             "attn_status_string", "attn_get_device_error", "attn_decode_workspace_bytes",
             "attn_selftest_wait_timeout", "attn_decode_splitkv_states", "attn_combine_states",
             "attn_decode_graph_create", "attn_decode_graph_launch", "attn_decode_graph_destroy",
-            "attn_fwd_mod", "attn_row_ranges", "attn_decode_varlen", "attn_decode_prefix"]
+            "attn_fwd_mod", "attn_row_ranges", "attn_decode_varlen", "attn_decode_prefix",
+            "attn_cache_write", "attn_cache_read", "attn_paged_fwd", "attn_paged_decode"]
 DEVERR_SELFTEST = 0x10
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024
 
@@ -92,6 +93,18 @@ def load(path: str = LIB_PATH):
         lib.attn_decode_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, f,
                                            vp, vp]
         lib.attn_decode_prefix.restype = i
+        ll = ctypes.c_longlong
+        lib.attn_cache_write.argtypes = [vp, vp, ll, ll, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i,
+                                         vp]
+        lib.attn_cache_write.restype = i
+        lib.attn_cache_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp]
+        lib.attn_cache_read.restype = i
+        lib.attn_paged_fwd.argtypes = [vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i,
+                                       i, i, f, vp]
+        lib.attn_paged_fwd.restype = i
+        lib.attn_paged_decode.argtypes = [vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f,
+                                          vp]
+        lib.attn_paged_decode.restype = i
         lib.attn_decode_workspace_bytes.argtypes = [i, i, i, i]
         lib.attn_decode_workspace_bytes.restype = ctypes.c_longlong
         _lib = lib
@@ -110,6 +123,14 @@ def _int(x) -> int:
     """A size for a C int, which would take what does not fit modulo 2^32."""
     x = int(x)
     if not -2**31 <= x < 2**31:
+        _check(-3)  # ATTN_ERR_SHAPE
+    return x
+
+
+def _long(x) -> int:
+    """A stride for a C long long."""
+    x = int(x)
+    if not -2**63 <= x < 2**63:
         _check(-3)  # ATTN_ERR_SHAPE
     return x
 
@@ -288,6 +309,46 @@ def attn_decode_prefix(q, kprefix, vprefix, kcache, vcache, lens, o, lse, B, Hq,
                                      _ptr(vcache), _ptr(lens), _ptr(o), _ptr(lse), _int(B), _int(Hq),
                                      _int(Hkv), _int(Np), _int(Ncap), _int(D), float(scale),
                                      _cap(softcap), _ptr(slopes), _stream(stream)))
+
+
+def attn_cache_write(k, v, k_stride, v_stride, kpages, vpages, kscale, vscale, table, lens, offsets,
+                     B, T, Hkv, D, page, P, M, stream=None) -> None:
+    """``attn_cache_write`` of include/attn.h: new tokens' K and V into the pages of
+    their requests; with ``kscale`` and ``vscale`` quantised to e4m3."""
+    _check(load().attn_cache_write(_ptr(k), _ptr(v), _long(k_stride), _long(v_stride), _ptr(kpages),
+                                   _ptr(vpages), _ptr(kscale), _ptr(vscale), _ptr(table), _ptr(lens),
+                                   _ptr(offsets), _int(B), _int(T), _int(Hkv), _int(D), _int(page),
+                                   _int(P), _int(M), _stream(stream)))
+
+
+def attn_cache_read(kpages, vpages, kscale, vscale, table, lens, offsets, k, v, B, T, Hkv, D, page,
+                    P, M, stream=None) -> None:
+    """``attn_cache_read`` of include/attn.h: the last tokens of each request as
+    dense bf16 rows."""
+    _check(load().attn_cache_read(_ptr(kpages), _ptr(vpages), _ptr(kscale), _ptr(vscale), _ptr(table),
+                                  _ptr(lens), _ptr(offsets), _ptr(k), _ptr(v), _int(B), _int(T),
+                                  _int(Hkv), _int(D), _int(page), _int(P), _int(M),
+                                  _stream(stream)))
+
+
+def attn_paged_fwd(q, q_stride, kpages, vpages, kscale, vscale, table, lens, offsets, o, lse, B, T,
+                   max_new, Hq, Hkv, D, page, P, M, causal, scale, stream=None) -> None:
+    """``attn_paged_fwd`` of include/attn.h: attention of several new tokens of
+    each request over its paged cache."""
+    _check(load().attn_paged_fwd(_ptr(q), _long(q_stride), _ptr(kpages), _ptr(vpages), _ptr(kscale),
+                                 _ptr(vscale), _ptr(table), _ptr(lens), _ptr(offsets), _ptr(o),
+                                 _ptr(lse), _int(B), _int(T), _int(max_new), _int(Hq), _int(Hkv),
+                                 _int(D), _int(page), _int(P), _int(M), int(bool(causal)),
+                                 float(scale), _stream(stream)))
+
+
+def attn_paged_decode(q, q_stride, kpages, vpages, kscale, vscale, table, lens, o, lse, B, Hq, Hkv, D,
+                      page, P, M, scale, stream=None) -> None:
+    """``attn_paged_decode`` of include/attn.h: one new token per request."""
+    _check(load().attn_paged_decode(_ptr(q), _long(q_stride), _ptr(kpages), _ptr(vpages),
+                                    _ptr(kscale), _ptr(vscale), _ptr(table), _ptr(lens), _ptr(o),
+                                    _ptr(lse), _int(B), _int(Hq), _int(Hkv), _int(D), _int(page),
+                                    _int(P), _int(M), float(scale), _stream(stream)))
 
 
 def attn_decode_workspace_bytes(B, Hq, D, nsplit) -> int:
@@ -650,3 +711,225 @@ def decode_prefix(q, kprefix, vprefix, kcache, vcache, lens=None, *, scale: floa
     _torch or _import_torch()
     return _decode((_lib or load()).attn_decode_prefix, q, (kprefix, vprefix), kcache, vcache, lens,
                    scale, softcap, slopes, stream)
+
+
+# ----------------------------------------------------------------------- paged cache
+#
+# The cache is a pair of tensors of pages [P, Hkv, page, D], bf16 or float8_e4m3fn with
+# scale bytes [P, Hkv, page] (uint8); table [B, M], lens [B] and offsets [B + 1] are int32
+# tensors on the same device (see include/attn.h for what they mean).  Checks as above:
+# plain comparisons first, the words only for a call that fails them.
+
+
+def _page_sizes(kpages, vpages, kscale, vscale, table, lens, offsets):
+    """(device, sizes of the cache) if its tensors fit together, else None."""
+    torch = _torch
+    try:
+        P, Hkv, page, D = kpages.shape
+        B, M = table.shape
+        dev, i32, kind = kpages.get_device(), torch.int32, kpages.dtype
+        if not (vpages.shape == kpages.shape and vpages.dtype is kind and dev >= 0
+                and vpages.get_device() == dev and kpages.is_contiguous() and vpages.is_contiguous()
+                and table.dtype is i32 and table.get_device() == dev and table.is_contiguous()
+                and lens.dtype is i32 and lens.shape == (B,) and lens.get_device() == dev
+                and lens.is_contiguous()):
+            return None
+        if offsets is not None and _aux_bad(offsets, i32, (B + 1,), dev):
+            return None
+        if kind is torch.bfloat16:
+            if kscale is not None or vscale is not None:
+                return None
+        elif kind is torch.float8_e4m3fn:
+            for x in (kscale, vscale):
+                if _aux_bad(x, torch.uint8, (P, Hkv, page), dev):
+                    return None
+        else:
+            return None
+    except (AttributeError, ValueError):
+        return None
+    return dev, (P, Hkv, page, D, B, M)
+
+
+def _rows_stride(x, heads, D, dev):
+    """Elements from one token of x [T, heads, D] to the next if it can be passed on."""
+    try:
+        if (x.dim() == 3 and x.dtype is _torch.bfloat16 and x.get_device() == dev
+                and x.shape[1] == heads and x.shape[2] == D and x.stride(2) == 1
+                and (x.stride(1) == D or heads == 1)):
+            # (torch gives the stride of a single token as it likes)
+            return x.stride(0) if x.shape[0] > 1 else heads * D
+    except AttributeError:
+        pass
+    return None
+
+
+def _refuse_pages(kpages, vpages, kscale, vscale, table, lens, offsets, rows):
+    """The words for a call whose tensors do not fit together."""
+    torch = _import_torch()
+    _check_ranks({"kpages": kpages, "vpages": vpages, "table": table},
+                 {"kpages": 4, "vpages": 4, "table": 2})
+    for name, x in (("kpages", kpages), ("vpages", vpages)):
+        if x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise TypeError(f"{name} must be bfloat16 or float8_e4m3fn, got {x.dtype}")
+    if not kpages.is_cuda:
+        raise ValueError("kpages must be a CUDA tensor")
+    P, Hkv, page, D = kpages.shape
+    B, M = table.shape
+    quant = kpages.dtype == torch.float8_e4m3fn
+    if quant and (kscale is None or vscale is None):
+        raise ValueError("float8_e4m3fn pages need kscale and vscale")
+    if not quant and (kscale is not None or vscale is not None):
+        raise ValueError("bfloat16 pages have no kscale and vscale")
+    if not kpages.is_contiguous():
+        raise ValueError("kpages must be contiguous")
+    if lens is None:
+        raise TypeError("lens must be a torch tensor")
+    _check_aux(kpages.device, vpages=(vpages, kpages.dtype, kpages.shape),
+               kscale=(kscale, torch.uint8, (P, Hkv, page)),
+               vscale=(vscale, torch.uint8, (P, Hkv, page)),
+               table=(table, torch.int32, (B, M)), lens=(lens, torch.int32, (B,)),
+               offsets=(offsets, torch.int32, (B + 1,)))
+    for name, (x, heads) in rows.items():
+        _check_ranks({name: x}, {name: 3})
+        if x.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16, got {x.dtype}")
+        if x.device != kpages.device:
+            raise ValueError(f"{name} is on {x.device}, expected {kpages.device}")
+        if x.shape[2] != D or heads is not None and x.shape[1] != heads:
+            raise ValueError(f"{name} must have shape [T, {heads or 'Hq'}, {D}], got {tuple(x.shape)}")
+        if x.stride(2) != 1 or x.shape[1] > 1 and x.stride(1) != D:
+            raise ValueError(f"the heads of a token of {name} must be contiguous")
+    raise ValueError("the tensors do not fit together")
+
+
+def cache_write(k, v, kpages, vpages, table, lens, offsets=None, *, kscale=None, vscale=None,
+                stream=None) -> None:
+    """Put the new tokens k, v [T,Hkv,D] into the pages of their requests: rows
+    ``offsets[b]`` .. ``offsets[b+1]`` are the last of the ``lens[b]`` tokens that
+    request b then has (None: row b is request b's one).  float8_e4m3fn pages
+    are written quantised, their scales into ``kscale`` and ``vscale``.  k and v may be
+    slices of a wider tensor, each token's heads contiguous."""
+    _torch or _import_torch()
+    sizes = _page_sizes(kpages, vpages, kscale, vscale, table, lens, offsets)
+    ks = vs = None
+    if sizes is not None:
+        dev, (P, Hkv, page, D, B, M) = sizes
+        ks, vs = _rows_stride(k, Hkv, D, dev), _rows_stride(v, Hkv, D, dev)
+    if ks is None or vs is None:
+        heads = kpages.shape[1] if getattr(kpages, "ndim", 0) == 4 else None
+        _refuse_pages(kpages, vpages, kscale, vscale, table, lens, offsets,
+                      {"k": (k, heads), "v": (v, heads)})
+    T = k.shape[0]
+    if v.shape[0] != T or offsets is None and T != B:
+        raise ValueError(f"inconsistent T: {T}, {v.shape[0]}" + ("" if offsets is not None else f", B {B}"))
+    if stream is not None or _current_device() != dev:
+        _elsewhere(lambda: cache_write(k, v, kpages, vpages, table, lens, offsets, kscale=kscale,
+                                       vscale=vscale) or (),
+                   dev, stream, (k, v, kpages, vpages, table, lens, offsets, kscale, vscale))
+        return
+    rc = (_lib or load()).attn_cache_write(
+        k.data_ptr(), v.data_ptr(), ks, vs, kpages.data_ptr(), vpages.data_ptr(),
+        None if kscale is None else kscale.data_ptr(), None if vscale is None else vscale.data_ptr(),
+        table.data_ptr(), lens.data_ptr(), None if offsets is None else offsets.data_ptr(), B, T, Hkv,
+        D, page, P, M, _raw_stream(dev))
+    if rc:
+        _check(rc)
+
+
+def cache_read(kpages, vpages, table, lens, offsets=None, rows: int | None = None, *, kscale=None,
+               vscale=None, stream=None):
+    """K, V [rows,Hkv,D] bf16: the last ``offsets[b+1] - offsets[b]`` tokens of each
+    request, at rows ``offsets[b]`` .. (None: the last token of request b at row
+    b), as they were written or dequantised.  Rows that belong to no request
+    are not written."""
+    torch = _torch or _import_torch()
+    sizes = _page_sizes(kpages, vpages, kscale, vscale, table, lens, offsets)
+    if sizes is None:
+        _refuse_pages(kpages, vpages, kscale, vscale, table, lens, offsets, {})
+    dev, (P, Hkv, page, D, B, M) = sizes
+    if rows is None:
+        if offsets is not None:
+            raise ValueError("rows must be given with offsets")
+        rows = B
+    elif offsets is None and rows != B:
+        raise ValueError(f"rows must be B = {B} without offsets, got {rows}")
+    if rows < 0 or rows >> 31:
+        _check(-3)  # ATTN_ERR_SHAPE
+    if stream is not None or _current_device() != dev:
+        return _elsewhere(lambda: cache_read(kpages, vpages, table, lens, offsets, rows, kscale=kscale,
+                                             vscale=vscale),
+                          dev, stream, (kpages, vpages, table, lens, offsets, kscale, vscale))
+    k, v = (torch.empty_strided((rows, Hkv, D), (Hkv * D, D, 1), dtype=torch.bfloat16,
+                                device=kpages.device) for _ in range(2))
+    rc = (_lib or load()).attn_cache_read(
+        kpages.data_ptr(), vpages.data_ptr(), None if kscale is None else kscale.data_ptr(),
+        None if vscale is None else vscale.data_ptr(), table.data_ptr(), lens.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), k.data_ptr(), v.data_ptr(), B, rows, Hkv, D,
+        page, P, M, _raw_stream(dev))
+    if rc:
+        _check(rc)
+    return k, v
+
+
+def _paged(q, kpages, vpages, table, lens, offsets, max_new, causal, kscale, vscale, scale, stream):
+    """What the two attention calls share; offsets None: decode."""
+    torch = _torch or _import_torch()
+    sizes = _page_sizes(kpages, vpages, kscale, vscale, table, lens, offsets)
+    stride = None
+    if sizes is not None and getattr(q, "ndim", 0) == 3:
+        dev, (P, Hkv, page, D, B, M) = sizes
+        T, Hq = q.shape[0], q.shape[1]
+        stride = _rows_stride(q, Hq, D, dev)
+    if stride is None:
+        _refuse_pages(kpages, vpages, kscale, vscale, table, lens, offsets, {"q": (q, None)})
+    if offsets is None and T != B:
+        raise ValueError(f"inconsistent B: {T}, {B}")
+    if stream is not None or _current_device() != dev:
+        return _elsewhere(lambda: _paged(q, kpages, vpages, table, lens, offsets, max_new, causal,
+                                         kscale, vscale, scale, None),
+                          dev, stream, (q, kpages, vpages, table, lens, offsets, kscale, vscale))
+    device = q.device
+    o = torch.empty_strided((T, Hq, D), (Hq * D, D, 1), dtype=torch.bfloat16, device=device)
+    lse = torch.empty_strided((T, Hq), (Hq, 1), dtype=torch.float32, device=device)
+    lib = _lib or load()
+    cache = (kpages.data_ptr(), vpages.data_ptr(), None if kscale is None else kscale.data_ptr(),
+             None if vscale is None else vscale.data_ptr(), table.data_ptr(), lens.data_ptr())
+    if scale is None:
+        scale = D ** -0.5
+    if offsets is None:
+        rc = lib.attn_paged_decode(q.data_ptr(), stride, *cache, o.data_ptr(), lse.data_ptr(), B, Hq,
+                                   Hkv, D, page, P, M, scale, _raw_stream(dev))
+    else:
+        if max_new is None:
+            max_new = T
+        elif max_new >> 31:
+            _check(-3)  # ATTN_ERR_SHAPE: ctypes would pass it modulo 2^32
+        rc = lib.attn_paged_fwd(q.data_ptr(), stride, *cache, offsets.data_ptr(), o.data_ptr(),
+                                lse.data_ptr(), B, T, max_new, Hq, Hkv, D, page, P, M, bool(causal),
+                                scale, _raw_stream(dev))
+    if rc:
+        _check(rc)
+    return o, lse
+
+
+def paged_forward(q, kpages, vpages, table, lens, offsets, *, max_new: int | None = None,
+                  causal: bool = True, kscale=None, vscale=None, scale: float | None = None,
+                  stream=None):
+    """O [T,Hq,D], LSE [T,Hq] = attention of the new tokens q [T,Hq,D] (rows
+    ``offsets[b]`` .. ``offsets[b+1]`` of request b, the last of its ``lens[b]`` tokens) over
+    the pages of their requests, which hold the new tokens' K and V already
+    (``cache_write``).  A token sees those up to itself, without ``causal`` all of its
+    request's.  ``max_new``: the most new tokens that a request has (None: T); giving
+    it lets short chunks take the quicker way.  Rows that see nothing give 0 and
+    -inf; rows that belong to no request are not written."""
+    if offsets is None:
+        raise TypeError("offsets must be a torch tensor")
+    return _paged(q, kpages, vpages, table, lens, offsets, max_new, causal, kscale, vscale, scale,
+                  stream)
+
+
+def paged_decode(q, kpages, vpages, table, lens, *, kscale=None, vscale=None,
+                 scale: float | None = None, stream=None):
+    """``paged_forward`` of one token per request: O, LSE [B,Hq] of q [B,Hq,D] over the
+    first ``lens[b]`` tokens of request b."""
+    return _paged(q, kpages, vpages, table, lens, None, None, False, kscale, vscale, scale, stream)

@@ -157,6 +157,26 @@ int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, in
   return encode_4d(map, base, D, G, Hkv, B, requests);
 }
 
+// 3-D view [P * Hkv, page, D] of a cache's pages, box {128 bytes of a row, rows, 1}.
+int encode_pages(CUtensorMap* map, const void* base, const PagedArrays& c, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn;
+  if (int rc = encode_fn(&fn)) return rc;
+  const int elem = c.quant ? 1 : 2, row = c.D * elem;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.page),
+                              static_cast<cuuint64_t>(c.P) * c.Hkv};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row),
+                                 static_cast<cuuint64_t>(c.page) * row};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(row < 128 ? c.D : 128 / elem),
+                             static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, c.quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_TMA;
+}
+
 int check_device() {
   DeviceState* st = nullptr;
   return device_state(&st);

@@ -16,6 +16,7 @@ enum : unsigned int {
   kErrWaitCorr = 1u << 3,     // correction / epilogue gave up waiting
   kErrSelfTest = 1u << 4,     // the wait self-test ran out, as intended
   kErrLens = 1u << 5,         // a decode's lengths changed while it was planned
+  kErrPage = 1u << 6,         // a page number out of range
 };
 
 // Forward (prefill) launch parameters.  Tensor maps are 3-D views with a
@@ -225,6 +226,52 @@ int with_own_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, voi
 // Return an ATTN_* status.
 int mod_fwd(const ModFwdParams& p, cudaStream_t stream);
 int mod_decode(const ModDecodeParams& p, cudaStream_t stream);
+
+// A paged cache (see paged.cuh).
+struct PagedArrays {
+  void* kpages;        // [P, Hkv, page, D] bf16, or e4m3 codes (quant)
+  void* vpages;
+  uint8_t* kscale;     // [P, Hkv, page] scale bytes (quant), else NULL
+  uint8_t* vscale;
+  const int* table;    // [B, M] page numbers
+  const int* lens;     // [B] tokens in the cache, the new ones among them
+  const int* offsets;  // [B + 1] rows of the new tokens; NULL: row b is request b's one
+  int B, T, Hkv, D, page, P, M;  // T: rows of the dense tensors
+  int quant;
+};
+// Dense rows that go into the cache (k, v) or come out of it (k_out, v_out, [T, Hkv, D]).
+struct CacheRows {
+  const void* k;
+  const void* v;
+  void* k_out;
+  void* v_out;
+  long long k_stride, v_stride;  // elements from one token to the next
+  unsigned int* err;
+};
+cudaError_t launch_cache_rows(const PagedArrays& c, const CacheRows& r, bool read,
+                              cudaStream_t stream);
+
+// Attention of new tokens over a paged cache.
+struct PagedParams {
+  CUtensorMap tmap_k, tmap_v;  // pages as [P * Hkv, page, D], box {128 bytes, rows, 1}
+  PagedArrays c;
+  const void* q;       // [T, Hq, D] bf16, q_stride elements from one token to the next
+  long long q_stride;
+  void* o;             // [T, Hq, D] bf16
+  float* lse;          // [T, Hq]
+  int Hq, G, causal;
+  float scale_log2;
+  unsigned ctas;       // of the split kernel
+  float* part_o;       // partial states: [slot, rows of a block, D], and their
+  float2* part_ml;     // maximum (log2 units) and sum
+  unsigned int* err;
+  uint64_t wait_limit_ns;
+};
+// The kernel for few rows, and what its scratch takes.
+size_t paged_stream_scratch(const PagedParams& p, int rows, size_t* ml_at);
+cudaError_t launch_paged_stream(const PagedParams& p, int rows, int dev, cudaStream_t stream);
+// Tensor map over pages; box: rows of a page per copy.
+int encode_pages(CUtensorMap* map, const void* base, const PagedArrays& c, int box);
 
 // ATTN_OK when the current device is an sm_103, else the status to return; and
 // what a launch needs to know of it, asked for once.

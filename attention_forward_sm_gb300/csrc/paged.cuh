@@ -1,0 +1,102 @@
+// What the kernels over a paged cache share: its layout on the device, and where
+// a request's new tokens and pages are.
+//
+// K and V stand in pages [P, Hkv, page, D], table[b][i] naming the i-th page of
+// request b.  The part of a page that belongs to one KV head is one block of
+// `page` rows: a box of a tensor map, and one copy.  lens[b] counts the tokens
+// of request b in the cache, the new ones among them; the new ones are the rows
+// offsets[b] .. offsets[b + 1] of the dense tensors.
+//
+// Everything on the device is taken as it comes: lengths and offsets are clamped
+// and a page number out of range stands for a page of zeros that takes no
+// writes (kErrPage), so that no contents of these arrays lead out of bounds.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+__device__ __forceinline__ int clamp_len(const PagedArrays& c, int b) {
+  return min(max(c.lens[b], 0), c.M * c.page);
+}
+
+// The rows [first, first + n) of the dense tensors that request b's new tokens are.
+struct Rows {
+  int first, n;
+};
+__device__ __forceinline__ Rows request_rows(const PagedArrays& c, int b) {
+  if (!c.offsets) return {b, 1};
+  const int lo = min(max(c.offsets[b], 0), c.T);
+  const int hi = min(max(c.offsets[b + 1], lo), c.T);
+  return {lo, hi - lo};
+}
+
+// Request that row t belongs to, -1 if none: one past the offsets that are <= t,
+// found by a whole warp, which looks at 32 of them at a time.
+__device__ __forceinline__ int find_request(const PagedArrays& c, int t, int lane) {
+  if (!c.offsets) return t < c.B ? t : -1;
+  int lo = 0, hi = c.B;
+  const int begin = c.offsets[0];
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + (lane + 1) * step - 1;
+    const bool behind = i < hi && c.offsets[i + 1] <= t;
+    const int k = __popc(__ballot_sync(0xFFFFFFFFu, behind));
+    hi = min(hi, lo + (k + 1) * step - 1);
+    lo = min(lo + k * step, hi);
+  }
+  return lo < c.B && t >= begin ? lo : -1;
+}
+
+// Page that holds position pos of request b, or -1.
+__device__ __forceinline__ int page_of(const PagedArrays& c, int b, int pos) {
+  const int id = c.table[static_cast<size_t>(b) * c.M + pos / c.page];
+  return static_cast<unsigned>(id) < static_cast<unsigned>(c.P) ? id : -1;
+}
+
+// Contiguous global -> shared copy, completion counted in bytes on `bar`.
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// ---------------------------------------------------------------- e4m3 codes to bf16
+// A code s eeee mmm moved to bits 15 and 10 .. 4 of a bf16 is its value times 2^-120
+// (the exponents' biases are 7 and 127), subnormal codes included; a product with
+// 2^(120 + e) is code * 2^e, exact.  Scale bytes (e + 127) above 134 would take the
+// factor out of bf16: what is above goes into e4m3_rest.
+constexpr uint32_t kScaleNan = 255, kScaleMost = 134;
+
+// The codes in bytes 1 and 3 of u (the others do not matter), times the factors f.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t u, uint32_t f) {
+  const uint32_t x = (u >> 4 & 0x07F007F0u) | (u & 0x80008000u);
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
+  return y;
+}
+__device__ __forceinline__ uint32_t e4m3_factor16(uint32_t scale) {
+  return scale == kScaleNan ? 0x7FFFu : (min(scale, kScaleMost) + 120u) << 7;
+}
+// One scale for both values of a pair; one for each.
+__device__ __forceinline__ uint32_t e4m3_factor(uint32_t scale) {
+  return e4m3_factor16(scale) * 0x10001u;
+}
+__device__ __forceinline__ uint32_t e4m3_factors(uint32_t lo, uint32_t hi) {
+  return e4m3_factor16(lo) | e4m3_factor16(hi) << 16;
+}
+__device__ __forceinline__ float e4m3_rest(uint32_t scale) {
+  return __uint_as_float((max(scale, kScaleMost) - kScaleMost + 127u) << 23);
+}
+
+}  // namespace
+}  // namespace attn

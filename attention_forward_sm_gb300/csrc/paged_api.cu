@@ -1,0 +1,171 @@
+// C entries of the calls over a paged cache (attn_cache_write, attn_cache_read,
+// attn_paged_fwd, attn_paged_decode): argument checks and launches.  The contracts
+// are in include/attn.h.
+#include <math.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "../../include/attn.h"
+#include "internal.h"
+
+namespace attn {
+namespace {
+
+bool misaligned(const void* p, unsigned to) {
+  return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) != 0;
+}
+
+// Checks the arguments that describe a cache and its requests and fills *c.
+int paged_arrays(const void* kpages, const void* vpages, const unsigned char* kscale,
+                 const unsigned char* vscale, const int* table, const int* lens,
+                 const int* offsets, int B, int T, int Hkv, int D, int page, int P, int M,
+                 PagedArrays* c) {
+  if (!kpages || !vpages || !table || !lens || !kscale != !vscale) return ATTN_ERR_NULL;
+  if (B < 1 || B > 65536 || T < 0 || T > (1 << 24) || Hkv < 1 || Hkv > 65535 || P < 1 || M < 1)
+    return ATTN_ERR_SHAPE;
+  if (D != 64 && D != 128) return ATTN_ERR_SHAPE;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return ATTN_ERR_SHAPE;
+  if (static_cast<long long>(P) * Hkv >= (1ll << 31) ||
+      static_cast<long long>(M) * page > (1 << 21))
+    return ATTN_ERR_SHAPE;
+  for (const void* x : {kpages, vpages, static_cast<const void*>(kscale),
+                        static_cast<const void*>(vscale)})
+    if (misaligned(x, 16)) return ATTN_ERR_ALIGN;
+  for (const int* x : {table, lens, offsets})
+    if (misaligned(x, 4)) return ATTN_ERR_ALIGN;
+  *c = PagedArrays{const_cast<void*>(kpages), const_cast<void*>(vpages),
+                   const_cast<uint8_t*>(kscale), const_cast<uint8_t*>(vscale), table, lens, offsets,
+                   B, T, Hkv, D, page, P, M, kscale != nullptr};
+  return ATTN_OK;
+}
+
+// A dense tensor's elements from one token to the next.
+int check_stride(long long stride, int heads, int D) {
+  return stride < static_cast<long long>(heads) * D || stride % 8 != 0 || stride > (1ll << 40)
+             ? ATTN_ERR_SHAPE
+             : ATTN_OK;
+}
+
+struct PagedLaunch {
+  PagedParams* p;
+  int rows, dev;
+  size_t ml_at;
+};
+int launch_paged(void* ctx, void* scratch, cudaStream_t stream) {
+  const PagedLaunch& l = *static_cast<PagedLaunch*>(ctx);
+  l.p->part_o = static_cast<float*>(scratch);
+  l.p->part_ml = reinterpret_cast<float2*>(static_cast<char*>(scratch) + l.ml_at);
+  return launch_paged_stream(*l.p, l.rows, l.dev, stream) == cudaSuccess ? ATTN_OK
+                                                                        : ATTN_ERR_LAUNCH;
+}
+
+int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, float* lse, int Hq,
+           int max_new, int causal, float scale, cudaStream_t stream) {
+  if (!isfinite(scale) || scale < 0.f) return ATTN_ERR_SHAPE;
+  if (Hq < 1 || Hq > 65535 || Hq % c.Hkv != 0 || Hq / c.Hkv > 128 || max_new < 0)
+    return ATTN_ERR_SHAPE;
+  if (int rc = check_stride(q_stride, Hq, c.D)) return rc;
+  if (c.T == 0 || max_new == 0) return ATTN_OK;
+  if (!q || !o || !lse) return ATTN_ERR_NULL;
+  for (const void* x : {q, static_cast<const void*>(o), static_cast<const void*>(lse)})
+    if (misaligned(x, 16)) return ATTN_ERR_ALIGN;
+  PagedParams p = {};
+  p.c = c;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.o = o;
+  p.lse = lse;
+  p.Hq = Hq;
+  p.G = Hq / c.Hkv;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  PagedLaunch l = {};
+  l.rows = std::min<long long>(max_new, c.T) * p.G <= 8 ? 8 : 16;
+  // units of work are numbered in 32 bits
+  const long long blocks = static_cast<long long>(c.T) * p.G / l.rows + c.B;
+  if (blocks * c.Hkv * (static_cast<long long>(c.M) * c.page / 64 + 1) >= (1ll << 31))
+    return ATTN_ERR_SHAPE;
+  DeviceInfo di;
+  if (int rc = device_info(&di)) return rc;
+  const int box = std::min(c.page, 64);
+  if (int rc = encode_pages(&p.tmap_k, c.kpages, c, box)) return rc;
+  if (int rc = encode_pages(&p.tmap_v, c.vpages, c, box)) return rc;
+  p.ctas = static_cast<unsigned>(di.sms);
+  p.err = di.err_word;
+  p.wait_limit_ns = wait_limit_ns();
+  l.p = &p;
+  l.dev = di.dev;
+  return with_scratch(paged_stream_scratch(p, l.rows, &l.ml_at), di.dev, stream, launch_paged, &l);
+}
+
+int cache_rows(const PagedArrays& c, CacheRows r, bool read, cudaStream_t stream) {
+  if (int rc = check_stride(r.k_stride, c.Hkv, c.D)) return rc;
+  if (int rc = check_stride(r.v_stride, c.Hkv, c.D)) return rc;
+  if (c.T == 0) return ATTN_OK;
+  const void* k = read ? r.k_out : r.k;
+  const void* v = read ? r.v_out : r.v;
+  if (!k || !v) return ATTN_ERR_NULL;
+  if (misaligned(k, 16) || misaligned(v, 16)) return ATTN_ERR_ALIGN;
+  DeviceInfo di;
+  if (int rc = device_info(&di)) return rc;
+  r.err = di.err_word;
+  return launch_cache_rows(c, r, read, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+int attn_cache_write(const void* k, const void* v, long long k_stride, long long v_stride,
+                     void* kpages, void* vpages, unsigned char* kscale, unsigned char* vscale,
+                     const int* table, const int* lens, const int* offsets, int B, int T, int Hkv,
+                     int D, int page, int P, int M, cudaStream_t stream) {
+  PagedArrays c;
+  if (int rc = paged_arrays(kpages, vpages, kscale, vscale, table, lens, offsets, B, T, Hkv, D,
+                            page, P, M, &c))
+    return rc;
+  return cache_rows(c, CacheRows{k, v, nullptr, nullptr, k_stride, v_stride, nullptr}, false,
+                    stream);
+}
+
+int attn_cache_read(const void* kpages, const void* vpages, const unsigned char* kscale,
+                    const unsigned char* vscale, const int* table, const int* lens,
+                    const int* offsets, void* k, void* v, int B, int T, int Hkv, int D, int page,
+                    int P, int M, cudaStream_t stream) {
+  PagedArrays c;
+  if (int rc = paged_arrays(kpages, vpages, kscale, vscale, table, lens, offsets, B, T, Hkv, D,
+                            page, P, M, &c))
+    return rc;
+  const long long stride = static_cast<long long>(Hkv) * D;
+  return cache_rows(c, CacheRows{nullptr, nullptr, k, v, stride, stride, nullptr}, true, stream);
+}
+
+int attn_paged_fwd(const void* q, long long q_stride, const void* kpages, const void* vpages,
+                   const unsigned char* kscale, const unsigned char* vscale, const int* table,
+                   const int* lens, const int* offsets, void* o, float* lse, int B, int T,
+                   int max_new, int Hq, int Hkv, int D, int page, int P, int M, int causal,
+                   float scale, cudaStream_t stream) {
+  if (!offsets) return ATTN_ERR_NULL;
+  PagedArrays c;
+  if (int rc = paged_arrays(kpages, vpages, kscale, vscale, table, lens, offsets, B, T, Hkv, D,
+                            page, P, M, &c))
+    return rc;
+  return attend(c, q, q_stride, o, lse, Hq, max_new, causal, scale, stream);
+}
+
+int attn_paged_decode(const void* q, long long q_stride, const void* kpages, const void* vpages,
+                      const unsigned char* kscale, const unsigned char* vscale, const int* table,
+                      const int* lens, void* o, float* lse, int B, int Hq, int Hkv, int D,
+                      int page, int P, int M, float scale, cudaStream_t stream) {
+  PagedArrays c;
+  if (int rc = paged_arrays(kpages, vpages, kscale, vscale, table, lens, nullptr, B, B, Hkv, D,
+                            page, P, M, &c))
+    return rc;
+  return attend(c, q, q_stride, o, lse, Hq, 1, 0, scale, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,179 @@
+// How the split attention kernels over a paged cache share out their work, and the
+// partial states they leave.
+#pragma once
+
+#include <math_constants.h>
+
+#include "paged.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kUnitKeys = 64;  // keys of a unit of work of the kernel for few rows
+
+// `total` units dealt out in runs, as equal as they can be.
+struct Deal {
+  uint32_t runs, each, more;  // the first `more` runs have each + 1
+  __device__ Deal(uint32_t total, uint32_t ctas)
+      : runs(min(total, ctas)), each(runs ? total / runs : 0), more(runs ? total % runs : 0) {}
+  __device__ uint32_t start(uint32_t r) const { return r * each + min(r, more); }
+  __device__ uint32_t run_of(uint32_t x) const {
+    const uint32_t cut = more * (each + 1);
+    return x < cut ? x / (each + 1) : min(more + (x - cut) / each, runs - 1);
+  }
+};
+
+struct PlanShared {
+  uint32_t warp_sum[16];
+  uint32_t total;
+  int b;
+  uint32_t in_request;
+};
+struct PlanPlace {
+  uint32_t first, end;  // units of this CTA
+  int b;                // request that holds the first one,
+  uint32_t in_request;  // and which of its units that is
+};
+
+// Units of a request: for each KV head and block of rows, its key tiles (one where
+// there is no key, so that the rows' results are written).
+struct StreamPlan {
+  const PagedArrays& c;
+  int G, block_rows;
+  __device__ StreamPlan(const PagedArrays& c, int G, int block_rows)
+      : c(c), G(G), block_rows(block_rows) {}
+  __device__ uint32_t tiles(int len) const {
+    return static_cast<uint32_t>(max(1, (len + kUnitKeys - 1) / kUnitKeys));
+  }
+  __device__ int blocks(int n) const {
+    return static_cast<int>((static_cast<long long>(n) * G + block_rows - 1) / block_rows);
+  }
+  __device__ uint32_t units(int n, int len) const {
+    return static_cast<uint32_t>(c.Hkv) * static_cast<uint32_t>(blocks(n)) * tiles(len);
+  }
+  __device__ uint32_t units_of(int b) const {
+    const Rows rows = request_rows(c, b);
+    return rows.n > 0 ? units(rows.n, clamp_len(c, b)) : 0;
+  }
+  // The units of the requests [lo, hi) that a thread adds up, and those in front of
+  // them; sh.total gets the sum of all.  All kThreads threads call this.
+  template <int kThreads>
+  __device__ uint32_t scan(PlanShared& sh, int* lo, int* hi, uint32_t* own) const {
+    const int per = (c.B + kThreads - 1) / kThreads;
+    *lo = min(static_cast<int>(threadIdx.x) * per, c.B);
+    *hi = min(*lo + per, c.B);
+    uint32_t sum = 0;
+    for (int b = *lo; b < *hi; ++b) sum += units_of(b);
+    *own = sum;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += up;
+    }
+    if (lane == 31) sh.warp_sum[warp] = sum;
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sh.warp_sum[w];
+      total += sh.warp_sum[w];
+    }
+    if (threadIdx.x == 0) sh.total = total;
+    return before + sum - *own;
+  }
+  // Where CTA `cta` of `ctas` begins and ends.
+  template <int kThreads>
+  __device__ PlanPlace place(PlanShared& sh, uint32_t cta, uint32_t ctas) const {
+    if (threadIdx.x == 0) sh.b = c.B;
+    int lo, hi;
+    uint32_t own;
+    uint32_t before = scan<kThreads>(sh, &lo, &hi, &own);
+    __syncthreads();
+    const Deal deal(sh.total, ctas);
+    PlanPlace at = {0, 0, c.B, 0};
+    if (cta < deal.runs) {
+      at.first = deal.start(cta);
+      at.end = deal.start(cta + 1);
+      if (at.first >= before && at.first - before < own) {
+        int b = lo;
+        uint32_t rest = at.first - before;
+        for (; b < hi; ++b) {
+          const uint32_t u = units_of(b);
+          if (rest < u) break;
+          rest -= u;
+        }
+        sh.b = b;
+        sh.in_request = rest;
+      }
+    }
+    __syncthreads();
+    at.b = sh.b;
+    at.in_request = sh.in_request;
+    return at;
+  }
+  // Units in front of request b, of the calling warp's choice (< 0: none).  Every warp
+  // of the block calls this; sh.total is the sum of all afterwards.
+  template <int kThreads>
+  __device__ uint32_t before(PlanShared& sh, uint32_t (&starts)[kThreads], int b) const {
+    int lo, hi;
+    uint32_t own;
+    starts[threadIdx.x] = scan<kThreads>(sh, &lo, &hi, &own);
+    __syncthreads();
+    if (b < 0) return 0;
+    const int per = (c.B + kThreads - 1) / kThreads;
+    uint32_t sum = starts[b / per];
+    for (int i = b / per * per; i < b; ++i) sum += units_of(i);
+    return sum;
+  }
+};
+
+// A state (maximum, sum, O) of one row that states are added to; a lane holds
+// D / 32 consecutive elements of O.  The maximum of a state that saw nothing is
+// -inf, its sum and O 0; a NaN among the scores leaves them NaN.
+template <int D>
+struct State {
+  static constexpr int E = D / 32;
+  float l = 0.f, o[E];
+  __device__ State() {
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+  }
+  // ml: its maximum and sum; top: the largest maximum of all
+  __device__ void add(float2 ml, float top, const float* from, int lane) {
+    const float w = ml.x == -CUDART_INF_F ? 1.f : ex2_approx(ml.x - top);
+    l = fmaf(w, ml.y, l);
+    if constexpr (E == 4) {
+      const float4 x = reinterpret_cast<const float4*>(from)[lane];
+      o[0] = fmaf(w, x.x, o[0]);
+      o[1] = fmaf(w, x.y, o[1]);
+      o[2] = fmaf(w, x.z, o[2]);
+      o[3] = fmaf(w, x.w, o[3]);
+    } else {
+      const float2 x = reinterpret_cast<const float2*>(from)[lane];
+      o[0] = fmaf(w, x.x, o[0]);
+      o[1] = fmaf(w, x.y, o[1]);
+    }
+  }
+  __device__ void store(float* to, int lane) const {
+    if constexpr (E == 4)
+      reinterpret_cast<float4*>(to)[lane] = make_float4(o[0], o[1], o[2], o[3]);
+    else
+      reinterpret_cast<float2*>(to)[lane] = make_float2(o[0], o[1]);
+  }
+  // O and LSE of row t, query head hq
+  __device__ void finish(const PagedParams& p, int t, int hq, float top, int lane) const {
+    const size_t row = static_cast<size_t>(t) * p.Hq + hq;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t* dst = static_cast<uint32_t*>(p.o) + row * (D / 2) + lane * (E / 2);
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    else
+      *dst = pack_bf16x2(o[0] * inv, o[1] * inv);
+    if (lane == 0)
+      p.lse[row] = l == 0.f ? -CUDART_INF_F : (top + log2f(l)) * 0.69314718055994530942f;
+  }
+};
+
+}  // namespace
+}  // namespace attn

@@ -14,6 +14,11 @@
  * masks (documents, prefixes, a length per request, a shared prefix):
  * attn_fwd_mod, attn_row_ranges, attn_decode_varlen, attn_decode_prefix.
  *
+ * A server's cache, in pages that its requests take as they grow: attn_cache_write
+ * and attn_cache_read put tokens in and get them out, in bf16 or quantised to
+ * e4m3, attn_paged_fwd attends with several new tokens of each request,
+ * attn_paged_decode with one.
+ *
  * Sources for the operations:
  *   - "FlashAttention-3 vs Triton Kernels" (dailyaiworld), introduction:
  *     FlashAttention's IO-aware tiling computes the softmax attention output
@@ -76,6 +81,7 @@ enum attn_status {
 #define ATTN_DEVERR_WAIT_CORR 0x8u    /* correction / epilogue gave up waiting */
 #define ATTN_DEVERR_SELFTEST 0x10u    /* attn_selftest_wait_timeout ran out, as intended */
 #define ATTN_DEVERR_LENS 0x20u        /* a decode's lengths changed while it ran */
+#define ATTN_DEVERR_PAGE 0x40u        /* a page number out of range in a paged cache's table */
 
 /*
  * attn_fwd -- attention forward (prefill).
@@ -419,6 +425,101 @@ int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix,
                        const void *kcache, const void *vcache, const int *lens, void *o,
                        float *lse, int B, int Hq, int Hkv, int Np, int Ncap, int D, float scale,
                        float softcap, const float *slopes, cudaStream_t stream);
+
+/*
+ * A paged cache.  Four calls share its layout:
+ *
+ *   kpages, vpages [P, Hkv, page, D]  contiguous, 16, 32, 64 or 128 tokens a page:
+ *                  bf16, or, where kscale and vscale are given, e4m3 codes
+ *   kscale, vscale [P, Hkv, page]     scale bytes of the codes, or both NULL
+ *   table   [B, M] int32: the pages of request b in order; what is behind its
+ *           last token's page is not read
+ *   lens    [B] int32: tokens of request b in its cache, the new ones among
+ *           them (clamped to [0, M * page])
+ *   offsets [B + 1] int32, ascending: the new tokens of request b are the rows
+ *           offsets[b] .. offsets[b + 1] - 1 of the dense tensors, which have T
+ *           rows; rows in front of offsets[0] and from offsets[B] on belong to
+ *           nobody and are left alone.  NULL (where allowed): row b, of B
+ *
+ * Row i of n new tokens is at position lens[b] - n + i, which is slot
+ * position % page of page table[b][position / page].  lens, offsets and table
+ * stay on the device; they must not change while a call that reads them runs.
+ * A page number outside [0, P) stands for a page of zeros, into which nothing is
+ * written, and sets ATTN_DEVERR_PAGE.
+ *
+ * Quantised, the row of a token and KV head with largest magnitude a has the scale
+ * 2^e, e the least integer with a <= 448 * 2^e but at least -100 and at most 100
+ * (0 for a row of zeros), held as the byte e + 127, and the codes e4m3(x / 2^e),
+ * rounded to nearest even and saturating.  code * 2^e is exact in bf16.  A row that
+ * holds a NaN has the byte 255 and stands for NaN.  (Of codes that came about
+ * otherwise, 0x7F and 0xFF, e4m3's NaN, are read as +-480 by the attention calls.)
+ *
+ * Limits: 1 <= B <= 65536, 0 <= T <= 2^24, Hkv <= 65535, D in {64, 128},
+ * P * Hkv < 2^31, M * page <= 2^21; strides (elements from one token to the next)
+ * at least the row and multiples of 8 (ATTN_ERR_SHAPE); tensors 16-byte, int32
+ * arrays 4-byte aligned (ATTN_ERR_ALIGN).  T = 0 does nothing.
+ */
+
+/*
+ * attn_cache_write -- the new tokens' K and V into their pages.
+ *
+ *   k, v [T, Hkv, D] bf16, a token's heads contiguous, k_stride and v_stride elements
+ *   from one token to the next (slices of a joint projection, say).
+ *
+ * Tokens at negative positions (more new tokens than lens[b]) are dropped.  No two
+ * requests may write the same page at the same slot.  Slots of other tokens, also
+ * in the same pages, keep what they hold.
+ */
+int attn_cache_write(const void *k, const void *v, long long k_stride, long long v_stride,
+                     void *kpages, void *vpages, unsigned char *kscale, unsigned char *vscale,
+                     const int *table, const int *lens, const int *offsets, int B, int T, int Hkv,
+                     int D, int page, int P, int M, cudaStream_t stream);
+
+/*
+ * attn_cache_read -- the last tokens of each request as dense rows: row i of the n
+ * rows offsets[b] .. offsets[b + 1] - 1 of k and v [T, Hkv, D] bf16 (contiguous,
+ * written) gets the token at position lens[b] - n + i.  Rows at negative positions
+ * get zeros.
+ */
+int attn_cache_read(const void *kpages, const void *vpages, const unsigned char *kscale,
+                    const unsigned char *vscale, const int *table, const int *lens,
+                    const int *offsets, void *k, void *v, int B, int T, int Hkv, int D, int page,
+                    int P, int M, cudaStream_t stream);
+
+/*
+ * attn_paged_fwd -- attention of several new tokens of each request over its cache,
+ * which holds them already (attn_cache_write).
+ *
+ *   q   [T, Hq, D] bf16, q_stride elements from one token to the next
+ *   o   [T, Hq, D] bf16, lse [T, Hq] fp32, contiguous, written
+ *   max_new  at least the largest number of new tokens of a request (T is enough);
+ *            it decides how the work is laid out, not what is computed
+ *
+ * The row at position p sees with causal != 0 the keys 0 .. p of its request, else
+ * all lens[b] of them.  A row that sees none gives O = 0 and LSE = -infinity.
+ * Numerics as attn_fwd.  A key that a row does not see has no influence on it; V may
+ * hold anything behind lens[b], but a NaN or infinity in V at a position below
+ * lens[b] may reach all rows of the same (request, KV head).
+ *
+ * Limits: Hq % Hkv == 0, Hq <= 65535, Hq / Hkv <= 128, max_new >= 0; scale finite and
+ * >= 0; the rows times the keys in units of work within 32 bits:
+ * (T * Hq / Hkv / 8 + B) * Hkv * (M * page / 64 + 1) < 2^31.  Scratch as
+ * attn_decode_varlen.
+ */
+int attn_paged_fwd(const void *q, long long q_stride, const void *kpages, const void *vpages,
+                   const unsigned char *kscale, const unsigned char *vscale, const int *table,
+                   const int *lens, const int *offsets, void *o, float *lse, int B, int T,
+                   int max_new, int Hq, int Hkv, int D, int page, int P, int M, int causal,
+                   float scale, cudaStream_t stream);
+
+/*
+ * attn_paged_decode -- attn_paged_fwd of one new token per request: q [B, Hq, D],
+ * o [B, Hq, D], lse [B, Hq].
+ */
+int attn_paged_decode(const void *q, long long q_stride, const void *kpages, const void *vpages,
+                      const unsigned char *kscale, const unsigned char *vscale, const int *table,
+                      const int *lens, void *o, float *lse, int B, int Hq, int Hkv, int D,
+                      int page, int P, int M, float scale, cudaStream_t stream);
 
 /* Human-readable name of an ATTN_* status code (static string). */
 const char *attn_status_string(int status);
