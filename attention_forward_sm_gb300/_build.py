@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libattn.so")
 SOURCES = ["api.cu", "fwd_sm103a.cu", "decode_sm103a.cu", "decode_noalloc.cu", "decode_graph.cu",
            "decode_scratch.cu", "host_pipeline.cu", "row_ranges.cu", "mod_api.cu",
            "mod_launch.cu", "mod_fwd_d64.cu", "mod_fwd_d128.cu",
-           "paged_api.cu", "paged_cache.cu", "paged_stream.cu",
+           "paged_api.cu", "paged_cache.cu", "paged_stream.cu", "paged_tile.cu",
            *(f"mod_split_d{d}_h{h}.cu" for d in (64, 128) for h in (0, 4, 8))]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

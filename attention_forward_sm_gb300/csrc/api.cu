@@ -98,13 +98,16 @@ int encode_3d(CUtensorMap* map, const void* base, int D, int N, long long BH, in
 // 4-D view [B, Hkv, G, D] of a contiguous bf16 tensor, box {64, G, 1, requests},
 // 128-byte swizzle: the G query heads of a KV head, of `requests` requests, as
 // consecutive rows of a tile.
-int encode_4d(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B, int requests) {
+// (`stride` elements from one request to the next; 0: G * Hkv * D.)
+int encode_4d(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B, int requests,
+              long long stride) {
   PFN_cuTensorMapEncodeTiled_v12000 fn;
   if (int rc = encode_fn(&fn)) return rc;
   const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(G),
                         static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(B)};
-  cuuint64_t strides[3] = {row, row * G, row * G * Hkv};
+  cuuint64_t strides[3] = {row, row * G,
+                           stride ? static_cast<cuuint64_t>(stride) * 2 : row * G * Hkv};
   cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(requests)};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
@@ -152,9 +155,9 @@ int encode_rows(CUtensorMap* map, const void* base, int D, int N, long long BH, 
   return encode_3d(map, base, D, N, BH, rows, stride);
 }
 
-int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B,
-                   int requests) {
-  return encode_4d(map, base, D, G, Hkv, B, requests);
+int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B, int requests,
+                   long long stride) {
+  return encode_4d(map, base, D, G, Hkv, B, requests, stride);
 }
 
 // 3-D view [P * Hkv, page, D] of a cache's pages, box {128 bytes of a row, rows, 1}.

@@ -210,7 +210,8 @@ cudaError_t launch_mod_split_d128_h8(const ModKernelParams& p, unsigned grid, in
 // queries of a decode, box {64, G, 1, requests}.  Return an ATTN_* status.
 int encode_rows(CUtensorMap* map, const void* base, int D, int N, long long BH, int rows,
                 int stride = 0);  // rows from one [N, D] to the next; 0: N
-int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B, int requests);
+int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, int B, int requests,
+                   long long stride = 0);  // elements from one to the next; 0: G Hkv D
 
 // Device scratch of `bytes` for the kernels that launch(ctx, scratch, stream)
 // queues on `stream`: the stream's cached buffer or, during capture, one of the
@@ -254,6 +255,7 @@ cudaError_t launch_cache_rows(const PagedArrays& c, const CacheRows& r, bool rea
 // Attention of new tokens over a paged cache.
 struct PagedParams {
   CUtensorMap tmap_k, tmap_v;  // pages as [P * Hkv, page, D], box {128 bytes, rows, 1}
+  CUtensorMap tmap_q;          // [T, Hkv, G, D], box {64, G, 1, 128 / G} (many rows)
   PagedArrays c;
   const void* q;       // [T, Hq, D] bf16, q_stride elements from one token to the next
   long long q_stride;
@@ -270,6 +272,9 @@ struct PagedParams {
 // The kernel for few rows, and what its scratch takes.
 size_t paged_stream_scratch(const PagedParams& p, int rows, size_t* ml_at);
 cudaError_t launch_paged_stream(const PagedParams& p, int rows, int dev, cudaStream_t stream);
+// The kernel for many rows, likewise.
+size_t paged_tile_scratch(const PagedParams& p, size_t* ml_at);
+cudaError_t launch_paged_tile(const PagedParams& p, int dev, cudaStream_t stream);
 // Tensor map over pages; box: rows of a page per copy.
 int encode_pages(CUtensorMap* map, const void* base, const PagedArrays& c, int box);
 

@@ -49,15 +49,16 @@ int check_stride(long long stride, int heads, int D) {
 
 struct PagedLaunch {
   PagedParams* p;
-  int rows, dev;
+  int rows, dev;  // rows: of a block of the kernel for few rows; 0: the one for many
   size_t ml_at;
 };
 int launch_paged(void* ctx, void* scratch, cudaStream_t stream) {
   const PagedLaunch& l = *static_cast<PagedLaunch*>(ctx);
   l.p->part_o = static_cast<float*>(scratch);
   l.p->part_ml = reinterpret_cast<float2*>(static_cast<char*>(scratch) + l.ml_at);
-  return launch_paged_stream(*l.p, l.rows, l.dev, stream) == cudaSuccess ? ATTN_OK
-                                                                        : ATTN_ERR_LAUNCH;
+  const cudaError_t e = l.rows ? launch_paged_stream(*l.p, l.rows, l.dev, stream)
+                               : launch_paged_tile(*l.p, l.dev, stream);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, float* lse, int Hq,
@@ -79,24 +80,36 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
   p.Hq = Hq;
   p.G = Hq / c.Hkv;
   p.causal = causal ? 1 : 0;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  // (never 0: an unseen score is -inf and has to stay it; 1e-37 times any product
+  // below 1e30 is 0 next to a score's roundings)
+  p.scale_log2 = std::max(scale * 1.4426950408889634f, 1e-37f);
   PagedLaunch l = {};
-  l.rows = std::min<long long>(max_new, c.T) * p.G <= 8 ? 8 : 16;
-  // units of work are numbered in 32 bits
-  const long long blocks = static_cast<long long>(c.T) * p.G / l.rows + c.B;
+  l.p = &p;
+  // Few rows share each key (up to 16): the kernel that streams the cache.  An accumulator
+  // of the one for many rows takes kSegmentKeys keys at most.
+  const long long rows = std::min<long long>(max_new, c.T) * p.G;
+  const bool many = rows > 16 && static_cast<long long>(c.M) * c.page <= kSegmentKeys;
+  l.rows = many ? 0 : rows <= 8 ? 8 : 16;
+  // the streaming kernel numbers its units of work in 32 bits
+  const long long blocks = static_cast<long long>(c.T) * p.G / 8 + c.B;
   if (blocks * c.Hkv * (static_cast<long long>(c.M) * c.page / 64 + 1) >= (1ll << 31))
     return ATTN_ERR_SHAPE;
   DeviceInfo di;
   if (int rc = device_info(&di)) return rc;
-  const int box = std::min(c.page, 64);
-  if (int rc = encode_pages(&p.tmap_k, c.kpages, c, box)) return rc;
-  if (int rc = encode_pages(&p.tmap_v, c.vpages, c, box)) return rc;
-  p.ctas = static_cast<unsigned>(di.sms);
+  const int box = many ? c.page : std::min(c.page, 64);
+  if (!many || !c.quant) {
+    if (int rc = encode_pages(&p.tmap_k, c.kpages, c, box)) return rc;
+    if (int rc = encode_pages(&p.tmap_v, c.vpages, c, box)) return rc;
+  }
+  if (many)
+    if (int rc = encode_queries(&p.tmap_q, q, c.D, p.G, c.Hkv, c.T, 128 / p.G, q_stride)) return rc;
+  p.ctas = std::min(static_cast<unsigned>(di.sms), kMostCtas);
   p.err = di.err_word;
   p.wait_limit_ns = wait_limit_ns();
-  l.p = &p;
   l.dev = di.dev;
-  return with_scratch(paged_stream_scratch(p, l.rows, &l.ml_at), di.dev, stream, launch_paged, &l);
+  const size_t bytes = many ? paged_tile_scratch(p, &l.ml_at)
+                            : paged_stream_scratch(p, l.rows, &l.ml_at);
+  return with_scratch(bytes, di.dev, stream, launch_paged, &l);
 }
 
 int cache_rows(const PagedArrays& c, CacheRows r, bool read, cudaStream_t stream) {

@@ -127,6 +127,144 @@ struct StreamPlan {
   }
 };
 
+// ---------------------------------------------------------------- the kernel for many rows
+//
+// An item is 2 * (128 / G) tokens of one KV head; its cost is the keys that its last
+// token sees, and kItemCost for what every item takes besides (the products fill and drain,
+// the epilogue).  The costs of a request's items are in arithmetic progression, so
+// their sums have closed forms and nothing about them is stored.
+constexpr int kTileKeys = 128;
+constexpr int kItemCost = 256;
+
+struct CostShared {
+  long long warp_sum[24];
+  long long total, rest;
+  int b;
+};
+struct CostPlace {
+  long long total, first, end;  // of the whole line, of this CTA
+  long long rest;               // first's distance from the start of request b, which holds it
+  int b;
+};
+struct CostItem {
+  long long x0, cost;  // where it starts on the line, how long it is
+  int row0, left, before, len;
+  int h, j, n_kv;
+};
+
+struct CostPlan {
+  const PagedArrays& c;
+  int tokens, causal;  // of an item
+  __device__ CostPlan(const PagedArrays& c, int G, int causal)
+      : c(c), tokens(2 * (128 / G)), causal(causal) {}
+  __device__ int items(int n) const { return (n + tokens - 1) / tokens; }
+  // costs of the first j items of a KV head, j < items(n); of item j; of all
+  __device__ long long before(int n, int len, int j) const {
+    if (!causal) return static_cast<long long>(j) * (len + kItemCost);
+    return static_cast<long long>(j) * (max(len - n, 0) + kItemCost) +
+           static_cast<long long>(tokens) * (static_cast<long long>(j) * (j + 1) / 2);
+  }
+  __device__ long long cost(int n, int len, int j) const {
+    return kItemCost + (!causal || j == items(n) - 1
+                            ? len
+                            : max(len - n, 0) + static_cast<long long>(j + 1) * tokens);
+  }
+  __device__ long long head(int n, int len) const {
+    const int last = items(n) - 1;
+    return before(n, len, last) + cost(n, len, last);
+  }
+  __device__ long long request(int b) const {
+    const Rows rows = request_rows(c, b);
+    return rows.n > 0 ? c.Hkv * head(rows.n, clamp_len(c, b)) : 0;
+  }
+  __device__ long long start(long long total, unsigned cta, unsigned ctas) const {
+    return total / ctas * cta + total % ctas * cta / ctas;
+  }
+  // Where CTA `cta` of `ctas` begins and ends; all kThreads threads call this.
+  template <int kThreads>
+  __device__ CostPlace place(CostShared& sh, unsigned cta, unsigned ctas) const {
+    const int per = (c.B + kThreads - 1) / kThreads;
+    const int lo = min(static_cast<int>(threadIdx.x) * per, c.B), hi = min(lo + per, c.B);
+    long long own = 0;
+    for (int b = lo; b < hi; ++b) own += request(b);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long sum = own;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += up;
+    }
+    if (lane == 31) sh.warp_sum[warp] = sum;
+    if (threadIdx.x == 0) sh.b = c.B;
+    __syncthreads();
+    long long in_front = sum - own, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) in_front += sh.warp_sum[w];
+      total += sh.warp_sum[w];
+    }
+    CostPlace at;
+    at.total = total;
+    at.first = start(total, cta, ctas);
+    at.end = start(total, cta + 1, ctas);
+    if (at.first >= in_front && at.first - in_front < own) {
+      long long rest = at.first - in_front;
+      int b = lo;
+      for (; b < hi; ++b) {
+        const long long x = request(b);
+        if (rest < x) break;
+        rest -= x;
+      }
+      sh.b = b;
+      sh.rest = rest;
+    }
+    __syncthreads();
+    at.b = sh.b;
+    at.rest = sh.rest;
+    return at;
+  }
+  // Item (h, j) of request b, at x0 on the line.
+  __device__ CostItem make(int b, int h, int j, long long x0) const {
+    const Rows rows = request_rows(c, b);
+    const int len = clamp_len(c, b);
+    CostItem i;
+    i.x0 = x0;
+    i.cost = cost(rows.n, len, j);
+    i.row0 = rows.first + j * tokens;
+    i.left = rows.n - j * tokens;
+    i.before = len - rows.n + j * tokens;
+    i.len = len;
+    i.h = h;
+    i.j = j;
+    const int seen = causal ? min(len, i.before + min(i.left, tokens)) : len;
+    i.n_kv = max(1, (seen + kTileKeys - 1) / kTileKeys);
+    return i;
+  }
+  // The item that holds a CTA's first point.
+  __device__ CostItem item(const CostPlace& at) const {
+    const Rows rows = request_rows(c, at.b);
+    const int len = clamp_len(c, at.b);
+    const long long per_head = head(rows.n, len);
+    const int h = static_cast<int>(at.rest / per_head);
+    const long long rest = at.rest % per_head;
+    int lo = 0, hi = items(rows.n) - 1;  // the last j with before(j) <= rest
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (before(rows.n, len, mid) <= rest)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return make(at.b, h, lo, at.first - rest + before(rows.n, len, lo));
+  }
+  // The first key tile of what lies behind point y of an item.
+  __device__ int cut(const CostItem& i, long long y) const {
+    if (y <= 0) return 0;
+    if (y >= i.cost) return i.n_kv;
+    return static_cast<int>(min(max(y - kItemCost, 0ll) / kTileKeys,
+                                static_cast<long long>(i.n_kv)));
+  }
+};
+
 // A state (maximum, sum, O) of one row that states are added to; a lane holds
 // D / 32 consecutive elements of O.  The maximum of a state that saw nothing is
 // -inf, its sum and O 0; a NaN among the scores leaves them NaN.

@@ -1,0 +1,752 @@
+// Attention of many new tokens of each request over its paged cache: chunks of
+// prompts, alone or beside single tokens.
+//
+// The rows of a (request, KV head) are its new tokens times the G query heads that
+// share the head, token by token, so that K and V are read once for all of them; a
+// tile is the 128 / G tokens that fit 128 rows.  A CTA works on two tiles (an item:
+// 2 * (128 / G) tokens of one KV head) as in fwd_sm103a.cu, whose roles and barriers
+// these are: S_t = Q_t K^T and O_t in tensor memory, sixteen softmax warps that write
+// P_t over S_t, a warp that issues every tcgen05.mma, one that loads.
+//
+// Pages.  A key tile is 128 keys, one tensor copy per page (and 128 bytes of a row).
+// What lies behind the last token may hold anything, and an unseen key's weight of 0
+// times a NaN of V is none.  So the copy of the last page begins above the page, at a
+// negative row, which fills with zeros: the page's tokens come to stand at the end of
+// its rows (the mask knows), and pages behind it are copied from behind the last page
+// there is, as zeros.
+//
+// Quantised pages come in as they are, and four warps turn them into bf16 tiles next
+// to the softmax: 2 * 128 * D codes for each 128 keys, about 600 issue slots per
+// scheduler at D = 128, of the 2700 cycles that the products take.
+//
+// Work is dealt out by keys: every item has a cost, its keys and a constant, the items
+// of all requests make one line, and each CTA takes an equal stretch of it.  An item
+// that is cut has a partial state in each CTA, which tile_merge_kernel joins.
+// Bound by the tensor cores: 4 D flops per row and key.
+#include <math_constants.h>
+
+#include <atomic>
+
+#include "../../include/attn.h"
+#include "fwd_tile.cuh"
+#include "paged_plan.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpConvert = 20;
+
+template <int D, bool kQuant>
+struct TileCfg {
+  static constexpr int kThreads = kQuant ? 768 : 640;
+  // setmaxnreg: 4 softmax warpgroups and 1 or 2 others, out of what the launch gets
+  static constexpr uint32_t kRegSoftmax = kQuant ? 104 : 112, kRegOther = 32;
+  static constexpr int kReaders = kQuant ? 21 : 17;  // of an item, besides the loader
+  static constexpr int kTileBytes = kBM * D * 2, kChunks = D / 64;
+  static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
+  static constexpr int kRaw = 4;  // quantised tiles in the ring, and their size
+  static constexpr int kRawBytes = kBN * D;
+  static constexpr int kOffKV = 2 * kTileBytes;
+  static constexpr int kOffRaw = kOffKV + kStages * kTileBytes;
+  static constexpr int kOffScale = kOffRaw + (kQuant ? kRaw * kRawBytes : 0);
+  static constexpr int kSmem = kOffScale + (kQuant ? kRaw * kBN : 0) + 1024;
+  static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
+  static_assert(4 * 128 * kRegSoftmax + (kThreads - 512) * kRegOther <=
+                    kThreads * (65536 / kThreads / 8 * 8),
+                "register split");
+};
+
+struct Item {
+  int row0, left;    // first dense row; tokens of the request from there on
+  int before, len;   // keys in front of that token; tokens of the request
+  int h, tiles;      // KV head; query tiles with rows, 0: no item
+  int tile0, tile1;  // key tiles
+  int slot, b;       // partial state, -1: none; request
+};
+
+// The items of a CTA's stretch of the line, one after the other.
+struct CostWalk {
+  const CostPlan& plan;
+  const CostPlace& at;
+  CostItem item;
+  int b, blocks;
+  bool fresh = true;
+  __device__ CostWalk(const CostPlan& plan, const CostPlace& at) : plan(plan), at(at), b(at.b) {
+    if (b < plan.c.B && at.first < at.end) {
+      item = plan.item(at);
+      blocks = plan.items(request_rows(plan.c, b).n);
+    } else {
+      b = plan.c.B;
+    }
+  }
+  // The next part with key tiles; slot: of its partial state, 0 or 1, or -1.
+  __device__ bool next(Item* it, int* slot) {
+    while (b < plan.c.B) {
+      if (!fresh) {
+        const long long x0 = item.x0 + item.cost;
+        if (x0 >= at.end) break;
+        int h = item.h, j = item.j + 1;
+        if (j == blocks) {
+          j = 0;
+          ++h;
+        }
+        if (h == plan.c.Hkv) {
+          h = 0;
+          do ++b;
+          while (b < plan.c.B && request_rows(plan.c, b).n == 0);
+          if (b == plan.c.B) break;
+          blocks = plan.items(request_rows(plan.c, b).n);
+        }
+        item = plan.make(b, h, j, x0);
+      }
+      fresh = false;
+      const int t0 = plan.cut(item, at.first - item.x0), t1 = plan.cut(item, at.end - item.x0);
+      if (t0 >= t1) continue;
+      *it = Item{item.row0, item.left, item.before, item.len, item.h,
+                 item.left > plan.tokens / 2 ? 2 : 1, t0, t1, -1, b};
+      *slot = t0 == 0 && t1 == item.n_kv ? -1 : t0 == 0;
+      return true;
+    }
+    return false;
+  }
+};
+
+template <bool kQuant>
+struct TileShared {
+  uint64_t q_full, q_empty;          // per item
+  uint64_t s_full[2], p_full[2];     // per key tile of query tile t
+  uint64_t o_done[2];                // per item of query tile t
+  uint64_t mma_done;
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t raw_full[4], raw_empty[4];
+  uint64_t item_full[2], item_empty[2];
+  Item item[2];
+  uint32_t raw_bad[4];  // copies of the tile whose page is out of range, a bit each
+  CostShared plan;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int D, bool kQuant>
+__global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
+    paged_tile_kernel(const __grid_constant__ PagedParams p) {
+  using C = TileCfg<D, kQuant>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  __shared__ TileShared<kQuant> ms;
+  static_assert(C::kSmem + sizeof(ms) <= 227 * 1024, "shared memory");
+  const uint32_t abort_flag = smem_u32(&ms.abort_flag);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == kWarpLoad && lane == 0) {
+    mbar_init(&ms.q_full, 1);
+    mbar_init(&ms.q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&ms.s_full[t], 1);
+      mbar_init(&ms.p_full[t], 8);
+      mbar_init(&ms.o_done[t], 1);
+      mbar_init(&ms.item_full[t], 1);
+      mbar_init(&ms.item_empty[t], C::kReaders);
+    }
+    mbar_init(&ms.mma_done, 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&ms.kv_full[s], kQuant ? 4 : 1);
+      mbar_init(&ms.kv_empty[s], 1);
+    }
+    for (int s = 0; s < C::kRaw; ++s) {
+      mbar_init(&ms.raw_full[s], 1);
+      mbar_init(&ms.raw_empty[s], 4);
+    }
+    ms.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tmap_q);
+    if (!kQuant) {
+      tma_prefetch_desc(&p.tmap_k);
+      tma_prefetch_desc(&p.tmap_v);
+    }
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&ms.tmem_base, 512);
+    tmem_relinquish();
+  }
+  const CostPlan plan(p.c, p.G, p.causal);
+  const CostPlace at = plan.place<C::kThreads>(ms.plan, blockIdx.x, p.ctas);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = ms.tmem_base;
+
+  // waits for item k; false when there is none
+  auto next_item = [&](uint32_t k, Item* it, uint32_t site) -> bool {
+    if (!warp_all(mbar_wait(&ms.item_full[k & 1], (k >> 1) & 1, abort_flag, p.err, site,
+                            p.wait_limit_ns)))
+      return false;
+    *it = ms.item[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ms.item_empty[k & 1]);
+    return it->tiles > 0;
+  };
+
+  if (warp < 16) {
+    // ---- softmax and epilogue: warps 8t .. 8t + 7 serve query tile t, two warps a
+    // 32-lane quarter of tensor memory, two threads a row (64 keys of a tile each)
+    reg_alloc<C::kRegSoftmax>();
+    const int t = warp >> 3;
+    const int lbase = (warp & 3) * 32 + ((warp >> 2) & 1) * 16;
+    const int r = lbase + (lane & 15);  // row within the tile
+    const int c = lane >> 4;            // half of the row's keys
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(lbase) << 16);
+    const uint32_t s_addr = lane_addr + (t ? C::kColS1 : C::kColS0);
+    const uint32_t o_addr = lane_addr + (t ? C::kColO1 : C::kColO0);
+    const int per_tile = kBM / p.G;                // tokens of a tile
+    const int token = t * per_tile + r / p.G;      // of the item
+    const bool in_tile = r < per_tile * p.G;
+    uint32_t step = 0, done = 0;  // key tiles and items of query tile t so far
+    Item it;
+    for (uint32_t k = 0; next_item(k, &it, kErrWaitSoftmax); ++k) {
+      if (t >= it.tiles) continue;
+      const bool real = in_tile && token < it.left;
+      // keys that the row sees, and that every row of the tile does
+      const int vis = !real ? 0 : p.causal ? min(it.len, it.before + token + 1) : it.len;
+      const int all_see = p.causal ? min(it.len, it.before + t * per_tile + 1) : it.len;
+      // the last page's tokens stand `shift` rows further down from key `cut` on
+      const int cut = kQuant ? 0 : max(it.len - 1, 0) / p.c.page * p.c.page;
+      const int shift = kQuant ? 0 : cut + p.c.page - it.len;
+      float m = -CUDART_INF_F, l = 0.f;
+      bool ok = true;
+      for (int j = it.tile0; j < it.tile1; ++j, ++step) {
+        if (!warp_all(mbar_wait(&ms.s_full[t], step & 1, abort_flag, p.err, kErrWaitSoftmax,
+                                p.wait_limit_ns))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float s[64];
+        if constexpr (kQuant) {  // (the launch's 80 registers do not hold 64 at once)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t sr[32];
+            tmem_ld_pair32<64>(s_addr + 32 * h, sr);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[32 * h + i] = __uint_as_float(sr[i]);
+          }
+        } else {
+          uint32_t sr[64];
+          tmem_ld_pair64<64>(s_addr, sr);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
+        }
+        if ((j + 1) * kBN > all_see) {
+          // columns [0, end) and [from, to) of this thread's are visible
+          const int col0 = j * kBN + c * 64;
+          const bool moved = shift > 0 && (j + 1) * kBN > cut;
+          const int end = (moved ? min(cut, vis) : vis) - col0;
+          const int from = moved ? cut + shift - col0 : 64;
+          const int to = vis + shift - col0;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i >= end && (i < from || i >= to)) s[i] = -CUDART_INF_F;
+        }
+        float mx;
+        {
+          float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]);
+          float a2 = fmaxf(s[4], s[5]), a3 = fmaxf(s[6], s[7]);
+#pragma unroll
+          for (int i = 8; i < 64; i += 8) {
+            a0 = max3f(a0, s[i], s[i + 1]);
+            a1 = max3f(a1, s[i + 2], s[i + 3]);
+            a2 = max3f(a2, s[i + 4], s[i + 5]);
+            a3 = max3f(a3, s[i + 6], s[i + 7]);
+          }
+          mx = max3f(a0, a1, fmaxf(a2, a3));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+        }
+        const float m_tile = mx * p.scale_log2;  // (scale_log2 > 0)
+        float alpha = 1.f;
+        if (m_tile > m + 8.f) {  // a stale maximum is as good up to there
+          alpha = ex2_approx(m - m_tile);  // 0 the first time
+          m = m_tile;
+        }
+        // p = 2^(s * scale - m); a row that has seen nothing keeps m = -inf: its
+        // scores are -inf and stay it next to a reference of 0
+        const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+        const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
+        const uint64_t negm2 = f32x2(neg_m, neg_m);
+        uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          float x0, x1, x2, x3;
+          unpack_f32x2(fma_f32x2(f32x2(s[i], s[i + 1]), scale2, negm2), x0, x1);
+          unpack_f32x2(fma_f32x2(f32x2(s[i + 2], s[i + 3]), scale2, negm2), x2, x3);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
+          acc0 = add_f32x2(acc0, f32x2(p0, p1));
+          acc1 = add_f32x2(acc1, f32x2(p2, p3));
+          pk[i / 2] = pack_bf16x2(p0, p1);
+          pk[i / 2 + 1] = pack_bf16x2(p2, p3);
+        }
+        float u0, u1;
+        unpack_f32x2(add_f32x2(acc0, acc1), u0, u1);
+        l = fmaf(l, alpha, u0 + u1);
+        // Rescale O_t where a maximum moved: every product of earlier key tiles has
+        // retired (issued before the S_t that woke this warp), that of this one waits.
+        if (j > it.tile0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int kk = 0; kk < D / 32; ++kk) {
+            uint32_t v[16];
+            tmem_ld_pair16<D / 2>(o_addr + kk * 16, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+            tmem_st_pair16<D / 2>(o_addr + kk * 16, v);
+          }
+          tmem_st_wait();
+        }
+        tmem_st_pair32<32>(s_addr, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.p_full[t]);
+      }
+      // ---- epilogue: O / l and LSE, or the partial state
+      ok = ok && warp_all(mbar_wait(&ms.o_done[t], done & 1, abort_flag, p.err, kErrWaitCorr,
+                                    p.wait_limit_ns));
+      if (!ok) break;
+      ++done;
+      tc_fence_after();
+      const float l_row = l + __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+      const bool whole = it.slot < 0;
+      const float inv = !whole ? 1.f : l_row == 0.f ? 0.f : 1.f / l_row;
+      const size_t out_row = static_cast<size_t>(it.row0 + token) * p.Hq + it.h * p.G + r % p.G;
+      const size_t part_row = static_cast<size_t>(max(it.slot, 0)) * (2 * kBM) + t * kBM + r;
+#pragma unroll
+      for (int kk = 0; kk < D / 64; ++kk) {
+        uint32_t v[32];
+        tmem_ld_pair32<D / 2>(o_addr + kk * 32, v);
+        const int col = c * (D / 2) + kk * 32;
+        if (!real) continue;
+        if (whole) {
+          uint4* dst =
+              reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out_row * D + col);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(v[8 * g + 2 * i]) * inv,
+                                 __uint_as_float(v[8 * g + 2 * i + 1]) * inv);
+            st_global_v4_evict_first(dst + g, w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + part_row * D + col);
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            dst[g] = make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
+                                 __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
+        }
+      }
+      if (c == 0 && real) {
+        if (whole)
+          p.lse[out_row] =
+              l_row == 0.f ? -CUDART_INF_F : (m + log2f(l_row)) * 0.69314718055994530942f;
+        else
+          p.part_ml[part_row] = make_float2(m, l_row);
+      }
+    }
+  } else if (warp == kWarpLoad) {
+    // ---- the plan's items, their Q tiles, and K_j, V_j through the ring
+    reg_dealloc<C::kRegOther>();
+    uint32_t k = 0;           // items
+    uint32_t slot = 0, round = 0;  // next place in the ring
+    constexpr uint32_t kRing = kQuant ? C::kRaw : C::kStages;
+    uint64_t* const full = kQuant ? ms.raw_full : ms.kv_full;
+    uint64_t* const empty = kQuant ? ms.raw_empty : ms.kv_empty;
+    const int page = p.c.page;
+    const int boxes = kBN / page;
+    const int per_tile = kBM / p.G;
+    const uint64_t policy = l2_policy_evict_last();
+    bool ok = true;
+    CostWalk walk(plan, at);
+    Item it;
+    int slot_first = 0;
+    while (ok && walk.next(&it, &slot_first)) {
+      if (!warp_all(mbar_wait(&ms.item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort_flag, p.err,
+                              kErrWaitLoad, p.wait_limit_ns))) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        it.slot = slot_first < 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + slot_first;
+        ms.item[k & 1] = it;
+        mbar_arrive(&ms.item_full[k & 1]);
+      }
+      int pbase = -256, ids = 0;
+      const uint32_t n = 2u * static_cast<uint32_t>(it.tile1 - it.tile0);
+      for (uint32_t i = 0; i < n && ok; ++i) {
+        const int key0 = (it.tile0 + static_cast<int>(i >> 1)) * kBN;
+        // copy `box` of the tile: page and rows (lane l holds entry pbase + l of the table)
+        if (key0 / page < pbase || key0 / page + boxes > pbase + 32) {
+          pbase = key0 / page;
+          ids = pbase + lane < p.c.M
+                    ? p.c.table[static_cast<size_t>(it.b) * p.c.M + pbase + lane]
+                    : -1;
+        }
+        const int box = kQuant ? lane : lane / C::kChunks;
+        const int key = key0 + box * page;
+        const int id = __shfl_sync(0xFFFFFFFFu, ids, (key / page - pbase) & 31);
+        const bool mine = box < boxes;
+        const bool there = key < it.len;
+        const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.c.P);
+        const uint32_t bad = __ballot_sync(0xFFFFFFFFu, mine && there && !good);
+        if (bad && lane == 0) atomicOr(p.err, kErrPage);
+        if (!warp_all(mbar_wait(&empty[slot], (round & 1) ^ 1, abort_flag, p.err, kErrWaitLoad,
+                                p.wait_limit_ns))) {
+          ok = false;
+          break;
+        }
+        if constexpr (kQuant) {
+          const bool copy = mine && there && good;
+          const int rows = min(page, it.len - key);
+          uint32_t bytes = copy ? static_cast<uint32_t>(rows * D + page) : 0;
+          bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
+          if (lane == 0) {
+            ms.raw_bad[slot] = bad;
+            mbar_arrive_expect_tx(&full[slot], bytes);
+          }
+          __syncwarp();
+          if (copy) {
+            const size_t from = (static_cast<size_t>(id) * p.c.Hkv + it.h) * page;
+            const uint8_t* src = static_cast<const uint8_t*>((i & 1) ? p.c.vpages : p.c.kpages);
+            bulk_copy(smem + C::kOffRaw + slot * C::kRawBytes + box * page * D, src + from * D,
+                      static_cast<uint32_t>(rows * D), &full[slot], policy);
+            bulk_copy(smem + C::kOffScale + slot * kBN + box * page,
+                      ((i & 1) ? p.c.vscale : p.c.kscale) + from, static_cast<uint32_t>(page),
+                      &full[slot], policy);
+          }
+        } else {
+          mbar_arrive_expect_tx_elect(&full[slot], C::kTileBytes);
+          if (mine) {
+            const int z = there && good ? id * p.c.Hkv + it.h : p.c.P * p.c.Hkv;
+            const int y = min(it.len - key, page) - page;  // the tokens at the end of the rows
+            const int ch = lane % C::kChunks;
+            tma_load_3d(smem + C::kOffKV + slot * C::kTileBytes + ch * (kBN * 128) +
+                            box * page * 128,
+                        (i & 1) ? &p.tmap_v : &p.tmap_k, &full[slot], ch * 64, there ? y : 0, z,
+                        policy);
+          }
+          __syncwarp();
+        }
+        if (++slot == kRing) {
+          slot = 0;
+          ++round;
+        }
+        if (i == 0) {
+          // Q, once the item before has used its own
+          if (k > 0 && !warp_all(mbar_wait(&ms.q_empty, (k - 1) & 1, abort_flag, p.err,
+                                           kErrWaitLoad, p.wait_limit_ns))) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx_elect(&ms.q_full,
+                                      static_cast<uint32_t>(it.tiles * per_tile * p.G * D * 2));
+          for (int t = 0; t < it.tiles; ++t)
+            for (int ch = 0; ch < C::kChunks; ++ch)
+              tma_load_4d_elect(smem + t * C::kTileBytes + ch * (kBM * 128), &p.tmap_q, &ms.q_full,
+                                ch * 64, 0, it.h, it.row0 + t * per_tile, l2_policy_evict_first());
+        }
+      }
+      ++k;
+    }
+    if (ok && warp_all(mbar_wait(&ms.item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort_flag, p.err,
+                                 kErrWaitLoad, p.wait_limit_ns))) {
+      if (lane == 0) {
+        ms.item[k & 1].tiles = 0;
+        mbar_arrive(&ms.item_full[k & 1]);
+      }
+    }
+    if (abort_set(abort_flag)) {
+      // copies in flight land before the CTA leaves: those of the last Q (of item k, or the
+      // one before) and of the last round of the ring
+      if (k > 0) drain_wait(&ms.q_full, (k - 1) & 1);
+      drain_wait(&ms.q_full, k & 1);
+      for (uint32_t i = 0; i < kRing; ++i) {
+        if (i < slot)
+          drain_wait(&full[i], round & 1);
+        else if (round > 0)
+          drain_wait(&full[i], (round - 1) & 1);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ---- S_t = Q_t K_j^T, O_t += P_t V_j
+    reg_dealloc<C::kRegOther>();
+    constexpr uint32_t kTileDesc = C::kTileBytes >> 4;
+    const uint32_t desc_k = sdesc_sw128_lo(smem_u32(smem + C::kOffKV), 16);
+    constexpr uint32_t kQ0 = 0u - static_cast<uint32_t>(C::kOffKV >> 4), kQ1 = kQ0 + kTileDesc;
+    constexpr uint32_t kVFromK = static_cast<uint32_t>(((kBM * 128) >> 4) - 1) << 16;
+    auto issue_s = [&](int t, uint32_t slot) {
+      const uint32_t b0 = desc_k + slot * kTileDesc;
+      if (t)
+        issue_s_steps<D, false, C::kColS1, kQ1>(tmem, desc_k, b0);
+      else
+        issue_s_steps<D, false, C::kColS0, kQ0>(tmem, desc_k, b0);
+      mma_commit(&ms.s_full[t]);
+    };
+    auto issue_pv = [&](int t, uint32_t slot, uint32_t acc) {
+      const uint32_t b0 = desc_k + slot * kTileDesc;
+      if (t)
+        issue_pv_steps<D, false, C::kColO1, C::kColS1, kVFromK>(tmem, b0, acc);
+      else
+        issue_pv_steps<D, false, C::kColO0, C::kColS0, kVFromK>(tmem, b0, acc);
+    };
+    uint32_t p_step[2] = {0, 0};  // P tiles waited for
+    uint32_t slot = 0, round = 0;
+    auto wait_kv = [&]() -> bool {
+      return warp_all(mbar_wait(&ms.kv_full[slot], round & 1, abort_flag, p.err, kErrWaitMma,
+                                p.wait_limit_ns));
+    };
+    auto advance = [&]() {
+      if (++slot == C::kStages) {
+        slot = 0;
+        ++round;
+      }
+    };
+    auto wait_p = [&](int t) -> bool {
+      const uint32_t step = t ? p_step[1]++ : p_step[0]++;
+      if (!warp_all(mbar_wait(&ms.p_full[t], step & 1, abort_flag, p.err, kErrWaitMma,
+                              p.wait_limit_ns)))
+        return false;
+      tc_fence_after();
+      return true;
+    };
+    Item it;
+    bool ok = true;
+    for (uint32_t k = 0; ok && next_item(k, &it, kErrWaitMma); ++k) {
+      const int tiles = it.tiles, n = it.tile1 - it.tile0;
+      ok = warp_all(mbar_wait(&ms.q_full, k & 1, abort_flag, p.err, kErrWaitMma, p.wait_limit_ns));
+      // ring order K_0 V_0 K_1 V_1 ...; S of key tile i + 1 goes out with P V of tile i
+      uint32_t v_slot = 0;
+      for (int i = 0; i < n && ok; ++i) {
+        ok = wait_kv();  // K_i
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t k_slot = slot;
+        for (int t = 0; t < tiles && ok; ++t) {
+          if (i > 0) {
+            ok = wait_p(t);
+            if (!ok) break;
+            issue_pv(t, v_slot, i > 1 ? 1u : 0u);
+          }
+          issue_s(t, k_slot);
+        }
+        if (!ok) break;
+        mma_commit(&ms.kv_empty[k_slot]);
+        if (i > 0) mma_commit(&ms.kv_empty[v_slot]);
+        advance();
+        ok = wait_kv();  // V_i
+        v_slot = slot;
+        advance();
+      }
+      if (!ok) break;
+      mma_commit(&ms.q_empty);
+      tc_fence_after();
+      for (int t = 0; t < tiles && ok; ++t) {
+        ok = wait_p(t);
+        if (ok) {
+          issue_pv(t, v_slot, n > 1 ? 1u : 0u);
+          mma_commit(&ms.o_done[t]);
+        }
+      }
+      if (ok) mma_commit(&ms.kv_empty[v_slot]);
+    }
+    // all MMAs retire before the CTA gives tensor memory back
+    mma_commit(&ms.mma_done);
+    drain_wait(&ms.mma_done, 0);
+  } else {
+    reg_dealloc<C::kRegOther>();
+    if (kQuant && warp >= kWarpConvert) {
+      // ---- quantised tiles to bf16 ones, rows behind the last token to zeros
+      const int tid = threadIdx.x - kWarpConvert * 32;
+      uint32_t raw = 0, raw_round = 0, slot = 0, round = 0;
+      Item it;
+      bool ok = true;
+      for (uint32_t k = 0; ok && next_item(k, &it, kErrWaitLoad); ++k) {
+        const uint32_t n = 2u * static_cast<uint32_t>(it.tile1 - it.tile0);
+        for (uint32_t i = 0; i < n; ++i) {
+          const int key0 = (it.tile0 + static_cast<int>(i >> 1)) * kBN;
+          ok = warp_all(mbar_wait(&ms.raw_full[raw], raw_round & 1, abort_flag, p.err,
+                                  kErrWaitLoad, p.wait_limit_ns)) &&
+               warp_all(mbar_wait(&ms.kv_empty[slot], (round & 1) ^ 1, abort_flag, p.err,
+                                  kErrWaitLoad, p.wait_limit_ns));
+          if (!ok) break;
+          const uint32_t bad = ms.raw_bad[raw];
+          const uint8_t* codes = smem + C::kOffRaw + raw * C::kRawBytes;
+          const uint8_t* scales = smem + C::kOffScale + raw * kBN;
+          uint8_t* tile = smem + C::kOffKV + slot * C::kTileBytes;
+          constexpr int kPieces = D / 16;  // of 16 codes in a row
+#pragma unroll 2
+          for (int q = tid; q < kBN * kPieces; q += 128) {
+            const int row = q / kPieces, piece = q % kPieces;
+            uint4 x = *reinterpret_cast<const uint4*>(codes + q * 16);
+            uint32_t scale = scales[row];
+            if (key0 + row >= it.len || (bad >> (row / p.c.page) & 1u)) {
+              x = make_uint4(0, 0, 0, 0);
+              scale = 127;
+            }
+            const uint32_t f = e4m3_factor(scale), w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // bytes 0 2 and 1 3, then in order
+              const uint32_t a = e4m3_pair(w[e] << 8, f), b = e4m3_pair(w[e], f);
+              y[2 * e] = __byte_perm(a, b, 0x5410);
+              y[2 * e + 1] = __byte_perm(a, b, 0x7632);
+            }
+            if (__any_sync(0xFFFFFFFFu, scale > kScaleMost && scale != kScaleNan)) {
+              const uint32_t rest =
+                  (max(scale == kScaleNan ? 0u : scale, kScaleMost) - kScaleMost + 127u) << 7;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y[e]) : "r"(rest * 0x10001u));
+            }
+            // (the lanes of the row's halves store their two pieces in opposite order:
+            // no two of eight lanes in the same banks)
+            const int hi = piece / (kPieces / 2) & 1;
+            const uint32_t at16 = static_cast<uint32_t>(piece * 2);
+            uint8_t* dst = tile + (at16 >> 3) * (kBN * 128) + row * 128;
+            const uint32_t a0 = ((at16 & 7) ^ (row & 7)) << 4, a1 = a0 ^ 16;
+            *reinterpret_cast<uint4*>(dst + (hi ? a1 : a0)) =
+                hi ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + (hi ? a0 : a1)) =
+                hi ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(y[4], y[5], y[6], y[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ms.kv_full[slot]);
+            mbar_arrive(&ms.raw_empty[raw]);
+          }
+          if (++raw == C::kRaw) {
+            raw = 0;
+            ++raw_round;
+          }
+          if (++slot == C::kStages) {
+            slot = 0;
+            ++round;
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partial states of the items that were cut.  Block (c, y): the item in which
+// CTA c + 1 begins, if that is its first cut, and an eighth of its rows.
+constexpr int kMergeSplit = 8;
+
+template <int D>
+__global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__ PagedParams p) {
+  __shared__ CostShared shared;
+  __shared__ int slots[kMostCtas], count;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const CostPlan plan(p.c, p.G, p.causal);
+  const CostPlace at = plan.place<256>(shared, blockIdx.x + 1, p.ctas);
+  if (threadIdx.x == 0) count = 0;
+  __syncthreads();
+  CostItem item;
+  bool cut = at.b < p.c.B;
+  if (cut) {
+    item = plan.item(at);
+    const long long before = plan.start(at.total, blockIdx.x, p.ctas);
+    cut = item.x0 < at.first && before <= item.x0;
+  }
+  if (!cut) {  // (the same for the whole block)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  // its parts: slots in the order of the CTAs
+  if (warp == 0) {
+    int n = 0;
+    for (unsigned c0 = blockIdx.x; c0 < p.ctas; c0 += 32) {
+      const unsigned c = c0 + lane;
+      int t0 = 0, t1 = 0;
+      if (c < p.ctas) {
+        t0 = plan.cut(item, plan.start(at.total, c, p.ctas) - item.x0);
+        t1 = plan.cut(item, plan.start(at.total, c + 1, p.ctas) - item.x0);
+      }
+      const uint32_t has = __ballot_sync(0xFFFFFFFFu, t1 > t0);
+      if (t1 > t0) slots[n + __popc(has & ((1u << lane) - 1u))] = 2 * static_cast<int>(c) + (t0 == 0);
+      n += __popc(has);
+      if (__shfl_sync(0xFFFFFFFFu, t0, 31) >= item.n_kv) break;
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int n = count;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n < 2) return;  // in one CTA after all
+  const int per_tile = kBM / p.G, in_tile = per_tile * p.G;
+  const int rows = min(2 * per_tile, item.left) * p.G;
+  for (int i = static_cast<int>(blockIdx.y) * 8 + warp; i < rows; i += 8 * kMergeSplit) {
+    const int t = i / in_tile, r = t * kBM + i % in_tile;
+    auto state = [&](int k) { return static_cast<size_t>(slots[k]) * (2 * kBM) + r; };
+    float top = -CUDART_INF_F;
+    for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_ml[state(k)].x);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    State<D> sum;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) sum.add(p.part_ml[state(k)], top, p.part_o + state(k) * D, lane);
+    sum.finish(p, item.row0 + i / p.G, item.h * p.G + i % p.G, top, lane);
+  }
+}
+
+template <int D, bool kQuant>
+cudaError_t launch_tile(const PagedParams& p, int dev, cudaStream_t stream) {
+  using C = TileCfg<D, kQuant>;
+  static std::atomic<bool> ready[64];
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_tile_kernel<D, kQuant>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true, std::memory_order_release);
+  }
+  paged_tile_kernel<D, kQuant><<<p.ctas, C::kThreads, C::kSmem, stream>>>(p);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  if (p.ctas < 2) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ctas - 1, kMergeSplit);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<D>, p);
+}
+
+}  // namespace
+
+size_t paged_tile_scratch(const PagedParams& p, size_t* ml_at) {
+  *ml_at = static_cast<size_t>(p.ctas) * 2 * (2 * kBM) * p.c.D * sizeof(float);
+  return *ml_at + static_cast<size_t>(p.ctas) * 2 * (2 * kBM) * sizeof(float2);
+}
+
+cudaError_t launch_paged_tile(const PagedParams& p, int dev, cudaStream_t stream) {
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (p.c.D == 128)
+    return p.c.quant ? launch_tile<128, true>(p, dev, stream)
+                     : launch_tile<128, false>(p, dev, stream);
+  return p.c.quant ? launch_tile<64, true>(p, dev, stream) : launch_tile<64, false>(p, dev, stream);
+}
+
+}  // namespace attn
