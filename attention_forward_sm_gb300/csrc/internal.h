@@ -270,6 +270,7 @@ struct PagedParams {
   uint64_t wait_limit_ns;
 };
 // The kernel for few rows, and what its scratch takes.
+unsigned paged_stream_ctas(const PagedParams& p, int rows);  // per SM
 size_t paged_stream_scratch(const PagedParams& p, int rows, size_t* ml_at);
 cudaError_t launch_paged_stream(const PagedParams& p, int rows, int dev, cudaStream_t stream);
 // The kernel for many rows, likewise.

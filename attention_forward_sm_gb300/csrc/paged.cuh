@@ -74,7 +74,7 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 // A code s eeee mmm moved to bits 15 and 10 .. 4 of a bf16 is its value times 2^-120
 // (the exponents' biases are 7 and 127), subnormal codes included; a product with
 // 2^(120 + e) is code * 2^e, exact.  Scale bytes (e + 127) above 134 would take the
-// factor out of bf16: what is above goes into e4m3_rest.
+// factor out of bf16: what is above is a second one.
 constexpr uint32_t kScaleNan = 255, kScaleMost = 134;
 
 // The codes in bytes 1 and 3 of u (the others do not matter), times the factors f.
@@ -84,18 +84,33 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t u, uint32_t f) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f));
   return y;
 }
+// Two codes (the lower byte first) as f16, which holds every one exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+  return h;
+}
+// 2^e and e of a scale byte; NaN for the one that says so.
+__device__ __forceinline__ float scale_value(uint32_t scale) {
+  return __uint_as_float(scale == kScaleNan ? 0x7FFFFFFFu : scale << 23);
+}
+__device__ __forceinline__ float scale_exponent(uint32_t scale) {
+  return static_cast<float>(static_cast<int>(scale) - 127);
+}
+// 16 codes in order, under one factor.
+__device__ __forceinline__ void e4m3_row16(const uint4& x, uint32_t f, uint32_t (&y)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = e4m3_pair(__byte_perm(w[i], 0, 0x1404), f);
+    y[2 * i + 1] = e4m3_pair(__byte_perm(w[i], 0, 0x3424), f);
+  }
+}
 __device__ __forceinline__ uint32_t e4m3_factor16(uint32_t scale) {
   return scale == kScaleNan ? 0x7FFFu : (min(scale, kScaleMost) + 120u) << 7;
 }
-// One scale for both values of a pair; one for each.
 __device__ __forceinline__ uint32_t e4m3_factor(uint32_t scale) {
   return e4m3_factor16(scale) * 0x10001u;
-}
-__device__ __forceinline__ uint32_t e4m3_factors(uint32_t lo, uint32_t hi) {
-  return e4m3_factor16(lo) | e4m3_factor16(hi) << 16;
-}
-__device__ __forceinline__ float e4m3_rest(uint32_t scale) {
-  return __uint_as_float((max(scale, kScaleMost) - kScaleMost + 127u) << 23);
 }
 
 }  // namespace

@@ -92,7 +92,7 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
   l.rows = many ? 0 : rows <= 8 ? 8 : 16;
   // the streaming kernel numbers its units of work in 32 bits
   const long long blocks = static_cast<long long>(c.T) * p.G / 8 + c.B;
-  if (blocks * c.Hkv * (static_cast<long long>(c.M) * c.page / 64 + 1) >= (1ll << 31))
+  if (blocks * c.Hkv * (static_cast<long long>(c.M) * c.page / 64 + 3) >= (1ll << 31))
     return ATTN_ERR_SHAPE;
   DeviceInfo di;
   if (int rc = device_info(&di)) return rc;
@@ -104,6 +104,7 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
   if (many)
     if (int rc = encode_queries(&p.tmap_q, q, c.D, p.G, c.Hkv, c.T, 128 / p.G, q_stride)) return rc;
   p.ctas = std::min(static_cast<unsigned>(di.sms), kMostCtas);
+  if (!many) p.ctas *= paged_stream_ctas(p, l.rows);
   p.err = di.err_word;
   p.wait_limit_ns = wait_limit_ns();
   l.dev = di.dev;

@@ -13,6 +13,8 @@
 // Bound by memory.  A lane moves 8 elements of a row and D / 8 lanes a row, so that
 // a row is one run of whole sectors on either side; a CTA takes kTokens tokens, whose
 // pages are looked up once, by a warp each, ahead of the rows.
+#include <cuda_fp16.h>
+
 #include "../../include/attn.h"
 #include "paged.cuh"
 
@@ -30,17 +32,9 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
   return x;
 }
 
-// Two e4m3 codes (the lower byte first) as floats.
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-      : "=r"(h)
-      : "r"(codes));
-  float2 f;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-      : "=f"(f.x), "=f"(f.y)
-      : "r"(h));
-  return f;
+  const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(codes));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
@@ -74,7 +68,7 @@ __device__ __forceinline__ uint2 quantise_row(const uint4& x, uint8_t* scale) {
   return q;
 }
 __device__ __forceinline__ uint4 dequantise(const uint2& q, uint32_t scale) {
-  const float f = __uint_as_float(scale == kScaleNan ? 0x7FFFFFFFu : scale << 23);
+  const float f = scale_value(scale);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

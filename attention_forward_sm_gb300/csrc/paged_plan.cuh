@@ -17,26 +17,26 @@ struct Deal {
   __device__ Deal(uint32_t total, uint32_t ctas)
       : runs(min(total, ctas)), each(runs ? total / runs : 0), more(runs ? total % runs : 0) {}
   __device__ uint32_t start(uint32_t r) const { return r * each + min(r, more); }
-  __device__ uint32_t run_of(uint32_t x) const {
-    const uint32_t cut = more * (each + 1);
-    return x < cut ? x / (each + 1) : min(more + (x - cut) / each, runs - 1);
-  }
 };
 
 struct PlanShared {
   uint32_t warp_sum[16];
-  uint32_t total;
   int b;
   uint32_t in_request;
 };
 struct PlanPlace {
-  uint32_t first, end;  // units of this CTA
+  uint32_t total;       // units of all
+  uint32_t first, end;  // of this CTA
   int b;                // request that holds the first one,
   uint32_t in_request;  // and which of its units that is
 };
 
-// Units of a request: for each KV head and block of rows, its key tiles (one where
-// there is no key, so that the rows' results are written).
+// What a block of rows costs besides its keys, in units: its queries, and joining and
+// storing what the warps have.
+constexpr uint32_t kBlockCost = 2;
+
+// An item is a block of rows of one KV head; it is worth its key tiles (one where there
+// is no key, so that the rows' results are written) and kBlockCost, which come first.
 struct StreamPlan {
   const PagedArrays& c;
   int G, block_rows;
@@ -49,48 +49,37 @@ struct StreamPlan {
     return static_cast<int>((static_cast<long long>(n) * G + block_rows - 1) / block_rows);
   }
   __device__ uint32_t units(int n, int len) const {
-    return static_cast<uint32_t>(c.Hkv) * static_cast<uint32_t>(blocks(n)) * tiles(len);
+    return static_cast<uint32_t>(c.Hkv) * static_cast<uint32_t>(blocks(n)) *
+           (tiles(len) + kBlockCost);
   }
   __device__ uint32_t units_of(int b) const {
     const Rows rows = request_rows(c, b);
     return rows.n > 0 ? units(rows.n, clamp_len(c, b)) : 0;
   }
-  // The units of the requests [lo, hi) that a thread adds up, and those in front of
-  // them; sh.total gets the sum of all.  All kThreads threads call this.
+  // Where CTA `cta` of `ctas` begins and ends; all kThreads threads call this.
   template <int kThreads>
-  __device__ uint32_t scan(PlanShared& sh, int* lo, int* hi, uint32_t* own) const {
+  __device__ PlanPlace place(PlanShared& sh, uint32_t cta, uint32_t ctas) const {
     const int per = (c.B + kThreads - 1) / kThreads;
-    *lo = min(static_cast<int>(threadIdx.x) * per, c.B);
-    *hi = min(*lo + per, c.B);
-    uint32_t sum = 0;
-    for (int b = *lo; b < *hi; ++b) sum += units_of(b);
-    *own = sum;
+    const int lo = min(static_cast<int>(threadIdx.x) * per, c.B), hi = min(lo + per, c.B);
+    uint32_t own = 0;
+    for (int b = lo; b < hi; ++b) own += units_of(b);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t sum = own;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
       if (lane >= d) sum += up;
     }
     if (lane == 31) sh.warp_sum[warp] = sum;
+    if (threadIdx.x == 0) sh.b = c.B;
     __syncthreads();
-    uint32_t before = 0, total = 0;
+    uint32_t before = sum - own, total = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += sh.warp_sum[w];
       total += sh.warp_sum[w];
     }
-    if (threadIdx.x == 0) sh.total = total;
-    return before + sum - *own;
-  }
-  // Where CTA `cta` of `ctas` begins and ends.
-  template <int kThreads>
-  __device__ PlanPlace place(PlanShared& sh, uint32_t cta, uint32_t ctas) const {
-    if (threadIdx.x == 0) sh.b = c.B;
-    int lo, hi;
-    uint32_t own;
-    uint32_t before = scan<kThreads>(sh, &lo, &hi, &own);
-    __syncthreads();
-    const Deal deal(sh.total, ctas);
-    PlanPlace at = {0, 0, c.B, 0};
+    PlanPlace at = {total, 0, 0, c.B, 0};
+    const Deal deal(total, ctas);
     if (cta < deal.runs) {
       at.first = deal.start(cta);
       at.end = deal.start(cta + 1);
@@ -110,20 +99,6 @@ struct StreamPlan {
     at.b = sh.b;
     at.in_request = sh.in_request;
     return at;
-  }
-  // Units in front of request b, of the calling warp's choice (< 0: none).  Every warp
-  // of the block calls this; sh.total is the sum of all afterwards.
-  template <int kThreads>
-  __device__ uint32_t before(PlanShared& sh, uint32_t (&starts)[kThreads], int b) const {
-    int lo, hi;
-    uint32_t own;
-    starts[threadIdx.x] = scan<kThreads>(sh, &lo, &hi, &own);
-    __syncthreads();
-    if (b < 0) return 0;
-    const int per = (c.B + kThreads - 1) / kThreads;
-    uint32_t sum = starts[b / per];
-    for (int i = b / per * per; i < b; ++i) sum += units_of(i);
-    return sum;
   }
 };
 

@@ -42,7 +42,8 @@ struct Unit {
   int key0, len, slot;     // first key; tokens in the cache; partial state, -1: none
   int row0, rows;          // first row of the dense tensors; new tokens
 };
-constexpr int kUnitFirst = 1, kUnitLast = 2, kUnitEnd = 4;  // of the block's part here; no unit
+constexpr int kUnitFirst = 1, kUnitLast = 2, kUnitEnd = 4;  // a team's first and last of an
+                                                            // item; there are no more
 
 template <int D, bool kQuant, int NT>
 struct StreamCfg {
@@ -51,15 +52,18 @@ struct StreamCfg {
   static constexpr int kTile = kUnitKeys * kRowBytes;  // K or V of a unit
   static constexpr int kScales = kQuant ? 2 * kUnitKeys : 0;
   static constexpr int kMerge = kWarps * kRows * D * 4;
-  // as many stages as fit beside the buffer for merging, 128 KB of copies in flight at most
-  static constexpr int kRoom = 226 * 1024 - 1024 - kMerge;
+  // Two CTAs on an SM where the registers allow it: one joins its warps' states and
+  // stores while the other goes on.
+  static constexpr int kCtas = kQuant && NT == 1 ? 2 : 1;
+  // As many stages as fit beside the buffer for merging, at most 16, and an even number:
+  // a stage belongs to one team, which so sees every phase of its barrier.
+  static constexpr int kRoom = (kCtas == 1 ? 227 : 113) * 1024 - 3072 - kMerge;
   static constexpr int kFit = kRoom / (2 * kTile + kScales);
-  static constexpr int kWant = 196 * 1024 / (2 * kTile);
-  static constexpr int kStages = kFit < kWant ? kFit : kWant;
+  static constexpr int kStages = kFit < 16 ? kFit / 2 * 2 : 16;
   static constexpr int kOffMerge = kStages * 2 * kTile;
   static constexpr int kOffScales = kOffMerge + kMerge;
   static constexpr int kSmem = kOffScales + kStages * kScales + 1024;  // + alignment
-  static_assert(kStages >= 3, "shared memory");
+  static_assert(kStages >= 2 && kStages % 2 == 0, "shared memory");
 };
 
 template <int kStages, int kRows>
@@ -72,32 +76,47 @@ struct StreamShared {
   int abort_flag;
 };
 
+// bf16 or f16 operands.
+template <bool kHalf>
 __device__ __forceinline__ void mma_16n8k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+#define ATTN_MMA_16N8K16(TYPE)                                                                  \
+  asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                    \
+      ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                    \
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                          \
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+  if constexpr (kHalf)
+    ATTN_MMA_16N8K16("f16");
+  else
+    ATTN_MMA_16N8K16("bf16");
+#undef ATTN_MMA_16N8K16
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The two lower and the two upper of four codes.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  return e4m3x2_to_f16x2(static_cast<uint16_t>(x));
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  return e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16));
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ void lds128(uint32_t (&x)[4], uint32_t addr) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void lds64(uint32_t (&x)[4], uint32_t addr) {
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
-  uint32_t x;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
-  return x;
+template <int kBytes>
+__device__ __forceinline__ void load_piece(uint32_t (&x)[4], const uint8_t* from) {
+  if constexpr (kBytes == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(from);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(from);
+    x[0] = v.x, x[1] = v.y, x[2] = x[3] = 0;
+  }
 }
 
 // Key that row i of a 16-key block stands for.  For i = 2a + b < 8: the keys of
@@ -121,22 +140,21 @@ __device__ __forceinline__ uint32_t swizzled(int row, int at) {
 }
 
 template <int D, bool kQuant, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
     paged_stream_kernel(const __grid_constant__ PagedParams p) {
   using C = StreamCfg<D, kQuant, NT>;
   constexpr int kStages = C::kStages, kRows = C::kRows, kRowBytes = C::kRowBytes;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   __shared__ StreamShared<kStages, kRows> ms;
-  static_assert(C::kSmem + sizeof(ms) <= 227 * 1024, "shared memory");
+  static_assert((C::kSmem + sizeof(ms) + 1024) * C::kCtas <= 228 * 1024, "shared memory");
   const uint32_t abort_flag = smem_u32(&ms.abort_flag);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ms.full[s], 1);
-      mbar_init(&ms.empty[s], kWarps);
+      mbar_init(&ms.empty[s], kWarps / 2);
     }
     mbar_init(&ms.merge_full, kWarps);
     mbar_init(&ms.merge_empty, kWarps);
@@ -165,17 +183,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int blocks = plan.blocks(rows.n);
       int pbase = -64, ids = 0;
       while (in_request < units && u < at.end && ok) {
-        // a block's part that lies in this CTA
-        const uint32_t item = in_request / tiles, tile0 = in_request % tiles;
-        const uint32_t n = min(tiles - tile0, at.end - u);
+        // an item's part that lies in this CTA, what it costs and its key tiles
+        const uint32_t item = in_request / (tiles + kBlockCost);
+        const uint32_t from = in_request % (tiles + kBlockCost);
+        const uint32_t cost = min(tiles + kBlockCost - from, at.end - u);
+        const uint32_t tile0 = max(from, kBlockCost) - kBlockCost;
+        const uint32_t n = max(from + cost, kBlockCost) - kBlockCost - tile0;
+        u += cost;
+        in_request += cost;
         const int h = static_cast<int>(item) / blocks, block = static_cast<int>(item) % blocks;
         const int slot = n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tile0 == 0);
-        for (uint32_t i = 0; i < n; ++i, ++s) {
+        // the teams take turns, so that both have as many units: one may be without keys
+        const uint32_t both = (n + 1) & ~1u;
+        for (uint32_t i = 0; i < both; ++i, ++s) {
           const int key0 = static_cast<int>(tile0 + i) * kUnitKeys;
           const uint32_t st = s % kStages;
           // pages of this unit: lane l holds entry pbase + l of the table's row
           const int page0 = key0 / p.c.page;
-          const int n_box = max(0, min(kUnitKeys, len - key0) + box - 1) / box;
+          const int keys = i < n ? min(kUnitKeys, len - key0) : 0;
+          const int n_box = (max(0, keys) + box - 1) / box;
           const int page1 = (key0 + max(n_box - 1, 0) * box) / p.c.page;
           if (page0 < pbase || page1 >= pbase + 32) {
             pbase = page0;
@@ -201,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           if (lane == 0) {
-            ms.unit[st] = Unit{(i == 0 ? kUnitFirst : 0) | (i == n - 1 ? kUnitLast : 0),
-                               b, h, block, key0, len, slot, rows.first, rows.n};
+            ms.unit[st] = Unit{(i < 2 ? kUnitFirst : 0) | (i + 2 >= both ? kUnitLast : 0),
+                               b, h, block, i < n ? key0 : len, len, slot, rows.first, rows.n};
             mbar_arrive_expect_tx(
                 &ms.full[st],
                 static_cast<uint32_t>(2 * box * (n_box * kRowBytes +
@@ -229,13 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        u += n;
-        in_request += n;
       }
       ++b;
       in_request = 0;
     }
-    if (ok) {
+    for (int i = 0; i < 2 && ok; ++i, ++s) {
       const uint32_t st = s % kStages;
       if (warp_all(mbar_wait(&ms.empty[st], ((s / kStages) & 1u) ^ 1u, abort_flag, p.err,
                              kErrWaitLoad, p.wait_limit_ns)) &&
@@ -243,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ms.unit[st].flags = kUnitEnd;
         mbar_arrive(&ms.full[st]);
       }
+      __syncwarp();
     }
     if (abort_set(abort_flag))  // copies in flight land before the CTA leaves
       for (uint32_t i = s > kStages ? s - kStages : 0u; i < s; ++i)
@@ -258,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int vkey1 = my_key + block_key(2 * t + 1);
   constexpr int kSteps = D / 16;  // products per S^T, and 16-row tiles of O^T
   uint32_t qf[NT][2 * kSteps];
-  float o[NT][kSteps][4], m[NT][2], l[NT][2];
+  float o[NT][kSteps][4], m[NT][2], l[NT][2], by_row[NT][2];
   int vis[NT][2], first_vis = 0;
   uint32_t merges = 0;
-  for (uint32_t s = 0;; ++s) {
+  for (uint32_t s = static_cast<uint32_t>(warp) / 4;; s += 2) {  // the team's units
     const uint32_t st = s % kStages;
     if (!warp_all(mbar_wait(&ms.full[st], (s / kStages) & 1u, abort_flag, p.err, kErrWaitMma,
                             p.wait_limit_ns)))
@@ -275,34 +300,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int nt = 0; nt < NT; ++nt) {
         const int r = nt * 8 + g;
         const int row = un.block * kRows + r;
-        const bool real = r < n_rows;
         const uint8_t* q =
             static_cast<const uint8_t*>(p.q) +
             2 * (static_cast<size_t>(un.row0 + row / p.G) * p.q_stride +
                  static_cast<size_t>(un.h * p.G + row % p.G) * D);
-        // the elements that go with those of K that the thread loads: piece 4c + t
-        // of a row, its 16-bit pairs in order (bf16) or its bytes 0 2 1 3 of each word
+        // the elements that go with those of K that the thread loads: piece 4c + t of a
+        // row, its pairs in order
+        constexpr int kWords = kQuant ? 8 : 4;  // of the query for one piece
 #pragma unroll
-        for (int c = 0; c < kRowBytes / 64; ++c) {
-          uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-          if (real) {
-            const uint4* src = reinterpret_cast<const uint4*>(q + (4 * c + t) * (kQuant ? 32 : 16));
-            x[0] = src[0];
-            if constexpr (kQuant) x[1] = src[1];
-          }
-          if constexpr (kQuant) {
-            const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+        for (int c = 0; c < kRowBytes / 64; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              qf[nt][8 * c + 2 * i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);
-              qf[nt][8 * c + 2 * i + 1] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
-            }
-          } else {
-            qf[nt][4 * c] = x[0].x;
-            qf[nt][4 * c + 1] = x[0].y;
-            qf[nt][4 * c + 2] = x[0].z;
-            qf[nt][4 * c + 3] = x[0].w;
+          for (int i = 0; i < kWords / 4; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (r < n_rows) x = *reinterpret_cast<const uint4*>(q + ((4 * c + t) * kWords + 4 * i) * 4);
+            qf[nt][c * kWords + 4 * i] = x.x;
+            qf[nt][c * kWords + 4 * i + 1] = x.y;
+            qf[nt][c * kWords + 4 * i + 2] = x.z;
+            qf[nt][c * kWords + 4 * i + 3] = x.w;
           }
+        float scale = 1.f;
+        if constexpr (kQuant) {
+          // to f16, over a power of two that makes the row's largest element 1 to 2: exact
+          // but below 2^-14, where a step is 2^-24
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 2 * kSteps; ++i)
+            top = max(top, max(qf[nt][i] << 16 & 0x7FFFFFFFu, qf[nt][i] & 0x7FFFFFFFu));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          const uint32_t e = min(max(top >> 23, 1u), 253u);
+          scale = __uint_as_float(e << 23);
+          const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+          for (int i = 0; i < 2 * kSteps; ++i)
+            qf[nt][i] = pack_f16x2(__uint_as_float(qf[nt][i] << 16) * inv,
+                                   __uint_as_float(qf[nt][i] & 0xFFFF0000u) * inv);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -310,6 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           vis[nt][k] = p.causal ? min(un.len, before + row_of + 1) : un.len;
           m[nt][k] = -CUDART_INF_F;
           l[nt][k] = 0.f;
+          by_row[nt][k] =
+              kQuant ? p.scale_log2 * __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4 * k) : p.scale_log2;
         }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
@@ -320,50 +354,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     const int k0 = un.key0 + my_key;
-    if ((s & 1u) == static_cast<uint32_t>(warp >> 2) && k0 < un.len) {
-      const uint32_t ktile = smem_u32(smem) + st * (2 * C::kTile), vtile = ktile + C::kTile;
+    if (k0 < un.len) {
+      const uint8_t *ktile = smem + st * (2 * C::kTile), *vtile = ktile + C::kTile;
+      [[maybe_unused]] const uint8_t* scales = smem + C::kOffScales + st * C::kScales;
       float x[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[nt][k] = 0.f;
-      [[maybe_unused]] uint32_t f_lo = 0, f_hi = 0, scales = 0;
-      float by_lo = p.scale_log2, by_hi = p.scale_log2;
-      if constexpr (kQuant) {
-        scales = smem_u32(smem) + C::kOffScales + st * C::kScales;
-        const uint32_t lo = lds8(scales + row_lo), hi = lds8(scales + row_hi);
-        f_lo = e4m3_factor(lo);
-        f_hi = e4m3_factor(hi);
-        by_lo *= e4m3_rest(lo);
-        by_hi *= e4m3_rest(hi);
-      }
 #pragma unroll
       for (int c = 0; c < kRowBytes / 64; ++c) {
         uint32_t a[4], e[4];
-        lds128(a, ktile + swizzled<kRowBytes>(row_lo, (4 * c + t) * 16));
-        lds128(e, ktile + swizzled<kRowBytes>(row_hi, (4 * c + t) * 16));
+        load_piece<16>(a, ktile + swizzled<kRowBytes>(row_lo, (4 * c + t) * 16));
+        load_piece<16>(e, ktile + swizzled<kRowBytes>(row_hi, (4 * c + t) * 16));
         if constexpr (kQuant) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t a0 = e4m3_pair(a[i] << 8, f_lo), a2 = e4m3_pair(a[i], f_lo);
-            const uint32_t a1 = e4m3_pair(e[i] << 8, f_hi), a3 = e4m3_pair(e[i], f_hi);
+            const uint32_t a0 = e4m3_lo(a[i]), a2 = e4m3_hi(a[i]);
+            const uint32_t a1 = e4m3_lo(e[i]), a3 = e4m3_hi(e[i]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_16n8k16(x[nt], a0, a1, a2, a3, qf[nt][8 * c + 2 * i], qf[nt][8 * c + 2 * i + 1]);
+              mma_16n8k16<true>(x[nt], a0, a1, a2, a3, qf[nt][8 * c + 2 * i], qf[nt][8 * c + 2 * i + 1]);
           }
         } else {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_16n8k16(x[nt], a[0], e[0], a[1], e[1], qf[nt][4 * c], qf[nt][4 * c + 1]);
-            mma_16n8k16(x[nt], a[2], e[2], a[3], e[3], qf[nt][4 * c + 2], qf[nt][4 * c + 3]);
+            mma_16n8k16<false>(x[nt], a[0], e[0], a[1], e[1], qf[nt][4 * c], qf[nt][4 * c + 1]);
+            mma_16n8k16<false>(x[nt], a[2], e[2], a[3], e[3], qf[nt][4 * c + 2], qf[nt][4 * c + 3]);
           }
         }
       }
       // scores in log2 units, unseen ones -inf
+      const float by_lo = kQuant ? scale_value(scales[row_lo]) : 1.f;
+      const float by_hi = kQuant ? scale_value(scales[row_hi]) : 1.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[nt][k] *= k < 2 ? by_lo : by_hi;
+        for (int k = 0; k < 4; ++k) {
+          x[nt][k] *= by_row[nt][k & 1];
+          if constexpr (kQuant) x[nt][k] *= k < 2 ? by_lo : by_hi;
+        }
       if (k0 + 16 > first_vis) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -371,19 +401,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k)
             if (un.key0 + (k < 2 ? row_lo : row_hi) >= vis[nt][k & 1]) x[nt][k] = -CUDART_INF_F;
       }
+      // Quantised, a weight of V's codes is 2^(x + e), e the exponent of V's scale, and the
+      // maximum is of x + e: then no weight is more than 2^8, and what f16 loses (steps
+      // of 2^-24) is next to the largest product, since every row of codes reaches
+      // beyond 224.  The sum of weights is of 2^x, over the same reference.
+      float ev[2] = {0.f, 0.f};
+      [[maybe_unused]] uint32_t vscale[2] = {127, 127};
+      if constexpr (kQuant) {
+        vscale[0] = scales[kUnitKeys + row_lo];
+        vscale[1] = scales[kUnitKeys + row_hi];
+        if (vscale[0] != kScaleNan) ev[0] = scale_exponent(vscale[0]);
+        if (vscale[1] != kScaleNan) ev[1] = scale_exponent(vscale[1]);
+      }
       // The maximum moves only when a score is above it by more than 2^8: a stale one
       // is as good (the sum has the same), and the vote is cheaper than the maximum.
       bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) above = above || x[nt][k] > m[nt][k & 1] + 8.f;
+        for (int k = 0; k < 4; ++k) above = above || x[nt][k] + ev[k >> 1] > m[nt][k & 1] + 8.f;
       if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float top = fmaxf(x[nt][k], x[nt][k + 2]);
+            float top = fmaxf(x[nt][k] + ev[0], x[nt][k + 2] + ev[1]);
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
@@ -399,76 +441,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
       }
-      // V: rows behind the last token may hold anything, and 0 * NaN is none
-      const bool tail = k0 + 16 > un.len;
       uint32_t pf[NT][2];
-      [[maybe_unused]] float rest_lo = 1.f, rest_hi = 1.f;
-      if constexpr (kQuant) {
-        rest_lo = e4m3_rest(lds8(scales + kUnitKeys + row_lo));
-        rest_hi = e4m3_rest(lds8(scales + kUnitKeys + row_hi));
-      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = x[nt][k] == -CUDART_INF_F ? 0.f : ex2_approx(x[nt][k] - m[nt][k & 1]);
-        l[nt][0] += w[0] + w[2];
-        l[nt][1] += w[1] + w[3];
-        if constexpr (kQuant) {
-          w[0] *= rest_lo;
-          w[1] *= rest_lo;
-          w[2] *= rest_hi;
-          w[3] *= rest_hi;
+        for (int k = 0; k < 4; ++k) {
+          const bool none = x[nt][k] == -CUDART_INF_F;
+          const float d = x[nt][k] - m[nt][k & 1];
+          w[k] = none ? 0.f : ex2_approx(d);
+          l[nt][k & 1] += w[k];
+          if constexpr (kQuant) w[k] = none ? 0.f : ex2_approx(d + ev[k >> 1]);
         }
-        // bf16 for the product, as V is
-        pf[nt][0] = transpose_8x8(pack_bf16x2(w[0], w[1]));
-        pf[nt][1] = transpose_8x8(pack_bf16x2(w[2], w[3]));
+        // rounded for the product: to bf16, as V is, or f16
+        pf[nt][0] = transpose_8x8(kQuant ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
+        pf[nt][1] = transpose_8x8(kQuant ? pack_f16x2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
       }
+      // V: rows behind the last token may hold anything, and 0 * NaN is none; rows that
+      // stand for NaN
+      const bool tail = k0 + 16 > un.len;
       const int keys[4] = {vkey, vkey1, vkey + 8, vkey1 + 8};
       constexpr int kVBytes = kQuant ? D / 8 : 16;  // a thread's piece of a row
-      [[maybe_unused]] uint32_t f[2];
-      if constexpr (kQuant) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t by[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            by[k] = lds8(scales + kUnitKeys + keys[2 * i + k]);
-            if (tail && un.key0 + keys[2 * i + k] >= un.len) by[k] = 127;
-          }
-          f[i] = e4m3_factors(by[0], by[1]);
-        }
-      }
+      [[maybe_unused]] const bool odd =
+          kQuant && (tail || __any_sync(0xFFFFFFFFu, max(vscale[0], vscale[1]) == kScaleNan));
 #pragma unroll
       for (int half = 0; half < (kQuant ? 1 : D / 64); ++half) {
         uint32_t v[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t from = vtile + swizzled<kRowBytes>(keys[i], half * 128 + g * kVBytes);
-          if constexpr (kVBytes == 16)
-            lds128(v[i], from);
-          else
-            lds64(v[i], from);
-          if (tail && un.key0 + keys[i] >= un.len)
+          load_piece<kVBytes>(v[i], vtile + swizzled<kRowBytes>(keys[i], half * 128 + g * kVBytes));
+          if (kQuant ? odd : tail) {
+            const bool none = un.key0 + keys[i] >= un.len;
+            const bool nan = kQuant && scales[kUnitKeys + keys[i]] == kScaleNan;
+            if (none || nan)
 #pragma unroll
-            for (int k = 0; k < kVBytes / 4; ++k) v[i][k] = 0;
+              for (int k = 0; k < kVBytes / 4; ++k) v[i][k] = none ? 0u : 0x7F7F7F7Fu;
+          }
         }
 #pragma unroll
         for (int i = 0; i < kVBytes / 4; ++i) {
           if constexpr (kQuant) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {  // bytes 2k, 2k + 1 of the word
-              const uint32_t s0 = 0x4000 + 0x2020 * k, s1 = s0 + 0x1010;
-              uint32_t a[4];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                a[2 * j] = e4m3_pair(__byte_perm(v[2 * j][i], v[2 * j + 1][i], s0), f[j]);
-                a[2 * j + 1] = e4m3_pair(__byte_perm(v[2 * j][i], v[2 * j + 1][i], s1), f[j]);
-              }
+              // byte 2k of both keys, then byte 2k + 1
+              const uint32_t both = k ? 0x7362 : 0x5140;
+              const uint32_t lo = __byte_perm(v[0][i], v[1][i], both);
+              const uint32_t hi = __byte_perm(v[2][i], v[3][i], both);
+              const uint32_t a0 = e4m3_lo(lo), a1 = e4m3_hi(lo);
+              const uint32_t a2 = e4m3_lo(hi), a3 = e4m3_hi(hi);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_16n8k16(o[nt][2 * i + k], a[0], a[1], a[2], a[3], pf[nt][0], pf[nt][1]);
+                mma_16n8k16<true>(o[nt][2 * i + k], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
             }
           } else {
             const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410);
@@ -477,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_16n8k16(o[nt][half * 4 + i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+              mma_16n8k16<false>(o[nt][half * 4 + i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
           }
         }
       }
@@ -536,65 +559,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// W warps join the partial states of a (row, query head) whose keys several CTAs
-// had; the others' results are there already.  The plan, which needs no result
-// of the kernel before, is found ahead of the wait for it.
-template <int D, int W>
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedParams p,
-                                                          int block_rows) {
+// Joins the partial states of the items that were cut.  Block c: the item in which CTA
+// c + 1 begins, if that is its first cut.  The plan, which needs no result of the
+// kernel before, is found ahead of the wait for it.  Rows are few and parts may be
+// many: the warps share out rows first, then a row's parts.
+template <int D>
+__global__ void __launch_bounds__(256) stream_merge_kernel(const __grid_constant__ PagedParams p,
+                                                           int block_rows) {
   __shared__ PlanShared shared;
-  __shared__ uint32_t starts_of[256];
   __shared__ alignas(16) float sums[8][D];
   __shared__ float2 tops[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const StreamPlan plan(p.c, p.G, block_rows);
-  const long long row = static_cast<long long>(blockIdx.x) * (8 / W) + warp / W;
-  const int t = static_cast<int>(row / p.Hq), hq = static_cast<int>(row % p.Hq);
-  const int b = row < static_cast<long long>(p.c.T) * p.Hq ? find_request(p.c, t, lane) : -1;
-  const uint32_t before = plan.before<256>(shared, starts_of, b);
-  int first = 0, n = 0, r = 0;
-  bool starts = false;
-  if (b >= 0) {
-    const Rows rows = request_rows(p.c, b);
-    const int len = clamp_len(p.c, b);
-    const int in_head = (t - rows.first) * p.G + hq % p.G;
-    const uint32_t tiles = plan.tiles(len);
-    const uint32_t u0 = before + (static_cast<uint32_t>(hq / p.G) * plan.blocks(rows.n) +
-                                  static_cast<uint32_t>(in_head / block_rows)) * tiles;
-    r = in_head % block_rows;
-    const Deal deal(shared.total, p.ctas);
-    if (t - rows.first < rows.n && u0 + tiles <= shared.total) {
-      first = static_cast<int>(deal.run_of(u0));
-      n = static_cast<int>(deal.run_of(u0 + tiles - 1)) - first + 1;
-      starts = deal.start(first) <= u0;
+  const PlanPlace at = plan.place<256>(shared, blockIdx.x + 1, p.ctas);
+  const Deal deal(at.total, p.ctas);
+  uint32_t x0 = 0, c0 = 0, parts = 0;
+  int row0 = 0, rows = 0, h = 0, block = 0;
+  if (at.b < p.c.B) {
+    const Rows r = request_rows(p.c, at.b);
+    const uint32_t cost = plan.tiles(clamp_len(p.c, at.b)) + kBlockCost;
+    const uint32_t item = at.in_request / cost;
+    x0 = at.first - at.in_request % cost;
+    if (at.first > x0 && deal.start(blockIdx.x) <= x0) {
+      const int blocks = plan.blocks(r.n);
+      h = static_cast<int>(item) / blocks;
+      block = static_cast<int>(item) % blocks;
+      row0 = r.first;
+      rows = min(block_rows, r.n * p.G - block * block_rows);
+      // its parts: CTAs that have keys of it, behind its first kBlockCost units
+      c0 = blockIdx.x;
+      while (deal.start(c0 + 1) <= x0 + kBlockCost) ++c0;
+      uint32_t c1 = c0;
+      while (deal.start(c1 + 1) < x0 + cost) ++c1;
+      parts = c1 - c0 + 1;
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  auto state = [&](int i) {
-    return (static_cast<size_t>(first + i) * 2 + (i == 0 && starts ? 1 : 0)) * block_rows + r;
-  };
-  State<D> sum;
-  float top = -CUDART_INF_F;
-  if (n > 1) {
-    for (int i = part + W * lane; i < n; i += 32 * W) top = fmaxf(top, p.part_ml[state(i)].x);
+  if (parts < 2) return;  // (the same for the whole block)
+  const int groups = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;  // of warps, a row each
+  const int share = 8 / groups, part = warp % share;
+  for (int first = 0; first < rows; first += groups) {
+    const int r = first + warp / share;
+    State<D> sum;
+    float top = -CUDART_INF_F;
+    if (r < rows) {
+      // (a part that holds the item's first key is in the CTA's slot 1)
+      auto state = [&](uint32_t i) {
+        return (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * block_rows + r;
+      };
+      for (uint32_t i = lane; i < parts; i += 32) top = fmaxf(top, p.part_ml[state(i)].x);
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
 #pragma unroll 4
-    for (int i = part; i < n; i += W) sum.add(p.part_ml[state(i)], top, p.part_o + state(i) * D, lane);
+      for (uint32_t i = part; i < parts; i += share)
+        sum.add(p.part_ml[state(i)], top, p.part_o + state(i) * D, lane);
+    }
+    if (share > 1) {
+      sum.store(sums[warp], lane);
+      if (lane == 0) tops[warp] = make_float2(top, sum.l);
+      __syncthreads();
+      if (part == 0 && r < rows)
+        for (int i = 1; i < share; ++i) sum.add(tops[warp + i], top, sums[warp + i], lane);
+    }
+    if (part == 0 && r < rows) {
+      const int row = block * block_rows + r;
+      sum.finish(p, row0 + row / p.G, h * p.G + row % p.G, top, lane);
+    }
   }
-  if constexpr (W > 1) {
-    sum.store(sums[warp], lane);
-    if (lane == 0) tops[warp] = make_float2(top, sum.l);
-    __syncthreads();
-    if (part > 0) return;
-    State<D> all;
-#pragma unroll
-    for (int i = 0; i < W; ++i) top = fmaxf(top, tops[warp + i].x);
-#pragma unroll
-    for (int i = 0; i < W; ++i) all.add(tops[warp + i], top, sums[warp + i], lane);
-    sum = all;
-  }
-  if (n > 1) sum.finish(p, t, hq, top, lane);
 }
 
 template <int D, bool kQuant, int NT>
@@ -611,11 +642,10 @@ cudaError_t launch_stream(const PagedParams& p, int dev, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <int D, int W>
+template <int D>
 cudaError_t launch_merge(const PagedParams& p, int rows, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  const long long all = static_cast<long long>(p.c.T) * p.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((all + 8 / W - 1) / (8 / W)));
+  cfg.gridDim = dim3(p.ctas - 1);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -623,10 +653,14 @@ cudaError_t launch_merge(const PagedParams& p, int rows, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, W>, p, rows);
+  return cudaLaunchKernelEx(&cfg, stream_merge_kernel<D>, p, rows);
 }
 
 }  // namespace
+
+unsigned paged_stream_ctas(const PagedParams& p, int rows) {
+  return p.c.quant && rows == 8 ? 2 : 1;
+}
 
 size_t paged_stream_scratch(const PagedParams& p, int rows, size_t* ml_at) {
   *ml_at = static_cast<size_t>(p.ctas) * 2 * rows * p.c.D * sizeof(float);
@@ -643,10 +677,8 @@ cudaError_t launch_paged_stream(const PagedParams& p, int rows, int dev, cudaStr
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   cudaError_t e = table[p.c.D == 128][p.c.quant][rows == 16](p, dev, stream);
   if (e != cudaSuccess) return e;
-  const bool wide = static_cast<long long>(p.c.T) * p.Hq <= 4096;
-  if (p.c.D == 128)
-    return wide ? launch_merge<128, 4>(p, rows, stream) : launch_merge<128, 1>(p, rows, stream);
-  return wide ? launch_merge<64, 4>(p, rows, stream) : launch_merge<64, 1>(p, rows, stream);
+  if (p.ctas < 2) return cudaSuccess;
+  return p.c.D == 128 ? launch_merge<128>(p, rows, stream) : launch_merge<64>(p, rows, stream);
 }
 
 }  // namespace attn

@@ -40,7 +40,7 @@ template <int D, bool kQuant>
 struct TileCfg {
   static constexpr int kThreads = kQuant ? 768 : 640;
   // setmaxnreg: 4 softmax warpgroups and 1 or 2 others, out of what the launch gets
-  static constexpr uint32_t kRegSoftmax = kQuant ? 104 : 112, kRegOther = 32;
+  static constexpr uint32_t kRegSoftmax = kQuant ? 96 : 112, kRegOther = kQuant ? 48 : 32;
   static constexpr int kReaders = kQuant ? 21 : 17;  // of an item, besides the loader
   static constexpr int kTileBytes = kBM * D * 2, kChunks = D / 64;
   static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
@@ -132,8 +132,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     paged_tile_kernel(const __grid_constant__ PagedParams p) {
   using C = TileCfg<D, kQuant>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   __shared__ TileShared<kQuant> ms;
   static_assert(C::kSmem + sizeof(ms) <= 227 * 1024, "shared memory");
   const uint32_t abort_flag = smem_u32(&ms.abort_flag);
@@ -567,7 +566,21 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     reg_dealloc<C::kRegOther>();
     if (kQuant && warp >= kWarpConvert) {
       // ---- quantised tiles to bf16 ones, rows behind the last token to zeros
+      // A thread has the same 16 elements of every kStep-th row.  The lanes of a row's two
+      // halves store their 16-byte pieces in opposite order, so that no two of eight
+      // lanes meet in a bank.
       const int tid = threadIdx.x - kWarpConvert * 32;
+      constexpr int kPieces = D / 16, kStep = 128 / kPieces, kRounds = kBN / kStep;
+      const int row0 = tid / kPieces, piece = tid % kPieces;
+      const bool hi = piece >= kPieces / 2;
+      uint8_t* const dst = smem + C::kOffKV + (piece >> 2) * (kBN * 128) + row0 * 128;
+      const uint32_t at0 = (((piece * 2) & 7) ^ (row0 & 7)) << 4;
+      auto store = [&](uint8_t* to, const uint32_t (&y)[8]) {
+        *reinterpret_cast<uint4*>(to + (hi ? at0 ^ 16u : at0)) =
+            hi ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(to + (hi ? at0 : at0 ^ 16u)) =
+            hi ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(y[4], y[5], y[6], y[7]);
+      };
       uint32_t raw = 0, raw_round = 0, slot = 0, round = 0;
       Item it;
       bool ok = true;
@@ -581,45 +594,39 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
                                   kErrWaitLoad, p.wait_limit_ns));
           if (!ok) break;
           const uint32_t bad = ms.raw_bad[raw];
-          const uint8_t* codes = smem + C::kOffRaw + raw * C::kRawBytes;
+          const uint8_t* codes = smem + C::kOffRaw + raw * C::kRawBytes + tid * 16;
           const uint8_t* scales = smem + C::kOffScale + raw * kBN;
-          uint8_t* tile = smem + C::kOffKV + slot * C::kTileBytes;
-          constexpr int kPieces = D / 16;  // of 16 codes in a row
-#pragma unroll 2
-          for (int q = tid; q < kBN * kPieces; q += 128) {
-            const int row = q / kPieces, piece = q % kPieces;
-            uint4 x = *reinterpret_cast<const uint4*>(codes + q * 16);
-            uint32_t scale = scales[row];
-            if (key0 + row >= it.len || (bad >> (row / p.c.page) & 1u)) {
-              x = make_uint4(0, 0, 0, 0);
-              scale = 127;
-            }
-            const uint32_t f = e4m3_factor(scale), w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // bytes 0 2 and 1 3, then in order
-              const uint32_t a = e4m3_pair(w[e] << 8, f), b = e4m3_pair(w[e], f);
-              y[2 * e] = __byte_perm(a, b, 0x5410);
-              y[2 * e + 1] = __byte_perm(a, b, 0x7632);
-            }
-            if (__any_sync(0xFFFFFFFFu, scale > kScaleMost && scale != kScaleNan)) {
+          uint8_t* to = dst + slot * C::kTileBytes;
+          // rows that are not there, and scales beyond one factor, or NaN: rare
+          const uint32_t most = __vcmpgtu4(reinterpret_cast<const uint32_t*>(scales)[lane],
+                                           kScaleMost * 0x01010101u);
+          if (key0 + kBN > it.len || bad || __any_sync(0xFFFFFFFFu, most != 0)) {
+#pragma unroll 1
+            for (int q = 0; q < kRounds; ++q) {
+              const int row = row0 + q * kStep;
+              uint4 x = *reinterpret_cast<const uint4*>(codes + q * 2048);
+              uint32_t scale = scales[row];
+              if (key0 + row >= it.len || (bad >> (row / p.c.page) & 1u)) {
+                x = make_uint4(0, 0, 0, 0);
+                scale = 127;
+              }
+              uint32_t y[8];
+              e4m3_row16(x, e4m3_factor(scale), y);
               const uint32_t rest =
                   (max(scale == kScaleNan ? 0u : scale, kScaleMost) - kScaleMost + 127u) << 7;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y[e]) : "r"(rest * 0x10001u));
+              store(to + q * (kStep * 128), y);
             }
-            // (the lanes of the row's halves store their two pieces in opposite order:
-            // no two of eight lanes in the same banks)
-            const int hi = piece / (kPieces / 2) & 1;
-            const uint32_t at16 = static_cast<uint32_t>(piece * 2);
-            uint8_t* dst = tile + (at16 >> 3) * (kBN * 128) + row * 128;
-            const uint32_t a0 = ((at16 & 7) ^ (row & 7)) << 4, a1 = a0 ^ 16;
-            *reinterpret_cast<uint4*>(dst + (hi ? a1 : a0)) =
-                hi ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(dst + (hi ? a0 : a1)) =
-                hi ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(y[4], y[5], y[6], y[7]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < kRounds; ++q) {
+              const uint4 x = *reinterpret_cast<const uint4*>(codes + q * 2048);
+              uint32_t y[8];
+              e4m3_row16(x, (scales[row0 + q * kStep] + 120u) * 0x00800080u, y);
+              store(to + q * (kStep * 128), y);
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();

@@ -451,8 +451,9 @@ int attn_decode_prefix(const void *q, const void *kprefix, const void *vprefix,
  * 2^e, e the least integer with a <= 448 * 2^e but at least -100 and at most 100
  * (0 for a row of zeros), held as the byte e + 127, and the codes e4m3(x / 2^e),
  * rounded to nearest even and saturating.  code * 2^e is exact in bf16.  A row that
- * holds a NaN has the byte 255 and stands for NaN.  (Of codes that came about
- * otherwise, 0x7F and 0xFF, e4m3's NaN, are read as +-480 by the attention calls.)
+ * holds a NaN has the byte 255 and stands for NaN.  Other
+ * codes that are NaN (0x7F, 0xFF) and other scale bytes do not come about so, and
+ * what the calls make of them is not specified.
  *
  * Limits: 1 <= B <= 65536, 0 <= T <= 2^24, Hkv <= 65535, D in {64, 128},
  * P * Hkv < 2^31, M * page <= 2^21; strides (elements from one token to the next)
@@ -503,7 +504,7 @@ int attn_cache_read(const void *kpages, const void *vpages, const unsigned char 
  *
  * Limits: Hq % Hkv == 0, Hq <= 65535, Hq / Hkv <= 128, max_new >= 0; scale finite and
  * >= 0; the rows times the keys in units of work within 32 bits:
- * (T * Hq / Hkv / 8 + B) * Hkv * (M * page / 64 + 1) < 2^31.  Scratch as
+ * (T * Hq / Hkv / 8 + B) * Hkv * (M * page / 64 + 3) < 2^31.  Scratch as
  * attn_decode_varlen.
  */
 int attn_paged_fwd(const void *q, long long q_stride, const void *kpages, const void *vpages,
