@@ -252,6 +252,14 @@ struct CacheRows {
 cudaError_t launch_cache_rows(const PagedArrays& c, const CacheRows& r, bool read,
                               cudaStream_t stream);
 
+// An item that was cut, written by the CTA that has its first part: the parts are that
+// CTA's state 1 and state 0 of the `parts` - 1 CTAs behind it.
+struct PagedCut {
+  int parts;       // 0: none begins in this CTA
+  int row0, left;  // first dense row; tokens of the request from there on
+  int h, first;    // KV head; number of the item's first row among that token's and its next
+};
+
 // Attention of new tokens over a paged cache.
 struct PagedParams {
   CUtensorMap tmap_k, tmap_v;  // pages as [P * Hkv, page, D], box {128 bytes, rows, 1}
@@ -266,15 +274,16 @@ struct PagedParams {
   unsigned ctas;       // of the split kernel
   float* part_o;       // partial states: [slot, rows of a block, D], and their
   float2* part_ml;     // maximum (log2 units) and sum
+  PagedCut* cuts;      // of every CTA
   unsigned int* err;
   uint64_t wait_limit_ns;
 };
 // The kernel for few rows, and what its scratch takes.
 unsigned paged_stream_ctas(const PagedParams& p, int rows);  // per SM
-size_t paged_stream_scratch(const PagedParams& p, int rows, size_t* ml_at);
+size_t paged_stream_state(const PagedParams& p, int rows);  // rows of partial states
 cudaError_t launch_paged_stream(const PagedParams& p, int rows, int dev, cudaStream_t stream);
 // The kernel for many rows, likewise.
-size_t paged_tile_scratch(const PagedParams& p, size_t* ml_at);
+size_t paged_tile_state(const PagedParams& p);
 cudaError_t launch_paged_tile(const PagedParams& p, int dev, cudaStream_t stream);
 // Tensor map over pages; box: rows of a page per copy.
 int encode_pages(CUtensorMap* map, const void* base, const PagedArrays& c, int box);

@@ -50,12 +50,13 @@ int check_stride(long long stride, int heads, int D) {
 struct PagedLaunch {
   PagedParams* p;
   int rows, dev;  // rows: of a block of the kernel for few rows; 0: the one for many
-  size_t ml_at;
+  size_t states;  // rows of partial states
 };
 int launch_paged(void* ctx, void* scratch, cudaStream_t stream) {
   const PagedLaunch& l = *static_cast<PagedLaunch*>(ctx);
   l.p->part_o = static_cast<float*>(scratch);
-  l.p->part_ml = reinterpret_cast<float2*>(static_cast<char*>(scratch) + l.ml_at);
+  l.p->part_ml = reinterpret_cast<float2*>(l.p->part_o + l.states * l.p->c.D);
+  l.p->cuts = reinterpret_cast<PagedCut*>(l.p->part_ml + l.states);
   const cudaError_t e = l.rows ? launch_paged_stream(*l.p, l.rows, l.dev, stream)
                                : launch_paged_tile(*l.p, l.dev, stream);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
@@ -108,8 +109,9 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
   p.err = di.err_word;
   p.wait_limit_ns = wait_limit_ns();
   l.dev = di.dev;
-  const size_t bytes = many ? paged_tile_scratch(p, &l.ml_at)
-                            : paged_stream_scratch(p, l.rows, &l.ml_at);
+  l.states = many ? paged_tile_state(p) : paged_stream_state(p, l.rows);
+  const size_t bytes =
+      l.states * (c.D * sizeof(float) + sizeof(float2)) + p.ctas * sizeof(PagedCut);
   return with_scratch(bytes, di.dev, stream, launch_paged, &l);
 }
 

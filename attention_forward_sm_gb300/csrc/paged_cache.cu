@@ -11,8 +11,8 @@
 // and comes back as NaN.
 //
 // Bound by memory.  A lane moves 8 elements of a row and D / 8 lanes a row, so that
-// a row is one run of whole sectors on either side; a CTA takes kTokens tokens, whose
-// pages are looked up once, by a warp each, ahead of the rows.
+// a row is one run of whole sectors on either side; a CTA takes up to kTokens tokens,
+// whose pages are looked up once, by a warp each, ahead of the rows.
 #include <cuda_fp16.h>
 
 #include "../../include/attn.h"
@@ -22,7 +22,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 16;  // tokens per CTA
+constexpr int kTokens = 16;  // tokens per CTA, at most
 
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 x;
@@ -80,14 +80,14 @@ __device__ __forceinline__ uint4 dequantise(const uint2& q, uint32_t scale) {
 
 template <int D, bool kQuant, bool kRead>
 __global__ void __launch_bounds__(kThreads)
-    cache_rows_kernel(const PagedArrays c, const CacheRows r) {
+    cache_rows_kernel(const PagedArrays c, const CacheRows r, int tokens) {
   constexpr int kLanes = D / 8;               // of a row
   constexpr int kGroups = kThreads / kLanes;  // rows at a time
   constexpr int kAhead = 4;                   // of them in flight
   __shared__ int2 where[kTokens];             // (page, slot); page -1: none, -2: no such row
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t0 = static_cast<int>(blockIdx.x) * kTokens;
-  for (int i = warp; i < kTokens; i += kThreads / 32) {
+  const int t0 = static_cast<int>(blockIdx.x) * tokens;
+  for (int i = warp; i < tokens; i += kThreads / 32) {
     const int t = t0 + i;
     int2 at = make_int2(-2, 0);
     const int b = t < c.T ? find_request(c, t, lane) : -1;
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
 
   const int heads = 2 * c.Hkv;  // of K, then of V
-  const int rows = min(kTokens, c.T - t0) * heads;
+  const int rows = min(tokens, c.T - t0) * heads;
   const int e0 = (threadIdx.x % kLanes) * 8;
   const bool first_lane = threadIdx.x % kLanes == 0;
   for (int i0 = threadIdx.x / kLanes; i0 < (rows + kGroups - 1) / kGroups * kGroups;
@@ -173,8 +173,10 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int D, bool kQuant, bool kRead>
 cudaError_t launch(const PagedArrays& c, const CacheRows& r, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((c.T + kTokens - 1) / kTokens);
-  cache_rows_kernel<D, kQuant, kRead><<<grid, kThreads, 0, stream>>>(c, r);
+  // a few CTAs for every SM before they take more tokens each
+  const int tokens = min(max(c.T / 1024, 1), kTokens);
+  const unsigned grid = static_cast<unsigned>((c.T + tokens - 1) / tokens);
+  cache_rows_kernel<D, kQuant, kRead><<<grid, kThreads, 0, stream>>>(c, r, tokens);
   return cudaGetLastError();
 }
 

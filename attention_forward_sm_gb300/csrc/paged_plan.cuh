@@ -110,15 +110,32 @@ struct StreamPlan {
 // their sums have closed forms and nothing about them is stored.
 constexpr int kTileKeys = 128;
 constexpr int kItemCost = 256;
+constexpr int kLeastShare = 512;  // of a CTA: none is left without a key tile of an item that
+                                  // reaches into the next one
 
 struct CostShared {
   long long warp_sum[24];
   long long total, rest;
   int b;
 };
+// The line of all costs in `runs` equal stretches.
+struct CostDeal {
+  long long each;
+  unsigned runs, more;
+  __device__ CostDeal() {}
+  __device__ CostDeal(long long total, unsigned ctas) {
+    runs = total >= static_cast<long long>(ctas) * kLeastShare
+               ? ctas
+               : max(1u, static_cast<unsigned>(total) / kLeastShare);
+    each = total / runs;
+    more = static_cast<unsigned>(total - each * runs);
+  }
+  __device__ long long start(unsigned r) const { return each * r + more * r / runs; }
+};
 struct CostPlace {
-  long long total, first, end;  // of the whole line, of this CTA
-  long long rest;               // first's distance from the start of request b, which holds it
+  CostDeal deal;
+  long long first, end;  // of this CTA
+  long long rest;        // first's distance from the start of request b, which holds it
   int b;
 };
 struct CostItem {
@@ -152,9 +169,6 @@ struct CostPlan {
     const Rows rows = request_rows(c, b);
     return rows.n > 0 ? c.Hkv * head(rows.n, clamp_len(c, b)) : 0;
   }
-  __device__ long long start(long long total, unsigned cta, unsigned ctas) const {
-    return total / ctas * cta + total % ctas * cta / ctas;
-  }
   // Where CTA `cta` of `ctas` begins and ends; all kThreads threads call this.
   template <int kThreads>
   __device__ CostPlace place(CostShared& sh, unsigned cta, unsigned ctas) const {
@@ -178,10 +192,10 @@ struct CostPlan {
       total += sh.warp_sum[w];
     }
     CostPlace at;
-    at.total = total;
-    at.first = start(total, cta, ctas);
-    at.end = start(total, cta + 1, ctas);
-    if (at.first >= in_front && at.first - in_front < own) {
+    at.deal = CostDeal(total, ctas);
+    at.first = at.deal.start(cta);
+    at.end = at.deal.start(cta + 1);
+    if (cta < at.deal.runs && at.first >= in_front && at.first - in_front < own) {
       long long rest = at.first - in_front;
       int b = lo;
       for (; b < hi; ++b) {
@@ -266,6 +280,20 @@ struct State {
       o[0] = fmaf(w, x.x, o[0]);
       o[1] = fmaf(w, x.y, o[1]);
     }
+  }
+  // Adds up `parts` states, the k-th one in row state(k); returns the largest maximum.
+  // (With `step`, only every step-th of them, from `part` on.)
+  template <class F>
+  __device__ float join(const PagedParams& p, int parts, int lane, F state, int part = 0,
+                        int step = 1) {
+    float top = -CUDART_INF_F;
+    for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.part_ml[state(k)].x);
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+#pragma unroll 4
+    for (int k = part; k < parts; k += step)
+      add(p.part_ml[state(k)], top, p.part_o + state(k) * D, lane);
+    return top;
   }
   __device__ void store(float* to, int lane) const {
     if constexpr (E == 4)

@@ -176,6 +176,8 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
     bool ok = true;
     int b = at.b;
     uint32_t in_request = at.in_request;  // unit within the request
+    const Deal deal(at.total, p.ctas);
+    PagedCut cut = {};
     for (uint32_t u = at.first; u < at.end && b < p.c.B && ok;) {
       const Rows rows = request_rows(p.c, b);
       const int len = clamp_len(p.c, b);
@@ -193,6 +195,13 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
         in_request += cost;
         const int h = static_cast<int>(item) / blocks, block = static_cast<int>(item) % blocks;
         const int slot = n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tile0 == 0);
+        if (n > 0 && n < tiles && tile0 == 0) {  // goes on in the next CTAs
+          const uint32_t rest = tiles - n;  // units behind at.end
+          uint32_t last = blockIdx.x + 1;
+          while (deal.start(last + 1) < at.end + rest) ++last;
+          cut = PagedCut{static_cast<int>(last - blockIdx.x) + 1, rows.first, rows.n, h,
+                         block * kRows};
+        }
         // the teams take turns, so that both have as many units: one may be without keys
         const uint32_t both = (n + 1) & ~1u;
         for (uint32_t i = 0; i < both; ++i, ++s) {
@@ -259,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
       ++b;
       in_request = 0;
     }
+    if (lane == 0) p.cuts[blockIdx.x] = cut;
     for (int i = 0; i < 2 && ok; ++i, ++s) {
       const uint32_t st = s % kStages;
       if (warp_all(mbar_wait(&ms.empty[st], ((s / kStages) & 1u) ^ 1u, abort_flag, p.err,
@@ -559,62 +569,33 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
   }
 }
 
-// Joins the partial states of the items that were cut.  Block c: the item in which CTA
-// c + 1 begins, if that is its first cut.  The plan, which needs no result of the
-// kernel before, is found ahead of the wait for it.  Rows are few and parts may be
-// many: the warps share out rows first, then a row's parts.
+// Joins the partial states of the items that were cut, block c that whose first part
+// CTA c has.  Rows are few and parts may be many: the warps share out rows first, then
+// a row's parts.
 template <int D>
 __global__ void __launch_bounds__(256) stream_merge_kernel(const __grid_constant__ PagedParams p,
                                                            int block_rows) {
-  __shared__ PlanShared shared;
   __shared__ alignas(16) float sums[8][D];
   __shared__ float2 tops[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const StreamPlan plan(p.c, p.G, block_rows);
-  const PlanPlace at = plan.place<256>(shared, blockIdx.x + 1, p.ctas);
-  const Deal deal(at.total, p.ctas);
-  uint32_t x0 = 0, c0 = 0, parts = 0;
-  int row0 = 0, rows = 0, h = 0, block = 0;
-  if (at.b < p.c.B) {
-    const Rows r = request_rows(p.c, at.b);
-    const uint32_t cost = plan.tiles(clamp_len(p.c, at.b)) + kBlockCost;
-    const uint32_t item = at.in_request / cost;
-    x0 = at.first - at.in_request % cost;
-    if (at.first > x0 && deal.start(blockIdx.x) <= x0) {
-      const int blocks = plan.blocks(r.n);
-      h = static_cast<int>(item) / blocks;
-      block = static_cast<int>(item) % blocks;
-      row0 = r.first;
-      rows = min(block_rows, r.n * p.G - block * block_rows);
-      // its parts: CTAs that have keys of it, behind its first kBlockCost units
-      c0 = blockIdx.x;
-      while (deal.start(c0 + 1) <= x0 + kBlockCost) ++c0;
-      uint32_t c1 = c0;
-      while (deal.start(c1 + 1) < x0 + cost) ++c1;
-      parts = c1 - c0 + 1;
-    }
-  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (parts < 2) return;  // (the same for the whole block)
+  const PagedCut cut = p.cuts[blockIdx.x];
+  if (cut.parts == 0) return;
+  const int rows = min(block_rows, cut.left * p.G - cut.first);
   const int groups = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;  // of warps, a row each
   const int share = 8 / groups, part = warp % share;
-  for (int first = 0; first < rows; first += groups) {
-    const int r = first + warp / share;
+  for (int from = 0; from < rows; from += groups) {
+    const int r = from + warp / share;
     State<D> sum;
     float top = -CUDART_INF_F;
-    if (r < rows) {
-      // (a part that holds the item's first key is in the CTA's slot 1)
-      auto state = [&](uint32_t i) {
-        return (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * block_rows + r;
-      };
-      for (uint32_t i = lane; i < parts; i += 32) top = fmaxf(top, p.part_ml[state(i)].x);
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-#pragma unroll 4
-      for (uint32_t i = part; i < parts; i += share)
-        sum.add(p.part_ml[state(i)], top, p.part_o + state(i) * D, lane);
-    }
-    if (share > 1) {
+    if (r < rows)
+      top = sum.join(
+          p, cut.parts, lane,
+          [&](int k) {
+            return (static_cast<size_t>(blockIdx.x + k) * 2 + (k == 0)) * block_rows + r;
+          },
+          part, share);
+    if (share > 1) {  // (then there is one turn)
       sum.store(sums[warp], lane);
       if (lane == 0) tops[warp] = make_float2(top, sum.l);
       __syncthreads();
@@ -622,8 +603,8 @@ __global__ void __launch_bounds__(256) stream_merge_kernel(const __grid_constant
         for (int i = 1; i < share; ++i) sum.add(tops[warp + i], top, sums[warp + i], lane);
     }
     if (part == 0 && r < rows) {
-      const int row = block * block_rows + r;
-      sum.finish(p, row0 + row / p.G, h * p.G + row % p.G, top, lane);
+      const int row = cut.first + r;
+      sum.finish(p, cut.row0 + row / p.G, cut.h * p.G + row % p.G, top, lane);
     }
   }
 }
@@ -662,9 +643,8 @@ unsigned paged_stream_ctas(const PagedParams& p, int rows) {
   return p.c.quant && rows == 8 ? 2 : 1;
 }
 
-size_t paged_stream_scratch(const PagedParams& p, int rows, size_t* ml_at) {
-  *ml_at = static_cast<size_t>(p.ctas) * 2 * rows * p.c.D * sizeof(float);
-  return *ml_at + static_cast<size_t>(p.ctas) * 2 * rows * sizeof(float2);
+size_t paged_stream_state(const PagedParams& p, int rows) {
+  return static_cast<size_t>(p.ctas) * 2 * rows;
 }
 
 cudaError_t launch_paged_stream(const PagedParams& p, int rows, int dev, cudaStream_t stream) {

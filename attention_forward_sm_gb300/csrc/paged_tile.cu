@@ -370,11 +370,19 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     CostWalk walk(plan, at);
     Item it;
     int slot_first = 0;
+    PagedCut cut = {};
     while (ok && walk.next(&it, &slot_first)) {
       if (!warp_all(mbar_wait(&ms.item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort_flag, p.err,
                               kErrWaitLoad, p.wait_limit_ns))) {
         ok = false;
         break;
+      }
+      if (slot_first == 1) {  // the CTA's last item, which goes on in the next ones
+        const long long end = walk.item.x0 + min(walk.item.cost,
+                                                 kItemCost + walk.item.n_kv * 1ll * kTileKeys);
+        unsigned last = blockIdx.x + 1;
+        while (at.deal.start(last + 1) < end) ++last;
+        cut = PagedCut{static_cast<int>(last - blockIdx.x) + 1, it.row0, it.left, it.h, 0};
       }
       if (lane == 0) {
         it.slot = slot_first < 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + slot_first;
@@ -458,6 +466,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
       }
       ++k;
     }
+    if (lane == 0) p.cuts[blockIdx.x] = cut;
     if (ok && warp_all(mbar_wait(&ms.item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort_flag, p.err,
                                  kErrWaitLoad, p.wait_limit_ns))) {
       if (lane == 0) {
@@ -655,64 +664,26 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
   }
 }
 
-// Joins the partial states of the items that were cut.  Block (c, y): the item in which
-// CTA c + 1 begins, if that is its first cut, and an eighth of its rows.
-constexpr int kMergeSplit = 8;
+// Joins the partial states of the items that were cut: block (c, y) some rows of the one
+// whose first part CTA c has, a warp each.
+constexpr int kMergeSplit = 16;
 
 template <int D>
 __global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__ PagedParams p) {
-  __shared__ CostShared shared;
-  __shared__ int slots[kMostCtas], count;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const CostPlan plan(p.c, p.G, p.causal);
-  const CostPlace at = plan.place<256>(shared, blockIdx.x + 1, p.ctas);
-  if (threadIdx.x == 0) count = 0;
-  __syncthreads();
-  CostItem item;
-  bool cut = at.b < p.c.B;
-  if (cut) {
-    item = plan.item(at);
-    const long long before = plan.start(at.total, blockIdx.x, p.ctas);
-    cut = item.x0 < at.first && before <= item.x0;
-  }
-  if (!cut) {  // (the same for the whole block)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  // its parts: slots in the order of the CTAs
-  if (warp == 0) {
-    int n = 0;
-    for (unsigned c0 = blockIdx.x; c0 < p.ctas; c0 += 32) {
-      const unsigned c = c0 + lane;
-      int t0 = 0, t1 = 0;
-      if (c < p.ctas) {
-        t0 = plan.cut(item, plan.start(at.total, c, p.ctas) - item.x0);
-        t1 = plan.cut(item, plan.start(at.total, c + 1, p.ctas) - item.x0);
-      }
-      const uint32_t has = __ballot_sync(0xFFFFFFFFu, t1 > t0);
-      if (t1 > t0) slots[n + __popc(has & ((1u << lane) - 1u))] = 2 * static_cast<int>(c) + (t0 == 0);
-      n += __popc(has);
-      if (__shfl_sync(0xFFFFFFFFu, t0, 31) >= item.n_kv) break;
-    }
-    if (lane == 0) count = n;
-  }
-  __syncthreads();
-  const int n = count;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (n < 2) return;  // in one CTA after all
+  const PagedCut cut = p.cuts[blockIdx.x];
+  if (cut.parts == 0) return;
   const int per_tile = kBM / p.G, in_tile = per_tile * p.G;
-  const int rows = min(2 * per_tile, item.left) * p.G;
+  const int rows = min(2 * per_tile, cut.left) * p.G;
   for (int i = static_cast<int>(blockIdx.y) * 8 + warp; i < rows; i += 8 * kMergeSplit) {
     const int t = i / in_tile, r = t * kBM + i % in_tile;
-    auto state = [&](int k) { return static_cast<size_t>(slots[k]) * (2 * kBM) + r; };
-    float top = -CUDART_INF_F;
-    for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_ml[state(k)].x);
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    auto state = [&](int k) {
+      return (static_cast<size_t>(blockIdx.x + k) * 2 + (k == 0)) * (2 * kBM) + r;
+    };
     State<D> sum;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) sum.add(p.part_ml[state(k)], top, p.part_o + state(k) * D, lane);
-    sum.finish(p, item.row0 + i / p.G, item.h * p.G + i % p.G, top, lane);
+    const float top = sum.join(p, cut.parts, lane, state);
+    sum.finish(p, cut.row0 + i / p.G, cut.h * p.G + i % p.G, top, lane);
   }
 }
 
@@ -730,7 +701,7 @@ cudaError_t launch_tile(const PagedParams& p, int dev, cudaStream_t stream) {
   if (cudaError_t e = cudaGetLastError()) return e;
   if (p.ctas < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas - 1, kMergeSplit);
+  cfg.gridDim = dim3(p.ctas - 1, kMergeSplit);  // (the last CTA's items end there)
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -743,10 +714,7 @@ cudaError_t launch_tile(const PagedParams& p, int dev, cudaStream_t stream) {
 
 }  // namespace
 
-size_t paged_tile_scratch(const PagedParams& p, size_t* ml_at) {
-  *ml_at = static_cast<size_t>(p.ctas) * 2 * (2 * kBM) * p.c.D * sizeof(float);
-  return *ml_at + static_cast<size_t>(p.ctas) * 2 * (2 * kBM) * sizeof(float2);
-}
+size_t paged_tile_state(const PagedParams& p) { return static_cast<size_t>(p.ctas) * 2 * 2 * kBM; }
 
 cudaError_t launch_paged_tile(const PagedParams& p, int dev, cudaStream_t stream) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;

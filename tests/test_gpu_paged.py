@@ -310,3 +310,29 @@ def _only(c, b):
     d = copy.copy(c)
     d.lens, d.dense = [c.lens[b]], [c.dense[b]]
     return d
+
+
+@pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,new", [(1, 1), (8, 1), (16, 1), (4, 4)])
+def test_long_contexts(quant, D, G, new):
+    """So many keys that every CTA goes around its ring many times, next to short requests."""
+    lens = [90001, 5, 4, 16384, 900]
+    c = ref.Cache(lens, 8, D, 128, quant, seed=12)
+    offsets = ref.offsets_of([new] * len(lens))
+    q = _randn((new * len(lens), 8 * G, D), 15)
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
+    check_attention(o, lse, q, c, offsets)
+
+
+@pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,new", [([9000, 700], [300, 650]), ([2500] * 9, [1] * 8 + [200]),
+                                      ([700, 3], [900, 5])])
+def test_long_chunks(quant, D, lens, new):
+    """Items that are cut between CTAs, at any place."""
+    c = ref.Cache(lens, 8, D, 64, quant, seed=13)
+    offsets = ref.offsets_of(new)
+    q = _randn((sum(new), 24, D), 16)
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=max(new), **c.scales())
+    check_attention(o, lse, q, c, offsets)
