@@ -239,6 +239,7 @@ struct PagedArrays {
   const int* offsets;  // [B + 1] rows of the new tokens; NULL: row b is request b's one
   int B, T, Hkv, D, page, P, M;  // T: rows of the dense tensors
   int quant;
+  int page_bits;  // page = 1 << page_bits: the loading warps have no time for divisions
 };
 // Dense rows that go into the cache (k, v) or come out of it (k_out, v_out, [T, Hkv, D]).
 struct CacheRows {

@@ -56,7 +56,7 @@ __device__ __forceinline__ int find_request(const PagedArrays& c, int t, int lan
 
 // Page that holds position pos of request b, or -1.
 __device__ __forceinline__ int page_of(const PagedArrays& c, int b, int pos) {
-  const int id = c.table[static_cast<size_t>(b) * c.M + pos / c.page];
+  const int id = c.table[static_cast<size_t>(b) * c.M + (pos >> c.page_bits)];
   return static_cast<unsigned>(id) < static_cast<unsigned>(c.P) ? id : -1;
 }
 
@@ -89,6 +89,25 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
   return h;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Bits of the larger magnitude of two bf16; both to f16, times f.
+__device__ __forceinline__ uint32_t bf16x2_top(uint32_t x) {
+  return max(x << 16 & 0x7FFFFFFFu, x & 0x7FFFFFFFu);
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x, float f) {
+  return pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f);
+}
+// The two lower and the two upper of four codes.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  return e4m3x2_to_f16x2(static_cast<uint16_t>(x));
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  return e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16));
 }
 // 2^e and e of a scale byte; NaN for the one that says so.
 __device__ __forceinline__ float scale_value(uint32_t scale) {

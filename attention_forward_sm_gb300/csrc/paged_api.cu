@@ -36,7 +36,8 @@ int paged_arrays(const void* kpages, const void* vpages, const unsigned char* ks
     if (misaligned(x, 4)) return ATTN_ERR_ALIGN;
   *c = PagedArrays{const_cast<void*>(kpages), const_cast<void*>(vpages),
                    const_cast<uint8_t*>(kscale), const_cast<uint8_t*>(vscale), table, lens, offsets,
-                   B, T, Hkv, D, page, P, M, kscale != nullptr};
+                   B, T, Hkv, D, page, P, M, kscale != nullptr,
+                   page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7};
   return ATTN_OK;
 }
 

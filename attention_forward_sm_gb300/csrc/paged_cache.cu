@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads)
       const int pos = clamp_len(c, b) - rows.n + (t - rows.first);
       at = make_int2(-1, 0);
       if (pos >= 0 && t - rows.first < rows.n) {
-        at = make_int2(page_of(c, b, pos), pos % c.page);
+        at = make_int2(page_of(c, b, pos), pos & (c.page - 1));
         if (at.x < 0 && lane == 0) atomicOr(r.err, kErrPage);
       }
     }

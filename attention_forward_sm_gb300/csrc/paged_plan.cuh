@@ -114,7 +114,7 @@ constexpr int kLeastShare = 512;  // of a CTA: none is left without a key tile o
                                   // reaches into the next one
 
 struct CostShared {
-  long long warp_sum[24];
+  long long warp_sum[32];
   long long total, rest;
   int b;
 };

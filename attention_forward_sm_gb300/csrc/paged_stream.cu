@@ -91,18 +91,6 @@ __device__ __forceinline__ void mma_16n8k16(float (&d)[4], uint32_t a0, uint32_t
     ATTN_MMA_16N8K16("bf16");
 #undef ATTN_MMA_16N8K16
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// The two lower and the two upper of four codes.
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
-  return e4m3x2_to_f16x2(static_cast<uint16_t>(x));
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
-  return e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16));
-}
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -170,7 +158,8 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
 
   if (warp == kWarps) {
     // ---- loading warp
-    const int box = min(p.c.page, kUnitKeys);
+    const int box_bits = min(p.c.page_bits, 6), box = 1 << box_bits;
+    static_assert(kUnitKeys == 64, "box_bits");
     const uint64_t policy = l2_policy_evict_first();
     uint32_t s = 0;
     bool ok = true;
@@ -208,17 +197,17 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
           const int key0 = static_cast<int>(tile0 + i) * kUnitKeys;
           const uint32_t st = s % kStages;
           // pages of this unit: lane l holds entry pbase + l of the table's row
-          const int page0 = key0 / p.c.page;
+          const int page0 = key0 >> p.c.page_bits;
           const int keys = i < n ? min(kUnitKeys, len - key0) : 0;
-          const int n_box = (max(0, keys) + box - 1) / box;
-          const int page1 = (key0 + max(n_box - 1, 0) * box) / p.c.page;
+          const int n_box = (max(0, keys) + box - 1) >> box_bits;
+          const int page1 = (key0 + (max(n_box - 1, 0) << box_bits)) >> p.c.page_bits;
           if (page0 < pbase || page1 >= pbase + 32) {
             pbase = page0;
             ids = pbase + lane < p.c.M ? p.c.table[static_cast<size_t>(b) * p.c.M + pbase + lane]
                                        : -1;
           }
           const int key = key0 + lane * box;
-          const int id = __shfl_sync(0xFFFFFFFFu, ids, (key / p.c.page - pbase) & 31);
+          const int id = __shfl_sync(0xFFFFFFFFu, ids, ((key >> p.c.page_bits) - pbase) & 31);
           if (!warp_all(mbar_wait(&ms.empty[st], ((s / kStages) & 1u) ^ 1u, abort_flag, p.err,
                                   kErrWaitLoad, p.wait_limit_ns))) {
             ok = false;
@@ -246,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
           __syncwarp();
           if (lane < n_box) {
             const int z = good ? id * p.c.Hkv + h : p.c.P * p.c.Hkv;
-            const int y = key % p.c.page;
+            const int y = key & (p.c.page - 1);
             uint8_t* dst = smem + st * (2 * C::kTile) + lane * box * (kRowBytes < 128 ? 64 : 128);
             constexpr int kPieces = kRowBytes / 128 > 0 ? kRowBytes / 128 : 1;
             constexpr int kElems = kQuant ? 128 : 64;  // of a 128-byte piece
@@ -335,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
           uint32_t top = 0;
 #pragma unroll
           for (int i = 0; i < 2 * kSteps; ++i)
-            top = max(top, max(qf[nt][i] << 16 & 0x7FFFFFFFu, qf[nt][i] & 0x7FFFFFFFu));
+            top = max(top, bf16x2_top(qf[nt][i]));
           top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
           top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
           const uint32_t e = min(max(top >> 23, 1u), 253u);
@@ -343,8 +332,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
           const float inv = __uint_as_float((254u - e) << 23);
 #pragma unroll
           for (int i = 0; i < 2 * kSteps; ++i)
-            qf[nt][i] = pack_f16x2(__uint_as_float(qf[nt][i] << 16) * inv,
-                                   __uint_as_float(qf[nt][i] & 0xFFFF0000u) * inv);
+            qf[nt][i] = bf16x2_to_f16x2(qf[nt][i], inv);
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {

@@ -38,18 +38,25 @@ constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpConvert = 20;
 
 template <int D, bool kQuant>
 struct TileCfg {
+  static constexpr int kConvert = 4;  // warps that convert
   static constexpr int kThreads = kQuant ? 768 : 640;
   // setmaxnreg: 4 softmax warpgroups and 1 or 2 others, out of what the launch gets
   static constexpr uint32_t kRegSoftmax = kQuant ? 96 : 112, kRegOther = kQuant ? 48 : 32;
   static constexpr int kReaders = kQuant ? 21 : 17;  // of an item, besides the loader
   static constexpr int kTileBytes = kBM * D * 2, kChunks = D / 64;
-  static constexpr int kStages = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
-  static constexpr int kRaw = 4;  // quantised tiles in the ring, and their size
-  static constexpr int kRawBytes = kBN * D;
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  // Quantised tiles in a ring of their own, their scales (K: and those of V) behind.
+  // Two, one of K and one of V: with four there would be room for three converted ones at
+  // D = 128, and K_j+1 would wait for K_j's place (490 us, with two 460).
+  static constexpr int kRaw = 2, kRawBytes = kBN * D, kScaleBytes = 2 * kBN;
   static constexpr int kOffKV = 2 * kTileBytes;
   static constexpr int kOffRaw = kOffKV + kStages * kTileBytes;
   static constexpr int kOffScale = kOffRaw + (kQuant ? kRaw * kRawBytes : 0);
-  static constexpr int kSmem = kOffScale + (kQuant ? kRaw * kBN : 0) + 1024;
+  static constexpr int kSmem = kOffScale + (kQuant ? kRaw * kScaleBytes : 0) + 1024;
+  // bf16 operands, or f16 ones
+  static constexpr uint32_t kTypes = kQuant ? (1u << 7 | 1u << 10) : 0;
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, kBN, false) & ~kTypes;
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, true) & ~kTypes;
   static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
   static_assert(4 * 128 * kRegSoftmax + (kThreads - 512) * kRegOther <=
                     kThreads * (65536 / kThreads / 8 * 8),
@@ -113,19 +120,164 @@ struct CostWalk {
 
 template <bool kQuant>
 struct TileShared {
-  uint64_t q_full, q_empty;          // per item
+  uint64_t q_full[2], q_ready[2];    // per item of query tile t (ready: converted to f16)
+  uint64_t q_empty;                  // per item
   uint64_t s_full[2], p_full[2];     // per key tile of query tile t
   uint64_t o_done[2];                // per item of query tile t
   uint64_t mma_done;
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t raw_full[4], raw_empty[4];
+  uint64_t raw_full[2], raw_empty[2];
   uint64_t item_full[2], item_empty[2];
   Item item[2];
-  uint32_t raw_bad[4];  // copies of the tile whose page is out of range, a bit each
+  uint32_t raw_bad[2];  // copies of the tile whose page is out of range, a bit each
+  // Quantised: what the converted K and V of a key tile are to be multiplied by, as scale
+  // bytes (of the tiles i, i + 8, ...; the converting warps are three ahead at most).
+  uint2 kv_scale[8];
   CostShared plan;
   uint32_t tmem_base;
   int abort_flag;
 };
+
+// The factor 2^(scale - most) of a row among those of a tile, as f16: exact down to 2^-24,
+// 0 below (of V: a row that far below its neighbours is lost next to them).  NaN for a
+// row that stands for it.
+__device__ __forceinline__ uint32_t f16_factor(uint32_t scale, uint32_t most) {
+  const uint32_t d = most - scale;
+  const uint32_t f = d <= 14 ? (15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+  return scale == kScaleNan ? 0x7FFFu : f;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
+// The warps that make f16 operands K_0, V_0, K_1 ... of codes.  f16 holds every code, and
+// turning codes into it is one instruction for two, where bf16 takes five: with bf16
+// the schedulers had no room for them next to the softmax (1024 tokens behind 30000, 32
+// heads on 8, D 128: 460 us; without any conversion 320).  A tile's values are over the
+// largest of its scales, which the softmax puts back, and Q is converted at its start.
+template <int D, class C, class Shared, class Next>
+__device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_t* smem,
+                                        uint32_t abort_flag, Next next_item) {
+  constexpr int kThreads = 32 * C::kConvert;
+  const int tid = threadIdx.x - kWarpConvert * 32, lane = threadIdx.x & 31;
+  // A thread has the same 16 elements of every kStep-th row.  The lanes of a row's two
+  // halves store their 16-byte pieces in opposite order, so that no two of eight
+  // lanes meet in a bank.
+  constexpr int kPieces = D / 16, kStep = kThreads / kPieces, kRounds = kBN / kStep;
+  const int row0 = tid / kPieces, piece = tid % kPieces;
+  const bool hi = piece >= kPieces / 2;
+  uint8_t* const dst = smem + C::kOffKV + (piece >> 2) * (kBN * 128) + row0 * 128;
+  const uint32_t at0 = ((((piece * 2) & 7) ^ (row0 & 7)) << 4) ^ (hi ? 16u : 0u);
+  auto one = [&](uint8_t* to, const uint4& x, uint32_t f) {
+    const uint32_t w[4] = {hi ? x.z : x.x, hi ? x.w : x.y, hi ? x.x : x.z, hi ? x.y : x.w};
+    uint32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] = mul_f16x2(e4m3_lo(w[i]), f);
+      y[2 * i + 1] = mul_f16x2(e4m3_hi(w[i]), f);
+    }
+    *reinterpret_cast<uint4*>(to + at0) = make_uint4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<uint4*>(to + (at0 ^ 16u)) = make_uint4(y[4], y[5], y[6], y[7]);
+  };
+  // The largest of a tile's scales, and whether all are within 14 of it and there is
+  // nothing odd: then every factor is a normal f16 number.
+  auto largest = [&](const uint8_t* scales, bool whole, int rows, uint32_t bad, bool* plain) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(scales)[lane];
+    const uint32_t s0 = w & 255u, s1 = w >> 8 & 255u, s2 = w >> 16 & 255u, s3 = w >> 24;
+    uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(max(s0, s1), max(s2, s3)));
+    const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(min(s0, s1), min(s2, s3)));
+    *plain = whole && most != kScaleNan && most - least <= 14;
+    if (!*plain) {  // of rows that are there and not NaN; 27 if there is none
+      most = 27;
+      const uint32_t s[4] = {s0, s1, s2, s3};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * lane + i;
+        if (s[i] != kScaleNan && row < rows && !(bad >> (row >> p.c.page_bits) & 1u))
+          most = max(most, s[i]);
+      }
+      most = __reduce_max_sync(0xFFFFFFFFu, most);
+    }
+    return most;
+  };
+
+  uint32_t raw = 0, raw_round = 0, slot = 0, round = 0, step = 0;
+  Item it;
+  for (uint32_t k = 0; next_item(k, &it, kErrWaitLoad); ++k) {
+    const uint32_t n = 2u * static_cast<uint32_t>(it.tile1 - it.tile0);
+    uint32_t most = 0, next_most = 0;  // the largest scale of the tile; of V of the same keys
+    bool plain = false, next_plain = false;
+    for (uint32_t i = 0; i < n; ++i) {
+      if (!warp_all(mbar_wait(&ms.raw_full[raw], raw_round & 1, abort_flag, p.err, kErrWaitLoad,
+                              p.wait_limit_ns)) ||
+          !warp_all(mbar_wait(&ms.kv_empty[slot], (round & 1) ^ 1, abort_flag, p.err, kErrWaitLoad,
+                              p.wait_limit_ns)))
+        return;
+      const bool of_v = i & 1;
+      const int there = it.len - (it.tile0 + static_cast<int>(i >> 1)) * kBN;  // rows
+      const uint32_t bad = ms.raw_bad[raw];
+      const uint8_t* codes = smem + C::kOffRaw + raw * C::kRawBytes + tid * 16;
+      const uint8_t* scales = smem + C::kOffScale + raw * C::kScaleBytes;
+      const bool whole = there >= kBN && !bad;
+      if (!of_v) {
+        most = largest(scales, whole, there, bad, &plain);
+        next_most = largest(scales + kBN, whole, there, bad, &next_plain);
+        if (tid == 0) ms.kv_scale[step % 8] = make_uint2(most, next_most);
+      } else {
+        most = next_most;
+        plain = next_plain;
+        scales += kBN;
+      }
+      uint8_t* to = dst + slot * C::kTileBytes;
+      if (!plain) {  // rows that are not there: zeros
+#pragma unroll 1
+        for (int q = 0; q < kRounds; ++q) {
+          const int row = row0 + q * kStep;
+          const bool none = row >= there || (bad >> (row >> p.c.page_bits) & 1u);
+          const uint4 x = none ? make_uint4(0, 0, 0, 0)
+                               : *reinterpret_cast<const uint4*>(codes + q * (kStep * D));
+          one(to + q * (kStep * 128), x, none ? 0u : f16_factor(scales[row], most) * 0x10001u);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.raw_empty[raw]);
+      } else {
+        // (their loads ahead of their stores, which might alias them)
+        constexpr int kAhead = 2;
+#pragma unroll
+        for (int q = 0; q < kRounds; q += kAhead) {
+          uint4 x[kAhead];
+          uint32_t f[kAhead];
+#pragma unroll
+          for (int e = 0; e < kAhead; ++e) {
+            x[e] = *reinterpret_cast<const uint4*>(codes + (q + e) * (kStep * D));
+            f[e] = scales[row0 + (q + e) * kStep];
+          }
+          if (q + kAhead == kRounds) {  // read: the next one may come
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.raw_empty[raw]);
+          }
+#pragma unroll
+          for (int e = 0; e < kAhead; ++e)
+            one(to + (q + e) * (kStep * 128), x[e], (f[e] + 15u - most) * 0x04000400u);
+        }
+      }
+      if (of_v) ++step;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.kv_full[slot]);
+      if (++raw == C::kRaw) {
+        raw = 0;
+        ++raw_round;
+      }
+      if (++slot == C::kStages) {
+        slot = 0;
+        ++round;
+      }
+    }
+  }
+}
 
 template <int D, bool kQuant>
 __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
@@ -139,9 +291,10 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == kWarpLoad && lane == 0) {
-    mbar_init(&ms.q_full, 1);
     mbar_init(&ms.q_empty, 1);
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&ms.q_full[t], 1);
+      mbar_init(&ms.q_ready[t], 8);
       mbar_init(&ms.s_full[t], 1);
       mbar_init(&ms.p_full[t], 8);
       mbar_init(&ms.o_done[t], 1);
@@ -150,12 +303,12 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     }
     mbar_init(&ms.mma_done, 1);
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&ms.kv_full[s], kQuant ? 4 : 1);
+      mbar_init(&ms.kv_full[s], kQuant ? C::kConvert : 1);
       mbar_init(&ms.kv_empty[s], 1);
     }
     for (int s = 0; s < C::kRaw; ++s) {
       mbar_init(&ms.raw_full[s], 1);
-      mbar_init(&ms.raw_empty[s], 4);
+      mbar_init(&ms.raw_empty[s], C::kConvert);
     }
     ms.abort_flag = 0;
     fence_mbar_init();
@@ -203,18 +356,53 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     const int token = t * per_tile + r / p.G;      // of the item
     const bool in_tile = r < per_tile * p.G;
     uint32_t step = 0, done = 0;  // key tiles and items of query tile t so far
+    [[maybe_unused]] uint32_t all_steps = 0;  // key tiles of the CTA
     Item it;
     for (uint32_t k = 0; next_item(k, &it, kErrWaitSoftmax); ++k) {
+      const uint32_t steps = all_steps;
+      if constexpr (kQuant) all_steps += static_cast<uint32_t>(it.tile1 - it.tile0);
       if (t >= it.tiles) continue;
       const bool real = in_tile && token < it.left;
       // keys that the row sees, and that every row of the tile does
       const int vis = !real ? 0 : p.causal ? min(it.len, it.before + token + 1) : it.len;
       const int all_see = p.causal ? min(it.len, it.before + t * per_tile + 1) : it.len;
       // the last page's tokens stand `shift` rows further down from key `cut` on
-      const int cut = kQuant ? 0 : max(it.len - 1, 0) / p.c.page * p.c.page;
+      const int cut = kQuant ? 0 : max(it.len - 1, 0) & -p.c.page;
       const int shift = kQuant ? 0 : cut + p.c.page - it.len;
       float m = -CUDART_INF_F, l = 0.f;
       bool ok = true;
+      [[maybe_unused]] float row_scale = p.scale_log2;
+      if constexpr (kQuant) {
+        // Q to f16, a thread's half of its row: over a power of two that makes the row's
+        // largest element 1 to 2, exact but below 2^-14, where a step is 2^-24
+        if (!warp_all(mbar_wait(&ms.q_full[t], done & 1, abort_flag, p.err, kErrWaitSoftmax,
+                                p.wait_limit_ns)))
+          break;
+        uint8_t* q = smem + t * C::kTileBytes + (D == 128 ? c * (kBM * 128) : 0) + r * 128;
+        constexpr int kPieces = D / 16;  // of 16 bytes in half a row
+        auto at = [&](int i) {
+          return reinterpret_cast<uint4*>(q + (((D == 128 ? i : kPieces * c + i) ^ (r & 7)) << 4));
+        };
+        uint4 x[kPieces];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          x[i] = *at(i);
+          top = max(top, max(max(bf16x2_top(x[i].x), bf16x2_top(x[i].y)),
+                             max(bf16x2_top(x[i].z), bf16x2_top(x[i].w))));
+        }
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+        const uint32_t e = min(max(top >> 23, 1u), 253u);
+        row_scale *= __uint_as_float(e << 23);
+        const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          *at(i) = make_uint4(bf16x2_to_f16x2(x[i].x, inv), bf16x2_to_f16x2(x[i].y, inv),
+                              bf16x2_to_f16x2(x[i].z, inv), bf16x2_to_f16x2(x[i].w, inv));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.q_ready[t]);
+      }
       for (int j = it.tile0; j < it.tile1; ++j, ++step) {
         if (!warp_all(mbar_wait(&ms.s_full[t], step & 1, abort_flag, p.err, kErrWaitSoftmax,
                                 p.wait_limit_ns))) {
@@ -262,7 +450,20 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
           mx = max3f(a0, a1, fmaxf(a2, a3));
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
         }
-        const float m_tile = mx * p.scale_log2;  // (scale_log2 > 0)
+        // Quantised, the tile's K and V are to be multiplied by 2^a and 2^e: scores by 2^a,
+        // and the weights stand for 2^(x + e), with the maximum of x + e; the sum is of 2^x
+        // over the same reference.
+        float scale = p.scale_log2;
+        [[maybe_unused]] float e = 0.f, sum_scale = 1.f;
+        if constexpr (kQuant) {
+          // (there since S is: its operands were converted before)
+          const uint2 by = ms.kv_scale[(steps + static_cast<uint32_t>(j - it.tile0)) % 8];
+          scale = row_scale * scale_value(by.x);
+          e = scale_exponent(by.y);
+          sum_scale = __uint_as_float((254u - by.y) << 23);
+        }
+        float m_tile = mx * scale;  // (scale > 0)
+        if constexpr (kQuant) m_tile += e;
         float alpha = 1.f;
         if (m_tile > m + 8.f) {  // a stale maximum is as good up to there
           alpha = ex2_approx(m - m_tile);  // 0 the first time
@@ -270,8 +471,8 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         }
         // p = 2^(s * scale - m); a row that has seen nothing keeps m = -inf: its
         // scores are -inf and stay it next to a reference of 0
-        const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
-        const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
+        const float neg_m = (m == -CUDART_INF_F ? 0.f : -m) + (kQuant ? e : 0.f);
+        const uint64_t scale2 = f32x2(scale, scale);
         const uint64_t negm2 = f32x2(neg_m, neg_m);
         uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
         uint32_t pk[32];
@@ -284,12 +485,12 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
           const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
           acc0 = add_f32x2(acc0, f32x2(p0, p1));
           acc1 = add_f32x2(acc1, f32x2(p2, p3));
-          pk[i / 2] = pack_bf16x2(p0, p1);
-          pk[i / 2 + 1] = pack_bf16x2(p2, p3);
+          pk[i / 2] = kQuant ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          pk[i / 2 + 1] = kQuant ? pack_f16x2(p2, p3) : pack_bf16x2(p2, p3);
         }
         float u0, u1;
         unpack_f32x2(add_f32x2(acc0, acc1), u0, u1);
-        l = fmaf(l, alpha, u0 + u1);
+        l = fmaf(l, alpha, kQuant ? (u0 + u1) * sum_scale : u0 + u1);
         // Rescale O_t where a maximum moved: every product of earlier key tiles has
         // retired (issued before the S_t that woke this warp), that of this one waits.
         if (j > it.tile0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
@@ -358,12 +559,13 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     // ---- the plan's items, their Q tiles, and K_j, V_j through the ring
     reg_dealloc<C::kRegOther>();
     uint32_t k = 0;           // items
+    uint32_t q_loads = 0, q_loads1 = 0;  // of query tiles 0 and 1
     uint32_t slot = 0, round = 0;  // next place in the ring
     constexpr uint32_t kRing = kQuant ? C::kRaw : C::kStages;
     uint64_t* const full = kQuant ? ms.raw_full : ms.kv_full;
     uint64_t* const empty = kQuant ? ms.raw_empty : ms.kv_empty;
-    const int page = p.c.page;
-    const int boxes = kBN / page;
+    const int page = p.c.page, page_bits = p.c.page_bits;
+    const int boxes = kBN >> page_bits;
     const int per_tile = kBM / p.G;
     const uint64_t policy = l2_policy_evict_last();
     bool ok = true;
@@ -394,15 +596,15 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
       for (uint32_t i = 0; i < n && ok; ++i) {
         const int key0 = (it.tile0 + static_cast<int>(i >> 1)) * kBN;
         // copy `box` of the tile: page and rows (lane l holds entry pbase + l of the table)
-        if (key0 / page < pbase || key0 / page + boxes > pbase + 32) {
-          pbase = key0 / page;
+        if ((key0 >> page_bits) < pbase || (key0 >> page_bits) + boxes > pbase + 32) {
+          pbase = key0 >> page_bits;
           ids = pbase + lane < p.c.M
                     ? p.c.table[static_cast<size_t>(it.b) * p.c.M + pbase + lane]
                     : -1;
         }
         const int box = kQuant ? lane : lane / C::kChunks;
-        const int key = key0 + box * page;
-        const int id = __shfl_sync(0xFFFFFFFFu, ids, (key / page - pbase) & 31);
+        const int key = key0 + (box << page_bits);
+        const int id = __shfl_sync(0xFFFFFFFFu, ids, ((key >> page_bits) - pbase) & 31);
         const bool mine = box < boxes;
         const bool there = key < it.len;
         const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.c.P);
@@ -416,7 +618,8 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         if constexpr (kQuant) {
           const bool copy = mine && there && good;
           const int rows = min(page, it.len - key);
-          uint32_t bytes = copy ? static_cast<uint32_t>(rows * D + page) : 0;
+          const int scales = (i & 1) ? 1 : 2;  // with K, V's too
+          uint32_t bytes = copy ? static_cast<uint32_t>(rows * D + scales * page) : 0;
           bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
           if (lane == 0) {
             ms.raw_bad[slot] = bad;
@@ -428,9 +631,11 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
             const uint8_t* src = static_cast<const uint8_t*>((i & 1) ? p.c.vpages : p.c.kpages);
             bulk_copy(smem + C::kOffRaw + slot * C::kRawBytes + box * page * D, src + from * D,
                       static_cast<uint32_t>(rows * D), &full[slot], policy);
-            bulk_copy(smem + C::kOffScale + slot * kBN + box * page,
-                      ((i & 1) ? p.c.vscale : p.c.kscale) + from, static_cast<uint32_t>(page),
-                      &full[slot], policy);
+            uint8_t* to = smem + C::kOffScale + slot * C::kScaleBytes + (box << page_bits);
+            if (!(i & 1))
+              bulk_copy(to, p.c.kscale + from, static_cast<uint32_t>(page), &full[slot], policy);
+            bulk_copy(to + kBN, p.c.vscale + from, static_cast<uint32_t>(page), &full[slot],
+                      policy);
           }
         } else {
           mbar_arrive_expect_tx_elect(&full[slot], C::kTileBytes);
@@ -456,12 +661,16 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx_elect(&ms.q_full,
-                                      static_cast<uint32_t>(it.tiles * per_tile * p.G * D * 2));
-          for (int t = 0; t < it.tiles; ++t)
+          for (int t = 0; t < it.tiles; ++t) {
+            mbar_arrive_expect_tx_elect(&ms.q_full[t],
+                                        static_cast<uint32_t>(per_tile * p.G * D * 2));
             for (int ch = 0; ch < C::kChunks; ++ch)
-              tma_load_4d_elect(smem + t * C::kTileBytes + ch * (kBM * 128), &p.tmap_q, &ms.q_full,
-                                ch * 64, 0, it.h, it.row0 + t * per_tile, l2_policy_evict_first());
+              tma_load_4d_elect(smem + t * C::kTileBytes + ch * (kBM * 128), &p.tmap_q,
+                                &ms.q_full[t], ch * 64, 0, it.h, it.row0 + t * per_tile,
+                                l2_policy_evict_first());
+          }
+          ++q_loads;
+          q_loads1 += it.tiles > 1;
         }
       }
       ++k;
@@ -475,10 +684,10 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
       }
     }
     if (abort_set(abort_flag)) {
-      // copies in flight land before the CTA leaves: those of the last Q (of item k, or the
-      // one before) and of the last round of the ring
-      if (k > 0) drain_wait(&ms.q_full, (k - 1) & 1);
-      drain_wait(&ms.q_full, k & 1);
+      // copies in flight land before the CTA leaves: the last Q tiles, and the last round
+      // of the ring
+      if (q_loads > 0) drain_wait(&ms.q_full[0], (q_loads - 1) & 1);
+      if (q_loads1 > 0) drain_wait(&ms.q_full[1], (q_loads1 - 1) & 1);
       for (uint32_t i = 0; i < kRing; ++i) {
         if (i < slot)
           drain_wait(&full[i], round & 1);
@@ -496,19 +705,19 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     auto issue_s = [&](int t, uint32_t slot) {
       const uint32_t b0 = desc_k + slot * kTileDesc;
       if (t)
-        issue_s_steps<D, false, C::kColS1, kQ1>(tmem, desc_k, b0);
+        issue_s_rec<false, C::kColS1, kQ1, 0, 0, C::kIdescS, 0, D / 16>(tmem, desc_k, b0);
       else
-        issue_s_steps<D, false, C::kColS0, kQ0>(tmem, desc_k, b0);
+        issue_s_rec<false, C::kColS0, kQ0, 0, 0, C::kIdescS, 0, D / 16>(tmem, desc_k, b0);
       mma_commit(&ms.s_full[t]);
     };
     auto issue_pv = [&](int t, uint32_t slot, uint32_t acc) {
       const uint32_t b0 = desc_k + slot * kTileDesc;
       if (t)
-        issue_pv_steps<D, false, C::kColO1, C::kColS1, kVFromK>(tmem, b0, acc);
+        issue_pv_rec<false, C::kColO1, C::kColS1, kVFromK, C::kIdescPV, 0>(tmem, b0, acc);
       else
-        issue_pv_steps<D, false, C::kColO0, C::kColS0, kVFromK>(tmem, b0, acc);
+        issue_pv_rec<false, C::kColO0, C::kColS0, kVFromK, C::kIdescPV, 0>(tmem, b0, acc);
     };
-    uint32_t p_step[2] = {0, 0};  // P tiles waited for
+    uint32_t p_step[2] = {0, 0}, q_step1 = 0;  // P tiles waited for, items with query tile 1
     uint32_t slot = 0, round = 0;
     auto wait_kv = [&]() -> bool {
       return warp_all(mbar_wait(&ms.kv_full[slot], round & 1, abort_flag, p.err, kErrWaitMma,
@@ -532,7 +741,6 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     bool ok = true;
     for (uint32_t k = 0; ok && next_item(k, &it, kErrWaitMma); ++k) {
       const int tiles = it.tiles, n = it.tile1 - it.tile0;
-      ok = warp_all(mbar_wait(&ms.q_full, k & 1, abort_flag, p.err, kErrWaitMma, p.wait_limit_ns));
       // ring order K_0 V_0 K_1 V_1 ...; S of key tile i + 1 goes out with P V of tile i
       uint32_t v_slot = 0;
       for (int i = 0; i < n && ok; ++i) {
@@ -545,6 +753,12 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
             ok = wait_p(t);
             if (!ok) break;
             issue_pv(t, v_slot, i > 1 ? 1u : 0u);
+          } else {
+            const uint32_t q_phase = (t ? q_step1++ : k) & 1;  // (tile 0 is in every item)
+            ok = warp_all(mbar_wait(kQuant ? &ms.q_ready[t] : &ms.q_full[t], q_phase, abort_flag,
+                                    p.err, kErrWaitMma, p.wait_limit_ns));
+            if (!ok) break;
+            tc_fence_after();
           }
           issue_s(t, k_slot);
         }
@@ -573,86 +787,8 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     drain_wait(&ms.mma_done, 0);
   } else {
     reg_dealloc<C::kRegOther>();
-    if (kQuant && warp >= kWarpConvert) {
-      // ---- quantised tiles to bf16 ones, rows behind the last token to zeros
-      // A thread has the same 16 elements of every kStep-th row.  The lanes of a row's two
-      // halves store their 16-byte pieces in opposite order, so that no two of eight
-      // lanes meet in a bank.
-      const int tid = threadIdx.x - kWarpConvert * 32;
-      constexpr int kPieces = D / 16, kStep = 128 / kPieces, kRounds = kBN / kStep;
-      const int row0 = tid / kPieces, piece = tid % kPieces;
-      const bool hi = piece >= kPieces / 2;
-      uint8_t* const dst = smem + C::kOffKV + (piece >> 2) * (kBN * 128) + row0 * 128;
-      const uint32_t at0 = (((piece * 2) & 7) ^ (row0 & 7)) << 4;
-      auto store = [&](uint8_t* to, const uint32_t (&y)[8]) {
-        *reinterpret_cast<uint4*>(to + (hi ? at0 ^ 16u : at0)) =
-            hi ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint4*>(to + (hi ? at0 : at0 ^ 16u)) =
-            hi ? make_uint4(y[0], y[1], y[2], y[3]) : make_uint4(y[4], y[5], y[6], y[7]);
-      };
-      uint32_t raw = 0, raw_round = 0, slot = 0, round = 0;
-      Item it;
-      bool ok = true;
-      for (uint32_t k = 0; ok && next_item(k, &it, kErrWaitLoad); ++k) {
-        const uint32_t n = 2u * static_cast<uint32_t>(it.tile1 - it.tile0);
-        for (uint32_t i = 0; i < n; ++i) {
-          const int key0 = (it.tile0 + static_cast<int>(i >> 1)) * kBN;
-          ok = warp_all(mbar_wait(&ms.raw_full[raw], raw_round & 1, abort_flag, p.err,
-                                  kErrWaitLoad, p.wait_limit_ns)) &&
-               warp_all(mbar_wait(&ms.kv_empty[slot], (round & 1) ^ 1, abort_flag, p.err,
-                                  kErrWaitLoad, p.wait_limit_ns));
-          if (!ok) break;
-          const uint32_t bad = ms.raw_bad[raw];
-          const uint8_t* codes = smem + C::kOffRaw + raw * C::kRawBytes + tid * 16;
-          const uint8_t* scales = smem + C::kOffScale + raw * kBN;
-          uint8_t* to = dst + slot * C::kTileBytes;
-          // rows that are not there, and scales beyond one factor, or NaN: rare
-          const uint32_t most = __vcmpgtu4(reinterpret_cast<const uint32_t*>(scales)[lane],
-                                           kScaleMost * 0x01010101u);
-          if (key0 + kBN > it.len || bad || __any_sync(0xFFFFFFFFu, most != 0)) {
-#pragma unroll 1
-            for (int q = 0; q < kRounds; ++q) {
-              const int row = row0 + q * kStep;
-              uint4 x = *reinterpret_cast<const uint4*>(codes + q * 2048);
-              uint32_t scale = scales[row];
-              if (key0 + row >= it.len || (bad >> (row / p.c.page) & 1u)) {
-                x = make_uint4(0, 0, 0, 0);
-                scale = 127;
-              }
-              uint32_t y[8];
-              e4m3_row16(x, e4m3_factor(scale), y);
-              const uint32_t rest =
-                  (max(scale == kScaleNan ? 0u : scale, kScaleMost) - kScaleMost + 127u) << 7;
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(y[e]) : "r"(rest * 0x10001u));
-              store(to + q * (kStep * 128), y);
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < kRounds; ++q) {
-              const uint4 x = *reinterpret_cast<const uint4*>(codes + q * 2048);
-              uint32_t y[8];
-              e4m3_row16(x, (scales[row0 + q * kStep] + 120u) * 0x00800080u, y);
-              store(to + q * (kStep * 128), y);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ms.kv_full[slot]);
-            mbar_arrive(&ms.raw_empty[raw]);
-          }
-          if (++raw == C::kRaw) {
-            raw = 0;
-            ++raw_round;
-          }
-          if (++slot == C::kStages) {
-            slot = 0;
-            ++round;
-          }
-        }
-      }
+    if constexpr (kQuant) {
+      if (warp >= kWarpConvert) convert<D, C>(p, ms, smem, abort_flag, next_item);
     }
   }
 
