@@ -94,7 +94,7 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
   l.rows = many ? 0 : rows <= 8 ? 8 : 16;
   // the streaming kernel numbers its units of work in 32 bits
   const long long blocks = static_cast<long long>(c.T) * p.G / 8 + c.B;
-  if (blocks * c.Hkv * (static_cast<long long>(c.M) * c.page / 64 + 3) >= (1ll << 31))
+  if (blocks * c.Hkv * (static_cast<long long>(c.M) * c.page / 64 + 5) >= (1ll << 31))
     return ATTN_ERR_SHAPE;
   DeviceInfo di;
   if (int rc = device_info(&di)) return rc;

@@ -51,7 +51,7 @@ struct StreamCfg {
   static constexpr int kRowBytes = kQuant ? D : 2 * D;
   static constexpr int kTile = kUnitKeys * kRowBytes;  // K or V of a unit
   static constexpr int kScales = kQuant ? 2 * kUnitKeys : 0;
-  static constexpr int kMerge = kWarps * kRows * D * 4;
+  static constexpr int kMerge = kWarps / 2 * kRows * D * 4;
   // Two CTAs on an SM where the registers allow it: one joins its warps' states and
   // stores while the other goes on.
   static constexpr int kCtas = kQuant && NT == 1 ? 2 : 1;
@@ -69,7 +69,7 @@ struct StreamCfg {
 template <int kStages, int kRows>
 struct StreamShared {
   uint64_t full[kStages], empty[kStages];
-  uint64_t merge_full, merge_empty;
+  uint64_t team_full, merge_full, merge_empty;
   Unit unit[kStages];
   float2 ml[kWarps][kRows];
   PlanShared plan;
@@ -144,13 +144,15 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
       mbar_init(&ms.full[s], 1);
       mbar_init(&ms.empty[s], kWarps / 2);
     }
-    mbar_init(&ms.merge_full, kWarps);
+    mbar_init(&ms.team_full, kWarps / 2);
+    mbar_init(&ms.merge_full, kWarps / 2);
     mbar_init(&ms.merge_empty, kWarps);
     ms.abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.tmap_k);
     tma_prefetch_desc(&p.tmap_v);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for what the stream did before
   const StreamPlan plan(p.c, p.G, kRows);
   // (its barriers also publish the mbarriers)
   const PlanPlace at = plan.place<kThreads>(ms.plan, blockIdx.x, p.ctas);
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
     int b = at.b;
     uint32_t in_request = at.in_request;  // unit within the request
     const Deal deal(at.total, p.ctas);
+    constexpr uint32_t kBlockCost = block_cost(kQuant);
     PagedCut cut = {};
     for (uint32_t u = at.first; u < at.end && b < p.c.B && ok;) {
       const Rows rows = request_rows(p.c, b);
@@ -507,30 +510,78 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
     if (lane == 0) mbar_arrive(&ms.empty[st]);
     if (!(un.flags & kUnitLast)) continue;
 
-    // ---- the warps' states of the block, joined through shared memory
-    float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+    // ---- the warps' states of the block, joined through shared memory: the second team's
+    // with the first team's, register by register, then those four by rows
+    float* const merge = reinterpret_cast<float*>(smem + C::kOffMerge) + (warp & 3) * kRows * D;
     if (!warp_all(mbar_wait(&ms.merge_empty, (merges & 1u) ^ 1u, abort_flag, p.err, kErrWaitCorr,
                             p.wait_limit_ns)))
       return;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int d = 4; d < 32; d *= 2) l[nt][k] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][k], d);
-        const int r = nt * 8 + 2 * t + k;
-        if (g == 0) ms.ml[warp][r] = make_float2(m[nt][k], l[nt][k]);
-        float* row = merge + (warp * kRows + r) * D;
+    auto say = [&](int as) {  // maximum and sum of every row
+      if (g == 0)
 #pragma unroll
-        for (int i = 0; i < kSteps; i += 2) {
-          // four elements of the row: the thread's tiles i and i + 1
-          const int d = kQuant ? g * (D / 8) + 2 * i : (i / 4) * 64 + g * 8 + 2 * (i % 4);
-          *reinterpret_cast<float4*>(row + d) =
-              make_float4(o[nt][i][k], o[nt][i][k + 2], o[nt][i + 1][k], o[nt][i + 1][k + 2]);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) ms.ml[as][nt * 8 + 2 * t + k] = make_float2(m[nt][k], l[nt][k]);
+    };
+    float4* const mine = reinterpret_cast<float4*>(merge) + lane;
+    if (warp >= 4) {
+      say(warp);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+          mine[(nt * kSteps + i) * 32] = make_float4(o[nt][i][0], o[nt][i][1], o[nt][i][2], o[nt][i][3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.team_full);
+    } else {
+      if (!warp_all(mbar_wait(&ms.team_full, merges & 1u, abort_flag, p.err, kErrWaitCorr,
+                              p.wait_limit_ns)))
+        return;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float a[2], e[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 ml = ms.ml[warp + 4][nt * 8 + 2 * t + k];
+          const float top = fmaxf(m[nt][k], ml.x);
+          a[k] = m[nt][k] == -CUDART_INF_F ? 1.f : ex2_approx(m[nt][k] - top);
+          e[k] = ml.x == -CUDART_INF_F ? 1.f : ex2_approx(ml.x - top);
+          m[nt][k] = top;
+          l[nt][k] = l[nt][k] * a[k] + ml.y * e[k];
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const float4 x = mine[(nt * kSteps + i) * 32];
+          o[nt][i][0] = o[nt][i][0] * a[0] + x.x * e[0];
+          o[nt][i][1] = o[nt][i][1] * a[1] + x.y * e[1];
+          o[nt][i][2] = o[nt][i][2] * a[0] + x.z * e[0];
+          o[nt][i][3] = o[nt][i][3] * a[1] + x.w * e[1];
         }
       }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ms.merge_full);
+      __syncwarp();  // (the warp's part of the buffer is read)
+      say(warp);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float* row = merge + (nt * 8 + 2 * t + k) * D;
+#pragma unroll
+          for (int i = 0; i < kSteps; i += 2) {
+            // four elements of the row: the thread's tiles i and i + 1
+            const int d = kQuant ? g * (D / 8) + 2 * i : (i / 4) * 64 + g * 8 + 2 * (i % 4);
+            *reinterpret_cast<float4*>(row + d) =
+                make_float4(o[nt][i][k], o[nt][i][k + 2], o[nt][i + 1][k], o[nt][i + 1][k + 2]);
+          }
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.merge_full);
+    }
     if (!warp_all(mbar_wait(&ms.merge_full, merges & 1u, abort_flag, p.err, kErrWaitCorr,
                             p.wait_limit_ns)))
       return;
@@ -538,10 +589,11 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
       State<D> sum;
       float top = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) top = fmaxf(top, ms.ml[i][r].x);
+      for (int i = 0; i < kWarps / 2; ++i) top = fmaxf(top, ms.ml[i][r].x);
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i)
-        sum.add(ms.ml[i][r], top, merge + (i * kRows + r) * D, lane);
+      for (int i = 0; i < kWarps / 2; ++i)
+        sum.add(ms.ml[i][r], top,
+                reinterpret_cast<float*>(smem + C::kOffMerge) + (i * kRows + r) * D, lane);
       const int row = un.block * kRows + r;
       if (un.slot < 0) {
         sum.finish(p, un.row0 + row / p.G, un.h * p.G + row % p.G, top, lane);
@@ -607,22 +659,8 @@ cudaError_t launch_stream(const PagedParams& p, int dev, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
-  paged_stream_kernel<D, kQuant, NT><<<p.ctas, kThreads, C::kSmem, stream>>>(p);
-  return cudaGetLastError();
-}
-
-template <int D>
-cudaError_t launch_merge(const PagedParams& p, int rows, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas - 1);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, stream_merge_kernel<D>, p, rows);
+  return launch_overlapped(paged_stream_kernel<D, kQuant, NT>, dim3(p.ctas), kThreads, C::kSmem,
+                           stream, p);
 }
 
 }  // namespace
@@ -646,7 +684,8 @@ cudaError_t launch_paged_stream(const PagedParams& p, int rows, int dev, cudaStr
   cudaError_t e = table[p.c.D == 128][p.c.quant][rows == 16](p, dev, stream);
   if (e != cudaSuccess) return e;
   if (p.ctas < 2) return cudaSuccess;
-  return p.c.D == 128 ? launch_merge<128>(p, rows, stream) : launch_merge<64>(p, rows, stream);
+  return launch_overlapped(p.c.D == 128 ? stream_merge_kernel<128> : stream_merge_kernel<64>,
+                           dim3(p.ctas - 1), 256, 0, stream, p, rows);
 }
 
 }  // namespace attn

@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     tmem_alloc(&ms.tmem_base, 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for what the stream did before
   const CostPlan plan(p.c, p.G, p.causal);
   const CostPlace at = plan.place<C::kThreads>(ms.plan, blockIdx.x, p.ctas);
   tc_fence_before();
@@ -833,19 +834,12 @@ cudaError_t launch_tile(const PagedParams& p, int dev, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
-  paged_tile_kernel<D, kQuant><<<p.ctas, C::kThreads, C::kSmem, stream>>>(p);
-  if (cudaError_t e = cudaGetLastError()) return e;
+  if (cudaError_t e = launch_overlapped(paged_tile_kernel<D, kQuant>, dim3(p.ctas), C::kThreads,
+                                        C::kSmem, stream, p))
+    return e;
   if (p.ctas < 2) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas - 1, kMergeSplit);  // (the last CTA's items end there)
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tile_merge_kernel<D>, p);
+  // (the last CTA's items end there)
+  return launch_overlapped(tile_merge_kernel<D>, dim3(p.ctas - 1, kMergeSplit), 256, 0, stream, p);
 }
 
 }  // namespace

@@ -504,7 +504,7 @@ int attn_cache_read(const void *kpages, const void *vpages, const unsigned char 
  *
  * Limits: Hq % Hkv == 0, Hq <= 65535, Hq / Hkv <= 128, max_new >= 0; scale finite and
  * >= 0; the rows times the keys in units of work within 32 bits:
- * (T * Hq / Hkv / 8 + B) * Hkv * (M * page / 64 + 3) < 2^31.  Scratch as
+ * (T * Hq / Hkv / 8 + B) * Hkv * (M * page / 64 + 5) < 2^31.  Scratch as
  * attn_decode_varlen.
  */
 int attn_paged_fwd(const void *q, long long q_stride, const void *kpages, const void *vpages,
