@@ -1,5 +1,5 @@
 // Partial-state scratch of the split decodes (attn_decode_splitkv, _states,
-// attn_decode_varlen, attn_decode_prefix): a small per-device cache of device
+// attn_decode_varlen, attn_decode_prefix, attn_paged_fwd): a small per-device cache of device
 // buffers, one per recently used stream, so that a decode step allocates nothing
 // once its stream has been seen.
 //
@@ -35,6 +35,7 @@ struct Entry {
   size_t bytes = 0;
   cudaEvent_t done = nullptr;  // recorded after the entry's last use
   unsigned long long last_use = 0;
+  unsigned turns = 0;  // calls that used this buffer, modulo 2^32; 0: its contents are nobody's
   bool live = false;
 };
 
@@ -44,32 +45,34 @@ struct Cache {
   unsigned long long tick = 0;
 };
 Cache g_cache[kMaxDevices];
+// Of the calls that keep something in their buffers from one to the next.
+Cache g_turns_cache[kMaxDevices];
 
-}  // namespace
 
-int with_own_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
-                     void* ctx) {
+// launch(buffer, turn), turn 0 for a buffer with unknown contents
+template <class Launch>
+int own_buffer(size_t bytes, cudaStream_t stream, Launch launch) {
   void* ws = nullptr;
   if (cudaMallocAsync(&ws, bytes, stream) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_ALLOC;
   }
-  int rc = launch(ctx, ws, stream);
+  int rc = launch(ws, 0u);
   if (cudaFreeAsync(ws, stream) != cudaSuccess && rc == ATTN_OK) rc = ATTN_ERR_CUDA;
   return rc;
 }
 
-int with_scratch(size_t bytes, int dev, cudaStream_t stream,
-                 int (*launch)(void*, void*, cudaStream_t), void* ctx) {
+template <class Launch>
+int cached_buffer(Cache* caches, size_t bytes, int dev, cudaStream_t stream, Launch launch) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_CUDA;
   }
-  if (cap != cudaStreamCaptureStatusNone) return with_own_scratch(bytes, stream, launch, ctx);
+  if (cap != cudaStreamCaptureStatusNone) return own_buffer(bytes, stream, launch);
 
   if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_DEVICE;
-  Cache& c = g_cache[dev];
+  Cache& c = caches[dev];
   // held until the launches and the event record are queued, so that no
   // other host thread frees or regrows this buffer in between
   std::lock_guard<std::mutex> lock(c.mu);
@@ -115,6 +118,7 @@ int with_scratch(size_t bytes, int dev, cudaStream_t stream,
     }
     en->ptr = nullptr;
     en->bytes = 0;
+    en->turns = 0;
     if (cudaMallocAsync(&en->ptr, bytes, stream) != cudaSuccess) {
       cudaGetLastError();
       en->ptr = nullptr;
@@ -124,10 +128,31 @@ int with_scratch(size_t bytes, int dev, cudaStream_t stream,
     en->bytes = bytes;
   }
   en->last_use = ++c.tick;
-  int rc = launch(ctx, en->ptr, stream);
+  int rc = launch(en->ptr, en->turns);
+  en->turns = rc != ATTN_OK ? 0 : en->turns + 1 == 0 ? 2 : en->turns + 1;  // (keeps its parity)
   // recorded even after a failed launch: whatever did get queued is covered
   if (cudaEventRecord(en->done, stream) != cudaSuccess && rc == ATTN_OK) rc = ATTN_ERR_CUDA;
   return rc;
+}
+
+}  // namespace
+
+int with_own_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
+                     void* ctx) {
+  return own_buffer(bytes, stream, [=](void* ws, unsigned) { return launch(ctx, ws, stream); });
+}
+
+int with_scratch(size_t bytes, int dev, cudaStream_t stream,
+                 int (*launch)(void*, void*, cudaStream_t), void* ctx) {
+  return cached_buffer(g_cache, bytes, dev, stream,
+                       [=](void* ws, unsigned) { return launch(ctx, ws, stream); });
+}
+
+int with_turns(size_t bytes, int dev, cudaStream_t stream,
+               int (*launch)(void*, void*, unsigned, cudaStream_t), void* ctx) {
+  return cached_buffer(g_turns_cache, bytes, dev, stream, [=](void* ws, unsigned turn) {
+    return launch(ctx, ws, turn, stream);
+  });
 }
 
 int decode_with_cached_scratch(DecodeParams& p, cudaStream_t stream) {

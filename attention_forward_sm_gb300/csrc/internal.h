@@ -223,6 +223,13 @@ int with_scratch(size_t bytes, int dev, cudaStream_t stream,
 int with_own_scratch(size_t bytes, cudaStream_t stream, int (*launch)(void*, void*, cudaStream_t),
                      void* ctx);
 
+// As with_scratch, for kernels that keep something in the buffer from one call to the
+// next: turn counts the calls that have used it, 0 where its contents are unknown (a new
+// buffer, one after a failed call, every captured call).
+int with_turns(size_t bytes, int dev, cudaStream_t stream,
+               int (*launch)(void* ctx, void* scratch, unsigned turn, cudaStream_t stream),
+               void* ctx);
+
 // Check the device and queue the kernels; arguments are checked before.
 // Return an ATTN_* status.
 int mod_fwd(const ModFwdParams& p, cudaStream_t stream);
@@ -253,15 +260,16 @@ struct CacheRows {
 cudaError_t launch_cache_rows(const PagedArrays& c, const CacheRows& r, bool read,
                               cudaStream_t stream);
 
-// An item that was cut, written by the CTA that has its first part: the parts are that
-// CTA's state 1 and state 0 of the `parts` - 1 CTAs behind it.
+// An item of the kernel for many rows that was cut, written by the CTA that has its first
+// part: the parts are that CTA's state 1 and state 0 of the `parts` - 1 CTAs behind it.
 struct PagedCut {
   int parts;       // 0: none begins in this CTA
   int row0, left;  // first dense row; tokens of the request from there on
-  int h, first;    // KV head; number of the item's first row among that token's and its next
+  int h;           // KV head
 };
 
 // Attention of new tokens over a paged cache.
+constexpr uint32_t kPagedCounts = 16 * 2 * kMostCtas;
 struct PagedParams {
   CUtensorMap tmap_k, tmap_v;  // pages as [P * Hkv, page, D], box {128 bytes, rows, 1}
   CUtensorMap tmap_q;          // [T, Hkv, G, D], box {64, G, 1, 128 / G} (many rows)
@@ -275,7 +283,12 @@ struct PagedParams {
   unsigned ctas;       // of the split kernel
   float* part_o;       // partial states: [slot, rows of a block, D], and their
   float2* part_ml;     // maximum (log2 units) and sum
-  PagedCut* cuts;      // of every CTA
+  PagedCut* cuts;      // of every CTA (many rows)
+  // Few rows: for each CTA that has an item's first part, and 16 shares of its rows: how many of
+  // the parts' CTAs have stored theirs.  Two sets that calls use in turn, each call
+  // clearing the other one, so that a call that failed leaves nothing behind.
+  uint32_t* arrived;   // [kPagedCounts]
+  uint32_t* clear;
   unsigned int* err;
   uint64_t wait_limit_ns;
 };

@@ -48,19 +48,32 @@ int check_stride(long long stride, int heads, int D) {
              : ATTN_OK;
 }
 
+// Two sets of counts, in front of the partial states.
+constexpr size_t kCountBytes = 2 * kPagedCounts * sizeof(uint32_t);
+
 struct PagedLaunch {
   PagedParams* p;
   int rows, dev;  // rows: of a block of the kernel for few rows; 0: the one for many
   size_t states;  // rows of partial states
 };
-int launch_paged(void* ctx, void* scratch, cudaStream_t stream) {
+int launch_stream(void* ctx, void* scratch, unsigned turn, cudaStream_t stream) {
+  const PagedLaunch& l = *static_cast<PagedLaunch*>(ctx);
+  uint32_t* const counts = static_cast<uint32_t*>(scratch);
+  l.p->part_o = reinterpret_cast<float*>(counts + 2 * kPagedCounts);
+  l.p->part_ml = reinterpret_cast<float2*>(l.p->part_o + l.states * l.p->c.D);
+  if (turn == 0 && cudaMemsetAsync(counts, 0, kCountBytes, stream) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  l.p->arrived = counts + (turn & 1) * kPagedCounts;
+  l.p->clear = counts + (turn + 1 & 1) * kPagedCounts;
+  return launch_paged_stream(*l.p, l.rows, l.dev, stream) == cudaSuccess ? ATTN_OK
+                                                                         : ATTN_ERR_LAUNCH;
+}
+int launch_tile(void* ctx, void* scratch, cudaStream_t stream) {
   const PagedLaunch& l = *static_cast<PagedLaunch*>(ctx);
   l.p->part_o = static_cast<float*>(scratch);
   l.p->part_ml = reinterpret_cast<float2*>(l.p->part_o + l.states * l.p->c.D);
   l.p->cuts = reinterpret_cast<PagedCut*>(l.p->part_ml + l.states);
-  const cudaError_t e = l.rows ? launch_paged_stream(*l.p, l.rows, l.dev, stream)
-                               : launch_paged_tile(*l.p, l.dev, stream);
-  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+  return launch_paged_tile(*l.p, l.dev, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, float* lse, int Hq,
@@ -111,9 +124,9 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
   p.wait_limit_ns = wait_limit_ns();
   l.dev = di.dev;
   l.states = many ? paged_tile_state(p) : paged_stream_state(p, l.rows);
-  const size_t bytes =
-      l.states * (c.D * sizeof(float) + sizeof(float2)) + p.ctas * sizeof(PagedCut);
-  return with_scratch(bytes, di.dev, stream, launch_paged, &l);
+  const size_t bytes = l.states * (c.D * sizeof(float) + sizeof(float2));
+  return many ? with_scratch(bytes + p.ctas * sizeof(PagedCut), di.dev, stream, launch_tile, &l)
+              : with_turns(bytes + kCountBytes, di.dev, stream, launch_stream, &l);
 }
 
 int cache_rows(const PagedArrays& c, CacheRows r, bool read, cudaStream_t stream) {

@@ -19,18 +19,26 @@ struct Deal {
   __device__ Deal(uint32_t total, uint32_t ctas)
       : runs(min(total, ctas)), each(runs ? total / runs : 0), more(runs ? total % runs : 0) {}
   __device__ uint32_t start(uint32_t r) const { return r * each + min(r, more); }
+  __device__ uint32_t run_of(uint32_t x) const {
+    const uint32_t cut = more * (each + 1);
+    return x < cut ? x / (each + 1) : min(more + (x - cut) / each, runs - 1);
+  }
 };
 
 struct PlanShared {
   uint32_t warp_sum[16];
   int b;
   uint32_t in_request;
+  Rows rows;
+  int len;
 };
 struct PlanPlace {
   uint32_t total;       // units of all
   uint32_t first, end;  // of this CTA
   int b;                // request that holds the first one,
   uint32_t in_request;  // and which of its units that is
+  Rows rows;            // of that request, and its tokens
+  int len;
 };
 
 // What a block of rows costs besides its keys, in units (of half the bytes, quantised):
@@ -83,7 +91,7 @@ struct StreamPlan {
       if (w < warp) before += sh.warp_sum[w];
       total += sh.warp_sum[w];
     }
-    PlanPlace at = {total, 0, 0, c.B, 0};
+    PlanPlace at = {total, 0, 0, c.B, 0, {0, 0}, 0};
     const Deal deal(total, ctas);
     if (cta < deal.runs) {
       at.first = deal.start(cta);
@@ -98,11 +106,15 @@ struct StreamPlan {
         }
         sh.b = b;
         sh.in_request = rest;
+        sh.rows = request_rows(c, b);
+        sh.len = clamp_len(c, b);
       }
     }
     __syncthreads();
     at.b = sh.b;
     at.in_request = sh.in_request;
+    at.rows = sh.rows;
+    at.len = sh.len;
     return at;
   }
 };
@@ -271,33 +283,35 @@ struct State {
     for (int e = 0; e < E; ++e) o[e] = 0.f;
   }
   // ml: its maximum and sum; top: the largest maximum of all
+  template <bool kGlobal = false>
   __device__ void add(float2 ml, float top, const float* from, int lane) {
     const float w = ml.x == -CUDART_INF_F ? 1.f : ex2_approx(ml.x - top);
     l = fmaf(w, ml.y, l);
     if constexpr (E == 4) {
-      const float4 x = reinterpret_cast<const float4*>(from)[lane];
+      const float4* at = reinterpret_cast<const float4*>(from) + lane;
+      const float4 x = kGlobal ? __ldcg(at) : *at;
       o[0] = fmaf(w, x.x, o[0]);
       o[1] = fmaf(w, x.y, o[1]);
       o[2] = fmaf(w, x.z, o[2]);
       o[3] = fmaf(w, x.w, o[3]);
     } else {
-      const float2 x = reinterpret_cast<const float2*>(from)[lane];
+      const float2* at = reinterpret_cast<const float2*>(from) + lane;
+      const float2 x = kGlobal ? __ldcg(at) : *at;
       o[0] = fmaf(w, x.x, o[0]);
       o[1] = fmaf(w, x.y, o[1]);
     }
   }
-  // Adds up `parts` states, the k-th one in row state(k); returns the largest maximum.
-  // (With `step`, only every step-th of them, from `part` on.)
+  // Adds up `parts` states that other CTAs stored, the k-th one in row state(k) (read in
+  // L2, where they are); returns the largest maximum.
   template <class F>
-  __device__ float join(const PagedParams& p, int parts, int lane, F state, int part = 0,
-                        int step = 1) {
+  __device__ float join(const PagedParams& p, int parts, int lane, F state) {
     float top = -CUDART_INF_F;
-    for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.part_ml[state(k)].x);
+    for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(&p.part_ml[state(k)]).x);
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
 #pragma unroll 4
-    for (int k = part; k < parts; k += step)
-      add(p.part_ml[state(k)], top, p.part_o + state(k) * D, lane);
+    for (int k = 0; k < parts; ++k)
+      add<true>(__ldcg(&p.part_ml[state(k)]), top, p.part_o + state(k) * D, lane);
     return top;
   }
   __device__ void store(float* to, int lane) const {
@@ -320,6 +334,27 @@ struct State {
       p.lse[row] = l == 0.f ? -CUDART_INF_F : (top + log2f(l)) * 0.69314718055994530942f;
   }
 };
+
+// The next call's counts (all of them: that call may have more CTAs).
+__device__ __forceinline__ void clear_counts(const PagedParams& p) {
+  for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < kPagedCounts;
+       i += gridDim.x * blockDim.x)
+    p.clear[i] = 0;
+}
+
+// Says that a warp's stores of a part are done, of the rows counted in *count of the lanes
+// that have one; which of these lanes' rows have all `parts` of them stored now, so that
+// this warp, the last one, joins them.
+__device__ __forceinline__ uint32_t last_to_arrive(uint32_t* count, int parts, bool has) {
+  __syncwarp();
+  uint32_t before = 0;
+  if (has) {
+    __threadfence();
+    before = atomicAdd(count, 1u);
+    __threadfence();
+  }
+  return __ballot_sync(0xFFFFFFFFu, has && before + 1 == static_cast<uint32_t>(parts));
+}
 
 // Launches a kernel that may start while the one before it ends, and waits for that one
 // itself (griddepcontrol.wait) before it reads or writes anything but its parameters.

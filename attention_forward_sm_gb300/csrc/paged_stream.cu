@@ -6,8 +6,8 @@
 // read, so a call is bound by reading the cache once.  The keys of all blocks,
 // 64 to a unit, make one long sequence of units, which is dealt out evenly among the
 // CTAs (one per SM): a request of any length among any others costs its bytes.  A
-// block that ends up in several CTAs has a partial state (maximum, sum, O) in each;
-// paged_merge_kernel joins them.
+// block that ends up in several CTAs has a partial state (maximum, sum, O) in each; the
+// warp that is the last to store its part of a row joins them, in the CTAs' order.
 //
 // A CTA is one loading warp and eight computing warps around a ring of stages, one
 // unit each: K and V of 64 keys by tensor copies, a box per page.  A unit belongs to
@@ -40,6 +40,7 @@ constexpr int kThreads = (kWarps + 1) * 32;
 struct Unit {
   int flags, b, h, block;  // of kUnit..; request, KV head, block of rows
   int key0, len, slot;     // first key; tokens in the cache; partial state, -1: none
+  int cta0, parts;         // where the block's first part is; how many there are
   int row0, rows;          // first row of the dense tensors; new tokens
 };
 constexpr int kUnitFirst = 1, kUnitLast = 2, kUnitEnd = 4;  // a team's first and last of an
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
   // (its barriers also publish the mbarriers)
   const PlanPlace at = plan.place<kThreads>(ms.plan, blockIdx.x, p.ctas);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  clear_counts(p);
 
   if (warp == kWarps) {
     // ---- loading warp
@@ -169,10 +171,9 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
     uint32_t in_request = at.in_request;  // unit within the request
     const Deal deal(at.total, p.ctas);
     constexpr uint32_t kBlockCost = block_cost(kQuant);
-    PagedCut cut = {};
     for (uint32_t u = at.first; u < at.end && b < p.c.B && ok;) {
-      const Rows rows = request_rows(p.c, b);
-      const int len = clamp_len(p.c, b);
+      const Rows rows = b == at.b ? at.rows : request_rows(p.c, b);
+      const int len = b == at.b ? at.len : clamp_len(p.c, b);
       const uint32_t tiles = plan.tiles(len), units = plan.units(rows.n, len);
       const int blocks = plan.blocks(rows.n);
       int pbase = -64, ids = 0;
@@ -187,12 +188,11 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
         in_request += cost;
         const int h = static_cast<int>(item) / blocks, block = static_cast<int>(item) % blocks;
         const int slot = n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tile0 == 0);
-        if (n > 0 && n < tiles && tile0 == 0) {  // goes on in the next CTAs
-          const uint32_t rest = tiles - n;  // units behind at.end
-          uint32_t last = blockIdx.x + 1;
-          while (deal.start(last + 1) < at.end + rest) ++last;
-          cut = PagedCut{static_cast<int>(last - blockIdx.x) + 1, rows.first, rows.n, h,
-                         block * kRows};
+        int cta0 = 0, parts = 0;
+        if (n > 0 && n < tiles) {
+          const uint32_t key_units = u - cost - from + kBlockCost;  // where its key tiles begin
+          cta0 = static_cast<int>(deal.run_of(key_units));
+          parts = static_cast<int>(deal.run_of(key_units + tiles - 1)) - cta0 + 1;
         }
         // the teams take turns, so that both have as many units: one may be without keys
         const uint32_t both = (n + 1) & ~1u;
@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
           }
           if (lane == 0) {
             ms.unit[st] = Unit{(i < 2 ? kUnitFirst : 0) | (i + 2 >= both ? kUnitLast : 0),
-                               b, h, block, i < n ? key0 : len, len, slot, rows.first, rows.n};
+                               b, h, block, i < n ? key0 : len, len, slot, cta0, parts, rows.first,
+                               rows.n};
             mbar_arrive_expect_tx(
                 &ms.full[st],
                 static_cast<uint32_t>(2 * box * (n_box * kRowBytes +
@@ -260,7 +261,6 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
       ++b;
       in_request = 0;
     }
-    if (lane == 0) p.cuts[blockIdx.x] = cut;
     for (int i = 0; i < 2 && ok; ++i, ++s) {
       const uint32_t st = s % kStages;
       if (warp_all(mbar_wait(&ms.empty[st], ((s / kStages) & 1u) ^ 1u, abort_flag, p.err,
@@ -603,49 +603,23 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
         if (lane == 0) p.part_ml[to] = make_float2(top, sum.l);
       }
     }
+    if (un.slot >= 0) {
+      // the rows whose last part this was (lane i: the warp's i-th)
+      const int r0 = warp + lane * kWarps;
+      uint32_t last = last_to_arrive(&p.arrived[un.cta0 * 16 + min(r0, kRows - 1)], un.parts,
+                                     r0 < min(kRows, n_rows));
+      for (; last; last &= last - 1) {
+        const int r = warp + (__ffs(last) - 1) * kWarps, row = un.block * kRows + r;
+        State<D> all;
+        const float most = all.join(p, un.parts, lane, [&](int k) {
+          return (static_cast<size_t>(un.cta0 + k) * 2 + (k == 0)) * kRows + r;
+        });
+        all.finish(p, un.row0 + row / p.G, un.h * p.G + row % p.G, most, lane);
+      }
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms.merge_empty);
     ++merges;
-  }
-}
-
-// Joins the partial states of the items that were cut, block c that whose first part
-// CTA c has.  Rows are few and parts may be many: the warps share out rows first, then
-// a row's parts.
-template <int D>
-__global__ void __launch_bounds__(256) stream_merge_kernel(const __grid_constant__ PagedParams p,
-                                                           int block_rows) {
-  __shared__ alignas(16) float sums[8][D];
-  __shared__ float2 tops[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const PagedCut cut = p.cuts[blockIdx.x];
-  if (cut.parts == 0) return;
-  const int rows = min(block_rows, cut.left * p.G - cut.first);
-  const int groups = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;  // of warps, a row each
-  const int share = 8 / groups, part = warp % share;
-  for (int from = 0; from < rows; from += groups) {
-    const int r = from + warp / share;
-    State<D> sum;
-    float top = -CUDART_INF_F;
-    if (r < rows)
-      top = sum.join(
-          p, cut.parts, lane,
-          [&](int k) {
-            return (static_cast<size_t>(blockIdx.x + k) * 2 + (k == 0)) * block_rows + r;
-          },
-          part, share);
-    if (share > 1) {  // (then there is one turn)
-      sum.store(sums[warp], lane);
-      if (lane == 0) tops[warp] = make_float2(top, sum.l);
-      __syncthreads();
-      if (part == 0 && r < rows)
-        for (int i = 1; i < share; ++i) sum.add(tops[warp + i], top, sums[warp + i], lane);
-    }
-    if (part == 0 && r < rows) {
-      const int row = cut.first + r;
-      sum.finish(p, cut.row0 + row / p.G, cut.h * p.G + row % p.G, top, lane);
-    }
   }
 }
 
@@ -681,11 +655,7 @@ cudaError_t launch_paged_stream(const PagedParams& p, int rows, int dev, cudaStr
       {{launch_stream<128, false, 1>, launch_stream<128, false, 2>},
        {launch_stream<128, true, 1>, launch_stream<128, true, 2>}}};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  cudaError_t e = table[p.c.D == 128][p.c.quant][rows == 16](p, dev, stream);
-  if (e != cudaSuccess) return e;
-  if (p.ctas < 2) return cudaSuccess;
-  return launch_overlapped(p.c.D == 128 ? stream_merge_kernel<128> : stream_merge_kernel<64>,
-                           dim3(p.ctas - 1), 256, 0, stream, p, rows);
+  return table[p.c.D == 128][p.c.quant][rows == 16](p, dev, stream);
 }
 
 }  // namespace attn

@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
                                                  kItemCost + walk.item.n_kv * 1ll * kTileKeys);
         unsigned last = blockIdx.x + 1;
         while (at.deal.start(last + 1) < end) ++last;
-        cut = PagedCut{static_cast<int>(last - blockIdx.x) + 1, it.row0, it.left, it.h, 0};
+        cut = PagedCut{static_cast<int>(last - blockIdx.x) + 1, it.row0, it.left, it.h};
       }
       if (lane == 0) {
         it.slot = slot_first < 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + slot_first;
