@@ -126,9 +126,13 @@ struct StreamPlan {
 // the epilogue).  The costs of a request's items are in arithmetic progression, so
 // their sums have closed forms and nothing about them is stored.
 constexpr int kTileKeys = 128;
-constexpr int kItemCost = 256;
-constexpr int kLeastShare = 512;  // of a CTA: none is left without a key tile of an item that
-                                  // reaches into the next one
+constexpr int kItemCost = 512;
+// A CTA's share of the line at least: what an item that is cut costs its CTAs (partial
+// states of 128 KB, one after the other) is several key tiles, and no CTA may be left without
+// one of an item that reaches into the next.  Item cost and least share of 256 and 512,
+// 512 and 1024, 512 and 2048: requests of 1 to 500 tokens behind 64 to 6000 38, 35.5, 48 us;
+// of 77 to 700, D 64, 29.1, 28.3, 36.9; long chunks all the same.
+constexpr int kLeastShare = 1024;
 
 struct CostShared {
   long long warp_sum[32];

@@ -506,6 +506,8 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
         }
       }
     }
+    // (nothing orders a read whose value is still on its way before the next copy's writes)
+    fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms.empty[st]);
     if (!(un.flags & kUnitLast)) continue;

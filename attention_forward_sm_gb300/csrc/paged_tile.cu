@@ -240,8 +240,6 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
                                : *reinterpret_cast<const uint4*>(codes + q * (kStep * D));
           one(to + q * (kStep * 128), x, none ? 0u : f16_factor(scales[row], most) * 0x10001u);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.raw_empty[raw]);
       } else {
         // (their loads ahead of their stores, which might alias them)
         constexpr int kAhead = 2;
@@ -254,19 +252,20 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
             x[e] = *reinterpret_cast<const uint4*>(codes + (q + e) * (kStep * D));
             f[e] = scales[row0 + (q + e) * kStep];
           }
-          if (q + kAhead == kRounds) {  // read: the next one may come
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.raw_empty[raw]);
-          }
 #pragma unroll
           for (int e = 0; e < kAhead; ++e)
             one(to + (q + e) * (kStep * 128), x[e], (f[e] + 15u - most) * 0x04000400u);
         }
       }
       if (of_v) ++step;
+      // (also of the reads: without it, or ahead of what uses their values, the next copy
+      // may land before them)
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.kv_full[slot]);
+      if (lane == 0) {
+        mbar_arrive(&ms.kv_full[slot]);
+        mbar_arrive(&ms.raw_empty[raw]);
+      }
       if (++raw == C::kRaw) {
         raw = 0;
         ++raw_round;
@@ -529,23 +528,25 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         const int col = c * (D / 2) + kk * 32;
         if (!real) continue;
         if (whole) {
-          uint4* dst =
-              reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out_row * D + col);
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + out_row * D + col;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t w[4];
+          for (int g = 0; g < 2; ++g, dst += 16) {
+            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(v[8 * g + 2 * i]) * inv,
-                                 __uint_as_float(v[8 * g + 2 * i + 1]) * inv);
-            st_global_v4_evict_first(dst + g, w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 8; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(v[16 * g + 2 * i]) * inv,
+                                 __uint_as_float(v[16 * g + 2 * i + 1]) * inv);
+            if ((reinterpret_cast<uintptr_t>(p.o) & 31) == 0) {
+              st_global_v8(dst, w);
+            } else {
+              st_global_v4_evict_first(dst, w[0], w[1], w[2], w[3]);
+              st_global_v4_evict_first(dst + 8, w[4], w[5], w[6], w[7]);
+            }
           }
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + part_row * D + col);
+          // (whole sectors)
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            dst[g] = make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
-                                 __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
+          for (int g = 0; g < 4; ++g) st_global_v8(p.part_o + part_row * D + col + 8 * g, v + 8 * g);
         }
       }
       if (c == 0 && real) {
