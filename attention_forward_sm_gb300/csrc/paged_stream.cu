@@ -9,17 +9,17 @@
 // block that ends up in several CTAs has a partial state (maximum, sum, O) in each; the
 // warp that is the last to store its part of a row joins them, in the CTAs' order.
 //
-// A CTA is one loading warp and eight computing warps around a ring of stages, one
-// unit each: K and V of 64 keys by tensor copies, a box per page.  A unit belongs to
-// four of the computing warps, 16 keys each, every other unit to the other four.
+// A CTA is one or two loading warps and two teams of four computing ones around a ring of
+// stages, one unit each: K and V of 64 keys by tensor copies, a box per page.  Every other
+// unit is the first team's, 16 keys a warp, the rest the second's.
 // Rows are few, so the keys are the rows of the products (mma.sync m16n8k16):
 //   S^T [16 keys, 8 rows] = K [16, D] Q^T,   O^T [D, 8 rows] += V^T [D, 16] P^T.
 // A tcgen05.mma has at least 64 rows of one operand in shared memory or TMEM and
 // would take the keys through either; here they go from shared memory straight into
-// registers, where e4m3 codes become bf16 on the way.  Which key and which
+// registers, where e4m3 codes become f16 on the way.  Which key and which
 // dimension a thread's piece of an operand stands for is free as long as both
 // operands agree, and chosen so that every load is 16 bytes of a swizzled row
-// without bank conflicts: row i of a 16-key block is key kKey(i), and a thread
+// without bank conflicts: row i of a 16-key block is key block_key(i), and a thread
 // has whole 16-byte pieces of the keys' rows.  P^T is S^T transposed within a warp
 // (movmatrix).
 #include <math_constants.h>
@@ -33,10 +33,10 @@
 namespace attn {
 namespace {
 
-constexpr int kWarps = 8;  // computing
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kTeams = 2;
+constexpr int kWarps = 4 * kTeams;  // computing
 
-// One unit in the ring, as the loading warp describes it.
+// One unit in the ring, as a loading warp describes it.
 struct Unit {
   int flags, b, h, block;  // of kUnit..; request, KV head, block of rows
   int key0, len, slot;     // first key; tokens in the cache; partial state, -1: none
@@ -48,23 +48,29 @@ constexpr int kUnitFirst = 1, kUnitLast = 2, kUnitEnd = 4;  // a team's first an
 
 template <int D, bool kQuant, int NT>
 struct StreamCfg {
+  // A unit costs a loading warp some 1300 cycles, one after another; quantised, 700 cycles
+  // bring one in, so each team has a loader of its own (64 requests of 16 to 12000 tokens
+  // 57 -> 51 us).  bf16 units are on their way for 1400 (the same requests 77 us, with
+  // two 82).
+  static constexpr int kLoaders = kQuant ? kTeams : 1;
+  static constexpr int kThreads = (kWarps + kLoaders) * 32;
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowBytes = kQuant ? D : 2 * D;
   static constexpr int kTile = kUnitKeys * kRowBytes;  // K or V of a unit
   static constexpr int kScales = kQuant ? 2 * kUnitKeys : 0;
-  static constexpr int kMerge = kWarps / 2 * kRows * D * 4;
+  static constexpr int kMerge = (kWarps - 4) * kRows * D * 4;
   // Two CTAs on an SM where the registers allow it: one joins its warps' states and
   // stores while the other goes on.
   static constexpr int kCtas = kQuant && NT == 1 ? 2 : 1;
-  // As many stages as fit beside the buffer for merging, at most 16, and an even number:
-  // a stage belongs to one team, which so sees every phase of its barrier.
+  // As many stages as fit beside the buffer for merging, at most 16, and a multiple of the
+  // teams: a stage belongs to one of them, which so sees every phase of its barrier.
   static constexpr int kRoom = (kCtas == 1 ? 227 : 113) * 1024 - 3072 - kMerge;
   static constexpr int kFit = kRoom / (2 * kTile + kScales);
-  static constexpr int kStages = kFit < 16 ? kFit / 2 * 2 : 16;
+  static constexpr int kStages = (kFit < 16 ? kFit : 16) / kTeams * kTeams;
   static constexpr int kOffMerge = kStages * 2 * kTile;
   static constexpr int kOffScales = kOffMerge + kMerge;
   static constexpr int kSmem = kOffScales + kStages * kScales + 1024;  // + alignment
-  static_assert(kStages >= 2 && kStages % 2 == 0, "shared memory");
+  static_assert(kStages >= kTeams, "shared memory");
 };
 
 template <int kStages, int kRows>
@@ -129,10 +135,11 @@ __device__ __forceinline__ uint32_t swizzled(int row, int at) {
 }
 
 template <int D, bool kQuant, int NT>
-__global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
+__global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
     paged_stream_kernel(const __grid_constant__ PagedParams p) {
   using C = StreamCfg<D, kQuant, NT>;
   constexpr int kStages = C::kStages, kRows = C::kRows, kRowBytes = C::kRowBytes;
+  constexpr int kLoaders = C::kLoaders, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   __shared__ StreamShared<kStages, kRows> ms;
@@ -143,10 +150,10 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ms.full[s], 1);
-      mbar_init(&ms.empty[s], kWarps / 2);
+      mbar_init(&ms.empty[s], 4);
     }
-    mbar_init(&ms.team_full, kWarps / 2);
-    mbar_init(&ms.merge_full, kWarps / 2);
+    mbar_init(&ms.team_full, kWarps - 4);
+    mbar_init(&ms.merge_full, 4);
     mbar_init(&ms.merge_empty, kWarps);
     ms.abort_flag = 0;
     fence_mbar_init();
@@ -160,12 +167,13 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   clear_counts(p);
 
-  if (warp == kWarps) {
-    // ---- loading warp
+  if (warp >= kWarps) {
+    // ---- a loading warp: of every kLoaders-th unit
+    const uint32_t loader = static_cast<uint32_t>(warp - kWarps);
     const int box_bits = min(p.c.page_bits, 6), box = 1 << box_bits;
     static_assert(kUnitKeys == 64, "box_bits");
     const uint64_t policy = l2_policy_evict_first();
-    uint32_t s = 0;
+    uint32_t s = loader;
     bool ok = true;
     int b = at.b;
     uint32_t in_request = at.in_request;  // unit within the request
@@ -194,9 +202,9 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
           cta0 = static_cast<int>(deal.run_of(key_units));
           parts = static_cast<int>(deal.run_of(key_units + tiles - 1)) - cta0 + 1;
         }
-        // the teams take turns, so that both have as many units: one may be without keys
-        const uint32_t both = (n + 1) & ~1u;
-        for (uint32_t i = 0; i < both; ++i, ++s) {
+        // the teams take turns, so that all have as many units: some may be without keys
+        const uint32_t all = (n + kTeams - 1) / kTeams * kTeams;
+        for (uint32_t i = loader; i < all; i += kLoaders, s += kLoaders) {
           const int key0 = static_cast<int>(tile0 + i) * kUnitKeys;
           const uint32_t st = s % kStages;
           // pages of this unit: lane l holds entry pbase + l of the table's row
@@ -228,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
             __syncwarp();
           }
           if (lane == 0) {
-            ms.unit[st] = Unit{(i < 2 ? kUnitFirst : 0) | (i + 2 >= both ? kUnitLast : 0),
+            ms.unit[st] = Unit{(i < kTeams ? kUnitFirst : 0) | (i + kTeams >= all ? kUnitLast : 0),
                                b, h, block, i < n ? key0 : len, len, slot, cta0, parts, rows.first,
                                rows.n};
             mbar_arrive_expect_tx(
@@ -261,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
       ++b;
       in_request = 0;
     }
-    for (int i = 0; i < 2 && ok; ++i, ++s) {
+    for (int i = 0; i < kTeams / kLoaders && ok; ++i, s += kLoaders) {
       const uint32_t st = s % kStages;
       if (warp_all(mbar_wait(&ms.empty[st], ((s / kStages) & 1u) ^ 1u, abort_flag, p.err,
                              kErrWaitLoad, p.wait_limit_ns)) &&
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
       __syncwarp();
     }
     if (abort_set(abort_flag))  // copies in flight land before the CTA leaves
-      for (uint32_t i = s > kStages ? s - kStages : 0u; i < s; ++i)
+      for (uint32_t i = s >= kStages ? s - kStages : loader; i < s; i += kLoaders)
         drain_wait(&ms.full[i % kStages], (i / kStages) & 1u);
     return;
   }
@@ -288,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
   float o[NT][kSteps][4], m[NT][2], l[NT][2], by_row[NT][2];
   int vis[NT][2], first_vis = 0;
   uint32_t merges = 0;
-  for (uint32_t s = static_cast<uint32_t>(warp) / 4;; s += 2) {  // the team's units
+  for (uint32_t s = static_cast<uint32_t>(warp) / 4;; s += kTeams) {  // the team's units
     const uint32_t st = s % kStages;
     if (!warp_all(mbar_wait(&ms.full[st], (s / kStages) & 1u, abort_flag, p.err, kErrWaitMma,
                             p.wait_limit_ns)))
@@ -512,9 +520,10 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
     if (lane == 0) mbar_arrive(&ms.empty[st]);
     if (!(un.flags & kUnitLast)) continue;
 
-    // ---- the warps' states of the block, joined through shared memory: the second team's
+    // ---- the warps' states of the block, joined through shared memory: the other teams'
     // with the first team's, register by register, then those four by rows
-    float* const merge = reinterpret_cast<float*>(smem + C::kOffMerge) + (warp & 3) * kRows * D;
+    float* const merge = reinterpret_cast<float*>(smem + C::kOffMerge) +
+                         (warp < 4 ? warp : warp - 4) * kRows * D;
     if (!warp_all(mbar_wait(&ms.merge_empty, (merges & 1u) ^ 1u, abort_flag, p.err, kErrWaitCorr,
                             p.wait_limit_ns)))
       return;
@@ -546,26 +555,29 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
                               p.wait_limit_ns)))
         return;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float a[2], e[2];
+      for (int team = 1; team < kTeams; ++team)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 ml = ms.ml[warp + 4][nt * 8 + 2 * t + k];
-          const float top = fmaxf(m[nt][k], ml.x);
-          a[k] = m[nt][k] == -CUDART_INF_F ? 1.f : ex2_approx(m[nt][k] - top);
-          e[k] = ml.x == -CUDART_INF_F ? 1.f : ex2_approx(ml.x - top);
-          m[nt][k] = top;
-          l[nt][k] = l[nt][k] * a[k] + ml.y * e[k];
-        }
+        for (int nt = 0; nt < NT; ++nt) {
+          float a[2], e[2];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const float4 x = mine[(nt * kSteps + i) * 32];
-          o[nt][i][0] = o[nt][i][0] * a[0] + x.x * e[0];
-          o[nt][i][1] = o[nt][i][1] * a[1] + x.y * e[1];
-          o[nt][i][2] = o[nt][i][2] * a[0] + x.z * e[0];
-          o[nt][i][3] = o[nt][i][3] * a[1] + x.w * e[1];
+          for (int k = 0; k < 2; ++k) {
+            const float2 ml = ms.ml[warp + 4 * team][nt * 8 + 2 * t + k];
+            const float top = fmaxf(m[nt][k], ml.x);
+            a[k] = m[nt][k] == -CUDART_INF_F ? 1.f : ex2_approx(m[nt][k] - top);
+            e[k] = ml.x == -CUDART_INF_F ? 1.f : ex2_approx(ml.x - top);
+            m[nt][k] = top;
+            l[nt][k] = l[nt][k] * a[k] + ml.y * e[k];
+          }
+          const float4* theirs = mine + (team - 1) * (kRows * D);  // (4 warps' parts further)
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const float4 x = theirs[(nt * kSteps + i) * 32];
+            o[nt][i][0] = o[nt][i][0] * a[0] + x.x * e[0];
+            o[nt][i][1] = o[nt][i][1] * a[1] + x.y * e[1];
+            o[nt][i][2] = o[nt][i][2] * a[0] + x.z * e[0];
+            o[nt][i][3] = o[nt][i][3] * a[1] + x.w * e[1];
+          }
         }
-      }
       __syncwarp();  // (the warp's part of the buffer is read)
       say(warp);
 #pragma unroll
@@ -591,9 +603,9 @@ __global__ void __launch_bounds__(kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
       State<D> sum;
       float top = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < kWarps / 2; ++i) top = fmaxf(top, ms.ml[i][r].x);
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, ms.ml[i][r].x);
 #pragma unroll
-      for (int i = 0; i < kWarps / 2; ++i)
+      for (int i = 0; i < 4; ++i)
         sum.add(ms.ml[i][r], top,
                 reinterpret_cast<float*>(smem + C::kOffMerge) + (i * kRows + r) * D, lane);
       const int row = un.block * kRows + r;
@@ -635,7 +647,7 @@ cudaError_t launch_stream(const PagedParams& p, int dev, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
-  return launch_overlapped(paged_stream_kernel<D, kQuant, NT>, dim3(p.ctas), kThreads, C::kSmem,
+  return launch_overlapped(paged_stream_kernel<D, kQuant, NT>, dim3(p.ctas), C::kThreads, C::kSmem,
                            stream, p);
 }
 
