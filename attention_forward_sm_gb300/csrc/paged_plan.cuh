@@ -58,16 +58,18 @@ struct StreamPlan {
   __device__ uint32_t tiles(int len) const {
     return static_cast<uint32_t>(max(1, (len + kUnitKeys - 1) / kUnitKeys));
   }
-  __device__ int blocks(int n) const {
-    return static_cast<int>((static_cast<long long>(n) * G + block_rows - 1) / block_rows);
+  __device__ int blocks(int n) const {  // of 8 or 16 rows
+    return static_cast<int>((static_cast<long long>(n) * G + block_rows - 1) >>
+                            (block_rows == 8 ? 3 : 4));
   }
   __device__ uint32_t units(int n, int len) const {
     return static_cast<uint32_t>(c.Hkv) * static_cast<uint32_t>(blocks(n)) *
            (tiles(len) + block_cost);
   }
   __device__ uint32_t units_of(int b) const {
+    const int len = clamp_len(c, b);  // (its load beside the others)
     const Rows rows = request_rows(c, b);
-    return rows.n > 0 ? units(rows.n, clamp_len(c, b)) : 0;
+    return rows.n > 0 ? units(rows.n, len) : 0;
   }
   // Where CTA `cta` of `ctas` begins and ends; all kThreads threads call this.
   template <int kThreads>
@@ -286,36 +288,49 @@ struct State {
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
   }
+  using Vec = std::conditional_t<E == 4, float4, float2>;
   // ml: its maximum and sum; top: the largest maximum of all
-  template <bool kGlobal = false>
-  __device__ void add(float2 ml, float top, const float* from, int lane) {
+  __device__ void add(float2 ml, float top, const Vec& x) {
     const float w = ml.x == -CUDART_INF_F ? 1.f : ex2_approx(ml.x - top);
     l = fmaf(w, ml.y, l);
+    o[0] = fmaf(w, x.x, o[0]);
+    o[1] = fmaf(w, x.y, o[1]);
     if constexpr (E == 4) {
-      const float4* at = reinterpret_cast<const float4*>(from) + lane;
-      const float4 x = kGlobal ? __ldcg(at) : *at;
-      o[0] = fmaf(w, x.x, o[0]);
-      o[1] = fmaf(w, x.y, o[1]);
       o[2] = fmaf(w, x.z, o[2]);
       o[3] = fmaf(w, x.w, o[3]);
-    } else {
-      const float2* at = reinterpret_cast<const float2*>(from) + lane;
-      const float2 x = kGlobal ? __ldcg(at) : *at;
-      o[0] = fmaf(w, x.x, o[0]);
-      o[1] = fmaf(w, x.y, o[1]);
     }
   }
+  __device__ void add(float2 ml, float top, const float* from, int lane) {
+    add(ml, top, reinterpret_cast<const Vec*>(from)[lane]);
+  }
   // Adds up `parts` states that other CTAs stored, the k-th one in row state(k) (read in
-  // L2, where they are); returns the largest maximum.
+  // L2, where they are), four at a time; returns the largest maximum.
   template <class F>
   __device__ float join(const PagedParams& p, int parts, int lane, F state) {
     float top = -CUDART_INF_F;
-    for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(&p.part_ml[state(k)]).x);
+    for (int k0 = 0; k0 < parts; k0 += 4) {
+      float2 ml[4];
+      Vec x[4];
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k)
-      add<true>(__ldcg(&p.part_ml[state(k)]), top, p.part_o + state(k) * D, lane);
+      for (int i = 0; i < 4; ++i) {
+        ml[i] = make_float2(-CUDART_INF_F, 0.f);
+        x[i] = Vec{};
+        if (k0 + i >= parts) continue;
+        const size_t row = state(k0 + i);
+        ml[i] = __ldcg(&p.part_ml[row]);
+        x[i] = __ldcg(reinterpret_cast<const Vec*>(p.part_o + row * D) + lane);
+      }
+      float most = top;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) most = fmaxf(most, ml[i].x);
+      const float alpha = top == -CUDART_INF_F ? 1.f : ex2_approx(top - most);
+      top = most;
+      l *= alpha;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= alpha;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add(ml[i], top, x[i]);
+    }
     return top;
   }
   __device__ void store(float* to, int lane) const {
