@@ -411,14 +411,18 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         }
         tc_fence_after();
         float s[64];
-        if constexpr (kQuant) {  // (the launch's 80 registers do not hold 64 at once)
+        [[maybe_unused]] uint2 by = make_uint2(127, 127);
+        if constexpr (kQuant) {
+          // (there since S is: its operands were converted before)
+          by = ms.kv_scale[(steps + static_cast<uint32_t>(j - it.tile0)) % 8];
+          // (in two: the launch's 80 registers do not hold 64 results of one instruction)
+          uint32_t sr[2][32];
+          tmem_ld_pair32_start<64>(s_addr, sr[0]);
+          tmem_ld_pair32_start<64>(s_addr + 32, sr[1]);
+          tmem_ld_finish(sr[0]);
+          tmem_ld_finish(sr[1]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t sr[32];
-            tmem_ld_pair32<64>(s_addr + 32 * h, sr);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[32 * h + i] = __uint_as_float(sr[i]);
-          }
+          for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i / 32][i % 32]);
         } else {
           uint32_t sr[64];
           tmem_ld_pair64<64>(s_addr, sr);
@@ -456,8 +460,6 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         float scale = p.scale_log2;
         [[maybe_unused]] float e = 0.f, sum_scale = 1.f;
         if constexpr (kQuant) {
-          // (there since S is: its operands were converted before)
-          const uint2 by = ms.kv_scale[(steps + static_cast<uint32_t>(j - it.tile0)) % 8];
           scale = row_scale * scale_value(by.x);
           e = scale_exponent(by.y);
           sum_scale = __uint_as_float((254u - by.y) << 23);

@@ -413,6 +413,27 @@ __device__ __forceinline__ void tmem_ld_pair32(uint32_t taddr, uint32_t (&r)[32]
       : "r"(taddr), "n"(kHalf)
       : "memory");
 }
+// The same without the wait, and the wait for all such loads of the warp, after which r may
+// be used.
+template <uint32_t kHalf>
+__device__ __forceinline__ void tmem_ld_pair32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32], %33;"
+      : ATTN_R8(0), ATTN_R8(8), ATTN_R8(16), ATTN_R8(24)
+      : "r"(taddr), "n"(kHalf)
+      : "memory");
+}
+#define ATTN_RW8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), \
+    "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void tmem_ld_finish(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : ATTN_RW8(0), ATTN_RW8(8), ATTN_RW8(16), ATTN_RW8(24)
+               :
+               : "memory");
+}
+#undef ATTN_RW8
 template <uint32_t kHalf>
 __device__ __forceinline__ void tmem_ld_pair16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
