@@ -76,6 +76,8 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 // 2^(120 + e) is code * 2^e, exact.  Scale bytes (e + 127) above 134 would take the
 // factor out of bf16: what is above is a second one.
 constexpr uint32_t kScaleNan = 255, kScaleMost = 134;
+// The least scale that a row has, 2^-100; a row of zeros has 2^0.
+constexpr uint32_t kScaleLeast = 27, kScaleOfZeros = 127;
 
 // The codes in bytes 1 and 3 of u (the others do not matter), times the factors f.
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t u, uint32_t f) {
@@ -109,6 +111,7 @@ __device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
 __device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
   return e4m3x2_to_f16x2(static_cast<uint16_t>(x >> 16));
 }
+__device__ __forceinline__ uint32_t or_of(const uint4& x) { return x.x | x.y | x.z | x.w; }
 // 2^e and e of a scale byte; NaN for the one that says so.
 __device__ __forceinline__ float scale_value(uint32_t scale) {
   return __uint_as_float(scale == kScaleNan ? 0x7FFFFFFFu : scale << 23);

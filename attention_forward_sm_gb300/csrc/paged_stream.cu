@@ -228,11 +228,11 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
           const uint32_t bad = __ballot_sync(0xFFFFFFFFu, lane < n_box && !good);
           uint8_t* scales = smem + C::kOffScales + st * C::kScales + lane * box;
           if (bad) {
-            // a page of zeros: the copies fill with them; its scales are written here
+            // a page of zeros: the copies fill with them; its scales, the least, are written here
             if (lane == 0) atomicOr(p.err, kErrPage);
             if (kQuant && (bad >> lane & 1u))
               for (int i = 0; i < 2 * box; ++i)
-                scales[(i < box ? 0 : kUnitKeys) + i % box] = 127;
+                scales[(i < box ? 0 : kUnitKeys) + i % box] = kScaleLeast;
             __syncwarp();
           }
           if (lane == 0) {
@@ -413,12 +413,24 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
       // Quantised, a weight of V's codes is 2^(x + e), e the exponent of V's scale, and the
       // maximum is of x + e: then no weight is more than 2^8, and what f16 loses (steps
       // of 2^-24) is next to the largest product, since every row of codes reaches
-      // beyond 224.  The sum of weights is of 2^x, over the same reference.
+      // beyond 224 but one of zeros, which says 2^0 and counts as the least.  The sum of
+      // weights is of 2^x, over the same reference.
       float ev[2] = {0.f, 0.f};
       [[maybe_unused]] uint32_t vscale[2] = {127, 127};
       if constexpr (kQuant) {
         vscale[0] = scales[kUnitKeys + row_lo];
         vscale[1] = scales[kUnitKeys + row_hi];
+        if (__any_sync(0xFFFFFFFFu, vscale[0] == kScaleOfZeros || vscale[1] == kScaleOfZeros)) {
+          const int rows[2] = {row_lo, row_hi};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t bits = vscale[k] == kScaleOfZeros ? 0u : ~0u;
+#pragma unroll 1
+            for (int at = 0; at < D; at += 16)
+              bits |= or_of(*reinterpret_cast<const uint4*>(vtile + swizzled<kRowBytes>(rows[k], at)));
+            if (!(bits & 0x7F7F7F7Fu)) vscale[k] = kScaleLeast;
+          }
+        }
         if (vscale[0] != kScaleNan) ev[0] = scale_exponent(vscale[0]);
         if (vscale[1] != kScaleNan) ev[1] = scale_exponent(vscale[1]);
       }

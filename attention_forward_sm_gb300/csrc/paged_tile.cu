@@ -182,25 +182,38 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
     *reinterpret_cast<uint4*>(to + (at0 ^ 16u)) = make_uint4(y[4], y[5], y[6], y[7]);
   };
   // The largest of a tile's scales, and whether all are within 14 of it and there is
-  // nothing odd: then every factor is a normal f16 number.
-  auto largest = [&](const uint8_t* scales, bool whole, int rows, uint32_t bad, bool* plain) {
+  // nothing odd: then every factor is a normal f16 number.  Else only rows count that are
+  // there and not NaN, nor zeros, whose scale says 2^0 and could leave nothing of the
+  // others; landed() says that the codes are in place (false: they never will be).
+  auto largest = [&](const uint8_t* scales, const uint8_t* codes, bool whole, int rows, uint32_t bad,
+                     bool* plain, uint32_t* most, auto landed) {
     const uint32_t w = reinterpret_cast<const uint32_t*>(scales)[lane];
-    const uint32_t s0 = w & 255u, s1 = w >> 8 & 255u, s2 = w >> 16 & 255u, s3 = w >> 24;
-    uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(max(s0, s1), max(s2, s3)));
-    const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(min(s0, s1), min(s2, s3)));
-    *plain = whole && most != kScaleNan && most - least <= 14;
-    if (!*plain) {  // of rows that are there and not NaN; 27 if there is none
-      most = 27;
-      const uint32_t s[4] = {s0, s1, s2, s3};
+    uint32_t s[4] = {w & 255u, w >> 8 & 255u, w >> 16 & 255u, w >> 24};
+    *most = __reduce_max_sync(0xFFFFFFFFu, max(max(s[0], s[1]), max(s[2], s[3])));
+    const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(min(s[0], s[1]), min(s[2], s[3])));
+    *plain = whole && *most != kScaleNan && *most - least <= 14;
+    if (*plain) return true;
+    bool zeros = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * lane + i;
+      if (s[i] == kScaleNan || row >= rows || (bad >> (row >> p.c.page_bits) & 1u))
+        s[i] = kScaleLeast;
+      zeros = zeros || s[i] == kScaleOfZeros;
+    }
+    if (__any_sync(0xFFFFFFFFu, zeros)) {
+      if (!landed()) return false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = 4 * lane + i;
-        if (s[i] != kScaleNan && row < rows && !(bad >> (row >> p.c.page_bits) & 1u))
-          most = max(most, s[i]);
+        uint32_t bits = s[i] == kScaleOfZeros ? 0u : ~0u;
+#pragma unroll 1
+        for (int at = 0; at < D; at += 16)
+          bits |= or_of(*reinterpret_cast<const uint4*>(codes + (4 * lane + i) * D + at));
+        if (!(bits & 0x7F7F7F7Fu)) s[i] = kScaleLeast;
       }
-      most = __reduce_max_sync(0xFFFFFFFFu, most);
     }
-    return most;
+    *most = __reduce_max_sync(0xFFFFFFFFu, max(max(s[0], s[1]), max(s[2], s[3])));
+    return true;
   };
 
   uint32_t raw = 0, raw_round = 0, slot = 0, round = 0, step = 0;
@@ -218,12 +231,18 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
       const bool of_v = i & 1;
       const int there = it.len - (it.tile0 + static_cast<int>(i >> 1)) * kBN;  // rows
       const uint32_t bad = ms.raw_bad[raw];
-      const uint8_t* codes = smem + C::kOffRaw + raw * C::kRawBytes + tid * 16;
+      const uint8_t* tile = smem + C::kOffRaw + raw * C::kRawBytes;
+      const uint8_t* codes = tile + tid * 16;
       const uint8_t* scales = smem + C::kOffScale + raw * C::kScaleBytes;
       const bool whole = there >= kBN && !bad;
       if (!of_v) {
-        most = largest(scales, whole, there, bad, &plain);
-        next_most = largest(scales + kBN, whole, there, bad, &next_plain);
+        // (V's raw tile is the next one, and comes in while this one is held)
+        if (!largest(scales, tile, whole, there, bad, &plain, &most, [] { return true; }) ||
+            !largest(scales + kBN, tile + C::kRawBytes, whole, there, bad, &next_plain, &next_most, [&] {
+              return warp_all(mbar_wait(&ms.raw_full[raw + 1], raw_round & 1, abort_flag, p.err,
+                                        kErrWaitLoad, p.wait_limit_ns));
+            }))
+          return;
         if (tid == 0) ms.kv_scale[step % 8] = make_uint2(most, next_most);
       } else {
         most = next_most;
@@ -460,7 +479,8 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         float scale = p.scale_log2;
         [[maybe_unused]] float e = 0.f, sum_scale = 1.f;
         if constexpr (kQuant) {
-          scale = row_scale * scale_value(by.x);
+          // (never 0, as scale_log2: the product of a row of zeros and the smallest of scales)
+          scale = fmaxf(row_scale * scale_value(by.x), 1e-37f);
           e = scale_exponent(by.y);
           sum_scale = __uint_as_float((254u - by.y) << 23);
         }

@@ -20,7 +20,7 @@ def _randn(shape, seed, sigma=1.0):
     return (torch.randn(shape, generator=g) * sigma).to(BF16).cuda()
 
 
-def check_attention(o, lse, q, cache, offsets, causal=True, scale=None):
+def check_attention(o, lse, q, cache, offsets, causal=True, scale=None, more=0.0):
     """|dO| <= 2^-8 (sum_j w_j |v_j| + |O|): a weight and the output are each rounded to bf16
     once, off by half a step, 2^-8, at most; a fiftieth more for everything in 32 bits.
     |dLSE|: a score is a sum of D products in 32 bits, each addition off by 2^-23 of the
@@ -37,7 +37,7 @@ def check_attention(o, lse, q, cache, offsets, causal=True, scale=None):
     empty = torch.isinf(rl)
     assert torch.equal(torch.isinf(lse) & (lse < 0), empty)
     norm = max((float(k.norm(dim=-1).max()) for k, _ in cache.dense if k.numel()), default=0.0)
-    tol = cache.D * 2.0 ** -23 * scale * norm * float(q.float().norm(dim=-1).max()) + 2.0 ** -21
+    tol = cache.D * 2.0 ** -23 * scale * norm * float(q.float().norm(dim=-1).max()) + 2.0 ** -21 + more
     far = (lse - rl)[~empty].abs() - rl[~empty].abs() * 2.0 ** -23
     assert far.numel() == 0 or float(far.max()) <= tol, (float(far.max()), tol)
     assert attn.attn_get_device_error() == 0
@@ -284,6 +284,31 @@ def test_scales_of_every_size(new):
     q = _randn((new, 4, 128), 13, sigma=1e-3)
     o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, scale=0.05, **c.scales())
     check_attention(o, lse, q, c, offsets, scale=0.05)
+
+
+@pytest.mark.parametrize("sigma", [1.0, 1e-8, 1e-25])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("G,new", [(4, 1), (4, 3), (2, 70)])
+def test_zeros_beside_small_values(sigma, D, page, G, new):
+    """Rows of zeros have the scale 2^0, however small the others are; a query of zeros."""
+    lens = [150, 300]
+    c = ref.Cache(lens, 1, D, page, True, seed=16, sigma=sigma)
+    for b, n in enumerate(lens):
+        k, v = c.dense[b]
+        for i in [0, 5, 64, 65, n - 1] + list(range(100, 140)):
+            at, slot = int(c.table[b, i // page]), i % page
+            for pages, scale, x in ((c.kp, c.ks, k), (c.vp, c.vs, v)):
+                pages.view(torch.uint8)[at, 0, slot] = 0x80 * (i % 2)
+                scale[at, 0, slot] = 127
+                x[i] = 0
+    offsets = ref.offsets_of([new, new])
+    q = _randn((2 * new, G, D), 17)
+    q[0] = q[-1, 1:] = 0
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
+    # The sum of weights is over 2^m with m near the exponents of V's scales, 64 to 128 in
+    # magnitude at most: a score less m is rounded by 2^-18, the sum's logarithm is off by 2^-17.
+    check_attention(o, lse, q, c, offsets, more=math.log(2) * (2.0 ** -18 + 2.0 ** -17))
 
 
 @pytest.mark.parametrize("new", [1, 5, 70])
