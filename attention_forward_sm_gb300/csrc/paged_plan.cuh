@@ -138,7 +138,7 @@ constexpr int kLeastShare = 1024;
 
 struct CostShared {
   long long warp_sum[32];
-  long long total, rest;
+  long long rest;
   int b;
 };
 // The line of all costs in `runs` equal stretches.

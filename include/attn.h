@@ -498,14 +498,25 @@ int attn_cache_read(const void *kpages, const void *vpages, const unsigned char 
  *
  * The row at position p sees with causal != 0 the keys 0 .. p of its request, else
  * all lens[b] of them.  A row that sees none gives O = 0 and LSE = -infinity.
- * Numerics as attn_fwd.  A key that a row does not see has no influence on it; V may
- * hold anything behind lens[b], but a NaN or infinity in V at a position below
- * lens[b] may reach all rows of the same (request, KV head).
+ * A key that a row does not see has no influence on it; V may hold anything behind
+ * lens[b], but a NaN or infinity in V at a position below lens[b] may reach all rows
+ * of the same (request, KV head).
+ *
+ * Numerics as attn_fwd; quantised, weights and queries are rounded to f16 (queries over
+ * a power of two that makes a row's largest element 1 to 2) and products with the
+ * codes are exact.  f16 ends 2^-24 below 1: next to a row of V 2^24 times as
+ * large, a row has little or no influence however large its weight, and likewise a
+ * query's elements 2^24 below its largest.  (Rows of zeros count as the smallest.)  Where
+ * scales of V lie more than 2^96 apart within a request, O and LSE lose keys.
+ *
+ * max_new * Hq / Hkv up to 16, or M * page above 2^18, takes the kernel for few rows,
+ * which reads the cache once for every 16 rows; else that for many rows, which reads it
+ * once for every 2 * (128 / (Hq / Hkv)) tokens.
  *
  * Limits: Hq % Hkv == 0, Hq <= 65535, Hq / Hkv <= 128, max_new >= 0; scale finite and
  * >= 0; the rows times the keys in units of work within 32 bits:
- * (T * Hq / Hkv / 8 + B) * Hkv * (M * page / 64 + 5) < 2^31.  Scratch as
- * attn_decode_varlen.
+ * (T * Hq / Hkv / 8 + B) * Hkv * (M * page / 64 + 5) < 2^31.  Scratch, about 40
+ * MB at most: a buffer per stream as attn_decode_varlen, the kernel for few rows one of its own.
  */
 int attn_paged_fwd(const void *q, long long q_stride, const void *kpages, const void *vpages,
                    const unsigned char *kscale, const unsigned char *vscale, const int *table,
