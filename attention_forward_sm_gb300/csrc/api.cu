@@ -174,22 +174,24 @@ int encode_queries(CUtensorMap* map, const void* base, int D, int G, int Hkv, in
   return encode_4d(map, base, D, G, Hkv, B, requests, stride);
 }
 
-// 3-D view [P * Hkv, page, D] of a cache's pages, box {128 bytes of a row, rows, 1}.
-int encode_pages(CUtensorMap* map, const void* base, const PagedArrays& c, int box_rows) {
+// 4-D view [P * Hkv, pieces, page, 128 bytes] of a cache's pages, a piece being 128 bytes
+// of every row (or the whole of narrower ones); box: `rows` rows of one piece or of all.
+int encode_pages(CUtensorMap* map, const void* base, const PagedArrays& c, int rows, bool all) {
   PFN_cuTensorMapEncodeTiled_v12000 fn;
   if (int rc = encode_fn(&fn)) return rc;
-  const int elem = c.quant ? 1 : 2, row = c.D * elem;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.page),
+  const int elem = c.quant ? 1 : 2, row = c.D * elem, piece = row < 128 ? row : 128;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(piece / elem), static_cast<cuuint64_t>(c.page),
+                              static_cast<cuuint64_t>(row / piece),
                               static_cast<cuuint64_t>(c.P) * c.Hkv};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row),
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(piece),
                                  static_cast<cuuint64_t>(c.page) * row};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(row < 128 ? c.D : 128 / elem),
-                             static_cast<cuuint32_t>(box_rows), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(piece / elem), static_cast<cuuint32_t>(rows),
+                             static_cast<cuuint32_t>(all ? row / piece : 1), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = encode_in_context(
-      fn, map, c.quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+      fn, map, c.quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
       const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-      row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+      piece < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_TMA;
 }

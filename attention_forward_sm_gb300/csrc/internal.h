@@ -271,7 +271,7 @@ struct PagedCut {
 // Attention of new tokens over a paged cache.
 constexpr uint32_t kPagedCounts = 16 * 2 * kMostCtas;
 struct PagedParams {
-  CUtensorMap tmap_k, tmap_v;  // pages as [P * Hkv, page, D], box {128 bytes, rows, 1}
+  CUtensorMap tmap_k, tmap_v;  // pages as [P * Hkv, pieces, page, 128 bytes]
   CUtensorMap tmap_q;          // [T, Hkv, G, D], box {64, G, 1, 128 / G} (many rows)
   PagedArrays c;
   const void* q;       // [T, Hq, D] bf16, q_stride elements from one token to the next
@@ -293,14 +293,15 @@ struct PagedParams {
   uint64_t wait_limit_ns;
 };
 // The kernel for few rows, and what its scratch takes.
+int paged_stream_box(const PagedArrays& c);                 // rows of a page per copy
 unsigned paged_stream_ctas(const PagedParams& p, int rows);  // per SM
 size_t paged_stream_state(const PagedParams& p, int rows);  // rows of partial states
 cudaError_t launch_paged_stream(const PagedParams& p, int rows, int dev, cudaStream_t stream);
 // The kernel for many rows, likewise.
 size_t paged_tile_state(const PagedParams& p);
 cudaError_t launch_paged_tile(const PagedParams& p, int dev, cudaStream_t stream);
-// Tensor map over pages; box: rows of a page per copy.
-int encode_pages(CUtensorMap* map, const void* base, const PagedArrays& c, int box);
+// Tensor map over pages; a copy is `rows` rows of a page, 128 bytes of them or all.
+int encode_pages(CUtensorMap* map, const void* base, const PagedArrays& c, int rows, bool all);
 
 // ATTN_OK when the current device is an sm_103, else the status to return; and
 // what a launch needs to know of it, asked for once.

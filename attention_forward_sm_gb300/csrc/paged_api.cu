@@ -111,10 +111,10 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
     return ATTN_ERR_SHAPE;
   DeviceInfo di;
   if (int rc = device_info(&di)) return rc;
-  const int box = many ? c.page : std::min(c.page, 64);
+  const int box = many ? c.page : paged_stream_box(c);
   if (!many || !c.quant) {
-    if (int rc = encode_pages(&p.tmap_k, c.kpages, c, box)) return rc;
-    if (int rc = encode_pages(&p.tmap_v, c.vpages, c, box)) return rc;
+    if (int rc = encode_pages(&p.tmap_k, c.kpages, c, box, !many)) return rc;
+    if (int rc = encode_pages(&p.tmap_v, c.vpages, c, box, !many)) return rc;
   }
   if (many)
     if (int rc = encode_queries(&p.tmap_q, q, c.D, p.G, c.Hkv, c.T, 128 / p.G, q_stride)) return rc;

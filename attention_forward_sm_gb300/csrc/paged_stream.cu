@@ -10,7 +10,8 @@
 // warp that is the last to store its part of a row joins them, in the CTAs' order.
 //
 // A CTA is one or two loading warps and two teams of four computing ones around a ring of
-// stages, one unit each: K and V of 64 keys by tensor copies, a box per page.  Every other
+// stages, one unit each: K and V of 64 keys by tensor copies, a box per page or 16 whole
+// rows of 256 bytes.  Every other
 // unit is the first team's, 16 keys a warp, the rest the second's.
 // Rows are few, so the keys are the rows of the products (mma.sync m16n8k16):
 //   S^T [16 keys, 8 rows] = K [16, D] Q^T,   O^T [D, 8 rows] += V^T [D, 16] P^T.
@@ -23,13 +24,14 @@
 // has whole 16-byte pieces of the keys' rows.  P^T is S^T transposed within a warp
 // (movmatrix).
 //
-// Measured, D = 128: 8 requests of 500 to 65536 tokens, 32 heads on 8, bf16 82 us, 6.5 TB/s;
+// Measured, D = 128: 8 requests of 500 to 65536 tokens, 32 heads on 8, bf16 81 us, 6.6 TB/s;
 // 64 of 16 to 12000, 64 heads on 8, e4m3 51 us, 4.9 TB/s (issue slots 50%; of a short call like
 // this one 3.5 us go by until the first keys are there and some 5 at the end on the
-// last parts); 16 of 100 to 16384 with 4 tokens each, bf16 57 us.  Quantised with 9 to 16
+// last parts); 16 of 100 to 16384 with 4 tokens each, bf16 51 us.  Quantised with 9 to 16
 // rows 4.2 TB/s: one CTA on an SM for its registers, bound by the conversion and products.
 #include <math_constants.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "../../include/attn.h"
@@ -54,10 +56,10 @@ constexpr int kUnitFirst = 1, kUnitLast = 2, kUnitEnd = 4;  // a team's first an
 
 template <int D, bool kQuant, int NT>
 struct StreamCfg {
-  // A unit costs a loading warp some 1300 cycles, one after another; quantised, 700 cycles
-  // bring one in, so each team has a loader of its own (64 requests of 16 to 12000 tokens
-  // 57 -> 51 us).  bf16 units are on their way for 1400 (the same requests 77 us, with
-  // two 82).
+  // A copy costs a loading warp some 80 cycles, a unit more than 700, which is what brings a
+  // quantised one in: there each team has a loader of its own (64 requests of 16 to 12000
+  // tokens 57 -> 51 us).  bf16 units are on their way for 1400 (the same requests 77 us,
+  // with two 82).
   static constexpr int kLoaders = kQuant ? kTeams : 1;
   static constexpr int kThreads = (kWarps + kLoaders) * 32;
   static constexpr int kRows = 8 * NT;
@@ -130,14 +132,15 @@ __device__ __forceinline__ int block_key(int i) {
 }
 
 // Where byte `at` of row `row` of a copied tile is: 128-byte rows swizzled by 128
-// bytes (tiles of wider rows are two such tiles), 64-byte rows by 64.
+// bytes, 64-byte rows by 64; of wider rows, copied 16 at a time, the first halves and
+// then the second ones.
 template <int kRowBytes>
 __device__ __forceinline__ uint32_t swizzled(int row, int at) {
   if constexpr (kRowBytes == 64)
     return static_cast<uint32_t>(row * 64 + (at ^ ((row >> 1 & 3) << 4)));
   else
-    return static_cast<uint32_t>((at >> 7) * (kUnitKeys * 128) + row * 128 +
-                                 ((at & 127) ^ ((row & 7) << 4)));
+    return static_cast<uint32_t>((kRowBytes == 256 ? (row & ~15) * 128 : 0) + (at >> 7) * 2048 +
+                                 row * 128 + ((at & 127) ^ ((row & 7) << 4)));
 }
 
 template <int D, bool kQuant, int NT>
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
   if (warp >= kWarps) {
     // ---- a loading warp: of every kLoaders-th unit
     const uint32_t loader = static_cast<uint32_t>(warp - kWarps);
-    const int box_bits = min(p.c.page_bits, 6), box = 1 << box_bits;
+    const int box_bits = kRowBytes == 256 ? 4 : min(p.c.page_bits, 6), box = 1 << box_bits;
     static_assert(kUnitKeys == 64, "box_bits");
     const uint64_t policy = l2_policy_evict_first();
     uint32_t s = loader;
@@ -254,16 +257,9 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
           if (lane < n_box) {
             const int z = good ? id * p.c.Hkv + h : p.c.P * p.c.Hkv;
             const int y = key & (p.c.page - 1);
-            uint8_t* dst = smem + st * (2 * C::kTile) + lane * box * (kRowBytes < 128 ? 64 : 128);
-            constexpr int kPieces = kRowBytes / 128 > 0 ? kRowBytes / 128 : 1;
-            constexpr int kElems = kQuant ? 128 : 64;  // of a 128-byte piece
-#pragma unroll
-            for (int c = 0; c < kPieces; ++c) {
-              tma_load_3d(dst + c * (kUnitKeys * 128), &p.tmap_k, &ms.full[st], c * kElems, y, z,
-                          policy);
-              tma_load_3d(dst + C::kTile + c * (kUnitKeys * 128), &p.tmap_v, &ms.full[st],
-                          c * kElems, y, z, policy);
-            }
+            uint8_t* dst = smem + st * (2 * C::kTile) + lane * box * kRowBytes;
+            tma_load_4d(dst, &p.tmap_k, &ms.full[st], 0, y, 0, z, policy);
+            tma_load_4d(dst + C::kTile, &p.tmap_v, &ms.full[st], 0, y, 0, z, policy);
             if (kQuant && good) {
               const size_t from = static_cast<size_t>(z) * p.c.page + y;
               bulk_copy(scales, p.c.kscale + from, box, &ms.full[st], policy);
@@ -492,11 +488,11 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
       [[maybe_unused]] const bool odd =
           kQuant && (tail || __any_sync(0xFFFFFFFFu, max(vscale[0], vscale[1]) == kScaleNan));
 #pragma unroll
-      for (int half = 0; half < (kQuant ? 1 : D / 64); ++half) {
+      for (int part = 0; part < (kQuant ? 1 : D / 64); ++part) {
         uint32_t v[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          load_piece<kVBytes>(v[i], vtile + swizzled<kRowBytes>(keys[i], half * 128 + g * kVBytes));
+          load_piece<kVBytes>(v[i], vtile + swizzled<kRowBytes>(keys[i], part * 128 + g * kVBytes));
           if (kQuant ? odd : tail) {
             const bool none = un.key0 + keys[i] >= un.len;
             const bool nan = kQuant && scales[kUnitKeys + keys[i]] == kScaleNan;
@@ -527,7 +523,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
             const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_16n8k16<false>(o[nt][half * 4 + i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+              mma_16n8k16<false>(o[nt][part * 4 + i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
           }
         }
       }
@@ -670,6 +666,14 @@ cudaError_t launch_stream(const PagedParams& p, int dev, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// Rows of 256 bytes, twice what a swizzled box holds, take a box with both halves of 16 rows,
+// so that a warp's keys are in one of them: half the copies of boxes of single halves with
+// pages of 16 (8 requests of 500 to 65536 tokens 101 -> 81 us, 16 of 65536 with 16 rows
+// 774 -> 605), and with longer pages no more time than larger boxes.
+int paged_stream_box(const PagedArrays& c) {
+  return !c.quant && c.D == 128 ? 16 : std::min(c.page, kUnitKeys);
+}
 
 unsigned paged_stream_ctas(const PagedParams& p, int rows) {
   return p.c.quant && rows == 8 ? 2 : 1;

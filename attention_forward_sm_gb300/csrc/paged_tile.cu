@@ -671,10 +671,9 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
             const int z = there && good ? id * p.c.Hkv + it.h : p.c.P * p.c.Hkv;
             const int y = min(it.len - key, page) - page;  // the tokens at the end of the rows
             const int ch = lane % C::kChunks;
-            tma_load_3d(smem + C::kOffKV + slot * C::kTileBytes + ch * (kBN * 128) +
+            tma_load_4d(smem + C::kOffKV + slot * C::kTileBytes + ch * (kBN * 128) +
                             box * page * 128,
-                        (i & 1) ? &p.tmap_v : &p.tmap_k, &full[slot], ch * 64, there ? y : 0, z,
-                        policy);
+                        (i & 1) ? &p.tmap_v : &p.tmap_k, &full[slot], 0, there ? y : 0, ch, z, policy);
           }
           __syncwarp();
         }
