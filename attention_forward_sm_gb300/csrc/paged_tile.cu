@@ -38,14 +38,14 @@
 namespace attn {
 namespace {
 
-constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpConvert = 20;
+constexpr int kWarpLoad = 16, kWarpMma = 17, kWarpLoadV = 18, kWarpConvert = 20;
 
 template <int D, bool kQuant>
 struct TileCfg {
   static constexpr int kConvert = 4;  // warps that convert
   static constexpr int kThreads = kQuant ? 768 : 640;
   // setmaxnreg: 4 softmax warpgroups and 1 or 2 others, out of what the launch gets
-  static constexpr uint32_t kRegSoftmax = kQuant ? 96 : 112, kRegOther = kQuant ? 48 : 32;
+  static constexpr uint32_t kRegSoftmax = kQuant ? 96 : 104, kRegOther = kQuant ? 48 : 64;
   static constexpr int kReaders = kQuant ? 21 : 17;  // of an item, besides the loader
   static constexpr int kTileBytes = kBM * D * 2, kChunks = D / 64;
   static constexpr int kStages = D == 128 ? 4 : 8;
@@ -311,6 +311,11 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
   static_assert(C::kSmem + sizeof(ms) <= 227 * 1024, "shared memory");
   const uint32_t abort_flag = smem_u32(&ms.abort_flag);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // A copy costs a loading warp some 80 cycles, and a key tile of small pages is 2 * 8 or
+  // 2 * 16 of them: there V has a loading warp of its own (2048 tokens behind 16001, 32 heads
+  // on 8, D = 128, pages of 16: 428 -> 345 us, of 32 381 -> 365; of 64 362 either way, and
+  // quantised what two gave short chunks lost).
+  const bool split = !kQuant && p.c.page <= 32;
 
   if (warp == kWarpLoad && lane == 0) {
     mbar_init(&ms.q_empty, 1);
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
       mbar_init(&ms.p_full[t], 8);
       mbar_init(&ms.o_done[t], 1);
       mbar_init(&ms.item_full[t], 1);
-      mbar_init(&ms.item_empty[t], C::kReaders);
+      mbar_init(&ms.item_empty[t], C::kReaders + split);
     }
     mbar_init(&ms.mma_done, 1);
     for (int s = 0; s < C::kStages; ++s) {
@@ -583,45 +588,41 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
           p.part_ml[part_row] = make_float2(m, l_row);
       }
     }
-  } else if (warp == kWarpLoad) {
+  } else if (warp == kWarpLoad || (!kQuant && warp == kWarpLoadV)) {
     // ---- the plan's items, their Q tiles, and K_j, V_j through the ring
     reg_dealloc<C::kRegOther>();
-    uint32_t k = 0;           // items
-    uint32_t q_loads = 0, q_loads1 = 0;  // of query tiles 0 and 1
-    uint32_t slot = 0, round = 0;  // next place in the ring
     constexpr uint32_t kRing = kQuant ? C::kRaw : C::kStages;
+    static_assert(kRing % 2 == 0, "K and V have places of their own");
     uint64_t* const full = kQuant ? ms.raw_full : ms.kv_full;
     uint64_t* const empty = kQuant ? ms.raw_empty : ms.kv_empty;
     const int page = p.c.page, page_bits = p.c.page_bits;
     const int boxes = kBN >> page_bits;
     const int per_tile = kBM / p.G;
     const uint64_t policy = l2_policy_evict_last();
-    bool ok = true;
-    CostWalk walk(plan, at);
-    Item it;
-    int slot_first = 0;
-    PagedCut cut = {};
-    while (ok && walk.next(&it, &slot_first)) {
-      if (!warp_all(mbar_wait(&ms.item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort_flag, p.err,
-                              kErrWaitLoad, p.wait_limit_ns))) {
-        ok = false;
-        break;
+    uint32_t k = 0;                      // items
+    uint32_t q_loads = 0, q_loads1 = 0;  // of query tiles 0 and 1
+    const uint32_t first = !kQuant && warp == kWarpLoadV, every = split ? 2 : 1;  // tiles that it loads
+    uint32_t slot = first, round = 0;  // next place in the ring
+    // Q of item k, once the item before has used its own
+    auto load_q = [&](const Item& it) -> bool {
+      if (k > 0 && !warp_all(mbar_wait(&ms.q_empty, (k - 1) & 1, abort_flag, p.err, kErrWaitLoad,
+                                       p.wait_limit_ns)))
+        return false;
+      for (int t = 0; t < it.tiles; ++t) {
+        mbar_arrive_expect_tx_elect(&ms.q_full[t], static_cast<uint32_t>(per_tile * p.G * D * 2));
+        for (int ch = 0; ch < C::kChunks; ++ch)
+          tma_load_4d_elect(smem + t * C::kTileBytes + ch * (kBM * 128), &p.tmap_q, &ms.q_full[t],
+                            ch * 64, 0, it.h, it.row0 + t * per_tile, l2_policy_evict_first());
       }
-      if (slot_first == 1) {  // the CTA's last item, which goes on in the next ones
-        const long long end = walk.item.x0 + min(walk.item.cost,
-                                                 kItemCost + walk.item.n_kv * 1ll * kTileKeys);
-        unsigned last = blockIdx.x + 1;
-        while (at.deal.start(last + 1) < end) ++last;
-        cut = PagedCut{static_cast<int>(last - blockIdx.x) + 1, it.row0, it.left, it.h};
-      }
-      if (lane == 0) {
-        it.slot = slot_first < 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + slot_first;
-        ms.item[k & 1] = it;
-        mbar_arrive(&ms.item_full[k & 1]);
-      }
+      ++q_loads;
+      q_loads1 += it.tiles > 1;
+      return true;
+    };
+    auto load_tiles = [&](const Item& it) -> bool {
       int pbase = -256, ids = 0;
       const uint32_t n = 2u * static_cast<uint32_t>(it.tile1 - it.tile0);
-      for (uint32_t i = 0; i < n && ok; ++i) {
+      for (uint32_t i = first; i < n; i += every) {
+        const bool of_v = i & 1;
         const int key0 = (it.tile0 + static_cast<int>(i >> 1)) * kBN;
         // copy `box` of the tile: page and rows (lane l holds entry pbase + l of the table)
         if ((key0 >> page_bits) < pbase || (key0 >> page_bits) + boxes > pbase + 32) {
@@ -639,14 +640,12 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         const uint32_t bad = __ballot_sync(0xFFFFFFFFu, mine && there && !good);
         if (bad && lane == 0) atomicOr(p.err, kErrPage);
         if (!warp_all(mbar_wait(&empty[slot], (round & 1) ^ 1, abort_flag, p.err, kErrWaitLoad,
-                                p.wait_limit_ns))) {
-          ok = false;
-          break;
-        }
+                                p.wait_limit_ns)))
+          return false;
         if constexpr (kQuant) {
           const bool copy = mine && there && good;
           const int rows = min(page, it.len - key);
-          const int scales = (i & 1) ? 1 : 2;  // with K, V's too
+          const int scales = of_v ? 1 : 2;  // with K, V's too
           uint32_t bytes = copy ? static_cast<uint32_t>(rows * D + scales * page) : 0;
           bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
           if (lane == 0) {
@@ -656,11 +655,11 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
           __syncwarp();
           if (copy) {
             const size_t from = (static_cast<size_t>(id) * p.c.Hkv + it.h) * page;
-            const uint8_t* src = static_cast<const uint8_t*>((i & 1) ? p.c.vpages : p.c.kpages);
+            const uint8_t* src = static_cast<const uint8_t*>(of_v ? p.c.vpages : p.c.kpages);
             bulk_copy(smem + C::kOffRaw + slot * C::kRawBytes + box * page * D, src + from * D,
                       static_cast<uint32_t>(rows * D), &full[slot], policy);
             uint8_t* to = smem + C::kOffScale + slot * C::kScaleBytes + (box << page_bits);
-            if (!(i & 1))
+            if (!of_v)
               bulk_copy(to, p.c.kscale + from, static_cast<uint32_t>(page), &full[slot], policy);
             bulk_copy(to + kBN, p.c.vscale + from, static_cast<uint32_t>(page), &full[slot],
                       policy);
@@ -673,49 +672,55 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
             const int ch = lane % C::kChunks;
             tma_load_4d(smem + C::kOffKV + slot * C::kTileBytes + ch * (kBN * 128) +
                             box * page * 128,
-                        (i & 1) ? &p.tmap_v : &p.tmap_k, &full[slot], 0, there ? y : 0, ch, z, policy);
+                        of_v ? &p.tmap_v : &p.tmap_k, &full[slot], 0, there ? y : 0, ch, z, policy);
           }
           __syncwarp();
         }
-        if (++slot == kRing) {
-          slot = 0;
+        slot += every;
+        if (slot >= kRing) {
+          slot -= kRing;
           ++round;
         }
-        if (i == 0) {
-          // Q, once the item before has used its own
-          if (k > 0 && !warp_all(mbar_wait(&ms.q_empty, (k - 1) & 1, abort_flag, p.err,
-                                           kErrWaitLoad, p.wait_limit_ns))) {
-            ok = false;
-            break;
-          }
-          for (int t = 0; t < it.tiles; ++t) {
-            mbar_arrive_expect_tx_elect(&ms.q_full[t],
-                                        static_cast<uint32_t>(per_tile * p.G * D * 2));
-            for (int ch = 0; ch < C::kChunks; ++ch)
-              tma_load_4d_elect(smem + t * C::kTileBytes + ch * (kBM * 128), &p.tmap_q,
-                                &ms.q_full[t], ch * 64, 0, it.h, it.row0 + t * per_tile,
-                                l2_policy_evict_first());
-          }
-          ++q_loads;
-          q_loads1 += it.tiles > 1;
+        if (i == 0 && !load_q(it)) return false;
+      }
+      return true;
+    };
+    if (!kQuant && warp == kWarpLoadV) {
+      Item it;
+      while (split && next_item(k, &it, kErrWaitLoad) && load_tiles(it)) ++k;
+    } else {
+      CostWalk walk(plan, at);
+      PagedCut cut = {};
+      for (;; ++k) {
+        Item it;
+        int part = 0;
+        const bool more = walk.next(&it, &part);
+        if (!warp_all(mbar_wait(&ms.item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort_flag, p.err,
+                                kErrWaitLoad, p.wait_limit_ns)))
+          break;
+        if (!more) it.tiles = 0;
+        if (more && part == 1) {  // the CTA's last item, which goes on in the next ones
+          const long long end = walk.item.x0 + min(walk.item.cost,
+                                                   kItemCost + walk.item.n_kv * 1ll * kTileKeys);
+          unsigned last = blockIdx.x + 1;
+          while (at.deal.start(last + 1) < end) ++last;
+          cut = PagedCut{static_cast<int>(last - blockIdx.x) + 1, it.row0, it.left, it.h};
         }
+        if (lane == 0) {
+          it.slot = part < 0 ? -1 : 2 * static_cast<int>(blockIdx.x) + part;
+          ms.item[k & 1] = it;
+          mbar_arrive(&ms.item_full[k & 1]);
+        }
+        if (!more || !load_tiles(it)) break;
       }
-      ++k;
-    }
-    if (lane == 0) p.cuts[blockIdx.x] = cut;
-    if (ok && warp_all(mbar_wait(&ms.item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort_flag, p.err,
-                                 kErrWaitLoad, p.wait_limit_ns))) {
-      if (lane == 0) {
-        ms.item[k & 1].tiles = 0;
-        mbar_arrive(&ms.item_full[k & 1]);
-      }
+      if (lane == 0) p.cuts[blockIdx.x] = cut;
     }
     if (abort_set(abort_flag)) {
       // copies in flight land before the CTA leaves: the last Q tiles, and the last round
       // of the ring
       if (q_loads > 0) drain_wait(&ms.q_full[0], (q_loads - 1) & 1);
       if (q_loads1 > 0) drain_wait(&ms.q_full[1], (q_loads1 - 1) & 1);
-      for (uint32_t i = 0; i < kRing; ++i) {
+      for (uint32_t i = first; i < kRing; i += every) {
         if (i < slot)
           drain_wait(&full[i], round & 1);
         else if (round > 0)
