@@ -105,7 +105,8 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
   const long long rows = std::min<long long>(max_new, c.T) * p.G;
   const bool many = rows > 16 && static_cast<long long>(c.M) * c.page <= kSegmentKeys;
   l.rows = many ? 0 : rows <= 8 ? 8 : 16;
-  // the streaming kernel numbers its units of work in 32 bits
+  // the streaming kernel numbers its units of work in 32 bits: a block of rows has
+  // M * page / 64 + 9 of them at most, less than twice what is counted here
   const long long blocks = static_cast<long long>(c.T) * p.G / 8 + c.B;
   if (blocks * c.Hkv * (static_cast<long long>(c.M) * c.page / 64 + 5) >= (1ll << 31))
     return ATTN_ERR_SHAPE;

@@ -41,11 +41,14 @@ struct PlanPlace {
   int len;
 };
 
-// What a block of rows costs besides its keys, in units (of half the bytes, quantised):
-// its queries, and joining and storing what the warps have.  Quantised, 64 requests of
-// 16 to 12000 tokens take 62 us with 2, 57 with 4, 58 with 6, 64 with 10; bf16, 16
-// requests of 100 to 16384 with 4 tokens each 57.5 with 2, 58.5 with 4, 59.5 with 6.
-__host__ __device__ constexpr uint32_t block_cost(bool quant) { return quant ? 4 : 2; }
+// What a block of rows costs besides its keys, in units: its queries, and joining and
+// storing what the warps have.  32 requests of 16 to 12000 tokens, bf16, 8 rows: 45.1 us
+// with 2, 43.2 with 3, 43.5 with 4; 16 rows 70, 58, 49.8, and 50.1 with 6.  Quantised, whose
+// units are half the bytes, 64 requests, 8 rows: 54.2 with 3, 50.8 with 4, 50.8 with 6; 16
+// rows 123 with 4, 78 with 8, 81 with 16.
+__host__ __device__ constexpr uint32_t block_cost(bool quant, int block_rows) {
+  return quant && block_rows == 16 ? 8 : 4;
+}
 
 // An item is a block of rows of one KV head; it is worth its key tiles (one where there
 // is no key, so that the rows' results are written) and block_cost, which comes first.
@@ -54,7 +57,7 @@ struct StreamPlan {
   int G, block_rows;
   uint32_t block_cost;
   __device__ StreamPlan(const PagedArrays& c, int G, int block_rows)
-      : c(c), G(G), block_rows(block_rows), block_cost(attn::block_cost(c.quant)) {}
+      : c(c), G(G), block_rows(block_rows), block_cost(attn::block_cost(c.quant, block_rows)) {}
   __device__ uint32_t tiles(int len) const {
     return static_cast<uint32_t>(max(1, (len + kUnitKeys - 1) / kUnitKeys));
   }
@@ -299,9 +302,6 @@ struct State {
       o[2] = fmaf(w, x.z, o[2]);
       o[3] = fmaf(w, x.w, o[3]);
     }
-  }
-  __device__ void add(float2 ml, float top, const float* from, int lane) {
-    add(ml, top, reinterpret_cast<const Vec*>(from)[lane]);
   }
   // Adds up `parts` states that other CTAs stored, the k-th one in row state(k) (read in
   // L2, where they are), four at a time; returns the largest maximum.

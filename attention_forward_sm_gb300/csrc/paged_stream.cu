@@ -9,10 +9,9 @@
 // block that ends up in several CTAs has a partial state (maximum, sum, O) in each; the
 // warp that is the last to store its part of a row joins them, in the CTAs' order.
 //
-// A CTA is one or two loading warps and two teams of four computing ones around a ring of
-// stages, one unit each: K and V of 64 keys by tensor copies, a box per page or 16 whole
-// rows of 256 bytes.  Every other
-// unit is the first team's, 16 keys a warp, the rest the second's.
+// A CTA is one to three loading warps and two or three teams of four computing ones around a
+// ring of stages, one unit each: K and V of 64 keys by tensor copies, a box per page or
+// 16 whole rows of 256 bytes.  The teams take units in turn, a warp 16 keys of each.
 // Rows are few, so the keys are the rows of the products (mma.sync m16n8k16):
 //   S^T [16 keys, 8 rows] = K [16, D] Q^T,   O^T [D, 8 rows] += V^T [D, 16] P^T.
 // A tcgen05.mma has at least 64 rows of one operand in shared memory or TMEM and
@@ -24,11 +23,10 @@
 // has whole 16-byte pieces of the keys' rows.  P^T is S^T transposed within a warp
 // (movmatrix).
 //
-// Measured, D = 128: 8 requests of 500 to 65536 tokens, 32 heads on 8, bf16 81 us, 6.6 TB/s;
+// Measured, D = 128: 8 requests of 500 to 65536 tokens, 32 heads on 8, bf16 79 us, 6.7 TB/s;
 // 64 of 16 to 12000, 64 heads on 8, e4m3 51 us, 4.9 TB/s (issue slots 50%; of a short call like
 // this one 3.5 us go by until the first keys are there and some 5 at the end on the
-// last parts); 16 of 100 to 16384 with 4 tokens each, bf16 51 us.  Quantised with 9 to 16
-// rows 4.2 TB/s: one CTA on an SM for its registers, bound by the conversion and products.
+// last parts); 16 of 100 to 16384 with 4 tokens each, bf16 45 us, 5.2 TB/s.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -40,9 +38,6 @@
 
 namespace attn {
 namespace {
-
-constexpr int kTeams = 2;
-constexpr int kWarps = 4 * kTeams;  // computing
 
 // One unit in the ring, as a loading warp describes it.
 struct Unit {
@@ -56,6 +51,12 @@ constexpr int kUnitFirst = 1, kUnitLast = 2, kUnitEnd = 4;  // a team's first an
 
 template <int D, bool kQuant, int NT>
 struct StreamCfg {
+  // Quantised, 9 to 16 rows: latencies are the bound, and three teams hide more of them.  Their
+  // 128 registers a thread hold no queries, which are in shared memory (16 requests of 30000
+  // tokens 229 -> 198 us, 64 of 7000 225 -> 197).
+  static constexpr bool kSharedQ = kQuant && NT == 2;
+  static constexpr int kTeams = kSharedQ ? 3 : 2;
+  static constexpr int kWarps = 4 * kTeams;  // computing
   // A copy costs a loading warp some 80 cycles, a unit more than 700, which is what brings a
   // quantised one in: there each team has a loader of its own (64 requests of 16 to 12000
   // tokens 57 -> 51 us).  bf16 units are on their way for 1400 (the same requests 77 us,
@@ -67,21 +68,23 @@ struct StreamCfg {
   static constexpr int kTile = kUnitKeys * kRowBytes;  // K or V of a unit
   static constexpr int kScales = kQuant ? 2 * kUnitKeys : 0;
   static constexpr int kMerge = (kWarps - 4) * kRows * D * 4;
+  static constexpr int kQueries = kSharedQ ? kRows * D * 2 : 0;
   // Two CTAs on an SM where the registers allow it: one joins its warps' states and
   // stores while the other goes on.
   static constexpr int kCtas = kQuant && NT == 1 ? 2 : 1;
   // As many stages as fit beside the buffer for merging, at most 16, and a multiple of the
   // teams: a stage belongs to one of them, which so sees every phase of its barrier.
-  static constexpr int kRoom = (kCtas == 1 ? 227 : 113) * 1024 - 3072 - kMerge;
+  static constexpr int kRoom = (kCtas == 1 ? 227 : 113) * 1024 - 3072 - kMerge - kQueries;
   static constexpr int kFit = kRoom / (2 * kTile + kScales);
   static constexpr int kStages = (kFit < 16 ? kFit : 16) / kTeams * kTeams;
   static constexpr int kOffMerge = kStages * 2 * kTile;
-  static constexpr int kOffScales = kOffMerge + kMerge;
+  static constexpr int kOffQueries = kOffMerge + kMerge;
+  static constexpr int kOffScales = kOffQueries + kQueries;
   static constexpr int kSmem = kOffScales + kStages * kScales + 1024;  // + alignment
   static_assert(kStages >= kTeams, "shared memory");
 };
 
-template <int kStages, int kRows>
+template <int kStages, int kRows, int kWarps>
 struct StreamShared {
   uint64_t full[kStages], empty[kStages];
   uint64_t team_full, merge_full, merge_empty;
@@ -143,15 +146,20 @@ __device__ __forceinline__ uint32_t swizzled(int row, int at) {
                                  row * 128 + ((at & 127) ^ ((row & 7) << 4)));
 }
 
+// Where piece i (of 4 elements) of a row of O stands in the buffer for merging: eight lanes
+// that store pieces of a row, 2 or 4 apart, do so in different banks.
+__device__ __forceinline__ int merge_slot(int i) { return i ^ (i >> 3 & 3); }
+
 template <int D, bool kQuant, int NT>
 __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg<D, kQuant, NT>::kCtas))
     paged_stream_kernel(const __grid_constant__ PagedParams p) {
   using C = StreamCfg<D, kQuant, NT>;
   constexpr int kStages = C::kStages, kRows = C::kRows, kRowBytes = C::kRowBytes;
   constexpr int kLoaders = C::kLoaders, kThreads = C::kThreads;
+  constexpr int kTeams = C::kTeams, kWarps = C::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
-  __shared__ StreamShared<kStages, kRows> ms;
+  __shared__ StreamShared<kStages, kRows, kWarps> ms;
   static_assert((C::kSmem + sizeof(ms) + 1024) * C::kCtas <= 228 * 1024, "shared memory");
   const uint32_t abort_flag = smem_u32(&ms.abort_flag);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -187,7 +195,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
     int b = at.b;
     uint32_t in_request = at.in_request;  // unit within the request
     const Deal deal(at.total, p.ctas);
-    constexpr uint32_t kBlockCost = block_cost(kQuant);
+    constexpr uint32_t kBlockCost = block_cost(kQuant, kRows);
     for (uint32_t u = at.first; u < at.end && b < p.c.B && ok;) {
       const Rows rows = b == at.b ? at.rows : request_rows(p.c, b);
       const int len = b == at.b ? at.len : clamp_len(p.c, b);
@@ -294,7 +302,8 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
   const int vkey = my_key + block_key(2 * t);  // V: keys vkey, ^4, + 8 of each
   const int vkey1 = my_key + block_key(2 * t + 1);
   constexpr int kSteps = D / 16;  // products per S^T, and 16-row tiles of O^T
-  uint32_t qf[NT][2 * kSteps];
+  uint32_t qf[C::kSharedQ ? 1 : NT][2 * kSteps];
+  uint4* const shared_q = reinterpret_cast<uint4*>(smem + C::kOffQueries) + lane;
   float o[NT][kSteps][4], m[NT][2], l[NT][2], by_row[NT][2];
   int vis[NT][2], first_vis = 0;
   uint32_t merges = 0;
@@ -319,16 +328,17 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
         // the elements that go with those of K that the thread loads: piece 4c + t of a
         // row, its pairs in order
         constexpr int kWords = kQuant ? 8 : 4;  // of the query for one piece
+        uint32_t(&qn)[2 * kSteps] = qf[C::kSharedQ ? 0 : nt];
 #pragma unroll
         for (int c = 0; c < kRowBytes / 64; ++c)
 #pragma unroll
           for (int i = 0; i < kWords / 4; ++i) {
             uint4 x = make_uint4(0, 0, 0, 0);
             if (r < n_rows) x = *reinterpret_cast<const uint4*>(q + ((4 * c + t) * kWords + 4 * i) * 4);
-            qf[nt][c * kWords + 4 * i] = x.x;
-            qf[nt][c * kWords + 4 * i + 1] = x.y;
-            qf[nt][c * kWords + 4 * i + 2] = x.z;
-            qf[nt][c * kWords + 4 * i + 3] = x.w;
+            qn[c * kWords + 4 * i] = x.x;
+            qn[c * kWords + 4 * i + 1] = x.y;
+            qn[c * kWords + 4 * i + 2] = x.z;
+            qn[c * kWords + 4 * i + 3] = x.w;
           }
         float scale = 1.f;
         if constexpr (kQuant) {
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
           uint32_t top = 0;
 #pragma unroll
           for (int i = 0; i < 2 * kSteps; ++i)
-            top = max(top, bf16x2_top(qf[nt][i]));
+            top = max(top, bf16x2_top(qn[i]));
           top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
           top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
           const uint32_t e = min(max(top >> 23, 1u), 253u);
@@ -345,7 +355,16 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
           const float inv = __uint_as_float((254u - e) << 23);
 #pragma unroll
           for (int i = 0; i < 2 * kSteps; ++i)
-            qf[nt][i] = bf16x2_to_f16x2(qf[nt][i], inv);
+            qn[i] = bf16x2_to_f16x2(qn[i], inv);
+        }
+        if constexpr (C::kSharedQ) {
+          // (every warp stores the same; those of the item before are not read any more, since
+          // all warps' states of it are joined)
+#pragma unroll
+          for (int i = 0; i < kSteps / 2; ++i)
+            shared_q[(nt * (kSteps / 2) + i) * 32] =
+                make_uint4(qn[4 * i], qn[4 * i + 1], qn[4 * i + 2], qn[4 * i + 3]);
+          __syncwarp();
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -380,12 +399,23 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
         load_piece<16>(e, ktile + swizzled<kRowBytes>(row_hi, (4 * c + t) * 16));
         if constexpr (kQuant) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 4; i += 2) {
             const uint32_t a0 = e4m3_lo(a[i]), a2 = e4m3_hi(a[i]);
             const uint32_t a1 = e4m3_lo(e[i]), a3 = e4m3_hi(e[i]);
+            const uint32_t b0 = e4m3_lo(a[i + 1]), b2 = e4m3_hi(a[i + 1]);
+            const uint32_t b1 = e4m3_lo(e[i + 1]), b3 = e4m3_hi(e[i + 1]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16n8k16<true>(x[nt], a0, a1, a2, a3, qf[nt][8 * c + 2 * i], qf[nt][8 * c + 2 * i + 1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              uint4 y;
+              if constexpr (C::kSharedQ) {
+                y = shared_q[(nt * (kSteps / 2) + 2 * c + i / 2) * 32];
+              } else {
+                const uint32_t* from = &qf[nt][8 * c + 2 * i];
+                y = make_uint4(from[0], from[1], from[2], from[3]);
+              }
+              mma_16n8k16<true>(x[nt], a0, a1, a2, a3, y.x, y.y);
+              mma_16n8k16<true>(x[nt], b0, b1, b2, b3, y.z, y.w);
+            }
           }
         } else {
 #pragma unroll
@@ -603,7 +633,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
           for (int i = 0; i < kSteps; i += 2) {
             // four elements of the row: the thread's tiles i and i + 1
             const int d = kQuant ? g * (D / 8) + 2 * i : (i / 4) * 64 + g * 8 + 2 * (i % 4);
-            *reinterpret_cast<float4*>(row + d) =
+            reinterpret_cast<float4*>(row)[merge_slot(d / 4)] =
                 make_float4(o[nt][i][k], o[nt][i][k + 2], o[nt][i + 1][k], o[nt][i + 1][k + 2]);
           }
         }
@@ -616,12 +646,14 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
     for (int r = warp; r < min(kRows, n_rows); r += kWarps) {
       State<D> sum;
       float top = -CUDART_INF_F;
+      const int from = D == 128 ? merge_slot(lane) : 2 * merge_slot(lane / 2) + lane % 2;
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, ms.ml[i][r].x);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         sum.add(ms.ml[i][r], top,
-                reinterpret_cast<float*>(smem + C::kOffMerge) + (i * kRows + r) * D, lane);
+                reinterpret_cast<const typename State<D>::Vec*>(
+                    reinterpret_cast<float*>(smem + C::kOffMerge) + (i * kRows + r) * D)[from]);
       const int row = un.block * kRows + r;
       if (un.slot < 0) {
         sum.finish(p, un.row0 + row / p.G, un.h * p.G + row % p.G, top, lane);
