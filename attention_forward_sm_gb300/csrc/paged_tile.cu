@@ -23,8 +23,8 @@
 // that is cut has a partial state in each CTA, which tile_merge_kernel joins.
 // Bound by the tensor cores, 4 D flops per row and key, and the chain of a query tile
 // (scores, softmax pass, products), two of which alternate.  32 heads on 8, D = 128: bf16,
-// 2048 tokens behind 16001 352 us, of which 336 this kernel (1.7 PFLOP/s, tensor pipe 74%)
-// and 15 the joining; e4m3, 1024 behind 30000 402 us, 394 and 13, tensor pipe 56%, issue slots
+// 2048 tokens behind 16001 356 us, of which 333 this kernel (1.7 PFLOP/s, tensor pipe 74%)
+// and 15 the joining; e4m3, 1024 behind 30000 403 us, 388 and 13, tensor pipe 56%, issue slots
 // 54%: the conversion's instructions and 96 registers for the softmax warps.  Short chunks are bound by 6 us until the first
 // product and 5 from one item to the next.
 #include <math_constants.h>
