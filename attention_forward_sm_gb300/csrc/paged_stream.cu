@@ -74,7 +74,7 @@ struct StreamCfg {
   static constexpr int kCtas = kQuant && NT == 1 ? 2 : 1;
   // As many stages as fit beside the buffer for merging, at most 16, and a multiple of the
   // teams: a stage belongs to one of them, which so sees every phase of its barrier.
-  static constexpr int kRoom = (kCtas == 1 ? 227 : 113) * 1024 - 3072 - kMerge - kQueries;
+  static constexpr int kRoom = (kCtas == 1 ? 224 : 110) * 1024 - kMerge - kQueries;
   static constexpr int kFit = kRoom / (2 * kTile + kScales);
   static constexpr int kStages = (kFit < 16 ? kFit : 16) / kTeams * kTeams;
   static constexpr int kOffMerge = kStages * 2 * kTile;
