@@ -50,9 +50,10 @@ struct TileCfg {
   static constexpr int kTileBytes = kBM * D * 2, kChunks = D / 64;
   static constexpr int kStages = D == 128 ? 4 : 8;
   // Quantised tiles in a ring of their own, their scales (K: and those of V) behind.
-  // Two, one of K and one of V: with four there would be room for three converted ones at
-  // D = 128, and K_j+1 would wait for K_j's place (6% slower).
-  static constexpr int kRaw = 2, kRawBytes = kBN * D, kScaleBytes = 2 * kBN;
+  // D = 128: two, one of K and one of V; with four there would be room for three converted
+  // ones, and K_j+1 would wait for K_j's place (6% slower).  D = 64 has room for six (16
+  // requests of 30000 tokens with 8 of 32 heads on 8 each 307 -> 279 us, long chunks the same).
+  static constexpr int kRaw = D == 128 ? 2 : 6, kRawBytes = kBN * D, kScaleBytes = 2 * kBN;
   static constexpr int kOffKV = 2 * kTileBytes;
   static constexpr int kOffRaw = kOffKV + kStages * kTileBytes;
   static constexpr int kOffScale = kOffRaw + (kQuant ? kRaw * kRawBytes : 0);
@@ -130,10 +131,10 @@ struct TileShared {
   uint64_t o_done[2];                // per item of query tile t
   uint64_t mma_done;
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t raw_full[2], raw_empty[2];
+  uint64_t raw_full[6], raw_empty[6];
   uint64_t item_full[2], item_empty[2];
   Item item[2];
-  uint32_t raw_bad[2];  // copies of the tile whose page is out of range, a bit each
+  uint32_t raw_bad[6];  // copies of the tile whose page is out of range, a bit each
   // Quantised: what the converted K and V of a key tile are to be multiplied by, as scale
   // bytes (of the tiles i, i + 8, ...; the converting warps are three ahead at most).
   uint2 kv_scale[8];
