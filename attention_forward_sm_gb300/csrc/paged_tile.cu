@@ -136,18 +136,26 @@ struct TileShared {
   Item item[2];
   uint32_t raw_bad[6];  // copies of the tile whose page is out of range, a bit each
   // Quantised: what the converted K and V of a key tile are to be multiplied by, as scale
-  // bytes (of the tiles i, i + 8, ...; the converting warps are three ahead at most).
+  // bytes, or kScaleEach (of the tiles i, i + 8, ...; the converting warps are three ahead
+  // at most).
   uint2 kv_scale[8];
   CostShared plan;
   uint32_t tmem_base;
   int abort_flag;
 };
 
+// In place of the scale byte of a tile: its codes were converted as they are, and each key has
+// its own.
+constexpr uint32_t kScaleEach = 0;
+// Scales of K so far apart at most are brought under the largest one: a code is a multiple of
+// 2^-9, and f16 holds multiples of 2^-24.
+constexpr uint32_t kScaleSpanK = 14;
+
 // The factor 2^(scale - most) of a row among those of a tile, as f16: exact down to 2^-24,
-// 0 below (of V: a row that far below its neighbours is lost next to them).  NaN for a
-// row that stands for it.
+// 0 below (of V: a row that far below its neighbours is lost next to them).  1 where each
+// key has its own scale, NaN for a row that stands for it.
 __device__ __forceinline__ uint32_t f16_factor(uint32_t scale, uint32_t most) {
-  const uint32_t d = most - scale;
+  const uint32_t d = most == kScaleEach ? 0 : most - scale;
   const uint32_t f = d <= 14 ? (15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
   return scale == kScaleNan ? 0x7FFFu : f;
 }
@@ -190,8 +198,9 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
   // nothing odd: then every factor is a normal f16 number.  Else only rows count that are
   // there and not NaN, nor zeros, whose scale says 2^0 and could leave nothing of the
   // others; landed() says that the codes are in place (false: they never will be).
+  // kScaleEach where those that count are more than `span` apart.
   auto largest = [&](const uint8_t* scales, const uint8_t* codes, bool whole, int rows, uint32_t bad,
-                     bool* plain, uint32_t* most, auto landed) {
+                     uint32_t span, bool* plain, uint32_t* most, auto landed) {
     const uint32_t w = reinterpret_cast<const uint32_t*>(scales)[lane];
     uint32_t s[4] = {w & 255u, w >> 8 & 255u, w >> 16 & 255u, w >> 24};
     *most = __reduce_max_sync(0xFFFFFFFFu, max(max(s[0], s[1]), max(s[2], s[3])));
@@ -199,12 +208,13 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
     *plain = whole && *most != kScaleNan && *most - least <= 14;
     if (*plain) return true;
     bool zeros = false;
+    uint32_t counts = 15;  // a bit for each of the lane's rows
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 4 * lane + i;
       if (s[i] == kScaleNan || row >= rows || (bad >> (row >> p.c.page_bits) & 1u))
-        s[i] = kScaleLeast;
-      zeros = zeros || s[i] == kScaleOfZeros;
+        counts &= ~(1u << i);
+      zeros = zeros || ((counts >> i & 1u) && s[i] == kScaleOfZeros);
     }
     if (__any_sync(0xFFFFFFFFu, zeros)) {
       if (!landed()) return false;
@@ -214,10 +224,18 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
 #pragma unroll 1
         for (int at = 0; at < D; at += 16)
           bits |= or_of(*reinterpret_cast<const uint4*>(codes + (4 * lane + i) * D + at));
-        if (!(bits & 0x7F7F7F7Fu)) s[i] = kScaleLeast;
+        if (!(bits & 0x7F7F7F7Fu)) counts &= ~(1u << i);
       }
     }
-    *most = __reduce_max_sync(0xFFFFFFFFu, max(max(s[0], s[1]), max(s[2], s[3])));
+    uint32_t hi_scale = kScaleLeast, lo_scale = 255;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!(counts >> i & 1u)) continue;
+      hi_scale = max(hi_scale, s[i]);
+      lo_scale = min(lo_scale, s[i]);
+    }
+    *most = __reduce_max_sync(0xFFFFFFFFu, hi_scale);
+    if (__reduce_min_sync(0xFFFFFFFFu, lo_scale) + span < *most) *most = kScaleEach;
     return true;
   };
 
@@ -242,8 +260,10 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
       const bool whole = there >= kBN && !bad;
       if (!of_v) {
         // (V's raw tile is the next one, and comes in while this one is held)
-        if (!largest(scales, tile, whole, there, bad, &plain, &most, [] { return true; }) ||
-            !largest(scales + kBN, tile + C::kRawBytes, whole, there, bad, &next_plain, &next_most, [&] {
+        if (!largest(scales, tile, whole, there, bad, kScaleSpanK, &plain, &most,
+                     [] { return true; }) ||
+            !largest(scales + kBN, tile + C::kRawBytes, whole, there, bad, 255, &next_plain,
+                     &next_most, [&] {
               return warp_all(mbar_wait(&ms.raw_full[raw + 1], raw_round & 1, abort_flag, p.err,
                                         kErrWaitLoad, p.wait_limit_ns));
             }))
@@ -359,6 +379,31 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = ms.tmem_base;
 
+  // Quantised: 16 scale bytes of an item's keys from `key` on; 2^0 where there are none.
+  [[maybe_unused]] auto scale_bytes = [&](const uint8_t* scales, const Item& it, int key) {
+    uint4 x = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    if (key < it.len) {
+      const int id =
+          __ldcg(&p.c.table[static_cast<size_t>(it.b) * p.c.M + (key >> p.c.page_bits)]);
+      if (static_cast<unsigned>(id) < static_cast<unsigned>(p.c.P))
+        x = __ldcg(reinterpret_cast<const uint4*>(
+            scales + (static_cast<size_t>(id) * p.c.Hkv + it.h) * p.c.page +
+            (key & (p.c.page - 1))));
+    }
+    return x;
+  };
+  // Scores of 64 keys from `key` on, each times the scale of its K.  (Read where they are: a
+  // tile's scales lie this far apart in few caches, and are not worth shared memory.)
+  [[maybe_unused]] auto each_scale = [&](const Item& it, int key, float (&s)[64]) {
+#pragma unroll
+    for (int i = 0; i < 64; i += 16) {
+      const uint4 x = scale_bytes(p.c.kscale, it, key + i);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int n = 0; n < 16; ++n) s[i + n] *= scale_value(w[n / 4] >> (8 * (n % 4)) & 255u);
+    }
+  };
+
   // waits for item k; false when there is none
   auto next_item = [&](uint32_t k, Item* it, uint32_t site) -> bool {
     if (!warp_all(mbar_wait(&ms.item_full[k & 1], (k >> 1) & 1, abort_flag, p.err, site,
@@ -457,6 +502,12 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
           tmem_ld_pair64<64>(s_addr, sr);
 #pragma unroll
           for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
+        }
+        if constexpr (kQuant) {
+          if (by.x == kScaleEach) {
+            each_scale(it, j * kBN + c * 64, s);
+            by.x = 127;
+          }
         }
         if ((j + 1) * kBN > all_see) {
           // columns [0, end) and [from, to) of this thread's are visible

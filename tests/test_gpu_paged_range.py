@@ -1,0 +1,143 @@
+"""Paged attention over keys and values of very different sizes: what a row does not see, or
+sees with next to no weight, costs the others nothing.  Against the definition in 64 bits, with
+bounds that count the roundings of each cache type."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import paged_ref as ref  # noqa: E402
+from attention_forward_sm_gb300 import binding as attn  # noqa: E402
+from test_gpu_paged import _randn  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+BF16 = ref.BF16
+
+
+def resize(c, b, i, k=0, v=0):
+    """Key i of request b: K times 2^k, V times 2^v, by their scales or, in bf16, values."""
+    at, slot = int(c.table[b, i // c.page]), i % c.page
+    for x, pages, scale, e in ((c.dense[b][0], c.kp, c.ks, k), (c.dense[b][1], c.vp, c.vs, v)):
+        x[i] *= 2.0 ** e
+        if not c.quant:
+            pages[at, :, slot] = x[i].to(BF16)
+        elif e:
+            scale[at, :, slot] += e
+
+
+def _exponents(c, b):
+    """2^e of the rows of V [n, Hkv] of request b."""
+    n = c.lens[b]
+    i = torch.arange(n, device="cuda")
+    e = c.vs[c.table[b].long()[i // c.page], :, i % c.page].double() - 127
+    return torch.where(c.dense[b][1].abs().amax(-1) > 0, e, torch.full_like(e, -100.0))
+
+
+def check_range(o, lse, q, c, offsets, causal=True, scale=None, only=None):
+    """Of every request and head, or of `only` these.  A score is a sum of D products in 32 bits,
+    each addition off by 2^-23 of the sum of magnitudes at most: d_j = scale sum_i D 2^-23
+    |q_i k_ji|; a query's elements below 2^-14 of its largest are rounded by 2^-25 of that.
+    A weight is rounded to bf16 or f16 (half a step 2^-8, 2^-11) and O to bf16 (2^-8); so with
+    softmax weights w and everything else in 32 bits (a fiftieth more)
+      |dO| <= 2^-8 |O| + sum_j w_j (2^-8 or 2^-11) |v_j| + sum_j w_j d_j (|v_j| + |O|) + floor,
+    and n 2^-27 sum_j w_j |v_j| for sums of n products that are cut 26 bits below the highest.
+    floor, quantised: half a step of f16 is 2^-25 at least, and the largest product of a weight
+    and a scale of V, M = max_j w_j 2^e_j, stands for 2^10 in it, or, since a tile may
+    have one scale, for 2^10 over as much as V's scales differ, 2^2 at the least:
+    sum_j 2^-35 M min(2^8, max_j 2^e_j / min_j 2^e_j) |code_j|.
+    LSE: sum_j w_j d_j, four roundings (score, less the reference, the reference, the end) of
+    numbers below |x| + |e| + 64 by 2^-24, 2^-21 for the exponentials and the logarithm."""
+    scale = c.D ** -0.5 if scale is None else scale
+    off = offsets.tolist()
+    G = q.shape[1] // c.Hkv
+    half = 2.0 ** -11 if c.quant else 2.0 ** -8
+    for b, (k, v) in enumerate(c.dense):
+        n, m = off[b + 1] - off[b], c.lens[b]
+        rows = slice(off[b], off[b + 1])
+        pos = torch.arange(n, device="cuda") + (m - n)
+        seen = torch.arange(m, device="cuda")[None] <= (pos[:, None] if causal else m)
+        for h in range(q.shape[1]):
+            if only and (b, h) not in only:
+                continue
+            kh, vh, qh = k[:, h // G], v[:, h // G], q[rows, h].double()
+            x = (scale * (qh @ kh.T)).masked_fill(~seen, -math.inf)
+            rl = torch.logsumexp(x, 1)
+            w = torch.exp(x - rl[:, None])
+            ro = w @ vh
+            most = qh.abs().amax(1, keepdim=True)
+            small = (qh != 0) & (qh.abs() < 2.0 ** -14 * most)
+            d = w * scale * ((c.D * 2.0 ** -23 * qh.abs() + 2.0 ** -25 * most * small) @ kh.abs().T)
+            bound = 2.0 ** -8 * ro.abs() + (half + m * 2.0 ** -27) * (w @ vh.abs()) + d @ vh.abs() + d.sum(1, keepdim=True) * ro.abs()
+            far = torch.zeros(n, device="cuda", dtype=torch.float64)
+            if c.quant:
+                e = _exponents(c, b)[:, h // G]
+                top = (w * torch.exp2(e)).amax(1, keepdim=True) * 2.0 ** min(8.0, float(e.max() - e.min()))
+                bound += 2.0 ** -35 * top * (seen.double() @ (vh.abs() / torch.exp2(e)[:, None]))
+                far += e.abs().amax()
+            off_by = (o[rows, h].double() - ro).abs() / (1.02 * bound + 1e-30)
+            assert float(off_by.max()) <= 1, (b, h, int(off_by.amax(1).argmax()), float(off_by.max()))
+            tol = 1.02 * d.sum(1) + 2.0 ** -21 + 2.0 ** -22 * (x.amax(1).abs() * math.log2(math.e) + far + 64)
+            off_by = (lse[rows, h].double() - rl).abs() / tol
+            assert float(off_by.max()) <= 1, (b, h, int(off_by.argmax()), float(off_by.max()))
+    assert attn.attn_get_device_error() == 0
+
+
+QUANT = pytest.mark.parametrize("quant", [False, True], ids=["bf16", "e4m3"])
+# the kernel for few rows and the one for many
+KERNELS = pytest.mark.parametrize("G,new", [(4, 3), (2, 70)])
+
+
+@QUANT
+@KERNELS
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 128])
+def test_plain_values(quant, G, new, D, page):
+    lens = [300, 129, 2000]
+    c = ref.Cache(lens, 2, D, page, quant, seed=1)
+    offsets = ref.offsets_of([new] * 3)
+    q = _randn((3 * new, 2 * G, D), 2)
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
+    check_range(o, lse, q, c, offsets)
+
+
+@QUANT
+@KERNELS
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("k,v", [(30, 0), (16, 0)])
+def test_unseen_keys_have_no_influence(quant, G, new, D, k, v):
+    """The last token's K and V far larger than the others: the rows in front of it do not see
+    it (and the row that does is next to orthogonal to it)."""
+    lens = [300, 77]
+    c = ref.Cache(lens, 1, D, 16, quant, seed=3)
+    offsets = ref.offsets_of([new, new])
+    q = _randn((2 * new, G, D), 4)
+    q[new - 1] = q[2 * new - 1] = 0
+    for b, n in enumerate(lens):
+        resize(c, b, n - 1, k, v)
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
+    check_range(o, lse, q, c, offsets)
+
+
+@QUANT
+@KERNELS
+@pytest.mark.parametrize("e", [12, 15, 22, 30])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_large_key_across_the_query(quant, G, new, e, D):
+    """A key that is seen by all, large in a dimension that no query has: its score is 0."""
+    lens = [300, 90]
+    c = ref.Cache(lens, 1, D, 32, quant, seed=5)
+    offsets = ref.offsets_of([new, new])
+    q = _randn((2 * new, G, D), 6)
+    q[..., 0] = 0
+    for b in range(2):
+        at = int(c.table[b, 0])
+        x = torch.zeros(D, device="cuda")
+        x[0] = 256.0
+        if quant:
+            c.kp.view(torch.uint8)[at, 0, 5] = x.to(ref.E4M3).view(torch.uint8)
+            c.ks[at, 0, 5] = 127
+        c.dense[b][0][5] = x.double()
+        resize(c, b, 5, e)
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
+    check_range(o, lse, q, c, offsets)
