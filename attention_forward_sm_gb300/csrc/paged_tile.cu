@@ -139,6 +139,8 @@ struct TileShared {
   // bytes, or kScaleEach (of the tiles i, i + 8, ...; the converting warps are three ahead
   // at most).
   uint2 kv_scale[8];
+  uint4 v_silent[8];  // V's with kScaleEach: rows that are zeros, NaN or not there (row 4 l + i:
+                      // bit l of word i)
   CostShared plan;
   uint32_t tmem_base;
   int abort_flag;
@@ -147,17 +149,16 @@ struct TileShared {
 // In place of the scale byte of a tile: its codes were converted as they are, and each key has
 // its own.
 constexpr uint32_t kScaleEach = 0;
-// Scales of K so far apart at most are brought under the largest one: a code is a multiple of
-// 2^-9, and f16 holds multiples of 2^-24.
-constexpr uint32_t kScaleSpanK = 14;
+// Scales so far apart at most are brought under the largest one.  K: a code is a multiple of
+// 2^-9, and f16 holds multiples of 2^-24.  V: the tile's weights are over that of a
+// row with the largest scale, which need not have any, and end at 2^-24 too.
+constexpr uint32_t kScaleSpanK = 14, kScaleSpanV = 8;
 
-// The factor 2^(scale - most) of a row among those of a tile, as f16: exact down to 2^-24,
-// 0 below (of V: a row that far below its neighbours is lost next to them).  1 where each
-// key has its own scale, NaN for a row that stands for it.
+// The factor 2^(scale - most) of a row among those of a tile, as f16; 1 where each key has its
+// own scale, NaN for a row that stands for it.  (Further below there are only zeros.)
 __device__ __forceinline__ uint32_t f16_factor(uint32_t scale, uint32_t most) {
   const uint32_t d = most == kScaleEach ? 0 : most - scale;
-  const uint32_t f = d <= 14 ? (15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
-  return scale == kScaleNan ? 0x7FFFu : f;
+  return scale == kScaleNan ? 0x7FFFu : d <= kScaleSpanK ? (15 - d) << 10 : 0u;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t y;
@@ -194,18 +195,18 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
     *reinterpret_cast<uint4*>(to + at0) = make_uint4(y[0], y[1], y[2], y[3]);
     *reinterpret_cast<uint4*>(to + (at0 ^ 16u)) = make_uint4(y[4], y[5], y[6], y[7]);
   };
-  // The largest of a tile's scales, and whether all are within 14 of it and there is
+  // The largest of a tile's scales, and whether all are within `span` of it and there is
   // nothing odd: then every factor is a normal f16 number.  Else only rows count that are
   // there and not NaN, nor zeros, whose scale says 2^0 and could leave nothing of the
   // others; landed() says that the codes are in place (false: they never will be).
-  // kScaleEach where those that count are more than `span` apart.
+  // kScaleEach where those that count are more than `span` apart; silent: the others.
   auto largest = [&](const uint8_t* scales, const uint8_t* codes, bool whole, int rows, uint32_t bad,
-                     uint32_t span, bool* plain, uint32_t* most, auto landed) {
+                     uint32_t span, bool* plain, uint32_t* most, uint4* silent, auto landed) {
     const uint32_t w = reinterpret_cast<const uint32_t*>(scales)[lane];
     uint32_t s[4] = {w & 255u, w >> 8 & 255u, w >> 16 & 255u, w >> 24};
     *most = __reduce_max_sync(0xFFFFFFFFu, max(max(s[0], s[1]), max(s[2], s[3])));
     const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(min(s[0], s[1]), min(s[2], s[3])));
-    *plain = whole && *most != kScaleNan && *most - least <= 14;
+    *plain = whole && *most != kScaleNan && *most - least <= span;
     if (*plain) return true;
     bool zeros = false;
     uint32_t counts = 15;  // a bit for each of the lane's rows
@@ -235,7 +236,13 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
       lo_scale = min(lo_scale, s[i]);
     }
     *most = __reduce_max_sync(0xFFFFFFFFu, hi_scale);
-    if (__reduce_min_sync(0xFFFFFFFFu, lo_scale) + span < *most) *most = kScaleEach;
+    if (__reduce_min_sync(0xFFFFFFFFu, lo_scale) + span < *most) {
+      *most = kScaleEach;
+      *silent = make_uint4(__ballot_sync(0xFFFFFFFFu, !(counts & 1u)),
+                           __ballot_sync(0xFFFFFFFFu, !(counts & 2u)),
+                           __ballot_sync(0xFFFFFFFFu, !(counts & 4u)),
+                           __ballot_sync(0xFFFFFFFFu, !(counts & 8u)));
+    }
     return true;
   };
 
@@ -260,15 +267,19 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
       const bool whole = there >= kBN && !bad;
       if (!of_v) {
         // (V's raw tile is the next one, and comes in while this one is held)
-        if (!largest(scales, tile, whole, there, bad, kScaleSpanK, &plain, &most,
+        uint4 silent = make_uint4(0, 0, 0, 0);
+        if (!largest(scales, tile, whole, there, bad, kScaleSpanK, &plain, &most, &silent,
                      [] { return true; }) ||
-            !largest(scales + kBN, tile + C::kRawBytes, whole, there, bad, 255, &next_plain,
-                     &next_most, [&] {
+            !largest(scales + kBN, tile + C::kRawBytes, whole, there, bad, kScaleSpanV, &next_plain,
+                     &next_most, &silent, [&] {
               return warp_all(mbar_wait(&ms.raw_full[raw + 1], raw_round & 1, abort_flag, p.err,
                                         kErrWaitLoad, p.wait_limit_ns));
             }))
           return;
-        if (tid == 0) ms.kv_scale[step % 8] = make_uint2(most, next_most);
+        if (tid == 0) {
+          ms.kv_scale[step % 8] = make_uint2(most, next_most);
+          if (next_most == kScaleEach) ms.v_silent[step % 8] = silent;
+        }
       } else {
         most = next_most;
         plain = next_plain;
@@ -404,6 +415,22 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
     }
   };
 
+  // Exponents of the scales of V of these keys, f(i, exponent) for each; `silent` ones least.
+  [[maybe_unused]] auto each_exponent = [&](const Item& it, int key, const uint4& silent, auto f) {
+    const uint32_t none[4] = {silent.x, silent.y, silent.z, silent.w};
+    const int bit = (key & (kBN - 1)) / 4;
+#pragma unroll
+    for (int i = 0; i < 64; i += 16) {
+      const uint4 x = scale_bytes(p.c.vscale, it, key + i);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const bool is_silent = none[n % 4] >> (bit + (i + n) / 4) & 1u;
+        f(i + n, scale_exponent(is_silent ? kScaleLeast : w[n / 4] >> (8 * (n % 4)) & 255u));
+      }
+    }
+  };
+
   // waits for item k; false when there is none
   auto next_item = [&](uint32_t k, Item* it, uint32_t site) -> bool {
     if (!warp_all(mbar_wait(&ms.item_full[k & 1], (k >> 1) & 1, abort_flag, p.err, site,
@@ -485,10 +512,11 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         }
         tc_fence_after();
         float s[64];
+        [[maybe_unused]] const uint32_t tile = (steps + static_cast<uint32_t>(j - it.tile0)) % 8;
         [[maybe_unused]] uint2 by = make_uint2(127, 127);
         if constexpr (kQuant) {
           // (there since S is: its operands were converted before)
-          by = ms.kv_scale[(steps + static_cast<uint32_t>(j - it.tile0)) % 8];
+          by = ms.kv_scale[tile];
           // (in two: the launch's 80 registers do not hold 64 results of one instruction)
           uint32_t sr[2][32];
           tmem_ld_pair32_start<64>(s_addr, sr[0]);
@@ -503,11 +531,17 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
         }
+        // Quantised, the tile's K and V are to be multiplied by 2^a and 2^e: scores by 2^a,
+        // and the weights stand for 2^(x + e), with the maximum of x + e; the sum is of 2^x
+        // over the same reference.
+        float scale = p.scale_log2;
+        [[maybe_unused]] float e = 0.f, sum_scale = 1.f;
         if constexpr (kQuant) {
-          if (by.x == kScaleEach) {
-            each_scale(it, j * kBN + c * 64, s);
-            by.x = 127;
-          }
+          if (by.x == kScaleEach) each_scale(it, j * kBN + c * 64, s);
+          // (never 0, as scale_log2: the product of a row of zeros and the smallest of scales)
+          scale = fmaxf(by.x == kScaleEach ? row_scale : row_scale * scale_value(by.x), 1e-37f);
+          e = scale_exponent(by.y);
+          sum_scale = __uint_as_float((254u - by.y) << 23);
         }
         if ((j + 1) * kBN > all_see) {
           // columns [0, end) and [from, to) of this thread's are visible
@@ -519,6 +553,14 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (i >= end && (i < from || i >= to)) s[i] = -CUDART_INF_F;
+        }
+        if constexpr (kQuant) {
+          if (by.y == kScaleEach) {  // x + e of every key in place of the scores
+            each_exponent(it, j * kBN + c * 64, ms.v_silent[tile],
+                          [&](int i, float e_i) { s[i] = fmaf(s[i], scale, e_i); });
+            scale = 1.f;
+            e = sum_scale = 0.f;
+          }
         }
         float mx;
         {
@@ -534,17 +576,6 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
           mx = max3f(a0, a1, fmaxf(a2, a3));
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
         }
-        // Quantised, the tile's K and V are to be multiplied by 2^a and 2^e: scores by 2^a,
-        // and the weights stand for 2^(x + e), with the maximum of x + e; the sum is of 2^x
-        // over the same reference.
-        float scale = p.scale_log2;
-        [[maybe_unused]] float e = 0.f, sum_scale = 1.f;
-        if constexpr (kQuant) {
-          // (never 0, as scale_log2: the product of a row of zeros and the smallest of scales)
-          scale = fmaxf(row_scale * scale_value(by.x), 1e-37f);
-          e = scale_exponent(by.y);
-          sum_scale = __uint_as_float((254u - by.y) << 23);
-        }
         float m_tile = mx * scale;  // (scale > 0)
         if constexpr (kQuant) m_tile += e;
         float alpha = 1.f;
@@ -555,6 +586,12 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         // p = 2^(s * scale - m); a row that has seen nothing keeps m = -inf: its
         // scores are -inf and stay it next to a reference of 0
         const float neg_m = (m == -CUDART_INF_F ? 0.f : -m) + (kQuant ? e : 0.f);
+        if constexpr (kQuant) {
+          l *= alpha;
+          if (by.y == kScaleEach)
+            each_exponent(it, j * kBN + c * 64, ms.v_silent[tile],
+                          [&](int i, float e_i) { l += ex2_approx(s[i] + (neg_m - e_i)); });
+        }
         const uint64_t scale2 = f32x2(scale, scale);
         const uint64_t negm2 = f32x2(neg_m, neg_m);
         uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
@@ -573,7 +610,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         }
         float u0, u1;
         unpack_f32x2(add_f32x2(acc0, acc1), u0, u1);
-        l = fmaf(l, alpha, kQuant ? (u0 + u1) * sum_scale : u0 + u1);
+        l = kQuant ? fmaf(u0 + u1, sum_scale, l) : fmaf(l, alpha, u0 + u1);
         // Rescale O_t where a maximum moved: every product of earlier key tiles has
         // retired (issued before the S_t that woke this warp), that of this one waits.
         if (j > it.tile0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {

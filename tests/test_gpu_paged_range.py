@@ -104,7 +104,7 @@ def test_plain_values(quant, G, new, D, page):
 @QUANT
 @KERNELS
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("k,v", [(30, 0), (16, 0)])
+@pytest.mark.parametrize("k,v", [(30, 0), (0, 30), (16, 16), (0, 11)])
 def test_unseen_keys_have_no_influence(quant, G, new, D, k, v):
     """The last token's K and V far larger than the others: the rows in front of it do not see
     it (and the row that does is next to orthogonal to it)."""
@@ -141,3 +141,60 @@ def test_a_large_key_across_the_query(quant, G, new, e, D):
         resize(c, b, 5, e)
     o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
     check_range(o, lse, q, c, offsets)
+
+
+@QUANT
+@KERNELS
+@pytest.mark.parametrize("sigma,v", [(1.0, 30), (1.0, 9), (2.0 ** -40, 90)])
+def test_large_values_of_little_weight(quant, G, new, sigma, v):
+    """A value 2^v times the others', under a weight that leaves nothing of it."""
+    lens = [300, 90]
+    c = ref.Cache(lens, 1, 64, 64, quant, seed=7)
+    offsets = ref.offsets_of([new, new])
+    q = _randn((2 * new, G, 64), 8)
+    q[..., 0] = 16.0
+    for b, n in enumerate(lens):
+        for i in range(n):
+            resize(c, b, i, 0, round(math.log2(sigma)))
+        at = int(c.table[b, 0])
+        x = torch.zeros(64, device="cuda")
+        x[0] = -64.0  # a score of -128
+        if quant:
+            c.kp.view(torch.uint8)[at, 0, 9] = x.to(ref.E4M3).view(torch.uint8)
+            c.ks[at, 0, 9] = 127
+        else:
+            c.kp[at, 0, 9] = x.to(BF16)
+        c.dense[b][0][9] = x.double()
+        resize(c, b, 9, 0, v)
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
+    check_range(o, lse, q, c, offsets)
+
+
+@QUANT
+@KERNELS
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_scale_decides_a_row(quant, G, new, D):
+    """Queries that each select one key, whose sizes run far apart: every row is the value of
+    its key, and no other."""
+    n = D
+    c = ref.Cache([n], 1, D, 16, quant, seed=9)
+    k = torch.zeros(n, D, device="cuda")
+    k[torch.arange(n), torch.arange(n)] = 8.0
+    c.dense[0][0][:] = k.double()[:, None]
+    shift = [(0, -60), (9, 0), (-20, 3), (14, 12), (-3, 30), (0, -90), (20, 7)]
+    for i in range(n):
+        at, slot = int(c.table[0, i // 16]), i % 16
+        if quant:
+            c.kp.view(torch.uint8)[at, 0, slot] = k[i].to(ref.E4M3).view(torch.uint8)
+            c.ks[at, 0, slot] = 127
+        resize(c, 0, i, *shift[i % 7])
+    for first in range(0, n - new + 1, max(new // 2, 1) * (7 if new < 8 else 1)):
+        q = torch.zeros(new, G, D, device="cuda")
+        for r in range(new):
+            for h in range(G):
+                i = (first + r + 3 * h) % n
+                q[r, h, i] = 12.5 * 2.0 ** -shift[i % 7][0]  # a score of 100
+        q = q.to(BF16)
+        offsets = ref.offsets_of([new])
+        o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, causal=False, scale=1.0, **c.scales())
+        check_range(o, lse, q, c, offsets, causal=False, scale=1.0)
