@@ -123,6 +123,13 @@ struct CostWalk {
   }
 };
 
+// What the softmax needs to have a key tile's scales one by one.
+struct FarKeys {
+  uint2 by;             // as scale bytes, or kScaleEach
+  uint4 silent;         // rows of V that are zeros, NaN or not there (row 4 l + i: bit l of word i)
+  int b, h, len, key0;  // request, KV head, its tokens, the tile's first key
+};
+
 template <bool kQuant>
 struct TileShared {
   uint64_t q_full[2], q_ready[2];    // per item of query tile t (ready: converted to f16)
@@ -135,12 +142,11 @@ struct TileShared {
   uint64_t item_full[2], item_empty[2];
   Item item[2];
   uint32_t raw_bad[6];  // copies of the tile whose page is out of range, a bit each
-  // Quantised: what the converted K and V of a key tile are to be multiplied by, as scale
-  // bytes, or kScaleEach (of the tiles i, i + 8, ...; the converting warps are three ahead
-  // at most).
-  uint2 kv_scale[8];
-  uint4 v_silent[8];  // V's with kScaleEach: rows that are zeros, NaN or not there (row 4 l + i:
-                      // bit l of word i)
+  // Quantised: what the converted K and V of a key tile are to be multiplied by, 2^a and 2^e, as
+  // 2^a, e, 2^-e and whether it is in `far` how (then 1, and where V's scales are each key's
+  // own 0 and 0): of the tiles i, i + 8, ...; the converting warps are three ahead at most.
+  float4 kv_scale[8];
+  FarKeys far[8];
   CostShared plan;
   uint32_t tmem_base;
   int abort_flag;
@@ -277,8 +283,15 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
             }))
           return;
         if (tid == 0) {
-          ms.kv_scale[step % 8] = make_uint2(most, next_most);
-          if (next_most == kScaleEach) ms.v_silent[step % 8] = silent;
+          const bool far_k = most == kScaleEach, far_v = next_most == kScaleEach;
+          ms.kv_scale[step % 8] =
+              make_float4(far_k || far_v ? 1.f : scale_value(most),
+                          far_v ? 0.f : scale_exponent(next_most),
+                          far_v ? 0.f : __uint_as_float((254u - next_most) << 23),
+                          far_k || far_v ? 1.f : 0.f);
+          if (far_k || far_v)
+            ms.far[step % 8] = FarKeys{make_uint2(most, next_most), silent, it.b, it.h, it.len,
+                                       (it.tile0 + static_cast<int>(i >> 1)) * kBN};
         }
       } else {
         most = next_most;
@@ -331,6 +344,84 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
       }
     }
   }
+}
+
+// A key tile whose scales lie far apart: a thread's 64 scores in tensor memory, from s_addr on, get
+// K's scales, or, where V's are each key's own, x + e takes their place, and what is returned
+// is the sum of 2^x over the reference that the tile gets.  Such tiles are few, and none of the
+// softmax' registers are spent on them: a function of its own, which reads the scales where
+// they are.  (1024 tokens behind 30000, 32 heads on 8, D 128, no such tile: without all this 402 us,
+// so 408, as a branch within the loop 416.)
+__device__ __noinline__ float far_scores(const PagedArrays& c, const FarKeys& far, uint32_t s_addr,
+                                         float row_scale, float m, int vis, int half) {
+  const uint2 by = far.by;
+  const float by_k = fmaxf(by.x == kScaleEach ? row_scale : row_scale * scale_value(by.x), 1e-37f);
+  const uint32_t none[4] = {far.silent.x, far.silent.y, far.silent.z, far.silent.w};
+  // 16 scale bytes from key on; 2^0 where there are none
+  auto bytes = [&](const uint8_t* scales, int key) {
+    const int* entry = c.table + static_cast<size_t>(far.b) * c.M + (key >> c.page_bits);
+    const int id = key < far.len ? __ldcg(entry) : -1;
+    if (static_cast<unsigned>(id) >= static_cast<unsigned>(c.P))
+      return make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    return __ldcg(reinterpret_cast<const uint4*>(
+        scales + (static_cast<size_t>(id) * c.Hkv + far.h) * c.page + (key & (c.page - 1))));
+  };
+  auto exponents = [&](int col, float (&e)[16]) {
+    const uint4 x = bytes(c.vscale, far.key0 + col);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const bool silent = none[i % 4] >> ((col + i) / 4) & 1u;
+      e[i] = scale_exponent(silent ? kScaleLeast : w[i / 4] >> (8 * (i % 4)) & 255u);
+    }
+  };
+  float top = -CUDART_INF_F;
+#pragma unroll 1
+  for (int i = 0; i < 64; i += 16) {
+    const int col = half * 64 + i;
+    uint32_t v[16];
+    tmem_ld_pair16<64>(s_addr + i, v);
+    if (by.x == kScaleEach) {
+      const uint4 x = bytes(c.kscale, far.key0 + col);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int n = 0; n < 16; ++n)
+        v[n] = __float_as_uint(__uint_as_float(v[n]) *
+                               scale_value(w[n / 4] >> (8 * (n % 4)) & 255u));
+    }
+    if (by.y == kScaleEach) {
+      float e[16];
+      exponents(col, e);
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const float x = fmaf(__uint_as_float(v[n]), by_k, e[n]);
+        if (far.key0 + col + n < vis) top = fmaxf(top, x);
+        v[n] = __float_as_uint(x);
+      }
+    }
+    __syncwarp();
+    tmem_st_pair16<64>(s_addr + i, v);
+  }
+  tmem_st_wait();
+  float sum = 0.f;
+  if (by.y == kScaleEach) {
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+    if (top > m + 8.f) m = top;  // (as the softmax will)
+    const float from_m = m == -CUDART_INF_F ? 0.f : -m;
+#pragma unroll 1
+    for (int i = 0; i < 64; i += 16) {
+      const int col = half * 64 + i;
+      uint32_t v[16];
+      float e[16];
+      tmem_ld_pair16<64>(s_addr + i, v);
+      exponents(col, e);
+#pragma unroll
+      for (int n = 0; n < 16; ++n)
+        if (far.key0 + col + n < vis) sum += ex2_approx(__uint_as_float(v[n]) + (from_m - e[n]));
+      __syncwarp();
+    }
+  }
+  return sum;
 }
 
 template <int D, bool kQuant>
@@ -389,47 +480,6 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = ms.tmem_base;
-
-  // Quantised: 16 scale bytes of an item's keys from `key` on; 2^0 where there are none.
-  [[maybe_unused]] auto scale_bytes = [&](const uint8_t* scales, const Item& it, int key) {
-    uint4 x = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    if (key < it.len) {
-      const int id =
-          __ldcg(&p.c.table[static_cast<size_t>(it.b) * p.c.M + (key >> p.c.page_bits)]);
-      if (static_cast<unsigned>(id) < static_cast<unsigned>(p.c.P))
-        x = __ldcg(reinterpret_cast<const uint4*>(
-            scales + (static_cast<size_t>(id) * p.c.Hkv + it.h) * p.c.page +
-            (key & (p.c.page - 1))));
-    }
-    return x;
-  };
-  // Scores of 64 keys from `key` on, each times the scale of its K.  (Read where they are: a
-  // tile's scales lie this far apart in few caches, and are not worth shared memory.)
-  [[maybe_unused]] auto each_scale = [&](const Item& it, int key, float (&s)[64]) {
-#pragma unroll
-    for (int i = 0; i < 64; i += 16) {
-      const uint4 x = scale_bytes(p.c.kscale, it, key + i);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int n = 0; n < 16; ++n) s[i + n] *= scale_value(w[n / 4] >> (8 * (n % 4)) & 255u);
-    }
-  };
-
-  // Exponents of the scales of V of these keys, f(i, exponent) for each; `silent` ones least.
-  [[maybe_unused]] auto each_exponent = [&](const Item& it, int key, const uint4& silent, auto f) {
-    const uint32_t none[4] = {silent.x, silent.y, silent.z, silent.w};
-    const int bit = (key & (kBN - 1)) / 4;
-#pragma unroll
-    for (int i = 0; i < 64; i += 16) {
-      const uint4 x = scale_bytes(p.c.vscale, it, key + i);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const bool is_silent = none[n % 4] >> (bit + (i + n) / 4) & 1u;
-        f(i + n, scale_exponent(is_silent ? kScaleLeast : w[n / 4] >> (8 * (n % 4)) & 255u));
-      }
-    }
-  };
 
   // waits for item k; false when there is none
   auto next_item = [&](uint32_t k, Item* it, uint32_t site) -> bool {
@@ -512,15 +562,25 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         }
         tc_fence_after();
         float s[64];
-        [[maybe_unused]] const uint32_t tile = (steps + static_cast<uint32_t>(j - it.tile0)) % 8;
-        [[maybe_unused]] uint2 by = make_uint2(127, 127);
+        [[maybe_unused]] float4 by;
+        [[maybe_unused]] float by_row = row_scale;
+        [[maybe_unused]] float each_sum = 0.f;
         if constexpr (kQuant) {
           // (there since S is: its operands were converted before)
-          by = ms.kv_scale[tile];
+          const uint32_t tile = (steps + static_cast<uint32_t>(j - it.tile0)) % 8;
           // (in two: the launch's 80 registers do not hold 64 results of one instruction)
           uint32_t sr[2][32];
           tmem_ld_pair32_start<64>(s_addr, sr[0]);
           tmem_ld_pair32_start<64>(s_addr + 32, sr[1]);
+          by = ms.kv_scale[tile];
+          if (__builtin_expect(by.w != 0.f, 0)) {
+            tmem_ld_finish(sr[0]);  // (what has come is not used)
+            tmem_ld_finish(sr[1]);
+            each_sum = far_scores(p.c, ms.far[tile], s_addr, row_scale, m, vis, c);
+            if (by.z == 0.f) by_row = 1.f;
+            tmem_ld_pair32_start<64>(s_addr, sr[0]);
+            tmem_ld_pair32_start<64>(s_addr + 32, sr[1]);
+          }
           tmem_ld_finish(sr[0]);
           tmem_ld_finish(sr[1]);
 #pragma unroll
@@ -530,18 +590,6 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
           tmem_ld_pair64<64>(s_addr, sr);
 #pragma unroll
           for (int i = 0; i < 64; ++i) s[i] = __uint_as_float(sr[i]);
-        }
-        // Quantised, the tile's K and V are to be multiplied by 2^a and 2^e: scores by 2^a,
-        // and the weights stand for 2^(x + e), with the maximum of x + e; the sum is of 2^x
-        // over the same reference.
-        float scale = p.scale_log2;
-        [[maybe_unused]] float e = 0.f, sum_scale = 1.f;
-        if constexpr (kQuant) {
-          if (by.x == kScaleEach) each_scale(it, j * kBN + c * 64, s);
-          // (never 0, as scale_log2: the product of a row of zeros and the smallest of scales)
-          scale = fmaxf(by.x == kScaleEach ? row_scale : row_scale * scale_value(by.x), 1e-37f);
-          e = scale_exponent(by.y);
-          sum_scale = __uint_as_float((254u - by.y) << 23);
         }
         if ((j + 1) * kBN > all_see) {
           // columns [0, end) and [from, to) of this thread's are visible
@@ -553,14 +601,6 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (i >= end && (i < from || i >= to)) s[i] = -CUDART_INF_F;
-        }
-        if constexpr (kQuant) {
-          if (by.y == kScaleEach) {  // x + e of every key in place of the scores
-            each_exponent(it, j * kBN + c * 64, ms.v_silent[tile],
-                          [&](int i, float e_i) { s[i] = fmaf(s[i], scale, e_i); });
-            scale = 1.f;
-            e = sum_scale = 0.f;
-          }
         }
         float mx;
         {
@@ -576,6 +616,17 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
           mx = max3f(a0, a1, fmaxf(a2, a3));
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
         }
+        // Quantised, the tile's K and V are to be multiplied by 2^a and 2^e: scores by 2^a,
+        // and the weights stand for 2^(x + e), with the maximum of x + e; the sum is of 2^x
+        // over the same reference.
+        float scale = p.scale_log2;
+        [[maybe_unused]] float e = 0.f, sum_scale = 1.f;
+        if constexpr (kQuant) {
+          // (never 0, as scale_log2: the product of a row of zeros and the smallest of scales)
+          scale = fmaxf(by_row * by.x, 1e-37f);
+          e = by.y;
+          sum_scale = by.z;
+        }
         float m_tile = mx * scale;  // (scale > 0)
         if constexpr (kQuant) m_tile += e;
         float alpha = 1.f;
@@ -586,12 +637,6 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         // p = 2^(s * scale - m); a row that has seen nothing keeps m = -inf: its
         // scores are -inf and stay it next to a reference of 0
         const float neg_m = (m == -CUDART_INF_F ? 0.f : -m) + (kQuant ? e : 0.f);
-        if constexpr (kQuant) {
-          l *= alpha;
-          if (by.y == kScaleEach)
-            each_exponent(it, j * kBN + c * 64, ms.v_silent[tile],
-                          [&](int i, float e_i) { l += ex2_approx(s[i] + (neg_m - e_i)); });
-        }
         const uint64_t scale2 = f32x2(scale, scale);
         const uint64_t negm2 = f32x2(neg_m, neg_m);
         uint64_t acc0 = f32x2(0.f, 0.f), acc1 = acc0;
@@ -610,7 +655,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         }
         float u0, u1;
         unpack_f32x2(add_f32x2(acc0, acc1), u0, u1);
-        l = kQuant ? fmaf(u0 + u1, sum_scale, l) : fmaf(l, alpha, u0 + u1);
+        l = fmaf(l, alpha, kQuant ? fmaf(u0 + u1, sum_scale, each_sum) : u0 + u1);
         // Rescale O_t where a maximum moved: every product of earlier key tiles has
         // retired (issued before the S_t that woke this warp), that of this one waits.
         if (j > it.tile0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
