@@ -79,6 +79,15 @@ constexpr uint32_t kScaleNan = 255, kScaleMost = 134;
 // The least scale that a row has, 2^-100; a row of zeros has 2^0.
 constexpr uint32_t kScaleLeast = 27, kScaleOfZeros = 127;
 
+// Weights of V's codes, in f16: 2^(x + e - the largest x + e there was) stands for 2^kWeightTop
+// times it, and may grow by 2^kWeightRoom before the reference follows (2^15 in all, f16
+// ends below 2^16).  So a weight is rounded to 11 bits down to 2^-24 of the largest, and
+// many thousands of small ones beside a single large one are not lost.  The sum of weights
+// is of 2^x, over 2^kSumShift times that reference: with e between -100 and 100 and up to 2^21
+// keys it stays within 32 bits.  O is 2^kWeightLift times what goes with that sum.
+constexpr float kWeightTop = 10.f, kWeightRoom = 5.f, kSumShift = 8.f;
+constexpr float kWeightLift = kWeightTop + kSumShift, kWeightUnit = 0x1p-18f;
+
 // The codes in bytes 1 and 3 of u (the others do not matter), times the factors f.
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t u, uint32_t f) {
   const uint32_t x = (u >> 4 & 0x07F007F0u) | (u & 0x80008000u);

@@ -281,8 +281,8 @@ struct CostPlan {
 };
 
 // A state (maximum, sum, O) of one row that states are added to; a lane holds
-// D / 32 consecutive elements of O.  The maximum of a state that saw nothing is
-// -inf, its sum and O 0; a NaN among the scores leaves them NaN.
+// D / 32 consecutive elements of O (quantised, times 2^kWeightLift).  The maximum of a state
+// that saw nothing is -inf, its sum and O 0; a NaN among the scores leaves them NaN.
 template <int D>
 struct State {
   static constexpr int E = D / 32;
@@ -342,7 +342,7 @@ struct State {
   // O and LSE of row t, query head hq
   __device__ void finish(const PagedParams& p, int t, int hq, float top, int lane) const {
     const size_t row = static_cast<size_t>(t) * p.Hq + hq;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : (p.c.quant ? kWeightUnit : 1.f) / l;
     uint32_t* dst = static_cast<uint32_t*>(p.o) + row * (D / 2) + lane * (E / 2);
     if constexpr (E == 4)
       *reinterpret_cast<uint2*>(dst) =

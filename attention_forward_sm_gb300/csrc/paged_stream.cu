@@ -443,10 +443,9 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
             if (un.key0 + (k < 2 ? row_lo : row_hi) >= vis[nt][k & 1]) x[nt][k] = -CUDART_INF_F;
       }
       // Quantised, a weight of V's codes is 2^(x + e), e the exponent of V's scale, and the
-      // maximum is of x + e: then no weight is more than 2^8, and what f16 loses (steps
-      // of 2^-24) is next to the largest product, since every row of codes reaches
-      // beyond 224 but one of zeros, which says 2^0 and counts as the least.  The sum of
-      // weights is of 2^x, over the same reference.
+      // maximum is of x + e (see kWeightTop): what f16 loses is next to the largest
+      // product, since every row of codes reaches beyond 224 but one of zeros, which says
+      // 2^0 and counts as the least.
       float ev[2] = {0.f, 0.f};
       [[maybe_unused]] uint32_t vscale[2] = {127, 127};
       if constexpr (kQuant) {
@@ -466,13 +465,16 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
         if (vscale[0] != kScaleNan) ev[0] = scale_exponent(vscale[0]);
         if (vscale[1] != kScaleNan) ev[1] = scale_exponent(vscale[1]);
       }
-      // The maximum moves only when a score is above it by more than 2^8: a stale one
-      // is as good (the sum has the same), and the vote is cheaper than the maximum.
+      // The maximum moves only when a score is above it by more than 2^8 (quantised
+      // 2^kWeightRoom): a stale one is as good (the sum has the same), and the vote is cheaper
+      // than the maximum.
+      constexpr float kShift = kQuant ? kSumShift : 0.f;
+      constexpr float kStale = kQuant ? kWeightRoom - kSumShift : 8.f;
       bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) above = above || x[nt][k] + ev[k >> 1] > m[nt][k & 1] + 8.f;
+        for (int k = 0; k < 4; ++k) above = above || x[nt][k] + ev[k >> 1] > m[nt][k & 1] + kStale;
       if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -482,7 +484,8 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-            if (top > m[nt][k] + 8.f) {
+            if (top > m[nt][k] + kStale) {
+              top += kShift;
               const float alpha = ex2_approx(m[nt][k] - top);  // 0 the first time
               m[nt][k] = top;
               l[nt][k] *= alpha;
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
           const float d = x[nt][k] - m[nt][k & 1];
           w[k] = none ? 0.f : ex2_approx(d);
           l[nt][k & 1] += w[k];
-          if constexpr (kQuant) w[k] = none ? 0.f : ex2_approx(d + ev[k >> 1]);
+          if constexpr (kQuant) w[k] = none ? 0.f : ex2_approx(d + (ev[k >> 1] + kWeightLift));
         }
         // rounded for the product: to bf16, as V is, or f16
         pf[nt][0] = transpose_8x8(kQuant ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));

@@ -143,8 +143,9 @@ struct TileShared {
   Item item[2];
   uint32_t raw_bad[6];  // copies of the tile whose page is out of range, a bit each
   // Quantised: what the converted K and V of a key tile are to be multiplied by, 2^a and 2^e, as
-  // 2^a, e, 2^-e and whether it is in `far` how (then 1, and where V's scales are each key's
-  // own 0 and 0): of the tiles i, i + 8, ...; the converting warps are three ahead at most.
+  // 2^a, E = e + kWeightLift, 2^-E and whether it is in `far` how (then 1, and where V's scales
+  // are each key's own kWeightLift and 0): of the tiles i, i + 8, ...; the converting warps
+  // are three ahead at most.
   float4 kv_scale[8];
   FarKeys far[8];
   CostShared plan;
@@ -286,8 +287,10 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
           const bool far_k = most == kScaleEach, far_v = next_most == kScaleEach;
           ms.kv_scale[step % 8] =
               make_float4(far_k || far_v ? 1.f : scale_value(most),
-                          far_v ? 0.f : scale_exponent(next_most),
-                          far_v ? 0.f : __uint_as_float((254u - next_most) << 23),
+                          kWeightLift + (far_v ? 0.f : scale_exponent(next_most)),
+                          far_v ? 0.f
+                                : __uint_as_float((254u - static_cast<uint32_t>(kWeightLift) -
+                                                   next_most) << 23),
                           far_k || far_v ? 1.f : 0.f);
           if (far_k || far_v)
             ms.far[step % 8] = FarKeys{make_uint2(most, next_most), silent, it.b, it.h, it.len,
@@ -406,7 +409,8 @@ __device__ __noinline__ float far_scores(const PagedArrays& c, const FarKeys& fa
   float sum = 0.f;
   if (by.y == kScaleEach) {
     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-    if (top > m + 8.f) m = top;  // (as the softmax will)
+    top += kWeightLift;  // (from here as the softmax will)
+    if (top > m + (kWeightTop + kWeightRoom)) m = top - kWeightTop;
     const float from_m = m == -CUDART_INF_F ? 0.f : -m;
 #pragma unroll 1
     for (int i = 0; i < 64; i += 16) {
@@ -618,7 +622,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         }
         // Quantised, the tile's K and V are to be multiplied by 2^a and 2^e: scores by 2^a,
         // and the weights stand for 2^(x + e), with the maximum of x + e; the sum is of 2^x
-        // over the same reference.
+        // (with the references of kWeightTop).
         float scale = p.scale_log2;
         [[maybe_unused]] float e = 0.f, sum_scale = 1.f;
         if constexpr (kQuant) {
@@ -630,9 +634,10 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         float m_tile = mx * scale;  // (scale > 0)
         if constexpr (kQuant) m_tile += e;
         float alpha = 1.f;
-        if (m_tile > m + 8.f) {  // a stale maximum is as good up to there
-          alpha = ex2_approx(m - m_tile);  // 0 the first time
-          m = m_tile;
+        constexpr float kTop = kQuant ? kWeightTop : 0.f;
+        if (m_tile > m + (kQuant ? kTop + kWeightRoom : 8.f)) {  // a stale maximum is as good
+          alpha = ex2_approx(m - (m_tile - kTop));               // up to there; 0 the first time
+          m = m_tile - kTop;
         }
         // p = 2^(s * scale - m); a row that has seen nothing keeps m = -inf: its
         // scores are -inf and stay it next to a reference of 0
@@ -683,7 +688,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
       tc_fence_after();
       const float l_row = l + __shfl_xor_sync(0xFFFFFFFFu, l, 16);
       const bool whole = it.slot < 0;
-      const float inv = !whole ? 1.f : l_row == 0.f ? 0.f : 1.f / l_row;
+      const float inv = !whole ? 1.f : l_row == 0.f ? 0.f : (kQuant ? kWeightUnit : 1.f) / l_row;
       const size_t out_row = static_cast<size_t>(it.row0 + token) * p.Hq + it.h * p.G + r % p.G;
       const size_t part_row = static_cast<size_t>(max(it.slot, 0)) * (2 * kBM) + t * kBM + r;
 #pragma unroll

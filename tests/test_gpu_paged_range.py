@@ -198,3 +198,57 @@ def test_every_scale_decides_a_row(quant, G, new, D):
         offsets = ref.offsets_of([new])
         o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, causal=False, scale=1.0, **c.scales())
         check_range(o, lse, q, c, offsets, causal=False, scale=1.0)
+
+
+@QUANT
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,G,new", [(20, 4, 1), (1, 20, 240)])
+@pytest.mark.parametrize("bits", [20.4, 23.4, 25.4])
+def test_many_small_weights_beside_a_large_one(quant, D, B, G, new, bits):
+    """A first key that takes nearly all of the weight, but whose value is 0 in all dimensions
+    but one, and 2^17 others of 2^-bits of its weight each.  (So many requests or rows that a
+    CTA has one from the first key to the last.)"""
+    n, Hkv = 2 ** 17 + 77, 8
+    c = ref.Cache([n], Hkv, D, 128, quant, seed=11)
+    at = int(c.table[0, 0])
+    (k, v), dims = c.dense[0], torch.arange(D, device="cuda")
+    # the others' scores are 0, their values positive
+    k[1:, :, 0] = 0
+    k[0] = 64.0 * (dims == 0)
+    v.abs_()
+    v[0] = 3.5 * (dims == 0)
+    if quant:
+        c.kp.view(torch.uint8)[..., 0] = 0
+        c.vp.view(torch.uint8).bitwise_and_(0x7F)
+        for x, pages, scale in ((k, c.kp, c.ks), (v, c.vp, c.vs)):
+            pages.view(torch.uint8)[at, :, 0] = (x[0] * 64).float().clamp(max=448).to(ref.E4M3).view(torch.uint8)
+            scale[at, :, 0] = 127 - 6
+        k[0] = 7.0 * (dims == 0)
+    else:
+        c.kp[..., 0] = 0
+        c.vp.abs_()
+        c.kp[at, :, 0], c.vp[at, :, 0] = k[0].to(BF16), v[0].to(BF16)
+    # requests that share their pages
+    c.table, c.lens_t = c.table.repeat(B, 1), c.lens_t.repeat(B)
+    c.lens, c.dense = c.lens * B, c.dense * B
+    q = torch.zeros(B * new, Hkv * G, D, device="cuda")
+    q[..., 0] = bits * math.log(2) / float(k[0, 0, 0])
+    q = q.to(BF16)
+    offsets = ref.offsets_of([new] * B)
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, scale=1.0, **c.scales())
+    check_range(o, lse, q, c, offsets, scale=1.0, only=((0, 0), (B - 1, Hkv * G - 1)))
+
+
+@KERNELS
+@pytest.mark.parametrize("n", [130, 40000])
+def test_values_of_zeros(G, new, n):
+    """A cache whose V is all zeros: O is 0, LSE as ever."""
+    c = ref.Cache([n], 1, 64, 128, True, seed=15)
+    c.vp.view(torch.uint8).bitwise_and_(0x80)
+    c.vs.fill_(127)
+    c.dense[0][1].zero_()
+    offsets = ref.offsets_of([new])
+    q = _randn((new, G, 64), 16)
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
+    assert not o.any()
+    check_range(o, lse, q, c, offsets)
