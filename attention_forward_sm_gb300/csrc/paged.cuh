@@ -88,6 +88,14 @@ constexpr uint32_t kScaleLeast = 27, kScaleOfZeros = 127;
 constexpr float kWeightTop = 10.f, kWeightRoom = 5.f, kSumShift = 8.f;
 constexpr float kWeightLift = kWeightTop + kSumShift, kWeightUnit = 0x1p-18f;
 
+// 2^d in two factors.  Quantised, the references of a row's states are up to 200 apart, where
+// V's scales are, and 2^d alone would be 0 next to a sum that is as much above 1.
+template <bool kQuant>
+__device__ __forceinline__ float2 ex2_factors(float d) {
+  return kQuant ? make_float2(ex2_approx(fmaxf(d, -100.f)), ex2_approx(fminf(d + 100.f, 0.f)))
+                : make_float2(ex2_approx(d), 1.f);
+}
+
 // The codes in bytes 1 and 3 of u (the others do not matter), times the factors f.
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t u, uint32_t f) {
   const uint32_t x = (u >> 4 & 0x07F007F0u) | (u & 0x80008000u);

@@ -283,7 +283,7 @@ struct CostPlan {
 // A state (maximum, sum, O) of one row that states are added to; a lane holds
 // D / 32 consecutive elements of O (quantised, times 2^kWeightLift).  The maximum of a state
 // that saw nothing is -inf, its sum and O 0; a NaN among the scores leaves them NaN.
-template <int D>
+template <int D, bool kQuant>
 struct State {
   static constexpr int E = D / 32;
   float l = 0.f, o[E];
@@ -294,8 +294,9 @@ struct State {
   using Vec = std::conditional_t<E == 4, float4, float2>;
   // ml: its maximum and sum; top: the largest maximum of all
   __device__ void add(float2 ml, float top, const Vec& x) {
-    const float w = ml.x == -CUDART_INF_F ? 1.f : ex2_approx(ml.x - top);
-    l = fmaf(w, ml.y, l);
+    const float2 f = ex2_factors<kQuant>(ml.x == -CUDART_INF_F ? 0.f : ml.x - top);
+    const float w = f.x * f.y;
+    l = fmaf(f.x, ml.y * f.y, l);
     o[0] = fmaf(w, x.x, o[0]);
     o[1] = fmaf(w, x.y, o[1]);
     if constexpr (E == 4) {
@@ -323,11 +324,11 @@ struct State {
       float most = top;
 #pragma unroll
       for (int i = 0; i < 4; ++i) most = fmaxf(most, ml[i].x);
-      const float alpha = top == -CUDART_INF_F ? 1.f : ex2_approx(top - most);
+      const float2 f = ex2_factors<kQuant>(top == -CUDART_INF_F ? 0.f : top - most);
       top = most;
-      l *= alpha;
+      l = l * f.x * f.y;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= alpha;
+      for (int e = 0; e < E; ++e) o[e] *= f.x * f.y;
 #pragma unroll
       for (int i = 0; i < 4; ++i) add(ml[i], top, x[i]);
     }
@@ -342,7 +343,7 @@ struct State {
   // O and LSE of row t, query head hq
   __device__ void finish(const PagedParams& p, int t, int hq, float top, int lane) const {
     const size_t row = static_cast<size_t>(t) * p.Hq + hq;
-    const float inv = l == 0.f ? 0.f : (p.c.quant ? kWeightUnit : 1.f) / l;
+    const float inv = l == 0.f ? 0.f : (kQuant ? kWeightUnit : 1.f) / l;
     uint32_t* dst = static_cast<uint32_t*>(p.o) + row * (D / 2) + lane * (E / 2);
     if constexpr (E == 4)
       *reinterpret_cast<uint2*>(dst) =

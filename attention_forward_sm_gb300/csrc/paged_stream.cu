@@ -486,9 +486,10 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
             if (top > m[nt][k] + kStale) {
               top += kShift;
-              const float alpha = ex2_approx(m[nt][k] - top);  // 0 the first time
+              const float2 f = ex2_factors<kQuant>(m[nt][k] - top);  // 0 the first time
+              const float alpha = f.x * f.y;
               m[nt][k] = top;
-              l[nt][k] *= alpha;
+              l[nt][k] = l[nt][k] * f.x * f.y;
 #pragma unroll
               for (int i = 0; i < kSteps; ++i) {
                 o[nt][i][k] *= alpha;
@@ -610,10 +611,12 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
           for (int k = 0; k < 2; ++k) {
             const float2 ml = ms.ml[warp + 4 * team][nt * 8 + 2 * t + k];
             const float top = fmaxf(m[nt][k], ml.x);
-            a[k] = m[nt][k] == -CUDART_INF_F ? 1.f : ex2_approx(m[nt][k] - top);
-            e[k] = ml.x == -CUDART_INF_F ? 1.f : ex2_approx(ml.x - top);
+            const float2 f = ex2_factors<kQuant>(m[nt][k] == -CUDART_INF_F ? 0.f : m[nt][k] - top);
+            const float2 h = ex2_factors<kQuant>(ml.x == -CUDART_INF_F ? 0.f : ml.x - top);
+            a[k] = f.x * f.y;
+            e[k] = h.x * h.y;
             m[nt][k] = top;
-            l[nt][k] = l[nt][k] * a[k] + ml.y * e[k];
+            l[nt][k] = l[nt][k] * f.x * f.y + ml.y * h.x * h.y;
           }
           const float4* theirs = mine + (team - 1) * (kRows * D);  // (4 warps' parts further)
 #pragma unroll
@@ -647,7 +650,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
                             p.wait_limit_ns)))
       return;
     for (int r = warp; r < min(kRows, n_rows); r += kWarps) {
-      State<D> sum;
+      State<D, kQuant> sum;
       float top = -CUDART_INF_F;
       const int from = D == 128 ? merge_slot(lane) : 2 * merge_slot(lane / 2) + lane % 2;
 #pragma unroll
@@ -655,7 +658,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         sum.add(ms.ml[i][r], top,
-                reinterpret_cast<const typename State<D>::Vec*>(
+                reinterpret_cast<const typename State<D, kQuant>::Vec*>(
                     reinterpret_cast<float*>(smem + C::kOffMerge) + (i * kRows + r) * D)[from]);
       const int row = un.block * kRows + r;
       if (un.slot < 0) {
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
                                      r0 < min(kRows, n_rows));
       for (; last; last &= last - 1) {
         const int r = warp + (__ffs(last) - 1) * kWarps, row = un.block * kRows + r;
-        State<D> all;
+        State<D, kQuant> all;
         const float most = all.join(p, un.parts, lane, [&](int k) {
           return (static_cast<size_t>(un.cta0 + k) * 2 + (k == 0)) * kRows + r;
         });

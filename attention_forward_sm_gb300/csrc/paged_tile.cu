@@ -160,6 +160,9 @@ constexpr uint32_t kScaleEach = 0;
 // 2^-9, and f16 holds multiples of 2^-24.  V: the tile's weights are over that of a
 // row with the largest scale, which need not have any, and end at 2^-24 too.
 constexpr uint32_t kScaleSpanK = 14, kScaleSpanV = 8;
+// The sum of a tile's 2^x is taken from its weights, of 2^(x + e), while e is this near 0: then
+// none is lost under another tile's reference.
+constexpr uint32_t kScaleReachV = 48;
 
 // The factor 2^(scale - most) of a row among those of a tile, as f16; 1 where each key has its
 // own scale, NaN for a row that stands for it.  (Further below there are only zeros.)
@@ -206,14 +209,19 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
   // nothing odd: then every factor is a normal f16 number.  Else only rows count that are
   // there and not NaN, nor zeros, whose scale says 2^0 and could leave nothing of the
   // others; landed() says that the codes are in place (false: they never will be).
-  // kScaleEach where those that count are more than `span` apart; silent: the others.
+  // kScaleEach where those that count are more than `span` apart, or `reach` from 2^0; silent:
+  // the others.
   auto largest = [&](const uint8_t* scales, const uint8_t* codes, bool whole, int rows, uint32_t bad,
-                     uint32_t span, bool* plain, uint32_t* most, uint4* silent, auto landed) {
+                     uint32_t span, uint32_t reach, bool* plain, uint32_t* most, uint4* silent,
+                     auto landed) {
     const uint32_t w = reinterpret_cast<const uint32_t*>(scales)[lane];
     uint32_t s[4] = {w & 255u, w >> 8 & 255u, w >> 16 & 255u, w >> 24};
     *most = __reduce_max_sync(0xFFFFFFFFu, max(max(s[0], s[1]), max(s[2], s[3])));
     const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, min(min(s[0], s[1]), min(s[2], s[3])));
-    *plain = whole && *most != kScaleNan && *most - least <= span;
+    auto within = [&](uint32_t lo) {
+      return *most - lo <= span && *most + reach >= 127u && *most <= 127u + reach;
+    };
+    *plain = whole && *most != kScaleNan && within(least);
     if (*plain) return true;
     bool zeros = false;
     uint32_t counts = 15;  // a bit for each of the lane's rows
@@ -235,7 +243,7 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
         if (!(bits & 0x7F7F7F7Fu)) counts &= ~(1u << i);
       }
     }
-    uint32_t hi_scale = kScaleLeast, lo_scale = 255;
+    uint32_t hi_scale = kScaleLeast, lo_scale = kScaleNan;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (!(counts >> i & 1u)) continue;
@@ -243,7 +251,7 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
       lo_scale = min(lo_scale, s[i]);
     }
     *most = __reduce_max_sync(0xFFFFFFFFu, hi_scale);
-    if (__reduce_min_sync(0xFFFFFFFFu, lo_scale) + span < *most) {
+    if (!within(min(__reduce_min_sync(0xFFFFFFFFu, lo_scale), *most))) {
       *most = kScaleEach;
       *silent = make_uint4(__ballot_sync(0xFFFFFFFFu, !(counts & 1u)),
                            __ballot_sync(0xFFFFFFFFu, !(counts & 2u)),
@@ -275,10 +283,10 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
       if (!of_v) {
         // (V's raw tile is the next one, and comes in while this one is held)
         uint4 silent = make_uint4(0, 0, 0, 0);
-        if (!largest(scales, tile, whole, there, bad, kScaleSpanK, &plain, &most, &silent,
+        if (!largest(scales, tile, whole, there, bad, kScaleSpanK, 255, &plain, &most, &silent,
                      [] { return true; }) ||
-            !largest(scales + kBN, tile + C::kRawBytes, whole, there, bad, kScaleSpanV, &next_plain,
-                     &next_most, &silent, [&] {
+            !largest(scales + kBN, tile + C::kRawBytes, whole, there, bad, kScaleSpanV,
+                     kScaleReachV, &next_plain, &next_most, &silent, [&] {
               return warp_all(mbar_wait(&ms.raw_full[raw + 1], raw_round & 1, abort_flag, p.err,
                                         kErrWaitLoad, p.wait_limit_ns));
             }))
@@ -349,12 +357,12 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
   }
 }
 
-// A key tile whose scales lie far apart: a thread's 64 scores in tensor memory, from s_addr on, get
-// K's scales, or, where V's are each key's own, x + e takes their place, and what is returned
-// is the sum of 2^x over the reference that the tile gets.  Such tiles are few, and none of the
-// softmax' registers are spent on them: a function of its own, which reads the scales where
-// they are.  (1024 tokens behind 30000, 32 heads on 8, D 128, no such tile: without all this 402 us,
-// so 408, as a branch within the loop 416.)
+// A key tile whose scales lie far apart: a thread's 64 scores in tensor memory, from s_addr on,
+// get K's scales, or, where V's are each key's own, x + e takes their place, and what is
+// returned is the sum of 2^x over the reference that the tile gets.  Such tiles are few, and
+// none of the softmax' registers are spent on them: a function of its own, which reads the
+// scales where they are.  (1024 tokens behind 30000, 32 heads on 8, D 128, no such tile:
+// without all this 402 us, so 408, as a branch within the loop 416.)
 __device__ __noinline__ float far_scores(const PagedArrays& c, const FarKeys& far, uint32_t s_addr,
                                          float row_scale, float m, int vis, int half) {
   const uint2 by = far.by;
@@ -636,8 +644,10 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         float alpha = 1.f;
         constexpr float kTop = kQuant ? kWeightTop : 0.f;
         if (m_tile > m + (kQuant ? kTop + kWeightRoom : 8.f)) {  // a stale maximum is as good
-          alpha = ex2_approx(m - (m_tile - kTop));               // up to there; 0 the first time
+          const float2 f = ex2_factors<kQuant>(m - (m_tile - kTop));  // up to there
+          alpha = f.x * f.y;                                          // 0 the first time
           m = m_tile - kTop;
+          if constexpr (kQuant) l = l * f.x * f.y;
         }
         // p = 2^(s * scale - m); a row that has seen nothing keeps m = -inf: its
         // scores are -inf and stay it next to a reference of 0
@@ -660,7 +670,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
         }
         float u0, u1;
         unpack_f32x2(add_f32x2(acc0, acc1), u0, u1);
-        l = fmaf(l, alpha, kQuant ? fmaf(u0 + u1, sum_scale, each_sum) : u0 + u1);
+        l = kQuant ? l + fmaf(u0 + u1, sum_scale, each_sum) : fmaf(l, alpha, u0 + u1);
         // Rescale O_t where a maximum moved: every product of earlier key tiles has
         // retired (issued before the S_t that woke this warp), that of this one waits.
         if (j > it.tile0 && __any_sync(0xFFFFFFFFu, alpha != 1.f)) {
@@ -976,7 +986,7 @@ __global__ void __launch_bounds__(TileCfg<D, kQuant>::kThreads, 1)
 // with 8 blocks an item 37.9 us in all, with 16 34.8, 32 34.5; long chunks all the same.)
 constexpr int kMergeSplit = 16;
 
-template <int D>
+template <int D, bool kQuant>
 __global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__ PagedParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -989,7 +999,7 @@ __global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__
     auto state = [&](int k) {
       return (static_cast<size_t>(blockIdx.x + k) * 2 + (k == 0)) * (2 * kBM) + r;
     };
-    State<D> sum;
+    State<D, kQuant> sum;
     const float top = sum.join(p, cut.parts, lane, state);
     sum.finish(p, cut.row0 + i / p.G, cut.h * p.G + i % p.G, top, lane);
   }
@@ -1010,7 +1020,7 @@ cudaError_t launch_tile(const PagedParams& p, int dev, cudaStream_t stream) {
     return e;
   if (p.ctas < 2) return cudaSuccess;
   // (the last CTA's items end there)
-  return launch_overlapped(tile_merge_kernel<D>, dim3(p.ctas - 1, kMergeSplit), 256, 0, stream, p);
+  return launch_overlapped(tile_merge_kernel<D, kQuant>, dim3(p.ctas - 1, kMergeSplit), 256, 0, stream, p);
 }
 
 }  // namespace

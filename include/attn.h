@@ -502,12 +502,11 @@ int attn_cache_read(const void *kpages, const void *vpages, const unsigned char 
  * lens[b], but a NaN or infinity in V at a position below lens[b] may reach all rows
  * of the same (request, KV head).
  *
- * Numerics as attn_fwd; quantised, weights and queries are rounded to f16 (queries over
- * a power of two that makes a row's largest element 1 to 2) and products with the
- * codes are exact.  f16 ends 2^-24 below 1: next to a row of V 2^24 times as
- * large, a row has little or no influence however large its weight, and likewise a
- * query's elements 2^24 below its largest.  (Rows of zeros count as the smallest.)  Where
- * scales of V lie more than 2^96 apart within a request, O and LSE lose keys.
+ * Numerics as attn_fwd; quantised, weights and queries are rounded to f16 and products
+ * with the codes are exact.  f16 ends at 2^-24: a query's element is off by 2^-11 of
+ * itself or 2^-25 of the row's largest, and a weight times the scale of its V by 2^-11 of
+ * itself or 2^-27 of the largest such product that the row sees, whichever is more.
+ * LSE does not depend on V.
  *
  * max_new * Hq / Hkv up to 16, or M * page above 2^18, takes the kernel for few rows,
  * which reads the cache once for every 16 rows; else that for many rows, which reads it

@@ -240,6 +240,24 @@ def test_many_small_weights_beside_a_large_one(quant, D, B, G, new, bits):
 
 
 @KERNELS
+@pytest.mark.parametrize("spread", [(-100, 60), (60, -100), (-100, -100), (-50, 70)])
+def test_lse_knows_nothing_of_values(G, new, spread):
+    """Scales of V as far apart as they get, between tiles and within them."""
+    lens = [500, 200]
+    c = ref.Cache(lens, 1, 64, 64, True, seed=13)
+    offsets = ref.offsets_of([new, new])
+    q = _randn((2 * new, G, 64), 14)
+    for b, n in enumerate(lens):
+        for i in range(n):
+            at, slot = int(c.table[b, i // 64]), i % 64
+            e = spread[i // 128 % 2] if b == 0 else spread[i % 2]
+            c.dense[b][1][i] *= 2.0 ** (e + 127 - int(c.vs[at, 0, slot]))
+            c.vs[at, 0, slot] = e + 127
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
+    check_range(o, lse, q, c, offsets)
+
+
+@KERNELS
 @pytest.mark.parametrize("n", [130, 40000])
 def test_values_of_zeros(G, new, n):
     """A cache whose V is all zeros: O is 0, LSE as ever."""
