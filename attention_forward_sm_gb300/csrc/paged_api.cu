@@ -109,8 +109,10 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
   l.rows = many ? 0 : rows <= 8 ? 8 : 16;
   // the streaming kernel numbers its units of work in 32 bits: a block of rows has
   // M * page / 64 + 9 of them at most, less than twice what is counted here
+  // (the other one counts in 64 bits)
   const long long blocks = static_cast<long long>(c.T) * p.G / 8 + c.B;
-  if (blocks * c.Hkv * (static_cast<long long>(c.M) * c.page / 64 + 5) >= (1ll << 31))
+  if (!many &&
+      blocks * c.Hkv * (static_cast<long long>(c.M) * c.page / 64 + 5) >= (1ll << 31))
     return ATTN_ERR_SHAPE;
   DeviceInfo di;
   if (int rc = device_info(&di)) return rc;

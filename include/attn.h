@@ -513,8 +513,8 @@ int attn_cache_read(const void *kpages, const void *vpages, const unsigned char 
  * once for every 2 * (128 / (Hq / Hkv)) tokens.
  *
  * Limits: Hq % Hkv == 0, Hq <= 65535, Hq / Hkv <= 128, max_new >= 0; scale finite and
- * >= 0; the rows times the keys in units of work within 32 bits:
- * (T * Hq / Hkv / 8 + B) * Hkv * (M * page / 64 + 5) < 2^31.  Scratch, about 40
+ * >= 0; for the kernel for few rows, the rows times the keys in units of work within 32
+ * bits: (T * Hq / Hkv / 8 + B) * Hkv * (M * page / 64 + 5) < 2^31.  Scratch, about 40
  * MB at most: a buffer per stream as attn_decode_varlen, the kernel for few rows one of its own.
  */
 int attn_paged_fwd(const void *q, long long q_stride, const void *kpages, const void *vpages,
