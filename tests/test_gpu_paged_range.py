@@ -55,6 +55,8 @@ def check_range(o, lse, q, c, offsets, causal=True, scale=None, only=None):
     for b, (k, v) in enumerate(c.dense):
         n, m = off[b + 1] - off[b], c.lens[b]
         rows = slice(off[b], off[b + 1])
+        if n == 0 or m == 0:
+            continue
         pos = torch.arange(n, device="cuda") + (m - n)
         seen = torch.arange(m, device="cuda")[None] <= (pos[:, None] if causal else m)
         for h in range(q.shape[1]):
