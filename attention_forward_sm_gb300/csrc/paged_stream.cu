@@ -445,8 +445,9 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
       // Quantised, a weight of V's codes is 2^(x + e), e the exponent of V's scale, and the
       // maximum is of x + e (see kWeightTop): what f16 loses is next to the largest
       // product, since every row of codes reaches beyond 224 but one of zeros, which says
-      // 2^0 and counts as the least.
-      float ev[2] = {0.f, 0.f};
+      // 2^0 and counts as the least.  (ev: e + kWeightLift; m: the sum's reference.)
+      constexpr float kTop = kQuant ? kWeightTop : 0.f, kLift = kQuant ? kWeightLift : 0.f;
+      float ev[2] = {kLift, kLift};
       [[maybe_unused]] uint32_t vscale[2] = {127, 127};
       if constexpr (kQuant) {
         vscale[0] = scales[kUnitKeys + row_lo];
@@ -462,14 +463,13 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
             if (!(bits & 0x7F7F7F7Fu)) vscale[k] = kScaleLeast;
           }
         }
-        if (vscale[0] != kScaleNan) ev[0] = scale_exponent(vscale[0]);
-        if (vscale[1] != kScaleNan) ev[1] = scale_exponent(vscale[1]);
+        if (vscale[0] != kScaleNan) ev[0] = scale_exponent(vscale[0]) + kLift;
+        if (vscale[1] != kScaleNan) ev[1] = scale_exponent(vscale[1]) + kLift;
       }
       // The maximum moves only when a score is above it by more than 2^8 (quantised
       // 2^kWeightRoom): a stale one is as good (the sum has the same), and the vote is cheaper
       // than the maximum.
-      constexpr float kShift = kQuant ? kSumShift : 0.f;
-      constexpr float kStale = kQuant ? kWeightRoom - kSumShift : 8.f;
+      constexpr float kStale = kQuant ? kWeightTop + kWeightRoom : 8.f;
       bool above = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
             if (top > m[nt][k] + kStale) {
-              top += kShift;
+              top -= kTop;
               const float2 f = ex2_factors<kQuant>(m[nt][k] - top);  // 0 the first time
               const float alpha = f.x * f.y;
               m[nt][k] = top;
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(StreamCfg<D, kQuant, NT>::kThreads, (StreamCfg
           const float d = x[nt][k] - m[nt][k & 1];
           w[k] = none ? 0.f : ex2_approx(d);
           l[nt][k & 1] += w[k];
-          if constexpr (kQuant) w[k] = none ? 0.f : ex2_approx(d + (ev[k >> 1] + kWeightLift));
+          if constexpr (kQuant) w[k] = none ? 0.f : ex2_approx(d + ev[k >> 1]);
         }
         // rounded for the product: to bf16, as V is, or f16
         pf[nt][0] = transpose_8x8(kQuant ? pack_f16x2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
