@@ -102,8 +102,11 @@ int attend(const PagedArrays& c, const void* q, long long q_stride, void* o, flo
   l.p = &p;
   // Few rows share each key (up to 16): the kernel that streams the cache.  (For 17 to 32 it
   // reads it twice: 16 requests with 8 tokens of 32 heads on 8 behind 100 to 16384 75 us, the
-  // other 52; e4m3 67 and 62; with 4 tokens 45 and 52.)  An accumulator of the one for many
-  // rows takes kSegmentKeys keys at most.
+  // other 52; e4m3 67 and 64; with 4 tokens 45 and 52.)  An accumulator of the one for many
+  // rows takes kSegmentKeys keys at most, and lengths are on the device: so does a wider
+  // table, at the price of reading the cache for every 16 rows (2048 tokens behind 16001,
+  // 32 heads on 8, D 128: 5.0 ms for 0.36; e4m3, 1024 behind 30000, 3.1 for 0.41; a
+  // prompt of 500 87 us for 32).
   const long long rows = std::min<long long>(max_new, c.T) * p.G;
   const bool many = rows > 16 && static_cast<long long>(c.M) * c.page <= kSegmentKeys;
   l.rows = many ? 0 : rows <= 8 ? 8 : 16;

@@ -10,13 +10,15 @@
 // code * 2^e is a normal bf16 number.  A row that holds a NaN has the scale byte 255
 // and comes back as NaN.
 //
-// Bound by memory.  A lane moves 16 elements of a row (a row is one run of whole sectors on
-// either side) and D / 16 lanes a row; a CTA takes up to kTokens tokens, whose pages are
-// looked up once, by a warp each, ahead of the rows.  A lane keeps its head and goes
-// through tokens, so that a row costs little more than its loads and stores: with 8
-// elements a lane, and the row's token and head found by division, instructions were the
-// bound (26424 tokens of 8 heads, D 128, quantised 40 us, 152709 read back 165; now 28.7,
-// 84% of the measured copy bandwidth, and 150, 92%).
+// A lane moves 16 elements of a row (a row is one run of whole sectors on either side) and
+// D / 16 lanes a row; a CTA takes up to kTokens tokens, whose pages are looked up once, by
+// a warp each, ahead of the rows.  A lane keeps its head and goes through tokens, so that a
+// row costs little more than its loads and stores: with 8 elements a lane, and the row's
+// token and head found by division, instructions were the bound.  Long reads are bound by
+// memory: 152709 tokens of 8 heads, D 128, quantised, 148 us, 93% of the measured copy.
+// Writes wait for their loads, one row a lane behind the look-up of its page, more than half of
+// the time: 26424 of these tokens 35 us on data that is not in L2, 69% (DRAM busy 52%,
+// issue slots 61%; 29 us over and over on the same data), bf16 42, 75%.
 #include "../../include/attn.h"
 #include "paged.cuh"
 

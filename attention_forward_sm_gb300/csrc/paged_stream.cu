@@ -53,7 +53,7 @@ template <int D, bool kQuant, int NT>
 struct StreamCfg {
   // Quantised, 9 to 16 rows: latencies are the bound, and three teams hide more of them.  Their
   // 128 registers a thread hold no queries, which are in shared memory (16 requests of 30000
-  // tokens 229 -> 198 us, 64 of 7000 225 -> 197).
+  // tokens 229 -> 198 us, 64 of 7000 225 -> 197; 200 both with the weights' present range).
   static constexpr bool kSharedQ = kQuant && NT == 2;
   static constexpr int kTeams = kSharedQ ? 3 : 2;
   static constexpr int kWarps = 4 * kTeams;  // computing

@@ -23,10 +23,11 @@
 // that is cut has a partial state in each CTA, which tile_merge_kernel joins.
 // Bound by the tensor cores, 4 D flops per row and key, and the chain of a query tile
 // (scores, softmax pass, products), two of which alternate.  32 heads on 8, D = 128: bf16,
-// 2048 tokens behind 16001 356 us, of which 333 this kernel (1.7 PFLOP/s, tensor pipe 74%)
-// and 15 the joining; e4m3, 1024 behind 30000 403 us, 388 and 13, tensor pipe 56%, issue slots
-// 54%: the conversion's instructions and 96 registers for the softmax warps.  Short chunks are bound by 6 us until the first
-// product and 5 from one item to the next.
+// 2048 tokens behind 16001 350 to 380 us (with the power cap), of which 338 this kernel (1.7
+// PFLOP/s, tensor pipe 74%) and 15 the joining; e4m3, 1024 behind 30000 407 us, 400 and
+// 14, tensor pipe 55%, issue slots 55%: the conversion's instructions and 96 registers for
+// the softmax warps.  Short chunks are bound by 6 us until the first product and 5 from one
+// item to the next.
 #include <math_constants.h>
 
 #include <atomic>
@@ -179,8 +180,9 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 // The warps that make f16 operands K_0, V_0, K_1 ... of codes.  f16 holds every code, and
 // turning codes into it is one instruction for two, where bf16 takes five: with bf16
 // the schedulers had no room for them next to the softmax (1024 tokens behind 30000, 32
-// heads on 8, D 128: 460 us; now 402).  A tile's values are over the
-// largest of its scales, which the softmax puts back, and Q is converted at its start.
+// heads on 8, D 128: 460 us; f16 402).  A tile's values are over the largest of its scales,
+// which the softmax puts back, or, where these lie far apart, over each key's own (see
+// far_scores).  Q is converted by the softmax warps at an item's start.
 template <int D, class C, class Shared, class Next>
 __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_t* smem,
                                         uint32_t abort_flag, Next next_item) {
@@ -362,7 +364,8 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
 // returned is the sum of 2^x over the reference that the tile gets.  Such tiles are few, and
 // none of the softmax' registers are spent on them: a function of its own, which reads the
 // scales where they are.  (1024 tokens behind 30000, 32 heads on 8, D 128, no such tile:
-// without all this 402 us, so 408, as a branch within the loop 416.)
+// without all this 401 us, so 407, as branches within the loop 415; 1106 if every tile's
+// K has one, 2450 if V has.)
 __device__ __noinline__ float far_scores(const PagedArrays& c, const FarKeys& far, uint32_t s_addr,
                                          float row_scale, float m, int vis, int half) {
   const uint2 by = far.by;
@@ -1020,7 +1023,8 @@ cudaError_t launch_tile(const PagedParams& p, int dev, cudaStream_t stream) {
     return e;
   if (p.ctas < 2) return cudaSuccess;
   // (the last CTA's items end there)
-  return launch_overlapped(tile_merge_kernel<D, kQuant>, dim3(p.ctas - 1, kMergeSplit), 256, 0, stream, p);
+  return launch_overlapped(tile_merge_kernel<D, kQuant>, dim3(p.ctas - 1, kMergeSplit), 256, 0,
+                           stream, p);
 }
 
 }  // namespace
