@@ -210,12 +210,12 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
   // The largest of a tile's scales, and whether all are within `span` of it and there is
   // nothing odd: then every factor is a normal f16 number.  Else only rows count that are
   // there and not NaN, nor zeros, whose scale says 2^0 and could leave nothing of the
-  // others; landed() says that the codes are in place (false: they never will be).
-  // kScaleEach where those that count are more than `span` apart, or `reach` from 2^0; silent:
-  // the others.
+  // others (of V also those of other tiles); landed() says that the codes are in place
+  // (false: they never will be).  kScaleEach where those that count are more than `span`
+  // apart, or `reach` from 2^0; silent: the others.
   auto largest = [&](const uint8_t* scales, const uint8_t* codes, bool whole, int rows, uint32_t bad,
-                     uint32_t span, uint32_t reach, bool* plain, uint32_t* most, uint4* silent,
-                     auto landed) {
+                     bool of_v, bool* plain, uint32_t* most, uint4* silent, auto landed) {
+    const uint32_t span = of_v ? kScaleSpanV : kScaleSpanK, reach = of_v ? kScaleReachV : 255u;
     const uint32_t w = reinterpret_cast<const uint32_t*>(scales)[lane];
     uint32_t s[4] = {w & 255u, w >> 8 & 255u, w >> 16 & 255u, w >> 24};
     *most = __reduce_max_sync(0xFFFFFFFFu, max(max(s[0], s[1]), max(s[2], s[3])));
@@ -223,7 +223,8 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
     auto within = [&](uint32_t lo) {
       return *most - lo <= span && *most + reach >= 127u && *most <= 127u + reach;
     };
-    *plain = whole && *most != kScaleNan && within(least);
+    *plain = whole && *most != kScaleNan && within(least) &&
+             !(of_v && least <= kScaleOfZeros && kScaleOfZeros <= *most);
     if (*plain) return true;
     bool zeros = false;
     uint32_t counts = 15;  // a bit for each of the lane's rows
@@ -240,8 +241,9 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
       for (int i = 0; i < 4; ++i) {
         uint32_t bits = s[i] == kScaleOfZeros ? 0u : ~0u;
 #pragma unroll 1
-        for (int at = 0; at < D; at += 16)
-          bits |= or_of(*reinterpret_cast<const uint4*>(codes + (4 * lane + i) * D + at));
+        for (int at = 0; at < D; at += 16)  // (each lane begins elsewhere: other banks)
+          bits |= or_of(*reinterpret_cast<const uint4*>(codes + (4 * lane + i) * D +
+                                                        (at + 16 * lane) % D));
         if (!(bits & 0x7F7F7F7Fu)) counts &= ~(1u << i);
       }
     }
@@ -285,10 +287,10 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
       if (!of_v) {
         // (V's raw tile is the next one, and comes in while this one is held)
         uint4 silent = make_uint4(0, 0, 0, 0);
-        if (!largest(scales, tile, whole, there, bad, kScaleSpanK, 255, &plain, &most, &silent,
+        if (!largest(scales, tile, whole, there, bad, false, &plain, &most, &silent,
                      [] { return true; }) ||
-            !largest(scales + kBN, tile + C::kRawBytes, whole, there, bad, kScaleSpanV,
-                     kScaleReachV, &next_plain, &next_most, &silent, [&] {
+            !largest(scales + kBN, tile + C::kRawBytes, whole, there, bad, true, &next_plain,
+                     &next_most, &silent, [&] {
               return warp_all(mbar_wait(&ms.raw_full[raw + 1], raw_round & 1, abort_flag, p.err,
                                         kErrWaitLoad, p.wait_limit_ns));
             }))
@@ -365,7 +367,7 @@ __device__ __forceinline__ void convert(const PagedParams& p, Shared& ms, uint8_
 // none of the softmax' registers are spent on them: a function of its own, which reads the
 // scales where they are.  (1024 tokens behind 30000, 32 heads on 8, D 128, no such tile:
 // without all this 401 us, so 407, as branches within the loop 415; 1106 if every tile's
-// K has one, 2450 if V has.)
+// K has one, 2450 if V has, 2060 if V is zeros.)
 __device__ __noinline__ float far_scores(const PagedArrays& c, const FarKeys& far, uint32_t s_addr,
                                          float row_scale, float m, int vis, int half) {
   const uint2 by = far.by;
@@ -380,8 +382,9 @@ __device__ __noinline__ float far_scores(const PagedArrays& c, const FarKeys& fa
     return __ldcg(reinterpret_cast<const uint4*>(
         scales + (static_cast<size_t>(id) * c.Hkv + far.h) * c.page + (key & (c.page - 1))));
   };
+  const bool zeros = (none[0] & none[1] & none[2] & none[3]) == ~0u;  // all of V
   auto exponents = [&](int col, float (&e)[16]) {
-    const uint4 x = bytes(c.vscale, far.key0 + col);
+    const uint4 x = zeros ? make_uint4(0, 0, 0, 0) : bytes(c.vscale, far.key0 + col);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {

@@ -272,3 +272,64 @@ def test_values_of_zeros(G, new, n):
     o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
     assert not o.any()
     check_range(o, lse, q, c, offsets)
+
+
+@KERNELS
+@pytest.mark.parametrize("sigma", [1.0, 1e-8, 1e-25])
+@pytest.mark.parametrize("zeros", [range(0, 256), range(256, 384), range(500, 700)])
+def test_tiles_of_zeros_beside_small_values(G, new, sigma, zeros):
+    """Whole tiles of keys whose V is zeros and says 2^0."""
+    n = 700
+    c = ref.Cache([n], 1, 64, 64, True, seed=17, sigma=sigma)
+    up = -round(math.log2(sigma))  # K as large as ever
+    c.dense[0][0].mul_(2.0 ** up)
+    c.ks += up
+    for x in c.dense[0]:
+        x[list(zeros)] = 0
+    for i in zeros:
+        at, slot = int(c.table[0, i // 64]), i % 64
+        for pages, scale in ((c.kp, c.ks), (c.vp, c.vs)):
+            pages.view(torch.uint8)[at, :, slot] = 0x80 * (i % 2)
+            scale[at, :, slot] = 127
+    offsets = ref.offsets_of([new])
+    q = _randn((new, G, 64), 18)
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, causal=False, **c.scales())
+    check_range(o, lse, q, c, offsets, causal=False)
+
+
+@pytest.mark.parametrize("G,new,lens", [(4, 3, [9000, 130]), (2, 70, [300, 4000]), (3, 300, [9000, 700]), (16, 40, [1500, 41])])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("causal", [True, False])
+def test_scales_at_random(G, new, lens, D, page, causal):
+    """Runs of ordinary tokens and of tokens with scales of any size, items cut anywhere; pages out
+    of range and a key of NaN that only the last rows see."""
+    c = ref.Cache(lens, 2, D, page, True, seed=sum(lens) + D)
+    g = torch.Generator().manual_seed(page + new)
+    offsets = ref.offsets_of([new] * len(lens))
+    q = _randn((new * len(lens), 2 * G, D), 19)
+    for b, n in enumerate(lens):
+        i = torch.arange(n)
+        wild = (torch.rand(n // 100 + 1, generator=g) < 0.4)[i // 100]
+        at, slot = c.table[b].long()[(i // page).cuda()], (i % page).cuda()
+        for x, scale, lo, hi in ((c.dense[b][0], c.ks, -24, 1), (c.dense[b][1], c.vs, -30, 31)):
+            e = torch.randint(lo, hi, (n,), generator=g) * wild
+            x *= torch.exp2(e.double()).cuda()[:, None, None]
+            scale[at, :, slot] += e.to(torch.uint8).cuda()[:, None]  # (modulo 256)
+    bad = lens[0] // page // 2
+    c.table[0, bad] = -1
+    for x in c.dense[0]:
+        x[bad * page:(bad + 1) * page] = 0
+    o, lse = attn.paged_forward(q, *c.args(), offsets, max_new=new, causal=causal, **c.scales())
+    assert attn.attn_get_device_error() == 0x40
+    check_range(o, lse, q, c, offsets, causal=causal)
+    if causal:  # the last token's K NaN: nothing for those in front
+        for b, n in enumerate(lens):
+            c.ks[int(c.table[b, (n - 1) // page]), :, (n - 1) % page] = 255
+        o2, lse2 = attn.paged_forward(q, *c.args(), offsets, max_new=new, **c.scales())
+        assert attn.attn_get_device_error() == 0x40
+        for b in range(len(lens)):
+            last = (b + 1) * new - 1
+            assert torch.isnan(o2[last]).all() and torch.isnan(lse2[last]).all()
+            o2[last], lse2[last] = o[last], lse[last]
+        check_range(o2, lse2, q, c, offsets)
